@@ -12,7 +12,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblce.so")
 
 LCE_BF16, LCE_FP32 = 0, 1
-LCE_DEV_TARGET_RANGE, LCE_DEV_TIMEOUT = 0x1, 0x2
+LCE_DEV_TARGET_RANGE, LCE_DEV_TIMEOUT, LCE_DEV_SEQLENS = 0x1, 0x2, 0x4
 PROFILE_PHASES = 5
 PHASE_NAMES = ("compact_gather", "logits_lse", "lse_merge_loss", "backward", "dH_scatter")
 
@@ -51,6 +51,16 @@ SIGNATURES = {
                                        c_void_p, c_size_t, c_void_p]),
     "lce_embedding_backward_bf16": (c_int, [c_int, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int64, c_void_p,
                                             c_void_p, c_size_t, c_void_p]),
+    "lce_attention_forward": (c_int, [c_void_p]),
+    "lce_attention_backward": (c_int, [c_void_p]),
+    "lce_attention_workspace_size": (c_size_t, [c_void_p]),
+    "lce_block_norm_forward": (c_int, [c_void_p]),
+    "lce_block_norm_backward": (c_int, [c_void_p]),
+    "lce_block_norm_workspace_size": (c_size_t, [c_void_p]),
+    "lce_clip_workspace_size": (c_size_t, [c_int64]),
+    "lce_grad_norm": (c_int, [c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "lce_clip_grads": (c_int, [c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_float, c_float, c_void_p, c_void_p,
+                               c_void_p, c_size_t, c_void_p]),
 }
 
 
@@ -84,6 +94,38 @@ class LceArgs(ctypes.Structure):
         ("optim", c_void_p),
         ("row_gather", c_int),
         ("dW_bf16", c_int),
+    ]
+
+
+class LceAttn(ctypes.Structure):
+    """Mirror of lce_attn_t."""
+    _fields_ = [
+        ("dtype", c_int), ("causal", c_int), ("scale", c_float),
+        ("B", c_int64), ("Tq", c_int64), ("Tk", c_int64), ("Hq", c_int64), ("Hk", c_int64), ("D", c_int64),
+        ("cu_q", c_void_p), ("cu_k", c_void_p),
+        ("q", c_void_p), ("k", c_void_p), ("v", c_void_p),
+        ("q_ts", c_int64), ("q_hs", c_int64), ("k_ts", c_int64), ("k_hs", c_int64), ("v_ts", c_int64),
+        ("v_hs", c_int64),
+        ("o", c_void_p), ("o_ts", c_int64), ("o_hs", c_int64),
+        ("lse", c_void_p),
+        ("dO", c_void_p), ("dO_ts", c_int64), ("dO_hs", c_int64),
+        ("dq", c_void_p), ("dk", c_void_p), ("dv", c_void_p),
+        ("dq_ts", c_int64), ("dq_hs", c_int64), ("dk_ts", c_int64), ("dk_hs", c_int64), ("dv_ts", c_int64),
+        ("dv_hs", c_int64),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("stream", c_void_p),
+    ]
+
+
+class LceNorm(ctypes.Structure):
+    """Mirror of lce_norm_t."""
+    _fields_ = [
+        ("dtype", c_int), ("N", c_int64), ("d", c_int64), ("scale", c_float), ("eps", c_float),
+        ("x", c_void_p), ("b", c_void_p), ("w_post", c_void_p), ("gate", c_void_p), ("w_pre", c_void_p),
+        ("gate_full", c_int), ("ld_x", c_int64), ("ld_b", c_int64), ("ld_gate", c_int64),
+        ("r", c_void_p), ("n", c_void_p), ("rstd_post", c_void_p), ("rstd_pre", c_void_p),
+        ("dr", c_void_p), ("dn", c_void_p), ("ld_r", c_int64), ("ld_dr", c_int64), ("ld_dn", c_int64),
+        ("dx", c_void_p), ("db", c_void_p), ("dw_post", c_void_p), ("dgate", c_void_p), ("dw_pre", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("stream", c_void_p),
     ]
 
 

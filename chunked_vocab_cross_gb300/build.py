@@ -1,7 +1,7 @@
 """Compile liblce.so (the CUDA library behind include/lce.h) in-tree for sm_103a.
 
-One translation unit, one -gencode, no cmake: nvcc cross-compiles it on a
-machine without a GPU as well.
+Four translation units compiled in parallel by one nvcc call, one -gencode, no
+cmake: nvcc cross-compiles them on a machine without a GPU as well.
 """
 from __future__ import annotations
 
@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblce.so")
-SOURCES = ["lce_api.cu"]
+SOURCES = ["lce_api.cu", "lce_attn.cu", "lce_norm.cu", "lce_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -26,7 +26,7 @@ def _nvcc() -> str:
 
 
 def _inputs() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "lce.h"))
     files.append(os.path.abspath(__file__))
     return files
@@ -44,7 +44,7 @@ def build(force: bool = False, verbose: bool = False, out: str = LIB, extra: lis
     if not force and up_to_date(out):
         return out
     cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-shared",
-           "-cudart", "shared", "-I", INCLUDE, "-o", out + ".tmp",
+           "--threads", "0", "-cudart", "shared", "-I", INCLUDE, "-o", out + ".tmp",
            *[os.path.join(CSRC, s) for s in SOURCES], *(extra or [])]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -25,7 +25,9 @@
 // and finally k_loss_final (loss = sum of the chunks' sums / Nv). With a
 // stored lse (lse_in), k_lse_from_input replaces steps 3-5.
 // The input-embedding lookup and its gradient (lce_embedding_*) are separate
-// entry points over the kernels of lce_embed.cuh.
+// entry points over the kernels of lce_embed.cuh; attention, the block norms
+// and gradient clipping are translation units of their own (lce_attn.cu,
+// lce_norm.cu, lce_clip.cu) over the shared host record of lce_host.h.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -39,6 +41,7 @@
 #include "lce.h"
 #include "lce_embed.cuh"
 #include "lce_gemm.cuh"
+#include "lce_host.h"
 #include "lce_rows.cuh"
 
 using namespace lce;
@@ -69,6 +72,7 @@ std::mutex g_mu;
 struct DevInfo {
     bool ready = false;
     int sms = 0, major = 0, minor = 0;
+    int *status = nullptr;   // address of g_status on this device
 };
 DevInfo g_dev[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -149,6 +153,11 @@ lce_status_t device_info(DevInfo **out) {
                 t_last_cuda = e;
                 return LCE_ERR_CUDA;
             }
+        }
+        e = cudaGetSymbolAddress(reinterpret_cast<void **>(&di.status), g_status);
+        if (e != cudaSuccess) {
+            t_last_cuda = e;
+            return LCE_ERR_CUDA;
         }
         if (!g_encode) {
             void *fn = nullptr;
@@ -753,6 +762,31 @@ lce_status_t noalloc_scratch(void **out) {
 
 }  // namespace
 
+namespace lce {
+
+lce_status_t host_device(HostDev *out) {
+    DevInfo *di = nullptr;
+    const lce_status_t s = device_info(&di);
+    if (s != LCE_OK) return s;
+    out->sms = di->sms;
+    out->status = di->status;
+    out->encode = g_encode;
+    return LCE_OK;
+}
+
+lce_status_t host_cuda(cudaError_t e) {
+    if (e == cudaSuccess) return LCE_OK;
+    t_last_cuda = e;
+    return LCE_ERR_CUDA;
+}
+
+lce_status_t host_launched() {
+    count_launch();
+    return host_cuda(cudaGetLastError());
+}
+
+}  // namespace lce
+
 extern "C" {
 
 lce_status_t lce_run(const lce_args_t *a) {
@@ -1049,6 +1083,7 @@ lce_status_t lce_get_device_status(lce_stream_t stream, int32_t *bits) {
     *bits = v;
     if (v & LCE_DEV_TARGET_RANGE) return LCE_ERR_TARGET_RANGE;
     if (v & LCE_DEV_TIMEOUT) return LCE_ERR_TIMEOUT;
+    if (v & LCE_DEV_SEQLENS) return LCE_ERR_SHAPE;
     return LCE_OK;
 }
 

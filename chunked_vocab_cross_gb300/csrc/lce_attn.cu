@@ -1,0 +1,149 @@
+// Host side of attention over packed sequences: argument checks, workspace
+// and launches.
+#include "lce_attn_simt.cuh"
+#include "lce_host.h"
+
+using namespace lce;
+
+namespace {
+
+
+lce_status_t check_side(const void *p, int64_t ts, int64_t hs, int64_t T, int64_t H, int64_t D, int elt, bool out) {
+    if (T == 0) return LCE_OK;   // an empty side is never read or written
+    if (!p) return LCE_ERR_NULL;
+    if (host_misaligned(p) || (ts * elt) % 16 || (hs * elt) % 16) return LCE_ERR_ALIGN;
+    if (ts < 0 || hs < 0 || ts >= (int64_t(1) << 36) || hs >= (int64_t(1) << 36)) return LCE_ERR_SHAPE;
+    // rows of an output must not meet
+    if (out && ((T > 1 && ts < D) || (H > 1 && hs < D))) return LCE_ERR_SHAPE;
+    return LCE_OK;
+}
+
+lce_status_t check_shape(const lce_attn_t *a) {
+    if (!a) return LCE_ERR_NULL;
+    if (a->dtype != LCE_BF16 && a->dtype != LCE_FP32) return LCE_ERR_DTYPE;
+    constexpr int64_t kMost = int64_t(1) << 30;
+    if (a->Tq < 0 || a->Tk < 0 || a->Tq >= kMost || a->Tk >= kMost || a->B < 1 || a->B >= kMost || a->Hq < 1 ||
+        a->Hk < 1 || a->Hq > 65535 || a->Hq % a->Hk || a->D < 1 || a->D > 128)
+        return LCE_ERR_SHAPE;
+    if (a->D % 8) return LCE_ERR_ALIGN;
+    if ((a->cu_q == nullptr) != (a->cu_k == nullptr)) return LCE_ERR_NULL;
+    if (!a->cu_q && (a->Tq % a->B || a->Tk % a->B)) return LCE_ERR_SHAPE;
+    return LCE_OK;
+}
+
+lce_status_t check_common(const lce_attn_t *a) {
+    lce_status_t s = check_shape(a);
+    if (s != LCE_OK) return s;
+    if (!(a->scale == a->scale) || a->scale - a->scale != 0.f) return LCE_ERR_ARG;   // NaN or infinite
+    const int elt = a->dtype == LCE_BF16 ? 2 : 4;
+    if ((s = check_side(a->q, a->q_ts, a->q_hs, a->Tq, a->Hq, a->D, elt, false)) != LCE_OK) return s;
+    if ((s = check_side(a->k, a->k_ts, a->k_hs, a->Tk, a->Hk, a->D, elt, false)) != LCE_OK) return s;
+    if ((s = check_side(a->v, a->v_ts, a->v_hs, a->Tk, a->Hk, a->D, elt, false)) != LCE_OK) return s;
+    if (a->Tq > 0 && !a->lse) return LCE_ERR_NULL;
+    return LCE_OK;
+}
+
+AttnArgs make_args(const lce_attn_t *a, const HostDev &dev) {
+    AttnArgs r{};
+    r.q = a->q, r.k = a->k, r.v = a->v, r.o_in = a->o, r.dO = a->dO;
+    r.o = a->o, r.dq = a->dq, r.dk = a->dk, r.dv = a->dv;
+    r.lse = a->lse;
+    r.q_ts = a->q_ts, r.q_hs = a->q_hs, r.k_ts = a->k_ts, r.k_hs = a->k_hs, r.v_ts = a->v_ts, r.v_hs = a->v_hs;
+    r.o_ts = a->o_ts, r.o_hs = a->o_hs, r.dO_ts = a->dO_ts, r.dO_hs = a->dO_hs;
+    r.dq_ts = a->dq_ts, r.dq_hs = a->dq_hs, r.dk_ts = a->dk_ts, r.dk_hs = a->dk_hs, r.dv_ts = a->dv_ts, r.dv_hs = a->dv_hs;
+    const int B = static_cast<int>(a->B);
+    r.sq = SeqMap{a->cu_q, B, static_cast<int>(a->Tq), static_cast<int>(a->Tq / B)};
+    r.sk = SeqMap{a->cu_k, B, static_cast<int>(a->Tk), static_cast<int>(a->Tk / B)};
+    r.Hq = static_cast<int>(a->Hq);
+    r.Hk = static_cast<int>(a->Hk);
+    r.group = r.Hq / r.Hk;
+    r.D = static_cast<int>(a->D);
+    r.causal = a->causal != 0;
+    r.scale = a->scale;
+    r.scale_log2 = a->scale * kAttnLog2e;
+    r.status = dev.status;
+    return r;
+}
+
+template <typename K, typename... A>
+lce_status_t launch(K kernel, int64_t blocks, int threads, int smem, cudaStream_t st, const A &...args) {
+    if (blocks <= 0) return LCE_OK;
+    if (blocks >= (int64_t(1) << 31)) return LCE_ERR_SHAPE;
+    if (smem > 48 * 1024) {
+        const lce_status_t s = host_cuda(cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+        if (s != LCE_OK) return s;
+    }
+    kernel<<<static_cast<unsigned>(blocks), threads, smem, st>>>(args...);
+    return host_launched();
+}
+
+template <typename T, int DP>
+lce_status_t forward_simt(const AttnArgs &r, cudaStream_t st) {
+    const int64_t slots = seq_slots(r.sq.T, r.sq.B, kSimtTile);
+    return launch(k_attn_fwd_simt<T, DP>, slots * r.Hq, kSimtThreads, simt_smem(DP, 3, 1), st, r);
+}
+
+template <typename T, int DP>
+lce_status_t backward_simt(const AttnArgs &r, cudaStream_t st) {
+    const int64_t qslots = seq_slots(r.sq.T, r.sq.B, kSimtTile), kslots = seq_slots(r.sk.T, r.sk.B, kSimtTile);
+    lce_status_t s = launch(k_attn_stats<T, kSimtTile>, qslots * r.Hq, 256, 0, st, r);
+    if (s == LCE_OK && r.sq.T > 0) s = launch(k_attn_dq_simt<T, DP>, qslots * r.Hq, kSimtThreads, simt_smem(DP, 4, 1), st, r);
+    if (s == LCE_OK && r.sk.T > 0) s = launch(k_attn_dkv_simt<T, DP>, kslots * r.Hk, kSimtThreads, simt_smem(DP, 4, 2), st, r);
+    return s;
+}
+
+int stat_tile(const lce_attn_t *) { return kSimtTile; }
+
+}  // namespace
+
+extern "C" {
+
+size_t lce_attention_workspace_size(const lce_attn_t *a) {
+    if (check_shape(a) != LCE_OK) return 0;
+    const size_t rows = static_cast<size_t>(seq_slots(a->Tq, a->B, stat_tile(a))) * stat_tile(a);
+    return 2 * rows * static_cast<size_t>(a->Hq) * sizeof(float);
+}
+
+lce_status_t lce_attention_forward(const lce_attn_t *a) {
+    lce_status_t s = check_common(a);
+    if (s != LCE_OK) return s;
+    const int elt = a->dtype == LCE_BF16 ? 2 : 4;
+    if ((s = check_side(a->o, a->o_ts, a->o_hs, a->Tq, a->Hq, a->D, elt, true)) != LCE_OK) return s;
+    HostDev dev;
+    if ((s = host_device(&dev)) != LCE_OK) return s;
+    if (a->Tq == 0) return LCE_OK;
+    const AttnArgs r = make_args(a, dev);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
+    if (a->dtype == LCE_BF16)
+        return a->D <= 64 ? forward_simt<__nv_bfloat16, 64>(r, st) : forward_simt<__nv_bfloat16, 128>(r, st);
+    return a->D <= 64 ? forward_simt<float, 64>(r, st) : forward_simt<float, 128>(r, st);
+}
+
+lce_status_t lce_attention_backward(const lce_attn_t *a) {
+    lce_status_t s = check_common(a);
+    if (s != LCE_OK) return s;
+    const int elt = a->dtype == LCE_BF16 ? 2 : 4;
+    if ((s = check_side(a->o, a->o_ts, a->o_hs, a->Tq, a->Hq, a->D, elt, false)) != LCE_OK) return s;
+    if ((s = check_side(a->dO, a->dO_ts, a->dO_hs, a->Tq, a->Hq, a->D, elt, false)) != LCE_OK) return s;
+    if ((s = check_side(a->dq, a->dq_ts, a->dq_hs, a->Tq, a->Hq, a->D, elt, true)) != LCE_OK) return s;
+    if ((s = check_side(a->dk, a->dk_ts, a->dk_hs, a->Tk, a->Hk, a->D, elt, true)) != LCE_OK) return s;
+    if ((s = check_side(a->dv, a->dv_ts, a->dv_hs, a->Tk, a->Hk, a->D, elt, true)) != LCE_OK) return s;
+    HostDev dev;
+    if ((s = host_device(&dev)) != LCE_OK) return s;
+    if (a->Tq == 0 && a->Tk == 0) return LCE_OK;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
+    HostScratch scratch(st);
+    uint8_t *base = nullptr;
+    const size_t need = lce_attention_workspace_size(a);
+    if ((s = scratch.get(a->workspace, a->workspace_bytes, need, &base)) != LCE_OK) return s;
+    AttnArgs r = make_args(a, dev);
+    r.stat_stride = seq_slots(a->Tq, a->B, stat_tile(a)) * stat_tile(a);
+    r.lse2 = reinterpret_cast<float *>(base);
+    r.delta = r.lse2 + r.stat_stride * r.Hq;
+    if (a->dtype == LCE_BF16)
+        return a->D <= 64 ? backward_simt<__nv_bfloat16, 64>(r, st) : backward_simt<__nv_bfloat16, 128>(r, st);
+    return a->D <= 64 ? backward_simt<float, 64>(r, st) : backward_simt<float, 128>(r, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,155 @@
+// Attention over packed sequences: what every kernel of it shares. Arguments,
+// the map from a tile slot to its sequence, and the backward's row statistics.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <math.h>
+#include <stdint.h>
+
+namespace lce {
+
+constexpr float kAttnLog2e = 1.4426950408889634f;
+constexpr int kDevSeqlens = 4;   // LCE_DEV_SEQLENS
+constexpr int kDevTimeout = 2;   // LCE_DEV_TIMEOUT
+
+// Token ranges of the sequences of one side. Without offsets every sequence
+// has `len` tokens. Sequence number B is the tail: the tokens after cu[B],
+// which belong to no sequence and see an empty other side.
+struct SeqMap {
+    const int *cu;
+    int B, T, len;
+    __device__ __forceinline__ int raw(int b) const { return cu ? cu[b] : b * len; }
+    // first token of sequence b (b <= B), within [0, T] whatever the offsets hold
+    __device__ __forceinline__ int start(int b) const { return min(max(raw(b), 0), T); }
+    __device__ __forceinline__ int end(int b) const { return b >= B ? T : max(min(max(raw(b + 1), 0), T), start(b)); }
+};
+
+// Tile t of sequence b has the slot start(b)/TILE + b + t. Slots of different
+// sequences never meet (a sequence of L tokens from s on has at most
+// (s+L)/TILE - s/TILE + 1 tiles), so a tile finds its sequence by searching
+// one ascending function of the offsets and no tile list has to be built
+// first; at most B+1 slots are empty.
+__host__ __device__ inline int64_t seq_slots(int64_t T, int64_t B, int tile) { return T / tile + B + 1; }
+template <int TILE>
+__device__ __forceinline__ int slot_base(const SeqMap &m, int b) {
+    return m.start(b) / TILE + b;
+}
+
+struct AttnArgs {
+    const void *q, *k, *v, *o_in, *dO;
+    void *o, *dq, *dk, *dv;
+    float *lse;
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs, dO_ts, dO_hs, dq_ts, dq_hs, dk_ts, dk_hs, dv_ts, dv_hs;
+    SeqMap sq, sk;
+    int Hq, Hk, group, D;
+    int causal;
+    float scale, scale_log2;   // scale, scale * log2(e)
+    // backward: per query slot row, lse * log2(e) (+inf where the row takes no
+    // part) and delta; [Hq][slots * TILE]
+    float *lse2, *delta;
+    int64_t stat_stride;       // slots * TILE
+    int *status;
+};
+
+// The sequence whose tiles may include `slot`: the largest b in [0, B] with
+// slot_base(b) <= slot. All 32 lanes take part, each probing one of 32 points
+// of what is left, so 1024 sequences take two rounds of loads.
+template <int TILE>
+__device__ __forceinline__ int find_seq(const SeqMap &m, int slot) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = m.B + 1;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int off = lane * step;
+        const bool le = off < n && slot_base<TILE>(m, lo + off) <= slot;
+        const unsigned mask = __ballot_sync(0xffffffffu, le);
+        // offsets that do not ascend may leave holes; the highest hit is still inside [lo, lo + n)
+        const int hit = mask ? 31 - __clz(mask) : 0;
+        lo += hit * step;
+        n = min(step, n - hit * step);
+    }
+    return lo;
+}
+
+// One tile of one side: its sequence, its row range on both sides.
+struct TileInfo {
+    int b;             // sequence
+    int s0, len;       // first token and length of the sequence on the tile's own side
+    int t0;            // first row of the tile within the sequence
+    int o0, olen;      // first token and length of the sequence on the other side (tail: empty)
+};
+template <int TILE>
+__device__ __forceinline__ TileInfo tile_info(const SeqMap &own, const SeqMap &other, int slot) {
+    TileInfo t;
+    t.b = find_seq<TILE>(own, slot);
+    t.s0 = own.start(t.b);
+    t.len = own.end(t.b) - t.s0;
+    t.t0 = (slot - (t.s0 / TILE + t.b)) * TILE;
+    t.o0 = other.start(t.b);
+    t.olen = t.b < own.B ? other.end(t.b) - t.o0 : 0;
+    return t;
+}
+
+// Offsets must ascend from 0 within the tokens; one warp of one block looks.
+__device__ __forceinline__ void check_offsets(const SeqMap &m, int *status) {
+    if (!m.cu) return;
+    bool bad = false;
+    for (int b = threadIdx.x & 31; b <= m.B; b += 32) {
+        const int v = m.cu[b];
+        bad |= b == 0 ? v != 0 : v < m.cu[b - 1];
+        bad |= v > m.T;
+    }
+    if (bad) atomicOr(status, kDevSeqlens);
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Row statistics of the backward, by slot: delta_i = dO_i . o_i in fp32 and
+// lse_i in base 2, so that the gradient kernels read aligned rows of TILE
+// values. Rows without an allowed key (lse = -inf) and rows past a sequence's
+// end get lse2 = +inf: their probabilities come out as 2^-inf = 0.
+template <typename T, int TILE>
+__global__ void __launch_bounds__(256) k_attn_stats(const AttnArgs a) {
+    const int h = blockIdx.x % a.Hq;
+    const int slot = blockIdx.x / a.Hq;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0 && warp == 0) {
+        check_offsets(a.sq, a.status);
+        check_offsets(a.sk, a.status);
+    }
+    const TileInfo t = tile_info<TILE>(a.sq, a.sk, slot);
+    const T *o = static_cast<const T *>(a.o_in) + h * a.o_hs;
+    const T *g = static_cast<const T *>(a.dO) + h * a.dO_hs;
+    for (int r = warp; r < TILE; r += 8) {
+        const int i = t.t0 + r;
+        float lse2 = INFINITY, delta = 0.f;
+        if (i >= 0 && i < t.len) {
+            const int64_t tok = t.s0 + i;
+            const float l = a.lse[static_cast<int64_t>(h) * a.sq.T + tok];
+            if (l != -INFINITY && t.olen > 0) {
+                for (int c = lane; c < a.D; c += 32)
+                    delta = fmaf(to_f32(o[tok * a.o_ts + c]), to_f32(g[tok * a.dO_ts + c]), delta);
+                for (int m = 16; m; m >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, m);
+                lse2 = l * kAttnLog2e;
+            }
+        }
+        if (lane == 0) {
+            const int64_t at = h * a.stat_stride + static_cast<int64_t>(slot) * TILE + r;
+            a.lse2[at] = lse2;
+            a.delta[at] = delta;
+        }
+    }
+}
+
+}  // namespace lce

@@ -1,0 +1,267 @@
+// Global gradient norm over many tensors, and clipping by it.
+#include <cuda_bf16.h>
+
+#include "lce_host.h"
+
+using namespace lce;
+
+namespace {
+
+constexpr int kClipThreads = 256;
+constexpr int kChunkBytes = 32768;   // bytes of a tensor that a block takes at a time
+constexpr int kTable = 240;          // tensors a launch takes (the table travels as a kernel argument)
+constexpr int kBlocksPerSm = 8;
+constexpr int kMaxBlocks = 256 * kBlocksPerSm;
+
+struct ClipEntry {
+    const void *g;
+    void *out;
+    int64_t n;
+    int first;   // number of the tensor's first chunk within the launch
+    int fp32;
+};
+struct ClipTable {
+    ClipEntry t[kTable];
+    int count, chunks;
+};
+
+__device__ __forceinline__ int entry_of(const ClipTable &tab, int chunk) {
+    int lo = 0, hi = tab.count;   // the last entry with first <= chunk
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (tab.t[mid].first <= chunk) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// A chunk of a tensor: elements [begin, end), of which [vec, vec + 16-byte
+// multiple) can be taken 16 bytes at a time. Chunks are cut at multiples of
+// kChunkBytes of the address, so only a tensor's ends are ragged.
+struct Span {
+    int64_t begin, end, vb, ve;
+};
+template <typename T>
+__device__ __forceinline__ Span span_of(const ClipEntry &e, int chunk) {
+    constexpr int kPer = kChunkBytes / sizeof(T), kV = 16 / sizeof(T);
+    const int64_t lead = (reinterpret_cast<uintptr_t>(e.g) % 16) / sizeof(T);   // elements past a 16-byte boundary
+    Span s;
+    s.begin = static_cast<int64_t>(chunk) * kPer - lead;
+    s.end = min(s.begin + kPer, e.n);
+    s.vb = max(s.begin, int64_t(0));
+    if (s.begin < 0 && lead) s.vb = kV - lead;
+    s.begin = max(s.begin, int64_t(0));
+    s.vb = min(s.vb, s.end);
+    s.ve = s.vb + (s.end - s.vb) / kV * kV;
+    return s;
+}
+
+__device__ __forceinline__ float f32(float x) { return x; }
+__device__ __forceinline__ float f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+__device__ __forceinline__ float squares(const float4 &v, float s) {
+    return fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, s))));
+}
+__device__ __forceinline__ float squares16(const uint4 &v, float s) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xffff0000u);
+        s = fmaf(a, a, fmaf(b, b, s));
+    }
+    return s;
+}
+
+template <typename T>
+__device__ __forceinline__ float span_squares(const ClipEntry &e, const Span &sp) {
+    const T *g = static_cast<const T *>(e.g);
+    constexpr int kV = 16 / sizeof(T);
+    float s = 0.f;
+    for (int64_t i = sp.begin + threadIdx.x; i < sp.vb; i += kClipThreads) s = fmaf(f32(g[i]), f32(g[i]), s);
+    for (int64_t i = sp.vb + threadIdx.x * kV; i < sp.ve; i += kClipThreads * kV) {
+        if (sizeof(T) == 4) s = squares(*reinterpret_cast<const float4 *>(g + i), s);
+        else s = squares16(*reinterpret_cast<const uint4 *>(g + i), s);
+    }
+    for (int64_t i = sp.ve + threadIdx.x; i < sp.end; i += kClipThreads) s = fmaf(f32(g[i]), f32(g[i]), s);
+    return s;
+}
+
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double red[kClipThreads / 32];
+    for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0.0;
+    for (int i = 0; i < kClipThreads / 32; ++i) v += red[i];
+    return v;
+}
+
+// part[block] = sum of the squares of the block's chunks: fp32 along a
+// thread's elements of one chunk, fp64 across chunks and threads.
+__global__ void __launch_bounds__(kClipThreads) k_clip_squares(const __grid_constant__ ClipTable tab, double *part) {
+    double s = 0.0;
+    for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
+        const ClipEntry &e = tab.t[entry_of(tab, c)];
+        s += e.fp32 ? span_squares<float>(e, span_of<float>(e, c - e.first))
+                    : span_squares<__nv_bfloat16>(e, span_of<__nv_bfloat16>(e, c - e.first));
+    }
+    s = block_sum(s);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+__device__ __forceinline__ float norm_of(const double *part, int n) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n; i += kClipThreads) s += part[i];
+    return static_cast<float>(sqrt(block_sum(s)));
+}
+
+__global__ void __launch_bounds__(kClipThreads) k_clip_norm(const double *part, int n, float *norm) {
+    const float v = norm_of(part, n);
+    if (threadIdx.x == 0) *norm = v;
+}
+
+template <typename T>
+__device__ __forceinline__ void span_scale(const ClipEntry &e, const Span &sp, float c) {
+    const T *g = static_cast<const T *>(e.g);
+    T *o = static_cast<T *>(e.out);
+    constexpr int kV = 16 / sizeof(T);
+    // an output that lies otherwise than its gradient takes single elements
+    const bool vec = (reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(o)) % 16 == 0;
+    const int64_t vb = vec ? sp.vb : sp.begin, ve = vec ? sp.ve : sp.begin;
+    for (int64_t i = sp.begin + threadIdx.x; i < vb; i += kClipThreads) o[i] = static_cast<T>(f32(g[i]) * c);
+    for (int64_t i = vb + threadIdx.x * kV; i < ve; i += kClipThreads * kV) {
+        if (sizeof(T) == 4) {
+            float4 v = *reinterpret_cast<const float4 *>(g + i);
+            *reinterpret_cast<float4 *>(o + i) = make_float4(v.x * c, v.y * c, v.z * c, v.w * c);
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4 *>(g + i);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(w[k] << 16) * c,
+                                                         __uint_as_float(w[k] & 0xffff0000u) * c);
+                w[k] = *reinterpret_cast<uint32_t *>(&p);
+            }
+            *reinterpret_cast<uint4 *>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    for (int64_t i = ve + threadIdx.x; i < sp.end; i += kClipThreads) o[i] = static_cast<T>(f32(g[i]) * c);
+}
+
+// Every block adds up the partial sums itself (a few KB, in L2), forms the
+// factor and scales its chunks.
+__global__ void __launch_bounds__(kClipThreads) k_clip_scale(const __grid_constant__ ClipTable tab, const double *part,
+                                                             int n, float max_norm, float eps, int in_place,
+                                                             float *norm, float *factor) {
+    const float v = norm_of(part, n);
+    float c = max_norm / (v + eps);
+    if (c > 1.f) c = 1.f;   // a NaN stays
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *norm = v;
+        if (factor) *factor = c;
+    }
+    if (in_place && c == 1.f) return;
+    for (int k = blockIdx.x; k < tab.chunks; k += gridDim.x) {
+        const ClipEntry &e = tab.t[entry_of(tab, k)];
+        if (e.fp32) span_scale<float>(e, span_of<float>(e, k - e.first), c);
+        else span_scale<__nv_bfloat16>(e, span_of<__nv_bfloat16>(e, k - e.first), c);
+    }
+}
+
+lce_status_t check_clip(int64_t count, const void *const *grads, void *const *outs, const int64_t *sizes,
+                        const int32_t *dtypes, const float *norm) {
+    if (count < 0 || count >= (int64_t(1) << 24)) return LCE_ERR_SHAPE;
+    if (!norm || (count > 0 && (!grads || !sizes || !dtypes))) return LCE_ERR_NULL;
+    for (int64_t i = 0; i < count; ++i) {
+        if (dtypes[i] != LCE_BF16 && dtypes[i] != LCE_FP32) return LCE_ERR_DTYPE;
+        if (sizes[i] < 0 || sizes[i] >= (int64_t(1) << 40)) return LCE_ERR_SHAPE;
+        if (sizes[i] == 0) continue;
+        if (!grads[i] || (outs && !outs[i])) return LCE_ERR_NULL;
+        const uintptr_t elt = dtypes[i] == LCE_BF16 ? 2 : 4;
+        if (reinterpret_cast<uintptr_t>(grads[i]) % elt || (outs && reinterpret_cast<uintptr_t>(outs[i]) % elt))
+            return LCE_ERR_ALIGN;
+    }
+    return LCE_OK;
+}
+
+// The tensors from `*at` on that fit one launch.
+void fill_table(ClipTable &tab, int64_t *at, int64_t count, const void *const *grads, void *const *outs,
+                const int64_t *sizes, const int32_t *dtypes) {
+    tab.count = tab.chunks = 0;
+    for (; *at < count && tab.count < kTable; ++*at) {
+        const int64_t i = *at;
+        if (sizes[i] == 0) continue;
+        const int elt = dtypes[i] == LCE_BF16 ? 2 : 4;
+        const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(grads[i]) % 16);
+        const int64_t chunks = (sizes[i] * elt + lead + kChunkBytes - 1) / kChunkBytes;
+        if (tab.count && tab.chunks + chunks >= (int64_t(1) << 30)) break;
+        tab.t[tab.count++] = ClipEntry{grads[i], outs ? outs[i] : const_cast<void *>(grads[i]), sizes[i], tab.chunks,
+                                       dtypes[i] == LCE_FP32};
+        tab.chunks += static_cast<int>(chunks);
+    }
+}
+
+lce_status_t run_clip(int64_t count, const void *const *grads, void *const *outs, const int64_t *sizes,
+                      const int32_t *dtypes, bool clip, float max_norm, float eps, float *norm, float *factor,
+                      void *workspace, size_t workspace_bytes, lce_stream_t stream) {
+    lce_status_t s = check_clip(count, grads, outs, sizes, dtypes, norm);
+    if (s != LCE_OK) return s;
+    HostDev dev;
+    if ((s = host_device(&dev)) != LCE_OK) return s;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    HostScratch scratch(st);
+    uint8_t *base = nullptr;
+    if ((s = scratch.get(workspace, workspace_bytes, lce_clip_workspace_size(count), &base)) != LCE_OK) return s;
+    double *part = reinterpret_cast<double *>(base);
+    ClipTable tab;
+    int n = 0;
+    const int most = dev.sms * kBlocksPerSm < kMaxBlocks ? dev.sms * kBlocksPerSm : kMaxBlocks;
+    for (int64_t at = 0; at < count;) {
+        fill_table(tab, &at, count, grads, outs, sizes, dtypes);
+        if (!tab.count) break;
+        const int blocks = tab.chunks < most ? tab.chunks : most;
+        k_clip_squares<<<blocks, kClipThreads, 0, st>>>(tab, part + n);
+        if ((s = host_launched()) != LCE_OK) return s;
+        n += blocks;
+    }
+    if (!clip) {
+        k_clip_norm<<<1, kClipThreads, 0, st>>>(part, n, norm);
+        return host_launched();
+    }
+    bool done = false;
+    for (int64_t at = 0; at < count || !done;) {
+        fill_table(tab, &at, count, grads, outs, sizes, dtypes);
+        if (!tab.count && done) break;
+        const int blocks = tab.chunks < 1 ? 1 : tab.chunks < most ? tab.chunks : most;
+        k_clip_scale<<<blocks, kClipThreads, 0, st>>>(tab, part, n, max_norm, eps, outs == nullptr, norm, factor);
+        if ((s = host_launched()) != LCE_OK) return s;
+        done = true;
+    }
+    return LCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lce_clip_workspace_size(int64_t count) {
+    if (count < 0 || count >= (int64_t(1) << 24)) return 0;
+    return static_cast<size_t>((count + kTable - 1) / kTable + 1) * kMaxBlocks * sizeof(double);
+}
+
+lce_status_t lce_grad_norm(int64_t count, const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                           float *norm, void *workspace, size_t workspace_bytes, lce_stream_t stream) {
+    return run_clip(count, grads, nullptr, sizes, dtypes, false, 0.f, 0.f, norm, nullptr, workspace, workspace_bytes,
+                    stream);
+}
+
+lce_status_t lce_clip_grads(int64_t count, const void *const *grads, void *const *outs, const int64_t *sizes,
+                            const int32_t *dtypes, float max_norm, float eps, float *norm, float *factor,
+                            void *workspace, size_t workspace_bytes, lce_stream_t stream) {
+    if (!(max_norm >= 0.f) || !(eps >= 0.f)) return LCE_ERR_ARG;
+    return run_clip(count, grads, outs, sizes, dtypes, true, max_norm, eps, norm, factor, workspace, workspace_bytes,
+                    stream);
+}
+
+}  // extern "C"

@@ -82,6 +82,7 @@ typedef enum { LCE_BF16 = 0, LCE_FP32 = 1 } lce_dtype_t;
 /* Bits of the device status word (lce_get_device_status). */
 #define LCE_DEV_TARGET_RANGE 0x1  /* a non-ignored target was outside [0, V) */
 #define LCE_DEV_TIMEOUT      0x2  /* a pipeline wait gave up; that kernel returned early */
+#define LCE_DEV_SEQLENS      0x4  /* sequence offsets of an attention call that are not ascending within the tokens */
 
 /*
  * Forward only: writes the mean loss to the device scalar `loss`.
@@ -231,8 +232,8 @@ size_t lce_workspace_size_args(const lce_args_t *args);
 /*
  * Synchronises `stream`, then returns in *bits the current device's status
  * word (LCE_DEV_* bits accumulated since the last read) and clears it.
- * Returns LCE_ERR_TARGET_RANGE or LCE_ERR_TIMEOUT when the matching bit is
- * set, LCE_OK when the word is clear.
+ * Returns LCE_ERR_TARGET_RANGE, LCE_ERR_TIMEOUT or (LCE_DEV_SEQLENS)
+ * LCE_ERR_SHAPE when the matching bit is set, LCE_OK when the word is clear.
  */
 lce_status_t lce_get_device_status(lce_stream_t stream, int32_t *bits);
 
@@ -338,6 +339,131 @@ lce_status_t lce_embedding_backward(lce_dtype_t dtype, const void *dE, const int
 lce_status_t lce_embedding_backward_bf16(lce_dtype_t dtype, const void *dE, const int64_t *tokens, int64_t pad_id,
                                          int64_t N, int64_t d, int64_t V, void *dW, void *workspace,
                                          size_t workspace_bytes, lce_stream_t stream);
+
+/*
+ * Attention over packed sequences, and its backward pass: the mixing layer of
+ * a block between the embedding lookup and the head loss. For query token i
+ * and key token j of the same sequence,
+ *   s_ij  = scale * q_i . k_j,  allowed where not causal, or
+ *           pos(j) <= pos(i) + Lk - Lq   (causal, aligned at the ends),
+ *   lse_i = log sum_j exp(s_ij),   o_i = sum_j exp(s_ij - lse_i) v_j,
+ * and from (q, k, v, o, lse, dO), with the probabilities recomputed,
+ *   p_ij = exp(s_ij - lse_i),  delta_i = dO_i . o_i,
+ *   ds_ij = p_ij (dO_i . v_j - delta_i),
+ *   dq_i = scale * sum_j ds_ij k_j,  dk_j = scale * sum_i ds_ij q_i,
+ *   dv_j = sum_i p_ij dO_i,
+ * dk and dv summed over the query heads that share a key head. A row with no
+ * allowed key has o = 0, lse = -inf and no gradient.
+ *
+ * Layout. Token-major [tokens][heads][D]: element (t, h, c) of q lies at
+ * q + t*q_ts + h*q_hs + c, strides in elements, so q, k and v may be slices of
+ * one projection's output and dq, dk, dv slices of its gradient. lse is fp32
+ * [Hq][Tq], contiguous. cu_q and cu_k hold the B+1 ascending token offsets of
+ * the sequences (device int32, cu[0] = 0, cu[B] <= tokens); tokens after
+ * cu[B] belong to no sequence (o = 0, lse = -inf, zero gradients). NULL: B
+ * sequences of equal length. Either side of a sequence may be empty. Values of
+ * one sequence, infinities and NaN among them, never reach another sequence;
+ * inside a sequence a non-finite masked key or value may reach the rows that
+ * share its 128-token tile.
+ *
+ * dtype LCE_BF16 runs on the bf16 tensor cores with fp32 accumulation (the
+ * probabilities and their gradient are rounded to bf16 once, as operands);
+ * LCE_FP32 runs in fp32 arithmetic throughout. Requirements: 1 <= D <= 128,
+ * D % 8 == 0, Hq a multiple of Hk, 0 <= Tq, Tk < 2^30, 1 <= B < 2^30, Tq and Tk multiples
+ * of B without offsets; bases 16-byte aligned, strides multiples of 16 bytes,
+ * non-negative and (but for a single head or token) not zero for outputs.
+ * Results are deterministic. Scratch: lce_attention_workspace_size bytes
+ * (backward only), device, 16-byte aligned, or NULL for a stream-ordered
+ * allocation. Offsets that are not ascending within the tokens set
+ * LCE_DEV_SEQLENS; the outputs are then unspecified.
+ */
+typedef struct {
+    lce_dtype_t dtype;
+    int causal;
+    float scale;
+    int64_t B, Tq, Tk, Hq, Hk, D;
+    const int32_t *cu_q, *cu_k;      /* [B+1] device, or both NULL */
+    const void *q, *k, *v;
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;
+    void *o;                         /* [Tq][Hq][D]: written by the forward, read by the backward */
+    int64_t o_ts, o_hs;
+    float *lse;                      /* [Hq][Tq]: written by the forward, read by the backward */
+    const void *dO;                  /* backward only, as are the rest */
+    int64_t dO_ts, dO_hs;
+    void *dq, *dk, *dv;
+    int64_t dq_ts, dq_hs, dk_ts, dk_hs, dv_ts, dv_hs;
+    void *workspace;
+    size_t workspace_bytes;
+    lce_stream_t stream;
+} lce_attn_t;
+lce_status_t lce_attention_forward(const lce_attn_t *args);
+lce_status_t lce_attention_backward(const lce_attn_t *args);
+size_t lce_attention_workspace_size(const lce_attn_t *args);
+
+/*
+ * The norms before and after a block, fused with the block's gate and
+ * residual scale. For the residual stream x, the block's output b and
+ * rms(t) = sqrt(mean(t^2) + eps) over the d channels of a row:
+ *   y = b / rms(b) * w_post     (y = b without w_post)
+ *   r = x + scale * gate * y    (gate: none, [d], or [N,d] with gate_full)
+ *   n = r / rms(r) * w_pre      (the next block's input; absent without w_pre)
+ * The forward writes r, n and the fp32 rows rstd_post = 1/rms(b) and
+ * rstd_pre = 1/rms(r); r may be x (updated in place). Without b, r is x itself
+ * and only n and rstd_pre are written (r NULL). The backward takes r, b and
+ * the stored rstd, the gradients dr (of r, or NULL for zero) and dn (of n),
+ * and writes
+ *   dx = dr + rstd_pre * (u - rhat * mean(u * rhat)),   u = w_pre * dn,
+ *   dy = scale * gate * dx,  dgate = scale * dx * y (summed over rows for [d]),
+ *   db = rstd_post * (t - bhat * mean(t * bhat)),       t = w_post * dy,
+ *   dw_post = sum over rows of dy * bhat,  dw_pre = sum of dn * rhat,
+ * each rounded once to its own type. All tensors are of `dtype` (statistics
+ * fp32), rows of d contiguous elements, ld_* apart (0 = d); outputs are
+ * contiguous. d % 8 == 0, 8 <= d <= 16384, 0 <= N < 2^31, bases and row
+ * strides 16-byte aligned. Sums are fp32 in a fixed order (deterministic).
+ * Scratch (backward): lce_block_norm_workspace_size bytes or NULL.
+ */
+typedef struct {
+    lce_dtype_t dtype;
+    int64_t N, d;
+    float scale, eps;
+    const void *x, *b;
+    const void *w_post, *gate, *w_pre;
+    int gate_full;                   /* nonzero: gate is [N,d] */
+    int64_t ld_x, ld_b, ld_gate;
+    void *r, *n;                     /* r: written by the forward, read by the backward */
+    float *rstd_post, *rstd_pre;     /* [N]: written by the forward, read by the backward */
+    const void *dr, *dn;             /* backward only, as are the rest */
+    int64_t ld_r, ld_dr, ld_dn;
+    void *dx, *db, *dw_post, *dgate, *dw_pre;
+    void *workspace;
+    size_t workspace_bytes;
+    lce_stream_t stream;
+} lce_norm_t;
+lce_status_t lce_block_norm_forward(const lce_norm_t *args);
+lce_status_t lce_block_norm_backward(const lce_norm_t *args);
+size_t lce_block_norm_workspace_size(const lce_norm_t *args);
+
+/*
+ * Global gradient norm over `count` tensors and clipping by it:
+ *   norm = sqrt( sum over all elements of g^2 ),
+ *   factor = min(1, max_norm / (norm + eps)),   out = g * factor.
+ * grads, outs, sizes and dtypes are HOST arrays of `count` entries (device
+ * tensor addresses, element counts, lce_dtype_t); tensors are contiguous, of
+ * any size (zero included) and aligned to their element. outs NULL clips in
+ * place, and then writes nothing where the factor is 1; an out may be its own
+ * grad and must not overlap any other tensor. A norm that is not finite gives
+ * factor 0 (infinite) or NaN, as the formulas say. norm is a device fp32
+ * scalar; factor an optional one. The squares are summed in fp32 over short
+ * runs and in fp64 across them, in a fixed order (deterministic); an element
+ * beyond 1.8e19 makes the norm infinite. Scratch: lce_clip_workspace_size
+ * bytes of device memory (16-byte aligned) or NULL.
+ */
+size_t lce_clip_workspace_size(int64_t count);
+lce_status_t lce_grad_norm(int64_t count, const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                           float *norm, void *workspace, size_t workspace_bytes, lce_stream_t stream);
+lce_status_t lce_clip_grads(int64_t count, const void *const *grads, void *const *outs, const int64_t *sizes,
+                            const int32_t *dtypes, float max_norm, float eps, float *norm, float *factor,
+                            void *workspace, size_t workspace_bytes, lce_stream_t stream);
 
 /* ABI version: major*10000 + minor*100 + patch. */
 int lce_version(void);
