@@ -1,5 +1,7 @@
 // Host side of attention over packed sequences: argument checks, workspace
 // and launches.
+#include "lce_attn_bwd.cuh"
+#include "lce_attn_fwd.cuh"
 #include "lce_attn_simt.cuh"
 #include "lce_host.h"
 
@@ -13,6 +15,7 @@ lce_status_t check_side(const void *p, int64_t ts, int64_t hs, int64_t T, int64_
     if (!p) return LCE_ERR_NULL;
     if (host_misaligned(p) || (ts * elt) % 16 || (hs * elt) % 16) return LCE_ERR_ALIGN;
     if (ts < 0 || hs < 0 || ts >= (int64_t(1) << 36) || hs >= (int64_t(1) << 36)) return LCE_ERR_SHAPE;
+    if ((T > 1 && ts == 0) || (H > 1 && hs == 0)) return LCE_ERR_SHAPE;   // tensor maps have no zero strides
     // rows of an output must not meet
     if (out && ((T > 1 && ts < D) || (H > 1 && hs < D))) return LCE_ERR_SHAPE;
     return LCE_OK;
@@ -65,6 +68,23 @@ AttnArgs make_args(const lce_attn_t *a, const HostDev &dev) {
     return r;
 }
 
+// Tensor map of [tokens][heads][D] bf16 for boxes of 128 tokens of one head by
+// 64 channels. A tensor without tokens is never loaded from.
+lce_status_t encode(CUtensorMap *m, const HostDev &dev, const void *p, int64_t T, int64_t H, int64_t D, int64_t ts,
+                    int64_t hs) {
+    if (T == 0) return LCE_OK;
+    if (H == 1) hs = D;   // strides of dimensions of one entry are not used, but have to be valid
+    if (T == 1) ts = D;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(hs) * 2, static_cast<cuuint64_t>(ts) * 2};
+    cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(kTcTile)};
+    cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r = dev.encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
+                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? LCE_OK : LCE_ERR_SHAPE;
+}
+
 template <typename K, typename... A>
 lce_status_t launch(K kernel, int64_t blocks, int threads, int smem, cudaStream_t st, const A &...args) {
     if (blocks <= 0) return LCE_OK;
@@ -78,22 +98,47 @@ lce_status_t launch(K kernel, int64_t blocks, int threads, int smem, cudaStream_
     return host_launched();
 }
 
-template <typename T, int DP>
-lce_status_t forward_simt(const AttnArgs &r, cudaStream_t st) {
-    const int64_t slots = seq_slots(r.sq.T, r.sq.B, kSimtTile);
-    return launch(k_attn_fwd_simt<T, DP>, slots * r.Hq, kSimtThreads, simt_smem(DP, 3, 1), st, r);
+template <int NB>
+lce_status_t forward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
+    AttnMaps maps;
+    lce_status_t s = encode(&maps.q, dev, a->q, a->Tq, a->Hq, a->D, a->q_ts, a->q_hs);
+    if (s == LCE_OK) s = encode(&maps.k, dev, a->k, a->Tk, a->Hk, a->D, a->k_ts, a->k_hs);
+    if (s == LCE_OK) s = encode(&maps.v, dev, a->v, a->Tk, a->Hk, a->D, a->v_ts, a->v_hs);
+    if (s != LCE_OK) return s;
+    return launch(k_attn_fwd<NB>, seq_slots(r.sq.T, r.sq.B, kTcTile) * r.Hq, kFwdThreads, FwdSmem<NB>::kBytes, st, r,
+                  maps);
 }
 
-template <typename T, int DP>
+template <int DP>
+lce_status_t forward_simt(const AttnArgs &r, cudaStream_t st) {
+    const int64_t slots = seq_slots(r.sq.T, r.sq.B, kSimtTile);
+    return launch(k_attn_fwd_simt<DP>, slots * r.Hq, kSimtThreads, simt_smem(DP, 3, 1), st, r);
+}
+
+template <int DP>
 lce_status_t backward_simt(const AttnArgs &r, cudaStream_t st) {
     const int64_t qslots = seq_slots(r.sq.T, r.sq.B, kSimtTile), kslots = seq_slots(r.sk.T, r.sk.B, kSimtTile);
-    lce_status_t s = launch(k_attn_stats<T, kSimtTile>, qslots * r.Hq, 256, 0, st, r);
-    if (s == LCE_OK && r.sq.T > 0) s = launch(k_attn_dq_simt<T, DP>, qslots * r.Hq, kSimtThreads, simt_smem(DP, 4, 1), st, r);
-    if (s == LCE_OK && r.sk.T > 0) s = launch(k_attn_dkv_simt<T, DP>, kslots * r.Hk, kSimtThreads, simt_smem(DP, 4, 2), st, r);
+    lce_status_t s = launch(k_attn_stats<float, kSimtTile>, qslots * r.Hq, 256, 0, st, r);
+    if (s == LCE_OK && r.sq.T > 0) s = launch(k_attn_dq_simt<DP>, qslots * r.Hq, kSimtThreads, simt_smem(DP, 4, 1), st, r);
+    if (s == LCE_OK && r.sk.T > 0) s = launch(k_attn_dkv_simt<DP>, kslots * r.Hk, kSimtThreads, simt_smem(DP, 4, 2), st, r);
     return s;
 }
 
-int stat_tile(const lce_attn_t *) { return kSimtTile; }
+template <int NB>
+lce_status_t backward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
+    AttnMaps maps;
+    lce_status_t s = encode(&maps.q, dev, a->q, a->Tq, a->Hq, a->D, a->q_ts, a->q_hs);
+    if (s == LCE_OK) s = encode(&maps.k, dev, a->k, a->Tk, a->Hk, a->D, a->k_ts, a->k_hs);
+    if (s == LCE_OK) s = encode(&maps.v, dev, a->v, a->Tk, a->Hk, a->D, a->v_ts, a->v_hs);
+    if (s == LCE_OK) s = encode(&maps.dO, dev, a->dO, a->Tq, a->Hq, a->D, a->dO_ts, a->dO_hs);
+    const int64_t qslots = seq_slots(r.sq.T, r.sq.B, kTcTile), kslots = seq_slots(r.sk.T, r.sk.B, kTcTile);
+    if (s == LCE_OK) s = launch(k_attn_stats<__nv_bfloat16, kTcTile>, qslots * r.Hq, 256, 0, st, r);
+    if (s == LCE_OK && r.sk.T > 0) s = launch(k_attn_dkv<NB>, kslots * r.Hk, kBwdThreads, DkvSmem<NB>::kBytes, st, r, maps);
+    if (s == LCE_OK && r.sq.T > 0) s = launch(k_attn_dq<NB>, qslots * r.Hq, kBwdThreads, DqSmem<NB>::kBytes, st, r, maps);
+    return s;
+}
+
+int stat_tile(const lce_attn_t *a) { return a->dtype == LCE_BF16 ? kTcTile : kSimtTile; }
 
 }  // namespace
 
@@ -116,8 +161,8 @@ lce_status_t lce_attention_forward(const lce_attn_t *a) {
     const AttnArgs r = make_args(a, dev);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
     if (a->dtype == LCE_BF16)
-        return a->D <= 64 ? forward_simt<__nv_bfloat16, 64>(r, st) : forward_simt<__nv_bfloat16, 128>(r, st);
-    return a->D <= 64 ? forward_simt<float, 64>(r, st) : forward_simt<float, 128>(r, st);
+        return a->D <= 64 ? forward_tc<1>(a, r, dev, st) : forward_tc<2>(a, r, dev, st);
+    return a->D <= 64 ? forward_simt<64>(r, st) : forward_simt<128>(r, st);
 }
 
 lce_status_t lce_attention_backward(const lce_attn_t *a) {
@@ -142,8 +187,8 @@ lce_status_t lce_attention_backward(const lce_attn_t *a) {
     r.lse2 = reinterpret_cast<float *>(base);
     r.delta = r.lse2 + r.stat_stride * r.Hq;
     if (a->dtype == LCE_BF16)
-        return a->D <= 64 ? backward_simt<__nv_bfloat16, 64>(r, st) : backward_simt<__nv_bfloat16, 128>(r, st);
-    return a->D <= 64 ? backward_simt<float, 64>(r, st) : backward_simt<float, 128>(r, st);
+        return a->D <= 64 ? backward_tc<1>(a, r, dev, st) : backward_tc<2>(a, r, dev, st);
+    return a->D <= 64 ? backward_simt<64>(r, st) : backward_simt<128>(r, st);
 }
 
 }  // extern "C"

@@ -108,13 +108,6 @@ template <>
 __device__ __forceinline__ float to_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
 // Row statistics of the backward, by slot: delta_i = dO_i . o_i in fp32 and
 // lse_i in base 2, so that the gradient kernels read aligned rows of TILE
 // values. Rows without an allowed key (lse = -inf) and rows past a sequence's

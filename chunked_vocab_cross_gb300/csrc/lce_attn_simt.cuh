@@ -1,4 +1,4 @@
-// Attention in fp32 arithmetic: tiles of 64 queries by 64 keys in shared
+// Attention of fp32 tensors, in fp32 arithmetic: tiles of 64 queries by 64 keys in shared
 // memory, 256 threads in a 16 x 16 grid, each with four query rows (or key
 // rows) and every 16th column of each product. Bound by shared-memory loads
 // (eight for sixteen multiply-adds).
@@ -17,11 +17,11 @@ constexpr int simt_smem(int DP, int operands, int tiles) {
 }
 
 // rows [0, 64) x [0, DP) of fp32 from `rows` token rows of D elements; zero outside
-template <typename T, int DP>
-__device__ __forceinline__ void simt_load(float *dst, const T *src, int64_t stride, int rows, int D) {
+template <int DP>
+__device__ __forceinline__ void simt_load(float *dst, const float *src, int64_t stride, int rows, int D) {
     for (int i = threadIdx.x; i < kSimtTile * DP; i += kSimtThreads) {
         const int r = i / DP, c = i % DP;
-        dst[r * (DP + 1) + c] = (r < rows && c < D) ? to_f32(src[r * stride + c]) : 0.f;
+        dst[r * (DP + 1) + c] = (r < rows && c < D) ? src[r * stride + c] : 0.f;
     }
 }
 
@@ -52,18 +52,18 @@ __device__ __forceinline__ void simt_mix(const float *P, const float *B, int ty,
     }
 }
 
-template <typename T, int DP>
-__device__ __forceinline__ void simt_store(T *dst, int64_t stride, int rows, int D, int ty, int tx, float mul,
+template <int DP>
+__device__ __forceinline__ void simt_store(float *dst, int64_t stride, int rows, int D, int ty, int tx, float mul,
                                            const float (&acc)[4][DP / 16]) {
     for (int i = 0; i < 4; ++i) {
         const int r = ty * 4 + i;
         if (r >= rows) continue;
         for (int c = 0; c < DP / 16; ++c)
-            if (tx + 16 * c < D) dst[r * stride + tx + 16 * c] = from_f32<T>(acc[i][c] * mul);
+            if (tx + 16 * c < D) dst[r * stride + tx + 16 * c] = acc[i][c] * mul;
     }
 }
 
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kSimtThreads) k_attn_fwd_simt(const AttnArgs a) {
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + kSimtTile * (DP + 1), *V = K + kSimtTile * (DP + 1), *P = V + kSimtTile * (DP + 1);
@@ -78,14 +78,14 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_fwd_simt(const AttnArgs a
     if (t.t0 < 0 || rows <= 0) return;
     const int off = t.olen - t.len;   // causal: row i sees keys [0, i + off]
     const int kend = a.causal ? min(t.olen, t.t0 + rows + off) : t.olen;
-    simt_load<T, DP>(Q, static_cast<const T *>(a.q) + (t.s0 + t.t0) * a.q_ts + h * a.q_hs, a.q_ts, rows, a.D);
+    simt_load<DP>(Q, static_cast<const float *>(a.q) + (t.s0 + t.t0) * a.q_ts + h * a.q_hs, a.q_ts, rows, a.D);
     float o[4][DP / 16] = {}, m[4], l[4] = {};
     for (int i = 0; i < 4; ++i) m[i] = -INFINITY;
     for (int k0 = 0; k0 < kend; k0 += kSimtTile) {
         const int keys = min(kSimtTile, t.olen - k0);
         __syncthreads();
-        simt_load<T, DP>(K, static_cast<const T *>(a.k) + (t.o0 + k0) * a.k_ts + hk * a.k_hs, a.k_ts, keys, a.D);
-        simt_load<T, DP>(V, static_cast<const T *>(a.v) + (t.o0 + k0) * a.v_ts + hk * a.v_hs, a.v_ts, keys, a.D);
+        simt_load<DP>(K, static_cast<const float *>(a.k) + (t.o0 + k0) * a.k_ts + hk * a.k_hs, a.k_ts, keys, a.D);
+        simt_load<DP>(V, static_cast<const float *>(a.v) + (t.o0 + k0) * a.v_ts + hk * a.v_hs, a.v_ts, keys, a.D);
         __syncthreads();
         float s[4][4];
         simt_dot<DP>(Q, K, ty, tx, s);
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_fwd_simt(const AttnArgs a
             a.lse[static_cast<int64_t>(h) * a.sq.T + t.s0 + t.t0 + r] =
                 l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * (1.f / kAttnLog2e);
     }
-    simt_store<T, DP>(static_cast<T *>(a.o) + (t.s0 + t.t0) * a.o_ts + h * a.o_hs, a.o_ts, rows, a.D, ty, tx, 1.f, o);
+    simt_store<DP>(static_cast<float *>(a.o) + (t.s0 + t.t0) * a.o_ts + h * a.o_hs, a.o_ts, rows, a.D, ty, tx, 1.f, o);
 }
 
 // p and ds of one 64 x 64 tile from Q, K, dO, V in shared memory: rows are
@@ -147,7 +147,7 @@ __device__ __forceinline__ void simt_probs(const AttnArgs &a, const float *Q, co
     }
 }
 
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kSimtThreads) k_attn_dq_simt(const AttnArgs a) {
     extern __shared__ float sm[];
     constexpr int kOp = kSimtTile * (DP + 1);
@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_dq_simt(const AttnArgs a)
     const int off = t.olen - t.len;
     const int kend = a.causal ? min(t.olen, t.t0 + rows + off) : t.olen;
     const int64_t tok = t.s0 + t.t0;
-    simt_load<T, DP>(Q, static_cast<const T *>(a.q) + tok * a.q_ts + h * a.q_hs, a.q_ts, rows, a.D);
-    simt_load<T, DP>(G, static_cast<const T *>(a.dO) + tok * a.dO_ts + h * a.dO_hs, a.dO_ts, rows, a.D);
+    simt_load<DP>(Q, static_cast<const float *>(a.q) + tok * a.q_ts + h * a.q_hs, a.q_ts, rows, a.D);
+    simt_load<DP>(G, static_cast<const float *>(a.dO) + tok * a.dO_ts + h * a.dO_hs, a.dO_ts, rows, a.D);
     if (tid < kSimtTile) {
         const int64_t at = h * a.stat_stride + static_cast<int64_t>(slot) * kSimtTile + tid;
         stat[tid] = a.lse2[at];
@@ -171,17 +171,17 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_dq_simt(const AttnArgs a)
     for (int k0 = 0; k0 < kend; k0 += kSimtTile) {
         const int keys = min(kSimtTile, t.olen - k0);
         __syncthreads();
-        simt_load<T, DP>(K, static_cast<const T *>(a.k) + (t.o0 + k0) * a.k_ts + hk * a.k_hs, a.k_ts, keys, a.D);
-        simt_load<T, DP>(V, static_cast<const T *>(a.v) + (t.o0 + k0) * a.v_ts + hk * a.v_hs, a.v_ts, keys, a.D);
+        simt_load<DP>(K, static_cast<const float *>(a.k) + (t.o0 + k0) * a.k_ts + hk * a.k_hs, a.k_ts, keys, a.D);
+        simt_load<DP>(V, static_cast<const float *>(a.v) + (t.o0 + k0) * a.v_ts + hk * a.v_hs, a.v_ts, keys, a.D);
         __syncthreads();
         simt_probs<DP>(a, Q, K, G, V, stat, t.t0, k0, keys, off, ty, tx, nullptr, dS);
         __syncwarp();
         simt_mix<DP, false>(dS, K, ty, tx, acc);
     }
-    simt_store<T, DP>(static_cast<T *>(a.dq) + tok * a.dq_ts + h * a.dq_hs, a.dq_ts, rows, a.D, ty, tx, a.scale, acc);
+    simt_store<DP>(static_cast<float *>(a.dq) + tok * a.dq_ts + h * a.dq_hs, a.dq_ts, rows, a.D, ty, tx, a.scale, acc);
 }
 
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kSimtThreads) k_attn_dkv_simt(const AttnArgs a) {
     extern __shared__ float sm[];
     constexpr int kOp = kSimtTile * (DP + 1), kTl = kSimtTile * kSimtP;
@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_dkv_simt(const AttnArgs a
     if (t.t0 < 0 || keys <= 0) return;
     const int off = t.len - t.olen;
     const int64_t tok = t.s0 + t.t0;
-    simt_load<T, DP>(K, static_cast<const T *>(a.k) + tok * a.k_ts + hk * a.k_hs, a.k_ts, keys, a.D);
-    simt_load<T, DP>(V, static_cast<const T *>(a.v) + tok * a.v_ts + hk * a.v_hs, a.v_ts, keys, a.D);
+    simt_load<DP>(K, static_cast<const float *>(a.k) + tok * a.k_ts + hk * a.k_hs, a.k_ts, keys, a.D);
+    simt_load<DP>(V, static_cast<const float *>(a.v) + tok * a.v_ts + hk * a.v_hs, a.v_ts, keys, a.D);
     // the first query row that sees this tile's first key
     const int qfirst = a.causal ? max(0, t.t0 - off) / kSimtTile * kSimtTile : 0;
     float dk[4][DP / 16] = {}, dv[4][DP / 16] = {};
@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_dkv_simt(const AttnArgs a
             const int rows = min(kSimtTile, t.olen - q0);
             const int64_t qt = t.o0 + q0;
             __syncthreads();
-            simt_load<T, DP>(Q, static_cast<const T *>(a.q) + qt * a.q_ts + h * a.q_hs, a.q_ts, rows, a.D);
-            simt_load<T, DP>(G, static_cast<const T *>(a.dO) + qt * a.dO_ts + h * a.dO_hs, a.dO_ts, rows, a.D);
+            simt_load<DP>(Q, static_cast<const float *>(a.q) + qt * a.q_ts + h * a.q_hs, a.q_ts, rows, a.D);
+            simt_load<DP>(G, static_cast<const float *>(a.dO) + qt * a.dO_ts + h * a.dO_hs, a.dO_ts, rows, a.D);
             if (tid < kSimtTile) {
                 const int64_t at = h * a.stat_stride + static_cast<int64_t>(qslot0 + q0 / kSimtTile) * kSimtTile + tid;
                 stat[tid] = a.lse2[at];
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_dkv_simt(const AttnArgs a
             simt_mix<DP, true>(dS, Q, ty, tx, dk);
         }
     }
-    simt_store<T, DP>(static_cast<T *>(a.dk) + tok * a.dk_ts + hk * a.dk_hs, a.dk_ts, keys, a.D, ty, tx, a.scale, dk);
-    simt_store<T, DP>(static_cast<T *>(a.dv) + tok * a.dv_ts + hk * a.dv_hs, a.dv_ts, keys, a.D, ty, tx, 1.f, dv);
+    simt_store<DP>(static_cast<float *>(a.dk) + tok * a.dk_ts + hk * a.dk_hs, a.dk_ts, keys, a.D, ty, tx, a.scale, dk);
+    simt_store<DP>(static_cast<float *>(a.dv) + tok * a.dv_ts + hk * a.dv_hs, a.dv_ts, keys, a.D, ty, tx, 1.f, dv);
 }
 
 }  // namespace lce

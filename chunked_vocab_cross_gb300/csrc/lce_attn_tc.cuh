@@ -1,0 +1,149 @@
+// What the tensor-core attention kernels share: tiles of 128 tokens in
+// 128-byte-swizzled shared memory, bounded waits, MMA issue.
+//
+// A tile is NB column blocks (64 channels, 128 bytes a token) of 128 rows,
+// 16 KB each. Read along the channels (scores: A and B K-major) a K step of 16
+// channels is 32 bytes; read along the tokens (sums over tokens: B MN-major,
+// N = channels) a K step of 16 tokens is 2 KB and the next 64 channels are one
+// block, 16 KB, on. Channels past D arrive as zeros from the tensor map, so
+// any D runs as if rounded up to 16.
+#pragma once
+
+#include "lce_attn.cuh"
+#include "tc_ptx.cuh"
+
+namespace lce {
+
+constexpr int kTcTile = 128;
+constexpr int kTcBlock = kTcTile * 128;                 // bytes of one column block
+constexpr long long kTcWaitCycles = 2000000000LL;       // ~1 s: far above any legitimate wait
+constexpr long long kTcDrainCycles = 200000000LL;
+
+// Waits of one CTA: a wait that gives up raises the device status word and
+// the CTA's abort flag, on which all its other waits give up too.
+struct TcWaits {
+    volatile int *abort_flag;
+    int *status;
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
+        const uint32_t a = smem_u32(bar);
+        if (mbar_try_wait(a, parity)) return true;
+        const long long t0 = clock64();
+        for (;;) {
+            if (mbar_try_wait(a, parity)) return true;
+            if (*abort_flag) return false;
+            if (clock64() - t0 > kTcWaitCycles) {
+                *abort_flag = 1;
+                atomicOr(status, kDevTimeout);
+                return false;
+            }
+        }
+    }
+    // the same answer for all lanes of the warp
+    __device__ __forceinline__ bool all(uint64_t *bar, uint32_t parity) const {
+        return __all_sync(0xffffffffu, (*this)(bar, parity));
+    }
+};
+
+// Used only while shutting down: lets what is in flight land before the CTA
+// gives up its memory.
+__device__ __forceinline__ void tc_drain(uint64_t *bar, uint32_t parity) {
+    const uint32_t a = smem_u32(bar);
+    const long long t0 = clock64();
+    while (!mbar_try_wait(a, parity))
+        if (clock64() - t0 > kTcDrainCycles) return;
+}
+
+// One tile: 128 tokens of one head from token `tok` on. Tokens past the
+// tensor's end arrive as zeros; those of the next sequence as they are.
+template <int NB>
+__device__ __forceinline__ void tc_load_tile(uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int head, int tok) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) tma_load_3d(dst + b * kTcBlock, m, bar, b * 64, head, tok);
+}
+
+// Zeroes the rows from `rows` on of a loaded tile that is summed over its
+// tokens: 0 * NaN of a token beyond the sequence would reach every result.
+// Called by one whole warp between the load's arrival and the MMAs.
+template <int NB>
+__device__ __forceinline__ void tc_zero_rows(uint8_t *tile, int rows) {
+    const int lane = threadIdx.x & 31;
+    const int n = (kTcTile - rows) * 8;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        for (int i = lane; i < n; i += 32)
+            *reinterpret_cast<uint4 *>(tile + b * kTcBlock + rows * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// Descriptors of a tile read along its channels / along its tokens.
+__device__ __forceinline__ uint64_t tc_desc_k(const uint8_t *tile) { return sdesc_sw128(smem_u32(tile), 0, 1024); }
+__device__ __forceinline__ uint64_t tc_desc_mn(const uint8_t *tile) {
+    return sdesc_sw128(smem_u32(tile), kTcBlock, 1024);
+}
+// Offset of K step kk in descriptor units (16 bytes): along the channels, four steps a block.
+__device__ __forceinline__ uint64_t tc_step_k(int kk) { return (kk >> 2) * (kTcBlock >> 4) + (kk & 3) * 2; }
+__device__ __forceinline__ uint64_t tc_step_mn(int kk) { return kk * 128; }
+
+// D = A . B^T over the channels (both operands tiles).
+__device__ __forceinline__ void tc_mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int ksteps) {
+    for (int kk = 0; kk < ksteps; ++kk) umma_f16(d, a + tc_step_k(kk), b + tc_step_k(kk), idesc, kk > 0);
+}
+// D (+)= P . B over tokens: P in tensor memory (two tokens a column), B a tile.
+__device__ __forceinline__ void tc_mma_tokens(uint32_t d, uint32_t p, uint64_t b, uint32_t idesc, int ksteps,
+                                              bool accumulate) {
+    for (int kk = 0; kk < ksteps; ++kk) umma_f16_ts(d, p + kk * 8, b + tc_step_mn(kk), idesc, accumulate || kk > 0);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&p);
+}
+
+// 16-byte piece c of row r in a swizzled tile (byte offset).
+__device__ __forceinline__ int tc_piece(int r, int c) {
+    return (c >> 3) * kTcBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// Writes a warp's 32 rows of an accumulator to global memory as bf16: lane r
+// holds row r0 + r of the tile; the rows go through the warp's share of a free
+// tile, so that 16 (8 for 64 channels) lanes write one token's row.
+template <int NB>
+__device__ __forceinline__ void tc_store_rows(uint8_t *tile, uint32_t taddr, float mul, int r0, int rows,
+                                              __nv_bfloat16 *dst, int64_t stride, int D) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < NB * 2; ++c) {
+        uint32_t v[32];
+        tmem_ld32(taddr + c * 32, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 w;
+            w.x = pack_bf16(__uint_as_float(v[8 * i]) * mul, __uint_as_float(v[8 * i + 1]) * mul);
+            w.y = pack_bf16(__uint_as_float(v[8 * i + 2]) * mul, __uint_as_float(v[8 * i + 3]) * mul);
+            w.z = pack_bf16(__uint_as_float(v[8 * i + 4]) * mul, __uint_as_float(v[8 * i + 5]) * mul);
+            w.w = pack_bf16(__uint_as_float(v[8 * i + 6]) * mul, __uint_as_float(v[8 * i + 7]) * mul);
+            *reinterpret_cast<uint4 *>(tile + tc_piece(r0 + lane, c * 4 + i)) = w;
+        }
+    }
+    __syncwarp();
+    constexpr int kPer = NB * 8;   // pieces of a row
+#pragma unroll 4
+    for (int i = lane; i < 32 * kPer; i += 32) {
+        const int r = r0 + i / kPer, c = i % kPer;
+        if (r < rows && c * 8 < D)
+            *reinterpret_cast<uint4 *>(dst + r * stride + c * 8) = *reinterpret_cast<const uint4 *>(tile + tc_piece(r, c));
+    }
+}
+
+struct AttnMaps {
+    CUtensorMap q, k, v, dO;
+};
+
+}  // namespace lce

@@ -371,7 +371,7 @@ lce_status_t lce_embedding_backward_bf16(lce_dtype_t dtype, const void *dE, cons
  * LCE_FP32 runs in fp32 arithmetic throughout. Requirements: 1 <= D <= 128,
  * D % 8 == 0, Hq a multiple of Hk, 0 <= Tq, Tk < 2^30, 1 <= B < 2^30, Tq and Tk multiples
  * of B without offsets; bases 16-byte aligned, strides multiples of 16 bytes,
- * non-negative and (but for a single head or token) not zero for outputs.
+ * positive (but for a single head or token).
  * Results are deterministic. Scratch: lce_attention_workspace_size bytes
  * (backward only), device, 16-byte aligned, or NULL for a stream-ordered
  * allocation. Offsets that are not ascending within the tokens set
