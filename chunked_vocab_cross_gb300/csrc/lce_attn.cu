@@ -1,5 +1,7 @@
 // Host side of attention over packed sequences: argument checks, workspace
 // and launches.
+#include <type_traits>
+
 #include "lce_attn_bwd.cuh"
 #include "lce_attn_fwd.cuh"
 #include "lce_attn_simt.cuh"
@@ -98,14 +100,14 @@ lce_status_t launch(K kernel, int64_t blocks, int threads, int smem, cudaStream_
     return host_launched();
 }
 
-template <int NB>
+template <int KS>
 lce_status_t forward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
     AttnMaps maps;
     lce_status_t s = encode(&maps.q, dev, a->q, a->Tq, a->Hq, a->D, a->q_ts, a->q_hs);
     if (s == LCE_OK) s = encode(&maps.k, dev, a->k, a->Tk, a->Hk, a->D, a->k_ts, a->k_hs);
     if (s == LCE_OK) s = encode(&maps.v, dev, a->v, a->Tk, a->Hk, a->D, a->v_ts, a->v_hs);
     if (s != LCE_OK) return s;
-    return launch(k_attn_fwd<NB>, seq_slots(r.sq.T, r.sq.B, kTcTile) * r.Hq, kFwdThreads, FwdSmem<NB>::kBytes, st, r,
+    return launch(k_attn_fwd<KS>, seq_slots(r.sq.T, r.sq.B, kTcTile) * r.Hq, kFwdThreads, FwdSmem<KS>::kBytes, st, r,
                   maps);
 }
 
@@ -124,7 +126,7 @@ lce_status_t backward_simt(const AttnArgs &r, cudaStream_t st) {
     return s;
 }
 
-template <int NB>
+template <int KS>
 lce_status_t backward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
     AttnMaps maps;
     lce_status_t s = encode(&maps.q, dev, a->q, a->Tq, a->Hq, a->D, a->q_ts, a->q_hs);
@@ -133,9 +135,18 @@ lce_status_t backward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &
     if (s == LCE_OK) s = encode(&maps.dO, dev, a->dO, a->Tq, a->Hq, a->D, a->dO_ts, a->dO_hs);
     const int64_t qslots = seq_slots(r.sq.T, r.sq.B, kTcTile), kslots = seq_slots(r.sk.T, r.sk.B, kTcTile);
     if (s == LCE_OK) s = launch(k_attn_stats<__nv_bfloat16, kTcTile>, qslots * r.Hq, 256, 0, st, r);
-    if (s == LCE_OK && r.sk.T > 0) s = launch(k_attn_dkv<NB>, kslots * r.Hk, kBwdThreads, DkvSmem<NB>::kBytes, st, r, maps);
-    if (s == LCE_OK && r.sq.T > 0) s = launch(k_attn_dq<NB>, qslots * r.Hq, kBwdThreads, DqSmem<NB>::kBytes, st, r, maps);
+    if (s == LCE_OK && r.sk.T > 0) s = launch(k_attn_dkv<KS>, kslots * r.Hk, kBwdThreads, DkvSmem<KS>::kBytes, st, r, maps);
+    if (s == LCE_OK && r.sq.T > 0) s = launch(k_attn_dq<KS>, qslots * r.Hq, kBwdThreads, DqSmem<KS>::kBytes, st, r, maps);
     return s;
+}
+
+// The tensor-core kernels exist for 64, 80, 96 and 128 channels; others run as the next of these.
+template <typename F>
+lce_status_t by_channels(int64_t D, F f) {
+    if (D <= 64) return f(std::integral_constant<int, 4>());
+    if (D <= 80) return f(std::integral_constant<int, 5>());
+    if (D <= 96) return f(std::integral_constant<int, 6>());
+    return f(std::integral_constant<int, 8>());
 }
 
 int stat_tile(const lce_attn_t *a) { return a->dtype == LCE_BF16 ? kTcTile : kSimtTile; }
@@ -161,7 +172,7 @@ lce_status_t lce_attention_forward(const lce_attn_t *a) {
     const AttnArgs r = make_args(a, dev);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
     if (a->dtype == LCE_BF16)
-        return a->D <= 64 ? forward_tc<1>(a, r, dev, st) : forward_tc<2>(a, r, dev, st);
+        return by_channels(a->D, [&](auto ks) { return forward_tc<decltype(ks)::value>(a, r, dev, st); });
     return a->D <= 64 ? forward_simt<64>(r, st) : forward_simt<128>(r, st);
 }
 
@@ -187,7 +198,7 @@ lce_status_t lce_attention_backward(const lce_attn_t *a) {
     r.lse2 = reinterpret_cast<float *>(base);
     r.delta = r.lse2 + r.stat_stride * r.Hq;
     if (a->dtype == LCE_BF16)
-        return a->D <= 64 ? backward_tc<1>(a, r, dev, st) : backward_tc<2>(a, r, dev, st);
+        return by_channels(a->D, [&](auto ks) { return backward_tc<decltype(ks)::value>(a, r, dev, st); });
     return a->D <= 64 ? backward_simt<64>(r, st) : backward_simt<128>(r, st);
 }
 

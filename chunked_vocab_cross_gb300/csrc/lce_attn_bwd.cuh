@@ -23,27 +23,28 @@ namespace lce {
 
 constexpr int kBwdThreads = 320;
 
-template <int NB>
-struct DqSmem {
-    static constexpr int kTile = NB * kTcBlock;
+template <int KS>
+struct DqSmem : Chan<KS> {
+    using Chan<KS>::kTile;
     static constexpr int kKs = 3, kVs = 2;                         // ring slots of K and V
     static constexpr int kBars = (2 + kKs + kVs) * kTile;          // Q, dO, rings
     static constexpr int kBytes = kBars + 160 + 1024;              // alignment slack
 };
 
-template <int NB>
+template <int KS>
 __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dq(const __grid_constant__ AttnArgs a,
                                                             const __grid_constant__ AttnMaps maps) {
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    using L = DqSmem<NB>;
+    using L = DqSmem<KS>;
+    constexpr int NB = L::NB;
     uint8_t *sq = smem, *sg = smem + L::kTile, *sk = smem + 2 * L::kTile, *sv = sk + L::kKs * L::kTile;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars);
     uint64_t *k_full = bars, *k_empty = bars + 3, *v_full = bars + 6, *v_empty = bars + 8, *q_full = bars + 10,
              *s_full = bars + 11 /* two */, *dp_full = bars + 13, *ds_full = bars + 14, *fin = bars + 15;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 16);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
     const int h = blockIdx.x % a.Hq, hk = h / a.group;
     const int slot = gridDim.x / a.Hq - 1 - blockIdx.x / a.Hq;   // under a causal mask the last tiles have the most keys
@@ -74,10 +75,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dq(const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t tS[2] = {tmem, tmem + 128}, tP = tmem + 256, tQ = tmem + 384;
     const TcWaits wait{abort_flag, a.status};
-    const int ks = (a.D + 15) / 16;
 
     if (warp == 8) {
         if (lane == 0) {
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dq(const __grid_constan
             }
         }
     } else if (warp == 9) {
-        const uint32_t idS = idesc_f32acc(1, 128, 128, false, false), idQ = idesc_f32acc(1, 128, ks * 16, false, true);
+        const uint32_t idS = idesc_f32acc(1, 128, 128, false, false), idQ = idesc_f32acc(1, 128, KS * 16, false, true);
         const uint32_t idSn = idS | (a.scale < 0.f ? kIdescNegA : 0);
         const uint64_t dQ = tc_desc_k(sq), dG = tc_desc_k(sg);
         // S_j from K_j; its tokens past the sequence's end are zeroed for the sum that follows
@@ -112,9 +112,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dq(const __grid_constan
             if (!wait.all(&k_full[ki], (j / L::kKs) & 1)) return false;
             const int keys = min(kTcTile, t.olen - j * kTcTile);
             if (keys < kTcTile) tc_zero_rows<NB>(sk + ki * L::kTile, keys);
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
-                tc_mma_scores(tS[j & 1], dQ, tc_desc_k(sk + ki * L::kTile), idSn, ks);
+                tc_mma_scores<KS>(tS[j & 1], dQ, tc_desc_k(sk + ki * L::kTile), idSn);
                 umma_commit(&s_full[j & 1]);
             }
             __syncwarp();
@@ -125,9 +125,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dq(const __grid_constan
             if (!wait.all(&v_full[vi], (j / L::kVs) & 1)) return false;
             const int keys = min(kTcTile, t.olen - j * kTcTile);
             if (keys < kTcTile) tc_zero_rows<NB>(sv + vi * L::kTile, keys);
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
-                tc_mma_scores(tP, dG, tc_desc_k(sv + vi * L::kTile), idS, ks);
+                tc_mma_scores<KS>(tP, dG, tc_desc_k(sv + vi * L::kTile), idS);
                 umma_commit(&v_empty[vi]);
                 umma_commit(dp_full);
             }
@@ -140,18 +140,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dq(const __grid_constan
             if (!(ok = wait.all(ds_full, j & 1))) break;
             tc_fence_after();
             if (j + 1 < n && !(ok = dprobs(j + 1))) break;
-            if (lane == 0) {
-                const int keys = min(kTcTile, t.olen - j * kTcTile);
+            if (elect_one()) {
                 const uint64_t dK = tc_desc_mn(sk + (j % L::kKs) * L::kTile);
-                const int steps = (keys + 15) / 16;
-                for (int kk = 0; kk < steps; ++kk)
-                    umma_f16_ts(tQ, tS[j & 1] + (kk >> 2) * 64 + (kk & 3) * 8, dK + tc_step_mn(kk), idQ, j > 0 || kk > 0);
+                tc_mma_tokens<true>(tQ, tS[j & 1], dK, idQ, j > 0);
                 umma_commit(&k_empty[j % L::kKs]);
                 if (j + 1 == n) umma_commit(fin);
             }
             __syncwarp();
         }
-        if (!ok && lane == 0) {
+        if (!ok && elect_one()) {
             umma_commit(fin);
             tc_drain(fin, 0);
         }
@@ -213,9 +210,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dq(const __grid_constan
     }
 }
 
-template <int NB>
-struct DkvSmem {
-    static constexpr int kTile = NB * kTcBlock;
+template <int KS>
+struct DkvSmem : Chan<KS> {
+    using Chan<KS>::kTile;
     static constexpr int kQs = 3, kGs = 2;                             // ring slots of Q and dO
     static constexpr int kStat = 2 * kTcTile * 4;                      // lse2 and delta of a Q tile; two slots
     static constexpr int kStats = (2 + kQs + kGs) * kTile;             // K, V, rings
@@ -224,7 +221,7 @@ struct DkvSmem {
     static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
-template <int NB>
+template <int KS>
 __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_constant__ AttnArgs a,
                                                              const __grid_constant__ AttnMaps maps) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -232,7 +229,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_consta
         if (threadIdx.x == 0) atomicOr(a.status, kDevTimeout);
         return;
     }
-    using L = DkvSmem<NB>;
+    using L = DkvSmem<KS>;
+    constexpr int NB = L::NB;
     uint8_t *sk = smem, *sv = smem + L::kTile, *sq = smem + 2 * L::kTile, *sg = sq + L::kQs * L::kTile;
     float *stats = reinterpret_cast<float *>(smem + L::kStats);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars);
@@ -241,7 +239,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_consta
              *st_full = bars + 16 /* two */;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
     const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk;   // under a causal mask the first tiles have the most queries
     const TileInfo t = tile_info<kTcTile>(a.sk, a.sq, slot);      // own side: keys
@@ -275,10 +273,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
     const TcWaits wait{abort_flag, a.status};
-    const int ks = (a.D + 15) / 16;
 
     if (warp == 8) {
         if (lane == 0) {
@@ -315,7 +312,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_consta
             }
         }
     } else if (warp == 9) {
-        const uint32_t idS = idesc_f32acc(1, 128, 128, false, false), idG = idesc_f32acc(1, 128, ks * 16, false, true);
+        const uint32_t idS = idesc_f32acc(1, 128, 128, false, false), idG = idesc_f32acc(1, 128, KS * 16, false, true);
         const uint32_t idSn = idS | (a.scale < 0.f ? kIdescNegA : 0);
         const uint64_t dK = tc_desc_k(sk), dV = tc_desc_k(sv);
         auto queries = [&](int j) { return min(kTcTile, t.olen - (first + j % per_head) * kTcTile); };
@@ -324,9 +321,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_consta
             if (!wait.all(&q_full[qi], (j / L::kQs) & 1)) return false;
             const int q = queries(j);
             if (q < kTcTile) tc_zero_rows<NB>(sq + qi * L::kTile, q);
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
-                tc_mma_scores(tS, dK, tc_desc_k(sq + qi * L::kTile), idSn, ks);
+                tc_mma_scores<KS>(tS, dK, tc_desc_k(sq + qi * L::kTile), idSn);
                 umma_commit(s_full);
             }
             __syncwarp();
@@ -337,9 +334,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_consta
             if (!wait.all(&g_full[gi], (j / L::kGs) & 1)) return false;
             const int q = queries(j);
             if (q < kTcTile) tc_zero_rows<NB>(sg + gi * L::kTile, q);
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
-                tc_mma_scores(tP, dV, tc_desc_k(sg + gi * L::kTile), idS, ks);
+                tc_mma_scores<KS>(tP, dV, tc_desc_k(sg + gi * L::kTile), idS);
                 umma_commit(dp_full);
             }
             __syncwarp();
@@ -347,12 +344,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_consta
         };
         // acc (+)= A[keys x queries] . tile, A in two halves of 64 queries, 64 columns apart
         auto gather = [&](uint32_t acc, uint32_t A, const uint8_t *tile, int j, uint64_t *release) {
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
-                const uint64_t d = tc_desc_mn(tile);
-                const int steps = (queries(j) + 15) / 16;
-                for (int kk = 0; kk < steps; ++kk)
-                    umma_f16_ts(acc, A + (kk >> 2) * 64 + (kk & 3) * 8, d + tc_step_mn(kk), idG, j > 0 || kk > 0);
+                tc_mma_tokens<true>(acc, A, tc_desc_mn(tile), idG, j > 0);
                 umma_commit(release);
             }
             __syncwarp();
@@ -366,7 +360,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_consta
             gather(tK, tP, sq + (j % L::kQs) * L::kTile, j, &q_empty[j % L::kQs]);
             if (j + 1 < n && !(ok = dprobs(j + 1))) break;
         }
-        if (lane == 0) {
+        if (elect_one()) {
             umma_commit(fin);
             if (!ok) tc_drain(fin, 0);
         }

@@ -19,26 +19,27 @@ namespace lce {
 constexpr int kFwdThreads = 192;
 constexpr float kLazy = 8.f;
 
-template <int NB>
-struct FwdSmem {
-    static constexpr int kTile = NB * kTcBlock;
+template <int KS>
+struct FwdSmem : Chan<KS> {
+    using Chan<KS>::kTile;
     static constexpr int kBars = 3 * kTile;              // Q, two ring slots
     static constexpr int kBytes = kBars + 128 + 1024;    // alignment slack
 };
 
-template <int NB>
+template <int KS>
 __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_constant__ AttnArgs a,
                                                              const __grid_constant__ AttnMaps maps) {
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    using L = FwdSmem<NB>;
+    using L = FwdSmem<KS>;
+    constexpr int NB = L::NB;
     uint8_t *sq = smem, *ring = smem + L::kTile;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars);
     uint64_t *full = bars, *empty = bars + 2, *q_full = bars + 4, *s_full = bars + 5, *p_full = bars + 6,
              *o_done = bars + 7, *fin = bars + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 9);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
     const int h = blockIdx.x % a.Hq, hk = h / a.group;
     // longest rows first: under a causal mask the last tiles have the most keys
@@ -84,10 +85,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t tS = tmem, tO = tmem + 128;
     const TcWaits wait{abort_flag, a.status};
-    const int ks = (a.D + 15) / 16;   // K steps over the channels
 
     if (warp == 4) {
         if (lane == 0) {
@@ -108,14 +108,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
         }
     } else if (warp == 5) {
         const uint32_t idS = idesc_f32acc(1, 128, 128, false, false) | (a.scale < 0.f ? kIdescNegA : 0);
-        const uint32_t idO = idesc_f32acc(1, 128, ks * 16, false, true);
+        const uint32_t idO = idesc_f32acc(1, 128, KS * 16, false, true);
         const uint64_t dq = tc_desc_k(sq), dk = tc_desc_k(ring), dv = tc_desc_mn(ring + L::kTile);
         bool ok = wait.all(q_full, 0);
         for (int j = 0; ok && j < n; ++j) {
             if (!(ok = wait.all(&full[0], j & 1))) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
-                tc_mma_scores(tS, dq, dk, idS, ks);
+                tc_mma_scores<KS>(tS, dq, dk, idS);
                 umma_commit(&empty[0]);
                 umma_commit(s_full);
             }
@@ -124,15 +124,15 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
             const int keys = min(kTcTile, t.olen - j * kTcTile);
             if (keys < kTcTile) tc_zero_rows<NB>(ring + L::kTile, keys);
             if (!(ok = wait.all(p_full, j & 1))) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
-                tc_mma_tokens(tO, tS, dv, idO, (keys + 15) / 16, j > 0);
+                tc_mma_tokens<false>(tO, tS, dv, idO, j > 0);
                 umma_commit(&empty[1]);
                 umma_commit(o_done);
             }
             __syncwarp();
         }
-        if (!ok && lane == 0) {   // let the MMAs issued so far finish
+        if (!ok && elect_one()) {   // let the MMAs issued so far finish
             umma_commit(fin);
             tc_drain(fin, 0);
         }
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
                     tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < NB * 2; ++c) {
-                        if (c * 32 >= ks * 16) break;
+                        if (c * 32 >= KS * 16) break;
                         uint32_t v[32];
                         tmem_ld32(tO + lane_base + c * 32, v);
                         tmem_ld_wait();

@@ -19,6 +19,21 @@ constexpr int kTcBlock = kTcTile * 128;                 // bytes of one column b
 constexpr long long kTcWaitCycles = 2000000000LL;       // ~1 s: far above any legitimate wait
 constexpr long long kTcDrainCycles = 200000000LL;
 
+// Polls a barrier phase without a suspend-time hint: the softmax and MMA warps
+// hand each other every tile, and a waiter that sleeps longer than the hardware's
+// own short limit adds to that chain.
+__device__ __forceinline__ bool tc_try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Waits of one CTA: a wait that gives up raises the device status word and
 // the CTA's abort flag, on which all its other waits give up too.
 struct TcWaits {
@@ -26,10 +41,10 @@ struct TcWaits {
     int *status;
     __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
         const uint32_t a = smem_u32(bar);
-        if (mbar_try_wait(a, parity)) return true;
+        if (tc_try_wait(a, parity)) return true;
         const long long t0 = clock64();
         for (;;) {
-            if (mbar_try_wait(a, parity)) return true;
+            if (tc_try_wait(a, parity)) return true;
             if (*abort_flag) return false;
             if (clock64() - t0 > kTcWaitCycles) {
                 *abort_flag = 1;
@@ -49,7 +64,7 @@ struct TcWaits {
 __device__ __forceinline__ void tc_drain(uint64_t *bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
     const long long t0 = clock64();
-    while (!mbar_try_wait(a, parity))
+    while (!tc_try_wait(a, parity))
         if (clock64() - t0 > kTcDrainCycles) return;
 }
 
@@ -85,14 +100,29 @@ __device__ __forceinline__ uint64_t tc_desc_mn(const uint8_t *tile) {
 __device__ __forceinline__ uint64_t tc_step_k(int kk) { return (kk >> 2) * (kTcBlock >> 4) + (kk & 3) * 2; }
 __device__ __forceinline__ uint64_t tc_step_mn(int kk) { return kk * 128; }
 
-// D = A . B^T over the channels (both operands tiles).
-__device__ __forceinline__ void tc_mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int ksteps) {
-    for (int kk = 0; kk < ksteps; ++kk) umma_f16(d, a + tc_step_k(kk), b + tc_step_k(kk), idesc, kk > 0);
+// The kernels are compiled for KS steps of 16 channels (D rounded up), in NB
+// blocks of 64.
+template <int KS>
+struct Chan {
+    static constexpr int NB = (KS + 3) / 4;
+    static constexpr int kTile = NB * kTcBlock;
+};
+
+// D = A . B^T over the channels (both operands tiles). Unrolled: one thread
+// issues, and the address arithmetic of a rolled loop takes it longer than the
+// MMA takes the tensor core.
+template <int KS>
+__device__ __forceinline__ void tc_mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) umma_f16(d, a + tc_step_k(kk), b + tc_step_k(kk), idesc, kk > 0);
 }
-// D (+)= P . B over tokens: P in tensor memory (two tokens a column), B a tile.
-__device__ __forceinline__ void tc_mma_tokens(uint32_t d, uint32_t p, uint64_t b, uint32_t idesc, int ksteps,
-                                              bool accumulate) {
-    for (int kk = 0; kk < ksteps; ++kk) umma_f16_ts(d, p + kk * 8, b + tc_step_mn(kk), idesc, accumulate || kk > 0);
+// D (+)= P . B over 128 tokens: P in tensor memory (two tokens a column;
+// kHalves: its two halves of 64 tokens start 64 columns apart), B a tile.
+template <bool kHalves>
+__device__ __forceinline__ void tc_mma_tokens(uint32_t d, uint32_t p, uint64_t b, uint32_t idesc, bool accumulate) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        umma_f16_ts(d, p + kk * 8 + (kHalves ? (kk >> 2) * 32 : 0), b + tc_step_mn(kk), idesc, accumulate || kk > 0);
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -219,6 +219,20 @@ __device__ __forceinline__ void umma_commit_pair_mc(uint64_t *bar, uint16_t mask
                  : "memory");
 }
 
+// True in one lane, always the same one, of a converged warp. MMAs issued by
+// a lane chosen this way keep their operands in uniform registers; behind
+// `lane == 0` the compiler moves every operand of every MMA over from the
+// lane's own registers (about 110 cycles an MMA against the 64 it runs for).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // ---- single-CTA (cta_group::1) forms.
 
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t ncols) {
