@@ -768,6 +768,7 @@ lce_status_t host_device(HostDev *out) {
     DevInfo *di = nullptr;
     const lce_status_t s = device_info(&di);
     if (s != LCE_OK) return s;
+    out->index = static_cast<int>(di - g_dev);
     out->sms = di->sms;
     out->status = di->status;
     out->encode = g_encode;

@@ -87,16 +87,14 @@ lce_status_t encode(CUtensorMap *m, const HostDev &dev, const void *p, int64_t T
     return r == CUDA_SUCCESS ? LCE_OK : LCE_ERR_SHAPE;
 }
 
-template <typename K, typename... A>
-lce_status_t launch(K kernel, int64_t blocks, int threads, int smem, cudaStream_t st, const A &...args) {
-    if (blocks <= 0) return LCE_OK;
+template <auto kKernel, typename... A>
+lce_status_t launch(const HostDev &dev, int64_t blocks, int threads, int smem, cudaStream_t st, const A &...args) {
     if (blocks >= (int64_t(1) << 31)) return LCE_ERR_SHAPE;
     if (smem > 48 * 1024) {
-        const lce_status_t s = host_cuda(cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+        const lce_status_t s = host_smem<kKernel>(dev, smem);
         if (s != LCE_OK) return s;
     }
-    kernel<<<static_cast<unsigned>(blocks), threads, smem, st>>>(args...);
+    kKernel<<<static_cast<unsigned>(blocks), threads, smem, st>>>(args...);
     return host_launched();
 }
 
@@ -107,22 +105,22 @@ lce_status_t forward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &d
     if (s == LCE_OK) s = encode(&maps.k, dev, a->k, a->Tk, a->Hk, a->D, a->k_ts, a->k_hs);
     if (s == LCE_OK) s = encode(&maps.v, dev, a->v, a->Tk, a->Hk, a->D, a->v_ts, a->v_hs);
     if (s != LCE_OK) return s;
-    return launch(k_attn_fwd<KS>, seq_slots(r.sq.T, r.sq.B, kTcTile) * r.Hq, kFwdThreads, FwdSmem<KS>::kBytes, st, r,
+    return launch<k_attn_fwd<KS>>(dev, seq_slots(r.sq.T, r.sq.B, kTcTile) * r.Hq, kFwdThreads, FwdSmem<KS>::kBytes, st, r,
                   maps);
 }
 
 template <int DP>
-lce_status_t forward_simt(const AttnArgs &r, cudaStream_t st) {
+lce_status_t forward_simt(const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
     const int64_t slots = seq_slots(r.sq.T, r.sq.B, kSimtTile);
-    return launch(k_attn_fwd_simt<DP>, slots * r.Hq, kSimtThreads, simt_smem(DP, 3, 1), st, r);
+    return launch<k_attn_fwd_simt<DP>>(dev, slots * r.Hq, kSimtThreads, simt_smem(DP, 3, 1), st, r);
 }
 
 template <int DP>
-lce_status_t backward_simt(const AttnArgs &r, cudaStream_t st) {
+lce_status_t backward_simt(const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
     const int64_t qslots = seq_slots(r.sq.T, r.sq.B, kSimtTile), kslots = seq_slots(r.sk.T, r.sk.B, kSimtTile);
-    lce_status_t s = launch(k_attn_stats<float, kSimtTile>, qslots * r.Hq, 256, 0, st, r);
-    if (s == LCE_OK && r.sq.T > 0) s = launch(k_attn_dq_simt<DP>, qslots * r.Hq, kSimtThreads, simt_smem(DP, 4, 1), st, r);
-    if (s == LCE_OK && r.sk.T > 0) s = launch(k_attn_dkv_simt<DP>, kslots * r.Hk, kSimtThreads, simt_smem(DP, 4, 2), st, r);
+    lce_status_t s = launch<k_attn_stats<float, kSimtTile>>(dev, qslots * r.Hq, 256, 0, st, r);
+    if (s == LCE_OK && r.sq.T > 0) s = launch<k_attn_dq_simt<DP>>(dev, qslots * r.Hq, kSimtThreads, simt_smem(DP, 4, 1), st, r);
+    if (s == LCE_OK && r.sk.T > 0) s = launch<k_attn_dkv_simt<DP>>(dev, kslots * r.Hk, kSimtThreads, simt_smem(DP, 4, 2), st, r);
     return s;
 }
 
@@ -134,9 +132,9 @@ lce_status_t backward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &
     if (s == LCE_OK) s = encode(&maps.v, dev, a->v, a->Tk, a->Hk, a->D, a->v_ts, a->v_hs);
     if (s == LCE_OK) s = encode(&maps.dO, dev, a->dO, a->Tq, a->Hq, a->D, a->dO_ts, a->dO_hs);
     const int64_t qslots = seq_slots(r.sq.T, r.sq.B, kTcTile), kslots = seq_slots(r.sk.T, r.sk.B, kTcTile);
-    if (s == LCE_OK) s = launch(k_attn_stats<__nv_bfloat16, kTcTile>, qslots * r.Hq, 256, 0, st, r);
-    if (s == LCE_OK && r.sk.T > 0) s = launch(k_attn_dkv<KS>, kslots * r.Hk, kBwdThreads, DkvSmem<KS>::kBytes, st, r, maps);
-    if (s == LCE_OK && r.sq.T > 0) s = launch(k_attn_dq<KS>, qslots * r.Hq, kBwdThreads, DqSmem<KS>::kBytes, st, r, maps);
+    if (s == LCE_OK) s = launch<k_attn_stats<__nv_bfloat16, kTcTile>>(dev, qslots * r.Hq, 256, 0, st, r);
+    if (s == LCE_OK && r.sk.T > 0) s = launch<k_attn_dkv<KS>>(dev, kslots * r.Hk, kBwdThreads, DkvSmem<KS>::kBytes, st, r, maps);
+    if (s == LCE_OK && r.sq.T > 0) s = launch<k_attn_dq<KS>>(dev, qslots * r.Hq, kBwdThreads, DqSmem<KS>::kBytes, st, r, maps);
     return s;
 }
 
@@ -173,7 +171,7 @@ lce_status_t lce_attention_forward(const lce_attn_t *a) {
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
     if (a->dtype == LCE_BF16)
         return by_channels(a->D, [&](auto ks) { return forward_tc<decltype(ks)::value>(a, r, dev, st); });
-    return a->D <= 64 ? forward_simt<64>(r, st) : forward_simt<128>(r, st);
+    return a->D <= 64 ? forward_simt<64>(r, dev, st) : forward_simt<128>(r, dev, st);
 }
 
 lce_status_t lce_attention_backward(const lce_attn_t *a) {
@@ -199,7 +197,7 @@ lce_status_t lce_attention_backward(const lce_attn_t *a) {
     r.delta = r.lse2 + r.stat_stride * r.Hq;
     if (a->dtype == LCE_BF16)
         return by_channels(a->D, [&](auto ks) { return backward_tc<decltype(ks)::value>(a, r, dev, st); });
-    return a->D <= 64 ? backward_simt<64>(r, st) : backward_simt<128>(r, st);
+    return a->D <= 64 ? backward_simt<64>(r, dev, st) : backward_simt<128>(r, dev, st);
 }
 
 }  // extern "C"

@@ -7,11 +7,14 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "lce.h"
 
 namespace lce {
 
 struct HostDev {
+    int index = 0;           // device number, below 64
     int sms = 0;
     int *status = nullptr;   // device status word (LCE_DEV_* bits)
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
@@ -59,6 +62,18 @@ class HostScratch {
     void *p_ = nullptr;
     bool owned_ = false;
 };
+
+// Raises a kernel's dynamic shared-memory limit, once per kernel and device.
+template <auto kKernel>
+lce_status_t host_smem(const HostDev &dev, int bytes) {
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = uint64_t(1) << dev.index;
+    if (done.load(std::memory_order_relaxed) & bit) return LCE_OK;
+    const lce_status_t s = host_cuda(cudaFuncSetAttribute(reinterpret_cast<const void *>(kKernel),
+                                                          cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    if (s == LCE_OK) done.fetch_or(bit, std::memory_order_relaxed);
+    return s;
+}
 
 inline bool host_misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
