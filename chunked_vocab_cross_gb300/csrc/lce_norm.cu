@@ -2,7 +2,11 @@
 // kernels and host side of lce_block_norm_forward / _backward.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
+#include "f32x2.cuh"
 #include "lce_host.h"
+#include "tc_ptx.cuh"
 
 using namespace lce;
 
@@ -64,6 +68,7 @@ struct NormArgs {
     int64_t N;
     int d, gate_full;
     float scale, eps;
+    int *status;
     float *part;   // backward: partial column sums [3][groups][d] (w_pre, w_post, gate)
 };
 
@@ -283,24 +288,513 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormArgs a) {
     }
 }
 
-// Adds the blocks' column sums in block order: 32 columns a block, 8 threads
-// a column, joined in a fixed tree.
+// ---------------------------------------------------------------- ring kernels
+//
+// Persistent blocks whose rows arrive through a ring of shared-memory stages,
+// filled by untiled bulk copies that one thread issues: the copies of the next
+// rows are in flight while a row's sums are joined, so HBM is kept busy with
+// few threads and no registers for prefetching. A stage holds `groups`
+// consecutive rows, each taken by `tpr` threads with CH packs of 16 bytes;
+// the groups join their sums on barriers of their own and so cover each
+// other's waits. Weights (ones where there are none) stay in shared memory.
+// The work between two rows is mostly issue slots: hence the packed fp32
+// arithmetic, 16 to 32 elements a thread against the fixed cost of a sum, and
+// no branches on the options inside a row.
+struct RingGeo {
+    int tpr, groups, stages;
+    uint32_t row_bytes, array_bytes, stage_bytes;   // of one row; of one array's rows; of a stage
+};
+
+constexpr int kRingThreads = 512;   // threads of a block at most
+constexpr int kRingMaxStages = 8;
+constexpr long long kNormWaitCycles = 2000000000LL;   // ~1 s: far above any legitimate wait
+
+template <typename T>
+constexpr int kPack = 16 / sizeof(T);   // elements of a pack
+
+// 16 bytes as packed pairs of fp32
+template <typename T>
+struct Pack16;
+template <>
+struct Pack16<float> {
+    static __device__ __forceinline__ void get(const uint4 &v, f32x2 (&x)[2]) { x[0] = pack2u(v.x, v.y), x[1] = pack2u(v.z, v.w); }
+    static __device__ __forceinline__ uint4 set(const f32x2 (&x)[2]) {
+        float a, b, c, d;
+        unpack2(x[0], a, b), unpack2(x[1], c, d);
+        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+    }
+    static constexpr uint32_t kOnes = 0x3f800000u;
+};
+template <>
+struct Pack16<__nv_bfloat16> {
+    static __device__ __forceinline__ f32x2 pair(uint32_t w) { return pack2u(w << 16, w & 0xffff0000u); }
+    static __device__ __forceinline__ void get(const uint4 &v, f32x2 (&x)[4]) {
+        x[0] = pair(v.x), x[1] = pair(v.y), x[2] = pair(v.z), x[3] = pair(v.w);
+    }
+    static __device__ __forceinline__ uint32_t word(f32x2 v) {
+        float a, b;
+        unpack2(v, a, b);
+        __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t *>(&p);
+    }
+    static __device__ __forceinline__ uint4 set(const f32x2 (&x)[4]) { return make_uint4(word(x[0]), word(x[1]), word(x[2]), word(x[3])); }
+    static constexpr uint32_t kOnes = 0x3f803f80u;
+};
+
+struct RingBars {
+    uint64_t full[kRingMaxStages], empty[kRingMaxStages];
+    volatile int abort_flag;
+};
+
+__device__ __forceinline__ bool ring_wait(RingBars &b, uint64_t *bar, uint32_t parity, int *status) {
+    const uint32_t at = smem_u32(bar);
+    if (mbar_try_wait(at, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (mbar_try_wait(at, parity)) return true;
+        if (b.abort_flag) return false;
+        if (clock64() - t0 > kNormWaitCycles) {
+            b.abort_flag = 1;
+            atomicOr(status, LCE_DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// The arrays of a ring, copied by thread 0 of the block.
+template <typename T, int MAX>
+struct RingSource {
+    const T *src[MAX];
+    int64_t ld[MAX];   // row strides, elements
+    // starts the copies of the `per` rows from r0 on into stage s, if there are any
+    __device__ __forceinline__ void issue(uint8_t *ring, RingBars &bars, const RingGeo &g, int per, int s, int64_t r0, int64_t N, int d) const {
+        if (r0 >= N) return;
+        const int rows = static_cast<int>(min(static_cast<int64_t>(per), N - r0));
+        int count = 0;
+#pragma unroll
+        for (int k = 0; k < MAX; ++k) count += src[k] != nullptr;
+        mbar_arrive_expect_tx(&bars.full[s], count * rows * g.row_bytes);
+        uint8_t *dst = ring + s * g.stage_bytes;
+#pragma unroll
+        for (int k = 0; k < MAX; ++k) {
+            if (!src[k]) continue;
+            if (ld[k] == d) bulk_load(dst, src[k] + r0 * d, rows * g.row_bytes, &bars.full[s]);
+            else
+                for (int r = 0; r < rows; ++r) bulk_load(dst + r * g.row_bytes, src[k] + (r0 + r) * ld[k], g.row_bytes, &bars.full[s]);
+            dst += g.array_bytes;
+        }
+    }
+};
+
+// After a wait that gave up in stage s: lets the copies in flight (of the rows
+// from r0 on) land before the block gives up its memory.
+__device__ __forceinline__ void ring_drain(RingBars &bars, const RingGeo &g, int per, int s, uint32_t phase, int64_t r0, int64_t N) {
+    for (int i = 0; i < g.stages && r0 < N; ++i, r0 += static_cast<int64_t>(gridDim.x) * per) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(smem_u32(&bars.full[s]), phase) && clock64() - t0 < kNormWaitCycles / 10) {}
+        if (++s == g.stages) s = 0, phase ^= 1;
+    }
+}
+
+// Sum of K values over the `tpr` threads of a row, the same for all of them,
+// in a fixed order; `red`: the group's 2 x K x 16 floats, zero beyond its warps.
+template <int K>
+__device__ __forceinline__ void group_sum(float (&v)[K], float *red, int &flip, int tpr, int group, int t) {
+#pragma unroll
+    for (int m = 16; m; m >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
+    if (tpr == 32) return;
+    float *at = red + flip * K * 16;
+    flip ^= 1;
+    if ((t & 31) == 0)
+#pragma unroll
+        for (int k = 0; k < K; ++k) at[k * 16 + t / 32] = v[k];
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+    const int quads = (tpr + 127) / 128;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const float4 *p = reinterpret_cast<const float4 *>(at + k * 16);
+        const float4 x = p[0];
+        v[k] = (x.x + x.y) + (x.z + x.w);
+        for (int w = 1; w < quads; ++w) {
+            const float4 y = p[w];
+            v[k] += (y.x + y.y) + (y.z + y.w);
+        }
+    }
+}
+
+// Weights of a row into shared memory, `rows` of them (ones where there is none)
+template <typename T>
+__device__ __forceinline__ void load_weights(uint8_t *dst, const void *w, int row_bytes) {
+    constexpr uint32_t o = Pack16<T>::kOnes;
+    for (int i = threadIdx.x * 16; i < row_bytes; i += blockDim.x * 16)
+        *reinterpret_cast<uint4 *>(dst + i) = w ? *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(w) + i) : make_uint4(o, o, o, o);
+}
+
+constexpr int kRedFloats = 2 * 3 * 16;   // of a row group
+
+template <typename T, int CH>
+__global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArgs a, const RingGeo g) {
+    constexpr int V = kPack<T>, P = V / 2;
+    extern __shared__ __align__(128) uint8_t smem[];   // ring, then w_post, gate, w_pre
+    __shared__ RingBars bars;
+    __shared__ __align__(16) float red[16 * kRedFloats];
+    const int nwarps = blockDim.x / 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < g.stages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], nwarps);
+        bars.abort_flag = 0;
+        fence_mbar_init();
+    }
+    const int d = a.d;
+    const bool full_gate = a.gate && a.gate_full;
+    uint8_t *w_post = smem + g.stages * g.stage_bytes, *gate = w_post + g.row_bytes, *w_pre = gate + g.row_bytes;
+    load_weights<T>(w_post, a.w_post, g.row_bytes);
+    load_weights<T>(gate, full_gate ? nullptr : a.gate, g.row_bytes);
+    load_weights<T>(w_pre, a.w_pre, g.row_bytes);
+    for (int i = threadIdx.x; i < 16 * kRedFloats; i += blockDim.x) red[i] = 0.f;
+    __syncthreads();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * g.groups;
+    int64_t r0 = static_cast<int64_t>(blockIdx.x) * g.groups;
+    const RingSource<T, 3> src = {{static_cast<const T *>(a.x), static_cast<const T *>(a.b), full_gate ? static_cast<const T *>(a.gate) : nullptr},
+                                  {a.ld_x, a.ld_b, a.ld_gate}};
+    if (threadIdx.x == 0)
+        for (int i = 0; i < g.stages; ++i) src.issue(smem, bars, g, g.groups, i, r0 + i * step, a.N, d);
+    const int group = threadIdx.x / g.tpr, t = threadIdx.x % g.tpr;
+    float *my_red = red + group * kRedFloats;
+    const float inv_d = 1.f / d;
+    int flip = 0, s = 0;
+    uint32_t phase = 0;
+    for (; r0 < a.N; r0 += step) {
+        const int64_t row = r0 + group;
+        if (!__all_sync(0xffffffffu, ring_wait(bars, &bars.full[s], phase, a.status))) {
+            if (threadIdx.x == 0) ring_drain(bars, g, g.groups, s, phase, r0, a.N);
+            break;
+        }
+        const bool live = row < a.N;   // the first group always is
+        const uint8_t *at = smem + s * g.stage_bytes + group * g.row_bytes;
+        f32x2 r[CH][P];
+        uint4 vb[CH], vg[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int byte = (c * g.tpr + t) * 16;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            vb[c] = vg[c] = x;
+            if (byte < g.row_bytes) {
+                x = *reinterpret_cast<const uint4 *>(at + byte);
+                if (a.b) vb[c] = *reinterpret_cast<const uint4 *>(at + g.array_bytes + byte);
+                if (full_gate) vg[c] = *reinterpret_cast<const uint4 *>(at + 2 * g.array_bytes + byte);
+            }
+            Pack16<T>::get(x, r[c]);
+        }
+        __syncwarp();
+        if ((t & 31) == 0) mbar_arrive(&bars.empty[s]);   // everything is in registers
+        if (live) {
+            float rs = 1.f;
+            if (a.w_post) {
+                f32x2 q = both(0.f);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    f32x2 b[P];
+                    Pack16<T>::get(vb[c], b);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) q = fma2(b[i], b[i], q);
+                }
+                float sum[1] = {hsum2(q)};
+                group_sum(sum, my_red, flip, g.tpr, group, t);
+                rs = rsqrtf(sum[0] * inv_d + a.eps);
+                if (t == 0) a.rstd_post[row] = rs;
+            }
+            if (a.b) {
+                const f32x2 f = both(rs * a.scale);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const int byte = (c * g.tpr + t) * 16;
+                    if (byte >= g.row_bytes) continue;
+                    f32x2 y[P], w[P];
+                    Pack16<T>::get(vb[c], y);
+                    Pack16<T>::get(*reinterpret_cast<const uint4 *>(w_post + byte), w);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) y[i] = mul2(y[i], w[i]);
+                    Pack16<T>::get(full_gate ? vg[c] : *reinterpret_cast<const uint4 *>(gate + byte), w);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) r[c][i] = fma2(mul2(y[i], w[i]), f, r[c][i]);
+                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.r) + row * g.row_bytes + byte) = Pack16<T>::set(r[c]);
+                }
+            }
+        }
+        float sum[1] = {0.f};
+        if (live && a.w_pre) {
+            f32x2 q = both(0.f);
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int i = 0; i < P; ++i) q = fma2(r[c][i], r[c][i], q);   // zeros past d
+            sum[0] = hsum2(q);
+            group_sum(sum, my_red, flip, g.tpr, group, t);
+        }
+        // the stage's next rows, once every warp has taken its share
+        if (threadIdx.x == 0 && r0 + g.stages * step < a.N && ring_wait(bars, &bars.empty[s], phase, a.status))
+            src.issue(smem, bars, g, g.groups, s, r0 + g.stages * step, a.N, d);
+        if (live && a.w_pre) {
+            const float rs = rsqrtf(sum[0] * inv_d + a.eps);
+            if (t == 0) a.rstd_pre[row] = rs;
+            const f32x2 f = both(rs);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int byte = (c * g.tpr + t) * 16;
+                if (byte >= g.row_bytes) continue;
+                f32x2 w[P];
+                Pack16<T>::get(*reinterpret_cast<const uint4 *>(w_pre + byte), w);
+#pragma unroll
+                for (int i = 0; i < P; ++i) w[i] = mul2(mul2(r[c][i], f), w[i]);
+                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.n) + row * g.row_bytes + byte) = Pack16<T>::set(w);
+            }
+        }
+        if (++s == g.stages) s = 0, phase ^= 1;
+    }
+}
+
+// The two row sums in one round as in k_norm_bwd, with factors that are the
+// same for a whole row taken out: hat = rstd_pre r, t = dr + rstd_pre u,
+// z = b w_post gate, f = scale rstd_post:
+//   m1 = mean(u hat),  m2 = f (sum z t - rstd_pre m1 sum z hat) / d,
+//   dx = t - rstd_pre m1 hat,  e = f dx:  dgate = e b w_post,
+//   dw_post = e gate b,  db = e gate w_post - rstd_post^2 m2 b   (no w_post: the last term is 0).
+// A thread takes its columns of R rows at a time, which halves what it spends
+// on weights. The column sums stay in registers, one set a row group, and are
+// joined across the groups in shared memory at the end.
+template <typename T, int CH, int R>
+__global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArgs a, const RingGeo g) {
+    constexpr int V = kPack<T>, P = V / 2;
+    extern __shared__ __align__(128) uint8_t smem[];   // ring, then w_post, gate, w_pre
+    __shared__ RingBars bars;
+    __shared__ __align__(16) float red[16 * kRedFloats * R];
+    const int nwarps = blockDim.x / 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < g.stages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], nwarps);
+        bars.abort_flag = 0;
+        fence_mbar_init();
+    }
+    const int d = a.d;
+    const bool full_gate = a.gate && a.gate_full, col_gate = a.gate && !a.gate_full;
+    uint8_t *w_post = smem + g.stages * g.stage_bytes, *gate = w_post + g.row_bytes, *w_pre = gate + g.row_bytes;
+    load_weights<T>(w_post, a.w_post, g.row_bytes);
+    load_weights<T>(gate, full_gate ? nullptr : a.gate, g.row_bytes);
+    load_weights<T>(w_pre, a.w_pre, g.row_bytes);
+    for (int i = threadIdx.x; i < 16 * kRedFloats * R; i += blockDim.x) red[i] = 0.f;
+    __syncthreads();
+    const int per = g.groups * R;   // rows of a stage
+    const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+    int64_t r0 = static_cast<int64_t>(blockIdx.x) * per;
+    const RingSource<T, 5> src = {{a.w_pre ? static_cast<const T *>(a.r_in) : nullptr, a.w_pre ? static_cast<const T *>(a.dn) : nullptr,
+                                   static_cast<const T *>(a.b), full_gate ? static_cast<const T *>(a.gate) : nullptr, static_cast<const T *>(a.dr)},
+                                  {a.ld_r, a.ld_dn, a.ld_b, a.ld_gate, a.ld_dr}};
+    // places of the arrays in a stage
+    const uint32_t at_n = g.array_bytes, at_b = a.w_pre ? 2 * g.array_bytes : 0, at_g = at_b + (a.b ? g.array_bytes : 0),
+                   at_d = at_g + (full_gate ? g.array_bytes : 0);
+    if (threadIdx.x == 0)
+        for (int i = 0; i < g.stages; ++i) src.issue(smem, bars, g, per, i, r0 + i * step, a.N, d);
+    const int group = threadIdx.x / g.tpr, t = threadIdx.x % g.tpr;
+    float *my_red = red + group * kRedFloats * R;
+    const float inv_d = 1.f / d;
+    f32x2 s_pre[CH][P], s_post[CH][P], s_gate[CH][P];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < P; ++i) s_pre[c][i] = s_post[c][i] = s_gate[c][i] = both(0.f);
+    int flip = 0, s = 0;
+    uint32_t phase = 0;
+    float rp_next[R], ro_next[R];   // 1/rms of the rows to come, asked for a round ahead
+    auto rstd = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const bool live = row + k < a.N;
+            rp_next[k] = a.w_pre && live ? a.rstd_pre[row + k] : 0.f;
+            ro_next[k] = a.w_post && live ? a.rstd_post[row + k] : 1.f;
+        }
+    };
+    rstd(r0 + group * R);
+    for (; r0 < a.N; r0 += step) {
+        const int64_t row = r0 + group * R;
+        float rp[R], ro[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) rp[k] = rp_next[k], ro[k] = ro_next[k];
+        rstd(row + step);
+        if (!__all_sync(0xffffffffu, ring_wait(bars, &bars.full[s], phase, a.status))) {
+            if (threadIdx.x == 0) ring_drain(bars, g, per, s, phase, r0, a.N);
+            break;
+        }
+        const uint8_t *at = smem + s * g.stage_bytes + group * R * g.row_bytes;
+        f32x2 hat[R][CH][P], x[R][CH][P];
+        uint4 vb[R][CH];
+        f32x2 q[R][3];
+#pragma unroll
+        for (int k = 0; k < R; ++k) q[k][0] = q[k][1] = q[k][2] = both(0.f);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int byte = (c * g.tpr + t) * 16;
+            if (byte >= g.row_bytes) {
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    vb[k][c] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) hat[k][c][i] = x[k][c][i] = both(0.f);
+                }
+                continue;
+            }
+            f32x2 w[P], wz[P], u[P];
+            Pack16<T>::get(*reinterpret_cast<const uint4 *>(w_post + byte), wz);
+            Pack16<T>::get(*reinterpret_cast<const uint4 *>(gate + byte), w);
+#pragma unroll
+            for (int i = 0; i < P; ++i) wz[i] = mul2(wz[i], w[i]);
+            Pack16<T>::get(*reinterpret_cast<const uint4 *>(w_pre + byte), w);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const uint8_t *p = at + k * g.row_bytes + byte;
+                uint4 v = make_uint4(0, 0, 0, 0), vn = v, vd = v;
+                vb[k][c] = v;
+                // rows past the last hold what an earlier round left (or nothing at all): they count as zeros
+                const bool live = row + k < a.N;
+                if (live && a.w_pre) {
+                    v = *reinterpret_cast<const uint4 *>(p);
+                    vn = *reinterpret_cast<const uint4 *>(p + at_n);
+                }
+                if (live && a.b) vb[k][c] = *reinterpret_cast<const uint4 *>(p + at_b);
+                if (live && a.dr) vd = *reinterpret_cast<const uint4 *>(p + at_d);
+                Pack16<T>::get(v, hat[k][c]);
+                Pack16<T>::get(vn, u);
+                Pack16<T>::get(vd, x[k][c]);
+                const f32x2 rp2 = both(rp[k]);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    hat[k][c][i] = mul2(hat[k][c][i], rp2);
+                    s_pre[c][i] = fma2(u[i], hat[k][c][i], s_pre[c][i]);
+                    u[i] = mul2(u[i], w[i]);
+                    q[k][0] = fma2(u[i], hat[k][c][i], q[k][0]);
+                    x[k][c][i] = fma2(rp2, u[i], x[k][c][i]);
+                }
+                Pack16<T>::get(vb[k][c], u);
+                if (full_gate && live) {
+                    f32x2 gt[P];
+                    Pack16<T>::get(*reinterpret_cast<const uint4 *>(p + at_g), gt);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) u[i] = mul2(u[i], gt[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    u[i] = mul2(u[i], wz[i]);
+                    q[k][1] = fma2(u[i], x[k][c][i], q[k][1]);
+                    q[k][2] = fma2(u[i], hat[k][c][i], q[k][2]);
+                }
+            }
+        }
+        float sum[3 * R];
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int i = 0; i < 3; ++i) sum[3 * k + i] = hsum2(q[k][i]);
+        group_sum(sum, my_red, flip, g.tpr, group, t);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int byte = (c * g.tpr + t) * 16;
+            if (byte >= g.row_bytes) continue;
+            f32x2 w[P], gw[P];
+            Pack16<T>::get(*reinterpret_cast<const uint4 *>(w_post + byte), w);
+            Pack16<T>::get(*reinterpret_cast<const uint4 *>(gate + byte), gw);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                if (row + k >= a.N) continue;
+                const float m1 = rp[k] * sum[3 * k] * inv_d, f = a.scale * ro[k];
+                const f32x2 m1n = both(-m1), f2 = both(f);
+                const f32x2 m2n = both(a.w_post ? -(ro[k] * ro[k] * f * (sum[3 * k + 1] - m1 * sum[3 * k + 2]) * inv_d) : 0.f);
+                f32x2 (&y)[P] = x[k][c];
+#pragma unroll
+                for (int i = 0; i < P; ++i) y[i] = fma2(m1n, hat[k][c][i], y[i]);
+                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dx) + (row + k) * g.row_bytes + byte) = Pack16<T>::set(y);
+                if (!a.b) continue;
+                f32x2 b[P], dg[P];
+                Pack16<T>::get(vb[k][c], b);
+#pragma unroll
+                for (int i = 0; i < P; ++i) y[i] = mul2(y[i], f2), dg[i] = mul2(b[i], w[i]);
+                if (full_gate) {
+                    f32x2 gt[P];
+                    Pack16<T>::get(*reinterpret_cast<const uint4 *>(at + k * g.row_bytes + byte + at_g), gt);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) dg[i] = mul2(y[i], dg[i]), y[i] = mul2(y[i], gt[i]);
+                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dgate) + (row + k) * g.row_bytes + byte) = Pack16<T>::set(dg);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) s_gate[c][i] = fma2(y[i], dg[i], s_gate[c][i]), y[i] = mul2(y[i], gw[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    s_post[c][i] = fma2(y[i], b[i], s_post[c][i]);
+                    y[i] = fma2(m2n, b[i], mul2(y[i], w[i]));
+                }
+                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.db) + (row + k) * g.row_bytes + byte) = Pack16<T>::set(y);
+            }
+        }
+        __syncwarp();
+        if ((t & 31) == 0) mbar_arrive(&bars.empty[s]);
+        // the stage's next rows, once every warp is through with it
+        if (threadIdx.x == 0 && r0 + g.stages * step < a.N && ring_wait(bars, &bars.empty[s], phase, a.status))
+            src.issue(smem, bars, g, per, s, r0 + g.stages * step, a.N, d);
+        if (++s == g.stages) s = 0, phase ^= 1;
+    }
+    // the groups' sums, [group][d] at a time through the (now idle) ring
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        if (!(k == 0 ? a.w_pre != nullptr : k == 1 ? a.w_post != nullptr : col_gate)) continue;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int col = (c * g.tpr + t) * V;
+            if (col >= d) continue;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                float2 v;
+                unpack2(k == 0 ? s_pre[c][i] : k == 1 ? s_post[c][i] : s_gate[c][i], v.x, v.y);
+                *reinterpret_cast<float2 *>(sums + group * d + col + 2 * i) = v;
+            }
+        }
+        __syncthreads();
+        float *out = a.part + (static_cast<int64_t>(k) * gridDim.x + blockIdx.x) * d;
+        for (int i = threadIdx.x; i < d; i += blockDim.x) {
+            float v = 0.f;
+            for (int q = 0; q < g.groups; ++q) v += sums[q * d + i];
+            out[i] = v;
+        }
+        __syncthreads();
+    }
+}
+
+// Adds the blocks' column sums: eight quads of columns a block, 32 threads a
+// quad that each add every 32nd partial row, joined in a fixed order.
 template <typename T>
 __global__ void __launch_bounds__(256) k_norm_cols(const float *part, int groups, int d, T *dw_pre, T *dw_post,
                                                    T *dgate) {
-    __shared__ float red[8][33];
+    __shared__ float4 red[32][8];
     T *out = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dgate;
     if (!out) return;
-    const int x = threadIdx.x & 31, y = threadIdx.x / 32, col = blockIdx.x * 32 + x;
+    const int x = threadIdx.x & 7, y = threadIdx.x / 8, col = (blockIdx.x * 8 + x) * 4;
     const float *p = part + static_cast<int64_t>(blockIdx.y) * groups * d + col;
-    float s = 0.f;
-    if (col < d)
-        for (int g = y; g < groups; g += 8) s += p[static_cast<int64_t>(g) * d];
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < d) {
+#pragma unroll 8
+        for (int g = y; g < groups; g += 32) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + static_cast<int64_t>(g) * d);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+    }
     red[y][x] = s;
     __syncthreads();
-    if (y == 0 && col < d) {
-        for (int k = 1; k < 8; ++k) s += red[k][x];
-        out[col] = static_cast<T>(s);
+    if (y < 4 && col < d) {   // thread y of the quad takes its column y
+        const float *c = &red[0][x].x + y;
+        float v = 0.f;
+        for (int k = 0; k < 32; ++k) v += c[k * 32];
+        out[col + y] = static_cast<T>(v);
     }
 }
 
@@ -361,9 +855,62 @@ int row_threads(int d) {
 }
 int row_packs(int d) { return (d / kVec + 511) / 512; }
 
+constexpr int kRingBytes = 212 * 1024;   // dynamic shared memory of a ring kernel's block at most
+constexpr int kColGroups = 304;          // blocks of the backward at most (bounds its workspace)
+
+// The ring kernels' geometry for rows of d elements in `arrays` arrays, `ch`
+// packs a thread and `per` rows a group and stage; false where rows are too wide
+// for the threads of a block or for two stages.
+bool ring_geo(RingGeo *g, int d, int elt, int arrays, int ch, int per) {
+    const int packs = d * elt / 16;
+    g->tpr = ((packs + ch - 1) / ch + 31) / 32 * 32;
+    if (g->tpr > kRingThreads) return false;
+    g->groups = kRingThreads / g->tpr;
+    g->row_bytes = d * elt;
+    g->array_bytes = g->groups * per * g->row_bytes;
+    g->stage_bytes = arrays * g->array_bytes;
+    g->stages = std::min(kRingMaxStages, static_cast<int>((kRingBytes - 3 * g->row_bytes) / g->stage_bytes));
+    return g->stages >= 2;
+}
+
+// Packs a thread: as few as leave a row to 32 threads, at most `most`.
+int ring_packs(int d, int elt, int most) {
+    int ch = 1;
+    while (ch < most && d * elt / 16 > 32 * ch) ch *= 2;
+    return ch;
+}
+
+// Rows are handed out a stage at a time; at least one block, so that column
+// sums of no rows come out as zeros.
+int ring_grid(int64_t N, int groups, int most) {
+    const int64_t n = (N + groups - 1) / groups;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(n, most)));
+}
+
+template <auto kKernel>
+lce_status_t launch_ring(const HostDev &dev, const NormArgs &r, const RingGeo &g, int grid, int smem, cudaStream_t st) {
+    const lce_status_t s = host_smem<kKernel>(dev, kRingBytes);
+    if (s != LCE_OK) return s;
+    kKernel<<<grid, g.tpr * g.groups, smem, st>>>(r, g);
+    return host_launched();
+}
+
 template <typename T>
-lce_status_t forward(const lce_norm_t *a, cudaStream_t st) {
-    const NormArgs r = make_norm(a);
+lce_status_t forward(const lce_norm_t *a, const HostDev &dev, cudaStream_t st) {
+    NormArgs r = make_norm(a);
+    r.status = dev.status;
+    RingGeo g;
+    // a few rows have nothing to run ahead of: one block a row, fewer steps before the first load
+    const int ch = ring_packs(r.d, sizeof(T), 32 / kPack<T>);
+    if (a->N > 2 * dev.sms && ring_geo(&g, r.d, sizeof(T), (r.b ? 2 : 1) + (r.gate && r.gate_full ? 1 : 0), ch, 1)) {
+        const int grid = ring_grid(a->N, g.groups, dev.sms), smem = g.stages * g.stage_bytes + 3 * g.row_bytes;
+        switch (ch) {
+            case 1: return launch_ring<k_norm_fwd_ring<T, 1>>(dev, r, g, grid, smem, st);
+            case 2: return launch_ring<k_norm_fwd_ring<T, 2>>(dev, r, g, grid, smem, st);
+            case 4: return launch_ring<k_norm_fwd_ring<T, 4>>(dev, r, g, grid, smem, st);
+            default: return launch_ring<k_norm_fwd_ring<T, 32 / kPack<T>>>(dev, r, g, grid, smem, st);   // fp32: 8
+        }
+    }
     const unsigned grid = static_cast<unsigned>(a->N);
     const int th = row_threads(r.d);
     switch (row_packs(r.d)) {
@@ -374,37 +921,45 @@ lce_status_t forward(const lce_norm_t *a, cudaStream_t st) {
     return host_launched();
 }
 
-int64_t norm_groups(const lce_norm_t *a) { return a->N < 304 ? (a->N > 0 ? a->N : 1) : 304; }
-
-template <typename K>
-lce_status_t big_smem(K kernel, int smem) {
-    if (smem + 1024 <= 48 * 1024) return LCE_OK;   // 1024: the kernel's static share
-    return host_cuda(cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-}
-
 template <typename T>
-lce_status_t backward(const lce_norm_t *a, float *part, cudaStream_t st) {
+lce_status_t backward(const lce_norm_t *a, float *part, const HostDev &dev, cudaStream_t st) {
     NormArgs r = make_norm(a);
     r.part = part;
-    const int groups = static_cast<int>(norm_groups(a));
-    const int th = row_threads(r.d), smem = 3 * r.d * 4;
+    r.status = dev.status;
+    const bool full_gate = r.gate && r.gate_full;
+    const int arrays = (r.w_pre ? 2 : 0) + (r.b ? 1 : 0) + (full_gate ? 1 : 0) + (r.dr ? 1 : 0);
+    RingGeo g;
+    int grid;
     lce_status_t s;
-    auto go = [&](auto kernel) {
-        if ((s = big_smem(kernel, smem)) != LCE_OK) return s;
-        kernel<<<groups, th, smem, st>>>(r);
-        return host_launched();
-    };
-    switch (row_packs(r.d)) {
-        case 1: s = go(k_norm_bwd<T, 1>); break;
-        case 2: s = go(k_norm_bwd<T, 2>); break;
-        default: s = go(k_norm_bwd<T, 4>); break;
+    // two rows a thread while a row's packs go round once (their sums and the column sums fill the registers), else one
+    const int packs = r.d * static_cast<int>(sizeof(T)) / 16;
+    const int ch = packs <= kRingThreads ? 1 : packs <= 2 * kRingThreads ? 2 : 16 / kPack<T>, per = ch == 1 ? 2 : 1;
+    if (ring_geo(&g, r.d, sizeof(T), arrays, ch, per)) {
+        grid = ring_grid(a->N, g.groups * per, dev.sms);
+        const int smem = std::max<int>(g.stages * g.stage_bytes + 3 * g.row_bytes, g.groups * r.d * 4);
+        switch (ch) {
+            case 1: s = launch_ring<k_norm_bwd_ring<T, 1, 2>>(dev, r, g, grid, smem, st); break;
+            case 2: s = launch_ring<k_norm_bwd_ring<T, 2, 1>>(dev, r, g, grid, smem, st); break;
+            default: s = launch_ring<k_norm_bwd_ring<T, 16 / kPack<T>, 1>>(dev, r, g, grid, smem, st);   // fp32: 4
+        }
+    } else {
+        grid = ring_grid(a->N, 1, kColGroups);
+        const int th = row_threads(r.d), smem = 3 * r.d * 4;
+        auto go = [&](auto kernel) {
+            kernel<<<grid, th, smem, st>>>(r);
+            return host_launched();
+        };
+        switch (row_packs(r.d)) {
+            case 1: s = host_smem<k_norm_bwd<T, 1>>(dev, 3 * 4096 * 4); if (s == LCE_OK) s = go(k_norm_bwd<T, 1>); break;
+            case 2: s = host_smem<k_norm_bwd<T, 2>>(dev, 3 * 8192 * 4); if (s == LCE_OK) s = go(k_norm_bwd<T, 2>); break;
+            default: s = host_smem<k_norm_bwd<T, 4>>(dev, 3 * 16384 * 4); if (s == LCE_OK) s = go(k_norm_bwd<T, 4>); break;
+        }
     }
     if (s != LCE_OK) return s;
-    T *dgate = a->gate && !a->gate_full ? static_cast<T *>(a->dgate) : nullptr;
-    T *dpre = a->w_pre ? static_cast<T *>(a->dw_pre) : nullptr, *dpost = a->w_post ? static_cast<T *>(a->dw_post) : nullptr;
+    T *dgate = r.gate && !full_gate ? static_cast<T *>(a->dgate) : nullptr;
+    T *dpre = r.w_pre ? static_cast<T *>(a->dw_pre) : nullptr, *dpost = r.w_post ? static_cast<T *>(a->dw_post) : nullptr;
     if (!dgate && !dpre && !dpost) return LCE_OK;
-    k_norm_cols<T><<<dim3((r.d + 31) / 32, 3), 256, 0, st>>>(part, groups, r.d, dpre, dpost, dgate);
+    k_norm_cols<T><<<dim3((r.d + 31) / 32, 3), 256, 0, st>>>(part, grid, r.d, dpre, dpost, dgate);
     return host_launched();
 }
 
@@ -414,7 +969,7 @@ extern "C" {
 
 size_t lce_block_norm_workspace_size(const lce_norm_t *a) {
     if (!a || a->N < 0 || a->N >= (int64_t(1) << 31) || a->d < 8 || a->d > kMaxD || a->d % 8) return 0;
-    return static_cast<size_t>(3 * norm_groups(a) * a->d) * sizeof(float);
+    return static_cast<size_t>(3 * kColGroups * a->d) * sizeof(float);
 }
 
 lce_status_t lce_block_norm_forward(const lce_norm_t *a) {
@@ -424,7 +979,7 @@ lce_status_t lce_block_norm_forward(const lce_norm_t *a) {
     if ((s = host_device(&dev)) != LCE_OK) return s;
     if (a->N == 0) return LCE_OK;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
-    return a->dtype == LCE_BF16 ? forward<__nv_bfloat16>(a, st) : forward<float>(a, st);
+    return a->dtype == LCE_BF16 ? forward<__nv_bfloat16>(a, dev, st) : forward<float>(a, dev, st);
 }
 
 lce_status_t lce_block_norm_backward(const lce_norm_t *a) {
@@ -437,7 +992,7 @@ lce_status_t lce_block_norm_backward(const lce_norm_t *a) {
     uint8_t *base = nullptr;
     if ((s = scratch.get(a->workspace, a->workspace_bytes, lce_block_norm_workspace_size(a), &base)) != LCE_OK) return s;
     float *part = reinterpret_cast<float *>(base);
-    return a->dtype == LCE_BF16 ? backward<__nv_bfloat16>(a, part, st) : backward<float>(a, part, st);
+    return a->dtype == LCE_BF16 ? backward<__nv_bfloat16>(a, part, dev, st) : backward<float>(a, part, dev, st);
 }
 
 }  // extern "C"
