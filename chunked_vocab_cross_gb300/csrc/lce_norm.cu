@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "f32x2.cuh"
 #include "lce_host.h"
@@ -366,21 +367,23 @@ template <typename T, int MAX>
 struct RingSource {
     const T *src[MAX];
     int64_t ld[MAX];   // row strides, elements
-    // starts the copies of the `per` rows from r0 on into stage s, if there are any
+    // Starts the copies of the `per` rows from r0 on into stage s, if there are
+    // any. Rows past the last are copies of the last: they take part with
+    // factors of zero and are not stored.
     __device__ __forceinline__ void issue(uint8_t *ring, RingBars &bars, const RingGeo &g, int per, int s, int64_t r0, int64_t N, int d) const {
         if (r0 >= N) return;
-        const int rows = static_cast<int>(min(static_cast<int64_t>(per), N - r0));
         int count = 0;
 #pragma unroll
         for (int k = 0; k < MAX; ++k) count += src[k] != nullptr;
-        mbar_arrive_expect_tx(&bars.full[s], count * rows * g.row_bytes);
+        mbar_arrive_expect_tx(&bars.full[s], count * per * g.row_bytes);
         uint8_t *dst = ring + s * g.stage_bytes;
 #pragma unroll
         for (int k = 0; k < MAX; ++k) {
             if (!src[k]) continue;
-            if (ld[k] == d) bulk_load(dst, src[k] + r0 * d, rows * g.row_bytes, &bars.full[s]);
+            if (ld[k] == d && r0 + per <= N) bulk_load(dst, src[k] + r0 * d, per * g.row_bytes, &bars.full[s]);
             else
-                for (int r = 0; r < rows; ++r) bulk_load(dst + r * g.row_bytes, src[k] + (r0 + r) * ld[k], g.row_bytes, &bars.full[s]);
+                for (int r = 0; r < per; ++r)
+                    bulk_load(dst + r * g.row_bytes, src[k] + min(r0 + r, N - 1) * ld[k], g.row_bytes, &bars.full[s]);
             dst += g.array_bytes;
         }
     }
@@ -396,32 +399,56 @@ __device__ __forceinline__ void ring_drain(RingBars &bars, const RingGeo &g, int
     }
 }
 
-// Sum of K values over the `tpr` threads of a row, the same for all of them,
-// in a fixed order; `red`: the group's 2 x K x 16 floats, zero beyond its warps.
+// Sums of K <= 8 values over the `tpr` threads of a row group, the same for all
+// of them, in a fixed order. Within a warp the values are dealt out while they
+// are added: after exchanges over 16, 8 and 4 lanes a lane is left with one
+// value's sum over a quarter of the warp (K = 1: five plain exchanges). Across
+// the warps each adds up all partial sums by lanes again. `red`: the group's
+// 2 x 8 x 16 floats, zero beyond its warps.
 template <int K>
 __device__ __forceinline__ void group_sum(float (&v)[K], float *red, int &flip, int tpr, int group, int t) {
+    constexpr int M = K == 1 ? 1 : 8;
+    const int lane = t & 31;
+    float x[M];
 #pragma unroll
-    for (int m = 16; m; m >>= 1)
+    for (int k = 0; k < M; ++k) x[k] = k < K ? v[k] : 0.f;
+    if (K == 1) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
-    if (tpr == 32) return;
-    float *at = red + flip * K * 16;
-    flip ^= 1;
-    if ((t & 31) == 0)
+        for (int m = 16; m; m >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], m);
+    } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k) at[k * 16 + t / 32] = v[k];
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-    const int quads = (tpr + 127) / 128;
+        for (int h = M / 2, m = 16; h; h >>= 1, m >>= 1) {
+            const bool up = lane & m;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const float4 *p = reinterpret_cast<const float4 *>(at + k * 16);
-        const float4 x = p[0];
-        v[k] = (x.x + x.y) + (x.z + x.w);
-        for (int w = 1; w < quads; ++w) {
-            const float4 y = p[w];
-            v[k] += (y.x + y.y) + (y.z + y.w);
+            for (int k = 0; k < M / 2; ++k)
+                if (k < h) {
+                    const float keep = up ? x[k + h] : x[k], send = up ? x[k] : x[k + h];
+                    x[k] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                }
+        }
+        x[0] += __shfl_xor_sync(0xffffffffu, x[0], 2);
+        x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+    }
+    // lane 4j (K > 1) now has the sum of value number j with its bits 4, 3, 2 in that order: j = lane >> 2
+    if (tpr > 32) {
+        float *at = red + flip * M * 16;
+        flip ^= 1;
+        if (K == 1 ? lane == 0 : (lane & 3) == 0) at[(K == 1 ? 0 : (lane >> 2)) * 16 + t / 32] = x[0];
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+        if (K == 1) {
+            x[0] = at[lane & 15];
+#pragma unroll
+            for (int m = 8; m; m >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], m);
+        } else {
+            // four lanes a value, four warps' sums a lane
+            const float4 y = *reinterpret_cast<const float4 *>(at + (lane >> 2) * 16 + (lane & 3) * 4);
+            x[0] = (y.x + y.y) + (y.z + y.w);
+            x[0] += __shfl_xor_sync(0xffffffffu, x[0], 2);
+            x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
         }
     }
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = K == 1 ? x[0] : __shfl_sync(0xffffffffu, x[0], 4 * k);
 }
 
 // Weights of a row into shared memory, `rows` of them (ones where there is none)
@@ -432,9 +459,11 @@ __device__ __forceinline__ void load_weights(uint8_t *dst, const void *w, int ro
         *reinterpret_cast<uint4 *>(dst + i) = w ? *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(w) + i) : make_uint4(o, o, o, o);
 }
 
-constexpr int kRedFloats = 2 * 3 * 16;   // of a row group
+constexpr int kRedFloats = 2 * 8 * 16;   // of a row group
 
-template <typename T, int CH>
+// kAll: b, w_post and w_pre are there and the gate, if any, is per channel; the
+// options are then known when the kernel is compiled.
+template <typename T, int CH, bool kAll>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArgs a, const RingGeo g) {
     constexpr int V = kPack<T>, P = V / 2;
     extern __shared__ __align__(128) uint8_t smem[];   // ring, then w_post, gate, w_pre
@@ -447,7 +476,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
         fence_mbar_init();
     }
     const int d = a.d;
-    const bool full_gate = a.gate && a.gate_full;
+    const bool has_b = kAll || a.b, has_post = kAll || a.w_post, has_pre = kAll || a.w_pre, full_gate = !kAll && a.gate && a.gate_full;
     uint8_t *w_post = smem + g.stages * g.stage_bytes, *gate = w_post + g.row_bytes, *w_pre = gate + g.row_bytes;
     load_weights<T>(w_post, a.w_post, g.row_bytes);
     load_weights<T>(gate, full_gate ? nullptr : a.gate, g.row_bytes);
@@ -463,15 +492,17 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
     const int group = threadIdx.x / g.tpr, t = threadIdx.x % g.tpr;
     float *my_red = red + group * kRedFloats;
     const float inv_d = 1.f / d;
+    uint8_t *out_r = static_cast<uint8_t *>(a.r) + (r0 + group) * g.row_bytes + t * 16;
+    uint8_t *out_n = static_cast<uint8_t *>(a.n) + (r0 + group) * g.row_bytes + t * 16;
     int flip = 0, s = 0;
     uint32_t phase = 0;
-    for (; r0 < a.N; r0 += step) {
+    for (; r0 < a.N; r0 += step, out_r += step * g.row_bytes, out_n += step * g.row_bytes) {
         const int64_t row = r0 + group;
         if (!__all_sync(0xffffffffu, ring_wait(bars, &bars.full[s], phase, a.status))) {
             if (threadIdx.x == 0) ring_drain(bars, g, g.groups, s, phase, r0, a.N);
             break;
         }
-        const bool live = row < a.N;   // the first group always is
+        const bool live = row < a.N;
         const uint8_t *at = smem + s * g.stage_bytes + group * g.row_bytes;
         f32x2 r[CH][P];
         uint4 vb[CH], vg[CH];
@@ -482,16 +513,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
             vb[c] = vg[c] = x;
             if (byte < g.row_bytes) {
                 x = *reinterpret_cast<const uint4 *>(at + byte);
-                if (a.b) vb[c] = *reinterpret_cast<const uint4 *>(at + g.array_bytes + byte);
+                if (has_b) vb[c] = *reinterpret_cast<const uint4 *>(at + g.array_bytes + byte);
                 if (full_gate) vg[c] = *reinterpret_cast<const uint4 *>(at + 2 * g.array_bytes + byte);
             }
             Pack16<T>::get(x, r[c]);
         }
         __syncwarp();
         if ((t & 31) == 0) mbar_arrive(&bars.empty[s]);   // everything is in registers
-        if (live) {
+        {
             float rs = 1.f;
-            if (a.w_post) {
+            if (has_post) {
                 f32x2 q = both(0.f);
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
@@ -503,9 +534,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
                 float sum[1] = {hsum2(q)};
                 group_sum(sum, my_red, flip, g.tpr, group, t);
                 rs = rsqrtf(sum[0] * inv_d + a.eps);
-                if (t == 0) a.rstd_post[row] = rs;
+                if (t == 0 && live) a.rstd_post[row] = rs;
             }
-            if (a.b) {
+            if (has_b) {
                 const f32x2 f = both(rs * a.scale);
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
@@ -519,12 +550,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
                     Pack16<T>::get(full_gate ? vg[c] : *reinterpret_cast<const uint4 *>(gate + byte), w);
 #pragma unroll
                     for (int i = 0; i < P; ++i) r[c][i] = fma2(mul2(y[i], w[i]), f, r[c][i]);
-                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.r) + row * g.row_bytes + byte) = Pack16<T>::set(r[c]);
+                    if (live) *reinterpret_cast<uint4 *>(out_r + c * g.tpr * 16) = Pack16<T>::set(r[c]);
                 }
             }
         }
         float sum[1] = {0.f};
-        if (live && a.w_pre) {
+        if (has_pre) {
             f32x2 q = both(0.f);
 #pragma unroll
             for (int c = 0; c < CH; ++c)
@@ -536,9 +567,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
         // the stage's next rows, once every warp has taken its share
         if (threadIdx.x == 0 && r0 + g.stages * step < a.N && ring_wait(bars, &bars.empty[s], phase, a.status))
             src.issue(smem, bars, g, g.groups, s, r0 + g.stages * step, a.N, d);
-        if (live && a.w_pre) {
+        if (has_pre) {
             const float rs = rsqrtf(sum[0] * inv_d + a.eps);
-            if (t == 0) a.rstd_pre[row] = rs;
+            if (t == 0 && live) a.rstd_pre[row] = rs;
             const f32x2 f = both(rs);
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
@@ -548,7 +579,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
                 Pack16<T>::get(*reinterpret_cast<const uint4 *>(w_pre + byte), w);
 #pragma unroll
                 for (int i = 0; i < P; ++i) w[i] = mul2(mul2(r[c][i], f), w[i]);
-                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.n) + row * g.row_bytes + byte) = Pack16<T>::set(w);
+                if (live) *reinterpret_cast<uint4 *>(out_n + c * g.tpr * 16) = Pack16<T>::set(w);
             }
         }
         if (++s == g.stages) s = 0, phase ^= 1;
@@ -564,12 +595,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
 // A thread takes its columns of R rows at a time, which halves what it spends
 // on weights. The column sums stay in registers, one set a row group, and are
 // joined across the groups in shared memory at the end.
-template <typename T, int CH, int R>
+// kAll: dr, dn, b and w_pre are there and the gate, if any, is per channel.
+template <typename T, int CH, int R, bool kAll>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArgs a, const RingGeo g) {
     constexpr int V = kPack<T>, P = V / 2;
     extern __shared__ __align__(128) uint8_t smem[];   // ring, then w_post, gate, w_pre
     __shared__ RingBars bars;
-    __shared__ __align__(16) float red[16 * kRedFloats * R];
+    __shared__ __align__(16) float red[16 * kRedFloats];
     const int nwarps = blockDim.x / 32;
     if (threadIdx.x == 0) {
         for (int i = 0; i < g.stages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], nwarps);
@@ -577,12 +609,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
         fence_mbar_init();
     }
     const int d = a.d;
-    const bool full_gate = a.gate && a.gate_full, col_gate = a.gate && !a.gate_full;
+    const bool has_pre = kAll || a.w_pre, has_b = kAll || a.b, has_dr = kAll || a.dr, full_gate = !kAll && a.gate && a.gate_full;
     uint8_t *w_post = smem + g.stages * g.stage_bytes, *gate = w_post + g.row_bytes, *w_pre = gate + g.row_bytes;
     load_weights<T>(w_post, a.w_post, g.row_bytes);
     load_weights<T>(gate, full_gate ? nullptr : a.gate, g.row_bytes);
     load_weights<T>(w_pre, a.w_pre, g.row_bytes);
-    for (int i = threadIdx.x; i < 16 * kRedFloats * R; i += blockDim.x) red[i] = 0.f;
+    for (int i = threadIdx.x; i < 16 * kRedFloats; i += blockDim.x) red[i] = 0.f;
     __syncthreads();
     const int per = g.groups * R;   // rows of a stage
     const int64_t step = static_cast<int64_t>(gridDim.x) * per;
@@ -591,31 +623,33 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
                                    static_cast<const T *>(a.b), full_gate ? static_cast<const T *>(a.gate) : nullptr, static_cast<const T *>(a.dr)},
                                   {a.ld_r, a.ld_dn, a.ld_b, a.ld_gate, a.ld_dr}};
     // places of the arrays in a stage
-    const uint32_t at_n = g.array_bytes, at_b = a.w_pre ? 2 * g.array_bytes : 0, at_g = at_b + (a.b ? g.array_bytes : 0),
+    const uint32_t at_n = g.array_bytes, at_b = has_pre ? 2 * g.array_bytes : 0, at_g = at_b + (has_b ? g.array_bytes : 0),
                    at_d = at_g + (full_gate ? g.array_bytes : 0);
     if (threadIdx.x == 0)
         for (int i = 0; i < g.stages; ++i) src.issue(smem, bars, g, per, i, r0 + i * step, a.N, d);
     const int group = threadIdx.x / g.tpr, t = threadIdx.x % g.tpr;
-    float *my_red = red + group * kRedFloats * R;
+    float *my_red = red + group * kRedFloats;
     const float inv_d = 1.f / d;
     f32x2 s_pre[CH][P], s_post[CH][P], s_gate[CH][P];
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int i = 0; i < P; ++i) s_pre[c][i] = s_post[c][i] = s_gate[c][i] = both(0.f);
+    uint8_t *out_x = static_cast<uint8_t *>(a.dx) + (r0 + group * R) * g.row_bytes + t * 16;
+    uint8_t *out_b = static_cast<uint8_t *>(a.db) + (r0 + group * R) * g.row_bytes + t * 16;
     int flip = 0, s = 0;
     uint32_t phase = 0;
-    float rp_next[R], ro_next[R];   // 1/rms of the rows to come, asked for a round ahead
+    float rp_next[R], ro_next[R];   // 1/rms of the rows to come, asked for a round ahead; zeros past the last row
     auto rstd = [&](int64_t row) {
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             const bool live = row + k < a.N;
-            rp_next[k] = a.w_pre && live ? a.rstd_pre[row + k] : 0.f;
-            ro_next[k] = a.w_post && live ? a.rstd_post[row + k] : 1.f;
+            rp_next[k] = has_pre && live ? a.rstd_pre[row + k] : 0.f;
+            ro_next[k] = !live ? 0.f : a.w_post ? a.rstd_post[row + k] : 1.f;
         }
     };
     rstd(r0 + group * R);
-    for (; r0 < a.N; r0 += step) {
+    for (; r0 < a.N; r0 += step, out_x += step * g.row_bytes, out_b += step * g.row_bytes) {
         const int64_t row = r0 + group * R;
         float rp[R], ro[R];
 #pragma unroll
@@ -654,14 +688,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
                 const uint8_t *p = at + k * g.row_bytes + byte;
                 uint4 v = make_uint4(0, 0, 0, 0), vn = v, vd = v;
                 vb[k][c] = v;
-                // rows past the last hold what an earlier round left (or nothing at all): they count as zeros
-                const bool live = row + k < a.N;
-                if (live && a.w_pre) {
+                if (has_pre) {
                     v = *reinterpret_cast<const uint4 *>(p);
                     vn = *reinterpret_cast<const uint4 *>(p + at_n);
                 }
-                if (live && a.b) vb[k][c] = *reinterpret_cast<const uint4 *>(p + at_b);
-                if (live && a.dr) vd = *reinterpret_cast<const uint4 *>(p + at_d);
+                if (has_b) vb[k][c] = *reinterpret_cast<const uint4 *>(p + at_b);
+                if (has_dr) vd = *reinterpret_cast<const uint4 *>(p + at_d);
                 Pack16<T>::get(v, hat[k][c]);
                 Pack16<T>::get(vn, u);
                 Pack16<T>::get(vd, x[k][c]);
@@ -675,7 +707,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
                     x[k][c][i] = fma2(rp2, u[i], x[k][c][i]);
                 }
                 Pack16<T>::get(vb[k][c], u);
-                if (full_gate && live) {
+                if (full_gate) {
                     f32x2 gt[P];
                     Pack16<T>::get(*reinterpret_cast<const uint4 *>(p + at_g), gt);
 #pragma unroll
@@ -704,15 +736,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
             Pack16<T>::get(*reinterpret_cast<const uint4 *>(gate + byte), gw);
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                if (row + k >= a.N) continue;
+                const bool live = row + k < a.N;
+                const uint32_t o = k * g.row_bytes + c * g.tpr * 16;
                 const float m1 = rp[k] * sum[3 * k] * inv_d, f = a.scale * ro[k];
                 const f32x2 m1n = both(-m1), f2 = both(f);
                 const f32x2 m2n = both(a.w_post ? -(ro[k] * ro[k] * f * (sum[3 * k + 1] - m1 * sum[3 * k + 2]) * inv_d) : 0.f);
                 f32x2 (&y)[P] = x[k][c];
 #pragma unroll
                 for (int i = 0; i < P; ++i) y[i] = fma2(m1n, hat[k][c][i], y[i]);
-                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dx) + (row + k) * g.row_bytes + byte) = Pack16<T>::set(y);
-                if (!a.b) continue;
+                if (live) *reinterpret_cast<uint4 *>(out_x + o) = Pack16<T>::set(y);
+                if (!has_b) continue;
                 f32x2 b[P], dg[P];
                 Pack16<T>::get(vb[k][c], b);
 #pragma unroll
@@ -722,7 +755,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
                     Pack16<T>::get(*reinterpret_cast<const uint4 *>(at + k * g.row_bytes + byte + at_g), gt);
 #pragma unroll
                     for (int i = 0; i < P; ++i) dg[i] = mul2(y[i], dg[i]), y[i] = mul2(y[i], gt[i]);
-                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dgate) + (row + k) * g.row_bytes + byte) = Pack16<T>::set(dg);
+                    if (live) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dgate) + (row + k) * g.row_bytes + byte) = Pack16<T>::set(dg);
                 } else {
 #pragma unroll
                     for (int i = 0; i < P; ++i) s_gate[c][i] = fma2(y[i], dg[i], s_gate[c][i]), y[i] = mul2(y[i], gw[i]);
@@ -732,7 +765,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
                     s_post[c][i] = fma2(y[i], b[i], s_post[c][i]);
                     y[i] = fma2(m2n, b[i], mul2(y[i], w[i]));
                 }
-                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.db) + (row + k) * g.row_bytes + byte) = Pack16<T>::set(y);
+                if (live) *reinterpret_cast<uint4 *>(out_b + o) = Pack16<T>::set(y);
             }
         }
         __syncwarp();
@@ -747,7 +780,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
     float *sums = reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        if (!(k == 0 ? a.w_pre != nullptr : k == 1 ? a.w_post != nullptr : col_gate)) continue;
+        if (!(k == 0 ? a.w_pre != nullptr : k == 1 ? a.w_post != nullptr : a.gate && !a.gate_full)) continue;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int col = (c * g.tpr + t) * V;
@@ -855,7 +888,7 @@ int row_threads(int d) {
 }
 int row_packs(int d) { return (d / kVec + 511) / 512; }
 
-constexpr int kRingBytes = 212 * 1024;   // dynamic shared memory of a ring kernel's block at most
+constexpr int kRingBytes = 208 * 1024;   // dynamic shared memory of a ring kernel's block at most
 constexpr int kColGroups = 304;          // blocks of the backward at most (bounds its workspace)
 
 // The ring kernels' geometry for rows of d elements in `arrays` arrays, `ch`
@@ -904,11 +937,17 @@ lce_status_t forward(const lce_norm_t *a, const HostDev &dev, cudaStream_t st) {
     const int ch = ring_packs(r.d, sizeof(T), 32 / kPack<T>);
     if (a->N > 2 * dev.sms && ring_geo(&g, r.d, sizeof(T), (r.b ? 2 : 1) + (r.gate && r.gate_full ? 1 : 0), ch, 1)) {
         const int grid = ring_grid(a->N, g.groups, dev.sms), smem = g.stages * g.stage_bytes + 3 * g.row_bytes;
+        const bool all = r.b && r.w_post && r.w_pre && !(r.gate && r.gate_full);
+        auto go = [&](auto c) {
+            constexpr int CH = decltype(c)::value;
+            return all ? launch_ring<k_norm_fwd_ring<T, CH, true>>(dev, r, g, grid, smem, st)
+                       : launch_ring<k_norm_fwd_ring<T, CH, false>>(dev, r, g, grid, smem, st);
+        };
         switch (ch) {
-            case 1: return launch_ring<k_norm_fwd_ring<T, 1>>(dev, r, g, grid, smem, st);
-            case 2: return launch_ring<k_norm_fwd_ring<T, 2>>(dev, r, g, grid, smem, st);
-            case 4: return launch_ring<k_norm_fwd_ring<T, 4>>(dev, r, g, grid, smem, st);
-            default: return launch_ring<k_norm_fwd_ring<T, 32 / kPack<T>>>(dev, r, g, grid, smem, st);   // fp32: 8
+            case 1: return go(std::integral_constant<int, 1>());
+            case 2: return go(std::integral_constant<int, 2>());
+            case 4: return go(std::integral_constant<int, 4>());
+            default: return go(std::integral_constant<int, 32 / kPack<T>>());   // fp32: 8
         }
     }
     const unsigned grid = static_cast<unsigned>(a->N);
@@ -937,10 +976,16 @@ lce_status_t backward(const lce_norm_t *a, float *part, const HostDev &dev, cuda
     if (ring_geo(&g, r.d, sizeof(T), arrays, ch, per)) {
         grid = ring_grid(a->N, g.groups * per, dev.sms);
         const int smem = std::max<int>(g.stages * g.stage_bytes + 3 * g.row_bytes, g.groups * r.d * 4);
+        const bool all = r.w_pre && r.b && r.dr && !full_gate;
+        auto go = [&](auto c, auto rows) {
+            constexpr int CH = decltype(c)::value, R = decltype(rows)::value;
+            return all ? launch_ring<k_norm_bwd_ring<T, CH, R, true>>(dev, r, g, grid, smem, st)
+                       : launch_ring<k_norm_bwd_ring<T, CH, R, false>>(dev, r, g, grid, smem, st);
+        };
         switch (ch) {
-            case 1: s = launch_ring<k_norm_bwd_ring<T, 1, 2>>(dev, r, g, grid, smem, st); break;
-            case 2: s = launch_ring<k_norm_bwd_ring<T, 2, 1>>(dev, r, g, grid, smem, st); break;
-            default: s = launch_ring<k_norm_bwd_ring<T, 16 / kPack<T>, 1>>(dev, r, g, grid, smem, st);   // fp32: 4
+            case 1: s = go(std::integral_constant<int, 1>(), std::integral_constant<int, 2>()); break;
+            case 2: s = go(std::integral_constant<int, 2>(), std::integral_constant<int, 1>()); break;
+            default: s = go(std::integral_constant<int, 16 / kPack<T>>(), std::integral_constant<int, 1>());   // fp32: 4
         }
     } else {
         grid = ring_grid(a->N, 1, kColGroups);
