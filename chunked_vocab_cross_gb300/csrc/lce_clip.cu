@@ -9,7 +9,9 @@ namespace {
 
 constexpr int kClipThreads = 256;
 constexpr int kChunkBytes = 32768;   // bytes of a tensor that a block takes at a time
-constexpr int kTable = 240;          // tensors a launch takes (the table travels as a kernel argument)
+// Tensors a launch takes: the table travels as a kernel argument, whose size
+// the launch pays for, so a short list gets a short table.
+constexpr int kTable = 240, kShortTable = 32;
 constexpr int kBlocksPerSm = 8;
 constexpr int kMaxBlocks = 256 * kBlocksPerSm;
 
@@ -17,19 +19,21 @@ struct ClipEntry {
     const void *g;
     void *out;
     int64_t n;
-    int first;   // number of the tensor's first chunk within the launch
     int fp32;
 };
+template <int N>
 struct ClipTable {
-    ClipEntry t[kTable];
     int count, chunks;
+    int first[N];   // number of a tensor's first chunk within the launch; apart from the rest, since it is searched
+    ClipEntry t[N];
 };
 
-__device__ __forceinline__ int entry_of(const ClipTable &tab, int chunk) {
+template <int N>
+__device__ __forceinline__ int entry_of(const ClipTable<N> &tab, int chunk) {
     int lo = 0, hi = tab.count;   // the last entry with first <= chunk
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (tab.t[mid].first <= chunk) lo = mid;
+        if (tab.first[mid] <= chunk) lo = mid;
         else hi = mid;
     }
     return lo;
@@ -99,12 +103,14 @@ __device__ __forceinline__ double block_sum(double v) {
 
 // part[block] = sum of the squares of the block's chunks: fp32 along a
 // thread's elements of one chunk, fp64 across chunks and threads.
-__global__ void __launch_bounds__(kClipThreads) k_clip_squares(const __grid_constant__ ClipTable tab, double *part) {
+template <int N>
+__global__ void __launch_bounds__(kClipThreads) k_clip_squares(const __grid_constant__ ClipTable<N> tab, double *part) {
     double s = 0.0;
     for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-        const ClipEntry &e = tab.t[entry_of(tab, c)];
-        s += e.fp32 ? span_squares<float>(e, span_of<float>(e, c - e.first))
-                    : span_squares<__nv_bfloat16>(e, span_of<__nv_bfloat16>(e, c - e.first));
+        const int i = entry_of(tab, c), k = c - tab.first[i];
+        const ClipEntry &e = tab.t[i];
+        s += e.fp32 ? span_squares<float>(e, span_of<float>(e, k))
+                    : span_squares<__nv_bfloat16>(e, span_of<__nv_bfloat16>(e, k));
     }
     s = block_sum(s);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -133,7 +139,7 @@ __device__ __forceinline__ void span_scale(const ClipEntry &e, const Span &sp, f
     for (int64_t i = vb + threadIdx.x * kV; i < ve; i += kClipThreads * kV) {
         if (sizeof(T) == 4) {
             float4 v = *reinterpret_cast<const float4 *>(g + i);
-            *reinterpret_cast<float4 *>(o + i) = make_float4(v.x * c, v.y * c, v.z * c, v.w * c);
+            __stcs(reinterpret_cast<float4 *>(o + i), make_float4(v.x * c, v.y * c, v.z * c, v.w * c));
         } else {
             const uint4 v = *reinterpret_cast<const uint4 *>(g + i);
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -143,15 +149,17 @@ __device__ __forceinline__ void span_scale(const ClipEntry &e, const Span &sp, f
                                                          __uint_as_float(w[k] & 0xffff0000u) * c);
                 w[k] = *reinterpret_cast<uint32_t *>(&p);
             }
-            *reinterpret_cast<uint4 *>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            __stcs(reinterpret_cast<uint4 *>(o + i), make_uint4(w[0], w[1], w[2], w[3]));
         }
     }
     for (int64_t i = ve + threadIdx.x; i < sp.end; i += kClipThreads) o[i] = static_cast<T>(f32(g[i]) * c);
 }
 
 // Every block adds up the partial sums itself (a few KB, in L2), forms the
-// factor and scales its chunks.
-__global__ void __launch_bounds__(kClipThreads) k_clip_scale(const __grid_constant__ ClipTable tab, const double *part,
+// factor and scales its chunks, the last ones first: they are what the squares
+// left in L2, and the stores ask to be evicted before them.
+template <int N>
+__global__ void __launch_bounds__(kClipThreads) k_clip_scale(const __grid_constant__ ClipTable<N> tab, const double *part,
                                                              int n, float max_norm, float eps, int in_place,
                                                              float *norm, float *factor) {
     const float v = norm_of(part, n);
@@ -162,10 +170,11 @@ __global__ void __launch_bounds__(kClipThreads) k_clip_scale(const __grid_consta
         if (factor) *factor = c;
     }
     if (in_place && c == 1.f) return;
-    for (int k = blockIdx.x; k < tab.chunks; k += gridDim.x) {
-        const ClipEntry &e = tab.t[entry_of(tab, k)];
-        if (e.fp32) span_scale<float>(e, span_of<float>(e, k - e.first), c);
-        else span_scale<__nv_bfloat16>(e, span_of<__nv_bfloat16>(e, k - e.first), c);
+    for (int j = tab.chunks - 1 - blockIdx.x; j >= 0; j -= gridDim.x) {
+        const int i = entry_of(tab, j), k = j - tab.first[i];
+        const ClipEntry &e = tab.t[i];
+        if (e.fp32) span_scale<float>(e, span_of<float>(e, k), c);
+        else span_scale<__nv_bfloat16>(e, span_of<__nv_bfloat16>(e, k), c);
     }
 }
 
@@ -186,59 +195,76 @@ lce_status_t check_clip(int64_t count, const void *const *grads, void *const *ou
 }
 
 // The tensors from `*at` on that fit one launch.
-void fill_table(ClipTable &tab, int64_t *at, int64_t count, const void *const *grads, void *const *outs,
+template <int N>
+void fill_table(ClipTable<N> &tab, int64_t *at, int64_t count, const void *const *grads, void *const *outs,
                 const int64_t *sizes, const int32_t *dtypes) {
     tab.count = tab.chunks = 0;
-    for (; *at < count && tab.count < kTable; ++*at) {
+    for (; *at < count && tab.count < N; ++*at) {
         const int64_t i = *at;
         if (sizes[i] == 0) continue;
         const int elt = dtypes[i] == LCE_BF16 ? 2 : 4;
         const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(grads[i]) % 16);
         const int64_t chunks = (sizes[i] * elt + lead + kChunkBytes - 1) / kChunkBytes;
         if (tab.count && tab.chunks + chunks >= (int64_t(1) << 30)) break;
-        tab.t[tab.count++] = ClipEntry{grads[i], outs ? outs[i] : const_cast<void *>(grads[i]), sizes[i], tab.chunks,
+        tab.first[tab.count] = tab.chunks;
+        tab.t[tab.count++] = ClipEntry{grads[i], outs ? outs[i] : const_cast<void *>(grads[i]), sizes[i],
                                        dtypes[i] == LCE_FP32};
         tab.chunks += static_cast<int>(chunks);
     }
 }
 
-lce_status_t run_clip(int64_t count, const void *const *grads, void *const *outs, const int64_t *sizes,
-                      const int32_t *dtypes, bool clip, float max_norm, float eps, float *norm, float *factor,
-                      void *workspace, size_t workspace_bytes, lce_stream_t stream) {
-    lce_status_t s = check_clip(count, grads, outs, sizes, dtypes, norm);
+struct ClipCall {
+    int64_t count;
+    const void *const *grads;
+    void *const *outs;
+    const int64_t *sizes;
+    const int32_t *dtypes;
+    bool clip;
+    float max_norm, eps;
+    float *norm, *factor;
+};
+
+template <int N>
+lce_status_t launch_clip(const ClipCall &a, const HostDev &dev, double *part, cudaStream_t st) {
+    lce_status_t s;
+    ClipTable<N> tab;
+    int n = 0;
+    const int most = dev.sms * kBlocksPerSm < kMaxBlocks ? dev.sms * kBlocksPerSm : kMaxBlocks;
+    for (int64_t at = 0; at < a.count;) {
+        fill_table(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
+        if (!tab.count) break;
+        const int blocks = tab.chunks < most ? tab.chunks : most;
+        k_clip_squares<N><<<blocks, kClipThreads, 0, st>>>(tab, part + n);
+        if ((s = host_launched()) != LCE_OK) return s;
+        n += blocks;
+    }
+    if (!a.clip) {
+        k_clip_norm<<<1, kClipThreads, 0, st>>>(part, n, a.norm);
+        return host_launched();
+    }
+    bool done = false;
+    for (int64_t at = 0; at < a.count || !done;) {
+        fill_table(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
+        if (!tab.count && done) break;
+        const int blocks = tab.chunks < 1 ? 1 : tab.chunks < most ? tab.chunks : most;
+        k_clip_scale<N><<<blocks, kClipThreads, 0, st>>>(tab, part, n, a.max_norm, a.eps, a.outs == nullptr, a.norm, a.factor);
+        if ((s = host_launched()) != LCE_OK) return s;
+        done = true;
+    }
+    return LCE_OK;
+}
+
+lce_status_t run_clip(const ClipCall &a, void *workspace, size_t workspace_bytes, lce_stream_t stream) {
+    lce_status_t s = check_clip(a.count, a.grads, a.outs, a.sizes, a.dtypes, a.norm);
     if (s != LCE_OK) return s;
     HostDev dev;
     if ((s = host_device(&dev)) != LCE_OK) return s;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     HostScratch scratch(st);
     uint8_t *base = nullptr;
-    if ((s = scratch.get(workspace, workspace_bytes, lce_clip_workspace_size(count), &base)) != LCE_OK) return s;
+    if ((s = scratch.get(workspace, workspace_bytes, lce_clip_workspace_size(a.count), &base)) != LCE_OK) return s;
     double *part = reinterpret_cast<double *>(base);
-    ClipTable tab;
-    int n = 0;
-    const int most = dev.sms * kBlocksPerSm < kMaxBlocks ? dev.sms * kBlocksPerSm : kMaxBlocks;
-    for (int64_t at = 0; at < count;) {
-        fill_table(tab, &at, count, grads, outs, sizes, dtypes);
-        if (!tab.count) break;
-        const int blocks = tab.chunks < most ? tab.chunks : most;
-        k_clip_squares<<<blocks, kClipThreads, 0, st>>>(tab, part + n);
-        if ((s = host_launched()) != LCE_OK) return s;
-        n += blocks;
-    }
-    if (!clip) {
-        k_clip_norm<<<1, kClipThreads, 0, st>>>(part, n, norm);
-        return host_launched();
-    }
-    bool done = false;
-    for (int64_t at = 0; at < count || !done;) {
-        fill_table(tab, &at, count, grads, outs, sizes, dtypes);
-        if (!tab.count && done) break;
-        const int blocks = tab.chunks < 1 ? 1 : tab.chunks < most ? tab.chunks : most;
-        k_clip_scale<<<blocks, kClipThreads, 0, st>>>(tab, part, n, max_norm, eps, outs == nullptr, norm, factor);
-        if ((s = host_launched()) != LCE_OK) return s;
-        done = true;
-    }
-    return LCE_OK;
+    return a.count <= kShortTable ? launch_clip<kShortTable>(a, dev, part, st) : launch_clip<kTable>(a, dev, part, st);
 }
 
 }  // namespace
@@ -252,16 +278,14 @@ size_t lce_clip_workspace_size(int64_t count) {
 
 lce_status_t lce_grad_norm(int64_t count, const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
                            float *norm, void *workspace, size_t workspace_bytes, lce_stream_t stream) {
-    return run_clip(count, grads, nullptr, sizes, dtypes, false, 0.f, 0.f, norm, nullptr, workspace, workspace_bytes,
-                    stream);
+    return run_clip({count, grads, nullptr, sizes, dtypes, false, 0.f, 0.f, norm, nullptr}, workspace, workspace_bytes, stream);
 }
 
 lce_status_t lce_clip_grads(int64_t count, const void *const *grads, void *const *outs, const int64_t *sizes,
                             const int32_t *dtypes, float max_norm, float eps, float *norm, float *factor,
                             void *workspace, size_t workspace_bytes, lce_stream_t stream) {
     if (!(max_norm >= 0.f) || !(eps >= 0.f)) return LCE_ERR_ARG;
-    return run_clip(count, grads, outs, sizes, dtypes, true, max_norm, eps, norm, factor, workspace, workspace_bytes,
-                    stream);
+    return run_clip({count, grads, outs, sizes, dtypes, true, max_norm, eps, norm, factor}, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
