@@ -115,27 +115,38 @@ lce_status_t forward_simt(const AttnArgs &r, const HostDev &dev, cudaStream_t st
     return launch<k_attn_fwd_simt<DP>>(dev, slots * r.Hq, kSimtThreads, simt_smem(DP, 3, 1), st, r);
 }
 
+// Row statistics: 16 bytes a lane, as many lanes a row as it needs (8, 16 or 32).
+template <typename T, int TILE>
+lce_status_t row_stats(const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
+    const int64_t blocks = seq_slots(r.sq.T, r.sq.B, TILE) * r.Hq;
+    const int lanes = r.D * static_cast<int>(sizeof(T)) / 16;
+    if (lanes <= 8) return launch<k_attn_stats<T, TILE, 8>>(dev, blocks, kStatThreads, 0, st, r);
+    if constexpr (sizeof(T) == 4)
+        if (lanes > 16) return launch<k_attn_stats<T, TILE, 32>>(dev, blocks, kStatThreads, 0, st, r);
+    return launch<k_attn_stats<T, TILE, 16>>(dev, blocks, kStatThreads, 0, st, r);
+}
+
 template <int DP>
 lce_status_t backward_simt(const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
-    const int64_t qslots = seq_slots(r.sq.T, r.sq.B, kSimtTile), kslots = seq_slots(r.sk.T, r.sk.B, kSimtTile);
-    lce_status_t s = launch<k_attn_stats<float, kSimtTile>>(dev, qslots * r.Hq, 256, 0, st, r);
-    if (s == LCE_OK && r.sq.T > 0) s = launch<k_attn_dq_simt<DP>>(dev, qslots * r.Hq, kSimtThreads, simt_smem(DP, 4, 1), st, r);
-    if (s == LCE_OK && r.sk.T > 0) s = launch<k_attn_dkv_simt<DP>>(dev, kslots * r.Hk, kSimtThreads, simt_smem(DP, 4, 2), st, r);
-    return s;
+    const int64_t dq = seq_slots(r.sq.T, r.sq.B, kSimtTile) * r.Hq, dkv = seq_slots(r.sk.T, r.sk.B, kSimtTile) * r.Hk;
+    if (dq + dkv >= (int64_t(1) << 31)) return LCE_ERR_SHAPE;
+    const lce_status_t s = row_stats<float, kSimtTile>(r, dev, st);
+    return s != LCE_OK ? s : launch<k_attn_bwd_simt<DP>>(dev, dq + dkv, kSimtThreads, simt_smem(DP, 4, 2), st, r, static_cast<int>(dkv));
 }
 
 template <int KS>
 lce_status_t backward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
+    const int64_t dq = seq_slots(r.sq.T, r.sq.B, kTcTile) * r.Hq, dkv = seq_slots(r.sk.T, r.sk.B, kTcTile) * r.Hk;
+    if (dq + dkv >= (int64_t(1) << 31)) return LCE_ERR_SHAPE;
     AttnMaps maps;
     lce_status_t s = encode(&maps.q, dev, a->q, a->Tq, a->Hq, a->D, a->q_ts, a->q_hs);
     if (s == LCE_OK) s = encode(&maps.k, dev, a->k, a->Tk, a->Hk, a->D, a->k_ts, a->k_hs);
     if (s == LCE_OK) s = encode(&maps.v, dev, a->v, a->Tk, a->Hk, a->D, a->v_ts, a->v_hs);
     if (s == LCE_OK) s = encode(&maps.dO, dev, a->dO, a->Tq, a->Hq, a->D, a->dO_ts, a->dO_hs);
-    const int64_t qslots = seq_slots(r.sq.T, r.sq.B, kTcTile), kslots = seq_slots(r.sk.T, r.sk.B, kTcTile);
-    if (s == LCE_OK) s = launch<k_attn_stats<__nv_bfloat16, kTcTile>>(dev, qslots * r.Hq, 256, 0, st, r);
-    if (s == LCE_OK && r.sk.T > 0) s = launch<k_attn_dkv<KS>>(dev, kslots * r.Hk, kBwdThreads, DkvSmem<KS>::kBytes, st, r, maps);
-    if (s == LCE_OK && r.sq.T > 0) s = launch<k_attn_dq<KS>>(dev, qslots * r.Hq, kBwdThreads, DqSmem<KS>::kBytes, st, r, maps);
-    return s;
+    if (s == LCE_OK) s = row_stats<__nv_bfloat16, kTcTile>(r, dev, st);
+    if (s != LCE_OK) return s;
+    constexpr int smem = DqSmem<KS>::kBytes > DkvSmem<KS>::kBytes ? DqSmem<KS>::kBytes : DkvSmem<KS>::kBytes;
+    return launch<k_attn_bwd<KS>>(dev, dq + dkv, kBwdThreads, smem, st, r, maps, static_cast<int>(dkv));
 }
 
 // The tensor-core kernels exist for 64, 80, 96 and 128 channels; others run as the next of these.
@@ -171,7 +182,7 @@ lce_status_t lce_attention_forward(const lce_attn_t *a) {
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
     if (a->dtype == LCE_BF16)
         return by_channels(a->D, [&](auto ks) { return forward_tc<decltype(ks)::value>(a, r, dev, st); });
-    return a->D <= 64 ? forward_simt<64>(r, dev, st) : forward_simt<128>(r, dev, st);
+    return a->D <= 32 ? forward_simt<32>(r, dev, st) : a->D <= 64 ? forward_simt<64>(r, dev, st) : forward_simt<128>(r, dev, st);
 }
 
 lce_status_t lce_attention_backward(const lce_attn_t *a) {
@@ -197,7 +208,7 @@ lce_status_t lce_attention_backward(const lce_attn_t *a) {
     r.delta = r.lse2 + r.stat_stride * r.Hq;
     if (a->dtype == LCE_BF16)
         return by_channels(a->D, [&](auto ks) { return backward_tc<decltype(ks)::value>(a, r, dev, st); });
-    return a->D <= 64 ? backward_simt<64>(r, dev, st) : backward_simt<128>(r, dev, st);
+    return a->D <= 32 ? backward_simt<32>(r, dev, st) : a->D <= 64 ? backward_simt<64>(r, dev, st) : backward_simt<128>(r, dev, st);
 }
 
 }  // extern "C"

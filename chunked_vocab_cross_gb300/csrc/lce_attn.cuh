@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace lce {
 
 constexpr float kAttnLog2e = 1.4426950408889634f;
@@ -102,45 +104,72 @@ __device__ __forceinline__ void check_offsets(const SeqMap &m, int *status) {
     if (bad) atomicOr(status, kDevSeqlens);
 }
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T x);
-template <>
-__device__ __forceinline__ float to_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+// dot product of 16 bytes of each
+__device__ __forceinline__ float dot16(const float4 &a, const float4 &b) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w)));
+}
+__device__ __forceinline__ float dot16(const uint4 &a, const uint4 &b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+        s = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), s);
+    }
+    return s;
+}
+
+constexpr int kStatThreads = 256;
+
 // Row statistics of the backward, by slot: delta_i = dO_i . o_i in fp32 and
 // lse_i in base 2, so that the gradient kernels read aligned rows of TILE
 // values. Rows without an allowed key (lse = -inf) and rows past a sequence's
-// end get lse2 = +inf: their probabilities come out as 2^-inf = 0.
-template <typename T, int TILE>
-__global__ void __launch_bounds__(256) k_attn_stats(const AttnArgs a) {
+// end get lse2 = +inf: their probabilities come out as 2^-inf = 0. LPR lanes
+// take a row, 16 bytes each; a thread asks for all its rows before it adds any
+// up, since the kernel is nothing but waits for memory.
+template <typename T, int TILE, int LPR>
+__global__ void __launch_bounds__(kStatThreads) k_attn_stats(const AttnArgs a) {
+    using V = typename std::conditional<sizeof(T) == 4, float4, uint4>::type;
+    constexpr int kRows = kStatThreads / LPR;   // rows at once
+    constexpr int kTurns = TILE / kRows;
     const int h = blockIdx.x % a.Hq;
     const int slot = blockIdx.x / a.Hq;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    if (blockIdx.x == 0 && warp == 0) {
+    if (blockIdx.x == 0 && threadIdx.x < 32) {
         check_offsets(a.sq, a.status);
         check_offsets(a.sk, a.status);
     }
     const TileInfo t = tile_info<TILE>(a.sq, a.sk, slot);
-    const T *o = static_cast<const T *>(a.o_in) + h * a.o_hs;
-    const T *g = static_cast<const T *>(a.dO) + h * a.dO_hs;
-    for (int r = warp; r < TILE; r += 8) {
-        const int i = t.t0 + r;
-        float lse2 = INFINITY, delta = 0.f;
-        if (i >= 0 && i < t.len) {
+    const int r0 = threadIdx.x / LPR, piece = threadIdx.x % LPR;
+    constexpr int kPer = 16 / sizeof(T);
+    const bool mine = piece * kPer < a.D;
+    const T *o = static_cast<const T *>(a.o_in) + h * a.o_hs + piece * kPer;
+    const T *g = static_cast<const T *>(a.dO) + h * a.dO_hs + piece * kPer;
+    V x[kTurns], y[kTurns];
+    float l[kTurns];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int i = t.t0 + r0 + k * kRows;
+        x[k] = y[k] = V{};
+        l[k] = -INFINITY;
+        if (i >= 0 && i < t.len && t.olen > 0) {
             const int64_t tok = t.s0 + i;
-            const float l = a.lse[static_cast<int64_t>(h) * a.sq.T + tok];
-            if (l != -INFINITY && t.olen > 0) {
-                for (int c = lane; c < a.D; c += 32)
-                    delta = fmaf(to_f32(o[tok * a.o_ts + c]), to_f32(g[tok * a.dO_ts + c]), delta);
-                for (int m = 16; m; m >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, m);
-                lse2 = l * kAttnLog2e;
+            l[k] = a.lse[static_cast<int64_t>(h) * a.sq.T + tok];
+            if (mine) {
+                x[k] = *reinterpret_cast<const V *>(o + tok * a.o_ts);
+                y[k] = *reinterpret_cast<const V *>(g + tok * a.dO_ts);
             }
         }
-        if (lane == 0) {
-            const int64_t at = h * a.stat_stride + static_cast<int64_t>(slot) * TILE + r;
-            a.lse2[at] = lse2;
-            a.delta[at] = delta;
+    }
+    const int64_t at = h * a.stat_stride + static_cast<int64_t>(slot) * TILE;
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        float delta = dot16(x[k], y[k]);
+#pragma unroll
+        for (int m = LPR / 2; m; m >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, m);
+        if (piece == 0) {
+            const bool out = l[k] == -INFINITY;
+            a.lse2[at + r0 + k * kRows] = out ? INFINITY : l[k] * kAttnLog2e;
+            a.delta[at + r0 + k * kRows] = out ? 0.f : delta;
         }
     }
 }

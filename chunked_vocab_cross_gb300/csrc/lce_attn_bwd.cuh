@@ -1,12 +1,12 @@
-// Attention backward on the tensor cores (bf16): two kernels, so that every
-// gradient is summed in TMEM by one CTA in a fixed order, without atomics and
-// without a gradient buffer of partial sums. The probabilities are recomputed
-// in both (7 products of tiles instead of 5).
+// Attention backward on the tensor cores (bf16): two kinds of blocks, so that
+// every gradient is summed in TMEM by one CTA in a fixed order, without atomics
+// and without a gradient buffer of partial sums. The probabilities are
+// recomputed in both (7 products of tiles instead of 5).
 //
-// k_attn_dq: 128 query rows, walking the keys.
+// dq_block: 128 query rows, walking the keys.
 //   S = Q K^T, dP = dO V^T (128 x 128 fp32 in TMEM, rows = queries)
 //   dS = 2^(S - lse) (dP - delta), bf16 over S in TMEM;  dQ += dS K
-// k_attn_dkv: 128 keys of one key head, walking the queries of its query heads.
+// dkv_block: 128 keys of one key head, walking the queries of its query heads.
 //   S^T = K Q^T, dP^T = V dO^T (rows = keys)
 //   P^T over S^T: dV += P^T dO;  dS^T over dP^T: dK += dS^T Q
 // P and dS go back to TMEM as the A operands, so they never touch shared
@@ -28,14 +28,12 @@ struct DqSmem : Chan<KS> {
     using Chan<KS>::kTile;
     static constexpr int kKs = 3, kVs = 2;                         // ring slots of K and V
     static constexpr int kBars = (2 + kKs + kVs) * kTile;          // Q, dO, rings
-    static constexpr int kBytes = kBars + 160 + 1024;              // alignment slack
+    static constexpr int kBytes = kBars + 168;
 };
 
+// Block `block` of `blocks`; so too in dkv_block.
 template <int KS>
-__global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dq(const __grid_constant__ AttnArgs a,
-                                                            const __grid_constant__ AttnMaps maps) {
-    extern __shared__ uint8_t raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+__device__ __forceinline__ void dq_block(const AttnArgs &a, const AttnMaps &maps, uint8_t *smem, int block, int blocks) {
     using L = DqSmem<KS>;
     constexpr int NB = L::NB;
     uint8_t *sq = smem, *sg = smem + L::kTile, *sk = smem + 2 * L::kTile, *sv = sk + L::kKs * L::kTile;
@@ -46,8 +44,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dq(const __grid_constan
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
-    const int h = blockIdx.x % a.Hq, hk = h / a.group;
-    const int slot = gridDim.x / a.Hq - 1 - blockIdx.x / a.Hq;   // under a causal mask the last tiles have the most keys
+    const int h = block % a.Hq, hk = h / a.group;
+    const int slot = blocks / a.Hq - 1 - block / a.Hq;   // under a causal mask the last tiles have the most keys
     const TileInfo t = tile_info<kTcTile>(a.sq, a.sk, slot);
     const int rows = min(kTcTile, t.len - t.t0);
     if (t.t0 < 0 || rows <= 0) return;
@@ -222,13 +220,7 @@ struct DkvSmem : Chan<KS> {
 };
 
 template <int KS>
-__global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_constant__ AttnArgs a,
-                                                             const __grid_constant__ AttnMaps maps) {
-    extern __shared__ __align__(1024) uint8_t smem[];
-    if (smem_u32(smem) & 1023) {   // swizzled tiles need it; a launch has no other way to say so
-        if (threadIdx.x == 0) atomicOr(a.status, kDevTimeout);
-        return;
-    }
+__device__ __forceinline__ void dkv_block(const AttnArgs &a, const AttnMaps &maps, uint8_t *smem, int block) {
     using L = DkvSmem<KS>;
     constexpr int NB = L::NB;
     uint8_t *sk = smem, *sv = smem + L::kTile, *sq = smem + 2 * L::kTile, *sg = sq + L::kQs * L::kTile;
@@ -241,7 +233,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_consta
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
-    const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk;   // under a causal mask the first tiles have the most queries
+    const int hk = block % a.Hk, slot = block / a.Hk;   // under a causal mask the first tiles have the most queries
     const TileInfo t = tile_info<kTcTile>(a.sk, a.sq, slot);      // own side: keys
     const int keys = min(kTcTile, t.len - t.t0);
     if (t.t0 < 0 || keys <= 0) return;
@@ -439,6 +431,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_dkv(const __grid_consta
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// Both in one launch, the longer dK/dV blocks first: they share nothing but
+// their inputs, so the dQ blocks fill the SMs that the others leave idle.
+template <int KS>
+__global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_constant__ AttnArgs a,
+                                                             const __grid_constant__ AttnMaps maps, int dkv_blocks) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023) {   // swizzled tiles need it; a launch has no other way to say so
+        if (threadIdx.x == 0) atomicOr(a.status, kDevTimeout);
+        return;
+    }
+    const int block = blockIdx.x;
+    if (block < dkv_blocks) dkv_block<KS>(a, maps, smem, block);
+    else dq_block<KS>(a, maps, smem, block - dkv_blocks, gridDim.x - dkv_blocks);
 }
 
 }  // namespace lce

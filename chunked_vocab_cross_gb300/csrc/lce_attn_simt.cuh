@@ -1,7 +1,9 @@
-// Attention of fp32 tensors, in fp32 arithmetic: tiles of 64 queries by 64 keys in shared
-// memory, 256 threads in a 16 x 16 grid, each with four query rows (or key
-// rows) and every 16th column of each product. Bound by shared-memory loads
-// (eight for sixteen multiply-adds).
+// Attention of fp32 tensors, in fp32 arithmetic: tiles of 64 queries by 64 keys
+// in shared memory, 256 threads in a 16 x 16 grid, each with four query rows
+// (or key rows) and every 16th row of the other side, or DP/16 channels. Rows
+// are four floats longer than their data, so that both the reads along a row
+// (16 bytes at a time, 16 rows apart by lane) and those across it are free of
+// bank conflicts; 16-byte reads bring eight loads for 64 multiply-adds.
 #pragma once
 
 #include "lce_attn.cuh"
@@ -10,63 +12,107 @@ namespace lce {
 
 constexpr int kSimtTile = 64;
 constexpr int kSimtThreads = 256;
-constexpr int kSimtP = kSimtTile + 1;   // row pitch of a 64 x 64 tile: odd, so that columns are free of bank conflicts
+constexpr int kSimtP = kSimtTile + 4;   // row pitch of a 64 x 64 tile
 
 constexpr int simt_smem(int DP, int operands, int tiles) {
-    return (operands * kSimtTile * (DP + 1) + tiles * kSimtTile * kSimtP + 2 * kSimtTile) * 4;
+    return (operands * kSimtTile * (DP + 4) + tiles * kSimtTile * kSimtP + 2 * kSimtTile) * 4;
 }
 
-// rows [0, 64) x [0, DP) of fp32 from `rows` token rows of D elements; zero outside
+// rows [0, 64) x [0, DP) from `rows` token rows of D floats; zero outside
 template <int DP>
 __device__ __forceinline__ void simt_load(float *dst, const float *src, int64_t stride, int rows, int D) {
-    for (int i = threadIdx.x; i < kSimtTile * DP; i += kSimtThreads) {
-        const int r = i / DP, c = i % DP;
-        dst[r * (DP + 1) + c] = (r < rows && c < D) ? src[r * stride + c] : 0.f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kSimtTile * DP / 4; i += kSimtThreads) {
+        const int r = i / (DP / 4), c = i % (DP / 4) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows && c < D) v = *reinterpret_cast<const float4 *>(src + r * stride + c);
+        *reinterpret_cast<float4 *>(dst + r * (DP + 4) + c) = v;
     }
 }
 
 // acc[i][j] = A[ty*4+i] . B[tx+16j] over DP
 template <int DP>
 __device__ __forceinline__ void simt_dot(const float *A, const float *B, int ty, int tx, float (&acc)[4][4]) {
+#pragma unroll
     for (int i = 0; i < 4; ++i)
+#pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    for (int c = 0; c < DP; ++c) {
-        float x[4], y[4];
-        for (int i = 0; i < 4; ++i) x[i] = A[(ty * 4 + i) * (DP + 1) + c];
-        for (int j = 0; j < 4; ++j) y[j] = B[(tx + 16 * j) * (DP + 1) + c];
+#pragma unroll 4
+    for (int c = 0; c < DP; c += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(A + (ty * 4 + i) * (DP + 4) + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * (DP + 4) + c);
+#pragma unroll
         for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
     }
 }
 
-// acc[i][c] += sum_j P[ty*4+i][j] * B[j][tx+16c]   (kT: P is read as P[j][ty*4+i])
+// A thread's channels: DP/16 of them, in runs of at most four; run k starts at simt_col(tx, k).
+template <int DP>
+struct SimtCols {
+    static constexpr int kN = DP / 16, kRun = kN < 4 ? kN : 4, kRuns = kN / kRun;
+    static __device__ __forceinline__ int at(int tx, int run) { return run * 16 * kRun + tx * kRun; }
+};
+
+// acc[i][c] += sum_j P[ty*4+i][j] * B[j][column c]   (kT: P is read as P[j][ty*4+i])
 template <int DP, bool kT>
 __device__ __forceinline__ void simt_mix(const float *P, const float *B, int ty, int tx, float (&acc)[4][DP / 16]) {
-    for (int j = 0; j < kSimtTile; ++j) {
-        float x[4];
-        for (int i = 0; i < 4; ++i) x[i] = kT ? P[j * kSimtP + ty * 4 + i] : P[(ty * 4 + i) * kSimtP + j];
-        for (int c = 0; c < DP / 16; ++c) {
-            const float y = B[j * (DP + 1) + tx + 16 * c];
-            for (int i = 0; i < 4; ++i) acc[i][c] = fmaf(x[i], y, acc[i][c]);
+    using C = SimtCols<DP>;
+#pragma unroll 2
+    for (int j = 0; j < kSimtTile; j += 4) {
+        float x[4][4];   // [row][j]
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 v = *reinterpret_cast<const float4 *>(kT ? P + (j + i) * kSimtP + ty * 4 : P + (ty * 4 + i) * kSimtP + j);
+            if (kT) x[0][i] = v.x, x[1][i] = v.y, x[2][i] = v.z, x[3][i] = v.w;
+            else x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int r = 0; r < C::kRuns; ++r) {
+                float y[C::kRun];
+                const float *b = B + (j + k) * (DP + 4) + C::at(tx, r);
+                if (C::kRun == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(b);
+                    y[0] = v.x, y[1] = v.y, y[C::kRun / 2] = v.z, y[C::kRun - 1] = v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2 *>(b);
+                    y[0] = v.x, y[1] = v.y;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < C::kRun; ++c) acc[i][r * C::kRun + c] = fmaf(x[i][k], y[c], acc[i][r * C::kRun + c]);
+            }
     }
 }
 
 template <int DP>
 __device__ __forceinline__ void simt_store(float *dst, int64_t stride, int rows, int D, int ty, int tx, float mul,
                                            const float (&acc)[4][DP / 16]) {
+    using C = SimtCols<DP>;
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = ty * 4 + i;
         if (r >= rows) continue;
-        for (int c = 0; c < DP / 16; ++c)
-            if (tx + 16 * c < D) dst[r * stride + tx + 16 * c] = acc[i][c] * mul;
+#pragma unroll
+        for (int c = 0; c < C::kN; ++c) {
+            const int col = C::at(tx, c / C::kRun) + c % C::kRun;
+            if (col < D) dst[r * stride + col] = acc[i][c] * mul;
+        }
     }
 }
 
 template <int DP>
 __global__ void __launch_bounds__(kSimtThreads) k_attn_fwd_simt(const AttnArgs a) {
-    extern __shared__ float sm[];
-    float *Q = sm, *K = Q + kSimtTile * (DP + 1), *V = K + kSimtTile * (DP + 1), *P = V + kSimtTile * (DP + 1);
+    extern __shared__ __align__(16) float sm[];
+    float *Q = sm, *K = Q + kSimtTile * (DP + 4), *V = K + kSimtTile * (DP + 4), *P = V + kSimtTile * (DP + 4);
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
     const int h = blockIdx.x % a.Hq, hk = h / a.group;
     if (blockIdx.x == 0 && tid < 32) {
@@ -148,12 +194,11 @@ __device__ __forceinline__ void simt_probs(const AttnArgs &a, const float *Q, co
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kSimtThreads) k_attn_dq_simt(const AttnArgs a) {
-    extern __shared__ float sm[];
-    constexpr int kOp = kSimtTile * (DP + 1);
+__device__ __forceinline__ void dq_block_simt(const AttnArgs &a, float *sm, int block, int blocks) {
+    constexpr int kOp = kSimtTile * (DP + 4);
     float *Q = sm, *G = Q + kOp, *K = G + kOp, *V = K + kOp, *dS = V + kOp, *stat = dS + kSimtTile * kSimtP;
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-    const int h = blockIdx.x % a.Hq, hk = h / a.group, slot = blockIdx.x / a.Hq;
+    const int h = block % a.Hq, hk = h / a.group, slot = blocks / a.Hq - 1 - block / a.Hq;
     const TileInfo t = tile_info<kSimtTile>(a.sq, a.sk, slot);
     const int rows = min(kSimtTile, t.len - t.t0);
     if (t.t0 < 0 || rows <= 0) return;
@@ -182,12 +227,11 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_dq_simt(const AttnArgs a)
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kSimtThreads) k_attn_dkv_simt(const AttnArgs a) {
-    extern __shared__ float sm[];
-    constexpr int kOp = kSimtTile * (DP + 1), kTl = kSimtTile * kSimtP;
+__device__ __forceinline__ void dkv_block_simt(const AttnArgs &a, float *sm, int block) {
+    constexpr int kOp = kSimtTile * (DP + 4), kTl = kSimtTile * kSimtP;
     float *Q = sm, *G = Q + kOp, *K = G + kOp, *V = K + kOp, *P = V + kOp, *dS = P + kTl, *stat = dS + kTl;
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-    const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk;
+    const int hk = block % a.Hk, slot = block / a.Hk;
     const TileInfo t = tile_info<kSimtTile>(a.sk, a.sq, slot);   // own side: keys
     const int keys = min(kSimtTile, t.len - t.t0);
     if (t.t0 < 0 || keys <= 0) return;
@@ -220,6 +264,15 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_dkv_simt(const AttnArgs a
     }
     simt_store<DP>(static_cast<float *>(a.dk) + tok * a.dk_ts + hk * a.dk_hs, a.dk_ts, keys, a.D, ty, tx, a.scale, dk);
     simt_store<DP>(static_cast<float *>(a.dv) + tok * a.dv_ts + hk * a.dv_hs, a.dv_ts, keys, a.D, ty, tx, 1.f, dv);
+}
+
+// Both kinds of blocks in one launch, the longer dK/dV blocks first.
+template <int DP>
+__global__ void __launch_bounds__(kSimtThreads) k_attn_bwd_simt(const AttnArgs a, int dkv_blocks) {
+    extern __shared__ __align__(16) float sm[];
+    const int block = blockIdx.x;
+    if (block < dkv_blocks) dkv_block_simt<DP>(a, sm, block);
+    else dq_block_simt<DP>(a, sm, block - dkv_blocks, gridDim.x - dkv_blocks);
 }
 
 }  // namespace lce
