@@ -193,12 +193,10 @@ __device__ __forceinline__ void dq_block(const AttnArgs &a, const AttnMaps &maps
             __syncwarp();
             if (lane == 0) mbar_arrive(ds_full);
         }
-        if (ok && warp < 4) {
-            if ((ok = wait.all(fin, 0))) {
-                tc_fence_after();
-                tc_store_rows<NB>(sq, tQ + lane_base, a.scale, warp * 32, rows, dq, a.dq_ts, a.D);
-                tc_fence_before();
-            }
+        if (ok && wait.all(fin, 0)) {
+            tc_fence_after();
+            tc_store_half<KS>(half, sq, tQ + lane_base, a.scale, (warp & 3) * 32, rows, dq, a.dq_ts, a.D);
+            tc_fence_before();
         }
     }
     __syncthreads();
@@ -421,8 +419,8 @@ __device__ __forceinline__ void dkv_block(const AttnArgs &a, const AttnMaps &map
         }
         if (ok && wait.all(fin, 0)) {
             tc_fence_after();
-            if (half == 0) tc_store_rows<NB>(sv, tV + lane_base, 1.f, (warp & 3) * 32, keys, dv, a.dv_ts, a.D);
-            else tc_store_rows<NB>(sk, tK + lane_base, a.scale, (warp & 3) * 32, keys, dk, a.dk_ts, a.D);
+            tc_store_half<KS>(half, sv, tV + lane_base, 1.f, (warp & 3) * 32, keys, dv, a.dv_ts, a.D);
+            tc_store_half<KS>(half, sk, tK + lane_base, a.scale, (warp & 3) * 32, keys, dk, a.dk_ts, a.D);
             tc_fence_before();
         }
     }

@@ -9,6 +9,7 @@
 // any D runs as if rounded up to 16.
 #pragma once
 
+#include "f32x2.cuh"
 #include "lce_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -140,15 +141,21 @@ __device__ __forceinline__ int tc_piece(int r, int c) {
     return (c >> 3) * kTcBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-// Writes a warp's 32 rows of an accumulator to global memory as bf16: lane r
-// holds row r0 + r of the tile; the rows go through the warp's share of a free
-// tile, so that 16 (8 for 64 channels) lanes write one token's row.
-template <int NB>
+// The 32-channel chunks of an accumulator that a half of its threads takes.
+template <int KS>
+struct Chunks {
+    static constexpr int kAll = (KS + 1) / 2, kFirst = (kAll + 1) / 2;   // of both halves, of the first
+};
+
+// Writes chunks [C0, C0 + N) of a warp's 32 rows of an accumulator to global
+// memory as bf16: lane r holds row r0 + r of the tile; the rows go through the
+// warp's share of a free tile, so that neighbouring lanes write one token's row.
+template <int C0, int N>
 __device__ __forceinline__ void tc_store_rows(uint8_t *tile, uint32_t taddr, float mul, int r0, int rows,
                                               __nv_bfloat16 *dst, int64_t stride, int D) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int c = 0; c < NB * 2; ++c) {
+    for (int c = C0; c < C0 + N; ++c) {
         uint32_t v[32];
         tmem_ld32(taddr + c * 32, v);
         tmem_ld_wait();
@@ -163,13 +170,22 @@ __device__ __forceinline__ void tc_store_rows(uint8_t *tile, uint32_t taddr, flo
         }
     }
     __syncwarp();
-    constexpr int kPer = NB * 8;   // pieces of a row
+    constexpr int kPer = N * 4;   // pieces of a row
 #pragma unroll 4
     for (int i = lane; i < 32 * kPer; i += 32) {
-        const int r = r0 + i / kPer, c = i % kPer;
+        const int r = r0 + i / kPer, c = C0 * 4 + i % kPer;
         if (r < rows && c * 8 < D)
             *reinterpret_cast<uint4 *>(dst + r * stride + c * 8) = *reinterpret_cast<const uint4 *>(tile + tc_piece(r, c));
     }
+}
+
+// The same for the chunks of one half of the threads.
+template <int KS>
+__device__ __forceinline__ void tc_store_half(int half, uint8_t *tile, uint32_t taddr, float mul, int r0, int rows,
+                                              __nv_bfloat16 *dst, int64_t stride, int D) {
+    using C = Chunks<KS>;
+    if (half == 0) tc_store_rows<0, C::kFirst>(tile, taddr, mul, r0, rows, dst, stride, D);
+    else tc_store_rows<C::kFirst, C::kAll - C::kFirst>(tile, taddr, mul, r0, rows, dst, stride, D);
 }
 
 struct AttnMaps {

@@ -344,22 +344,23 @@ struct Pack16<__nv_bfloat16> {
 
 struct RingBars {
     uint64_t full[kRingMaxStages], empty[kRingMaxStages];
-    volatile int abort_flag;
+    volatile int gave_up[16];   // by row group
 };
 
-__device__ __forceinline__ bool ring_wait(RingBars &b, uint64_t *bar, uint32_t parity, int *status) {
+// A bounded wait. A row group whose wait gave up goes on to its next barrier
+// all the same (its warps must not leave one another waiting there) and leaves
+// the loop after it, on `gave_up`.
+__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, int *status) {
     const uint32_t at = smem_u32(bar);
     if (mbar_try_wait(at, parity)) return true;
     const long long t0 = clock64();
-    for (;;) {
-        if (mbar_try_wait(at, parity)) return true;
-        if (b.abort_flag) return false;
+    while (!mbar_try_wait(at, parity)) {
         if (clock64() - t0 > kNormWaitCycles) {
-            b.abort_flag = 1;
             atomicOr(status, LCE_DEV_TIMEOUT);
             return false;
         }
     }
+    return true;
 }
 
 // The arrays of a ring, copied by thread 0 of the block.
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
     const int nwarps = blockDim.x / 32;
     if (threadIdx.x == 0) {
         for (int i = 0; i < g.stages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], nwarps);
-        bars.abort_flag = 0;
+        for (int i = 0; i < 16; ++i) bars.gave_up[i] = 0;
         fence_mbar_init();
     }
     const int d = a.d;
@@ -498,10 +499,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
     uint32_t phase = 0;
     for (; r0 < a.N; r0 += step, out_r += step * g.row_bytes, out_n += step * g.row_bytes) {
         const int64_t row = r0 + group;
-        if (!__all_sync(0xffffffffu, ring_wait(bars, &bars.full[s], phase, a.status))) {
-            if (threadIdx.x == 0) ring_drain(bars, g, g.groups, s, phase, r0, a.N);
-            break;
-        }
+        // the vote also tells the compiler that the warp is together again
+        if (!__all_sync(0xffffffffu, ring_wait(&bars.full[s], phase, a.status))) bars.gave_up[group] = 1;
         const bool live = row < a.N;
         const uint8_t *at = smem + s * g.stage_bytes + group * g.row_bytes;
         f32x2 r[CH][P];
@@ -564,8 +563,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
             sum[0] = hsum2(q);
             group_sum(sum, my_red, flip, g.tpr, group, t);
         }
+        if (bars.gave_up[group]) {
+            if (threadIdx.x == 0) ring_drain(bars, g, g.groups, s, phase, r0, a.N);
+            break;
+        }
         // the stage's next rows, once every warp has taken its share
-        if (threadIdx.x == 0 && r0 + g.stages * step < a.N && ring_wait(bars, &bars.empty[s], phase, a.status))
+        if (threadIdx.x == 0 && r0 + g.stages * step < a.N && ring_wait(&bars.empty[s], phase, a.status))
             src.issue(smem, bars, g, g.groups, s, r0 + g.stages * step, a.N, d);
         if (has_pre) {
             const float rs = rsqrtf(sum[0] * inv_d + a.eps);
@@ -605,7 +608,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
     const int nwarps = blockDim.x / 32;
     if (threadIdx.x == 0) {
         for (int i = 0; i < g.stages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], nwarps);
-        bars.abort_flag = 0;
+        for (int i = 0; i < 16; ++i) bars.gave_up[i] = 0;
         fence_mbar_init();
     }
     const int d = a.d;
@@ -655,10 +658,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
 #pragma unroll
         for (int k = 0; k < R; ++k) rp[k] = rp_next[k], ro[k] = ro_next[k];
         rstd(row + step);
-        if (!__all_sync(0xffffffffu, ring_wait(bars, &bars.full[s], phase, a.status))) {
-            if (threadIdx.x == 0) ring_drain(bars, g, per, s, phase, r0, a.N);
-            break;
-        }
+        // the vote also tells the compiler that the warp is together again
+        if (!__all_sync(0xffffffffu, ring_wait(&bars.full[s], phase, a.status))) bars.gave_up[group] = 1;
         const uint8_t *at = smem + s * g.stage_bytes + group * R * g.row_bytes;
         f32x2 hat[R][CH][P], x[R][CH][P];
         uint4 vb[R][CH];
@@ -727,6 +728,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
 #pragma unroll
             for (int i = 0; i < 3; ++i) sum[3 * k + i] = hsum2(q[k][i]);
         group_sum(sum, my_red, flip, g.tpr, group, t);
+        if (bars.gave_up[group]) {
+            if (threadIdx.x == 0) ring_drain(bars, g, per, s, phase, r0, a.N);
+            break;
+        }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int byte = (c * g.tpr + t) * 16;
@@ -771,7 +776,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
         __syncwarp();
         if ((t & 31) == 0) mbar_arrive(&bars.empty[s]);
         // the stage's next rows, once every warp is through with it
-        if (threadIdx.x == 0 && r0 + g.stages * step < a.N && ring_wait(bars, &bars.empty[s], phase, a.status))
+        if (threadIdx.x == 0 && r0 + g.stages * step < a.N && ring_wait(&bars.empty[s], phase, a.status))
             src.issue(smem, bars, g, per, s, r0 + g.stages * step, a.N, d);
         if (++s == g.stages) s = 0, phase ^= 1;
     }
