@@ -23,7 +23,6 @@ struct SeqMap {
     __device__ __forceinline__ int raw(int b) const { return cu ? cu[b] : b * len; }
     // first token of sequence b (b <= B), within [0, T] whatever the offsets hold
     __device__ __forceinline__ int start(int b) const { return min(max(raw(b), 0), T); }
-    __device__ __forceinline__ int end(int b) const { return b >= B ? T : max(min(max(raw(b + 1), 0), T), start(b)); }
 };
 
 // Tile t of sequence b has the slot start(b)/TILE + b + t. Slots of different
@@ -53,26 +52,6 @@ struct AttnArgs {
     int *status;
 };
 
-// The sequence whose tiles may include `slot`: the largest b in [0, B] with
-// slot_base(b) <= slot. All 32 lanes take part, each probing one of 32 points
-// of what is left, so 1024 sequences take two rounds of loads.
-template <int TILE>
-__device__ __forceinline__ int find_seq(const SeqMap &m, int slot) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, n = m.B + 1;
-    while (n > 1) {
-        const int step = (n + 31) / 32;
-        const int off = lane * step;
-        const bool le = off < n && slot_base<TILE>(m, lo + off) <= slot;
-        const unsigned mask = __ballot_sync(0xffffffffu, le);
-        // offsets that do not ascend may leave holes; the highest hit is still inside [lo, lo + n)
-        const int hit = mask ? 31 - __clz(mask) : 0;
-        lo += hit * step;
-        n = min(step, n - hit * step);
-    }
-    return lo;
-}
-
 // One tile of one side: its sequence, its row range on both sides.
 struct TileInfo {
     int b;             // sequence
@@ -80,15 +59,43 @@ struct TileInfo {
     int t0;            // first row of the tile within the sequence
     int o0, olen;      // first token and length of the sequence on the other side (tail: empty)
 };
+
+// The tile of `slot`: its sequence is the largest b in [0, B] with
+// slot_base(b) <= slot. All 32 lanes take part, each probing one of 32 points
+// of what is left, so 1024 sequences take two rounds of loads; in the last
+// round the probes are neighbours and hold the sequence's start and end too.
+// Blocks begin with this, so what counts is the number of dependent loads.
 template <int TILE>
 __device__ __forceinline__ TileInfo tile_info(const SeqMap &own, const SeqMap &other, int slot) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = own.B + 1;
+    while (n > 31) {
+        const int step = (n + 31) / 32;
+        const int off = lane * step;
+        const bool le = off < n && slot_base<TILE>(own, lo + off) <= slot;
+        const unsigned mask = __ballot_sync(0xffffffffu, le);
+        // offsets that do not ascend may leave holes; the highest hit is still inside [lo, lo + n)
+        const int hit = mask ? 31 - __clz(mask) : 0;
+        lo += hit * step;
+        n = min(step, n - hit * step);
+        if (step == 1) break;
+    }
+    // sequences lo .. lo + n - 1 are left, n <= 31 (or one): lane i has the start of sequence lo + i
+    const int b = lo + lane;
+    const bool in = lane <= n && b <= own.B;
+    const int s = in ? own.start(b) : own.T, o = in ? other.start(b) : other.T;
+    const unsigned mask = __ballot_sync(0xffffffffu, lane < n && in && s / TILE + b <= slot);
+    const int hit = mask ? 31 - __clz(mask) : 0;
     TileInfo t;
-    t.b = find_seq<TILE>(own, slot);
-    t.s0 = own.start(t.b);
-    t.len = own.end(t.b) - t.s0;
+    t.b = lo + hit;
+    t.s0 = __shfl_sync(0xffffffffu, s, hit);
+    t.o0 = __shfl_sync(0xffffffffu, o, hit);
+    // the end: the next sequence's start, or (the tail) the last token
+    const int e = __shfl_sync(0xffffffffu, s, (hit + 1) & 31), oe = __shfl_sync(0xffffffffu, o, (hit + 1) & 31);
+    const bool tail = t.b >= own.B;
+    t.len = (tail ? own.T : max(e, t.s0)) - t.s0;
+    t.olen = tail ? 0 : max(oe, t.o0) - t.o0;
     t.t0 = (slot - (t.s0 / TILE + t.b)) * TILE;
-    t.o0 = other.start(t.b);
-    t.olen = t.b < own.B ? other.end(t.b) - t.o0 : 0;
     return t;
 }
 

@@ -44,6 +44,11 @@ __device__ __forceinline__ void dq_block(const AttnArgs &a, const AttnMaps &maps
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 16; ++i) mbar_init(&bars[i], i == 14 ? 8 : 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
     const int h = block % a.Hq, hk = h / a.group;
     const int slot = blocks / a.Hq - 1 - block / a.Hq;   // under a causal mask the last tiles have the most keys
     const TileInfo t = tile_info<kTcTile>(a.sq, a.sk, slot);
@@ -61,11 +66,6 @@ __device__ __forceinline__ void dq_block(const AttnArgs &a, const AttnMaps &maps
     }
     const int n = (kend + kTcTile - 1) / kTcTile;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 16; ++i) mbar_init(&bars[i], i == 14 ? 8 : 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
     if (warp == 9) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -231,6 +231,11 @@ __device__ __forceinline__ void dkv_block(const AttnArgs &a, const AttnMaps &map
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 18; ++i) mbar_init(&bars[i], i == 13 || i == 14 ? 8 : 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
     const int hk = block % a.Hk, slot = block / a.Hk;   // under a causal mask the first tiles have the most queries
     const TileInfo t = tile_info<kTcTile>(a.sk, a.sq, slot);      // own side: keys
     const int keys = min(kTcTile, t.len - t.t0);
@@ -251,11 +256,6 @@ __device__ __forceinline__ void dkv_block(const AttnArgs &a, const AttnMaps &map
     }
     const int n = per_head * a.group;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 18; ++i) mbar_init(&bars[i], i == 13 || i == 14 ? 8 : 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
     if (warp == 9) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -442,6 +442,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
         return;
     }
     const int block = blockIdx.x;
+    if (threadIdx.x == 32) {
+        tma_prefetch_map(&maps.q);
+        tma_prefetch_map(&maps.k);
+        tma_prefetch_map(&maps.v);
+        tma_prefetch_map(&maps.dO);
+    }
     if (block < dkv_blocks) dkv_block<KS>(a, maps, smem, block);
     else dq_block<KS>(a, maps, smem, block - dkv_blocks, gridDim.x - dkv_blocks);
 }

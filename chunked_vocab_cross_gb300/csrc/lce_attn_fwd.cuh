@@ -43,6 +43,22 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(s_full, 1);
+        mbar_init(p_full, 8);
+        mbar_init(o_done, 1);
+        mbar_init(fin, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&maps.q);
+        tma_prefetch_map(&maps.k);
+        tma_prefetch_map(&maps.v);
+    }
     const int h = blockIdx.x % a.Hq, hk = h / a.group;
     // longest rows first: under a causal mask the last tiles have the most keys
     const int slot = gridDim.x / a.Hq - 1 - blockIdx.x / a.Hq;
@@ -67,19 +83,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
     }
     const int n = (kend + kTcTile - 1) / kTcTile;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
-        }
-        mbar_init(q_full, 1);
-        mbar_init(s_full, 1);
-        mbar_init(p_full, 8);
-        mbar_init(o_done, 1);
-        mbar_init(fin, 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
     if (warp == 9) {
         tmem_alloc(tmem_slot, 256);
         tmem_relinquish();
