@@ -195,7 +195,7 @@ __device__ __forceinline__ void dq_block(const AttnArgs &a, const AttnMaps &maps
         }
         if (ok && wait.all(fin, 0)) {
             tc_fence_after();
-            tc_store_half<KS>(half, tQ + lane_base, a.scale, row < rows, dq + row * a.dq_ts, a.D, [] {});
+            tc_store_half<KS>(half, sq, tQ + lane_base, a.scale, (warp & 3) * 32, rows, dq, a.dq_ts, a.D, [] {});
             tc_fence_before();
         }
     }
@@ -419,9 +419,8 @@ __device__ __forceinline__ void dkv_block(const AttnArgs &a, const AttnMaps &map
         }
         if (ok && wait.all(fin, 0)) {
             tc_fence_after();
-            const int row = key - t.t0;
-            tc_store_half<KS>(half, tV + lane_base, 1.f, row < keys, dv + row * a.dv_ts, a.D, [] {});
-            tc_store_half<KS>(half, tK + lane_base, a.scale, row < keys, dk + row * a.dk_ts, a.D, [] {});
+            tc_store_half<KS>(half, sv, tV + lane_base, 1.f, (warp & 3) * 32, keys, dv, a.dv_ts, a.D, [] {});
+            tc_store_half<KS>(half, sk, tK + lane_base, a.scale, (warp & 3) * 32, keys, dk, a.dk_ts, a.D, [] {});
             tc_fence_before();
         }
     }

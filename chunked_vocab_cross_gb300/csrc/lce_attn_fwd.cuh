@@ -47,7 +47,8 @@ struct FwdWork {
 };
 
 struct FwdBars {
-    uint64_t k_full, k_empty, v_full, v_empty;   // loads of K and V tiles
+    uint64_t k_full, k_empty, v_full, v_empty;   // loads of K and V tiles (v_empty: of all but a work tile's last)
+    uint64_t staged;                             // O has gone out through V's slot
     uint64_t q_full, q_empty;                    // loads of Q
     uint64_t s_full, p_full, o_done, o_free;     // S and P, an O step done, O read
     uint64_t work_full[2], work_empty[2];
@@ -76,6 +77,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
         for (uint64_t *b : one) mbar_init(b, 1);
         mbar_init(&bar.p_full, 8);
         mbar_init(&bar.o_free, 8);
+        mbar_init(&bar.staged, 8);
         for (int i = 0; i < 2; ++i) mbar_init(&bar.work_empty[i], 9);
         bar.abort_flag = 0;
         fence_mbar_init();
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
             return w;
         };
         bool ok = true;
-        int tiles = 0, qs = 0, kv = 0;   // tiles handed over, Q loads and K/V pairs of loads so far
+        int tiles = 0, qs = 0, kv = 0, ve = 0;   // tiles handed over, Q loads, K/V pairs of loads, waits on v_empty so far
         auto publish = [&](const FwdWork &w) {
             if (!(ok = wait.all(&bar.work_empty[tiles & 1], ((tiles >> 1) & 1) ^ 1))) return;
             if (lane == 0) {
@@ -157,7 +159,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
                         tc_load_tile<NB>(sk, &maps.k, &bar.k_full, hk, at);
                     }
                     ++kl;
-                    if (!(ok = wait.all(&bar.v_empty, (kv & 1) ^ 1))) break;
+                    // a tile's first V waits for the output before it, the others for the MMAs that read V
+                    if (j == 0 ? qs > 1 && !(ok = wait.all(&bar.staged, qs & 1)) : !(ok = wait.all(&bar.v_empty, ve++ & 1))) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&bar.v_full, L::kTile);
                         tc_load_tile<NB>(sv, &maps.v, &bar.v_full, hk, at);
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
                 if (elect_one()) {
                     tc_fence_after();
                     tc_mma_tokens<true>(tO, tS, dv, idO, j > 0);
-                    umma_commit(&bar.v_empty);
+                    if (j + 1 < n) umma_commit(&bar.v_empty);
                     umma_commit(&bar.o_done);
                 }
                 __syncwarp();
@@ -259,12 +262,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.work_empty[tiles & 1]);
             if (w.h < 0) break;
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (static_cast<int64_t>(w.tok) + row) * a.o_ts + w.h * a.o_hs;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + static_cast<int64_t>(w.tok) * a.o_ts + w.h * a.o_hs;
             float *lse = a.lse + static_cast<int64_t>(w.h) * a.sq.T + w.tok + row;
             const bool live = row < w.rows;
             if (w.n == 0) {   // no row of the tile sees a key (or there are no rows)
                 if (live) {
-                    for (int c = half * 8; c < a.D; c += 16) *reinterpret_cast<uint4 *>(o + c) = make_uint4(0, 0, 0, 0);
+                    for (int c = half * 8; c < a.D; c += 16) *reinterpret_cast<uint4 *>(o + row * a.o_ts + c) = make_uint4(0, 0, 0, 0);
                     if (half == 0) *lse = -INFINITY;
                 }
                 continue;
@@ -348,11 +351,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
             const float part = hsum2(l2), l = part + exchange(part);
             const float inv = l != 0.f ? 1.f / l : 0.f;   // l of an empty row is 0; NaN stays
             if (half == 0 && live) *lse = l == 0.f ? -INFINITY : (m * sc + log2f(l)) * (1.f / kAttnLog2e);
-            tc_store_half<KS>(half, tO + lane_base, inv, live, o, a.D, [&] {
+            tc_store_half<KS>(half, sv, tO + lane_base, inv, quarter * 32, w.rows, o, a.o_ts, a.D, [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.o_free);
             });
+            fence_proxy_async_smem();   // V's slot goes back to the loads
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.staged);
         }
         tc_fence_before();
     }

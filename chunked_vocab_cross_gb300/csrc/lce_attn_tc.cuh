@@ -142,21 +142,27 @@ struct Chunks {
     static constexpr int kAll = (KS + 1) / 2, kFirst = (kAll + 1) / 2;   // of both halves, of the first
 };
 
-// Writes this half's chunks of one row of an accumulator per lane to global
-// memory as bf16. A lane stores 64 bytes of its own row at a time; the pieces
-// meet in L2. `release` is called once the accumulator has been read.
-template <int KS, typename F>
-__device__ __forceinline__ void tc_store_half(int half, uint32_t taddr, float mul, bool live, __nv_bfloat16 *dst, int D,
-                                              F release) {
-    using C = Chunks<KS>;
-    const int c0 = half ? C::kFirst : 0, c1 = half ? C::kAll : C::kFirst;
+// 16-byte piece c of row r in a swizzled tile (byte offset).
+__device__ __forceinline__ int tc_piece(int r, int c) {
+    return (c >> 3) * kTcBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// Writes chunks [C0, C0 + N) of a warp's 32 rows of an accumulator to global
+// memory as bf16: lane r holds row r0 + r of the tile. The rows go through the
+// warp's share of a free tile, so that a store covers whole lines of a few
+// rows (stored by each lane on its own, 32 rows at a time, they took 4700
+// cycles a tile instead of 700). `release` is called once the accumulator has
+// been read.
+template <int C0, int N, typename F>
+__device__ __forceinline__ void tc_store_rows(uint8_t *tile, uint32_t taddr, float mul, int r0, int rows,
+                                              __nv_bfloat16 *dst, int64_t stride, int D, F release) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int c = 0; c < C::kFirst; ++c) {
-        if (c0 + c >= c1) break;
+    for (int c = C0; c < C0 + N; ++c) {
         uint32_t v[32];
-        tmem_ld32(taddr + (c0 + c) * 32, v);
+        tmem_ld32(taddr + c * 32, v);
         tmem_ld_wait();
-        if (c0 + c + 1 == c1) release();
+        if (c + 1 == C0 + N) release();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint4 w;
@@ -164,10 +170,26 @@ __device__ __forceinline__ void tc_store_half(int half, uint32_t taddr, float mu
             w.y = pack_bf16(__uint_as_float(v[8 * i + 2]) * mul, __uint_as_float(v[8 * i + 3]) * mul);
             w.z = pack_bf16(__uint_as_float(v[8 * i + 4]) * mul, __uint_as_float(v[8 * i + 5]) * mul);
             w.w = pack_bf16(__uint_as_float(v[8 * i + 6]) * mul, __uint_as_float(v[8 * i + 7]) * mul);
-            const int col = (c0 + c) * 32 + i * 8;
-            if (live && col < D) *reinterpret_cast<uint4 *>(dst + col) = w;
+            *reinterpret_cast<uint4 *>(tile + tc_piece(r0 + lane, c * 4 + i)) = w;
         }
     }
+    __syncwarp();
+    constexpr int kPer = N * 4;   // pieces of a row
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int i = k * 32 + lane, r = r0 + i / kPer, c = C0 * 4 + i % kPer;
+        if (r < rows && c * 8 < D)
+            *reinterpret_cast<uint4 *>(dst + r * stride + c * 8) = *reinterpret_cast<const uint4 *>(tile + tc_piece(r, c));
+    }
+}
+
+// The same for the chunks of one half of the threads.
+template <int KS, typename F>
+__device__ __forceinline__ void tc_store_half(int half, uint8_t *tile, uint32_t taddr, float mul, int r0, int rows,
+                                              __nv_bfloat16 *dst, int64_t stride, int D, F release) {
+    using C = Chunks<KS>;
+    if (half == 0) tc_store_rows<0, C::kFirst>(tile, taddr, mul, r0, rows, dst, stride, D, release);
+    else tc_store_rows<C::kFirst, C::kAll - C::kFirst>(tile, taddr, mul, r0, rows, dst, stride, D, release);
 }
 
 struct AttnMaps {
