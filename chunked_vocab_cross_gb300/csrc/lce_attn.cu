@@ -145,8 +145,7 @@ lce_status_t backward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &
     if (s == LCE_OK) s = encode(&maps.dO, dev, a->dO, a->Tq, a->Hq, a->D, a->dO_ts, a->dO_hs);
     if (s == LCE_OK) s = row_stats<__nv_bfloat16, kTcTile>(r, dev, st);
     if (s != LCE_OK) return s;
-    constexpr int smem = DqSmem<KS>::kBytes > DkvSmem<KS>::kBytes ? DqSmem<KS>::kBytes : DkvSmem<KS>::kBytes;
-    return launch<k_attn_bwd<KS>>(dev, dq + dkv, kBwdThreads, smem, st, r, maps, static_cast<int>(dkv));
+    return launch<k_attn_bwd<KS>>(dev, dq + dkv, kBwdThreads, BwdSmem<KS>::kBytes, st, r, maps, static_cast<int>(dkv));
 }
 
 // The tensor-core kernels exist for 64, 80, 96 and 128 channels; others run as the next of these.

@@ -1,21 +1,28 @@
-// Attention backward on the tensor cores (bf16): two kinds of blocks, so that
+// Attention backward on the tensor cores (bf16): two kinds of work, so that
 // every gradient is summed in TMEM by one CTA in a fixed order, without atomics
 // and without a gradient buffer of partial sums. The probabilities are
 // recomputed in both (7 products of tiles instead of 5).
 //
-// dq_block: 128 query rows, walking the keys.
+// dQ: 128 query rows, walking the keys.
 //   S = Q K^T, dP = dO V^T (128 x 128 fp32 in TMEM, rows = queries)
 //   dS = 2^(S - lse) (dP - delta), bf16 over S in TMEM;  dQ += dS K
-// dkv_block: 128 keys of one key head, walking the queries of its query heads.
+// dK/dV: 128 keys of one key head, walking the queries of its query heads.
 //   S^T = K Q^T, dP^T = V dO^T (rows = keys)
 //   P^T over S^T: dV += P^T dO;  dS^T over dP^T: dK += dS^T Q
 // P and dS go back to TMEM as the A operands, so they never touch shared
 // memory.
 //
 // 320 threads: warps 0-7 the elementwise part (two threads a row, 64 columns
-// each), warp 8 TMA loads, warp 9 MMA issue. One CTA an SM: dkv fills the 512
-// columns of TMEM (S, dP, dV, dK), and the tiles fill the shared memory.
+// each), warp 8 loads, warp 9 MMA issue. One CTA an SM: dK/dV fills the 512
+// columns of TMEM, and the tiles fill the shared memory: two that stay for a
+// piece of work (`fixed`: Q and dO, or K and V), a ring of three (`a`: K, or Q)
+// and one of two (`b`: V, or dO). A CTA takes one piece of work after another
+// by cluster launch control, as in the forward; the loads and the first
+// products of the next run under the last sums and the output of the one
+// before. Both kinds are one grid, the longer dK/dV pieces first.
 #pragma once
+
+#include <stddef.h>
 
 #include "lce_attn_tc.cuh"
 
@@ -24,415 +31,48 @@ namespace lce {
 constexpr int kBwdThreads = 320;
 
 template <int KS>
-struct DqSmem : Chan<KS> {
+struct BwdSmem : Chan<KS> {
     using Chan<KS>::kTile;
-    static constexpr int kKs = 3, kVs = 2;                         // ring slots of K and V
-    static constexpr int kBars = (2 + kKs + kVs) * kTile;          // Q, dO, rings
-    static constexpr int kBytes = kBars + 168;
-};
-
-// Block `block` of `blocks`; so too in dkv_block.
-template <int KS>
-__device__ __forceinline__ void dq_block(const AttnArgs &a, const AttnMaps &maps, uint8_t *smem, int block, int blocks) {
-    using L = DqSmem<KS>;
-    constexpr int NB = L::NB;
-    uint8_t *sq = smem, *sg = smem + L::kTile, *sk = smem + 2 * L::kTile, *sv = sk + L::kKs * L::kTile;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars);
-    uint64_t *k_full = bars, *k_empty = bars + 3, *v_full = bars + 6, *v_empty = bars + 8, *q_full = bars + 10,
-             *s_full = bars + 11 /* two */, *dp_full = bars + 13, *ds_full = bars + 14, *fin = bars + 15;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 16);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 16; ++i) mbar_init(&bars[i], i == 14 ? 8 : 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    const int h = block % a.Hq, hk = h / a.group;
-    const int slot = blocks / a.Hq - 1 - block / a.Hq;   // under a causal mask the last tiles have the most keys
-    const TileInfo t = tile_info<kTcTile>(a.sq, a.sk, slot);
-    const int rows = min(kTcTile, t.len - t.t0);
-    if (t.t0 < 0 || rows <= 0) return;
-    const int off = t.olen - t.len;
-    const int kend = a.causal ? min(t.olen, t.t0 + rows + off) : t.olen;
-    const int64_t tok = t.s0 + t.t0;
-    __nv_bfloat16 *dq = static_cast<__nv_bfloat16 *>(a.dq) + tok * a.dq_ts + h * a.dq_hs;
-    if (kend <= 0) {
-        const int per = a.D / 8;
-        for (int i = threadIdx.x; i < rows * per; i += kBwdThreads)
-            *reinterpret_cast<uint4 *>(dq + (i / per) * a.dq_ts + (i % per) * 8) = make_uint4(0, 0, 0, 0);
-        return;
-    }
-    const int n = (kend + kTcTile - 1) / kTcTile;
-
-    if (warp == 9) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    const uint32_t tS[2] = {tmem, tmem + 128}, tP = tmem + 256, tQ = tmem + 384;
-    const TcWaits wait{abort_flag, a.status};
-
-    if (warp == 8) {
-        if (lane == 0) {
-            mbar_arrive_expect_tx(q_full, 2 * L::kTile);
-            tc_load_tile<NB>(sq, &maps.q, q_full, h, static_cast<int>(tok));
-            tc_load_tile<NB>(sg, &maps.dO, q_full, h, static_cast<int>(tok));
-            int j = 0, kl = 0, vl = 0;   // loads issued of each ring
-            for (; j < n; ++j) {
-                const int ki = j % L::kKs, vi = j % L::kVs, at = t.o0 + j * kTcTile;
-                if (!wait(&k_empty[ki], ((j / L::kKs) & 1) ^ 1)) break;
-                mbar_arrive_expect_tx(&k_full[ki], L::kTile);
-                tc_load_tile<NB>(sk + ki * L::kTile, &maps.k, &k_full[ki], hk, at);
-                ++kl;
-                if (!wait(&v_empty[vi], ((j / L::kVs) & 1) ^ 1)) break;
-                mbar_arrive_expect_tx(&v_full[vi], L::kTile);
-                tc_load_tile<NB>(sv + vi * L::kTile, &maps.v, &v_full[vi], hk, at);
-                ++vl;
-            }
-            if (j < n) {
-                tc_drain(q_full, 0);
-                for (int i = max(0, kl - L::kKs); i < kl; ++i) tc_drain(&k_full[i % L::kKs], (i / L::kKs) & 1);
-                for (int i = max(0, vl - L::kVs); i < vl; ++i) tc_drain(&v_full[i % L::kVs], (i / L::kVs) & 1);
-            }
-        }
-    } else if (warp == 9) {
-        const uint32_t idS = idesc_f32acc(1, 128, 128, false, false), idQ = idesc_f32acc(1, 128, KS * 16, false, true);
-        const uint32_t idSn = idS | (a.scale < 0.f ? kIdescNegA : 0);
-        const uint64_t dQ = tc_desc_k(sq), dG = tc_desc_k(sg);
-        // S_j from K_j; its tokens past the sequence's end are zeroed for the sum that follows
-        auto scores = [&](int j) {
-            const int ki = j % L::kKs;
-            if (!wait.all(&k_full[ki], (j / L::kKs) & 1)) return false;
-            const int keys = min(kTcTile, t.olen - j * kTcTile);
-            if (keys < kTcTile) tc_zero_rows<NB>(sk + ki * L::kTile, keys);
-            if (elect_one()) {
-                tc_fence_after();
-                tc_mma_scores<KS>(tS[j & 1], dQ, tc_desc_k(sk + ki * L::kTile), idSn);
-                umma_commit(&s_full[j & 1]);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto dprobs = [&](int j) {
-            const int vi = j % L::kVs;
-            if (!wait.all(&v_full[vi], (j / L::kVs) & 1)) return false;
-            const int keys = min(kTcTile, t.olen - j * kTcTile);
-            if (keys < kTcTile) tc_zero_rows<NB>(sv + vi * L::kTile, keys);
-            if (elect_one()) {
-                tc_fence_after();
-                tc_mma_scores<KS>(tP, dG, tc_desc_k(sv + vi * L::kTile), idS);
-                umma_commit(&v_empty[vi]);
-                umma_commit(dp_full);
-            }
-            __syncwarp();
-            return true;
-        };
-        bool ok = wait.all(q_full, 0) && scores(0) && dprobs(0);
-        for (int j = 0; ok && j < n; ++j) {
-            if (j + 1 < n && !(ok = scores(j + 1))) break;
-            if (!(ok = wait.all(ds_full, j & 1))) break;
-            tc_fence_after();
-            if (j + 1 < n && !(ok = dprobs(j + 1))) break;
-            if (elect_one()) {
-                const uint64_t dK = tc_desc_mn(sk + (j % L::kKs) * L::kTile);
-                tc_mma_tokens<true>(tQ, tS[j & 1], dK, idQ, j > 0);
-                umma_commit(&k_empty[j % L::kKs]);
-                if (j + 1 == n) umma_commit(fin);
-            }
-            __syncwarp();
-        }
-        if (!ok && elect_one()) {
-            umma_commit(fin);
-            tc_drain(fin, 0);
-        }
-    } else {
-        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const int half = warp >> 2;   // columns [64*half, +64)
-        const int row = (warp & 3) * 32 + lane;
-        const int last = t.t0 + row + off;
-        const float sc = fmaxf(fabsf(a.scale_log2), 1.2e-38f);
-        const int64_t at = h * a.stat_stride + static_cast<int64_t>(slot) * kTcTile + row;
-        const float lse2 = a.lse2[at], delta = a.delta[at];
-        bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            const uint32_t tSj = tS[j & 1] + lane_base + half * 64;
-            if (!(ok = wait.all(&s_full[j & 1], (j >> 1) & 1))) break;
-            tc_fence_after();
-            uint32_t s[2][32];
-            tmem_ld32(tSj, s[0]);
-            tmem_ld32(tSj + 32, s[1]);
-            tmem_ld_wait();
-            float p[64];
-#pragma unroll
-            for (int i = 0; i < 64; ++i) p[i] = ex2(fmaf(__uint_as_float(s[i / 32][i % 32]), sc, -lse2));
-            const int k0 = j * kTcTile, keys = min(kTcTile, t.olen - k0);
-            if (keys < kTcTile || (a.causal && k0 + kTcTile - 1 > t.t0 + (warp & 3) * 32 + off)) {
-                const int lim = (a.causal ? min(keys, last + 1 - k0) : keys) - half * 64;
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    if (i >= lim) p[i] = 0.f;
-            }
-            if (!(ok = wait.all(dp_full, j & 1))) break;
-            tc_fence_after();
-            tmem_ld32(tP + lane_base + half * 64, s[0]);
-            tmem_ld32(tP + lane_base + half * 64 + 32, s[1]);
-            tmem_ld_wait();
-            uint32_t ds[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                ds[i] = pack_bf16(p[2 * i] * (__uint_as_float(s[i / 16][2 * (i % 16)]) - delta),
-                                  p[2 * i + 1] * (__uint_as_float(s[i / 16][2 * (i % 16) + 1]) - delta));
-            tmem_st32(tSj, ds);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ds_full);
-        }
-        if (ok && wait.all(fin, 0)) {
-            tc_fence_after();
-            tc_store_half<KS>(half, sq, tQ + lane_base, a.scale, (warp & 3) * 32, rows, dq, a.dq_ts, a.D, [] {});
-            tc_fence_before();
-        }
-    }
-    __syncthreads();
-    if (warp == 9) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-    }
-}
-
-template <int KS>
-struct DkvSmem : Chan<KS> {
-    using Chan<KS>::kTile;
-    static constexpr int kQs = 3, kGs = 2;                             // ring slots of Q and dO
+    static constexpr int kAs = 3, kBs = 2;                             // ring slots
+    static constexpr int kA = 2 * kTile, kB = kA + kAs * kTile;        // after the fixed tiles
     static constexpr int kStat = 2 * kTcTile * 4;                      // lse2 and delta of a Q tile; two slots
-    static constexpr int kStats = (2 + kQs + kGs) * kTile;             // K, V, rings
+    static constexpr int kStats = kB + kBs * kTile;
     static constexpr int kBars = kStats + 2 * kStat;
-    static constexpr int kBytes = kBars + 168;   // no room for alignment slack: the kernel checks the base it gets
+    static constexpr int kBytes = kBars + 512;   // no room for alignment slack: the kernel checks the base it gets
     static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
-template <int KS>
-__device__ __forceinline__ void dkv_block(const AttnArgs &a, const AttnMaps &maps, uint8_t *smem, int block) {
-    using L = DkvSmem<KS>;
-    constexpr int NB = L::NB;
-    uint8_t *sk = smem, *sv = smem + L::kTile, *sq = smem + 2 * L::kTile, *sg = sq + L::kQs * L::kTile;
-    float *stats = reinterpret_cast<float *>(smem + L::kStats);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars);
-    uint64_t *q_full = bars, *q_empty = bars + 3, *g_full = bars + 6, *g_empty = bars + 8, *kv_full = bars + 10,
-             *s_full = bars + 11, *dp_full = bars + 12, *p_full = bars + 13, *ds_full = bars + 14, *fin = bars + 15,
-             *st_full = bars + 16 /* two */;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
+enum BwdKind : int { BWD_NONE = -1, BWD_DKV = 0, BWD_DQ = 1 };
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 18; ++i) mbar_init(&bars[i], i == 13 || i == 14 ? 8 : 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    const int hk = block % a.Hk, slot = block / a.Hk;   // under a causal mask the first tiles have the most queries
-    const TileInfo t = tile_info<kTcTile>(a.sk, a.sq, slot);      // own side: keys
-    const int keys = min(kTcTile, t.len - t.t0);
-    if (t.t0 < 0 || keys <= 0) return;
-    const int off = t.len - t.olen;   // causal: query i sees keys [0, i + off]
-    const int64_t tok = t.s0 + t.t0;
-    __nv_bfloat16 *dk = static_cast<__nv_bfloat16 *>(a.dk) + tok * a.dk_ts + hk * a.dk_hs;
-    __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(a.dv) + tok * a.dv_ts + hk * a.dv_hs;
-    const int first = a.causal ? max(0, t.t0 - off) / kTcTile : 0;   // first query tile that sees the tile's first key
-    const int per_head = (t.olen + kTcTile - 1) / kTcTile - first;
-    if (per_head <= 0) {
-        const int per = a.D / 8;
-        for (int i = threadIdx.x; i < keys * per; i += kBwdThreads) {
-            *reinterpret_cast<uint4 *>(dk + (i / per) * a.dk_ts + (i % per) * 8) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(dv + (i / per) * a.dv_ts + (i % per) * 8) = make_uint4(0, 0, 0, 0);
-        }
-        return;
-    }
-    const int n = per_head * a.group;
+// A piece of work as warp 8 hands it to the others.
+struct BwdWork {
+    int kind;
+    int head;       // query head (dQ) or key head
+    int rows;       // rows of the own tile (0: nothing to do)
+    int n;          // tiles of the other side, over all heads (0: zero gradients)
+    int tok;        // first token of the own tile
+    int t0;         // its position in the sequence
+    int off;        // Lk - Lq: under a causal mask query i sees keys [0, i + off]
+    int o0, olen;   // the other side: first token, length
+    int first, per; // dK/dV: first query tile, query tiles a head
+    int slot;       // dQ: the own tile's slot; dK/dV: the sequence's first query slot
+};
 
-    if (warp == 9) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
-    const TcWaits wait{abort_flag, a.status};
+struct BwdBars {
+    uint64_t a_full[3], a_empty[3], b_full[2], b_empty[2], f_full, f_empty;
+    uint64_t st_full[2];                          // row statistics (dK/dV)
+    uint64_t s_full[2], dp_full, p_full, ds_full; // S, dP, P, dS of a tile
+    uint64_t fin, acc_free;                       // a piece's sums done, read
+    uint64_t staged[2];                           // its output gone out through the staging slot (pieces in turn)
+    uint64_t work_full[2], work_empty[2];
+    uint64_t clc, dead;
+    uint4 answer;
+    BwdWork work[2];
+    uint32_t tmem;
+    int abort_flag;
+};
+static_assert(sizeof(BwdBars) <= 512, "room after the statistics");
 
-    if (warp == 8) {
-        if (lane == 0) {
-            mbar_arrive_expect_tx(kv_full, 2 * L::kTile);
-            tc_load_tile<NB>(sk, &maps.k, kv_full, hk, static_cast<int>(tok));
-            tc_load_tile<NB>(sv, &maps.v, kv_full, hk, static_cast<int>(tok));
-            const int64_t qslot0 = slot_base<kTcTile>(a.sq, t.b);
-            int h = hk * a.group, qt = first, j = 0, ql = 0, gl = 0, sl = 0;
-            for (; j < n; ++j) {
-                const int qi = j % L::kQs, gi = j % L::kGs, at = t.o0 + qt * kTcTile;
-                if (!wait(&q_empty[qi], ((j / L::kQs) & 1) ^ 1)) break;
-                mbar_arrive_expect_tx(&q_full[qi], L::kTile);
-                tc_load_tile<NB>(sq + qi * L::kTile, &maps.q, &q_full[qi], h, at);
-                ++ql;
-                if (!wait(&g_empty[gi], ((j / L::kGs) & 1) ^ 1)) break;
-                mbar_arrive_expect_tx(&g_full[gi], L::kTile);
-                tc_load_tile<NB>(sg + gi * L::kTile, &maps.dO, &g_full[gi], h, at);
-                ++gl;
-                // the statistics' slot is free once dK_(j-2), which follows their last use, has been summed
-                if (j >= 2 && !wait(&q_empty[(j - 2) % L::kQs], ((j - 2) / L::kQs) & 1)) break;
-                const int64_t st = h * a.stat_stride + (qslot0 + qt) * kTcTile;
-                float *dst = stats + (j & 1) * 2 * kTcTile;
-                mbar_arrive_expect_tx(&st_full[j & 1], L::kStat);
-                bulk_load(dst, a.lse2 + st, kTcTile * 4, &st_full[j & 1]);
-                bulk_load(dst + kTcTile, a.delta + st, kTcTile * 4, &st_full[j & 1]);
-                ++sl;
-                if (++qt == first + per_head) qt = first, ++h;
-            }
-            if (j < n) {
-                tc_drain(kv_full, 0);
-                for (int i = max(0, ql - L::kQs); i < ql; ++i) tc_drain(&q_full[i % L::kQs], (i / L::kQs) & 1);
-                for (int i = max(0, gl - L::kGs); i < gl; ++i) tc_drain(&g_full[i % L::kGs], (i / L::kGs) & 1);
-                for (int i = max(0, sl - 2); i < sl; ++i) tc_drain(&st_full[i & 1], (i >> 1) & 1);
-            }
-        }
-    } else if (warp == 9) {
-        const uint32_t idS = idesc_f32acc(1, 128, 128, false, false), idG = idesc_f32acc(1, 128, KS * 16, false, true);
-        const uint32_t idSn = idS | (a.scale < 0.f ? kIdescNegA : 0);
-        const uint64_t dK = tc_desc_k(sk), dV = tc_desc_k(sv);
-        auto queries = [&](int j) { return min(kTcTile, t.olen - (first + j % per_head) * kTcTile); };
-        auto scores = [&](int j) {
-            const int qi = j % L::kQs;
-            if (!wait.all(&q_full[qi], (j / L::kQs) & 1)) return false;
-            const int q = queries(j);
-            if (q < kTcTile) tc_zero_rows<NB>(sq + qi * L::kTile, q);
-            if (elect_one()) {
-                tc_fence_after();
-                tc_mma_scores<KS>(tS, dK, tc_desc_k(sq + qi * L::kTile), idSn);
-                umma_commit(s_full);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto dprobs = [&](int j) {
-            const int gi = j % L::kGs;
-            if (!wait.all(&g_full[gi], (j / L::kGs) & 1)) return false;
-            const int q = queries(j);
-            if (q < kTcTile) tc_zero_rows<NB>(sg + gi * L::kTile, q);
-            if (elect_one()) {
-                tc_fence_after();
-                tc_mma_scores<KS>(tP, dV, tc_desc_k(sg + gi * L::kTile), idS);
-                umma_commit(dp_full);
-            }
-            __syncwarp();
-            return true;
-        };
-        // acc (+)= A[keys x queries] . tile, A in two halves of 64 queries, 64 columns apart
-        auto gather = [&](uint32_t acc, uint32_t A, const uint8_t *tile, int j, uint64_t *release) {
-            if (elect_one()) {
-                tc_fence_after();
-                tc_mma_tokens<true>(acc, A, tc_desc_mn(tile), idG, j > 0);
-                umma_commit(release);
-            }
-            __syncwarp();
-        };
-        bool ok = wait.all(kv_full, 0) && scores(0) && dprobs(0);
-        for (int j = 0; ok && j < n; ++j) {
-            if (!(ok = wait.all(p_full, j & 1))) break;
-            gather(tV, tS, sg + (j % L::kGs) * L::kTile, j, &g_empty[j % L::kGs]);
-            if (j + 1 < n && !(ok = scores(j + 1))) break;
-            if (!(ok = wait.all(ds_full, j & 1))) break;
-            gather(tK, tP, sq + (j % L::kQs) * L::kTile, j, &q_empty[j % L::kQs]);
-            if (j + 1 < n && !(ok = dprobs(j + 1))) break;
-        }
-        if (elect_one()) {
-            umma_commit(fin);
-            if (!ok) tc_drain(fin, 0);
-        }
-    } else {
-        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const int half = warp >> 2;
-        const int key = t.t0 + (warp & 3) * 32 + lane;
-        const float sc = fmaxf(fabsf(a.scale_log2), 1.2e-38f);
-        const uint32_t tSh = tS + lane_base + half * 64, tPh = tP + lane_base + half * 64;
-        bool ok = true;
-        int qt = first;
-        for (int j = 0; j < n; ++j) {
-            const float4 *lse2 = reinterpret_cast<const float4 *>(stats + (j & 1) * 2 * kTcTile + half * 64);
-            const float4 *delta = lse2 + kTcTile / 4;
-            if (!(ok = wait.all(&st_full[j & 1], (j >> 1) & 1))) break;
-            if (!(ok = wait.all(s_full, j & 1))) break;
-            tc_fence_after();
-            uint32_t s[2][32];
-            tmem_ld32(tSh, s[0]);
-            tmem_ld32(tSh + 32, s[1]);
-            tmem_ld_wait();
-            float p[64];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float4 l = lse2[i];
-                const uint32_t *x = &s[i / 8][4 * (i % 8)];
-                p[4 * i] = ex2(fmaf(__uint_as_float(x[0]), sc, -l.x));
-                p[4 * i + 1] = ex2(fmaf(__uint_as_float(x[1]), sc, -l.y));
-                p[4 * i + 2] = ex2(fmaf(__uint_as_float(x[2]), sc, -l.z));
-                p[4 * i + 3] = ex2(fmaf(__uint_as_float(x[3]), sc, -l.w));
-            }
-            // causal: query i sees the key from i = key - off on; the warp's last key is its tightest
-            if (a.causal && qt * kTcTile < t.t0 + (warp & 3) * 32 + 31 - off) {
-                const int lim = key - off - qt * kTcTile - half * 64;
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    if (i < lim) p[i] = 0.f;
-            }
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
-            tmem_st32(tSh, w);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_full);
-            if (!(ok = wait.all(dp_full, j & 1))) break;
-            tc_fence_after();
-            tmem_ld32(tPh, s[0]);
-            tmem_ld32(tPh + 32, s[1]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float4 d = delta[i];
-                const uint32_t *x = &s[i / 8][4 * (i % 8)];
-                w[2 * i] = pack_bf16(p[4 * i] * (__uint_as_float(x[0]) - d.x), p[4 * i + 1] * (__uint_as_float(x[1]) - d.y));
-                w[2 * i + 1] = pack_bf16(p[4 * i + 2] * (__uint_as_float(x[2]) - d.z),
-                                         p[4 * i + 3] * (__uint_as_float(x[3]) - d.w));
-            }
-            tmem_st32(tPh, w);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ds_full);
-            if (++qt == first + per_head) qt = first;
-        }
-        if (ok && wait.all(fin, 0)) {
-            tc_fence_after();
-            tc_store_half<KS>(half, sv, tV + lane_base, 1.f, (warp & 3) * 32, keys, dv, a.dv_ts, a.D, [] {});
-            tc_store_half<KS>(half, sk, tK + lane_base, a.scale, (warp & 3) * 32, keys, dk, a.dk_ts, a.D, [] {});
-            tc_fence_before();
-        }
-    }
-    __syncthreads();
-    if (warp == 9) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-    }
-}
-
-// Both in one launch, the longer dK/dV blocks first: they share nothing but
-// their inputs, so the dQ blocks fill the SMs that the others leave idle.
 template <int KS>
 __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_constant__ AttnArgs a,
                                                              const __grid_constant__ AttnMaps maps, int dkv_blocks) {
@@ -441,15 +81,447 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
         if (threadIdx.x == 0) atomicOr(a.status, kDevTimeout);
         return;
     }
-    const int block = blockIdx.x;
-    if (threadIdx.x == 32) {
+    using L = BwdSmem<KS>;
+    constexpr int NB = L::NB;
+    uint8_t *f0 = smem, *f1 = smem + L::kTile, *sa = smem + L::kA, *sb = smem + L::kB;
+    float *stats = reinterpret_cast<float *>(smem + L::kStats);
+    BwdBars &bar = *reinterpret_cast<BwdBars *>(smem + L::kBars);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        uint64_t *all = bar.a_full;
+        for (int i = 0; i < static_cast<int>(offsetof(BwdBars, answer) / 8); ++i) mbar_init(&all[i], 1);
+        for (uint64_t *b : {&bar.p_full, &bar.ds_full, &bar.acc_free, &bar.staged[0], &bar.staged[1]}) mbar_init(b, 8);
+        for (int i = 0; i < 2; ++i) mbar_init(&bar.work_empty[i], 9);
+        bar.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(&bar.tmem, 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 256) {
         tma_prefetch_map(&maps.q);
         tma_prefetch_map(&maps.k);
         tma_prefetch_map(&maps.v);
         tma_prefetch_map(&maps.dO);
     }
-    if (block < dkv_blocks) dkv_block<KS>(a, maps, smem, block);
-    else dq_block<KS>(a, maps, smem, block - dkv_blocks, gridDim.x - dkv_blocks);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // columns: dK/dV has S, dP, dV, dK; dQ has two S, dP, dQ
+    const uint32_t tm = __shfl_sync(0xffffffffu, bar.tmem, 0);
+    const TcWaits wait{&bar.abort_flag, a.status};
+
+    if (warp == 8) {
+        auto find = [&](int block) {
+            BwdWork w{};
+            if (block < dkv_blocks) {   // under a causal mask the first key tiles have the most queries
+                const TileInfo t = tile_info<kTcTile>(a.sk, a.sq, block / a.Hk);
+                w.kind = BWD_DKV;
+                w.head = block % a.Hk;
+                w.rows = t.t0 < 0 ? 0 : max(0, min(kTcTile, t.len - t.t0));
+                w.off = t.len - t.olen;
+                w.first = a.causal ? max(0, t.t0 - w.off) / kTcTile : 0;   // the first that sees the tile's first key
+                w.per = max(0, (t.olen + kTcTile - 1) / kTcTile - w.first);
+                w.n = w.rows > 0 ? w.per * a.group : 0;
+                w.slot = t.o0 / kTcTile + t.b;
+                w.tok = t.s0 + t.t0, w.t0 = t.t0, w.o0 = t.o0, w.olen = t.olen;
+            } else {                    // ... and the last query tiles the most keys
+                block -= dkv_blocks;
+                const int slot = (gridDim.x - dkv_blocks) / a.Hq - 1 - block / a.Hq;
+                const TileInfo t = tile_info<kTcTile>(a.sq, a.sk, slot);
+                w.kind = BWD_DQ;
+                w.head = block % a.Hq;
+                w.rows = t.t0 < 0 ? 0 : max(0, min(kTcTile, t.len - t.t0));
+                w.off = t.olen - t.len;
+                const int kend = a.causal ? min(t.olen, t.t0 + w.rows + w.off) : t.olen;
+                w.n = w.rows > 0 && kend > 0 ? (kend + kTcTile - 1) / kTcTile : 0;
+                w.slot = slot;
+                w.tok = t.s0 + t.t0, w.t0 = t.t0, w.o0 = t.o0, w.olen = t.olen;
+            }
+            return w;
+        };
+        bool ok = true;
+        int pieces = 0;                       // handed over
+        int na = 0, nb = 0, nf = 0, ns = 0;   // loads of each kind so far
+        int stat0 = -1, stat1 = -1;           // the ring tile that each slot of statistics was last for
+        int staged = 0, need[3] = {0, 0, 0};  // outputs known to have gone out; how many must have, by ring slot
+        auto publish = [&](const BwdWork &w) {
+            if (!(ok = wait.all(&bar.work_empty[pieces & 1], ((pieces >> 1) & 1) ^ 1))) return;
+            if (lane == 0) {
+                bar.work[pieces & 1] = w;
+                mbar_arrive(&bar.work_full[pieces & 1]);
+            }
+            __syncwarp();
+            ++pieces;
+        };
+        auto await_staged = [&](int count) {
+            for (; ok && staged < count; ++staged) ok = wait.all(&bar.staged[staged & 1], (staged >> 1) & 1);
+            return ok;
+        };
+        bool asked = false;   // a request for the next block is in flight
+        int answers = 0;
+        BwdWork cur = find(blockIdx.x);
+        publish(cur);
+        while (ok && cur.kind != BWD_NONE) {
+            const bool dkv = cur.kind == BWD_DKV;
+            if (cur.n > 0) {
+                // seeing every output go out in turn, at most two pieces late, keeps the barriers' phases apart
+                if (!await_staged(nf - 1)) break;
+                if (!(ok = wait.all(&bar.f_empty, (nf & 1) ^ 1))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bar.f_full, 2 * L::kTile);
+                    tc_load_tile<NB>(f0, dkv ? &maps.k : &maps.q, &bar.f_full, cur.head, cur.tok);
+                    tc_load_tile<NB>(f1, dkv ? &maps.v : &maps.dO, &bar.f_full, cur.head, cur.tok);
+                }
+                ++nf;
+            }
+            BwdWork next{};
+            int h = dkv ? cur.head * a.group : cur.head / a.group, tile = cur.first;   // of the other side
+            const int steps = max(cur.n, 1);
+            for (int j = 0; j < steps; ++j) {
+                // The next piece is asked for when this one's last loads but one are due: late, so that a CTA with
+                // a long piece does not hold another that an idle one could start (asked for at the start, a
+                // backward of 250 pieces on 152 SMs took 47 us instead of 35), and early enough for it to be found.
+                if (j == max(0, cur.n - 2)) {
+                    if (lane == 0) {
+                        fence_proxy_async_smem();   // the last answer has been read
+                        clc_request(&bar.answer, &bar.clc);
+                    }
+                    asked = true;
+                }
+                if (j < cur.n) {
+                    const int ai = na % L::kAs, bi = nb % L::kBs, at = cur.o0 + tile * kTcTile;
+                    if (!await_staged(need[ai])) break;
+                    if (!(ok = wait.all(&bar.a_empty[ai], ((na / L::kAs) & 1) ^ 1))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bar.a_full[ai], L::kTile);
+                        tc_load_tile<NB>(sa + ai * L::kTile, dkv ? &maps.q : &maps.k, &bar.a_full[ai], h, at);
+                    }
+                    ++na;
+                    if (!(ok = wait.all(&bar.b_empty[bi], ((nb / L::kBs) & 1) ^ 1))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bar.b_full[bi], L::kTile);
+                        tc_load_tile<NB>(sb + bi * L::kTile, dkv ? &maps.dO : &maps.v, &bar.b_full[bi], h, at);
+                    }
+                    ++nb;
+                    if (dkv) {
+                        // a slot of statistics is free once the tile it was for has left its ring slot (its dK sum
+                        // follows the last use of them); one three loads back has, or this tile's slot were not free
+                        const int c = na - 1, p = (ns & 1) ? stat1 : stat0;
+                        if (p >= 0 && p > c - L::kAs && !(ok = wait.all(&bar.a_empty[p % L::kAs], (p / L::kAs) & 1))) break;
+                        ((ns & 1) ? stat1 : stat0) = c;
+                        if (lane == 0) {
+                            const int64_t st = h * a.stat_stride + static_cast<int64_t>(cur.slot + tile) * kTcTile;
+                            float *dst = stats + (ns & 1) * 2 * kTcTile;
+                            mbar_arrive_expect_tx(&bar.st_full[ns & 1], L::kStat);
+                            bulk_load(dst, a.lse2 + st, kTcTile * 4, &bar.st_full[ns & 1]);
+                            bulk_load(dst + kTcTile, a.delta + st, kTcTile * 4, &bar.st_full[ns & 1]);
+                        }
+                        ++ns;
+                    }
+                    ++tile;
+                    if (dkv && tile == cur.first + cur.per) tile = cur.first, ++h;
+                }
+                if (j + 1 == steps) {
+                    if (!(ok = wait.all(&bar.clc, answers & 1))) break;
+                    ++answers;
+                    asked = false;
+                    const int block = __shfl_sync(0xffffffffu, clc_answer(&bar.answer), 0);
+                    if (block >= 0) next = find(block);
+                    else next.kind = BWD_NONE;
+                    publish(next);
+                    if (!ok) break;
+                }
+            }
+            if (!ok) break;
+            // the output goes out through the ring slot of the piece's last tile, which is loaded last again
+            if (cur.n > 0) need[(na - 1) % L::kAs] = nf;
+            cur = next;
+        }
+        if (!ok && lane == 0) {   // what is in flight lands before the CTA gives up its memory
+            if (nf) tc_drain(&bar.f_full, (nf - 1) & 1);
+            for (int i = max(0, na - L::kAs); i < na; ++i) tc_drain(&bar.a_full[i % L::kAs], (i / L::kAs) & 1);
+            for (int i = max(0, nb - L::kBs); i < nb; ++i) tc_drain(&bar.b_full[i % L::kBs], (i / L::kBs) & 1);
+            for (int i = max(0, ns - 2); i < ns; ++i) tc_drain(&bar.st_full[i & 1], (i >> 1) & 1);
+            if (asked) tc_drain(&bar.clc, answers & 1);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        const uint32_t idS = idesc_f32acc(1, 128, 128, false, false), idG = idesc_f32acc(1, 128, KS * 16, false, true);
+        const uint32_t idSn = idS | (a.scale < 0.f ? kIdescNegA : 0);
+        const uint64_t d0 = tc_desc_k(f0), d1 = tc_desc_k(f1);
+        bool ok = true;
+        int na = 0, nb = 0, nf = 0, np = 0, nd = 0;   // tiles of each ring, pieces, P and dS tiles so far
+        int kind = BWD_NONE;                          // of the piece before
+        for (int pieces = 0; ok; ++pieces) {
+            if (!(ok = wait.all(&bar.work_full[pieces & 1], (pieces >> 1) & 1))) break;
+            const BwdWork &w = bar.work[pieces & 1];
+            const int k = __shfl_sync(0xffffffffu, w.kind, 0), n = __shfl_sync(0xffffffffu, w.n, 0),
+                      olen = __shfl_sync(0xffffffffu, w.olen, 0), first = __shfl_sync(0xffffffffu, w.first, 0),
+                      per = __shfl_sync(0xffffffffu, w.per, 0);
+            if (lane == 0) mbar_arrive(&bar.work_empty[pieces & 1]);
+            if (k == BWD_NONE) break;
+            if (n == 0) continue;
+            const bool dkv = k == BWD_DKV;
+            // the sums of the piece before have been read: needed before this piece's first sum, and before its first
+            // products where the kinds have their sums in different columns
+            bool free = nf == 0;
+            auto await_free = [&] {
+                if (!free) free = ok = wait.all(&bar.acc_free, (nf - 1) & 1);
+                return ok;
+            };
+            if (kind != k && !await_free()) break;
+            kind = k;
+            if (!(ok = wait.all(&bar.f_full, nf & 1))) break;
+            const uint32_t tP = dkv ? tm + 128 : tm + 256;
+            // tokens of the other side in tile j
+            auto tokens = [&](int j) { return min(kTcTile, olen - (dkv ? first + j % per : j) * kTcTile); };
+            auto scores = [&](int j) {
+                const int i = na + j, ai = i % L::kAs;
+                if (!wait.all(&bar.a_full[ai], (i / L::kAs) & 1)) return false;
+                uint8_t *tile = sa + ai * L::kTile;
+                const int left = tokens(j);
+                if (left < kTcTile) tc_zero_rows<NB>(tile, left);   // summed over below
+                const int buf = dkv ? 0 : j & 1;
+                if (elect_one()) {
+                    tc_fence_after();
+                    tc_mma_scores<KS>(tm + buf * 128, d0, tc_desc_k(tile), idSn);
+                    umma_commit(&bar.s_full[buf]);
+                }
+                __syncwarp();
+                return true;
+            };
+            auto dprobs = [&](int j) {
+                const int i = nb + j, bi = i % L::kBs;
+                if (!wait.all(&bar.b_full[bi], (i / L::kBs) & 1)) return false;
+                uint8_t *tile = sb + bi * L::kTile;
+                const int left = tokens(j);
+                if (left < kTcTile) tc_zero_rows<NB>(tile, left);
+                if (elect_one()) {
+                    tc_fence_after();
+                    tc_mma_scores<KS>(tP, d1, tc_desc_k(tile), idS);
+                    if (!dkv) umma_commit(&bar.b_empty[bi]);
+                    if (j + 1 == n) umma_commit(&bar.f_empty);   // the last use of the fixed tiles
+                    umma_commit(&bar.dp_full);
+                }
+                __syncwarp();
+                return true;
+            };
+            // acc (+)= A . tile over the tile's tokens, A in two halves of 64 tokens, 64 columns apart
+            auto sum = [&](uint32_t acc, uint32_t A, const uint8_t *tile, int j, uint64_t *release, bool last) {
+                if (elect_one()) {
+                    tc_fence_after();
+                    tc_mma_tokens<true>(acc, A, tc_desc_mn(tile), idG, j > 0);
+                    umma_commit(release);
+                    if (last) umma_commit(&bar.fin);
+                }
+                __syncwarp();
+            };
+            ok = scores(0) && dprobs(0);
+            if (dkv) {
+                for (int j = 0; ok && j < n; ++j) {
+                    const int ai = (na + j) % L::kAs, bi = (nb + j) % L::kBs;
+                    if (!(ok = wait.all(&bar.p_full, (np + j) & 1)) || !await_free()) break;
+                    sum(tm + 256, tm, sb + bi * L::kTile, j, &bar.b_empty[bi], false);
+                    if (j + 1 < n && !(ok = scores(j + 1))) break;
+                    if (!(ok = wait.all(&bar.ds_full, (nd + j) & 1))) break;
+                    sum(tm + 384, tP, sa + ai * L::kTile, j, &bar.a_empty[ai], j + 1 == n);
+                    if (j + 1 < n && !(ok = dprobs(j + 1))) break;
+                }
+                np += n;
+            } else {
+                for (int j = 0; ok && j < n; ++j) {
+                    const int ai = (na + j) % L::kAs;
+                    if (j + 1 < n && !(ok = scores(j + 1))) break;
+                    if (!(ok = wait.all(&bar.ds_full, (nd + j) & 1)) || !await_free()) break;
+                    tc_fence_after();
+                    if (j + 1 < n && !(ok = dprobs(j + 1))) break;
+                    sum(tm + 384, tm + (j & 1) * 128, sa + ai * L::kTile, j, &bar.a_empty[ai], j + 1 == n);
+                }
+            }
+            nd += n;
+            na += n;
+            nb += n;
+            ++nf;
+        }
+        if (!ok && elect_one()) {   // let the MMAs issued so far finish
+            umma_commit(&bar.dead);
+            tc_drain(&bar.dead, 0);
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, half = warp >> 2;   // columns [64*half, +64) of a tile
+        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+        const int row = quarter * 32 + lane;
+        const float sc = fmaxf(fabsf(a.scale_log2), 1.2e-38f);
+        const f32x2 sc2 = both(sc);
+        bool ok = true;
+        int na = 0, nf = 0, nd = 0, ns = 0, s0 = 0, s1 = 0;   // ring tiles, pieces, dS, statistics, S by buffer so far
+        for (int pieces = 0; ok; ++pieces) {
+            if (!(ok = wait.all(&bar.work_full[pieces & 1], (pieces >> 1) & 1))) break;
+            const BwdWork w = bar.work[pieces & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.work_empty[pieces & 1]);
+            if (w.kind == BWD_NONE) break;
+            const bool dkv = w.kind == BWD_DKV;
+            __nv_bfloat16 *out0, *out1 = nullptr;   // dQ, or dV and dK
+            int64_t ts0, ts1 = 0;
+            if (dkv) {
+                ts0 = a.dv_ts, ts1 = a.dk_ts;
+                out0 = static_cast<__nv_bfloat16 *>(a.dv) + w.tok * ts0 + w.head * a.dv_hs;
+                out1 = static_cast<__nv_bfloat16 *>(a.dk) + w.tok * ts1 + w.head * a.dk_hs;
+            } else {
+                ts0 = a.dq_ts;
+                out0 = static_cast<__nv_bfloat16 *>(a.dq) + w.tok * ts0 + w.head * a.dq_hs;
+            }
+            if (w.n == 0) {   // nothing on the other side
+                if (row < w.rows)
+                    for (int c = half * 8; c < a.D; c += 16) {
+                        *reinterpret_cast<uint4 *>(out0 + row * ts0 + c) = make_uint4(0, 0, 0, 0);
+                        if (dkv) *reinterpret_cast<uint4 *>(out1 + row * ts1 + c) = make_uint4(0, 0, 0, 0);
+                    }
+                continue;
+            }
+            if (dkv) {
+                const uint32_t tSh = tm + lane_base + half * 64, tPh = tSh + 128;
+                const int key = w.t0 + row;
+                int qt = w.first;
+                for (int j = 0; j < w.n; ++j, ++nd, ++ns, ++s0) {
+                    const float4 *lse2 = reinterpret_cast<const float4 *>(stats + (ns & 1) * 2 * kTcTile + half * 64);
+                    const float4 *delta = lse2 + kTcTile / 4;
+                    if (!(ok = wait.all(&bar.st_full[ns & 1], (ns >> 1) & 1))) break;
+                    if (!(ok = wait.all(&bar.s_full[0], s0 & 1))) break;
+                    tc_fence_after();
+                    uint32_t s[2][32];
+                    tmem_ld32(tSh, s[0]);
+                    tmem_ld32(tSh + 32, s[1]);
+                    tmem_ld_wait();
+                    float p[64];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float4 l = lse2[i];
+                        const uint32_t *x = &s[i / 8][4 * (i % 8)];
+                        unpack2(fma2(pack2u(x[0], x[1]), sc2, pack2(-l.x, -l.y)), p[4 * i], p[4 * i + 1]);
+                        unpack2(fma2(pack2u(x[2], x[3]), sc2, pack2(-l.z, -l.w)), p[4 * i + 2], p[4 * i + 3]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[4 * i + e] = ex2(p[4 * i + e]);
+                    }
+                    // causal: query i sees the key from i = key - off on; the warp's last key is its tightest
+                    if (a.causal && qt * kTcTile < w.t0 + quarter * 32 + 31 - w.off) {
+                        const int lim = key - w.off - qt * kTcTile - half * 64;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (i < lim) p[i] = 0.f;
+                    }
+                    uint32_t v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
+                    tmem_st32(tSh, v);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.p_full);
+                    if (!(ok = wait.all(&bar.dp_full, nd & 1))) break;
+                    tc_fence_after();
+                    tmem_ld32(tPh, s[0]);
+                    tmem_ld32(tPh + 32, s[1]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float4 d = delta[i];
+                        const uint32_t *x = &s[i / 8][4 * (i % 8)];
+                        float e, f;
+                        unpack2(mul2(pack2(p[4 * i], p[4 * i + 1]), add2(pack2u(x[0], x[1]), pack2(-d.x, -d.y))), e, f);
+                        v[2 * i] = pack_bf16(e, f);
+                        unpack2(mul2(pack2(p[4 * i + 2], p[4 * i + 3]), add2(pack2u(x[2], x[3]), pack2(-d.z, -d.w))), e, f);
+                        v[2 * i + 1] = pack_bf16(e, f);
+                    }
+                    tmem_st32(tPh, v);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.ds_full);
+                    if (++qt == w.first + w.per) qt = w.first;
+                }
+            } else {
+                const uint32_t tPh = tm + 256 + lane_base + half * 64;
+                const int last = w.t0 + row + w.off;   // causal: last key of the row
+                const int64_t at = w.head * a.stat_stride + static_cast<int64_t>(w.slot) * kTcTile + row;
+                const float lse2 = a.lse2[at], delta = a.delta[at];
+                const f32x2 nl2 = both(-lse2), nd2 = both(-delta);
+                for (int j = 0; j < w.n; ++j, ++nd) {
+                    const uint32_t tSj = tm + (j & 1) * 128 + lane_base + half * 64;
+                    int &sn = j & 1 ? s1 : s0;
+                    if (!(ok = wait.all(&bar.s_full[j & 1], sn & 1))) break;
+                    ++sn;
+                    tc_fence_after();
+                    uint32_t s[2][32];
+                    tmem_ld32(tSj, s[0]);
+                    tmem_ld32(tSj + 32, s[1]);
+                    tmem_ld_wait();
+                    float p[64];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        unpack2(fma2(pack2u(s[i / 16][2 * (i % 16)], s[i / 16][2 * (i % 16) + 1]), sc2, nl2), p[2 * i], p[2 * i + 1]);
+                        p[2 * i] = ex2(p[2 * i]), p[2 * i + 1] = ex2(p[2 * i + 1]);
+                    }
+                    const int k0 = j * kTcTile, keys = min(kTcTile, w.olen - k0);
+                    if (keys < kTcTile || (a.causal && k0 + kTcTile - 1 > w.t0 + quarter * 32 + w.off)) {
+                        const int lim = (a.causal ? min(keys, last + 1 - k0) : keys) - half * 64;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (i >= lim) p[i] = 0.f;
+                    }
+                    if (!(ok = wait.all(&bar.dp_full, nd & 1))) break;
+                    tc_fence_after();
+                    tmem_ld32(tPh, s[0]);
+                    tmem_ld32(tPh + 32, s[1]);
+                    tmem_ld_wait();
+                    uint32_t ds[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float e, f;
+                        unpack2(mul2(pack2(p[2 * i], p[2 * i + 1]),
+                                     add2(pack2u(s[i / 16][2 * (i % 16)], s[i / 16][2 * (i % 16) + 1]), nd2)), e, f);
+                        ds[i] = pack_bf16(e, f);
+                    }
+                    tmem_st32(tSj, ds);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.ds_full);
+                }
+            }
+            if (!ok || !(ok = wait.all(&bar.fin, nf & 1))) break;
+            ++nf;
+            na += w.n;
+            tc_fence_after();
+            uint8_t *tile = sa + (na - 1) % L::kAs * L::kTile;   // of the last tile: no longer read, not yet loaded again
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.acc_free);
+            };
+            if (dkv) {
+                tc_store_half<KS>(half, tile, tm + 256 + lane_base, 1.f, quarter * 32, w.rows, out0, ts0, a.D, [] {});
+                __syncwarp();
+                tc_store_half<KS>(half, tile, tm + 384 + lane_base, a.scale, quarter * 32, w.rows, out1, ts1, a.D, release);
+            } else {
+                tc_store_half<KS>(half, tile, tm + 384 + lane_base, a.scale, quarter * 32, w.rows, out0, ts0, a.D, release);
+            }
+            fence_proxy_async_smem();   // the slot goes back to the loads
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.staged[(nf - 1) & 1]);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
 }
 
 }  // namespace lce

@@ -135,11 +135,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
         publish(cur);
         int kl = 0, vl = 0;   // loads issued
         while (ok && cur.h >= 0) {
-            if (lane == 0) {
-                fence_proxy_async_smem();   // the last answer has been read
-                clc_request(&bar.answer, &bar.clc);
-            }
-            asked = true;
             const int hk = cur.h / a.group;
             if (cur.n > 0) {
                 if (!(ok = wait.all(&bar.q_empty, (qs & 1) ^ 1))) break;
@@ -150,7 +145,17 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
                 ++qs;
             }
             FwdWork next{};
-            for (int j = 0; j < max(cur.n, 1); ++j) {
+            const int steps = max(cur.n, 1);
+            for (int j = 0; j < steps; ++j) {
+                // the next tile is asked for when this one's last loads but one are due: late enough not to hold work
+                // that an idle CTA could start, early enough for it to be found
+                if (j == max(0, cur.n - 2)) {
+                    if (lane == 0) {
+                        fence_proxy_async_smem();   // the last answer has been read
+                        clc_request(&bar.answer, &bar.clc);
+                    }
+                    asked = true;
+                }
                 if (j < cur.n) {
                     const int at = cur.ktok + j * kTcTile;
                     if (!(ok = wait.all(&bar.k_empty, (kv & 1) ^ 1))) break;
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
                     ++vl;
                     ++kv;
                 }
-                if (j == 0) {   // the next tile, while this one's first loads are on their way
+                if (j + 1 == steps) {
                     if (!(ok = wait.all(&bar.clc, answers & 1))) break;
                     ++answers;
                     asked = false;
