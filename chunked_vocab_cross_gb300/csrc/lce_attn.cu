@@ -203,8 +203,8 @@ lce_status_t lce_attention_backward(const lce_attn_t *a) {
     if ((s = scratch.get(a->workspace, a->workspace_bytes, need, &base)) != LCE_OK) return s;
     AttnArgs r = make_args(a, dev);
     r.stat_stride = seq_slots(a->Tq, a->B, stat_tile(a)) * stat_tile(a);
-    r.lse2 = reinterpret_cast<float *>(base);
-    r.delta = r.lse2 + r.stat_stride * r.Hq;
+    r.nlse2 = reinterpret_cast<float *>(base);
+    r.ndelta = r.nlse2 + r.stat_stride * r.Hq;
     if (a->dtype == LCE_BF16)
         return by_channels(a->D, [&](auto ks) { return backward_tc<decltype(ks)::value>(a, r, dev, st); });
     return a->D <= 32 ? backward_simt<32>(r, dev, st) : a->D <= 64 ? backward_simt<64>(r, dev, st) : backward_simt<128>(r, dev, st);

@@ -45,9 +45,9 @@ struct AttnArgs {
     int Hq, Hk, group, D;
     int causal;
     float scale, scale_log2;   // scale, scale * log2(e)
-    // backward: per query slot row, lse * log2(e) (+inf where the row takes no
-    // part) and delta; [Hq][slots * TILE]
-    float *lse2, *delta;
+    // backward: per query slot row, -lse * log2(e) (-inf where the row takes no
+    // part) and -delta, both negative so that they are added; [Hq][slots * TILE]
+    float *nlse2, *ndelta;
     int64_t stat_stride;       // slots * TILE
     int *status;
 };
@@ -129,9 +129,9 @@ __device__ __forceinline__ float dot16(const uint4 &a, const uint4 &b) {
 constexpr int kStatThreads = 256;
 
 // Row statistics of the backward, by slot: delta_i = dO_i . o_i in fp32 and
-// lse_i in base 2, so that the gradient kernels read aligned rows of TILE
-// values. Rows without an allowed key (lse = -inf) and rows past a sequence's
-// end get lse2 = +inf: their probabilities come out as 2^-inf = 0. LPR lanes
+// lse_i in base 2, both negated, so that the gradient kernels read aligned rows
+// of TILE values and add them. Rows without an allowed key (lse = -inf) and rows
+// past a sequence's end get -inf: their probabilities come out as 2^-inf = 0. LPR lanes
 // take a row, 16 bytes each; a thread asks for all its rows before it adds any
 // up, since the kernel is nothing but waits for memory.
 template <typename T, int TILE, int LPR>
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kStatThreads) k_attn_stats(const AttnArgs a) {
         for (int m = LPR / 2; m; m >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, m);
         if (piece == 0) {
             const bool out = l[k] == -INFINITY;
-            a.lse2[at + r0 + k * kRows] = out ? INFINITY : l[k] * kAttnLog2e;
-            a.delta[at + r0 + k * kRows] = out ? 0.f : delta;
+            a.nlse2[at + r0 + k * kRows] = out ? -INFINITY : -l[k] * kAttnLog2e;
+            a.ndelta[at + r0 + k * kRows] = out ? 0.f : -delta;
         }
     }
 }

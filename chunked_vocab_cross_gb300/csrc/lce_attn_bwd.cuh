@@ -12,6 +12,14 @@
 // P and dS go back to TMEM as the A operands, so they never touch shared
 // memory.
 //
+// What bounds it is the chain from a product over the elementwise part to the
+// next product: the tensor core takes 512 cycles for 128 x 128 x 128, 400 more
+// when it starts from idle. So whatever can is issued ahead of its turn: P and
+// dS are handed over 32 columns at a time, the sums' first steps running under
+// the rest; dQ pieces ask for the next dP as soon as the last has been read;
+// and where TMEM has the room (S twice, dP and both sums: up to 64 channels)
+// dK/dV pieces ask for the next S before P is there.
+//
 // 320 threads: warps 0-7 the elementwise part (two threads a row, 64 columns
 // each), warp 8 loads, warp 9 MMA issue. One CTA an SM: dK/dV fills the 512
 // columns of TMEM, and the tiles fill the shared memory: two that stay for a
@@ -61,7 +69,10 @@ struct BwdWork {
 struct BwdBars {
     uint64_t a_full[3], a_empty[3], b_full[2], b_empty[2], f_full, f_empty;
     uint64_t st_full[2];                          // row statistics (dK/dV)
-    uint64_t s_full[2], dp_full, p_full, ds_full; // S, dP, P, dS of a tile
+    uint64_t s_full[2], dp_full, dp_read;         // S and dP of a tile; dP fetched (dQ)
+    // P and dS, each thread's first and second 32 columns. Two sets, for tiles in turn: a warp may hand over a tile
+    // while a slower one still has the tile before to hand over (never two: see where the next S and dP are asked for).
+    uint64_t p_full[2][2], ds_full[2][2];
     uint64_t fin, acc_free;                       // a piece's sums done, read
     uint64_t staged[2];                           // its output gone out through the staging slot (pieces in turn)
     uint64_t work_full[2], work_empty[2];
@@ -91,7 +102,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
     if (threadIdx.x == 0) {
         uint64_t *all = bar.a_full;
         for (int i = 0; i < static_cast<int>(offsetof(BwdBars, answer) / 8); ++i) mbar_init(&all[i], 1);
-        for (uint64_t *b : {&bar.p_full, &bar.ds_full, &bar.acc_free, &bar.staged[0], &bar.staged[1]}) mbar_init(b, 8);
+        for (int i = 0; i < 4; ++i) mbar_init(&bar.p_full[i >> 1][i & 1], 8), mbar_init(&bar.ds_full[i >> 1][i & 1], 8);
+        for (uint64_t *b : {&bar.dp_read, &bar.acc_free, &bar.staged[0], &bar.staged[1]}) mbar_init(b, 8);
         for (int i = 0; i < 2; ++i) mbar_init(&bar.work_empty[i], 9);
         bar.abort_flag = 0;
         fence_mbar_init();
@@ -109,7 +121,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // columns: dK/dV has S, dP, dV, dK; dQ has two S, dP, dQ
+    // TMEM columns: S (or two), dP, dV, dK; two S, dP, dQ
+    constexpr bool kTwoS = 3 * kTcTile + 2 * KS * 16 <= 512;   // room for two S beside dV and dK
+    constexpr uint32_t cP = kTwoS ? 256 : 128, cV = cP + 128, cK = kTwoS ? cV + KS * 16 : 384;   // dK/dV
+    constexpr uint32_t cP2 = 256, cQ = 384;                                                      // dQ
     const uint32_t tm = __shfl_sync(0xffffffffu, bar.tmem, 0);
     const TcWaits wait{&bar.abort_flag, a.status};
 
@@ -216,8 +231,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                             const int64_t st = h * a.stat_stride + static_cast<int64_t>(cur.slot + tile) * kTcTile;
                             float *dst = stats + (ns & 1) * 2 * kTcTile;
                             mbar_arrive_expect_tx(&bar.st_full[ns & 1], L::kStat);
-                            bulk_load(dst, a.lse2 + st, kTcTile * 4, &bar.st_full[ns & 1]);
-                            bulk_load(dst + kTcTile, a.delta + st, kTcTile * 4, &bar.st_full[ns & 1]);
+                            bulk_load(dst, a.nlse2 + st, kTcTile * 4, &bar.st_full[ns & 1]);
+                            bulk_load(dst + kTcTile, a.ndelta + st, kTcTile * 4, &bar.st_full[ns & 1]);
                         }
                         ++ns;
                     }
@@ -249,101 +264,129 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
         }
         __syncwarp();
     } else if (warp == 9) {
+        // One warp feeds the tensor core, and what it does between two products is on the chain that bounds the kernel:
+        // ring positions, phases and tokens left are counted along, descriptors are a base and a multiple.
         const uint32_t idS = idesc_f32acc(1, 128, 128, false, false), idG = idesc_f32acc(1, 128, KS * 16, false, true);
         const uint32_t idSn = idS | (a.scale < 0.f ? kIdescNegA : 0);
         const uint64_t d0 = tc_desc_k(f0), d1 = tc_desc_k(f1);
+        const uint64_t aK = tc_desc_k(sa), aM = tc_desc_mn(sa), bK = tc_desc_k(sb), bM = tc_desc_mn(sb);
+        constexpr uint32_t kStep = L::kTile >> 4;   // from slot to slot in a descriptor
         bool ok = true;
-        int na = 0, nb = 0, nf = 0, np = 0, nd = 0;   // tiles of each ring, pieces, P and dS tiles so far
-        int kind = BWD_NONE;                          // of the piece before
+        // Place in a ring and the phase of its barriers there.
+        struct Pos {
+            int i = 0;
+            uint32_t phase = 0;
+            __device__ __forceinline__ void next(int size) {
+                if (++i == size) i = 0, phase ^= 1;
+            }
+        };
+        Pos ra, rb, ua, ub;                     // next tile of the rings to multiply, and to sum over
+        uint32_t np = 0, pq = 0, nd = 0;        // tiles of P so far, phase of dP read, tiles of dS so far
+        int nf = 0;                             // pieces so far
+        int kind = BWD_NONE;                    // of the piece before
         for (int pieces = 0; ok; ++pieces) {
             if (!(ok = wait.all(&bar.work_full[pieces & 1], (pieces >> 1) & 1))) break;
             const BwdWork &w = bar.work[pieces & 1];
             const int k = __shfl_sync(0xffffffffu, w.kind, 0), n = __shfl_sync(0xffffffffu, w.n, 0),
                       olen = __shfl_sync(0xffffffffu, w.olen, 0), first = __shfl_sync(0xffffffffu, w.first, 0),
-                      per = __shfl_sync(0xffffffffu, w.per, 0);
+                      per = __shfl_sync(0xffffffffu, w.kind == BWD_DKV ? w.per : w.n, 0);
             if (lane == 0) mbar_arrive(&bar.work_empty[pieces & 1]);
             if (k == BWD_NONE) break;
             if (n == 0) continue;
             const bool dkv = k == BWD_DKV;
-            // the sums of the piece before have been read: needed before this piece's first sum, and before its first
-            // products where the kinds have their sums in different columns
-            bool free = nf == 0;
-            auto await_free = [&] {
-                if (!free) free = ok = wait.all(&bar.acc_free, (nf - 1) & 1);
-                return ok;
-            };
-            if (kind != k && !await_free()) break;
+            // The sums of the piece before have been read: needed before this piece's first sum, and before its first
+            // products where the kinds have their sums in different columns.
+            if (kind != k && nf > 0 && !(ok = wait.all(&bar.acc_free, (nf - 1) & 1))) break;
+            bool free = kind != k || nf == 0;
             kind = k;
             if (!(ok = wait.all(&bar.f_full, nf & 1))) break;
-            const uint32_t tP = dkv ? tm + 128 : tm + 256;
-            // tokens of the other side in tile j
-            auto tokens = [&](int j) { return min(kTcTile, olen - (dkv ? first + j % per : j) * kTcTile); };
-            auto scores = [&](int j) {
-                const int i = na + j, ai = i % L::kAs;
-                if (!wait.all(&bar.a_full[ai], (i / L::kAs) & 1)) return false;
-                uint8_t *tile = sa + ai * L::kTile;
-                const int left = tokens(j);
-                if (left < kTcTile) tc_zero_rows<NB>(tile, left);   // summed over below
-                const int buf = dkv ? 0 : j & 1;
+            const uint32_t tP = tm + (dkv ? cP : cP2);
+            const bool two = kTwoS || !dkv;     // S buffers
+            const int left0 = olen - first * kTcTile;
+            int sl = left0, sj = 0, dl = left0, dj = 0;   // tokens left in the head and tiles of it done, of S and of dP
+            int sbuf = 0, di = 0;                         // S buffer to write; dP tiles done
+            auto scores = [&] {
+                if (!wait.all(&bar.a_full[ra.i], ra.phase)) return false;
+                if (sl < kTcTile) tc_zero_rows<NB>(sa + ra.i * L::kTile, sl);   // summed over below
                 if (elect_one()) {
                     tc_fence_after();
-                    tc_mma_scores<KS>(tm + buf * 128, d0, tc_desc_k(tile), idSn);
-                    umma_commit(&bar.s_full[buf]);
+                    tc_mma_scores<KS>(tm + sbuf * 128, d0, aK + ra.i * kStep, idSn);
+                    umma_commit(&bar.s_full[sbuf]);
                 }
                 __syncwarp();
+                ra.next(L::kAs);
+                sl -= kTcTile;
+                if (++sj == per) sj = 0, sl = left0;
+                sbuf ^= two;
                 return true;
             };
-            auto dprobs = [&](int j) {
-                const int i = nb + j, bi = i % L::kBs;
-                if (!wait.all(&bar.b_full[bi], (i / L::kBs) & 1)) return false;
-                uint8_t *tile = sb + bi * L::kTile;
-                const int left = tokens(j);
-                if (left < kTcTile) tc_zero_rows<NB>(tile, left);
+            auto dprobs = [&] {
+                if (!wait.all(&bar.b_full[rb.i], rb.phase)) return false;
+                if (dl < kTcTile) tc_zero_rows<NB>(sb + rb.i * L::kTile, dl);
+                ++di;
                 if (elect_one()) {
                     tc_fence_after();
-                    tc_mma_scores<KS>(tP, d1, tc_desc_k(tile), idS);
-                    if (!dkv) umma_commit(&bar.b_empty[bi]);
-                    if (j + 1 == n) umma_commit(&bar.f_empty);   // the last use of the fixed tiles
+                    tc_mma_scores<KS>(tP, d1, bK + rb.i * kStep, idS);
                     umma_commit(&bar.dp_full);
+                    if (!dkv) umma_commit(&bar.b_empty[rb.i]);
+                    if (di == n) umma_commit(&bar.f_empty);   // the last use of the fixed tiles
                 }
                 __syncwarp();
+                rb.next(L::kBs);
+                dl -= kTcTile;
+                if (++dj == per) dj = 0, dl = left0;
                 return true;
             };
-            // acc (+)= A . tile over the tile's tokens, A in two halves of 64 tokens, 64 columns apart
-            auto sum = [&](uint32_t acc, uint32_t A, const uint8_t *tile, int j, uint64_t *release, bool last) {
+            // acc (+)= A . tile over the tile's tokens, A as it is handed over in two steps
+            auto sum = [&](uint32_t acc, uint32_t A, uint64_t tile, uint64_t (&sets)[2][2], uint32_t number, int j,
+                           uint64_t *release, bool last) {
+                uint64_t *full = sets[number & 1];
+                const uint32_t parity = (number >> 1) & 1;
+                if (!wait.all(&full[0], parity)) return false;
+                if (!free) {
+                    if (!wait.all(&bar.acc_free, (nf - 1) & 1)) return false;
+                    free = true;
+                }
                 if (elect_one()) {
                     tc_fence_after();
-                    tc_mma_tokens<true>(acc, A, tc_desc_mn(tile), idG, j > 0);
+                    tc_mma_tokens_chunk<0>(acc, A, tile, idG, j > 0);
+                }
+                __syncwarp();
+                if (!wait.all(&full[1], parity)) return false;
+                if (elect_one()) {
+                    tc_fence_after();
+                    tc_mma_tokens_chunk<1>(acc, A, tile, idG, true);
                     umma_commit(release);
                     if (last) umma_commit(&bar.fin);
                 }
                 __syncwarp();
+                return true;
             };
-            ok = scores(0) && dprobs(0);
+            ok = scores() && dprobs();
             if (dkv) {
                 for (int j = 0; ok && j < n; ++j) {
-                    const int ai = (na + j) % L::kAs, bi = (nb + j) % L::kBs;
-                    if (!(ok = wait.all(&bar.p_full, (np + j) & 1)) || !await_free()) break;
-                    sum(tm + 256, tm, sb + bi * L::kTile, j, &bar.b_empty[bi], false);
-                    if (j + 1 < n && !(ok = scores(j + 1))) break;
-                    if (!(ok = wait.all(&bar.ds_full, (nd + j) & 1))) break;
-                    sum(tm + 384, tP, sa + ai * L::kTile, j, &bar.a_empty[ai], j + 1 == n);
-                    if (j + 1 < n && !(ok = dprobs(j + 1))) break;
+                    const bool more = j + 1 < n;
+                    if (kTwoS && more && !(ok = scores())) break;
+                    if (!(ok = sum(tm + cV, tm + (kTwoS ? (j & 1) * 128 : 0), bM + ub.i * kStep, bar.p_full, np, j, &bar.b_empty[ub.i], false))) break;
+                    ub.next(L::kBs), ++np;
+                    if (!kTwoS && more && !(ok = scores())) break;
+                    if (!(ok = sum(tm + cK, tP, aM + ua.i * kStep, bar.ds_full, nd, j, &bar.a_empty[ua.i], !more))) break;
+                    ua.next(L::kAs), ++nd;
+                    if (more && !(ok = dprobs())) break;
                 }
-                np += n;
             } else {
                 for (int j = 0; ok && j < n; ++j) {
-                    const int ai = (na + j) % L::kAs;
-                    if (j + 1 < n && !(ok = scores(j + 1))) break;
-                    if (!(ok = wait.all(&bar.ds_full, (nd + j) & 1)) || !await_free()) break;
+                    const bool more = j + 1 < n;
+                    if (more && !(ok = scores())) break;
+                    if (!(ok = wait.all(&bar.dp_read, pq))) break;
+                    pq ^= 1;
                     tc_fence_after();
-                    if (j + 1 < n && !(ok = dprobs(j + 1))) break;
-                    sum(tm + 384, tm + (j & 1) * 128, sa + ai * L::kTile, j, &bar.a_empty[ai], j + 1 == n);
+                    if (more && !(ok = dprobs())) break;
+                    if (!(ok = sum(tm + cQ, tm + (j & 1) * 128, aM + ua.i * kStep, bar.ds_full, nd, j, &bar.a_empty[ua.i], !more))) break;
+                    ua.next(L::kAs), ++nd;
                 }
+                ub = rb;   // V is not summed over
             }
-            nd += n;
-            na += n;
-            nb += n;
             ++nf;
         }
         if (!ok && elect_one()) {   // let the MMAs issued so far finish
@@ -357,6 +400,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
         const int row = quarter * 32 + lane;
         const float sc = fmaxf(fabsf(a.scale_log2), 1.2e-38f);
         const f32x2 sc2 = both(sc);
+        // 32 columns of P or dS to the MMAs
+        auto hand_over = [&](uint32_t at, const uint32_t (&v)[16], uint64_t *full) {
+            tmem_st16(at, v);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
+        };
         bool ok = true;
         int na = 0, nf = 0, nd = 0, ns = 0, s0 = 0, s1 = 0;   // ring tiles, pieces, dS, statistics, S by buffer so far
         for (int pieces = 0; ok; ++pieces) {
@@ -385,79 +436,81 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                 continue;
             }
             if (dkv) {
-                const uint32_t tSh = tm + lane_base + half * 64, tPh = tSh + 128;
+                const uint32_t tPh = tm + cP + lane_base + half * 64;
                 const int key = w.t0 + row;
                 int qt = w.first;
-                for (int j = 0; j < w.n; ++j, ++nd, ++ns, ++s0) {
-                    const float4 *lse2 = reinterpret_cast<const float4 *>(stats + (ns & 1) * 2 * kTcTile + half * 64);
-                    const float4 *delta = lse2 + kTcTile / 4;
+                for (int j = 0; j < w.n; ++j, ++nd, ++ns) {
+                    const ulonglong2 *nlse2 = reinterpret_cast<const ulonglong2 *>(stats + (ns & 1) * 2 * kTcTile + half * 64);
+                    const ulonglong2 *ndelta = nlse2 + kTcTile / 4;   // packed pairs of fp32, as they lie
+                    const int buf = kTwoS ? j & 1 : 0;
+                    const uint32_t tSh = tm + buf * 128 + lane_base + half * 64;
+                    int &sn = buf ? s1 : s0;
                     if (!(ok = wait.all(&bar.st_full[ns & 1], (ns >> 1) & 1))) break;
-                    if (!(ok = wait.all(&bar.s_full[0], s0 & 1))) break;
+                    if (!(ok = wait.all(&bar.s_full[buf], sn & 1))) break;
+                    ++sn;
                     tc_fence_after();
-                    uint32_t s[2][32];
+                    uint32_t s[2][32], v[16];
                     tmem_ld32(tSh, s[0]);
                     tmem_ld32(tSh + 32, s[1]);
                     tmem_ld_wait();
-                    float p[64];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float4 l = lse2[i];
-                        const uint32_t *x = &s[i / 8][4 * (i % 8)];
-                        unpack2(fma2(pack2u(x[0], x[1]), sc2, pack2(-l.x, -l.y)), p[4 * i], p[4 * i + 1]);
-                        unpack2(fma2(pack2u(x[2], x[3]), sc2, pack2(-l.z, -l.w)), p[4 * i + 2], p[4 * i + 3]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) p[4 * i + e] = ex2(p[4 * i + e]);
-                    }
+                    float p[2][32];
                     // causal: query i sees the key from i = key - off on; the warp's last key is its tightest
-                    if (a.causal && qt * kTcTile < w.t0 + quarter * 32 + 31 - w.off) {
-                        const int lim = key - w.off - qt * kTcTile - half * 64;
+                    const bool cut = a.causal && qt * kTcTile < w.t0 + quarter * 32 + 31 - w.off;
+                    const int lim = key - w.off - qt * kTcTile - half * 64;
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (i < lim) p[i] = 0.f;
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const ulonglong2 l = nlse2[c * 8 + i];
+                            const uint32_t *x = &s[c][4 * i];
+                            unpack2(fma2(pack2u(x[0], x[1]), sc2, l.x), p[c][4 * i], p[c][4 * i + 1]);
+                            unpack2(fma2(pack2u(x[2], x[3]), sc2, l.y), p[c][4 * i + 2], p[c][4 * i + 3]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) p[c][4 * i + e] = ex2(p[c][4 * i + e]);
+                        }
+                        if (cut) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c * 32 + i < lim) p[c][i] = 0.f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = pack_bf16(p[c][2 * i], p[c][2 * i + 1]);
+                        hand_over(tSh + c * 16, v, &bar.p_full[ns & 1][c]);
                     }
-                    uint32_t v[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
-                    tmem_st32(tSh, v);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.p_full);
                     if (!(ok = wait.all(&bar.dp_full, nd & 1))) break;
                     tc_fence_after();
                     tmem_ld32(tPh, s[0]);
                     tmem_ld32(tPh + 32, s[1]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float4 d = delta[i];
-                        const uint32_t *x = &s[i / 8][4 * (i % 8)];
-                        float e, f;
-                        unpack2(mul2(pack2(p[4 * i], p[4 * i + 1]), add2(pack2u(x[0], x[1]), pack2(-d.x, -d.y))), e, f);
-                        v[2 * i] = pack_bf16(e, f);
-                        unpack2(mul2(pack2(p[4 * i + 2], p[4 * i + 3]), add2(pack2u(x[2], x[3]), pack2(-d.z, -d.w))), e, f);
-                        v[2 * i + 1] = pack_bf16(e, f);
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const ulonglong2 d = ndelta[c * 8 + i];
+                            const uint32_t *x = &s[c][4 * i];
+                            const float *y = &p[c][4 * i];
+                            float e, f;
+                            unpack2(mul2(pack2(y[0], y[1]), add2(pack2u(x[0], x[1]), d.x)), e, f);
+                            v[2 * i] = pack_bf16(e, f);
+                            unpack2(mul2(pack2(y[2], y[3]), add2(pack2u(x[2], x[3]), d.y)), e, f);
+                            v[2 * i + 1] = pack_bf16(e, f);
+                        }
+                        hand_over(tPh + c * 16, v, &bar.ds_full[nd & 1][c]);
                     }
-                    tmem_st32(tPh, v);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.ds_full);
                     if (++qt == w.first + w.per) qt = w.first;
                 }
             } else {
-                const uint32_t tPh = tm + 256 + lane_base + half * 64;
+                const uint32_t tPh = tm + cP2 + lane_base + half * 64;
                 const int last = w.t0 + row + w.off;   // causal: last key of the row
                 const int64_t at = w.head * a.stat_stride + static_cast<int64_t>(w.slot) * kTcTile + row;
-                const float lse2 = a.lse2[at], delta = a.delta[at];
-                const f32x2 nl2 = both(-lse2), nd2 = both(-delta);
+                const f32x2 nl2 = both(a.nlse2[at]), nd2 = both(a.ndelta[at]);
                 for (int j = 0; j < w.n; ++j, ++nd) {
                     const uint32_t tSj = tm + (j & 1) * 128 + lane_base + half * 64;
                     int &sn = j & 1 ? s1 : s0;
                     if (!(ok = wait.all(&bar.s_full[j & 1], sn & 1))) break;
                     ++sn;
                     tc_fence_after();
-                    uint32_t s[2][32];
+                    uint32_t s[2][32], v[16];
                     tmem_ld32(tSj, s[0]);
                     tmem_ld32(tSj + 32, s[1]);
                     tmem_ld_wait();
@@ -479,19 +532,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                     tmem_ld32(tPh, s[0]);
                     tmem_ld32(tPh + 32, s[1]);
                     tmem_ld_wait();
-                    uint32_t ds[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float e, f;
-                        unpack2(mul2(pack2(p[2 * i], p[2 * i + 1]),
-                                     add2(pack2u(s[i / 16][2 * (i % 16)], s[i / 16][2 * (i % 16) + 1]), nd2)), e, f);
-                        ds[i] = pack_bf16(e, f);
-                    }
-                    tmem_st32(tSj, ds);
-                    tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.ds_full);
+                    if (lane == 0) mbar_arrive(&bar.dp_read);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float e, f;
+                            unpack2(mul2(pack2(p[c * 32 + 2 * i], p[c * 32 + 2 * i + 1]), add2(pack2u(s[c][2 * i], s[c][2 * i + 1]), nd2)), e, f);
+                            v[i] = pack_bf16(e, f);
+                        }
+                        hand_over(tSj + c * 16, v, &bar.ds_full[nd & 1][c]);
+                    }
                 }
             }
             if (!ok || !(ok = wait.all(&bar.fin, nf & 1))) break;
@@ -505,11 +558,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                 if (lane == 0) mbar_arrive(&bar.acc_free);
             };
             if (dkv) {
-                tc_store_half<KS>(half, tile, tm + 256 + lane_base, 1.f, quarter * 32, w.rows, out0, ts0, a.D, [] {});
+                tc_store_half<KS>(half, tile, tm + cV + lane_base, 1.f, quarter * 32, w.rows, out0, ts0, a.D, [] {});
                 __syncwarp();
-                tc_store_half<KS>(half, tile, tm + 384 + lane_base, a.scale, quarter * 32, w.rows, out1, ts1, a.D, release);
+                tc_store_half<KS>(half, tile, tm + cK + lane_base, a.scale, quarter * 32, w.rows, out1, ts1, a.D, release);
             } else {
-                tc_store_half<KS>(half, tile, tm + 384 + lane_base, a.scale, quarter * 32, w.rows, out0, ts0, a.D, release);
+                tc_store_half<KS>(half, tile, tm + cQ + lane_base, a.scale, quarter * 32, w.rows, out0, ts0, a.D, release);
             }
             fence_proxy_async_smem();   // the slot goes back to the loads
             __syncwarp();

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
                 if (!(ok = wait.all(&bar.p_full, kv & 1))) break;
                 if (elect_one()) {
                     tc_fence_after();
-                    tc_mma_tokens<true>(tO, tS, dv, idO, j > 0);
+                    tc_mma_tokens(tO, tS, dv, idO, j > 0);
                     if (j + 1 < n) umma_commit(&bar.v_empty);
                     umma_commit(&bar.o_done);
                 }

@@ -183,12 +183,12 @@ __device__ __forceinline__ void simt_probs(const AttnArgs &a, const float *Q, co
     for (int i = 0; i < 4; ++i) {
         const int r = ty * 4 + i;
         const int lim = a.causal ? min(keys, q0 + r + off + 1 - k0) : keys;
-        const float lse2 = stat[r], delta = stat[kSimtTile + r];
+        const float nlse2 = stat[r], ndelta = stat[kSimtTile + r];
         for (int j = 0; j < 4; ++j) {
             const int c = tx + 16 * j;
-            const float p = c < lim ? exp2f(fmaf(s[i][j], a.scale_log2, -lse2)) : 0.f;
+            const float p = c < lim ? exp2f(fmaf(s[i][j], a.scale_log2, nlse2)) : 0.f;
             if (P) P[r * kSimtP + c] = p;
-            dS[r * kSimtP + c] = c < lim ? p * (d[i][j] - delta) : 0.f;
+            dS[r * kSimtP + c] = c < lim ? p * (d[i][j] + ndelta) : 0.f;
         }
     }
 }
@@ -209,8 +209,8 @@ __device__ __forceinline__ void dq_block_simt(const AttnArgs &a, float *sm, int 
     simt_load<DP>(G, static_cast<const float *>(a.dO) + tok * a.dO_ts + h * a.dO_hs, a.dO_ts, rows, a.D);
     if (tid < kSimtTile) {
         const int64_t at = h * a.stat_stride + static_cast<int64_t>(slot) * kSimtTile + tid;
-        stat[tid] = a.lse2[at];
-        stat[kSimtTile + tid] = a.delta[at];
+        stat[tid] = a.nlse2[at];
+        stat[kSimtTile + tid] = a.ndelta[at];
     }
     float acc[4][DP / 16] = {};
     for (int k0 = 0; k0 < kend; k0 += kSimtTile) {
@@ -252,8 +252,8 @@ __device__ __forceinline__ void dkv_block_simt(const AttnArgs &a, float *sm, int
             simt_load<DP>(G, static_cast<const float *>(a.dO) + qt * a.dO_ts + h * a.dO_hs, a.dO_ts, rows, a.D);
             if (tid < kSimtTile) {
                 const int64_t at = h * a.stat_stride + static_cast<int64_t>(qslot0 + q0 / kSimtTile) * kSimtTile + tid;
-                stat[tid] = a.lse2[at];
-                stat[kSimtTile + tid] = a.delta[at];
+                stat[tid] = a.nlse2[at];
+                stat[kSimtTile + tid] = a.ndelta[at];
             }
             __syncthreads();
             simt_probs<DP>(a, Q, K, G, V, stat, q0, t.t0, keys, off, ty, tx, P, dS);
