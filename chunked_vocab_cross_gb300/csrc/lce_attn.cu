@@ -87,14 +87,31 @@ lce_status_t encode(CUtensorMap *m, const HostDev &dev, const void *p, int64_t T
     return r == CUDA_SUCCESS ? LCE_OK : LCE_ERR_SHAPE;
 }
 
-template <auto kKernel, typename... A>
+// kEarly: the launch may begin before the one ahead of it in the stream has
+// ended, and waits in the kernel where it reads what that one wrote.
+template <auto kKernel, bool kEarly = false, typename... A>
 lce_status_t launch(const HostDev &dev, int64_t blocks, int threads, int smem, cudaStream_t st, const A &...args) {
     if (blocks >= (int64_t(1) << 31)) return LCE_ERR_SHAPE;
     if (smem > 48 * 1024) {
         const lce_status_t s = host_smem<kKernel>(dev, smem);
         if (s != LCE_OK) return s;
     }
-    kKernel<<<static_cast<unsigned>(blocks), threads, smem, st>>>(args...);
+    if constexpr (kEarly) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        const lce_status_t s = host_cuda(cudaLaunchKernelEx(&cfg, kKernel, args...));
+        if (s != LCE_OK) return s;
+    } else {
+        kKernel<<<static_cast<unsigned>(blocks), threads, smem, st>>>(args...);
+    }
     return host_launched();
 }
 
@@ -145,7 +162,7 @@ lce_status_t backward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &
     if (s == LCE_OK) s = encode(&maps.dO, dev, a->dO, a->Tq, a->Hq, a->D, a->dO_ts, a->dO_hs);
     if (s == LCE_OK) s = row_stats<__nv_bfloat16, kTcTile>(r, dev, st);
     if (s != LCE_OK) return s;
-    return launch<k_attn_bwd<KS>>(dev, dq + dkv, kBwdThreads, BwdSmem<KS>::kBytes, st, r, maps, static_cast<int>(dkv));
+    return launch<k_attn_bwd<KS>, true>(dev, dq + dkv, kBwdThreads, BwdSmem<KS>::kBytes, st, r, maps, static_cast<int>(dkv));
 }
 
 // The tensor-core kernels exist for 64, 80, 96 and 128 channels; others run as the next of these.

@@ -60,16 +60,49 @@ struct TileInfo {
     int o0, olen;      // first token and length of the sequence on the other side (tail: empty)
 };
 
+// Starts of the sequences lo + lane of both sides (the last token past B): what
+// the last step of a search needs.
+struct SeqStarts {
+    int lo, n;        // sequences lo .. lo + n - 1 may be the one, n <= 31
+    int own, other;
+};
+__device__ __forceinline__ SeqStarts load_starts(const SeqMap &own, const SeqMap &other, int lo, int n) {
+    const int lane = threadIdx.x & 31, b = lo + lane;
+    const bool in = lane <= n && b <= own.B;
+    return SeqStarts{lo, n, in ? own.start(b) : own.T, in ? other.start(b) : other.T};
+}
+
+// The tile of `slot` among the sequences of `st`: the largest b with
+// slot_base(b) <= slot. No memory is read.
+template <int TILE>
+__device__ __forceinline__ TileInfo tile_among(const SeqMap &own, const SeqMap &other, const SeqStarts &st, int slot) {
+    const int lane = threadIdx.x & 31, b = st.lo + lane;
+    const unsigned mask = __ballot_sync(0xffffffffu, lane < st.n && b <= own.B && st.own / TILE + b <= slot);
+    const int hit = mask ? 31 - __clz(mask) : 0;
+    TileInfo t;
+    t.b = st.lo + hit;
+    t.s0 = __shfl_sync(0xffffffffu, st.own, hit);
+    t.o0 = __shfl_sync(0xffffffffu, st.other, hit);
+    // the end: the next sequence's start, or (the tail) the last token
+    const int e = __shfl_sync(0xffffffffu, st.own, (hit + 1) & 31), oe = __shfl_sync(0xffffffffu, st.other, (hit + 1) & 31);
+    const bool tail = t.b >= own.B;
+    t.len = (tail ? own.T : max(e, t.s0)) - t.s0;
+    t.olen = tail ? 0 : max(oe, t.o0) - t.o0;
+    t.t0 = (slot - (t.s0 / TILE + t.b)) * TILE;
+    return t;
+}
+
+constexpr int kFewSeqs = 30;   // sequences whose starts, and the tail's, fit one load by a warp
+
 // The tile of `slot`: its sequence is the largest b in [0, B] with
 // slot_base(b) <= slot. All 32 lanes take part, each probing one of 32 points
-// of what is left, so 1024 sequences take two rounds of loads; in the last
-// round the probes are neighbours and hold the sequence's start and end too.
-// Blocks begin with this, so what counts is the number of dependent loads.
+// of what is left, so 1024 sequences take two rounds of loads; the last 31
+// sequences' starts then say everything.
 template <int TILE>
 __device__ __forceinline__ TileInfo tile_info(const SeqMap &own, const SeqMap &other, int slot) {
     const int lane = threadIdx.x & 31;
     int lo = 0, n = own.B + 1;
-    while (n > 31) {
+    while (n > kFewSeqs + 1) {
         const int step = (n + 31) / 32;
         const int off = lane * step;
         const bool le = off < n && slot_base<TILE>(own, lo + off) <= slot;
@@ -80,24 +113,23 @@ __device__ __forceinline__ TileInfo tile_info(const SeqMap &own, const SeqMap &o
         n = min(step, n - hit * step);
         if (step == 1) break;
     }
-    // sequences lo .. lo + n - 1 are left, n <= 31 (or one): lane i has the start of sequence lo + i
-    const int b = lo + lane;
-    const bool in = lane <= n && b <= own.B;
-    const int s = in ? own.start(b) : own.T, o = in ? other.start(b) : other.T;
-    const unsigned mask = __ballot_sync(0xffffffffu, lane < n && in && s / TILE + b <= slot);
-    const int hit = mask ? 31 - __clz(mask) : 0;
-    TileInfo t;
-    t.b = lo + hit;
-    t.s0 = __shfl_sync(0xffffffffu, s, hit);
-    t.o0 = __shfl_sync(0xffffffffu, o, hit);
-    // the end: the next sequence's start, or (the tail) the last token
-    const int e = __shfl_sync(0xffffffffu, s, (hit + 1) & 31), oe = __shfl_sync(0xffffffffu, o, (hit + 1) & 31);
-    const bool tail = t.b >= own.B;
-    t.len = (tail ? own.T : max(e, t.s0)) - t.s0;
-    t.olen = tail ? 0 : max(oe, t.o0) - t.o0;
-    t.t0 = (slot - (t.s0 / TILE + t.b)) * TILE;
-    return t;
+    return tile_among<TILE>(own, other, load_starts(own, other, lo, n), slot);
 }
+
+// The same for a warp that looks for many tiles: a few sequences' starts are
+// kept in its registers.
+template <int TILE>
+struct TileFinder {
+    const SeqMap &q, &k;
+    SeqStarts st;
+    __device__ __forceinline__ TileFinder(const SeqMap &q_, const SeqMap &k_) : q(q_), k(k_), st(load_starts(q_, k_, 0, min(q_.B, kFewSeqs) + 1)) {}
+    __device__ __forceinline__ TileInfo of_q(int slot) const {
+        return q.B <= kFewSeqs ? tile_among<TILE>(q, k, st, slot) : tile_info<TILE>(q, k, slot);
+    }
+    __device__ __forceinline__ TileInfo of_k(int slot) const {
+        return q.B <= kFewSeqs ? tile_among<TILE>(k, q, SeqStarts{0, st.n, st.other, st.own}, slot) : tile_info<TILE>(k, q, slot);
+    }
+};
 
 // Offsets must ascend from 0 within the tokens; one warp of one block looks.
 __device__ __forceinline__ void check_offsets(const SeqMap &m, int *status) {

@@ -129,10 +129,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
     const TcWaits wait{&bar.abort_flag, a.status};
 
     if (warp == 8) {
+        const TileFinder<kTcTile> finder(a.sq, a.sk);
         auto find = [&](int block) {
             BwdWork w{};
             if (block < dkv_blocks) {   // under a causal mask the first key tiles have the most queries
-                const TileInfo t = tile_info<kTcTile>(a.sk, a.sq, block / a.Hk);
+                const TileInfo t = finder.of_k(block / a.Hk);
                 w.kind = BWD_DKV;
                 w.head = block % a.Hk;
                 w.rows = t.t0 < 0 ? 0 : max(0, min(kTcTile, t.len - t.t0));
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
             } else {                    // ... and the last query tiles the most keys
                 block -= dkv_blocks;
                 const int slot = (gridDim.x - dkv_blocks) / a.Hq - 1 - block / a.Hq;
-                const TileInfo t = tile_info<kTcTile>(a.sq, a.sk, slot);
+                const TileInfo t = finder.of_q(slot);
                 w.kind = BWD_DQ;
                 w.head = block % a.Hq;
                 w.rows = t.t0 < 0 ? 0 : max(0, min(kTcTile, t.len - t.t0));
@@ -177,6 +178,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
         };
         bool asked = false;   // a request for the next block is in flight
         int answers = 0;
+        auto request = [&] {
+            if (lane == 0) {
+                fence_proxy_async_smem();   // the last answer has been read
+                clc_request(&bar.answer, &bar.clc);
+            }
+            __syncwarp();
+            asked = true;
+        };
         BwdWork cur = find(blockIdx.x);
         publish(cur);
         while (ok && cur.kind != BWD_NONE) {
@@ -199,13 +208,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                 // The next piece is asked for when this one's last loads but one are due: late, so that a CTA with
                 // a long piece does not hold another that an idle one could start (asked for at the start, a
                 // backward of 250 pieces on 152 SMs took 47 us instead of 35), and early enough for it to be found.
-                if (j == max(0, cur.n - 2)) {
-                    if (lane == 0) {
-                        fence_proxy_async_smem();   // the last answer has been read
-                        clc_request(&bar.answer, &bar.clc);
-                    }
-                    asked = true;
-                }
+                if (j == max(0, cur.n - 2)) request();
                 if (j < cur.n) {
                     const int ai = na % L::kAs, bi = nb % L::kBs, at = cur.o0 + tile * kTcTile;
                     if (!await_staged(need[ai])) break;
@@ -228,6 +231,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                         if (p >= 0 && p > c - L::kAs && !(ok = wait.all(&bar.a_empty[p % L::kAs], (p / L::kAs) & 1))) break;
                         ((ns & 1) ? stat1 : stat0) = c;
                         if (lane == 0) {
+                            griddep_wait();   // the statistics come from the launch before
                             const int64_t st = h * a.stat_stride + static_cast<int64_t>(cur.slot + tile) * kTcTile;
                             float *dst = stats + (ns & 1) * 2 * kTcTile;
                             mbar_arrive_expect_tx(&bar.st_full[ns & 1], L::kStat);
@@ -240,13 +244,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                     if (dkv && tile == cur.first + cur.per) tile = cur.first, ++h;
                 }
                 if (j + 1 == steps) {
-                    if (!(ok = wait.all(&bar.clc, answers & 1))) break;
-                    ++answers;
-                    asked = false;
-                    const int block = __shfl_sync(0xffffffffu, clc_answer(&bar.answer), 0);
-                    if (block >= 0) next = find(block);
-                    else next.kind = BWD_NONE;
-                    publish(next);
+                    for (;;) {
+                        if (!(ok = wait.all(&bar.clc, answers & 1))) break;
+                        ++answers;
+                        asked = false;
+                        const int block = __shfl_sync(0xffffffffu, clc_answer(&bar.answer), 0);
+                        if (block >= 0) next = find(block);
+                        else next.kind = BWD_NONE;
+                        if (next.kind == BWD_NONE || next.rows > 0) break;
+                        request();   // an empty slot: one more
+                    }
+                    if (ok) publish(next);
                     if (!ok) break;
                 }
             }
@@ -503,6 +511,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                 const uint32_t tPh = tm + cP2 + lane_base + half * 64;
                 const int last = w.t0 + row + w.off;   // causal: last key of the row
                 const int64_t at = w.head * a.stat_stride + static_cast<int64_t>(w.slot) * kTcTile + row;
+                griddep_wait();   // the statistics come from the launch before
                 const f32x2 nl2 = both(a.nlse2[at]), nd2 = both(a.ndelta[at]);
                 for (int j = 0; j < w.n; ++j, ++nd) {
                     const uint32_t tSj = tm + (j & 1) * 128 + lane_base + half * 64;
@@ -570,6 +579,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
         }
         tc_fence_before();
     }
+    griddep_wait();   // also where nothing was read of the launch before: the grid must not end ahead of it
     __syncthreads();
     if (warp == 9) {
         tc_fence_after();

@@ -50,7 +50,8 @@ struct FwdBars {
     uint64_t k_full, k_empty, v_full, v_empty;   // loads of K and V tiles (v_empty: of all but a work tile's last)
     uint64_t staged;                             // O has gone out through V's slot
     uint64_t q_full, q_empty;                    // loads of Q
-    uint64_t s_full, p_full, o_done, o_free;     // S and P, an O step done, O read
+    uint64_t s_full, p_full[2];                  // S; P, each thread's first and second 32 keys
+    uint64_t o_done, o_free;                     // an O step done, O read
     uint64_t work_full[2], work_empty[2];
     uint64_t clc, fin;
     uint4 answer;
@@ -75,7 +76,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
         uint64_t *one[] = {&bar.k_full, &bar.k_empty, &bar.v_full, &bar.v_empty, &bar.q_full, &bar.q_empty, &bar.s_full,
                            &bar.o_done, &bar.work_full[0], &bar.work_full[1], &bar.clc, &bar.fin};
         for (uint64_t *b : one) mbar_init(b, 1);
-        mbar_init(&bar.p_full, 8);
+        mbar_init(&bar.p_full[0], 8);
+        mbar_init(&bar.p_full[1], 8);
         mbar_init(&bar.o_free, 8);
         mbar_init(&bar.staged, 8);
         for (int i = 0; i < 2; ++i) mbar_init(&bar.work_empty[i], 9);
@@ -99,6 +101,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
     const TcWaits wait{&bar.abort_flag, a.status};
 
     if (warp == 8) {
+        const TileFinder<kTcTile> finder(a.sq, a.sk);
         // longest rows first: under a causal mask the last tiles have the most keys
         auto find = [&](int block) {
             if (block == 0) {
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
             }
             FwdWork w{};
             w.h = block % a.Hq;
-            const TileInfo t = tile_info<kTcTile>(a.sq, a.sk, gridDim.x / a.Hq - 1 - block / a.Hq);
+            const TileInfo t = finder.of_q(gridDim.x / a.Hq - 1 - block / a.Hq);
             const int off = t.olen - t.len;   // causal: row i sees keys [0, i + off]
             w.rows = t.t0 < 0 ? 0 : max(0, min(kTcTile, t.len - t.t0));
             const int kend = a.causal ? min(t.olen, t.t0 + w.rows + off) : t.olen;
@@ -131,6 +134,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
         };
         bool asked = false;   // a request for the next block is in flight
         int answers = 0;
+        auto request = [&] {
+            if (lane == 0) {
+                fence_proxy_async_smem();   // the last answer has been read
+                clc_request(&bar.answer, &bar.clc);
+            }
+            __syncwarp();
+            asked = true;
+        };
         FwdWork cur = find(blockIdx.x);
         publish(cur);
         int kl = 0, vl = 0;   // loads issued
@@ -149,13 +160,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
             for (int j = 0; j < steps; ++j) {
                 // the next tile is asked for when this one's last loads but one are due: late enough not to hold work
                 // that an idle CTA could start, early enough for it to be found
-                if (j == max(0, cur.n - 2)) {
-                    if (lane == 0) {
-                        fence_proxy_async_smem();   // the last answer has been read
-                        clc_request(&bar.answer, &bar.clc);
-                    }
-                    asked = true;
-                }
+                if (j == max(0, cur.n - 2)) request();
                 if (j < cur.n) {
                     const int at = cur.ktok + j * kTcTile;
                     if (!(ok = wait.all(&bar.k_empty, (kv & 1) ^ 1))) break;
@@ -174,13 +179,17 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
                     ++kv;
                 }
                 if (j + 1 == steps) {
-                    if (!(ok = wait.all(&bar.clc, answers & 1))) break;
-                    ++answers;
-                    asked = false;
-                    const int block = __shfl_sync(0xffffffffu, clc_answer(&bar.answer), 0);
-                    if (block >= 0) next = find(block);
-                    else next.h = -1;
-                    publish(next);
+                    for (;;) {
+                        if (!(ok = wait.all(&bar.clc, answers & 1))) break;
+                        ++answers;
+                        asked = false;
+                        const int block = __shfl_sync(0xffffffffu, clc_answer(&bar.answer), 0);
+                        if (block >= 0) next = find(block);
+                        else next.h = -1;
+                        if (next.h < 0 || next.rows > 0) break;
+                        request();   // an empty slot: one more
+                    }
+                    if (ok) publish(next);
                     if (!ok) break;
                 }
             }
@@ -222,10 +231,16 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
                 const int keys = min(kTcTile, left - j * kTcTile);
                 if (keys < kTcTile) tc_zero_rows<NB>(sv, keys);
                 if (j == 0 && !(ok = wait.all(&bar.o_free, (qs & 1) ^ 1))) break;   // the O before has been read
-                if (!(ok = wait.all(&bar.p_full, kv & 1))) break;
+                if (!(ok = wait.all(&bar.p_full[0], kv & 1))) break;
                 if (elect_one()) {
                     tc_fence_after();
-                    tc_mma_tokens(tO, tS, dv, idO, j > 0);
+                    tc_mma_tokens_chunk<0>(tO, tS, dv, idO, j > 0);
+                }
+                __syncwarp();
+                if (!(ok = wait.all(&bar.p_full[1], kv & 1))) break;
+                if (elect_one()) {
+                    tc_fence_after();
+                    tc_mma_tokens_chunk<1>(tO, tS, dv, idO, true);
                     if (j + 1 < n) umma_commit(&bar.v_empty);
                     umma_commit(&bar.o_done);
                 }
@@ -332,20 +347,24 @@ __global__ void __launch_bounds__(kFwdThreads, 2) k_attn_fwd(const __grid_consta
                     m = next;
                 }
                 const f32x2 base = both(m == -INFINITY ? 0.f : -m * sc), sc2 = both(sc);
-                uint32_t p[32];
+                // P in two steps, so that the first half of O's step runs under the second half of the exponents
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float x, y;
-                    unpack2(fma2(pack2u(s[i / 16][2 * (i % 16)], s[i / 16][2 * (i % 16) + 1]), sc2, base), x, y);
-                    x = ex2(x), y = ex2(y);
-                    l2 = add2(l2, pack2(x, y));
-                    p[i] = pack_bf16(x, y);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x, y;
+                        unpack2(fma2(pack2u(s[c][2 * i], s[c][2 * i + 1]), sc2, base), x, y);
+                        x = ex2(x), y = ex2(y);
+                        l2 = add2(l2, pack2(x, y));
+                        p[i] = pack_bf16(x, y);
+                    }
+                    tmem_st16(tSh + c * 16, p);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.p_full[c]);
                 }
-                tmem_st32(tSh, p);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.p_full);
             }
             if (!ok) break;
             if (!(ok = wait.all(&bar.o_done, (kv - 1) & 1))) {

@@ -117,14 +117,9 @@ __device__ __forceinline__ void tc_mma_scores(uint32_t d, uint64_t a, uint64_t b
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) umma_f16(d, a + tc_step_k(kk), b + tc_step_k(kk), idesc, kk > 0);
 }
-// D (+)= P . B over 128 tokens: P in tensor memory (two tokens a column), the
+// D (+)= P . B over tokens: P in tensor memory (two tokens a column), the
 // shares of the two threads of a row (64 tokens) 64 columns apart; B a tile.
-__device__ __forceinline__ void tc_mma_tokens(uint32_t d, uint32_t p, uint64_t b, uint32_t idesc, bool accumulate) {
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-        umma_f16_ts(d, p + (kk >> 2) * 64 + (kk & 3) * 8, b + tc_step_mn(kk), idesc, accumulate || kk > 0);
-}
-// The same for the first (kChunk = 0) or second 32 tokens of each share alone.
+// The first (kChunk = 0) or the second 32 tokens of each share.
 template <int kChunk>
 __device__ __forceinline__ void tc_mma_tokens_chunk(uint32_t d, uint32_t p, uint64_t b, uint32_t idesc, bool accumulate) {
 #pragma unroll
