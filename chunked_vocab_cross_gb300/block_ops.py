@@ -10,7 +10,6 @@ to be ready there (and stay alive until that stream is done with them)."""
 from __future__ import annotations
 
 import array
-import contextlib
 import functools
 import operator
 
@@ -19,19 +18,23 @@ import torch
 from . import _abi
 
 _DT = {torch.bfloat16: _abi.LCE_BF16, torch.float32: _abi.LCE_FP32}
-_NOTHING = contextlib.nullcontext()
 _ATTN, _NORM = _abi.packer(_abi.LceAttn), _abi.packer(_abi.LceNorm)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on(stream):
-    """Allocations inside belong to `stream` (None: the current one)."""
-    return _NOTHING if stream is None else torch.cuda.stream(stream)
+def _on_stream(call):
+    """With `stream` given, the call runs with that stream as the current one:
+    its allocations belong to it and its launches go there."""
+    @functools.wraps(call)
+    def wrapped(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return wrapped
 
 
-def _stream(stream, index: int) -> int:
-    if stream is not None:
-        return stream.cuda_stream
+def _stream(index: int) -> int:
     return _current_stream(index) if _current_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
@@ -51,22 +54,23 @@ def _like(t):
 
 # ------------------------------------------------------------------ attention
 
-def _tokens(name, t, ref, shape=None):
+def _tokens(name, t, device, dtype, shape=None):
     """(address, token stride, head stride) of a [T, heads, D] tensor, or of a
     [B, L, heads, D] one as [B*L, heads, D]. A dimension of one entry has no
     stride of its own."""
-    if t.device != ref.device or t.dtype != ref.dtype:
+    sh = t.shape
+    if t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor with q's device and dtype (there is no CPU path)")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    st, sh = t.stride(), t.shape
-    if st[-1] != 1 and sh[-1] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if shape is not None and sh != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(sh)}")
+    st = t.stride()
     H, D = sh[-2], sh[-1]
+    if st[-1] != 1 and D > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
     hs = st[-2] if H > 1 else D
     if len(sh) == 4:
         B, L = sh[0], sh[1]
-        if B > 1 and L > 0 and st[0] != (L * st[1] if L > 1 else st[0]):
+        if B > 1 and L > 1 and st[0] != L * st[1]:
             raise ValueError(f"{name}: the rows of a [B, L, heads, D] tensor must be evenly spaced over B and L")
         ts = st[1] if L > 1 else st[0] if B > 1 else H * D
     else:
@@ -113,52 +117,65 @@ def attention_workspace_size(Tq: int, Tk: int, Hq: int, Hk: int, D: int, batch: 
     return int(_abi.lib().lce_attention_workspace_size(_abi.ctypes.byref(a)))
 
 
-def attention_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, *, causal: bool = True, scale=None, out=None,
-                      stream=None):
+@_on_stream
+def attention_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, *, causal: bool = True, scale=None, out=None):
     """(o, lse) of softmax attention over packed sequences: q [Tq, heads, D],
     k and v [Tk, kv_heads, D] with int32 token offsets of the sequences (one
     sequence without them), or [B, L, heads, D] tensors of equal lengths. o has
     q's shape and dtype, lse is fp32 [heads, tokens]; rows that see no key get
-    o = 0 and lse = -inf. `scale` is D**-0.5 if not given; `out` receives o."""
+    o = 0 and lse = -inf. `scale` is D**-0.5 if not given; `out` receives o;
+    `stream`: the stream to run on (the current one if not given)."""
     B, Tq, Tk, Hq, Hk, D, pcq, pck = _sequences(q, k, v, cu_seqlens_q, cu_seqlens_k)
-    pq, pk, pv = _tokens("q", q, q), _tokens("k", k, q), _tokens("v", v, q)
-    device = q.device
-    with _on(stream):
-        if out is None:
-            out = _like(q)
-        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=device)
-        po = _tokens("out", out, q, q.shape)
-        args = _ATTN.pack(_DT[q.dtype], 1 if causal else 0, D ** -0.5 if scale is None else scale, B, Tq, Tk, Hq, Hk, D,
-                          pcq, pck, pq[0], pk[0], pv[0], pq[1], pq[2], pk[1], pk[2], pv[1], pv[2], po[0], po[1], po[2],
-                          lse.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, _stream(stream, device.index))
-        _abi.check(_abi.lib().lce_attention_forward(args), "lce_attention_forward")
+    device, dtype = q.device, q.dtype
+    pq, pk, pv = _tokens("q", q, device, dtype), _tokens("k", k, device, dtype), _tokens("v", v, device, dtype)
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype, device=device)
+        po, ots, ohs = out.data_ptr(), Hq * D, D
+    else:
+        po, ots, ohs = _tokens("out", out, device, dtype, q.shape)
+    lse = torch.empty((Hq, Tq), dtype=torch.float32, device=device)
+    args = _ATTN.pack(_DT[dtype], 1 if causal else 0, D ** -0.5 if scale is None else scale, B, Tq, Tk, Hq, Hk, D,
+                      pcq, pck, pq[0], pk[0], pv[0], pq[1], pq[2], pk[1], pk[2], pv[1], pv[2], po, ots, ohs,
+                      lse.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, _stream(device.index))
+    _abi.check(_abi.lib().lce_attention_forward(args), "lce_attention_forward")
     return out, lse
 
 
+@_on_stream
 def attention_backward(do, q, k, v, o, lse, cu_seqlens_q=None, cu_seqlens_k=None, *, causal: bool = True, scale=None,
-                       dq=None, dk=None, dv=None, workspace=None, stream=None):
+                       dq=None, dk=None, dv=None, workspace=None):
     """(dq, dk, dv) from the forward's inputs, its o and lse, and the gradient
     `do` of o; the probabilities are recomputed. dq, dk and dv may be given
     (strided slices of one gradient, say). `workspace`: a uint8 CUDA tensor of
-    at least attention_workspace_size bytes."""
+    at least attention_workspace_size bytes; `stream`: the stream to run on."""
     B, Tq, Tk, Hq, Hk, D, pcq, pck = _sequences(q, k, v, cu_seqlens_q, cu_seqlens_k)
-    pq, pk, pv = _tokens("q", q, q), _tokens("k", k, q), _tokens("v", v, q)
-    pg, po = _tokens("do", do, q, q.shape), _tokens("o", o, q, q.shape)
-    device = q.device
+    device, dtype = q.device, q.dtype
+    pq, pk, pv = _tokens("q", q, device, dtype), _tokens("k", k, device, dtype), _tokens("v", v, device, dtype)
+    pg, po = _tokens("do", do, device, dtype, q.shape), _tokens("o", o, device, dtype, q.shape)
     if lse.dtype != torch.float32 or lse.shape != (Hq, Tq) or not lse.is_contiguous() or lse.device != device:
         raise ValueError("lse must be the forward's contiguous fp32 [heads, tokens] tensor")
-    with _on(stream):
-        dq = _like(q) if dq is None else dq
-        dk = _like(k) if dk is None else dk
-        dv = _like(v) if dv is None else dv
-        px, py, pz = _tokens("dq", dq, q, q.shape), _tokens("dk", dk, q, k.shape), _tokens("dv", dv, q, k.shape)
-        ws, size, keep = _scratch(workspace, attention_workspace_size(Tq, Tk, Hq, Hk, D, B, q.dtype), device)
-        args = _ATTN.pack(_DT[q.dtype], 1 if causal else 0, D ** -0.5 if scale is None else scale, B, Tq, Tk, Hq, Hk, D,
-                          pcq, pck, pq[0], pk[0], pv[0], pq[1], pq[2], pk[1], pk[2], pv[1], pv[2], po[0], po[1], po[2],
-                          lse.data_ptr(), pg[0], pg[1], pg[2], px[0], py[0], pz[0], px[1], px[2], py[1], py[2], pz[1],
-                          pz[2], ws, size, _stream(stream, device.index))
-        _abi.check(_abi.lib().lce_attention_backward(args), "lce_attention_backward")
-        del keep
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=dtype, device=device)
+        px = dq.data_ptr(), Hq * D, D
+    else:
+        px = _tokens("dq", dq, device, dtype, q.shape)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=dtype, device=device)
+        py = dk.data_ptr(), Hk * D, D
+    else:
+        py = _tokens("dk", dk, device, dtype, k.shape)
+    if dv is None:
+        dv = torch.empty(k.shape, dtype=dtype, device=device)
+        pz = dv.data_ptr(), Hk * D, D
+    else:
+        pz = _tokens("dv", dv, device, dtype, k.shape)
+    ws, size, keep = _scratch(workspace, attention_workspace_size(Tq, Tk, Hq, Hk, D, B, dtype), device)
+    args = _ATTN.pack(_DT[dtype], 1 if causal else 0, D ** -0.5 if scale is None else scale, B, Tq, Tk, Hq, Hk, D,
+                      pcq, pck, pq[0], pk[0], pv[0], pq[1], pq[2], pk[1], pk[2], pv[1], pv[2], po[0], po[1], po[2],
+                      lse.data_ptr(), pg[0], pg[1], pg[2], px[0], py[0], pz[0], px[1], px[2], py[1], py[2], pz[1],
+                      pz[2], ws, size, _stream(device.index))
+    _abi.check(_abi.lib().lce_attention_backward(args), "lce_attention_backward")
+    del keep
     return dq, dk, dv
 
 
@@ -229,47 +246,49 @@ def block_norm_workspace_size(N: int, d: int) -> int:
     return int(_abi.lib().lce_block_norm_workspace_size(_abi.ctypes.byref(a)))
 
 
+@_on_stream
 def block_norm_forward(x, b=None, *, w_post=None, gate=None, w_pre=None, scale: float = 1.0, eps: float = 1e-6,
-                       out_r=None, stream=None):
+                       out_r=None):
     """(r, n, rstd_post, rstd_pre) for the residual stream x [N, d] and a
     block's output b [N, d]:
         r = x + scale * gate * rms_norm(b) * w_post,   n = rms_norm(r) * w_pre
     with gate [d] or [N, d]; any of w_post, gate and w_pre may be None (n and
     the matching rstd are None then). Without b, r is x itself. `out_r`
-    receives r and may be x (the stream updated in place)."""
+    receives r and may be x (the stream updated in place); `stream`: the stream
+    to run on (the current one if not given)."""
     dtype, N, d, pb, p_post, pg, p_pre, full = _norm_inputs(x, b, w_post, gate, w_pre)
     px = _rows("x", x, x)
     device = x.device
-    with _on(stream):
-        r, n, rstd_post, rstd_pre = x, None, None, None
-        pr = pn = ps_post = ps_pre = 0
-        if b is not None:
-            if out_r is None:
-                r = _like(x)
-            else:
-                r = out_r
-                if r.shape != x.shape or r.dtype != x.dtype or r.device != device or not r.is_contiguous():
-                    raise ValueError("out_r must be a contiguous tensor like x")
-            pr = r.data_ptr()
-        if p_post:
-            rstd_post = torch.empty(N, dtype=torch.float32, device=device)
-            ps_post = rstd_post.data_ptr()
-        if p_pre:
-            n = _like(x)
-            rstd_pre = torch.empty(N, dtype=torch.float32, device=device)
-            pn, ps_pre = n.data_ptr(), rstd_pre.data_ptr()
-        args = _NORM.pack(dtype, N, d, scale, eps, px[0], pb[0], p_post, pg[0], p_pre, full, px[1], pb[1], pg[1], pr, pn,
-                          ps_post, ps_pre, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, _stream(stream, device.index))
-        _abi.check(_abi.lib().lce_block_norm_forward(args), "lce_block_norm_forward")
+    r, n, rstd_post, rstd_pre = x, None, None, None
+    pr = pn = ps_post = ps_pre = 0
+    if b is not None:
+        if out_r is None:
+            r = _like(x)
+        else:
+            r = out_r
+            if r.shape != x.shape or r.dtype != x.dtype or r.device != device or not r.is_contiguous():
+                raise ValueError("out_r must be a contiguous tensor like x")
+        pr = r.data_ptr()
+    if p_post:
+        rstd_post = torch.empty(N, dtype=torch.float32, device=device)
+        ps_post = rstd_post.data_ptr()
+    if p_pre:
+        n = _like(x)
+        rstd_pre = torch.empty(N, dtype=torch.float32, device=device)
+        pn, ps_pre = n.data_ptr(), rstd_pre.data_ptr()
+    args = _NORM.pack(dtype, N, d, scale, eps, px[0], pb[0], p_post, pg[0], p_pre, full, px[1], pb[1], pg[1], pr, pn,
+                      ps_post, ps_pre, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, _stream(device.index))
+    _abi.check(_abi.lib().lce_block_norm_forward(args), "lce_block_norm_forward")
     return r, n, rstd_post, rstd_pre
 
 
+@_on_stream
 def block_norm_backward(dr, dn, r, b=None, *, w_post=None, gate=None, w_pre=None, scale: float = 1.0, rstd_post=None,
-                        rstd_pre=None, workspace=None, stream=None):
+                        rstd_pre=None, workspace=None):
     """(dx, db, dw_post, dgate, dw_pre) from the gradients dr of r (None: zero)
     and dn of n, the forward's r, b and rstd; None where the forward had no
     such input. `workspace`: a uint8 CUDA tensor of at least
-    block_norm_workspace_size(N, d) bytes."""
+    block_norm_workspace_size(N, d) bytes; `stream`: the stream to run on."""
     ref = r if r is not None else b
     dtype, N, d, pb, p_post, pg, p_pre, full = _norm_inputs(ref, b, w_post, gate, w_pre)
     pdr = (0, 0) if dr is None else _rows("dr", dr, ref)
@@ -278,26 +297,25 @@ def block_norm_backward(dr, dn, r, b=None, *, w_post=None, gate=None, w_pre=None
         if dn is None or r is None:
             raise ValueError("with w_pre the backward needs dn and r")
         pdn, pr = _rows("dn", dn, ref), _rows("r", r, ref)
+    device = ref.device
     stats = [0, 0]
     for i, (name, w, t) in enumerate((("rstd_post", w_post, rstd_post), ("rstd_pre", w_pre, rstd_pre))):
         if w is not None:
-            if t is None or t.dtype != torch.float32 or t.shape != (N,) or t.device != ref.device or not t.is_contiguous():
+            if t is None or t.dtype != torch.float32 or t.shape != (N,) or t.device != device or not t.is_contiguous():
                 raise ValueError(f"{name} must be the forward's contiguous fp32 [N] tensor")
             stats[i] = t.data_ptr()
-    device = ref.device
-    with _on(stream):
-        dx = _like(ref)
-        db = None if b is None else _like(b)
-        dw_post = None if w_post is None else torch.empty_like(w_post)
-        dgate = None if gate is None else _like(gate)
-        dw_pre = None if w_pre is None else torch.empty_like(w_pre)
-        at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-        ws, size, keep = _scratch(workspace, block_norm_workspace_size(N, d), device)
-        args = _NORM.pack(dtype, N, d, scale, 0.0, 0, pb[0], p_post, pg[0], p_pre, full, 0, pb[1], pg[1], pr[0], 0,
-                          stats[0], stats[1], pdr[0], pdn[0], pr[1], pdr[1], pdn[1], at(dx), at(db), at(dw_post),
-                          at(dgate), at(dw_pre), ws, size, _stream(stream, device.index))
-        _abi.check(_abi.lib().lce_block_norm_backward(args), "lce_block_norm_backward")
-        del keep
+    dx = _like(ref)
+    db = None if b is None else _like(b)
+    dw_post = None if w_post is None else torch.empty_like(w_post)
+    dgate = None if gate is None else _like(gate)
+    dw_pre = None if w_pre is None else torch.empty_like(w_pre)
+    at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    ws, size, keep = _scratch(workspace, block_norm_workspace_size(N, d), device)
+    args = _NORM.pack(dtype, N, d, scale, 0.0, 0, pb[0], p_post, pg[0], p_pre, full, 0, pb[1], pg[1], pr[0], 0,
+                      stats[0], stats[1], pdr[0], pdn[0], pr[1], pdr[1], pdn[1], at(dx), at(db), at(dw_post),
+                      at(dgate), at(dw_pre), ws, size, _stream(device.index))
+    _abi.check(_abi.lib().lce_block_norm_backward(args), "lce_block_norm_backward")
+    del keep
     return dx, db, dw_post, dgate, dw_pre
 
 
@@ -399,36 +417,44 @@ def _buffer(a):
     return None if a is None else a.buffer_info()[0]
 
 
-def grad_norm(grads, *, workspace=None, stream=None):
+def _clip_scratch(workspace, n, sizes, device):
+    # up to 2 MB, each tensor rounded up to 4 KB, the library needs no scratch (beyond, it would allocate it itself)
+    if workspace is None and 4 * sum(sizes) + 4096 * n <= 512 * 4096 and n <= 240:
+        return None, 0, None
+    return _scratch(workspace, clip_workspace_size(n), device)
+
+
+@_on_stream
+def grad_norm(grads, *, workspace=None):
     """The 2-norm of all tensors together (bf16 and fp32 may be mixed), a
-    0-d fp32 CUDA tensor; the host does not wait for it."""
+    0-d fp32 CUDA tensor; the host does not wait for it. `stream`: the stream
+    to run on (the current one if not given)."""
     grads = list(grads)
     index, ptrs, _, sizes, dtypes = _table(grads, None)
     n, device = len(grads), grads[0].device
-    with _on(stream):
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        at, size, keep = _scratch(workspace, clip_workspace_size(n), device)
-        _abi.check(_abi.lib().lce_grad_norm(n, _buffer(ptrs), _buffer(sizes), _buffer(dtypes), norm.data_ptr(), at, size,
-                                            _stream(stream, index)), "lce_grad_norm")
-        del keep
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    at, size, keep = _clip_scratch(workspace, n, sizes, device)
+    _abi.check(_abi.lib().lce_grad_norm(n, _buffer(ptrs), _buffer(sizes), _buffer(dtypes), norm.data_ptr(), at, size,
+                                        _stream(index)), "lce_grad_norm")
+    del keep
     return norm
 
 
-def clip_grad_norm(grads, max_norm: float, *, out=None, eps: float = 1e-6, return_factor: bool = False, workspace=None,
-                   stream=None):
+@_on_stream
+def clip_grad_norm(grads, max_norm: float, *, out=None, eps: float = 1e-6, return_factor: bool = False, workspace=None):
     """Scale all tensors by min(1, max_norm / (norm + eps)), norm being their
     2-norm together, and return the norm from before (0-d fp32 CUDA tensor;
     with return_factor (norm, factor)). In place, or into the tensors `out`
-    (each of its gradient's dtype and number of elements)."""
+    (each of its gradient's dtype and number of elements). `stream`: the stream
+    to run on."""
     grads = list(grads)
     index, ptrs, outs, sizes, dtypes = _table(grads, out if out is None else list(out))
     n, device = len(grads), grads[0].device
-    with _on(stream):
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        factor = torch.empty((), dtype=torch.float32, device=device) if return_factor else None
-        at, size, keep = _scratch(workspace, clip_workspace_size(n), device)
-        _abi.check(_abi.lib().lce_clip_grads(n, _buffer(ptrs), _buffer(outs), _buffer(sizes), _buffer(dtypes), max_norm, eps,
-                                             norm.data_ptr(), factor.data_ptr() if return_factor else None, at, size,
-                                             _stream(stream, index)), "lce_clip_grads")
-        del keep
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    factor = torch.empty((), dtype=torch.float32, device=device) if return_factor else None
+    at, size, keep = _clip_scratch(workspace, n, sizes, device)
+    _abi.check(_abi.lib().lce_clip_grads(n, _buffer(ptrs), _buffer(outs), _buffer(sizes), _buffer(dtypes), max_norm, eps,
+                                         norm.data_ptr(), factor.data_ptr() if return_factor else None, at, size,
+                                         _stream(index)), "lce_clip_grads")
+    del keep
     return (norm, factor) if return_factor else norm

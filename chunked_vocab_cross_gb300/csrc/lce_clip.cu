@@ -1,19 +1,31 @@
 // Global gradient norm over many tensors, and clipping by it.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "lce_host.h"
+#include "tc_ptx.cuh"
 
 using namespace lce;
 
 namespace {
 
-constexpr int kClipThreads = 256;
-constexpr int kChunkBytes = 32768;   // bytes of a tensor that a block takes at a time
+// The squares run best in many small blocks (191 us for 1.2 GB; 217 in blocks of 512 threads), the scaling in
+// fewer, since each adds up all blocks' sums first (362 us; 371).
+constexpr int kSqThreads = 256, kSqBlocksPerSm = 8;
+constexpr int kClipThreads = 512;
+constexpr int kChunkBytes = 65536;   // bytes of a tensor that a block takes at a time: eight loads a thread
 // Tensors a launch takes: the table travels as a kernel argument, whose size
 // the launch pays for, so a short list gets a short table.
 constexpr int kTable = 240, kShortTable = 32;
-constexpr int kBlocksPerSm = 8;
-constexpr int kMaxBlocks = 256 * kBlocksPerSm;
+constexpr int kBlocksPerSm = 4;
+constexpr int kMaxBlocks = 256 * kSqBlocksPerSm;
+// Up to 2 MB (each tensor counted in whole 4 KB) one cluster of eight blocks
+// does both passes in one launch, a warp 4 KB at a time so that all of it is in
+// flight at once, joining the blocks' sums through distributed shared memory.
+constexpr int kClusterChunks = 512;
+constexpr int kCluster = 8, kClusterThreads = 512;
+constexpr int kSmallChunkBytes = 4096;
 
 struct ClipEntry {
     const void *g;
@@ -39,15 +51,15 @@ __device__ __forceinline__ int entry_of(const ClipTable<N> &tab, int chunk) {
     return lo;
 }
 
-// A chunk of a tensor: elements [begin, end), of which [vec, vec + 16-byte
-// multiple) can be taken 16 bytes at a time. Chunks are cut at multiples of
-// kChunkBytes of the address, so only a tensor's ends are ragged.
+// A chunk of a tensor: elements [begin, end), of which [vb, ve) can be taken 16
+// bytes at a time. Chunks are cut at multiples of their size from the 16-byte
+// boundary at or before the tensor's start, so only its ends are ragged.
 struct Span {
     int64_t begin, end, vb, ve;
 };
-template <typename T>
+template <typename T, int kBytes>
 __device__ __forceinline__ Span span_of(const ClipEntry &e, int chunk) {
-    constexpr int kPer = kChunkBytes / sizeof(T), kV = 16 / sizeof(T);
+    constexpr int kPer = kBytes / sizeof(T), kV = 16 / sizeof(T);
     const int64_t lead = (reinterpret_cast<uintptr_t>(e.g) % 16) / sizeof(T);   // elements past a 16-byte boundary
     Span s;
     s.begin = static_cast<int64_t>(chunk) * kPer - lead;
@@ -76,50 +88,69 @@ __device__ __forceinline__ float squares16(const uint4 &v, float s) {
     return s;
 }
 
+// thread t of nt takes its share of a span
 template <typename T>
-__device__ __forceinline__ float span_squares(const ClipEntry &e, const Span &sp) {
+__device__ __forceinline__ float span_squares(const ClipEntry &e, const Span &sp, int t, int nt) {
     const T *g = static_cast<const T *>(e.g);
     constexpr int kV = 16 / sizeof(T);
     float s = 0.f;
-    for (int64_t i = sp.begin + threadIdx.x; i < sp.vb; i += kClipThreads) s = fmaf(f32(g[i]), f32(g[i]), s);
-    for (int64_t i = sp.vb + threadIdx.x * kV; i < sp.ve; i += kClipThreads * kV) {
+    for (int64_t i = sp.begin + t; i < sp.vb; i += nt) s = fmaf(f32(g[i]), f32(g[i]), s);
+    for (int64_t i = sp.vb + t * kV; i < sp.ve; i += nt * kV) {
         if (sizeof(T) == 4) s = squares(*reinterpret_cast<const float4 *>(g + i), s);
         else s = squares16(*reinterpret_cast<const uint4 *>(g + i), s);
     }
-    for (int64_t i = sp.ve + threadIdx.x; i < sp.end; i += kClipThreads) s = fmaf(f32(g[i]), f32(g[i]), s);
+    for (int64_t i = sp.ve + t; i < sp.end; i += nt) s = fmaf(f32(g[i]), f32(g[i]), s);
     return s;
 }
 
+// Sum over the block, the same for all threads, in a fixed order. A warp's fp64
+// addition takes 16 cycles of an SM, so one warp joins the warps' sums for all
+// (done by every thread, they were half of a short call).
+template <int kThreads>
 __device__ __forceinline__ double block_sum(double v) {
-    __shared__ double red[kClipThreads / 32];
+    __shared__ double red[kThreads / 32], total;
     for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = v;
     __syncthreads();
-    v = 0.0;
-    for (int i = 0; i < kClipThreads / 32; ++i) v += red[i];
-    return v;
+    if (threadIdx.x < 32) {
+        v = threadIdx.x < kThreads / 32 ? red[threadIdx.x] : 0.0;
+        for (int m = kThreads / 64; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        if (threadIdx.x == 0) total = v;
+    }
+    __syncthreads();
+    return total;
 }
 
 // part[block] = sum of the squares of the block's chunks: fp32 along a
 // thread's elements of one chunk, fp64 across chunks and threads.
 template <int N>
-__global__ void __launch_bounds__(kClipThreads) k_clip_squares(const __grid_constant__ ClipTable<N> tab, double *part) {
+__global__ void __launch_bounds__(kSqThreads) k_clip_squares(const __grid_constant__ ClipTable<N> tab, double *part) {
     double s = 0.0;
     for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
         const int i = entry_of(tab, c), k = c - tab.first[i];
         const ClipEntry &e = tab.t[i];
-        s += e.fp32 ? span_squares<float>(e, span_of<float>(e, k))
-                    : span_squares<__nv_bfloat16>(e, span_of<__nv_bfloat16>(e, k));
+        s += e.fp32 ? span_squares<float>(e, span_of<float, kChunkBytes>(e, k), threadIdx.x, kSqThreads)
+                    : span_squares<__nv_bfloat16>(e, span_of<__nv_bfloat16, kChunkBytes>(e, k), threadIdx.x, kSqThreads);
     }
-    s = block_sum(s);
+    s = block_sum<kSqThreads>(s);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
+// The norm from the blocks' sums, by one warp for the block.
 __device__ __forceinline__ float norm_of(const double *part, int n) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < n; i += kClipThreads) s += part[i];
-    return static_cast<float>(sqrt(block_sum(s)));
+    __shared__ float norm;
+    if (threadIdx.x < 32) {
+        double s[4] = {0.0, 0.0, 0.0, 0.0};
+        for (int i = threadIdx.x; i < n; i += 128)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k * 32 < n) s[k] += part[i + k * 32];
+        double v = (s[0] + s[1]) + (s[2] + s[3]);
+        for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        if (threadIdx.x == 0) norm = static_cast<float>(sqrt(v));
+    }
+    __syncthreads();
+    return norm;
 }
 
 __global__ void __launch_bounds__(kClipThreads) k_clip_norm(const double *part, int n, float *norm) {
@@ -128,15 +159,15 @@ __global__ void __launch_bounds__(kClipThreads) k_clip_norm(const double *part, 
 }
 
 template <typename T>
-__device__ __forceinline__ void span_scale(const ClipEntry &e, const Span &sp, float c) {
+__device__ __forceinline__ void span_scale(const ClipEntry &e, const Span &sp, float c, int t, int nt) {
     const T *g = static_cast<const T *>(e.g);
     T *o = static_cast<T *>(e.out);
     constexpr int kV = 16 / sizeof(T);
     // an output that lies otherwise than its gradient takes single elements
     const bool vec = (reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(o)) % 16 == 0;
     const int64_t vb = vec ? sp.vb : sp.begin, ve = vec ? sp.ve : sp.begin;
-    for (int64_t i = sp.begin + threadIdx.x; i < vb; i += kClipThreads) o[i] = static_cast<T>(f32(g[i]) * c);
-    for (int64_t i = vb + threadIdx.x * kV; i < ve; i += kClipThreads * kV) {
+    for (int64_t i = sp.begin + t; i < vb; i += nt) o[i] = static_cast<T>(f32(g[i]) * c);
+    for (int64_t i = vb + t * kV; i < ve; i += nt * kV) {
         if (sizeof(T) == 4) {
             float4 v = *reinterpret_cast<const float4 *>(g + i);
             __stcs(reinterpret_cast<float4 *>(o + i), make_float4(v.x * c, v.y * c, v.z * c, v.w * c));
@@ -152,7 +183,7 @@ __device__ __forceinline__ void span_scale(const ClipEntry &e, const Span &sp, f
             __stcs(reinterpret_cast<uint4 *>(o + i), make_uint4(w[0], w[1], w[2], w[3]));
         }
     }
-    for (int64_t i = ve + threadIdx.x; i < sp.end; i += kClipThreads) o[i] = static_cast<T>(f32(g[i]) * c);
+    for (int64_t i = ve + t; i < sp.end; i += nt) o[i] = static_cast<T>(f32(g[i]) * c);
 }
 
 // Every block adds up the partial sums itself (a few KB, in L2), forms the
@@ -173,8 +204,51 @@ __global__ void __launch_bounds__(kClipThreads) k_clip_scale(const __grid_consta
     for (int j = tab.chunks - 1 - blockIdx.x; j >= 0; j -= gridDim.x) {
         const int i = entry_of(tab, j), k = j - tab.first[i];
         const ClipEntry &e = tab.t[i];
-        if (e.fp32) span_scale<float>(e, span_of<float>(e, k), c);
-        else span_scale<__nv_bfloat16>(e, span_of<__nv_bfloat16>(e, k), c);
+        if (e.fp32) span_scale<float>(e, span_of<float, kChunkBytes>(e, k), c, threadIdx.x, kClipThreads);
+        else span_scale<__nv_bfloat16>(e, span_of<__nv_bfloat16, kChunkBytes>(e, k), c, threadIdx.x, kClipThreads);
+    }
+}
+
+// Both passes by one cluster. The sums are joined in block order.
+template <int N>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads)
+    k_clip_cluster(const __grid_constant__ ClipTable<N> tab, int clip, float max_norm, float eps, int in_place, float *norm,
+                   float *factor) {
+    __shared__ double mine;
+    const int rank = static_cast<int>(cluster_ctarank()), lane = threadIdx.x & 31;
+    constexpr int kWarps = kCluster * kClusterThreads / 32;
+    const int first = rank + threadIdx.x / 32 * kCluster;   // neighbouring chunks to different SMs
+    double s = 0.0;
+    for (int c = first; c < tab.chunks; c += kWarps) {
+        const int i = entry_of(tab, c), k = c - tab.first[i];
+        const ClipEntry &e = tab.t[i];
+        s += e.fp32 ? span_squares<float>(e, span_of<float, kSmallChunkBytes>(e, k), lane, 32)
+                    : span_squares<__nv_bfloat16>(e, span_of<__nv_bfloat16, kSmallChunkBytes>(e, k), lane, 32);
+    }
+    s = block_sum<kClusterThreads>(s);
+    if (threadIdx.x == 0) mine = s;
+    cluster_sync_all();
+    double total = 0.0;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) {
+        double v;
+        asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(map_to_cta(smem_u32(&mine), r)) : "memory");
+        total += v;
+    }
+    cluster_sync_all();   // nobody's sum goes away while another reads it
+    const float v = static_cast<float>(sqrt(total));
+    float c = max_norm / (v + eps);
+    if (c > 1.f) c = 1.f;   // a NaN stays
+    if (rank == 0 && threadIdx.x == 0) {
+        *norm = v;
+        if (factor) *factor = c;
+    }
+    if (!clip || (in_place && c == 1.f)) return;
+    for (int j = first; j < tab.chunks; j += kWarps) {
+        const int i = entry_of(tab, j), k = j - tab.first[i];
+        const ClipEntry &e = tab.t[i];
+        if (e.fp32) span_scale<float>(e, span_of<float, kSmallChunkBytes>(e, k), c, lane, 32);
+        else span_scale<__nv_bfloat16>(e, span_of<__nv_bfloat16, kSmallChunkBytes>(e, k), c, lane, 32);
     }
 }
 
@@ -195,7 +269,7 @@ lce_status_t check_clip(int64_t count, const void *const *grads, void *const *ou
 }
 
 // The tensors from `*at` on that fit one launch.
-template <int N>
+template <int N, int kBytes>
 void fill_table(ClipTable<N> &tab, int64_t *at, int64_t count, const void *const *grads, void *const *outs,
                 const int64_t *sizes, const int32_t *dtypes) {
     tab.count = tab.chunks = 0;
@@ -204,7 +278,7 @@ void fill_table(ClipTable<N> &tab, int64_t *at, int64_t count, const void *const
         if (sizes[i] == 0) continue;
         const int elt = dtypes[i] == LCE_BF16 ? 2 : 4;
         const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(grads[i]) % 16);
-        const int64_t chunks = (sizes[i] * elt + lead + kChunkBytes - 1) / kChunkBytes;
+        const int64_t chunks = (sizes[i] * elt + lead + kBytes - 1) / kBytes;
         if (tab.count && tab.chunks + chunks >= (int64_t(1) << 30)) break;
         tab.first[tab.count] = tab.chunks;
         tab.t[tab.count++] = ClipEntry{grads[i], outs ? outs[i] : const_cast<void *>(grads[i]), sizes[i],
@@ -224,17 +298,37 @@ struct ClipCall {
     float *norm, *factor;
 };
 
+// Small chunks of all tensors together (as fill_table cuts them).
+int64_t count_chunks(const ClipCall &a) {
+    int64_t n = 0;
+    for (int64_t i = 0; i < a.count; ++i) {
+        if (a.sizes[i] == 0) continue;
+        const int64_t bytes = a.sizes[i] * (a.dtypes[i] == LCE_BF16 ? 2 : 4) + static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.grads[i]) % 16);
+        n += (bytes + kSmallChunkBytes - 1) / kSmallChunkBytes;
+    }
+    return n;
+}
+
+template <int N>
+lce_status_t launch_small(const ClipCall &a, cudaStream_t st) {
+    ClipTable<N> tab;
+    int64_t at = 0;
+    fill_table<N, kSmallChunkBytes>(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
+    k_clip_cluster<N><<<kCluster, kClusterThreads, 0, st>>>(tab, a.clip, a.max_norm, a.eps, a.outs == nullptr, a.norm, a.factor);
+    return host_launched();
+}
+
 template <int N>
 lce_status_t launch_clip(const ClipCall &a, const HostDev &dev, double *part, cudaStream_t st) {
     lce_status_t s;
     ClipTable<N> tab;
     int n = 0;
-    const int most = dev.sms * kBlocksPerSm < kMaxBlocks ? dev.sms * kBlocksPerSm : kMaxBlocks;
+    const int most = dev.sms * kSqBlocksPerSm < kMaxBlocks ? dev.sms * kSqBlocksPerSm : kMaxBlocks;
     for (int64_t at = 0; at < a.count;) {
-        fill_table(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
+        fill_table<N, kChunkBytes>(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
         if (!tab.count) break;
         const int blocks = tab.chunks < most ? tab.chunks : most;
-        k_clip_squares<N><<<blocks, kClipThreads, 0, st>>>(tab, part + n);
+        k_clip_squares<N><<<blocks, kSqThreads, 0, st>>>(tab, part + n);
         if ((s = host_launched()) != LCE_OK) return s;
         n += blocks;
     }
@@ -244,9 +338,9 @@ lce_status_t launch_clip(const ClipCall &a, const HostDev &dev, double *part, cu
     }
     bool done = false;
     for (int64_t at = 0; at < a.count || !done;) {
-        fill_table(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
+        fill_table<N, kChunkBytes>(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
         if (!tab.count && done) break;
-        const int blocks = tab.chunks < 1 ? 1 : tab.chunks < most ? tab.chunks : most;
+        const int blocks = std::max(1, std::min(tab.chunks, dev.sms * kBlocksPerSm));
         k_clip_scale<N><<<blocks, kClipThreads, 0, st>>>(tab, part, n, a.max_norm, a.eps, a.outs == nullptr, a.norm, a.factor);
         if ((s = host_launched()) != LCE_OK) return s;
         done = true;
@@ -260,6 +354,9 @@ lce_status_t run_clip(const ClipCall &a, void *workspace, size_t workspace_bytes
     HostDev dev;
     if ((s = host_device(&dev)) != LCE_OK) return s;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (workspace && workspace_bytes < lce_clip_workspace_size(a.count)) return LCE_ERR_WORKSPACE;
+    if (a.count <= kTable && count_chunks(a) <= kClusterChunks)
+        return a.count <= kShortTable ? launch_small<kShortTable>(a, st) : launch_small<kTable>(a, st);
     HostScratch scratch(st);
     uint8_t *base = nullptr;
     if ((s = scratch.get(workspace, workspace_bytes, lce_clip_workspace_size(a.count), &base)) != LCE_OK) return s;
