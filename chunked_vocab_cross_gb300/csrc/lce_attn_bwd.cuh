@@ -418,11 +418,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
         };
         bool ok = true;
         int na = 0, nf = 0, nd = 0, ns = 0, s0 = 0, s1 = 0;   // ring tiles, pieces, dS, statistics, S by buffer so far
-        for (int pieces = 0; ok; ++pieces) {
-            if (!(ok = wait.all(&bar.work_full[pieces & 1], (pieces >> 1) & 1))) break;
-            const BwdWork w = bar.work[pieces & 1];
+        int pieces = 0;
+        BwdWork w, next;
+        f32x2 nl2 = both(0.f), nd2 = both(0.f);               // dQ: the row's statistics
+        // The next piece, and its row's statistics: fetched before the output of the one before goes out.
+        auto fetch = [&] {
+            if (!wait.all(&bar.work_full[pieces & 1], (pieces >> 1) & 1)) return false;
+            next = bar.work[pieces & 1];
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.work_empty[pieces & 1]);
+            ++pieces;
+            if (next.kind == BWD_DQ) {
+                griddep_wait();   // the statistics come from the launch before
+                const int64_t at = next.head * a.stat_stride + static_cast<int64_t>(next.slot) * kTcTile + row;
+                nl2 = both(a.nlse2[at]), nd2 = both(a.ndelta[at]);
+            }
+            return true;
+        };
+        ok = fetch();
+        while (ok) {
+            w = next;
             if (w.kind == BWD_NONE) break;
             const bool dkv = w.kind == BWD_DKV;
             __nv_bfloat16 *out0, *out1 = nullptr;   // dQ, or dV and dK
@@ -441,6 +456,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                         *reinterpret_cast<uint4 *>(out0 + row * ts0 + c) = make_uint4(0, 0, 0, 0);
                         if (dkv) *reinterpret_cast<uint4 *>(out1 + row * ts1 + c) = make_uint4(0, 0, 0, 0);
                     }
+                ok = fetch();
                 continue;
             }
             if (dkv) {
@@ -510,9 +526,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
             } else {
                 const uint32_t tPh = tm + cP2 + lane_base + half * 64;
                 const int last = w.t0 + row + w.off;   // causal: last key of the row
-                const int64_t at = w.head * a.stat_stride + static_cast<int64_t>(w.slot) * kTcTile + row;
-                griddep_wait();   // the statistics come from the launch before
-                const f32x2 nl2 = both(a.nlse2[at]), nd2 = both(a.ndelta[at]);
                 for (int j = 0; j < w.n; ++j, ++nd) {
                     const uint32_t tSj = tm + (j & 1) * 128 + lane_base + half * 64;
                     int &sn = j & 1 ? s1 : s0;
@@ -556,7 +569,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                     }
                 }
             }
-            if (!ok || !(ok = wait.all(&bar.fin, nf & 1))) break;
+            if (!ok || !(ok = fetch()) || !(ok = wait.all(&bar.fin, nf & 1))) break;
             ++nf;
             na += w.n;
             tc_fence_after();
