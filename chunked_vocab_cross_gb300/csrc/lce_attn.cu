@@ -64,6 +64,7 @@ AttnArgs make_args(const lce_attn_t *a, const HostDev &dev) {
     r.group = r.Hq / r.Hk;
     r.D = static_cast<int>(a->D);
     r.causal = a->causal != 0;
+    r.pair_heads = r.group % 2 == 0;
     r.scale = a->scale;
     r.scale_log2 = a->scale * kAttnLog2e;
     r.status = dev.status;
@@ -122,8 +123,8 @@ lce_status_t forward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &d
     if (s == LCE_OK) s = encode(&maps.k, dev, a->k, a->Tk, a->Hk, a->D, a->k_ts, a->k_hs);
     if (s == LCE_OK) s = encode(&maps.v, dev, a->v, a->Tk, a->Hk, a->D, a->v_ts, a->v_hs);
     if (s != LCE_OK) return s;
-    return launch<k_attn_fwd<KS>>(dev, seq_slots(r.sq.T, r.sq.B, kTcTile) * r.Hq, kFwdThreads, FwdSmem<KS>::kBytes, st, r,
-                  maps);
+    const int64_t work = r.pair_heads ? seq_slots(r.sq.T, r.sq.B, kTcTile) * (r.Hq / 2) : seq_slots(r.sq.T, r.sq.B, 2 * kTcTile) * r.Hq;
+    return launch<k_attn_fwd<KS>>(dev, work, kFwdThreads, FwdSmem<KS>::kBytes, st, r, maps);
 }
 
 template <int DP>

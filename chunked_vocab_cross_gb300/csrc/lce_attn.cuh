@@ -43,7 +43,7 @@ struct AttnArgs {
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs, dO_ts, dO_hs, dq_ts, dq_hs, dk_ts, dk_hs, dv_ts, dv_hs;
     SeqMap sq, sk;
     int Hq, Hk, group, D;
-    int causal;
+    int causal, pair_heads;    // pair_heads (tensor-core forward): a piece of work is two heads of a key head, else two tiles of rows
     float scale, scale_log2;   // scale, scale * log2(e)
     // backward: per query slot row, -lse * log2(e) (-inf where the row takes no
     // part) and -delta, both negative so that they are added; [Hq][slots * TILE]
