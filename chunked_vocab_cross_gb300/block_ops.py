@@ -418,8 +418,8 @@ def _buffer(a):
 
 
 def _clip_scratch(workspace, n, sizes, device):
-    # up to 2 MB, each tensor rounded up to 4 KB, the library needs no scratch (beyond, it would allocate it itself)
-    if workspace is None and 4 * sum(sizes) + 4096 * n <= 512 * 4096 and n <= 240:
+    # up to 1 MB, each tensor rounded up to 4 KB, the library needs no scratch (beyond, it would allocate it itself)
+    if workspace is None and 4 * sum(sizes) + 4096 * n <= 256 * 4096 and n <= 240:
         return None, 0, None
     return _scratch(workspace, clip_workspace_size(n), device)
 

@@ -10,21 +10,24 @@ using namespace lce;
 
 namespace {
 
-// The squares run best in many small blocks (191 us for 1.2 GB; 217 in blocks of 512 threads), the scaling in
-// fewer, since each adds up all blocks' sums first (362 us; 371).
+// What bounds both passes is HBM: 1.6 GB of bf16 in 20 tensors take 730 us, 4.8 GB at 6.6 TB/s (the squares alone
+// 245 us). The squares run best in many small blocks (191 us for 1.2 GB; 217 in blocks of 512 threads), the scaling
+// in fewer, since each adds up all blocks' sums first (362 us; 371).
 constexpr int kSqThreads = 256, kSqBlocksPerSm = 8;
 constexpr int kClipThreads = 512;
 constexpr int kChunkBytes = 65536;   // bytes of a tensor that a block takes at a time: eight loads a thread
-// Tensors a launch takes: the table travels as a kernel argument, whose size
-// the launch pays for, so a short list gets a short table.
-constexpr int kTable = 240, kShortTable = 32;
+// Tensors a launch takes: the table travels as a kernel argument (9 KB; a short
+// one for short lists made no difference to the host).
+constexpr int kTable = 240;
 constexpr int kBlocksPerSm = 4;
 constexpr int kMaxBlocks = 256 * kSqBlocksPerSm;
-// Up to 2 MB (each tensor counted in whole 4 KB) one cluster of eight blocks
-// does both passes in one launch, a warp 4 KB at a time so that all of it is in
-// flight at once, joining the blocks' sums through distributed shared memory.
-constexpr int kClusterChunks = 512;
-constexpr int kCluster = 8, kClusterThreads = 512;
+// Up to 1 MB (each tensor counted in whole 4 KB) one cluster of eight blocks
+// does both passes in one launch: a warp has one chunk of 4 KB and keeps it in
+// registers, and the blocks' sums are joined through distributed shared memory.
+// What bounds it is latency (0.1 MB in 20 tensors: 4.8 us, 6.6 with the two
+// launches; 0.84 MB in 29: 7.3 us, 8.0; and one launch less for the host).
+constexpr int kCluster = 8, kClusterThreads = 1024;
+constexpr int kClusterChunks = kCluster * kClusterThreads / 32;
 constexpr int kSmallChunkBytes = 4096;
 
 struct ClipEntry {
@@ -33,15 +36,13 @@ struct ClipEntry {
     int64_t n;
     int fp32;
 };
-template <int N>
 struct ClipTable {
     int count, chunks;
-    int first[N];   // number of a tensor's first chunk within the launch; apart from the rest, since it is searched
-    ClipEntry t[N];
+    int first[kTable];   // number of a tensor's first chunk within the launch; apart from the rest, since it is searched
+    ClipEntry t[kTable];
 };
 
-template <int N>
-__device__ __forceinline__ int entry_of(const ClipTable<N> &tab, int chunk) {
+__device__ __forceinline__ int entry_of(const ClipTable &tab, int chunk) {
     int lo = 0, hi = tab.count;   // the last entry with first <= chunk
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -88,11 +89,12 @@ __device__ __forceinline__ float squares16(const uint4 &v, float s) {
     return s;
 }
 
-// thread t of nt takes its share of a span
+// each thread takes its share of a span
 template <typename T>
-__device__ __forceinline__ float span_squares(const ClipEntry &e, const Span &sp, int t, int nt) {
+__device__ __forceinline__ float span_squares(const ClipEntry &e, const Span &sp) {
     const T *g = static_cast<const T *>(e.g);
-    constexpr int kV = 16 / sizeof(T);
+    constexpr int kV = 16 / sizeof(T), nt = kSqThreads;
+    const int t = threadIdx.x;
     float s = 0.f;
     for (int64_t i = sp.begin + t; i < sp.vb; i += nt) s = fmaf(f32(g[i]), f32(g[i]), s);
     for (int64_t i = sp.vb + t * kV; i < sp.ve; i += nt * kV) {
@@ -123,14 +125,13 @@ __device__ __forceinline__ double block_sum(double v) {
 
 // part[block] = sum of the squares of the block's chunks: fp32 along a
 // thread's elements of one chunk, fp64 across chunks and threads.
-template <int N>
-__global__ void __launch_bounds__(kSqThreads) k_clip_squares(const __grid_constant__ ClipTable<N> tab, double *part) {
+__global__ void __launch_bounds__(kSqThreads) k_clip_squares(const __grid_constant__ ClipTable tab, double *part) {
     double s = 0.0;
     for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
         const int i = entry_of(tab, c), k = c - tab.first[i];
         const ClipEntry &e = tab.t[i];
-        s += e.fp32 ? span_squares<float>(e, span_of<float, kChunkBytes>(e, k), threadIdx.x, kSqThreads)
-                    : span_squares<__nv_bfloat16>(e, span_of<__nv_bfloat16, kChunkBytes>(e, k), threadIdx.x, kSqThreads);
+        s += e.fp32 ? span_squares<float>(e, span_of<float, kChunkBytes>(e, k))
+                    : span_squares<__nv_bfloat16>(e, span_of<__nv_bfloat16, kChunkBytes>(e, k));
     }
     s = block_sum<kSqThreads>(s);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -158,39 +159,43 @@ __global__ void __launch_bounds__(kClipThreads) k_clip_norm(const double *part, 
     if (threadIdx.x == 0) *norm = v;
 }
 
+// 16 bytes of T, times c
 template <typename T>
-__device__ __forceinline__ void span_scale(const ClipEntry &e, const Span &sp, float c, int t, int nt) {
+__device__ __forceinline__ uint4 scaled(const uint4 &v, float c) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (sizeof(T) == 4) w[k] = __float_as_uint(__uint_as_float(w[k]) * c);
+        else {
+            __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(w[k] << 16) * c, __uint_as_float(w[k] & 0xffff0000u) * c);
+            w[k] = *reinterpret_cast<uint32_t *>(&p);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ void span_scale(const ClipEntry &e, const Span &sp, float c) {
     const T *g = static_cast<const T *>(e.g);
     T *o = static_cast<T *>(e.out);
-    constexpr int kV = 16 / sizeof(T);
+    constexpr int kV = 16 / sizeof(T), nt = kClipThreads;
+    const int t = threadIdx.x;
     // an output that lies otherwise than its gradient takes single elements
     const bool vec = (reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(o)) % 16 == 0;
     const int64_t vb = vec ? sp.vb : sp.begin, ve = vec ? sp.ve : sp.begin;
     for (int64_t i = sp.begin + t; i < vb; i += nt) o[i] = static_cast<T>(f32(g[i]) * c);
-    for (int64_t i = vb + t * kV; i < ve; i += nt * kV) {
-        if (sizeof(T) == 4) {
-            float4 v = *reinterpret_cast<const float4 *>(g + i);
-            __stcs(reinterpret_cast<float4 *>(o + i), make_float4(v.x * c, v.y * c, v.z * c, v.w * c));
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4 *>(g + i);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(w[k] << 16) * c,
-                                                         __uint_as_float(w[k] & 0xffff0000u) * c);
-                w[k] = *reinterpret_cast<uint32_t *>(&p);
-            }
-            __stcs(reinterpret_cast<uint4 *>(o + i), make_uint4(w[0], w[1], w[2], w[3]));
-        }
-    }
+    for (int64_t i = vb + t * kV; i < ve; i += nt * kV)
+        __stcs(reinterpret_cast<uint4 *>(o + i), scaled<T>(*reinterpret_cast<const uint4 *>(g + i), c));
     for (int64_t i = ve + t; i < sp.end; i += nt) o[i] = static_cast<T>(f32(g[i]) * c);
 }
 
 // Every block adds up the partial sums itself (a few KB, in L2), forms the
 // factor and scales its chunks, the last ones first: they are what the squares
-// left in L2, and the stores ask to be evicted before them.
-template <int N>
-__global__ void __launch_bounds__(kClipThreads) k_clip_scale(const __grid_constant__ ClipTable<N> tab, const double *part,
+// left in L2, and the stores ask to be evicted before them. Chunks stay with
+// block numbers equal modulo the grid, whose SMs then have them nearer (120 MB:
+// 61 us; 62 counted straight down, 70 first chunks first; 60 MB, all of it in
+// L2: 28, 34 and 29; 1.6 GB: 730 any way).
+__global__ void __launch_bounds__(kClipThreads) k_clip_scale(const __grid_constant__ ClipTable tab, const double *part,
                                                              int n, float max_norm, float eps, int in_place,
                                                              float *norm, float *factor) {
     const float v = norm_of(part, n);
@@ -201,55 +206,112 @@ __global__ void __launch_bounds__(kClipThreads) k_clip_scale(const __grid_consta
         if (factor) *factor = c;
     }
     if (in_place && c == 1.f) return;
-    for (int j = tab.chunks - 1 - blockIdx.x; j >= 0; j -= gridDim.x) {
+    const int g = gridDim.x, b = blockIdx.x;
+    if (b >= tab.chunks) return;
+    for (int j = b + (tab.chunks - 1 - b) / g * g; j >= 0; j -= g) {
         const int i = entry_of(tab, j), k = j - tab.first[i];
         const ClipEntry &e = tab.t[i];
-        if (e.fp32) span_scale<float>(e, span_of<float, kChunkBytes>(e, k), c, threadIdx.x, kClipThreads);
-        else span_scale<__nv_bfloat16>(e, span_of<__nv_bfloat16, kChunkBytes>(e, k), c, threadIdx.x, kClipThreads);
+        if (e.fp32) span_scale<float>(e, span_of<float, kChunkBytes>(e, k), c);
+        else span_scale<__nv_bfloat16>(e, span_of<__nv_bfloat16, kChunkBytes>(e, k), c);
     }
 }
 
-// Both passes by one cluster. The sums are joined in block order.
-template <int N>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads)
-    k_clip_cluster(const __grid_constant__ ClipTable<N> tab, int clip, float max_norm, float eps, int in_place, float *norm,
-                   float *factor) {
-    __shared__ double mine;
-    const int rank = static_cast<int>(cluster_ctarank()), lane = threadIdx.x & 31;
-    constexpr int kWarps = kCluster * kClusterThreads / 32;
-    const int first = rank + threadIdx.x / 32 * kCluster;   // neighbouring chunks to different SMs
-    double s = 0.0;
-    for (int c = first; c < tab.chunks; c += kWarps) {
-        const int i = entry_of(tab, c), k = c - tab.first[i];
-        const ClipEntry &e = tab.t[i];
-        s += e.fp32 ? span_squares<float>(e, span_of<float, kSmallChunkBytes>(e, k), lane, 32)
-                    : span_squares<__nv_bfloat16>(e, span_of<__nv_bfloat16, kSmallChunkBytes>(e, k), lane, 32);
-    }
-    s = block_sum<kClusterThreads>(s);
-    if (threadIdx.x == 0) mine = s;
-    cluster_sync_all();
-    double total = 0.0;
+// A warp's chunk of a tensor in registers: its 16-byte pieces, eight a lane,
+// and the up to seven elements on either side of them, one a lane.
+template <typename T>
+struct Held {
+    static constexpr int kV = 16 / sizeof(T), kPieces = kSmallChunkBytes / 16 / 32;
+    Span sp;
+    uint4 v[kPieces];
+    int64_t at;    // of the single element (-1: none)
+    float single;
+
+    __device__ __forceinline__ float load(const ClipEntry &e, int chunk, int lane) {
+        const T *g = static_cast<const T *>(e.g);
+        sp = span_of<T, kSmallChunkBytes>(e, chunk);
+        at = lane < 16 ? sp.begin + lane : sp.ve + lane - 16;
+        if (at >= (lane < 16 ? sp.vb : sp.end)) at = -1;
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r) {
-        double v;
-        asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(map_to_cta(smem_u32(&mine), r)) : "memory");
-        total += v;
+        for (int k = 0; k < kPieces; ++k) {
+            const int64_t i = sp.vb + (k * 32 + lane) * kV;
+            v[k] = i < sp.ve ? *reinterpret_cast<const uint4 *>(g + i) : make_uint4(0, 0, 0, 0);
+        }
+        single = at >= 0 ? f32(g[at]) : 0.f;
+        float s = single * single;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            if (sizeof(T) == 4) s = squares(*reinterpret_cast<const float4 *>(&v[k]), s);
+            else s = squares16(v[k], s);
+        }
+        return s;
     }
-    cluster_sync_all();   // nobody's sum goes away while another reads it
-    const float v = static_cast<float>(sqrt(total));
-    float c = max_norm / (v + eps);
-    if (c > 1.f) c = 1.f;   // a NaN stays
-    if (rank == 0 && threadIdx.x == 0) {
-        *norm = v;
-        if (factor) *factor = c;
+    __device__ __forceinline__ void store(const ClipEntry &e, float c, int lane) const {
+        T *o = static_cast<T *>(e.out);
+        const bool vec = (reinterpret_cast<uintptr_t>(e.g) ^ reinterpret_cast<uintptr_t>(o)) % 16 == 0;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const int64_t i = sp.vb + (k * 32 + lane) * kV;
+            if (i >= sp.ve) continue;
+            const uint4 w = scaled<T>(v[k], c);
+            if (vec) *reinterpret_cast<uint4 *>(o + i) = w;
+            else {
+                const T *x = reinterpret_cast<const T *>(&w);
+#pragma unroll
+                for (int q = 0; q < kV; ++q) o[i + q] = x[q];
+            }
+        }
+        if (at >= 0) o[at] = static_cast<T>(single * c);
     }
-    if (!clip || (in_place && c == 1.f)) return;
-    for (int j = first; j < tab.chunks; j += kWarps) {
-        const int i = entry_of(tab, j), k = j - tab.first[i];
-        const ClipEntry &e = tab.t[i];
-        if (e.fp32) span_scale<float>(e, span_of<float, kSmallChunkBytes>(e, k), c, lane, 32);
-        else span_scale<__nv_bfloat16>(e, span_of<__nv_bfloat16, kSmallChunkBytes>(e, k), c, lane, 32);
+};
+
+// Both passes by one cluster: fp32 within a warp's chunk, fp64 across the
+// chunks, joined in block order by one warp of each block (a warp's fp64
+// addition takes 16 cycles of an SM, its square root hundreds: done by every
+// warp they were most of the call, 9.9 us for 0.1 MB).
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads)
+    k_clip_cluster(const __grid_constant__ ClipTable tab, int clip, float max_norm, float eps, int in_place, float *norm,
+                   float *factor) {
+    __shared__ float red[kClusterThreads / 32], f;
+    __shared__ double mine;
+    const int rank = static_cast<int>(cluster_ctarank()), warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int c0 = rank + warp * kCluster;   // neighbouring chunks to different SMs
+    const bool any = c0 < tab.chunks;
+    const int i = any ? entry_of(tab, c0) : 0, k = any ? c0 - tab.first[i] : 0;
+    const ClipEntry &e = tab.t[i];
+    Held<float> hf;
+    Held<__nv_bfloat16> hb;
+    float s = 0.f;
+    if (any) s = e.fp32 ? hf.load(e, k, lane) : hb.load(e, k, lane);
+    for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (lane == 0) red[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        double v = red[lane];
+        for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        if (lane == 0) mine = v;
     }
+    cluster_sync_all();
+    if (warp == 0) {
+        double v = 0.0;
+        if (lane < kCluster)
+            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(map_to_cta(smem_u32(&mine), lane)) : "memory");
+        for (int m = kCluster / 2; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        if (lane == 0) {
+            const float n = static_cast<float>(sqrt(v));
+            float c = max_norm / (n + eps);
+            if (c > 1.f) c = 1.f;   // a NaN stays
+            f = c;
+            if (rank == 0) {
+                *norm = n;
+                if (factor) *factor = c;
+            }
+        }
+    }
+    cluster_sync_all();   // the factor is there, and nobody's sum goes away while another reads it
+    const float c = f;
+    if (!any || !clip || (in_place && c == 1.f)) return;
+    if (e.fp32) hf.store(e, c, lane);
+    else hb.store(e, c, lane);
 }
 
 lce_status_t check_clip(int64_t count, const void *const *grads, void *const *outs, const int64_t *sizes,
@@ -269,11 +331,11 @@ lce_status_t check_clip(int64_t count, const void *const *grads, void *const *ou
 }
 
 // The tensors from `*at` on that fit one launch.
-template <int N, int kBytes>
-void fill_table(ClipTable<N> &tab, int64_t *at, int64_t count, const void *const *grads, void *const *outs,
+template <int kBytes>
+void fill_table(ClipTable &tab, int64_t *at, int64_t count, const void *const *grads, void *const *outs,
                 const int64_t *sizes, const int32_t *dtypes) {
     tab.count = tab.chunks = 0;
-    for (; *at < count && tab.count < N; ++*at) {
+    for (; *at < count && tab.count < kTable; ++*at) {
         const int64_t i = *at;
         if (sizes[i] == 0) continue;
         const int elt = dtypes[i] == LCE_BF16 ? 2 : 4;
@@ -309,26 +371,24 @@ int64_t count_chunks(const ClipCall &a) {
     return n;
 }
 
-template <int N>
 lce_status_t launch_small(const ClipCall &a, cudaStream_t st) {
-    ClipTable<N> tab;
+    ClipTable tab;
     int64_t at = 0;
-    fill_table<N, kSmallChunkBytes>(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
-    k_clip_cluster<N><<<kCluster, kClusterThreads, 0, st>>>(tab, a.clip, a.max_norm, a.eps, a.outs == nullptr, a.norm, a.factor);
+    fill_table<kSmallChunkBytes>(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
+    k_clip_cluster<<<kCluster, kClusterThreads, 0, st>>>(tab, a.clip, a.max_norm, a.eps, a.outs == nullptr, a.norm, a.factor);
     return host_launched();
 }
 
-template <int N>
 lce_status_t launch_clip(const ClipCall &a, const HostDev &dev, double *part, cudaStream_t st) {
     lce_status_t s;
-    ClipTable<N> tab;
+    ClipTable tab;
     int n = 0;
     const int most = dev.sms * kSqBlocksPerSm < kMaxBlocks ? dev.sms * kSqBlocksPerSm : kMaxBlocks;
     for (int64_t at = 0; at < a.count;) {
-        fill_table<N, kChunkBytes>(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
+        fill_table<kChunkBytes>(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
         if (!tab.count) break;
         const int blocks = tab.chunks < most ? tab.chunks : most;
-        k_clip_squares<N><<<blocks, kSqThreads, 0, st>>>(tab, part + n);
+        k_clip_squares<<<blocks, kSqThreads, 0, st>>>(tab, part + n);
         if ((s = host_launched()) != LCE_OK) return s;
         n += blocks;
     }
@@ -338,10 +398,10 @@ lce_status_t launch_clip(const ClipCall &a, const HostDev &dev, double *part, cu
     }
     bool done = false;
     for (int64_t at = 0; at < a.count || !done;) {
-        fill_table<N, kChunkBytes>(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
+        fill_table<kChunkBytes>(tab, &at, a.count, a.grads, a.outs, a.sizes, a.dtypes);
         if (!tab.count && done) break;
         const int blocks = std::max(1, std::min(tab.chunks, dev.sms * kBlocksPerSm));
-        k_clip_scale<N><<<blocks, kClipThreads, 0, st>>>(tab, part, n, a.max_norm, a.eps, a.outs == nullptr, a.norm, a.factor);
+        k_clip_scale<<<blocks, kClipThreads, 0, st>>>(tab, part, n, a.max_norm, a.eps, a.outs == nullptr, a.norm, a.factor);
         if ((s = host_launched()) != LCE_OK) return s;
         done = true;
     }
@@ -356,12 +416,12 @@ lce_status_t run_clip(const ClipCall &a, void *workspace, size_t workspace_bytes
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (workspace && workspace_bytes < lce_clip_workspace_size(a.count)) return LCE_ERR_WORKSPACE;
     if (a.count <= kTable && count_chunks(a) <= kClusterChunks)
-        return a.count <= kShortTable ? launch_small<kShortTable>(a, st) : launch_small<kTable>(a, st);
+        return launch_small(a, st);
     HostScratch scratch(st);
     uint8_t *base = nullptr;
     if ((s = scratch.get(workspace, workspace_bytes, lce_clip_workspace_size(a.count), &base)) != LCE_OK) return s;
     double *part = reinterpret_cast<double *>(base);
-    return a.count <= kShortTable ? launch_clip<kShortTable>(a, dev, part, st) : launch_clip<kTable>(a, dev, part, st);
+    return launch_clip(a, dev, part, st);
 }
 
 }  // namespace

@@ -457,7 +457,7 @@ size_t lce_block_norm_workspace_size(const lce_norm_t *args);
  * runs and in fp64 across them, in a fixed order (deterministic); an element
  * beyond 1.8e19 makes the norm infinite. Scratch: lce_clip_workspace_size
  * bytes of device memory (16-byte aligned) or NULL (a stream-ordered
- * allocation; none for up to 2 MB of gradients, whose sums need no memory).
+ * allocation; none for up to 1 MB of gradients, whose sums need no memory).
  */
 size_t lce_clip_workspace_size(int64_t count);
 lce_status_t lce_grad_norm(int64_t count, const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
