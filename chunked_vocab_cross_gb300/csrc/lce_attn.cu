@@ -127,13 +127,16 @@ lce_status_t forward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &d
     return launch<k_attn_fwd<KS>>(dev, work, kFwdThreads, FwdSmem<KS>::kBytes, st, r, maps);
 }
 
+// DP: channels rounded up to 32, 64 or 128 (512 tokens, 4 heads, causal, forward and backward: 32 channels 34 and 53 us,
+// 64: 42 and 76, 128, or any as 128: 71 and 126).
 template <int DP>
 lce_status_t forward_simt(const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
     const int64_t slots = seq_slots(r.sq.T, r.sq.B, kSimtTile);
     return launch<k_attn_fwd_simt<DP>>(dev, slots * r.Hq, kSimtThreads, simt_smem(DP, 3, 1), st, r);
 }
 
-// Row statistics: 16 bytes a lane, as many lanes a row as it needs (8, 16 or 32).
+// Row statistics: 16 bytes a lane, as many lanes a row as it needs (8, 16 or 32; 32 heads of 64 channels over 1024
+// tokens: the backward takes 27.1 us with 8, 28.2 with 16).
 template <typename T, int TILE>
 lce_status_t row_stats(const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
     const int64_t blocks = seq_slots(r.sq.T, r.sq.B, TILE) * r.Hq;
@@ -166,7 +169,9 @@ lce_status_t backward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &
     return launch<k_attn_bwd<KS>, true>(dev, dq + dkv, kBwdThreads, BwdSmem<KS>::kBytes, st, r, maps, static_cast<int>(dkv));
 }
 
-// The tensor-core kernels exist for 64, 80, 96 and 128 channels; others run as the next of these.
+// The tensor-core kernels exist for 64, 80, 96 and 128 channels; others run as the next of these (8192 tokens in
+// sequences of 1024, causal, forward and backward: 32 heads of 64 channels 60 and 173 us, as 128 channels 69 and 222;
+// 16 heads of 80: 39 and 104, 41 and 119; of 96: 40 and 109, 44 and 121).
 template <typename F>
 lce_status_t by_channels(int64_t D, F f) {
     if (D <= 64) return f(std::integral_constant<int, 4>());

@@ -163,9 +163,9 @@ constexpr int kStatThreads = 256;
 // Row statistics of the backward, by slot: delta_i = dO_i . o_i in fp32 and
 // lse_i in base 2, both negated, so that the gradient kernels read aligned rows
 // of TILE values and add them. Rows without an allowed key (lse = -inf) and rows
-// past a sequence's end get -inf: their probabilities come out as 2^-inf = 0. LPR lanes
-// take a row, 16 bytes each; a thread asks for all its rows before it adds any
-// up, since the kernel is nothing but waits for memory.
+// past a sequence's end get -inf: their probabilities come out as 2^-inf = 0.
+// LPR lanes take a row, 16 bytes each; a thread asks for all its rows before it
+// adds any up, since the kernel is nothing but waits for memory.
 template <typename T, int TILE, int LPR>
 __global__ void __launch_bounds__(kStatThreads) k_attn_stats(const AttnArgs a) {
     using V = typename std::conditional<sizeof(T) == 4, float4, uint4>::type;

@@ -28,6 +28,13 @@
 // by cluster launch control, as in the forward; the loads and the first
 // products of the next run under the last sums and the output of the one
 // before. Both kinds are one grid, the longer dK/dV pieces first.
+//
+// Measured with 32 query and 8 key heads of 128 channels, causal, row statistics
+// included: one sequence of 8192 tokens 1.09 ms (1.26 PFLOP/s of the five
+// products that the mask leaves, 1.8 of the seven taken; 1.19 ms in long runs,
+// where power holds the clock near 1.5 GHz), sequences of 1024 211 us, of 128
+// 132 us; 32 heads of 64 channels over 3482 ragged tokens 80 us. Sixteen warps for the elementwise
+// part, four threads a row, gained 2 us there and lost 40 on 8192 tokens.
 #pragma once
 
 #include <stddef.h>
@@ -43,7 +50,7 @@ struct BwdSmem : Chan<KS> {
     using Chan<KS>::kTile;
     static constexpr int kAs = 3, kBs = 2;                             // ring slots
     static constexpr int kA = 2 * kTile, kB = kA + kAs * kTile;        // after the fixed tiles
-    static constexpr int kStat = 2 * kTcTile * 4;                      // lse2 and delta of a Q tile; two slots
+    static constexpr int kStat = 2 * kTcTile * 4;                      // nlse2 and ndelta of a Q tile; two slots
     static constexpr int kStats = kB + kBs * kTile;
     static constexpr int kBars = kStats + 2 * kStat;
     static constexpr int kBytes = kBars + 512;   // no room for alignment slack: the kernel checks the base it gets

@@ -3,7 +3,11 @@
 // (or key rows) and every 16th row of the other side, or DP/16 channels. Rows
 // are four floats longer than their data, so that both the reads along a row
 // (16 bytes at a time, 16 rows apart by lane) and those across it are free of
-// bank conflicts; 16-byte reads bring eight loads for 64 multiply-adds.
+// bank conflicts; 16-byte reads bring eight loads for 64 multiply-adds. What
+// bounds it is the multiply-adds with those loads, and at a few hundred tokens
+// the walk of the longest row (512 tokens, 4 heads of 64 channels, causal:
+// forward 42 us, backward 76). Training runs in bf16; this is for the small
+// fp32 configurations and for checking.
 #pragma once
 
 #include "lce_attn.cuh"

@@ -96,8 +96,9 @@ constexpr uint32_t kFmtBf16 = 1u;   // operand format code of bf16 in the f16-ki
 
 enum DevStatus : int { DEV_TARGET_RANGE = 1, DEV_TIMEOUT = 2 };
 
-// Device status word (LCE_DEV_* bits). The library is one translation unit,
-// so this header is the single definition.
+// Device status word (LCE_DEV_* bits). Only one translation unit of the library
+// takes this header, so it is the single definition; the others are given its
+// address (lce_host.h).
 __device__ int g_status = 0;
 
 __host__ __device__ inline int cdiv(int a, int b) { return (a + b - 1) / b; }

@@ -97,7 +97,9 @@ __device__ __forceinline__ void block_sum(float (&v)[K], float *red, int &flip) 
         for (int k = 0; k < K; ++k) v[k] += at[w * K + k];
 }
 
-// One block a row; a thread holds CH packs of its row's elements.
+// Few rows: one block a row, a thread holds CH packs of its row's elements.
+// What bounds it is latency: a launch, the loads, two sums over the block
+// (one row of 4096 bf16: 3.1 us, 305 rows 4.2 us).
 template <typename T, int CH>
 __global__ void __launch_bounds__(512) k_norm_fwd(const NormArgs a) {
     __shared__ float red[64];
@@ -179,7 +181,9 @@ __global__ void __launch_bounds__(512) k_norm_fwd(const NormArgs a) {
     }
 }
 
-// Persistent blocks, one row at a time. The two row sums of the formulas are
+// Rows too wide for the ring kernels below: persistent blocks, one row at a
+// time. What bounds it is latency, with nothing loaded ahead (8192 rows of 8192
+// bf16 took it 474 us; the ring 141, or 233 without kAll). The two row sums of the formulas are
 // taken in one round: with u = w_pre dn, m1 = mean(u rhat) and
 // z = scale gate w_post bhat, the second is
 //   sum(w_post dy bhat) = sum z (dr + rstd_pre u) - rstd_pre m1 sum z rhat.
@@ -298,9 +302,14 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormArgs a) {
 // consecutive rows, each taken by `tpr` threads with CH packs of 16 bytes;
 // the groups join their sums on barriers of their own and so cover each
 // other's waits. Weights (ones where there are none) stay in shared memory.
-// The work between two rows is mostly issue slots: hence the packed fp32
-// arithmetic, 16 to 32 elements a thread against the fixed cost of a sum, and
-// no branches on the options inside a row.
+// What bounds them is HBM, once the work between two rows hides behind it. That
+// work is mostly issue slots: hence the packed fp32 arithmetic, 16 to 32
+// elements a thread against the fixed cost of a sum, and no branches on the
+// options inside a row. The forward's inputs and outputs ask to leave L2 first
+// (16384 rows of 4096 bf16 from HBM: 89 us, 95 without; the backward gains
+// nothing from that). At that size, with norms on both sides and a gate per
+// channel: forward 89 us (6.0 TB/s), 125 with a block for each row; backward
+// 138 us with the 4 us of k_norm_cols (5.8 TB/s).
 struct RingGeo {
     int tpr, groups, stages;
     uint32_t row_bytes, array_bytes, stage_bytes;   // of one row; of one array's rows; of a stage
@@ -363,14 +372,13 @@ __device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, int *s
     return true;
 }
 
-// The arrays of a ring, copied by thread 0 of the block.
-template <typename T, int MAX>
+// The arrays of a ring, copied by thread 0 of the block. kOnce: first to leave L2.
+template <typename T, int MAX, bool kOnce>
 struct RingSource {
     const T *src[MAX];
     int64_t ld[MAX];   // row strides, elements
     // Starts the copies of the `per` rows from r0 on into stage s, if there are
-    // any. Rows past the last are copies of the last: they take part with
-    // factors of zero and are not stored.
+    // any. Rows past the last arrive as copies of the last.
     __device__ __forceinline__ void issue(uint8_t *ring, RingBars &bars, const RingGeo &g, int per, int s, int64_t r0, int64_t N, int d) const {
         if (r0 >= N) return;
         int count = 0;
@@ -381,10 +389,13 @@ struct RingSource {
 #pragma unroll
         for (int k = 0; k < MAX; ++k) {
             if (!src[k]) continue;
-            if (ld[k] == d && r0 + per <= N) bulk_load(dst, src[k] + r0 * d, per * g.row_bytes, &bars.full[s]);
+            auto load = [&](uint8_t *to, const T *from, uint32_t bytes) {
+                if (kOnce) bulk_load_once(to, from, bytes, &bars.full[s]);
+                else bulk_load(to, from, bytes, &bars.full[s]);
+            };
+            if (ld[k] == d && r0 + per <= N) load(dst, src[k] + r0 * d, per * g.row_bytes);
             else
-                for (int r = 0; r < per; ++r)
-                    bulk_load(dst + r * g.row_bytes, src[k] + min(r0 + r, N - 1) * ld[k], g.row_bytes, &bars.full[s]);
+                for (int r = 0; r < per; ++r) load(dst + r * g.row_bytes, src[k] + min(r0 + r, N - 1) * ld[k], g.row_bytes);
             dst += g.array_bytes;
         }
     }
@@ -452,7 +463,7 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float *red, int &flip, 
     for (int k = 0; k < K; ++k) v[k] = K == 1 ? x[0] : __shfl_sync(0xffffffffu, x[0], 4 * k);
 }
 
-// Weights of a row into shared memory, `rows` of them (ones where there is none)
+// Weights of a row into shared memory (ones where there are none)
 template <typename T>
 __device__ __forceinline__ void load_weights(uint8_t *dst, const void *w, int row_bytes) {
     constexpr uint32_t o = Pack16<T>::kOnes;
@@ -463,7 +474,8 @@ __device__ __forceinline__ void load_weights(uint8_t *dst, const void *w, int ro
 constexpr int kRedFloats = 2 * 8 * 16;   // of a row group
 
 // kAll: b, w_post and w_pre are there and the gate, if any, is per channel; the
-// options are then known when the kernel is compiled.
+// options are then known when the kernel is compiled (4096 rows of 4096 bf16:
+// 21.1 us against 22.8; no difference where HBM alone bounds it).
 template <typename T, int CH, bool kAll>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArgs a, const RingGeo g) {
     constexpr int V = kPack<T>, P = V / 2;
@@ -486,7 +498,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
     __syncthreads();
     const int64_t step = static_cast<int64_t>(gridDim.x) * g.groups;
     int64_t r0 = static_cast<int64_t>(blockIdx.x) * g.groups;
-    const RingSource<T, 3> src = {{static_cast<const T *>(a.x), static_cast<const T *>(a.b), full_gate ? static_cast<const T *>(a.gate) : nullptr},
+    const RingSource<T, 3, true> src = {{static_cast<const T *>(a.x), static_cast<const T *>(a.b), full_gate ? static_cast<const T *>(a.gate) : nullptr},
                                   {a.ld_x, a.ld_b, a.ld_gate}};
     if (threadIdx.x == 0)
         for (int i = 0; i < g.stages; ++i) src.issue(smem, bars, g, g.groups, i, r0 + i * step, a.N, d);
@@ -549,7 +561,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
                     Pack16<T>::get(full_gate ? vg[c] : *reinterpret_cast<const uint4 *>(gate + byte), w);
 #pragma unroll
                     for (int i = 0; i < P; ++i) r[c][i] = fma2(mul2(y[i], w[i]), f, r[c][i]);
-                    if (live) *reinterpret_cast<uint4 *>(out_r + c * g.tpr * 16) = Pack16<T>::set(r[c]);
+                    if (live) __stcs(reinterpret_cast<uint4 *>(out_r + c * g.tpr * 16), Pack16<T>::set(r[c]));
                 }
             }
         }
@@ -582,7 +594,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
                 Pack16<T>::get(*reinterpret_cast<const uint4 *>(w_pre + byte), w);
 #pragma unroll
                 for (int i = 0; i < P; ++i) w[i] = mul2(mul2(r[c][i], f), w[i]);
-                if (live) *reinterpret_cast<uint4 *>(out_n + c * g.tpr * 16) = Pack16<T>::set(w);
+                if (live) __stcs(reinterpret_cast<uint4 *>(out_n + c * g.tpr * 16), Pack16<T>::set(w));
             }
         }
         if (++s == g.stages) s = 0, phase ^= 1;
@@ -595,10 +607,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
 //   m1 = mean(u hat),  m2 = f (sum z t - rstd_pre m1 sum z hat) / d,
 //   dx = t - rstd_pre m1 hat,  e = f dx:  dgate = e b w_post,
 //   dw_post = e gate b,  db = e gate w_post - rstd_post^2 m2 b   (no w_post: the last term is 0).
-// A thread takes its columns of R rows at a time, which halves what it spends
-// on weights. The column sums stay in registers, one set a row group, and are
+// A thread takes its columns of R = 2 rows at a time where it has the registers,
+// which halves what it spends on weights (16384 rows of 4096 bf16: 140 us, 192
+// with one). The column sums stay in registers, one set a row group, and are
 // joined across the groups in shared memory at the end.
-// kAll: dr, dn, b and w_pre are there and the gate, if any, is per channel.
+// kAll: dr, dn, b and w_pre are there and the gate, if any, is per channel
+// (139 us, 141 without; 8192 rows of 8192, where the registers run out without
+// it: 141 and 233).
 template <typename T, int CH, int R, bool kAll>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArgs a, const RingGeo g) {
     constexpr int V = kPack<T>, P = V / 2;
@@ -622,7 +637,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
     const int per = g.groups * R;   // rows of a stage
     const int64_t step = static_cast<int64_t>(gridDim.x) * per;
     int64_t r0 = static_cast<int64_t>(blockIdx.x) * per;
-    const RingSource<T, 5> src = {{a.w_pre ? static_cast<const T *>(a.r_in) : nullptr, a.w_pre ? static_cast<const T *>(a.dn) : nullptr,
+    const RingSource<T, 5, false> src = {{a.w_pre ? static_cast<const T *>(a.r_in) : nullptr, a.w_pre ? static_cast<const T *>(a.dn) : nullptr,
                                    static_cast<const T *>(a.b), full_gate ? static_cast<const T *>(a.gate) : nullptr, static_cast<const T *>(a.dr)},
                                   {a.ld_r, a.ld_dn, a.ld_b, a.ld_gate, a.ld_dr}};
     // places of the arrays in a stage
@@ -660,7 +675,18 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
         rstd(row + step);
         // the vote also tells the compiler that the warp is together again
         if (!__all_sync(0xffffffffu, ring_wait(&bars.full[s], phase, a.status))) bars.gave_up[group] = 1;
-        const uint8_t *at = smem + s * g.stage_bytes + group * R * g.row_bytes;
+        uint8_t *at = smem + s * g.stage_bytes + group * R * g.row_bytes;
+        if (row + R > a.N) {   // rows past the last add nothing to the columns: zeros, as 0 * inf would
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    const int byte = (c * g.tpr + t) * 16;
+                    if (row + k < a.N || byte >= g.row_bytes) continue;
+                    for (uint8_t *p = at + k * g.row_bytes + byte, *end = smem + (s + 1) * g.stage_bytes; p < end; p += g.array_bytes)
+                        *reinterpret_cast<uint4 *>(p) = make_uint4(0, 0, 0, 0);
+                }
+        }
         f32x2 hat[R][CH][P], x[R][CH][P];
         uint4 vb[R][CH];
         f32x2 q[R][3];
@@ -809,11 +835,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
 }
 
 // Adds the blocks' column sums: eight quads of columns a block, 32 threads a
-// quad that each add every 32nd partial row, joined in a fixed order.
+// quad that each add every 32nd partial row, joined in a fixed order. Bounded by
+// latency: 4 us for 152 blocks' sums over 3 x 4096 columns (in L2).
 template <typename T>
 __global__ void __launch_bounds__(256) k_norm_cols(const float *part, int groups, int d, T *dw_pre, T *dw_post,
                                                    T *dgate) {
     __shared__ float4 red[32][8];
+    griddep_wait();
     T *out = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dgate;
     if (!out) return;
     const int x = threadIdx.x & 7, y = threadIdx.x / 8, col = (blockIdx.x * 8 + x) * 4;
@@ -894,12 +922,19 @@ int row_threads(int d) {
 int row_packs(int d) { return (d / kVec + 511) / 512; }
 
 constexpr int kRingBytes = 208 * 1024;   // dynamic shared memory of a ring kernel's block at most
+// Ring of the forward, if two stages do not take more: 128 KB are enough in flight, and less in turns is easier on
+// HBM (131072 rows of 512 bf16: 93 us, 94 with all of kRingBytes; 32768 rows of 2048: 88 us, 93).
+constexpr int kFwdRingBytes = 128 * 1024;
+// Few rows have nothing to run ahead of: up to this much of an array the forward takes a block for each row, with
+// fewer steps before its first load (rows of 4096 bf16: 305 in 4.2 us, 5.2 through the ring; 608 in 6.2 us, 5.4;
+// of 1024: 1216 in 3.6 us, 4.8; 4096 in 7.6 us, 7.0).
+constexpr int64_t kDirectBytes = 4 << 20;
 constexpr int kColGroups = 304;          // blocks of the backward at most (bounds its workspace)
 
 // The ring kernels' geometry for rows of d elements in `arrays` arrays, `ch`
 // packs a thread and `per` rows a group and stage; false where rows are too wide
 // for the threads of a block or for two stages.
-bool ring_geo(RingGeo *g, int d, int elt, int arrays, int ch, int per) {
+bool ring_geo(RingGeo *g, int d, int elt, int arrays, int ch, int per, int bytes) {
     const int packs = d * elt / 16;
     g->tpr = ((packs + ch - 1) / ch + 31) / 32 * 32;
     if (g->tpr > kRingThreads) return false;
@@ -907,11 +942,13 @@ bool ring_geo(RingGeo *g, int d, int elt, int arrays, int ch, int per) {
     g->row_bytes = d * elt;
     g->array_bytes = g->groups * per * g->row_bytes;
     g->stage_bytes = arrays * g->array_bytes;
-    g->stages = std::min(kRingMaxStages, static_cast<int>((kRingBytes - 3 * g->row_bytes) / g->stage_bytes));
-    return g->stages >= 2;
+    if (2 * g->stage_bytes + 3 * g->row_bytes > kRingBytes) return false;
+    g->stages = std::max(2, std::min(kRingMaxStages, static_cast<int>(std::min<int>(bytes, kRingBytes - 3 * g->row_bytes) / g->stage_bytes)));
+    return true;
 }
 
-// Packs a thread: as few as leave a row to 32 threads, at most `most`.
+// Packs a thread in the forward: as few as leave a row to 32 threads, at most
+// 32 elements (16384 rows of 4096 bf16: 95 us with four packs, 137 with one).
 int ring_packs(int d, int elt, int most) {
     int ch = 1;
     while (ch < most && d * elt / 16 > 32 * ch) ch *= 2;
@@ -938,9 +975,9 @@ lce_status_t forward(const lce_norm_t *a, const HostDev &dev, cudaStream_t st) {
     NormArgs r = make_norm(a);
     r.status = dev.status;
     RingGeo g;
-    // a few rows have nothing to run ahead of: one block a row, fewer steps before the first load
     const int ch = ring_packs(r.d, sizeof(T), 32 / kPack<T>);
-    if (a->N > 2 * dev.sms && ring_geo(&g, r.d, sizeof(T), (r.b ? 2 : 1) + (r.gate && r.gate_full ? 1 : 0), ch, 1)) {
+    const int arrays = (r.b ? 2 : 1) + (r.gate && r.gate_full ? 1 : 0);
+    if (a->N * r.d * static_cast<int64_t>(sizeof(T)) > kDirectBytes && ring_geo(&g, r.d, sizeof(T), arrays, ch, 1, kFwdRingBytes)) {
         const int grid = ring_grid(a->N, g.groups, dev.sms), smem = g.stages * g.stage_bytes + 3 * g.row_bytes;
         const bool all = r.b && r.w_post && r.w_pre && !(r.gate && r.gate_full);
         auto go = [&](auto c) {
@@ -975,10 +1012,11 @@ lce_status_t backward(const lce_norm_t *a, float *part, const HostDev &dev, cuda
     RingGeo g;
     int grid;
     lce_status_t s;
-    // two rows a thread while a row's packs go round once (their sums and the column sums fill the registers), else one
+    // two rows a thread while a row's packs go round once (their sums and the column sums fill the registers), else one;
+    // packs a thread: one, or as many as a row needs of 512 threads
     const int packs = r.d * static_cast<int>(sizeof(T)) / 16;
     const int ch = packs <= kRingThreads ? 1 : packs <= 2 * kRingThreads ? 2 : 16 / kPack<T>, per = ch == 1 ? 2 : 1;
-    if (ring_geo(&g, r.d, sizeof(T), arrays, ch, per)) {
+    if (ring_geo(&g, r.d, sizeof(T), arrays, ch, per, kRingBytes)) {
         grid = ring_grid(a->N, g.groups * per, dev.sms);
         const int smem = std::max<int>(g.stages * g.stage_bytes + 3 * g.row_bytes, g.groups * r.d * 4);
         const bool all = r.w_pre && r.b && r.dr && !full_gate;
@@ -999,17 +1037,27 @@ lce_status_t backward(const lce_norm_t *a, float *part, const HostDev &dev, cuda
             kernel<<<grid, th, smem, st>>>(r);
             return host_launched();
         };
-        switch (row_packs(r.d)) {
-            case 1: s = host_smem<k_norm_bwd<T, 1>>(dev, 3 * 4096 * 4); if (s == LCE_OK) s = go(k_norm_bwd<T, 1>); break;
-            case 2: s = host_smem<k_norm_bwd<T, 2>>(dev, 3 * 8192 * 4); if (s == LCE_OK) s = go(k_norm_bwd<T, 2>); break;
-            default: s = host_smem<k_norm_bwd<T, 4>>(dev, 3 * 16384 * 4); if (s == LCE_OK) s = go(k_norm_bwd<T, 4>); break;
-        }
+        // (over 8192 elements of bf16, over 4096 of fp32: the ring takes the others whatever the options)
+        constexpr int kWide = sizeof(T) == 4 ? 2 : 4;
+        if (row_packs(r.d) <= kWide) s = host_smem<k_norm_bwd<T, kWide>>(dev, 3 * kWide * 4096 * 4);
+        else s = host_smem<k_norm_bwd<T, 4>>(dev, 3 * 4 * 4096 * 4);
+        if (s == LCE_OK) s = row_packs(r.d) <= kWide ? go(k_norm_bwd<T, kWide>) : go(k_norm_bwd<T, 4>);
     }
     if (s != LCE_OK) return s;
     T *dgate = r.gate && !full_gate ? static_cast<T *>(a->dgate) : nullptr;
     T *dpre = r.w_pre ? static_cast<T *>(a->dw_pre) : nullptr, *dpost = r.w_post ? static_cast<T *>(a->dw_post) : nullptr;
     if (!dgate && !dpre && !dpost) return LCE_OK;
-    k_norm_cols<T><<<dim3((r.d + 31) / 32, 3), 256, 0, st>>>(part, grid, r.d, dpre, dpost, dgate);
+    // may start while the rows' kernel ends, and waits for it in the kernel
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((r.d + 31) / 32, 3);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if ((s = host_cuda(cudaLaunchKernelEx(&cfg, k_norm_cols<T>, static_cast<const float *>(part), grid, r.d, dpre, dpost, dgate))) != LCE_OK) return s;
     return host_launched();
 }
 

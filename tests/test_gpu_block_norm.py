@@ -158,6 +158,24 @@ def test_rows_of_zeros_and_not_finite():
     assert torch.equal(r2[keep], r[keep]) and torch.equal(n2[keep], n[keep]) and bool(n2[4].isnan().all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows", [1, 7, 33])
+def test_infinities_of_the_last_row_stay_infinities_in_the_column_sums(rows, dtype):
+    """An infinite gradient in the last row is an infinity in its own column's sums and nothing in the others'."""
+    t = make(rows, 256, dtype, True, "channel", True)
+    kw = dict(w_post=t["w_post"], gate=t["gate"], w_pre=t["w_pre"])
+    r, _, po, pr = lce.block_norm_forward(t["x"], t["b"], **kw)
+    t["dr"][rows - 1, 9] = float("inf")
+    dx, _, dw_post, dgate, dw_pre = lce.block_norm_backward(t["dr"], t["dn"], r, t["b"], rstd_post=po, rstd_pre=pr, **kw)
+    for got in (dx[rows - 1], dw_post, dgate):
+        assert torch.nonzero(~got.isfinite()).flatten().tolist() == [9] and bool(got[9].isinf())
+    assert bool(dw_pre.isfinite().all())
+    t["dr"][rows - 1, 9] = 0.0
+    t["dn"][rows - 1, 5] = float("-inf")
+    dw_pre = lce.block_norm_backward(t["dr"], t["dn"], r, t["b"], rstd_post=po, rstd_pre=pr, **kw)[4]
+    assert torch.nonzero(~dw_pre.isfinite()).flatten().tolist() == [5] and bool(dw_pre[5].isinf())
+
+
 def test_autograd_and_differences():
     """Central differences of the fp32 forward (h = 2^-7): truncation of order
     h^2, rounding of order 2^-24 |f| / h; the bound is 1e-2 of |grad||z|/sqrt(n)."""
