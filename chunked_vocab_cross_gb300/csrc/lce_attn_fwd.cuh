@@ -9,6 +9,8 @@
 // The maximum a row's exponents refer to moves only when it grows by more than
 // 2^8 (kLazy): until then P stays below 256 and O needs no rescaling, which
 // costs a round trip of O through registers. The last reference divides out.
+// kTwo: what rounding took from P goes in as a second bf16 operand, a product
+// more.
 //
 // What bounds it is shared memory: a product of 128 x 128 x 128 takes the
 // tensor core 512 cycles and reads 64 KB (S) or 32 KB (P V) there, at 128 bytes
@@ -82,7 +84,7 @@ struct FwdBars {
 };
 static_assert(sizeof(FwdBars) <= 512, "room after the maxima");
 
-template <int KS>
+template <int KS, bool kTwo>
 __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_constant__ AttnArgs a,
                                                              const __grid_constant__ AttnMaps maps) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -308,6 +310,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_consta
                 if (!wait.all(&bar.p_full[i][1], parity)) return false;
                 if (elect_one()) {
                     tc_fence_after();
+                    if constexpr (kTwo) {
+                        tc_mma_tokens_chunk<0>(tm + 256 + i * 128, tm + i * 128 + 32, dv + slot * kStep, idO, true);
+                        tc_mma_tokens_chunk<1>(tm + 256 + i * 128, tm + i * 128 + 32, dv + slot * kStep, idO, true);
+                    }
                     tc_mma_tokens_chunk<1>(tm + 256 + i * 128, tm + i * 128, dv + slot * kStep, idO, true);
                     umma_commit(&bar.o_done[i]);
                     if (done) umma_commit(&bar.v_empty[slot]);
@@ -441,7 +447,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_consta
                 // P in two steps, so that the first half of O's step runs under the second half of the exponents
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t p[16];
+                    uint32_t p[16], rest[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float x, y;
@@ -449,8 +455,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_consta
                         x = ex2(x), y = ex2(y);
                         l2 = add2(l2, pack2(x, y));
                         p[i] = pack_bf16(x, y);
+                        if constexpr (kTwo) rest[i] = pack_bf16(x - __uint_as_float(p[i] << 16), y - __uint_as_float(p[i] & 0xffff0000u));
                     }
                     tmem_st16(tSh + c * 16, p);
+                    if constexpr (kTwo) tmem_st16(tSh + 32 + c * 16, rest);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();

@@ -367,7 +367,8 @@ lce_status_t lce_embedding_backward_bf16(lce_dtype_t dtype, const void *dE, cons
  * share its 128-token tile.
  *
  * dtype LCE_BF16 runs on the bf16 tensor cores with fp32 accumulation (the
- * probabilities and their gradient are rounded to bf16 once, as operands);
+ * probabilities and their gradient are rounded to bf16 once, as operands; to
+ * two bf16 parts where Tq*Hq*D <= 2^18 and sequences average at most 512);
  * LCE_FP32 runs in fp32 arithmetic throughout. Requirements: 1 <= D <= 128,
  * D % 8 == 0, Hq a multiple of Hk, 0 <= Tq, Tk < 2^30, 1 <= B < 2^30, Tq and Tk multiples
  * of B without offsets; bases 16-byte aligned, strides multiples of 16 bytes,

@@ -1,8 +1,8 @@
 """Attention over packed sequences and its backward pass, through the public
 entry points, against the fp64 reference.
 
-Tolerances, elementwise, from the arithmetic (u = 2^-8 covers a rounding to
-bf16, at most 2^-9, twice over; e = 2^-24 is fp32's):
+Tolerances, elementwise, from the arithmetic (u = 2^-8 is bf16's unit
+roundoff, e = 2^-24 fp32's):
   forward   |err| <= u (|o| + sum p|v|) + F sum p|v|
   gradients |err| <= u (|g| + terms) + F parts
 where `terms` are the absolute terms the rounded operands (p, ds) enter with,
@@ -102,6 +102,47 @@ def test_bf16_lengths(lens, causal, D):
     check(lq, lk, 4, 2, D, causal, "bf16", tail=0 if lens == "one" else 3)
 
 
+def longer(lens):
+    """Tokens after the last sequence that make the call one of long rows, whose P and dS go in as one bf16 operand."""
+    return 513 * len(lens)
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("lens", list(LENS), ids=lambda s: s.replace(" ", "_"))
+@pytest.mark.parametrize("D", [64, 128])
+def test_bf16_lengths_one_part(lens, causal, D):
+    lq, lk = LENS[lens]
+    check(lq, lk, 4, 2, D, causal, "bf16", tail=longer(lq), seed=1)
+
+
+@pytest.mark.parametrize("D", [8, 24, 72, 80, 96, 104])
+def test_bf16_head_sizes_one_part(D):
+    check([150, 40], [150, 40], 2, 1, D, True, "bf16", tail=longer([150, 40]), seed=D)
+
+
+@pytest.mark.parametrize("heads", [(1, 1), (7, 1), (6, 3), (8, 8), (12, 4)], ids=lambda h: f"{h[0]}_{h[1]}")
+def test_bf16_head_layouts_one_part(heads):
+    check([200, 57], [200, 57], *heads, 64, True, "bf16", tail=longer([200, 57]), seed=2)
+    check([200, 57], [90, 157], *heads, 128, False, "bf16", tail=longer([200, 57]), seed=3)
+
+
+@pytest.mark.parametrize("heads,D", [((8, 8), 64), ((4, 1), 128)], ids=["8x64", "4of1x128"])
+def test_small_calls_lose_little_more_than_the_rounding_of_the_result(heads, D):
+    """Rounding values of any size to bf16 costs 2^-8 / sqrt(3) * sqrt(mean
+    1/m^2) = 0.00166 of their norm for significands m spread evenly over their
+    logarithm; a second rounding, of P or dS, would make it 0.00235. Small
+    calls keep the first: 0.0020 leaves a fifth for the sizes that come up."""
+    lens = [256]
+    q, k, v, do = make(lens, lens, *heads, D, "bf16", seed=11)
+    o, lse = lce.attention_forward(q, k, v)
+    grads = lce.attention_backward(do, q, k, v, o, lse)
+    want = [bo.attention_forward(f64(q), f64(k), f64(v), lens, lens, True, D ** -0.5)[0]]
+    ref = bo.attention_backward(f64(do), f64(q), f64(k), f64(v), f64(o), f64(lse), lens, lens, True, D ** -0.5)
+    want += [ref[n][0] for n in ("dq", "dk", "dv")]
+    for t, w in zip((o, *grads), want):
+        assert np.linalg.norm(f64(t) - w) <= 0.0020 * np.linalg.norm(w)
+
+
 @pytest.mark.parametrize("D", [8, 16, 24, 40, 56, 72, 80, 96, 104, 120])
 def test_bf16_head_sizes(D):
     check([150, 40], [150, 40], 2, 1, D, True, "bf16", seed=D)
@@ -143,12 +184,13 @@ def test_growing_maximum():
         assert np.all(np.abs(f64(o) - ro) <= 2.0 ** -8 * (np.abs(ro) + abs_o) + F * abs_o)
 
 
-def test_sequences_do_not_reach_each_other():
+@pytest.mark.parametrize("heads", [4, 16])
+def test_sequences_do_not_reach_each_other(heads):
     """NaN and infinities in one sequence and in the tokens after the last: the
     others' results are those without them, bit for bit."""
     for dtype in ("bf16", "fp32"):
         lens = [100, 60, 131, 9]
-        q, k, v, do = make(lens, lens, 4, 2, 64, dtype, tail=20)
+        q, k, v, do = make(lens, lens, heads, 2, 64, dtype, tail=20)
         run = lambda: lce.attention_forward(q, k, v, cu(lens))  # noqa: E731
         o, lse = run()
         grads = lce.attention_backward(do, q, k, v, o, lse, cu(lens))
@@ -170,9 +212,10 @@ def test_sequences_do_not_reach_each_other():
         lce.device_status()
 
 
-def test_masked_keys_that_are_not_finite_do_not_change_earlier_scores():
+@pytest.mark.parametrize("heads", [2, 24])
+def test_masked_keys_that_are_not_finite_do_not_change_earlier_scores(heads):
     """Causal: a key of NaN or infinity beyond a row's reach leaves the row's lse as it is."""
-    q, k, v, _ = make([200], [200], 2, 2, 64, "bf16")
+    q, k, v, _ = make([200], [200], heads, 2, 64, "bf16")
     _, lse = lce.attention_forward(q, k, v)
     k[150:] = float("nan")
     _, lse2 = lce.attention_forward(q, k, v)
