@@ -88,8 +88,7 @@ lce_status_t encode(CUtensorMap *m, const HostDev &dev, const void *p, int64_t T
     return r == CUDA_SUCCESS ? LCE_OK : LCE_ERR_SHAPE;
 }
 
-// kEarly: the launch may begin before the one ahead of it in the stream has
-// ended, and waits in the kernel where it reads what that one wrote.
+// kEarly: see host_launch_early.
 template <auto kKernel, bool kEarly = false, typename... A>
 lce_status_t launch(const HostDev &dev, int64_t blocks, int threads, int smem, cudaStream_t st, const A &...args) {
     if (blocks >= (int64_t(1) << 31)) return LCE_ERR_SHAPE;
@@ -97,22 +96,9 @@ lce_status_t launch(const HostDev &dev, int64_t blocks, int threads, int smem, c
         const lce_status_t s = host_smem<kKernel>(dev, smem);
         if (s != LCE_OK) return s;
     }
-    if constexpr (kEarly) {
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-        cfg.blockDim = dim3(threads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = st;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        const lce_status_t s = host_cuda(cudaLaunchKernelEx(&cfg, kKernel, args...));
-        if (s != LCE_OK) return s;
-    } else {
-        kKernel<<<static_cast<unsigned>(blocks), threads, smem, st>>>(args...);
-    }
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if constexpr (kEarly) return host_launch_early(kKernel, grid, threads, smem, st, args...);
+    kKernel<<<grid, threads, smem, st>>>(args...);
     return host_launched();
 }
 

@@ -75,6 +75,25 @@ lce_status_t host_smem(const HostDev &dev, int bytes) {
     return s;
 }
 
+// A launch that may begin before the one ahead of it in the stream has ended
+// (once all its blocks have allowed it, or ended), and waits in the kernel
+// where it reads what that one wrote.
+template <typename... P, typename... A>
+lce_status_t host_launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, const A &...args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const lce_status_t s = host_cuda(cudaLaunchKernelEx(&cfg, kernel, P(args)...));
+    return s != LCE_OK ? s : host_launched();
+}
+
 inline bool host_misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 }  // namespace lce

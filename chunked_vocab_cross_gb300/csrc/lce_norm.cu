@@ -1047,18 +1047,7 @@ lce_status_t backward(const lce_norm_t *a, float *part, const HostDev &dev, cuda
     T *dgate = r.gate && !full_gate ? static_cast<T *>(a->dgate) : nullptr;
     T *dpre = r.w_pre ? static_cast<T *>(a->dw_pre) : nullptr, *dpost = r.w_post ? static_cast<T *>(a->dw_post) : nullptr;
     if (!dgate && !dpre && !dpost) return LCE_OK;
-    // may start while the rows' kernel ends, and waits for it in the kernel
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((r.d + 31) / 32, 3);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if ((s = host_cuda(cudaLaunchKernelEx(&cfg, k_norm_cols<T>, static_cast<const float *>(part), grid, r.d, dpre, dpost, dgate))) != LCE_OK) return s;
-    return host_launched();
+    return host_launch_early(k_norm_cols<T>, dim3((r.d + 31) / 32, 3), 256, 0, st, part, grid, r.d, dpre, dpost, dgate);
 }
 
 }  // namespace
