@@ -11,8 +11,9 @@ using namespace lce;
 namespace {
 
 // What bounds both passes is HBM: 1.6 GB of bf16 in 20 tensors take 730 us, 4.8 GB at 6.6 TB/s (the squares alone
-// 245 us). The second launch begins under the first (60 MB 26.8 -> 26.4 us, 8 MB norm alone 6.2 -> 5.6). The squares run best in many small blocks (191 us for 1.2 GB; 217 in blocks of 512 threads), the scaling
-// in fewer, since each adds up all blocks' sums first (362 us; 371).
+// 245 us). The second launch begins under the first (60 MB 26.8 -> 26.4 us, the norm alone of 8 MB 6.2 -> 5.6). The
+// squares run best in many small blocks (191 us for 1.2 GB; 217 in blocks of 512 threads), the scaling in fewer, since
+// each adds up all blocks' sums first (362 us; 371).
 constexpr int kSqThreads = 256, kSqBlocksPerSm = 8;
 constexpr int kClipThreads = 512;
 constexpr int kChunkBytes = 65536;   // bytes of a tensor that a block takes at a time: eight loads a thread

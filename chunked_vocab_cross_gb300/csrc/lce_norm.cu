@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(512) k_norm_fwd(const NormArgs a) {
 
 // Rows too wide for the ring kernels below: persistent blocks, one row at a
 // time. What bounds it is latency, with nothing loaded ahead (8192 rows of 8192
-// bf16 took it 474 us; the ring 141, or 233 without kAll). The two row sums of the formulas are
-// taken in one round: with u = w_pre dn, m1 = mean(u rhat) and
+// bf16 took it 474 us, the ring 141). The two row sums of the formulas are taken
+// in one round: with u = w_pre dn, m1 = mean(u rhat) and
 // z = scale gate w_post bhat, the second is
 //   sum(w_post dy bhat) = sum z (dr + rstd_pre u) - rstd_pre m1 sum z rhat.
 // Column sums (weights, a gate per channel) stay in shared memory, each
@@ -310,6 +310,8 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormArgs a) {
 // nothing from that). At that size, with norms on both sides and a gate per
 // channel: forward 89 us (6.0 TB/s), 125 with a block for each row; backward
 // 138 us with the 4 us of k_norm_cols (5.8 TB/s).
+enum NormMode : int { NORM_ANY, NORM_ALL, NORM_FULL_GATE, NORM_NO_DR, NORM_PRE, NORM_POST };
+
 struct RingGeo {
     int tpr, groups, stages;
     uint32_t row_bytes, array_bytes, stage_bytes;   // of one row; of one array's rows; of a stage
@@ -473,10 +475,11 @@ __device__ __forceinline__ void load_weights(uint8_t *dst, const void *w, int ro
 
 constexpr int kRedFloats = 2 * 8 * 16;   // of a row group
 
-// kAll: b, w_post and w_pre are there and the gate, if any, is per channel; the
-// options are then known when the kernel is compiled (4096 rows of 4096 bf16:
+// NORM_ALL: b, w_post and w_pre are there and the gate, if any, is per channel;
+// NORM_FULL_GATE: with a gate per element. Those options are known when the
+// kernel is compiled (4096 rows of 4096 bf16:
 // 21.1 us against 22.8; no difference where HBM alone bounds it).
-template <typename T, int CH, bool kAll>
+template <typename T, int CH, int kMode>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArgs a, const RingGeo g) {
     constexpr int V = kPack<T>, P = V / 2;
     extern __shared__ __align__(128) uint8_t smem[];   // ring, then w_post, gate, w_pre
@@ -489,7 +492,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
         fence_mbar_init();
     }
     const int d = a.d;
-    const bool has_b = kAll || a.b, has_post = kAll || a.w_post, has_pre = kAll || a.w_pre, full_gate = !kAll && a.gate && a.gate_full;
+    const bool has_b = kMode || a.b, has_post = kMode || a.w_post, has_pre = kMode || a.w_pre,
+               full_gate = kMode == NORM_FULL_GATE || (kMode == NORM_ANY && a.gate && a.gate_full);
     uint8_t *w_post = smem + g.stages * g.stage_bytes, *gate = w_post + g.row_bytes, *w_pre = gate + g.row_bytes;
     load_weights<T>(w_post, a.w_post, g.row_bytes);
     load_weights<T>(gate, full_gate ? nullptr : a.gate, g.row_bytes);
@@ -611,10 +615,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
 // which halves what it spends on weights (16384 rows of 4096 bf16: 140 us, 192
 // with one). The column sums stay in registers, one set a row group, and are
 // joined across the groups in shared memory at the end.
-// kAll: dr, dn, b and w_pre are there and the gate, if any, is per channel
-// (139 us, 141 without; 8192 rows of 8192, where the registers run out without
-// it: 141 and 233).
-template <typename T, int CH, int R, bool kAll>
+// What is there is known when the kernel is compiled, since the registers go
+// to what might be: NORM_ALL: dr, dn, b and w_pre, and a gate per channel if
+// any; NORM_NO_DR: the same without dr; NORM_FULL_GATE: a gate per element;
+// NORM_PRE: no b; NORM_POST: no w_pre (8192 rows of 8192 bf16: 140, 131,
+// 171, 100 and 125 us; with options read in the kernel 233 for the first, 320,
+// 379, 270 and 295).
+template <typename T, int CH, int R, int kMode>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArgs a, const RingGeo g) {
     constexpr int V = kPack<T>, P = V / 2;
     extern __shared__ __align__(128) uint8_t smem[];   // ring, then w_post, gate, w_pre
@@ -627,7 +634,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd_ring(const NormArg
         fence_mbar_init();
     }
     const int d = a.d;
-    const bool has_pre = kAll || a.w_pre, has_b = kAll || a.b, has_dr = kAll || a.dr, full_gate = !kAll && a.gate && a.gate_full;
+    const bool has_pre = kMode != NORM_POST, has_b = kMode != NORM_PRE, has_dr = kMode == NORM_ALL || (kMode != NORM_NO_DR && a.dr),
+               full_gate = kMode == NORM_FULL_GATE || (kMode == NORM_POST && a.gate && a.gate_full);
     uint8_t *w_post = smem + g.stages * g.stage_bytes, *gate = w_post + g.row_bytes, *w_pre = gate + g.row_bytes;
     load_weights<T>(w_post, a.w_post, g.row_bytes);
     load_weights<T>(gate, full_gate ? nullptr : a.gate, g.row_bytes);
@@ -979,11 +987,12 @@ lce_status_t forward(const lce_norm_t *a, const HostDev &dev, cudaStream_t st) {
     const int arrays = (r.b ? 2 : 1) + (r.gate && r.gate_full ? 1 : 0);
     if (a->N * r.d * static_cast<int64_t>(sizeof(T)) > kDirectBytes && ring_geo(&g, r.d, sizeof(T), arrays, ch, 1, kFwdRingBytes)) {
         const int grid = ring_grid(a->N, g.groups, dev.sms), smem = g.stages * g.stage_bytes + 3 * g.row_bytes;
-        const bool all = r.b && r.w_post && r.w_pre && !(r.gate && r.gate_full);
+        const int mode = !(r.b && r.w_post && r.w_pre) ? NORM_ANY : r.gate && r.gate_full ? NORM_FULL_GATE : NORM_ALL;
         auto go = [&](auto c) {
             constexpr int CH = decltype(c)::value;
-            return all ? launch_ring<k_norm_fwd_ring<T, CH, true>>(dev, r, g, grid, smem, st)
-                       : launch_ring<k_norm_fwd_ring<T, CH, false>>(dev, r, g, grid, smem, st);
+            return mode == NORM_ALL         ? launch_ring<k_norm_fwd_ring<T, CH, NORM_ALL>>(dev, r, g, grid, smem, st)
+                   : mode == NORM_FULL_GATE ? launch_ring<k_norm_fwd_ring<T, CH, NORM_FULL_GATE>>(dev, r, g, grid, smem, st)
+                                            : launch_ring<k_norm_fwd_ring<T, CH, NORM_ANY>>(dev, r, g, grid, smem, st);
         };
         switch (ch) {
             case 1: return go(std::integral_constant<int, 1>());
@@ -1019,11 +1028,16 @@ lce_status_t backward(const lce_norm_t *a, float *part, const HostDev &dev, cuda
     if (ring_geo(&g, r.d, sizeof(T), arrays, ch, per, kRingBytes)) {
         grid = ring_grid(a->N, g.groups * per, dev.sms);
         const int smem = std::max<int>(g.stages * g.stage_bytes + 3 * g.row_bytes, g.groups * r.d * 4);
-        const bool all = r.w_pre && r.b && r.dr && !full_gate;
+        const int mode = !r.w_pre ? NORM_POST : !r.b ? NORM_PRE : full_gate ? NORM_FULL_GATE : r.dr ? NORM_ALL : NORM_NO_DR;
         auto go = [&](auto c, auto rows) {
             constexpr int CH = decltype(c)::value, R = decltype(rows)::value;
-            return all ? launch_ring<k_norm_bwd_ring<T, CH, R, true>>(dev, r, g, grid, smem, st)
-                       : launch_ring<k_norm_bwd_ring<T, CH, R, false>>(dev, r, g, grid, smem, st);
+            switch (mode) {
+                case NORM_ALL: return launch_ring<k_norm_bwd_ring<T, CH, R, NORM_ALL>>(dev, r, g, grid, smem, st);
+                case NORM_NO_DR: return launch_ring<k_norm_bwd_ring<T, CH, R, NORM_NO_DR>>(dev, r, g, grid, smem, st);
+                case NORM_FULL_GATE: return launch_ring<k_norm_bwd_ring<T, CH, R, NORM_FULL_GATE>>(dev, r, g, grid, smem, st);
+                case NORM_PRE: return launch_ring<k_norm_bwd_ring<T, CH, R, NORM_PRE>>(dev, r, g, grid, smem, st);
+                default: return launch_ring<k_norm_bwd_ring<T, CH, R, NORM_POST>>(dev, r, g, grid, smem, st);
+            }
         };
         switch (ch) {
             case 1: s = go(std::integral_constant<int, 1>(), std::integral_constant<int, 2>()); break;

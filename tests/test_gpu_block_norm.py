@@ -114,6 +114,29 @@ def test_options(post, gate, pre, dtype):
     check(37, 320, dtype, post, gate, pre, scale=-0.3, seed=2, wide=24, no_dr=pre)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 264), ("bf16", 4608), ("fp32", 2560), ("fp32", 5128)])
+@pytest.mark.parametrize("post,gate,pre,no_dr", [(True, "channel", True, False), (True, "channel", True, True), (False, "full", True, False),
+                                                 (True, "full", True, True), (True, "channel", False, False), (True, "full", False, False)])
+def test_options_in_the_backward_of_rows_of_all_widths(dtype, d, post, gate, pre, no_dr):
+    check(45, d, dtype, post, gate, pre, scale=0.7, seed=3, no_dr=no_dr)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 264), ("bf16", 4608), ("bf16", 8712), ("fp32", 2560), ("fp32", 5128)])
+@pytest.mark.parametrize("with_dr", [False, True])
+def test_norm_alone_at_all_widths(dtype, d, with_dr):
+    """Only w_pre. The bound is a rounding of the result and, for sums of d
+    or 45 products of values of order one, d + 45 fp32 roundings of the largest."""
+    t = make(45, d, dtype, False, "none", True)
+    x = t["x"].contiguous()
+    _, n, _, pr = lce.block_norm_forward(x, w_pre=t["w_pre"])
+    dr = t["dr"] if with_dr else None
+    dx, _, _, _, dw = lce.block_norm_backward(dr, t["dn"], x, w_pre=t["w_pre"], rstd_pre=pr)
+    want = bo.block_norm_backward(f64(dr) if with_dr else None, f64(t["dn"]), f64(x), w_pre=f64(t["w_pre"]), rstd_pre=f64(pr))
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    for got, w in ((dx, want[0]), (dw, want[4])):
+        assert np.all(np.abs(f64(got) - w) <= u * np.abs(w) + (d + 45) * 2.0 ** -24 * np.abs(w).max())
+
+
 def test_norm_alone_and_in_place():
     t = make(50, 512, "bf16", True, "channel", True)
     x = t["x"].contiguous()
