@@ -1,5 +1,6 @@
 // Host side of attention over packed sequences: argument checks, workspace
 // and launches.
+#include <algorithm>
 #include <type_traits>
 
 #include "lce_attn_bwd.cuh"
@@ -150,9 +151,39 @@ lce_status_t backward_simt(const AttnArgs &r, const HostDev &dev, cudaStream_t s
     return s != LCE_OK ? s : launch<k_attn_bwd_simt<DP>>(dev, dq + dkv, kSimtThreads, simt_smem(DP, 4, 2), st, r, static_cast<int>(dkv));
 }
 
+int stat_tile(const lce_attn_t *a) { return a->dtype == LCE_BF16 ? kTcTile : kSimtTile; }
+
+constexpr int kSms = 152;
+
+// Shares that a dK/dV piece's query heads are split into. A piece walks the query tiles of all heads of its key head;
+// where that is longer than an SM's part of all the work, shares of the heads are given to more SMs. The times compared
+// are in tiles of a walk: a piece costs 3 more for its start and output, 5 with an fp32 output, and the join 3; a mask
+// halves the average walk, not the longest. Of the lengths only the averages are known here. (Causal, 128 channels:
+// 32 heads of 8 key heads over 512 tokens 26 us against 30, over 1024 40 against 50, of 4 over 2048 102 against 169, 8
+// of 1 over 8192 295 against 631; split all the same, 28 heads of 4 over eight sequences of 256 took 59 against 32, and
+// 32 of 8 over 2048 tokens 107 against 92.)
+int shares(const lce_attn_t *a, bool causal) {
+    const int64_t group = a->Hq / a->Hk, tq = (a->Tq / a->B + kTcTile - 1) / kTcTile, tk = (a->Tk / a->B + kTcTile - 1) / kTcTile;
+    if (a->dtype != LCE_BF16 || group == 1 || a->Tk * a->Hk > (1 << 24)) return 1;
+    const double kv = static_cast<double>(a->B) * tk * a->Hk, q = static_cast<double>(a->B) * tq * a->Hq, mask = causal ? 0.5 : 1.0;
+    auto time = [&](int64_t n) {   // of the longest piece, or of everything shared out
+        const double more = n > 1 ? 5 : 3, walk = static_cast<double>(tq * group / n);
+        return std::max(walk + more, (kv * n * (walk * mask + more) + q * (tk * mask + 3)) / kSms) + (n > 1 ? 3 : 0);
+    };
+    int64_t best = 1;
+    for (int64_t n = 2; n <= group; ++n)
+        if (group % n == 0 && time(n) < 0.95 * time(best)) best = n;
+    return static_cast<int>(best);
+}
+
+size_t stat_bytes(const lce_attn_t *a) {
+    const size_t rows = static_cast<size_t>(seq_slots(a->Tq, a->B, stat_tile(a))) * stat_tile(a);
+    return 2 * rows * static_cast<size_t>(a->Hq) * sizeof(float);
+}
+
 template <int KS>
 lce_status_t backward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
-    const int64_t dq = seq_slots(r.sq.T, r.sq.B, kTcTile) * r.Hq, dkv = seq_slots(r.sk.T, r.sk.B, kTcTile) * r.Hk;
+    const int64_t dq = seq_slots(r.sq.T, r.sq.B, kTcTile) * r.Hq, dkv = seq_slots(r.sk.T, r.sk.B, kTcTile) * r.Hk * r.split;
     if (dq + dkv >= (int64_t(1) << 31)) return LCE_ERR_SHAPE;
     AttnMaps maps;
     lce_status_t s = encode(&maps.q, dev, a->q, a->Tq, a->Hq, a->D, a->q_ts, a->q_hs);
@@ -161,9 +192,16 @@ lce_status_t backward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &
     if (s == LCE_OK) s = encode(&maps.dO, dev, a->dO, a->Tq, a->Hq, a->D, a->dO_ts, a->dO_hs);
     if (s == LCE_OK) s = row_stats<__nv_bfloat16, kTcTile>(r, dev, st);
     if (s != LCE_OK) return s;
-    return few_outputs(a)
-               ? launch<k_attn_bwd<KS, true>, true>(dev, dq + dkv, kBwdThreads, BwdSmem<KS>::kBytes, st, r, maps, static_cast<int>(dkv))
-               : launch<k_attn_bwd<KS, false>, true>(dev, dq + dkv, kBwdThreads, BwdSmem<KS>::kBytes, st, r, maps, static_cast<int>(dkv));
+    auto go = [&](auto two, auto parts) {
+        return launch<k_attn_bwd<KS, decltype(two)::value, decltype(parts)::value>, true>(dev, dq + dkv, kBwdThreads, BwdSmem<KS>::kBytes, st, r, maps,
+                                                                                         static_cast<int>(dkv));
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    s = few_outputs(a) ? r.split > 1 ? go(yes, yes) : go(yes, no) : r.split > 1 ? go(no, yes) : go(no, no);
+    if (s != LCE_OK || r.split == 1) return s;
+    const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(r.sk.T) * r.Hk * 16 + kJoinThreads - 1) / kJoinThreads);
+    return host_launch_early(k_attn_join, dim3(blocks, 2), kJoinThreads, 0, st, r);
 }
 
 // The tensor-core kernels exist for 64, 80, 96 and 128 channels; others run as the next of these (8192 tokens in
@@ -177,16 +215,14 @@ lce_status_t by_channels(int64_t D, F f) {
     return f(std::integral_constant<int, 8>());
 }
 
-int stat_tile(const lce_attn_t *a) { return a->dtype == LCE_BF16 ? kTcTile : kSimtTile; }
-
 }  // namespace
 
 extern "C" {
 
 size_t lce_attention_workspace_size(const lce_attn_t *a) {
     if (check_shape(a) != LCE_OK) return 0;
-    const size_t rows = static_cast<size_t>(seq_slots(a->Tq, a->B, stat_tile(a))) * stat_tile(a);
-    return 2 * rows * static_cast<size_t>(a->Hq) * sizeof(float);
+    const int n = shares(a, true);   // the more of both masks
+    return stat_bytes(a) + (n > 1 ? static_cast<size_t>(n) * 2 * a->Tk * a->Hk * a->D * sizeof(float) : 0);
 }
 
 lce_status_t lce_attention_forward(const lce_attn_t *a) {
@@ -225,6 +261,8 @@ lce_status_t lce_attention_backward(const lce_attn_t *a) {
     r.stat_stride = seq_slots(a->Tq, a->B, stat_tile(a)) * stat_tile(a);
     r.nlse2 = reinterpret_cast<float *>(base);
     r.ndelta = r.nlse2 + r.stat_stride * r.Hq;
+    r.split = shares(a, a->causal != 0);
+    r.part = reinterpret_cast<float *>(base + stat_bytes(a));
     if (a->dtype == LCE_BF16)
         return by_channels(a->D, [&](auto ks) { return backward_tc<decltype(ks)::value>(a, r, dev, st); });
     return a->D <= 32 ? backward_simt<32>(r, dev, st) : a->D <= 64 ? backward_simt<64>(r, dev, st) : backward_simt<128>(r, dev, st);

@@ -8,6 +8,8 @@
 
 #include <type_traits>
 
+#include "tc_ptx.cuh"
+
 namespace lce {
 
 constexpr float kAttnLog2e = 1.4426950408889634f;
@@ -49,6 +51,9 @@ struct AttnArgs {
     // part) and -delta, both negative so that they are added; [Hq][slots * TILE]
     float *nlse2, *ndelta;
     int64_t stat_stride;       // slots * TILE
+    // tensor-core backward: a key head's query heads in `split` shares, whose sums of dV and dK go to part[share][2][Tk][Hk][D]
+    int split;
+    float *part;
     int *status;
 };
 
@@ -156,6 +161,32 @@ __device__ __forceinline__ float dot16(const uint4 &a, const uint4 &b) {
         s = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), s);
     }
     return s;
+}
+
+constexpr int kJoinThreads = 256;
+
+// dV (blockIdx.y = 0) and dK from the shares' sums, added in order: 16 threads
+// a row of a head. Bounded by latency (the sums lie in L2).
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const AttnArgs a) {
+    griddep_wait();   // launched early
+    const unsigned i = blockIdx.x * kJoinThreads + threadIdx.x, row = i / 16, c = i % 16 * 8;
+    const unsigned tok = row / a.Hk, h = row % a.Hk;
+    if (tok >= static_cast<unsigned>(a.sk.T) || c >= static_cast<unsigned>(a.D)) return;
+    const int64_t each = static_cast<int64_t>(a.sk.T) * a.Hk * a.D;
+    const float *p = a.part + blockIdx.y * each + static_cast<int64_t>(row) * a.D + c;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < a.split; ++k) {
+        const float4 x = *reinterpret_cast<const float4 *>(p + k * 2 * each), y = *reinterpret_cast<const float4 *>(p + k * 2 * each + 4);
+        s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w, s[4] += y.x, s[5] += y.y, s[6] += y.z, s[7] += y.w;
+    }
+    const float f = blockIdx.y ? a.scale : 1.f;
+    __nv_bfloat162 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __floats2bfloat162_rn(s[2 * k] * f, s[2 * k + 1] * f);
+    __nv_bfloat16 *out = blockIdx.y ? static_cast<__nv_bfloat16 *>(a.dk) + tok * a.dk_ts + h * a.dk_hs
+                                    : static_cast<__nv_bfloat16 *>(a.dv) + tok * a.dv_ts + h * a.dv_hs;
+    *reinterpret_cast<uint4 *>(out + c) = *reinterpret_cast<const uint4 *>(v);
 }
 
 constexpr int kStatThreads = 256;

@@ -30,7 +30,9 @@
 // and one of two (`b`: V, or dO). A CTA takes one piece of work after another
 // by cluster launch control, as in the forward; the loads and the first
 // products of the next run under the last sums and the output of the one
-// before. Both kinds are one grid, the longer dK/dV pieces first.
+// before. Both kinds are one grid, the longer dK/dV pieces first. Where a key
+// head's query heads would make them too long for the few there are, a piece
+// takes a share of the heads, and k_attn_join adds up the shares.
 //
 // Measured with 32 query and 8 key heads of 128 channels, causal, row statistics
 // included: one sequence of 8192 tokens 1.09 ms (1.26 PFLOP/s of the five
@@ -66,6 +68,7 @@ enum BwdKind : int { BWD_NONE = -1, BWD_DKV = 0, BWD_DQ = 1 };
 struct BwdWork {
     int kind;
     int head;       // query head (dQ) or key head
+    int share;      // dK/dV: of the key head's query heads
     int rows;       // rows of the own tile (0: nothing to do)
     int n;          // tiles of the other side, over all heads (0: zero gradients)
     int tok;        // first token of the own tile
@@ -94,7 +97,8 @@ struct BwdBars {
 };
 static_assert(sizeof(BwdBars) <= 512, "room after the statistics");
 
-template <int KS, bool kTwo>
+// kShares: as above. Known when the kernel is compiled, like kTwo: the code alone costs the other calls 7%.
+template <int KS, bool kTwo, bool kShares>
 __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_constant__ AttnArgs a,
                                                              const __grid_constant__ AttnMaps maps, int dkv_blocks) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -143,14 +147,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
         auto find = [&](int block) {
             BwdWork w{};
             if (block < dkv_blocks) {   // under a causal mask the first key tiles have the most queries
-                const TileInfo t = finder.of_k(block / a.Hk);
+                const int split = kShares ? a.split : 1, shares = a.Hk * split;
+                const TileInfo t = finder.of_k(block / shares);
                 w.kind = BWD_DKV;
-                w.head = block % a.Hk;
+                w.head = block % shares / split;
+                w.share = block % split;
                 w.rows = t.t0 < 0 ? 0 : max(0, min(kTcTile, t.len - t.t0));
                 w.off = t.len - t.olen;
                 w.first = a.causal ? max(0, t.t0 - w.off) / kTcTile : 0;   // the first that sees the tile's first key
                 w.per = max(0, (t.olen + kTcTile - 1) / kTcTile - w.first);
-                w.n = w.rows > 0 ? w.per * a.group : 0;
+                w.n = w.rows > 0 ? w.per * (kShares ? a.group / a.split : a.group) : 0;
                 w.slot = t.o0 / kTcTile + t.b;
                 w.tok = t.s0 + t.t0, w.t0 = t.t0, w.o0 = t.o0, w.olen = t.olen;
             } else {                    // ... and the last query tiles the most keys
@@ -212,7 +218,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                 ++nf;
             }
             BwdWork next{};
-            int h = dkv ? cur.head * a.group : cur.head / a.group, tile = cur.first;   // of the other side
+            int h = dkv ? cur.head * a.group + (kShares ? cur.share * (a.group / a.split) : 0) : cur.head / a.group, tile = cur.first;   // of the other side
             const int steps = max(cur.n, 1);
             for (int j = 0; j < steps; ++j) {
                 // The next piece is asked for when this one's last loads but one are due: late, so that a CTA with
@@ -476,6 +482,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                 ts0 = a.dq_ts;
                 out0 = static_cast<__nv_bfloat16 *>(a.dq) + w.tok * ts0 + w.head * a.dq_hs;
             }
+            float *part0 = nullptr, *part1 = nullptr;   // a share's dV and dK
+            const int64_t part_ts = static_cast<int64_t>(a.Hk) * a.D;
+            if (kShares && dkv) {
+                part0 = a.part + (w.share * 2 * static_cast<int64_t>(a.sk.T) + w.tok) * part_ts + w.head * a.D;
+                part1 = part0 + a.sk.T * part_ts;
+            }
+            if (kShares && w.n == 0 && dkv) {
+                if (row < w.rows)
+                    for (int c = half * 4; c < a.D; c += 8) {
+                        *reinterpret_cast<uint4 *>(part0 + row * part_ts + c) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(part1 + row * part_ts + c) = make_uint4(0, 0, 0, 0);
+                    }
+                ok = fetch();
+                continue;
+            }
             if (w.n == 0) {   // nothing on the other side
                 if (row < w.rows)
                     for (int c = half * 8; c < a.D; c += 16) {
@@ -599,7 +620,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.acc_free);
             };
-            if (dkv) {
+            if (kShares && dkv) {
+                tc_store_fp32<KS>(half, tile, tm + cV + lane_base, quarter * 32, w.rows, part0, part_ts, a.D, [] {});
+                tc_store_fp32<KS>(half, tile, tm + cK + lane_base, quarter * 32, w.rows, part1, part_ts, a.D, release);
+            } else if (dkv) {
                 tc_store_half<KS>(half, tile, tm + cV + lane_base, 1.f, quarter * 32, w.rows, out0, ts0, a.D, [] {});
                 __syncwarp();
                 tc_store_half<KS>(half, tile, tm + cK + lane_base, a.scale, quarter * 32, w.rows, out1, ts1, a.D, release);

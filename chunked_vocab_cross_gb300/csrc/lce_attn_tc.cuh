@@ -195,6 +195,39 @@ __device__ __forceinline__ void tc_store_half(int half, uint8_t *tile, uint32_t 
     else tc_store_rows<C::kFirst, C::kAll - C::kFirst>(tile, taddr, mul, r0, rows, dst, stride, D, release);
 }
 
+// The same in fp32, 16 channels at a time: each half of the threads has its half
+// of the tile's 128-byte rows.
+template <int KS, typename F>
+__device__ __forceinline__ void tc_store_fp32(int half, uint8_t *tile, uint32_t taddr, int r0, int rows, float *dst,
+                                              int64_t stride, int D, F release) {
+    using C = Chunks<KS>;
+    const int lane = threadIdx.x & 31;
+    const int last = half ? C::kAll : C::kFirst;
+#pragma unroll 1
+    for (int c = half ? C::kFirst : 0; c < last; ++c) {
+        uint32_t v[32];
+        tmem_ld32(taddr + c * 32, v);
+        tmem_ld_wait();
+        if (c + 1 == last) release();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4 *>(tile + (r0 + lane) * 128 + half * 64 + ((i ^ (lane & 3)) << 4)) =
+                    make_uint4(v[h * 16 + 4 * i], v[h * 16 + 4 * i + 1], v[h * 16 + 4 * i + 2], v[h * 16 + 4 * i + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = r0 + k * 8 + lane / 4, i = lane & 3, col = c * 32 + h * 16 + i * 4;
+                if (r < rows && col < D)
+                    *reinterpret_cast<uint4 *>(dst + r * stride + col) =
+                        *reinterpret_cast<const uint4 *>(tile + r * 128 + half * 64 + ((i ^ (r & 3)) << 4));
+            }
+            __syncwarp();
+        }
+    }
+}
+
 struct AttnMaps {
     CUtensorMap q, k, v, dO;
 };

@@ -126,6 +126,19 @@ def test_bf16_head_layouts_one_part(heads):
     check([200, 57], [90, 157], *heads, 128, False, "bf16", tail=longer([200, 57]), seed=3)
 
 
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("heads,D", [((14, 2), 96), ((16, 1), 64), ((6, 1), 128), ((8, 2), 80), ((28, 4), 8)],
+                         ids=lambda h: f"{h[0]}_{h[1]}" if isinstance(h, tuple) else str(h))
+def test_key_heads_whose_query_heads_are_shared_out(heads, D, causal):
+    """Few key tiles with many query heads each: dK and dV come as sums of
+    shares. Sequences without queries or keys, and tokens after the last."""
+    for lq, lk, tail in (([700], [700], 0), ([300, 0, 129, 1], [200, 77, 0, 300], 5), ([513, 200], [513, 200], 2100)):
+        q, k, v, do, o, lse, grads = check(lq, lk, *heads, D, causal, "bf16", tail=tail, seed=D)
+        again = lce.attention_backward(do, q, k, v, o, lse, cu(lq), cu(lk), causal=causal)
+        assert all(torch.equal(x, y) for x, y in zip(grads, again))
+        assert all(bool((t[sum(n):] == 0).all()) for t, n in zip(grads, (lq, lk, lk)))
+
+
 @pytest.mark.parametrize("heads,D", [((8, 8), 64), ((4, 1), 128)], ids=["8x64", "4of1x128"])
 def test_small_calls_lose_little_more_than_the_rounding_of_the_result(heads, D):
     """Rounding values of any size to bf16 costs 2^-8 / sqrt(3) * sqrt(mean
