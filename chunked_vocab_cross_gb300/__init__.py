@@ -6,8 +6,9 @@ library has not been built: there is no CPU fallback.
 """
 from ._abi import LIB_PATH, LceError, lib  # noqa: F401
 from .block_ops import (  # noqa: F401
-    attention, attention_backward, attention_forward, attention_workspace_size, block_norm, block_norm_backward,
-    block_norm_forward, block_norm_workspace_size, clip_grad_norm, clip_workspace_size, grad_norm,
+    attention, attention_backward, attention_forward, attention_forward_workspace_size, attention_workspace_size,
+    block_norm, block_norm_backward, block_norm_forward, block_norm_workspace_size, clip_grad_norm, clip_workspace_size,
+    grad_norm,
 )
 from .ops import (  # noqa: F401
     FusedOptimizer, device_status, embedding, embedding_backward, embedding_forward, embedding_workspace_size,

@@ -55,6 +55,7 @@ SIGNATURES = {
     "lce_attention_forward": (c_int, [c_void_p]),
     "lce_attention_backward": (c_int, [c_void_p]),
     "lce_attention_workspace_size": (c_size_t, [c_void_p]),
+    "lce_attention_forward_workspace_size": (c_size_t, [c_void_p]),
     "lce_block_norm_forward": (c_int, [c_void_p]),
     "lce_block_norm_backward": (c_int, [c_void_p]),
     "lce_block_norm_workspace_size": (c_size_t, [c_void_p]),

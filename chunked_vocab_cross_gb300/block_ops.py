@@ -117,14 +117,27 @@ def attention_workspace_size(Tq: int, Tk: int, Hq: int, Hk: int, D: int, batch: 
     return int(_abi.lib().lce_attention_workspace_size(_abi.ctypes.byref(a)))
 
 
+@functools.lru_cache(maxsize=256)
+def attention_forward_workspace_size(Tq: int, Tk: int, Hq: int, Hk: int, D: int, batch: int = 1, dtype=torch.bfloat16,
+                                     causal: bool = True) -> int:
+    """Bytes of scratch attention_forward needs: 0 but for few rows over long keys."""
+    a = _abi.LceAttn()
+    a.cu_q = a.cu_k = 16
+    a.dtype, a.B, a.Tq, a.Tk, a.Hq, a.Hk, a.D, a.causal = _DT[dtype], batch, Tq, Tk, Hq, Hk, D, 1 if causal else 0
+    return int(_abi.lib().lce_attention_forward_workspace_size(_abi.ctypes.byref(a)))
+
+
 @_on_stream
-def attention_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, *, causal: bool = True, scale=None, out=None):
+def attention_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, *, causal: bool = True, scale=None, out=None,
+                      workspace=None):
     """(o, lse) of softmax attention over packed sequences: q [Tq, heads, D],
     k and v [Tk, kv_heads, D] with int32 token offsets of the sequences (one
     sequence without them), or [B, L, heads, D] tensors of equal lengths. o has
     q's shape and dtype, lse is fp32 [heads, tokens]; rows that see no key get
     o = 0 and lse = -inf. `scale` is D**-0.5 if not given; `out` receives o;
-    `stream`: the stream to run on (the current one if not given)."""
+    `workspace`: a uint8 CUDA tensor of at least
+    attention_forward_workspace_size bytes; `stream`: the stream to run on (the
+    current one if not given)."""
     B, Tq, Tk, Hq, Hk, D, pcq, pck = _sequences(q, k, v, cu_seqlens_q, cu_seqlens_k)
     device, dtype = q.device, q.dtype
     pq, pk, pv = _tokens("q", q, device, dtype), _tokens("k", k, device, dtype), _tokens("v", v, device, dtype)
@@ -134,10 +147,15 @@ def attention_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, *, causal: 
     else:
         po, ots, ohs = _tokens("out", out, device, dtype, q.shape)
     lse = torch.empty((Hq, Tq), dtype=torch.float32, device=device)
+    ws, size, keep = 0, 0, None
+    need = attention_forward_workspace_size(Tq, Tk, Hq, Hk, D, B, dtype, causal)
+    if need:
+        ws, size, keep = _scratch(workspace, need, device)
     args = _ATTN.pack(_DT[dtype], 1 if causal else 0, D ** -0.5 if scale is None else scale, B, Tq, Tk, Hq, Hk, D,
                       pcq, pck, pq[0], pk[0], pv[0], pq[1], pq[2], pk[1], pk[2], pv[1], pv[2], po, ots, ohs,
-                      lse.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, _stream(device.index))
+                      lse.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, ws, size, _stream(device.index))
     _abi.check(_abi.lib().lce_attention_forward(args), "lce_attention_forward")
+    del keep
     return out, lse
 
 

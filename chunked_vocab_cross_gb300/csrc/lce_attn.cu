@@ -103,6 +103,32 @@ lce_status_t launch(const HostDev &dev, int64_t blocks, int threads, int smem, c
     return host_launched();
 }
 
+constexpr int kSms = 152;
+
+// Ranges that a row's keys are split into in the forward. Few rows and heads over long keys leave most SMs without
+// work; their walks are split as far as that makes the longest shorter. The times compared are in key tiles of a walk
+// (0.6 us): a piece costs 3 more for its start and output, 5 with an fp32 output, and the merge 3 and its bytes. Of
+// the lengths only the averages are known here. (32 heads of 8 key heads of 128 channels: one row over 2048 keys 17 us
+// against 26, over 32768 53 against 322; 2 heads, 8192 causal tokens: 44 against 86.)
+int ranges(const lce_attn_t *a) {
+    const int64_t group = a->Hq / a->Hk, tq = (a->Tq / a->B + kTcTile - 1) / kTcTile, tk = (a->Tk / a->B + kTcTile - 1) / kTcTile;
+    if (a->dtype != LCE_BF16 || tk <= 8 || a->Tq * a->Hq > (1 << 24)) return 1;
+    const double pieces = static_cast<double>(a->B) * (group % 2 == 0 ? tq * a->Hq / 2 : (tq + 1) / 2 * a->Hq),
+                 mask = a->causal && a->Tq == a->Tk ? 0.5 : 1.0, merge = static_cast<double>(a->Tq * a->Hq * a->D) * 8 / 3e6;
+    auto time = [&](int64_t n) {   // of the longest piece, or of everything shared out
+        const double more = n > 1 ? 5 : 3, walk = static_cast<double>((tk + n - 1) / n);
+        return std::max(walk + more, pieces * n * (walk * mask + more) / kSms) + (n > 1 ? 3 + n * merge : 0);
+    };
+    int64_t best = 1;
+    for (int64_t n = 2; n <= 64 && n <= tk / 2; ++n)
+        if (time(n) < 0.95 * time(best)) best = n;
+    return static_cast<int>(best);
+}
+
+size_t range_bytes(const lce_attn_t *a, int n) {
+    return n == 1 ? 0 : static_cast<size_t>(n) * a->Tq * a->Hq * (a->D + 1) * sizeof(float);
+}
+
 // Few outputs over short sequences: the rounding errors of P and dS do not average out over them (the norm of the
 // error of a result reached 1.7 times that of rounding the result alone; 1.4 over many), and so little work does not
 // fill the GPU. These calls take P and dS in two parts (backward of 256 tokens, 8 heads of 64 channels: 9.6 us against
@@ -119,8 +145,13 @@ lce_status_t forward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &d
     if (s == LCE_OK) s = encode(&maps.v, dev, a->v, a->Tk, a->Hk, a->D, a->v_ts, a->v_hs);
     if (s != LCE_OK) return s;
     const int64_t work = r.pair_heads ? seq_slots(r.sq.T, r.sq.B, kTcTile) * (r.Hq / 2) : seq_slots(r.sq.T, r.sq.B, 2 * kTcTile) * r.Hq;
-    return few_outputs(a) ? launch<k_attn_fwd<KS, true>>(dev, work, kFwdThreads, FwdSmem<KS>::kBytes, st, r, maps)
-                          : launch<k_attn_fwd<KS, false>>(dev, work, kFwdThreads, FwdSmem<KS>::kBytes, st, r, maps);
+    if (r.split == 1)
+        return few_outputs(a) ? launch<k_attn_fwd<KS, true, false>>(dev, work, kFwdThreads, FwdSmem<KS>::kBytes, st, r, maps)
+                              : launch<k_attn_fwd<KS, false, false>>(dev, work, kFwdThreads, FwdSmem<KS>::kBytes, st, r, maps);
+    s = launch<k_attn_fwd<KS, false, true>>(dev, work * r.split, kFwdThreads, FwdSmem<KS>::kBytes, st, r, maps);
+    if (s != LCE_OK) return s;
+    const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(r.sq.T) * r.Hq * 16 + kJoinThreads - 1) / kJoinThreads);
+    return host_launch_early(k_attn_merge, dim3(blocks), kJoinThreads, 0, st, r);
 }
 
 // DP: channels rounded up to 32, 64 or 128 (512 tokens, 4 heads, causal, forward and backward: 32 channels 34 and 53 us,
@@ -152,8 +183,6 @@ lce_status_t backward_simt(const AttnArgs &r, const HostDev &dev, cudaStream_t s
 }
 
 int stat_tile(const lce_attn_t *a) { return a->dtype == LCE_BF16 ? kTcTile : kSimtTile; }
-
-constexpr int kSms = 152;
 
 // Shares that a dK/dV piece's query heads are split into. A piece walks the query tiles of all heads of its key head;
 // where that is longer than an SM's part of all the work, shares of the heads are given to more SMs. The times compared
@@ -225,6 +254,10 @@ size_t lce_attention_workspace_size(const lce_attn_t *a) {
     return stat_bytes(a) + (n > 1 ? static_cast<size_t>(n) * 2 * a->Tk * a->Hk * a->D * sizeof(float) : 0);
 }
 
+size_t lce_attention_forward_workspace_size(const lce_attn_t *a) {
+    return check_shape(a) == LCE_OK ? range_bytes(a, ranges(a)) : 0;
+}
+
 lce_status_t lce_attention_forward(const lce_attn_t *a) {
     lce_status_t s = check_common(a);
     if (s != LCE_OK) return s;
@@ -233,8 +266,13 @@ lce_status_t lce_attention_forward(const lce_attn_t *a) {
     HostDev dev;
     if ((s = host_device(&dev)) != LCE_OK) return s;
     if (a->Tq == 0) return LCE_OK;
-    const AttnArgs r = make_args(a, dev);
+    AttnArgs r = make_args(a, dev);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
+    r.split = ranges(a);
+    HostScratch scratch(st);
+    uint8_t *base = nullptr;
+    if ((s = scratch.get(a->workspace, a->workspace_bytes, range_bytes(a, r.split), &base)) != LCE_OK) return s;
+    r.part = reinterpret_cast<float *>(base);
     if (a->dtype == LCE_BF16)
         return by_channels(a->D, [&](auto ks) { return forward_tc<decltype(ks)::value>(a, r, dev, st); });
     return a->D <= 32 ? forward_simt<32>(r, dev, st) : a->D <= 64 ? forward_simt<64>(r, dev, st) : forward_simt<128>(r, dev, st);

@@ -51,7 +51,9 @@ struct AttnArgs {
     // part) and -delta, both negative so that they are added; [Hq][slots * TILE]
     float *nlse2, *ndelta;
     int64_t stat_stride;       // slots * TILE
-    // tensor-core backward: a key head's query heads in `split` shares, whose sums of dV and dK go to part[share][2][Tk][Hk][D]
+    // tensor-core kernels. Backward: a key head's query heads in `split` shares, whose sums of dV and dK go to
+    // part[share][2][Tk][Hk][D]. Forward: a row's keys in `split` ranges, whose o goes to part[range][Tq][Hq][D] and
+    // whose lse lies after them, [range][Hq][Tq].
     int split;
     float *part;
     int *status;
@@ -180,13 +182,43 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const AttnArgs a) {
         const float4 x = *reinterpret_cast<const float4 *>(p + k * 2 * each), y = *reinterpret_cast<const float4 *>(p + k * 2 * each + 4);
         s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w, s[4] += y.x, s[5] += y.y, s[6] += y.z, s[7] += y.w;
     }
-    const float f = blockIdx.y ? a.scale : 1.f;
     __nv_bfloat162 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __floats2bfloat162_rn(s[2 * k] * f, s[2 * k + 1] * f);
+    for (int k = 0; k < 4; ++k) v[k] = __floats2bfloat162_rn(s[2 * k], s[2 * k + 1]);
     __nv_bfloat16 *out = blockIdx.y ? static_cast<__nv_bfloat16 *>(a.dk) + tok * a.dk_ts + h * a.dk_hs
                                     : static_cast<__nv_bfloat16 *>(a.dv) + tok * a.dv_ts + h * a.dv_hs;
     *reinterpret_cast<uint4 *>(out + c) = *reinterpret_cast<const uint4 *>(v);
+}
+
+// The forward's o and lse from its ranges': with lse = log sum exp(lse_k),
+// o = sum exp(lse_k - lse) o_k, added in order. 16 threads a row of a head.
+__global__ void __launch_bounds__(kJoinThreads) k_attn_merge(const AttnArgs a) {
+    griddep_wait();   // launched early
+    const int64_t row = (static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x) / 16, tok = row / a.Hq;
+    const int h = static_cast<int>(row % a.Hq), c = threadIdx.x % 16 * 8;
+    if (tok >= a.sq.T || c >= a.D) return;
+    const int64_t each = static_cast<int64_t>(a.sq.T) * a.Hq;
+    const float *p = a.part + row * a.D + c, *l = a.part + a.split * each * a.D + h * static_cast<int64_t>(a.sq.T) + tok;
+    float m = -INFINITY, sum = 0.f;
+    for (int k = 0; k < a.split; ++k) m = fmaxf(m, l[k * each]);   // passes a NaN by, which its weight brings back
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < a.split; ++k) {
+        const float v = l[k * each];
+        if (v == -INFINITY) continue;   // nothing was written
+        const float w = exp2f((v - m) * kAttnLog2e);
+        const float4 x = *reinterpret_cast<const float4 *>(p + k * each * a.D), y = *reinterpret_cast<const float4 *>(p + k * each * a.D + 4);
+        const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        sum += w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = fmaf(w, z[i], s[i]);
+    }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;   // a row without keys: zeros
+    __nv_bfloat162 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __floats2bfloat162_rn(s[2 * k] * inv, s[2 * k + 1] * inv);
+    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + tok * a.o_ts + h * a.o_hs + c) = *reinterpret_cast<const uint4 *>(v);
+    if (c == 0) a.lse[h * static_cast<int64_t>(a.sq.T) + tok] = sum != 0.f ? m + logf(sum) : -INFINITY;
 }
 
 constexpr int kStatThreads = 256;

@@ -621,8 +621,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                 if (lane == 0) mbar_arrive(&bar.acc_free);
             };
             if (kShares && dkv) {
-                tc_store_fp32<KS>(half, tile, tm + cV + lane_base, quarter * 32, w.rows, part0, part_ts, a.D, [] {});
-                tc_store_fp32<KS>(half, tile, tm + cK + lane_base, quarter * 32, w.rows, part1, part_ts, a.D, release);
+                tc_store_fp32<KS>(half, tile, tm + cV + lane_base, 1.f, quarter * 32, w.rows, part0, part_ts, a.D, [] {});
+                tc_store_fp32<KS>(half, tile, tm + cK + lane_base, a.scale, quarter * 32, w.rows, part1, part_ts, a.D, release);
             } else if (dkv) {
                 tc_store_half<KS>(half, tile, tm + cV + lane_base, 1.f, quarter * 32, w.rows, out0, ts0, a.D, [] {});
                 __syncwarp();

@@ -64,6 +64,8 @@ struct FwdSide {
 struct FwdWork {
     FwdSide side[2];   // n of the first is at most n of the second
     int hk;         // key head; -1: no more work
+    int first;      // first key tile
+    int range;
     int keys;       // keys of the sequence
     int ktok;       // first key token
 };
@@ -84,7 +86,9 @@ struct FwdBars {
 };
 static_assert(sizeof(FwdBars) <= 512, "room after the maxima");
 
-template <int KS, bool kTwo>
+// kRanges: a piece takes one of `split` ranges of its keys and leaves its o, in
+// fp32, and lse for k_attn_merge.
+template <int KS, bool kTwo, bool kRanges>
 __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_constant__ AttnArgs a,
                                                              const __grid_constant__ AttnMaps maps) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -137,8 +141,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_consta
                 check_offsets(a.sk, a.status);
             }
             FwdWork w{};
+            const int ranges = kRanges ? a.split : 1;
+            w.range = kRanges ? block % ranges : 0;
+            if (kRanges) block /= ranges;
             const int heads = a.pair_heads ? a.Hq / 2 : a.Hq;
-            const int slot = gridDim.x / heads - 1 - block / heads, h = block % heads;
+            const int slot = gridDim.x / (heads * ranges) - 1 - block / heads, h = block % heads;
             const TileInfo t = a.pair_heads ? finder.of_q(slot) : finder2.of_q(slot);
             const int off = t.olen - t.len;   // causal: row i sees keys [0, i + off]
 #pragma unroll
@@ -156,6 +163,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_consta
                 const FwdSide s = w.side[0];
                 w.side[0] = w.side[1];
                 w.side[1] = s;
+            }
+            if (kRanges) {   // the second side's keys in equal ranges
+                const int each = (w.side[1].n + ranges - 1) / ranges;
+                w.first = w.range * each;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) w.side[i].n = max(0, min(w.side[i].n - w.first, each));
             }
             w.hk = w.side[1].head / a.group;
             w.keys = t.olen;
@@ -217,7 +230,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_consta
                 // that an idle CTA could start, early enough for it to be found
                 if (j == max(0, n - 2)) request();
                 if (j < n) {
-                    const int at = cur.ktok + j * kTcTile, i = kv & 1;
+                    const int at = cur.ktok + (kRanges ? cur.first + j : j) * kTcTile, i = kv & 1;
                     const uint32_t phase = (kv >> 1) & 1;
                     if (!await_staged(0, need_k[i])) break;
                     if (!(ok = wait.all(&bar.k_empty[i], phase ^ 1))) break;
@@ -275,7 +288,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_consta
             if (!(ok = wait.all(&bar.work_full[pieces & 1], (pieces >> 1) & 1))) break;
             const FwdWork &w = bar.work[pieces & 1];
             const int hk = __shfl_sync(0xffffffffu, w.hk, 0), na = __shfl_sync(0xffffffffu, w.side[0].n, 0),
-                      nb = __shfl_sync(0xffffffffu, w.side[1].n, 0), keys = __shfl_sync(0xffffffffu, w.keys, 0);
+                      nb = __shfl_sync(0xffffffffu, w.side[1].n, 0), keys = __shfl_sync(0xffffffffu, kRanges ? w.keys - w.first * kTcTile : w.keys, 0);
             if (lane == 0) mbar_arrive(&bar.work_empty[pieces & 1]);
             if (hk < 0) break;
             if (nb == 0) continue;
@@ -374,16 +387,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_consta
             }
             const FwdWork &shared = bar.work[pieces & 1];
             const FwdSide w = shared.side[side];
-            const int hk = shared.hk, all_keys = shared.keys, tiles = shared.side[1].n;
+            const int hk = shared.hk, all_keys = shared.keys, tiles = shared.side[1].n, first = kRanges ? shared.first : 0, range = kRanges ? shared.range : 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.work_empty[pieces & 1]);
             if (hk < 0) break;
             __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + static_cast<int64_t>(w.tok) * a.o_ts + w.head * a.o_hs;
             float *lse = a.lse + static_cast<int64_t>(w.head) * a.sq.T + w.tok + row;
+            // of a range: o in [range][Tq][Hq][D], then lse in [range][Hq][Tq]
+            const int64_t part_ts = static_cast<int64_t>(a.Hq) * a.D;
+            float *part_o = nullptr;
+            if (kRanges) {
+                part_o = a.part + (range * static_cast<int64_t>(a.sq.T) + w.tok) * part_ts + w.head * a.D;
+                lse = a.part + a.split * (a.sq.T * part_ts) + (range * static_cast<int64_t>(a.Hq) + w.head) * a.sq.T + w.tok + row;
+            }
             const bool live = row < w.rows;
             if (w.n == 0) {   // no row of the tile sees a key (or there are no rows)
                 if (live) {
-                    for (int c = half * 8; c < a.D; c += 16) *reinterpret_cast<uint4 *>(o + row * a.o_ts + c) = make_uint4(0, 0, 0, 0);
+                    if (!kRanges)   // (the merge gives it no weight)
+                        for (int c = half * 8; c < a.D; c += 16) *reinterpret_cast<uint4 *>(o + row * a.o_ts + c) = make_uint4(0, 0, 0, 0);
                     if (half == 0) *lse = -INFINITY;
                 }
                 kv += tiles;   // of the other side
@@ -398,7 +419,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_consta
                     break;
                 }
                 tc_fence_after();
-                const int k0 = j * kTcTile;
+                const int k0 = (first + j) * kTcTile;
                 const int keys = min(kTcTile, all_keys - k0);
                 // the warp's first row is its tightest
                 const bool cut = keys < kTcTile || (a.causal && k0 + kTcTile - 1 > w.last + quarter * 32);
@@ -477,11 +498,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_fwd(const __grid_consta
             const float inv = l != 0.f ? 1.f / l : 0.f;   // l of an empty row is 0; NaN stays
             if (half == 0 && live) *lse = l == 0.f ? -INFINITY : (m * sc + log2f(l)) * (1.f / kAttnLog2e);
             uint8_t *tile = (side ? sv : sk) + ((kv - 1) & 1) * L::kTile;
-            tc_store_half<KS>(half, tile, tO, inv, quarter * 32, w.rows, o, a.o_ts, a.D, [&] {
+            auto release = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.o_free[side]);
-            });
+            };
+            if (kRanges) tc_store_fp32<KS>(half, tile, tO, inv, quarter * 32, w.rows, part_o, part_ts, a.D, release);
+            else tc_store_half<KS>(half, tile, tO, inv, quarter * 32, w.rows, o, a.o_ts, a.D, release);
             fence_proxy_async_smem();   // the slot goes back to the loads
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.staged[side][outs & 1]);

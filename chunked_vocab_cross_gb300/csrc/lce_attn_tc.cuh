@@ -198,7 +198,7 @@ __device__ __forceinline__ void tc_store_half(int half, uint8_t *tile, uint32_t 
 // The same in fp32, 16 channels at a time: each half of the threads has its half
 // of the tile's 128-byte rows.
 template <int KS, typename F>
-__device__ __forceinline__ void tc_store_fp32(int half, uint8_t *tile, uint32_t taddr, int r0, int rows, float *dst,
+__device__ __forceinline__ void tc_store_fp32(int half, uint8_t *tile, uint32_t taddr, float mul, int r0, int rows, float *dst,
                                               int64_t stride, int D, F release) {
     using C = Chunks<KS>;
     const int lane = threadIdx.x & 31;
@@ -209,6 +209,8 @@ __device__ __forceinline__ void tc_store_fp32(int half, uint8_t *tile, uint32_t 
         tmem_ld32(taddr + c * 32, v);
         tmem_ld_wait();
         if (c + 1 == last) release();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * mul);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll

@@ -373,9 +373,10 @@ lce_status_t lce_embedding_backward_bf16(lce_dtype_t dtype, const void *dE, cons
  * D % 8 == 0, Hq a multiple of Hk, 0 <= Tq, Tk < 2^30, 1 <= B < 2^30, Tq and Tk multiples
  * of B without offsets; bases 16-byte aligned, strides multiples of 16 bytes,
  * positive (but for a single head or token).
- * Results are deterministic. Scratch: lce_attention_workspace_size bytes
- * (backward only), device, 16-byte aligned, or NULL for a stream-ordered
- * allocation. Offsets that are not ascending within the tokens set
+ * Results are deterministic. Scratch: lce_attention_forward_workspace_size bytes
+ * (0 but for few rows over long keys, whose keys are taken in ranges) or
+ * lce_attention_workspace_size bytes (backward), device, 16-byte aligned, or
+ * NULL for a stream-ordered allocation. Offsets that are not ascending within the tokens set
  * LCE_DEV_SEQLENS; the outputs are then unspecified.
  */
 typedef struct {
@@ -400,6 +401,7 @@ typedef struct {
 lce_status_t lce_attention_forward(const lce_attn_t *args);
 lce_status_t lce_attention_backward(const lce_attn_t *args);
 size_t lce_attention_workspace_size(const lce_attn_t *args);
+size_t lce_attention_forward_workspace_size(const lce_attn_t *args);
 
 /*
  * The norms before and after a block, fused with the block's gate and

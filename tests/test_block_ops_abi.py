@@ -76,6 +76,12 @@ def test_attention_workspace(lib):
     assert 0 < ws() and ws(Tk=1000, B=1) >= ws()
     # row statistics, not probabilities: linear in the tokens
     assert ws(Tq=1 << 20, Tk=1 << 20, Hq=32, Hk=8, D=128) < (1 << 20) * 32 * 128 * 64
+    fwd = lambda **kw: lib.lce_attention_forward_workspace_size(_attn(**kw)[0])  # noqa: E731
+    assert fwd() == 0 and fwd(Tq=8192, Tk=8192, Hq=32, Hk=8, D=128, B=1) == 0 and fwd(D=12) == 0
+    # few rows over long keys: at most 64 ranges of o and lse in fp32
+    assert 0 < fwd(Tq=1, Tk=1 << 20, Hq=32, Hk=8, D=128, B=1) <= 64 * 32 * 129 * 4
+    # few query heads of one key head: the heads' sums of dK and dV
+    assert ws(Tq=1024, Tk=1024, Hq=16, Hk=1, D=128, B=1) > ws(Tq=1024, Tk=1024, Hq=16, Hk=16, D=128, B=1)
 
 
 def _norm(**kw):

@@ -126,6 +126,28 @@ def test_bf16_head_layouts_one_part(heads):
     check([200, 57], [90, 157], *heads, 128, False, "bf16", tail=longer([200, 57]), seed=3)
 
 
+@pytest.mark.parametrize("heads,D", [((4, 1), 128), ((1, 1), 64), ((6, 2), 80)], ids=lambda h: f"{h[0]}_{h[1]}" if isinstance(h, tuple) else str(h))
+@pytest.mark.parametrize("lens", [([1], [3000]), ([130], [2600]), ([1, 0, 3], [2500, 700, 3000]), ([1500], [1500]), ([40, 200], [2300, 90])],
+                         ids=lambda n: f"{n[0]}_{n[1]}".replace(" ", ""))
+def test_few_rows_over_long_keys(lens, heads, D):
+    """Rows whose keys are taken in ranges: the last range ragged, empty for
+    short sequences, or beyond what a causal row sees; rows without keys, and
+    tokens after the last sequence."""
+    lq, lk = lens
+    for causal in (True, False):
+        q, k, v, do, o, lse, _ = check(lq, lk, *heads, D, causal, "bf16", tail=3, seed=D)
+        o2, lse2 = lce.attention_forward(q, k, v, cu(lq), cu(lk), causal=causal)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        need = lce.attention_forward_workspace_size(q.shape[0], k.shape[0], *heads, D, len(lq), causal=causal)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+            o3, _ = lce.attention_forward(q, k, v, cu(lq), cu(lk), causal=causal, workspace=ws)
+            assert torch.equal(o, o3)
+            with pytest.raises(lce.LceError):
+                lce.attention_forward(q, k, v, cu(lq), cu(lk), causal=causal, workspace=ws[:need - 1])
+        assert bool((o[sum(lq):] == 0).all()) and bool((lse[:, sum(lq):] == -float("inf")).all())
+
+
 @pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
 @pytest.mark.parametrize("heads,D", [((14, 2), 96), ((16, 1), 64), ((6, 1), 128), ((8, 2), 80), ((28, 4), 8)],
                          ids=lambda h: f"{h[0]}_{h[1]}" if isinstance(h, tuple) else str(h))
