@@ -67,8 +67,7 @@ enum BwdKind : int { BWD_NONE = -1, BWD_DKV = 0, BWD_DQ = 1 };
 // A piece of work as warp 8 hands it to the others.
 struct BwdWork {
     int kind;
-    int head;       // query head (dQ) or key head
-    int share;      // dK/dV: of the key head's query heads
+    int head;       // query head (dQ) or key head; kShares: and, from bit 16 on, the share of its query heads
     int rows;       // rows of the own tile (0: nothing to do)
     int n;          // tiles of the other side, over all heads (0: zero gradients)
     int tok;        // first token of the own tile
@@ -150,8 +149,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
                 const int split = kShares ? a.split : 1, shares = a.Hk * split;
                 const TileInfo t = finder.of_k(block / shares);
                 w.kind = BWD_DKV;
-                w.head = block % shares / split;
-                w.share = block % split;
+                w.head = block % shares / split + (kShares ? block % split << 16 : 0);
                 w.rows = t.t0 < 0 ? 0 : max(0, min(kTcTile, t.len - t.t0));
                 w.off = t.len - t.olen;
                 w.first = a.causal ? max(0, t.t0 - w.off) / kTcTile : 0;   // the first that sees the tile's first key
@@ -206,19 +204,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
         publish(cur);
         while (ok && cur.kind != BWD_NONE) {
             const bool dkv = cur.kind == BWD_DKV;
+            const int own = kShares ? cur.head & 0xffff : cur.head;
             if (cur.n > 0) {
                 // seeing every output go out in turn, at most two pieces late, keeps the barriers' phases apart
                 if (!await_staged(nf - 1)) break;
                 if (!(ok = wait.all(&bar.f_empty, (nf & 1) ^ 1))) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&bar.f_full, 2 * L::kTile);
-                    tc_load_tile<NB>(f0, dkv ? &maps.k : &maps.q, &bar.f_full, cur.head, cur.tok);
-                    tc_load_tile<NB>(f1, dkv ? &maps.v : &maps.dO, &bar.f_full, cur.head, cur.tok);
+                    tc_load_tile<NB>(f0, dkv ? &maps.k : &maps.q, &bar.f_full, own, cur.tok);
+                    tc_load_tile<NB>(f1, dkv ? &maps.v : &maps.dO, &bar.f_full, own, cur.tok);
                 }
                 ++nf;
             }
             BwdWork next{};
-            int h = dkv ? cur.head * a.group + (kShares ? cur.share * (a.group / a.split) : 0) : cur.head / a.group, tile = cur.first;   // of the other side
+            int h = dkv ? own * a.group + (kShares ? (cur.head >> 16) * (a.group / a.split) : 0) : own / a.group, tile = cur.first;   // of the other side
             const int steps = max(cur.n, 1);
             for (int j = 0; j < steps; ++j) {
                 // The next piece is asked for when this one's last loads but one are due: late, so that a CTA with
@@ -485,7 +484,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_bwd(const __grid_consta
             float *part0 = nullptr, *part1 = nullptr;   // a share's dV and dK
             const int64_t part_ts = static_cast<int64_t>(a.Hk) * a.D;
             if (kShares && dkv) {
-                part0 = a.part + (w.share * 2 * static_cast<int64_t>(a.sk.T) + w.tok) * part_ts + w.head * a.D;
+                part0 = a.part + ((w.head >> 16) * 2 * static_cast<int64_t>(a.sk.T) + w.tok) * part_ts + (w.head & 0xffff) * a.D;
                 part1 = part0 + a.sk.T * part_ts;
             }
             if (kShares && w.n == 0 && dkv) {

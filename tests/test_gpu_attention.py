@@ -158,6 +158,11 @@ def test_key_heads_whose_query_heads_are_shared_out(heads, D, causal):
         q, k, v, do, o, lse, grads = check(lq, lk, *heads, D, causal, "bf16", tail=tail, seed=D)
         again = lce.attention_backward(do, q, k, v, o, lse, cu(lq), cu(lk), causal=causal)
         assert all(torch.equal(x, y) for x, y in zip(grads, again))
+        if lq == lk:
+            dx = torch.zeros(q.shape[0], heads[0] + 2 * heads[1], D, device="cuda", dtype=torch.bfloat16)
+            outs = dx.split((heads[0], heads[1], heads[1]), dim=1)
+            lce.attention_backward(do, q, k, v, o, lse, cu(lq), cu(lk), causal=causal, dq=outs[0], dk=outs[1], dv=outs[2])
+            assert all(torch.equal(x, y) for x, y in zip(grads, outs))
         assert all(bool((t[sum(n):] == 0).all()) for t, n in zip(grads, (lq, lk, lk)))
 
 
