@@ -234,6 +234,13 @@ def _rows(name, t, ref):
     return t.data_ptr() or 16, st[0] if sh[0] > 1 else sh[1]
 
 
+def _spread(t):
+    """t, or a copy of it where all its rows are one row of memory (expanded): a
+    row stride of 0 stands for d in the library. The caller keeps it until the
+    call is enqueued."""
+    return t.contiguous() if t is not None and t.dim() == 2 and t.stride(0) == 0 and t.shape[0] > 1 else t
+
+
 def _vector(name, t, ref):
     if t.shape != ref.shape[1:] or t.dtype != ref.dtype or t.device != ref.device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [d] tensor of the stream's dtype")
@@ -273,11 +280,13 @@ def block_norm_forward(x, b=None, *, w_post=None, gate=None, w_pre=None, scale: 
     with gate [d] or [N, d]; any of w_post, gate and w_pre may be None (n and
     the matching rstd are None then). Without b, r is x itself. `out_r`
     receives r and may be x (the stream updated in place); `stream`: the stream
-    to run on (the current one if not given)."""
+    to run on (the current one if not given). Expanded rows are copied first."""
+    r = x
+    x, b, gate = _spread(x), _spread(b), _spread(gate)
     dtype, N, d, pb, p_post, pg, p_pre, full = _norm_inputs(x, b, w_post, gate, w_pre)
     px = _rows("x", x, x)
     device = x.device
-    r, n, rstd_post, rstd_pre = x, None, None, None
+    n, rstd_post, rstd_pre = None, None, None
     pr = pn = ps_post = ps_pre = 0
     if b is not None:
         if out_r is None:
@@ -307,6 +316,7 @@ def block_norm_backward(dr, dn, r, b=None, *, w_post=None, gate=None, w_pre=None
     and dn of n, the forward's r, b and rstd; None where the forward had no
     such input. `workspace`: a uint8 CUDA tensor of at least
     block_norm_workspace_size(N, d) bytes; `stream`: the stream to run on."""
+    dr, dn, r, b, gate = _spread(dr), _spread(dn), _spread(r), _spread(b), _spread(gate)
     ref = r if r is not None else b
     dtype, N, d, pb, p_post, pg, p_pre, full = _norm_inputs(ref, b, w_post, gate, w_pre)
     pdr = (0, 0) if dr is None else _rows("dr", dr, ref)
