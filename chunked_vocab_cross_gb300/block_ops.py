@@ -221,6 +221,9 @@ def attention(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, *, causal: bool = T
 
 # ---------------------------------------------------------------- block norms
 
+_ONLY_W_PRE = "without b there is only the norm by w_pre"
+
+
 def _rows(name, t, ref):
     """(address, row stride) of a [N, d] tensor whose rows are contiguous. The
     address of a tensor without rows is not read; it must not be NULL, which
@@ -253,7 +256,7 @@ def _norm_inputs(ref, b, w_post, gate, w_pre):
     if dtype is None or not ref.is_cuda or ref.dim() != 2:
         raise ValueError("the stream must be a bfloat16 or float32 CUDA tensor [N, d] (there is no CPU path)")
     if b is None and (w_post is not None or gate is not None or w_pre is None):
-        raise ValueError("without b there is only the norm by w_pre")
+        raise ValueError(_ONLY_W_PRE)
     pg, full = (0, 0), 0
     if gate is not None:
         full = 1 if gate.dim() == 2 else 0
@@ -376,6 +379,8 @@ def block_norm(x, b=None, *, w_post=None, gate=None, w_pre=None, scale: float = 
     """Autograd form of block_norm_forward: (r, n); n is None without w_pre,
     and without b the first output is x passed through."""
     if b is None:
+        if w_post is not None or gate is not None or w_pre is None:
+            raise ValueError(_ONLY_W_PRE)
         return _Norm.apply(x, w_pre, eps)
     return _BlockNorm.apply(x, b, w_post, gate, w_pre, scale, eps)
 
