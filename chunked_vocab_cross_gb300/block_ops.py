@@ -35,6 +35,10 @@ def _on_stream(call):
 
 
 def _stream(index: int) -> int:
+    """The current stream of device `index`, which the tensors are on. The library
+    runs on the current device, whatever the stream."""
+    if index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
     return _current_stream(index) if _current_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
@@ -43,8 +47,8 @@ def _scratch(given, need: int, device):
     if given is None:
         given = torch.empty(need, dtype=torch.uint8, device=device)
         return given.data_ptr(), need, given
-    if not given.is_cuda or not given.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if given.device != device or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
     return given.data_ptr(), given.numel() * given.element_size(), given
 
 

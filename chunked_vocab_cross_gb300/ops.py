@@ -11,7 +11,12 @@ from . import _abi
 _DT = {torch.bfloat16: _abi.LCE_BF16, torch.float32: _abi.LCE_FP32}
 
 
-def _stream(stream) -> int:
+def _stream(stream, t=None) -> int:
+    """The stream to run on for the tensor t. The library runs on the current
+    device, whatever the stream."""
+    if t is not None and (t.get_device() != torch.cuda.current_device()
+                          or (stream is not None and stream.device != t.device)):
+        raise ValueError(f"tensors on {t.device} need it to be the current one, and a stream of its own")
     s = torch.cuda.current_stream() if stream is None else stream
     return int(s.cuda_stream)
 
@@ -19,6 +24,8 @@ def _stream(stream) -> int:
 def _check_inputs(H: torch.Tensor, W: torch.Tensor, targets: torch.Tensor):
     if not (H.is_cuda and W.is_cuda and targets.is_cuda):
         raise ValueError("H, W and targets must be CUDA tensors (there is no CPU path)")
+    if not H.device == W.device == targets.device:
+        raise ValueError("H, W and targets must be on one device")
     if H.dtype not in _DT or W.dtype != H.dtype:
         raise ValueError("H and W must both be bfloat16 or both float32")
     if targets.dtype != torch.int64:
@@ -75,7 +82,7 @@ def lce_run(H, W, targets, ignore_index: int = -100, *, loss=None, dH=None, dW=N
     a.token_chunk = int(token_chunk)
     a.optim = ctypes.addressof(optim) if optim is not None else None
     a.row_gather = 1 if row_gather else 0
-    a.stream = _stream(stream)
+    a.stream = _stream(stream, H)
     _abi.check(_abi.lib().lce_run(ctypes.byref(a)), "lce_run")
 
 
@@ -86,7 +93,7 @@ def lce_forward(H, W, targets, ignore_index: int = -100, *, return_lse: bool = F
     lse = torch.empty(H.shape[0], dtype=torch.float32, device=H.device) if return_lse else None
     if H.dtype == torch.bfloat16 and not return_lse:
         _abi.check(_abi.lib().lce_forward(H.data_ptr(), W.data_ptr(), targets.data_ptr(), int(ignore_index),
-                                          H.shape[0], H.shape[1], W.shape[0], loss.data_ptr(), _stream(stream)),
+                                          H.shape[0], H.shape[1], W.shape[0], loss.data_ptr(), _stream(stream, H)),
                    "lce_forward")
     else:
         lce_run(H, W, targets, ignore_index, loss=loss, lse=lse, stream=stream)
@@ -113,7 +120,7 @@ def lce_forward_backward(H, W, targets, ignore_index: int = -100, *, dW=None, ac
         _abi.check(_abi.lib().lce_forward_backward(H.data_ptr(), W.data_ptr(), targets.data_ptr(),
                                                    int(ignore_index), H.shape[0], H.shape[1], W.shape[0],
                                                    loss.data_ptr(), dH.data_ptr(), dW.data_ptr(),
-                                                   _stream(stream)),
+                                                   _stream(stream, H)),
                    "lce_forward_backward")
     else:
         lce_run(H, W, targets, ignore_index, loss=loss, dH=dH, dW=dW, accumulate_dW=accumulate_dW,
@@ -143,7 +150,7 @@ def lce_backward(H, W, targets, lse, ignore_index: int = -100, *, grad_loss=None
         _abi.check(_abi.lib().lce_backward(H.data_ptr(), W.data_ptr(), targets.data_ptr(), int(ignore_index),
                                            H.shape[0], H.shape[1], W.shape[0], lse.data_ptr(),
                                            grad_loss.data_ptr() if grad_loss is not None else None,
-                                           dH.data_ptr(), dW.data_ptr(), _stream(stream)),
+                                           dH.data_ptr(), dW.data_ptr(), _stream(stream, H)),
                    "lce_backward")
     else:
         lce_run(H, W, targets, ignore_index, dH=dH, dW=dW, accumulate_dW=accumulate_dW, lse_in=lse,
@@ -161,7 +168,7 @@ def lce_compact(targets, ignore_index: int = -100, V: int | None = None, *, stre
     inv = torch.empty(N, dtype=torch.int32, device=targets.device)
     counts = torch.empty(2, dtype=torch.int32, device=targets.device)
     _abi.check(_abi.lib().lce_compact(targets.data_ptr(), N, int(ignore_index), int(V if V else 2**31 - 1),
-                                      idx.data_ptr(), inv.data_ptr(), counts.data_ptr(), _stream(stream)),
+                                      idx.data_ptr(), inv.data_ptr(), counts.data_ptr(), _stream(stream, targets)),
                "lce_compact")
     nv, bad = counts.tolist()
     return idx[:nv], inv, nv, bad
@@ -296,7 +303,7 @@ def embedding_forward(W, tokens, pad_id: int = 0, *, out=None, stream=None):
     """E [N, d] (W's dtype): rows of W for the tokens, zero rows where the token
     is pad_id; non-padding ids outside [0, V) give zero rows and set the
     target-range bit of the device status word. `out` receives E if given."""
-    if not (W.is_cuda and tokens.is_cuda) or W.dtype not in _DT or tokens.dtype != torch.int64:
+    if not W.is_cuda or tokens.device != W.device or W.dtype not in _DT or tokens.dtype != torch.int64:
         raise ValueError("W must be a bf16/fp32 CUDA tensor and tokens int64 on the same device")
     if W.dim() != 2 or tokens.dim() != 1 or not W.is_contiguous():
         raise ValueError("W must be a contiguous [V, d] tensor and tokens [N]")
@@ -307,7 +314,7 @@ def embedding_forward(W, tokens, pad_id: int = 0, *, out=None, stream=None):
         raise ValueError("out must be a contiguous [N, d] tensor of W's dtype")
     _abi.check(_abi.lib().lce_embedding_forward(_DT[W.dtype], W.data_ptr(), tokens.data_ptr(), int(pad_id),
                                                 tokens.shape[0], W.shape[1], W.shape[0], out.data_ptr(),
-                                                _stream(stream)), "lce_embedding_forward")
+                                                _stream(stream, W)), "lce_embedding_forward")
     return out
 
 
@@ -323,7 +330,7 @@ def embedding_backward(dE, tokens, pad_id: int, V: int, *, dW=None, accumulate: 
     given bf16 dW (each row sum rounded once; overwritten). `workspace`: a
     uint8 CUDA tensor of at least embedding_workspace_size(N, d) bytes; without
     it the library allocates its scratch on the stream."""
-    if not (dE.is_cuda and tokens.is_cuda) or dE.dtype not in _DT or tokens.dtype != torch.int64:
+    if not dE.is_cuda or tokens.device != dE.device or dE.dtype not in _DT or tokens.dtype != torch.int64:
         raise ValueError("dE must be a bf16/fp32 CUDA tensor and tokens int64 on the same device")
     if dE.dim() != 2 or tokens.dim() != 1 or dE.shape[0] != tokens.shape[0]:
         raise ValueError("dE must be [N, d] and tokens [N]")
@@ -339,12 +346,12 @@ def embedding_backward(dE, tokens, pad_id: int, V: int, *, dW=None, accumulate: 
     if dW.dtype == torch.bfloat16:
         _abi.check(_abi.lib().lce_embedding_backward_bf16(_DT[dE.dtype], dE.data_ptr(), tokens.data_ptr(),
                                                           int(pad_id), tokens.shape[0], dE.shape[1], V,
-                                                          dW.data_ptr(), ws_ptr, ws_bytes, _stream(stream)),
+                                                          dW.data_ptr(), ws_ptr, ws_bytes, _stream(stream, dE)),
                    "lce_embedding_backward_bf16")
     else:
         _abi.check(_abi.lib().lce_embedding_backward(_DT[dE.dtype], dE.data_ptr(), tokens.data_ptr(), int(pad_id),
                                                      tokens.shape[0], dE.shape[1], V, dW.data_ptr(),
-                                                     1 if accumulate else 0, ws_ptr, ws_bytes, _stream(stream)),
+                                                     1 if accumulate else 0, ws_ptr, ws_bytes, _stream(stream, dE)),
                    "lce_embedding_backward")
     return dW
 
