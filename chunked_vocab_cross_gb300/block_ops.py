@@ -14,6 +14,7 @@ import functools
 import operator
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _abi
 
@@ -221,6 +222,7 @@ class _Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
         # autograd may hand over an expanded or permuted gradient, whose rows the kernels cannot read
@@ -377,6 +379,7 @@ class _BlockNorm(torch.autograd.Function):
         return r, n
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dr, dn):
         r, b, w_post, gate, w_pre, rstd_post, rstd_pre = ctx.saved_tensors
         ref = r if r is not None else b
@@ -414,6 +417,7 @@ class _Norm(torch.autograd.Function):
         return x.view_as(x), n
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dr, dn):
         x, w_pre, rstd = ctx.saved_tensors
         if dn is None:

@@ -5,6 +5,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _abi
 
@@ -211,6 +212,7 @@ class _LinearCrossEntropySplit(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         H, W, targets, lse = ctx.saved_tensors
         # the gradient of W in W's dtype, written by the library (a bf16 W
@@ -364,6 +366,7 @@ class _Embedding(torch.autograd.Function):
         return embedding_forward(W, tokens, pad_id)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dE):
         (tokens,) = ctx.saved_tensors
         # the gradient of W in W's dtype, written by the library from dE as it

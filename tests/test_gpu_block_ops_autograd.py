@@ -1,5 +1,5 @@
 """What autograd is told of the block operators: tensors that they write in
-place."""
+place, and gradients that cannot be differentiated again."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -63,3 +63,25 @@ def test_a_saved_tensor_that_was_overwritten_is_an_error():
     lce.clip_grad_norm([g], 0.1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+def calls():
+    q, k, v = (rand(20, 2, 32).requires_grad_(True) for _ in range(3))
+    W = rand(100, 64).requires_grad_(True)
+    x, b, w = rand(6, 64).requires_grad_(True), rand(6, 64).requires_grad_(True), rand(64).requires_grad_(True)
+    return {"attention": (q, lambda: lce.attention(q, k, v)), "block_norm": (b, lambda: lce.block_norm(x, b, w_post=w, w_pre=w)[1]),
+            "norm alone": (x, lambda: lce.block_norm(x, w_pre=w)[1]),
+            "linear_cross_entropy": (x, lambda: lce.linear_cross_entropy(x, W, torch.arange(6, device="cuda"))),
+            "embedding": (W, lambda: lce.embedding(W, torch.arange(6, device="cuda")))}
+
+
+@pytest.mark.parametrize("name", ["attention", "block_norm", "norm alone", "linear_cross_entropy", "embedding"])
+def test_gradients_are_not_differentiated_again_without_a_word(name):
+    """A penalty on a gradient: an error, not a gradient that lacks the penalty's terms."""
+    leaf, call = calls()[name]
+    (first,) = torch.autograd.grad(call().square().sum(), leaf)
+    (grad,) = torch.autograd.grad(call().square().sum(), leaf, create_graph=True)
+    assert grad.requires_grad
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        grad.square().sum().backward()
+    assert first.shape == grad.shape
