@@ -21,6 +21,7 @@ from . import _abi
 _DT = {torch.bfloat16: _abi.LCE_BF16, torch.float32: _abi.LCE_FP32}
 _ATTN, _NORM = _abi.packer(_abi.LceAttn), _abi.packer(_abi.LceNorm)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # CUDA is up: the tensors are there
 
 
 def _on_stream(call):
@@ -38,7 +39,7 @@ def _on_stream(call):
 def _stream(index: int) -> int:
     """The current stream of device `index`, which the tensors are on. The library
     runs on the current device, whatever the stream."""
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
     return _current_stream(index) if _current_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
@@ -241,6 +242,15 @@ def attention(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, *, causal: bool = T
 _ONLY_W_PRE = "without b there is only the norm by w_pre"
 
 
+class _Expanded(Exception):
+    """All rows of a tensor are one row of memory. The library has no such
+    stride: 0 stands for d there."""
+
+
+def _spread(t):
+    return t.contiguous() if t is not None and t.dim() == 2 and t.stride(0) == 0 else t
+
+
 def _rows(name, t, ref):
     """(address, row stride) of a [N, d] tensor whose rows are contiguous. The
     address of a tensor without rows is not read; it must not be NULL, which
@@ -251,14 +261,11 @@ def _rows(name, t, ref):
     st = t.stride()
     if st[1] != 1 and sh[1] > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.data_ptr() or 16, st[0] if sh[0] > 1 else sh[1]
-
-
-def _spread(t):
-    """t, or a copy of it where all its rows are one row of memory (expanded): a
-    row stride of 0 stands for d in the library. The caller keeps it until the
-    call is enqueued."""
-    return t.contiguous() if t is not None and t.dim() == 2 and t.stride(0) == 0 and t.shape[0] > 1 else t
+    if sh[0] < 2:
+        return t.data_ptr() or 16, sh[1]
+    if st[0] == 0:
+        raise _Expanded
+    return t.data_ptr(), st[0]
 
 
 def _vector(name, t, ref):
@@ -301,12 +308,15 @@ def block_norm_forward(x, b=None, *, w_post=None, gate=None, w_pre=None, scale: 
     the matching rstd are None then). Without b, r is x itself. `out_r`
     receives r and may be x (the stream updated in place); `stream`: the stream
     to run on (the current one if not given). Expanded rows are copied first."""
-    r = x
-    x, b, gate = _spread(x), _spread(b), _spread(gate)
-    dtype, N, d, pb, p_post, pg, p_pre, full = _norm_inputs(x, b, w_post, gate, w_pre)
-    px = _rows("x", x, x)
+    try:
+        dtype, N, d, pb, p_post, pg, p_pre, full = _norm_inputs(x, b, w_post, gate, w_pre)
+        px = _rows("x", x, x)
+    except _Expanded:
+        r, *rest = block_norm_forward(_spread(x), _spread(b), w_post=w_post, gate=_spread(gate), w_pre=w_pre, scale=scale,
+                                      eps=eps, out_r=out_r)
+        return x if b is None else r, *rest
     device = x.device
-    n, rstd_post, rstd_pre = None, None, None
+    r, n, rstd_post, rstd_pre = x, None, None, None
     pr = pn = ps_post = ps_pre = 0
     if b is not None:
         if out_r is None:
@@ -338,15 +348,18 @@ def block_norm_backward(dr, dn, r, b=None, *, w_post=None, gate=None, w_pre=None
     and dn of n, the forward's r, b and rstd; None where the forward had no
     such input. `workspace`: a uint8 CUDA tensor of at least
     block_norm_workspace_size(N, d) bytes; `stream`: the stream to run on."""
-    dr, dn, r, b, gate = _spread(dr), _spread(dn), _spread(r), _spread(b), _spread(gate)
     ref = r if r is not None else b
-    dtype, N, d, pb, p_post, pg, p_pre, full = _norm_inputs(ref, b, w_post, gate, w_pre)
-    pdr = (0, 0) if dr is None else _rows("dr", dr, ref)
-    pdn = pr = (0, 0)
-    if w_pre is not None:
-        if dn is None or r is None:
-            raise ValueError("with w_pre the backward needs dn and r")
-        pdn, pr = _rows("dn", dn, ref), _rows("r", r, ref)
+    try:
+        dtype, N, d, pb, p_post, pg, p_pre, full = _norm_inputs(ref, b, w_post, gate, w_pre)
+        pdr = (0, 0) if dr is None else _rows("dr", dr, ref)
+        pdn = pr = (0, 0)
+        if w_pre is not None:
+            if dn is None or r is None:
+                raise ValueError("with w_pre the backward needs dn and r")
+            pdn, pr = _rows("dn", dn, ref), _rows("r", r, ref)
+    except _Expanded:
+        return block_norm_backward(_spread(dr), _spread(dn), _spread(r), _spread(b), w_post=w_post, gate=_spread(gate),
+                                   w_pre=w_pre, scale=scale, rstd_post=rstd_post, rstd_pre=rstd_pre, workspace=workspace)
     device = ref.device
     stats = [0, 0]
     for i, (name, w, t) in enumerate((("rstd_post", w_post, rstd_post), ("rstd_pre", w_pre, rstd_pre))):

@@ -31,6 +31,7 @@ def test_tensors_of_another_device_than_the_current_one(monkeypatch):
 
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream())
+    monkeypatch.setattr(block_ops, "_current_device", lambda: 0)
     monkeypatch.setattr(block_ops, "_current_stream", lambda index: 7)
     assert block_ops._stream(0) == 7
     with pytest.raises(ValueError, match="current device"):

@@ -5,6 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import chunked_vocab_cross_gb300 as lce  # noqa: E402
+from chunked_vocab_cross_gb300 import block_ops  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -49,6 +50,7 @@ def test_refused_unless_current(name, monkeypatch):
     torch.cuda.synchronize()
     launches = lce.launch_count()
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(block_ops, "_current_device", lambda: 1)
     with pytest.raises(ValueError, match="current"):
         call()
     assert lce.launch_count() == launches
