@@ -16,7 +16,7 @@ namespace {
 // each adds up all blocks' sums first (362 us; 371).
 constexpr int kSqThreads = 256, kSqBlocksPerSm = 8;
 constexpr int kClipThreads = 512;
-constexpr int kChunkBytes = 65536;   // bytes of a tensor that a block takes at a time: eight loads a thread
+constexpr int kChunkBytes = 65536;   // bytes of a tensor that a block takes at a time: 16 loads a thread (the scaling: eight)
 // Tensors a launch takes: the table travels as a kernel argument (9 KB; a short
 // one for short lists made no difference to the host).
 constexpr int kTable = 240;
@@ -106,6 +106,26 @@ __device__ __forceinline__ float span_squares(const ClipEntry &e, const Span &sp
     return s;
 }
 
+// The same share in fp64, for squares whose sum overflows fp32 (values from about 1e18 on). A function of its own, so
+// that the common case keeps its registers.
+__device__ __forceinline__ double square64(float x) { return static_cast<double>(x) * x; }
+template <typename T>
+__device__ __noinline__ double span_squares64(const T *g, int64_t begin, int64_t vb, int64_t ve, int64_t end) {
+    constexpr int kV = 16 / sizeof(T), nt = kSqThreads;
+    const int t = threadIdx.x;
+    double s = 0.0;
+    for (int64_t i = begin + t; i < vb; i += nt) s += square64(f32(g[i]));
+    for (int64_t i = vb + t * kV; i < ve; i += nt * kV)
+        for (int k = 0; k < kV; ++k) s += square64(f32(g[i + k]));
+    for (int64_t i = ve + t; i < end; i += nt) s += square64(f32(g[i]));
+    return s;
+}
+template <typename T>
+__device__ __forceinline__ double span_sum(const ClipEntry &e, const Span &sp) {
+    const float s = span_squares<T>(e, sp);
+    return isinf(s) ? span_squares64(static_cast<const T *>(e.g), sp.begin, sp.vb, sp.ve, sp.end) : s;
+}
+
 // Sum over the block, the same for all threads, in a fixed order. A warp's fp64
 // addition takes 16 cycles of an SM, so one warp joins the warps' sums for all
 // (done by every thread, they were half of a short call).
@@ -124,15 +144,16 @@ __device__ __forceinline__ double block_sum(double v) {
     return total;
 }
 
-// part[block] = sum of the squares of the block's chunks: fp32 along a
-// thread's elements of one chunk, fp64 across chunks and threads.
+// part[block] = sum of the squares of the block's chunks: fp32 along a thread's
+// elements of one chunk (at most 66 of fp32, 130 of bf16) while they fit it,
+// fp64 across chunks and threads.
 __global__ void __launch_bounds__(kSqThreads) k_clip_squares(const __grid_constant__ ClipTable tab, double *part) {
     double s = 0.0;
     for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
         const int i = entry_of(tab, c), k = c - tab.first[i];
         const ClipEntry &e = tab.t[i];
-        s += e.fp32 ? span_squares<float>(e, span_of<float, kChunkBytes>(e, k))
-                    : span_squares<__nv_bfloat16>(e, span_of<__nv_bfloat16, kChunkBytes>(e, k));
+        s += e.fp32 ? span_sum<float>(e, span_of<float, kChunkBytes>(e, k))
+                    : span_sum<__nv_bfloat16>(e, span_of<__nv_bfloat16, kChunkBytes>(e, k));
     }
     s = block_sum<kSqThreads>(s);
     griddep_launch_dependents();
@@ -248,6 +269,17 @@ struct Held {
         }
         return s;
     }
+    // the lane's sum of squares in fp64
+    __device__ __forceinline__ double squares64() const {
+        double s = square64(single);
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const T *x = reinterpret_cast<const T *>(&v[k]);
+#pragma unroll
+            for (int q = 0; q < kV; ++q) s += square64(f32(x[q]));
+        }
+        return s;
+    }
     __device__ __forceinline__ void store(const ClipEntry &e, float c, int lane) const {
         T *o = static_cast<T *>(e.out);
         const bool vec = (reinterpret_cast<uintptr_t>(e.g) ^ reinterpret_cast<uintptr_t>(o)) % 16 == 0;
@@ -267,15 +299,16 @@ struct Held {
     }
 };
 
-// Both passes by one cluster: fp32 within a warp's chunk, fp64 across the
-// chunks, joined in block order by one warp of each block (a warp's fp64
+// Both passes by one cluster: fp32 within a warp's chunk (a lane's 33 or 65
+// elements, then the lanes) while the squares fit it, fp64 across the chunks,
+// joined in block order by one warp of each block (a warp's fp64
 // addition takes 16 cycles of an SM, its square root hundreds: done by every
 // warp they were most of the call, 9.9 us for 0.1 MB).
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads)
     k_clip_cluster(const __grid_constant__ ClipTable tab, int clip, float max_norm, float eps, int in_place, float *norm,
                    float *factor) {
-    __shared__ float red[kClusterThreads / 32], f;
-    __shared__ double mine;
+    __shared__ double red[kClusterThreads / 32], mine;
+    __shared__ float f;
     const int rank = static_cast<int>(cluster_ctarank()), warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int c0 = rank + warp * kCluster;   // neighbouring chunks to different SMs
     const bool any = c0 < tab.chunks;
@@ -286,7 +319,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThrea
     float s = 0.f;
     if (any) s = e.fp32 ? hf.load(e, k, lane) : hb.load(e, k, lane);
     for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    if (lane == 0) red[warp] = s;
+    double chunk = s;
+    if (isinf(s)) {   // for every lane of the warp: they all have the same sum
+        chunk = e.fp32 ? hf.squares64() : hb.squares64();
+        for (int m = 16; m; m >>= 1) chunk += __shfl_xor_sync(0xffffffffu, chunk, m);
+    }
+    if (lane == 0) red[warp] = chunk;
     __syncthreads();
     if (warp == 0) {
         double v = red[lane];

@@ -457,8 +457,10 @@ size_t lce_block_norm_workspace_size(const lce_norm_t *args);
  * grad and must not overlap any other tensor. A norm that is not finite gives
  * factor 0 (infinite) or NaN, as the formulas say. norm is a device fp32
  * scalar; factor an optional one. The squares are summed in fp32 over short
- * runs and in fp64 across them, in a fixed order (deterministic); an element
- * beyond 1.8e19 makes the norm infinite. Scratch: lce_clip_workspace_size
+ * runs and in fp64 across them, in a fixed order (deterministic); a run whose
+ * squares overflow fp32 is summed in fp64, so the norm is infinite only where
+ * fp32 cannot hold it. Elements below 1.1e-19, whose squares are subnormal,
+ * lose bits; below 2.6e-23 they count as zero. Scratch: lce_clip_workspace_size
  * bytes of device memory (16-byte aligned) or NULL (a stream-ordered
  * allocation; none for up to 1 MB of gradients, whose sums need no memory).
  */
