@@ -9,3 +9,16 @@ if ROOT not in sys.path:
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_103a) and the built liblce.so")
     config.addinivalue_line("markers", "slow: long-running (full-size oracle sweeps)")
+
+
+# These hand the library made-up addresses: they run only where nothing can be launched on them.
+MADE_UP_ADDRESSES = {"test_abi.py", "test_block_ops_abi.py"}
+
+
+def pytest_collection_modifyitems(items):
+    import pytest
+    import torch
+    found = [i for i in items if os.path.basename(str(i.path)) in MADE_UP_ADDRESSES]
+    if found and torch.cuda.is_available():
+        for i in found:
+            i.add_marker(pytest.mark.skip(reason="made-up addresses: only where there is no GPU"))
