@@ -12,6 +12,16 @@ using namespace lce;
 
 namespace {
 
+// Whether the rows of D elements that lie t * ts + h * hs on (t < T, h < H) are apart from one another.
+bool rows_apart(int64_t ts, int64_t hs, int64_t T, int64_t H, int64_t D) {
+    if ((T > 1 && ts < D) || (H > 1 && hs < D)) return false;
+    if (T <= 1 || H <= 1 || ts >= (H - 1) * hs + D || (hs - D) / ts >= T - 1) return true;   // tokens, or heads, outermost
+    for (int64_t h = 1; h < H; ++h) {   // interleaved: the tokens on either side of the head's distance
+        const int64_t t = h * hs / ts, past = h * hs - t * ts;
+        if ((t < T && past < D) || (t + 1 < T && ts - past < D)) return false;
+    }
+    return true;
+}
 
 lce_status_t check_side(const void *p, int64_t ts, int64_t hs, int64_t T, int64_t H, int64_t D, int elt, bool out) {
     if (T == 0) return LCE_OK;   // an empty side is never read or written
@@ -19,8 +29,7 @@ lce_status_t check_side(const void *p, int64_t ts, int64_t hs, int64_t T, int64_
     if (host_misaligned(p) || (ts * elt) % 16 || (hs * elt) % 16) return LCE_ERR_ALIGN;
     if (ts < 0 || hs < 0 || ts >= (int64_t(1) << 36) || hs >= (int64_t(1) << 36)) return LCE_ERR_SHAPE;
     if ((T > 1 && ts == 0) || (H > 1 && hs == 0)) return LCE_ERR_SHAPE;   // tensor maps have no zero strides
-    // rows of an output must not meet
-    if (out && ((T > 1 && ts < D) || (H > 1 && hs < D))) return LCE_ERR_SHAPE;
+    if (out && !rows_apart(ts, hs, T, H, D)) return LCE_ERR_SHAPE;
     return LCE_OK;
 }
 

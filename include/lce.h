@@ -372,7 +372,9 @@ lce_status_t lce_embedding_backward_bf16(lce_dtype_t dtype, const void *dE, cons
  * LCE_FP32 runs in fp32 arithmetic throughout. Requirements: 1 <= D <= 128,
  * D % 8 == 0, Hq a multiple of Hk, 0 <= Tq, Tk < 2^30, 1 <= B < 2^30, Tq and Tk multiples
  * of B without offsets; bases 16-byte aligned, strides multiples of 16 bytes,
- * positive (but for a single head or token).
+ * positive (but for a single head or token). The rows of an output must be apart
+ * from one another (checked), and outputs apart from each other and from every
+ * input (not checked).
  * Results are deterministic. Scratch: lce_attention_forward_workspace_size bytes
  * (0 but for few rows over long keys, whose keys are taken in ranges) or
  * lce_attention_workspace_size bytes (backward), device, 16-byte aligned, or

@@ -12,7 +12,7 @@ def pytest_configure(config):
 
 
 # These hand the library made-up addresses: they run only where nothing can be launched on them.
-MADE_UP_ADDRESSES = {"test_abi.py", "test_block_ops_abi.py"}
+MADE_UP_ADDRESSES = {"test_abi.py", "test_block_ops_abi.py", "test_attention_rules.py"}
 
 
 def pytest_collection_modifyitems(items):
