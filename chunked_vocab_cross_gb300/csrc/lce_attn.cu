@@ -112,7 +112,12 @@ lce_status_t launch(const HostDev &dev, int64_t blocks, int threads, int smem, c
     return host_launched();
 }
 
+// SMs that the two rules below reckon with: those of the one part this library runs on, as a constant, since the
+// workspace functions answer from the sizes alone, without a device.
 constexpr int kSms = 152;
+
+// Tiles of a sequence of average length, which is rounded up: a side with any tokens has a tile in each.
+int64_t average_tiles(int64_t T, int64_t B) { return ((T + B - 1) / B + kTcTile - 1) / kTcTile; }
 
 // Ranges that a row's keys are split into in the forward. Few rows and heads over long keys leave most SMs without
 // work; their walks are split as far as that makes the longest shorter. The times compared are in key tiles of a walk
@@ -120,7 +125,7 @@ constexpr int kSms = 152;
 // the lengths only the averages are known here. (32 heads of 8 key heads of 128 channels: one row over 2048 keys 17 us
 // against 26, over 32768 53 against 322; 2 heads, 8192 causal tokens: 44 against 86.)
 int ranges(const lce_attn_t *a) {
-    const int64_t group = a->Hq / a->Hk, tq = (a->Tq / a->B + kTcTile - 1) / kTcTile, tk = (a->Tk / a->B + kTcTile - 1) / kTcTile;
+    const int64_t group = a->Hq / a->Hk, tq = average_tiles(a->Tq, a->B), tk = average_tiles(a->Tk, a->B);
     if (a->dtype != LCE_BF16 || tk <= 8 || a->Tq * a->Hq > (1 << 24)) return 1;
     const double pieces = static_cast<double>(a->B) * (group % 2 == 0 ? tq * a->Hq / 2 : (tq + 1) / 2 * a->Hq),
                  mask = a->causal && a->Tq == a->Tk ? 0.5 : 1.0, merge = static_cast<double>(a->Tq * a->Hq * a->D) * 8 / 3e6;
@@ -201,7 +206,7 @@ int stat_tile(const lce_attn_t *a) { return a->dtype == LCE_BF16 ? kTcTile : kSi
 // of 1 over 8192 295 against 631; split all the same, 28 heads of 4 over eight sequences of 256 took 59 against 32, and
 // 32 of 8 over 2048 tokens 107 against 92.)
 int shares(const lce_attn_t *a, bool causal) {
-    const int64_t group = a->Hq / a->Hk, tq = (a->Tq / a->B + kTcTile - 1) / kTcTile, tk = (a->Tk / a->B + kTcTile - 1) / kTcTile;
+    const int64_t group = a->Hq / a->Hk, tq = average_tiles(a->Tq, a->B), tk = average_tiles(a->Tk, a->B);
     if (a->dtype != LCE_BF16 || group == 1 || a->Tk * a->Hk > (1 << 24)) return 1;
     const double kv = static_cast<double>(a->B) * tk * a->Hk, q = static_cast<double>(a->B) * tq * a->Hq, mask = causal ? 0.5 : 1.0;
     auto time = [&](int64_t n) {   // of the longest piece, or of everything shared out

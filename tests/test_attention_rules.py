@@ -53,3 +53,31 @@ def test_output_rows_agree_with_a_count(lib):
         apart = len(set(cells)) == len(cells)
         got = lib.lce_attention_forward(_attn(Tq=T, Tk=T, Hq=H, Hk=1, D=16, q_ts=16 * H, q_hs=16, o_ts=ts, o_hs=hs))
         assert (got in OK) == apart and (apart or got == 2), (T, H, ts, hs, got)
+
+
+def _ranges(lib, Tq, Hq, D, **kw):
+    """Ranges that the keys are taken in, from the scratch: each has an o and an lse in fp32."""
+    need = lib.lce_attention_forward_workspace_size(_attn(Tq=Tq, Hq=Hq, D=D, cu_q=4096, cu_k=4096, **kw))
+    each = Tq * Hq * (D + 1) * 4
+    assert need % each == 0
+    return max(need // each, 1)
+
+
+@pytest.mark.parametrize("B,heads,keys", [(1000, (2, 1), 4096), (64, (2, 1), 4096), (64, (32, 8), 4096), (8, (8, 8), 32768)])
+def test_a_sequence_without_a_query_does_not_change_the_ranges(lib, B, heads, keys):
+    """One-token decoding where a sequence or two have nothing to ask: still a tile of work for each of the others."""
+    kw = dict(B=B, Tk=B * keys, Hk=heads[1], causal=0)
+    for causal in (0, 1):
+        kw["causal"] = causal
+        n = _ranges(lib, B, heads[0], 128, **kw)
+        assert n == _ranges(lib, B - 1, heads[0], 128, **kw) == _ranges(lib, B // 2 + 1, heads[0], 128, **kw)
+    assert _ranges(lib, 1, heads[0], 128, **dict(kw, B=1, Tk=keys)) >= n
+
+
+@pytest.mark.parametrize("B", [2, 9, 100])
+def test_a_sequence_without_a_query_does_not_change_the_shares(lib, B):
+    """The backward's scratch over its row statistics: as many shares of dK and dV for B - 1 queries as for B."""
+    def shares(Tq, Hq=16):
+        ws = lambda h: lib.lce_attention_workspace_size(_attn(Tq=Tq, Tk=200 * B, B=B, Hq=Hq, Hk=h, D=64, cu_q=4096, cu_k=4096))  # noqa: E731
+        return ws(1) - ws(Hq)   # with as many key heads as query heads there is nothing to share
+    assert shares(B) == shares(B - 1)
