@@ -82,10 +82,9 @@ AttnArgs make_args(const lce_attn_t *a, const HostDev &dev) {
 }
 
 // Tensor map of [tokens][heads][D] bf16 for boxes of 128 tokens of one head by
-// 64 channels. A tensor without tokens is never loaded from.
+// 64 channels.
 lce_status_t encode(CUtensorMap *m, const HostDev &dev, const void *p, int64_t T, int64_t H, int64_t D, int64_t ts,
                     int64_t hs) {
-    if (T == 0) return LCE_OK;
     if (H == 1) hs = D;   // strides of dimensions of one entry are not used, but have to be valid
     if (T == 1) ts = D;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
@@ -151,12 +150,30 @@ bool few_outputs(const lce_attn_t *a) {
     return a->Tq * a->Hq * a->D <= (1 << 18) && a->Tq <= a->B * 512 && a->Tk <= a->B * 512;
 }
 
+// The maps of one side, queries or keys. A side without tokens has none of its own and is never loaded from; the kernels
+// prefetch all maps, so it gets the other side's.
+lce_status_t encode_queries(AttnMaps *m, const HostDev &dev, const lce_attn_t *a, bool backward) {
+    lce_status_t s = encode(&m->q, dev, a->q, a->Tq, a->Hq, a->D, a->q_ts, a->q_hs);
+    if (s == LCE_OK && backward) s = encode(&m->dO, dev, a->dO, a->Tq, a->Hq, a->D, a->dO_ts, a->dO_hs);
+    return s;
+}
+lce_status_t encode_keys(AttnMaps *m, const HostDev &dev, const lce_attn_t *a) {
+    const lce_status_t s = encode(&m->k, dev, a->k, a->Tk, a->Hk, a->D, a->k_ts, a->k_hs);
+    return s != LCE_OK ? s : encode(&m->v, dev, a->v, a->Tk, a->Hk, a->D, a->v_ts, a->v_hs);
+}
+lce_status_t encode_maps(AttnMaps *m, const HostDev &dev, const lce_attn_t *a, bool backward) {
+    lce_status_t s = LCE_OK;
+    if (a->Tq > 0) s = encode_queries(m, dev, a, backward);
+    if (a->Tk > 0 && s == LCE_OK) s = encode_keys(m, dev, a);
+    if (a->Tq == 0) m->q = m->dO = m->k;
+    if (a->Tk == 0) m->k = m->v = m->q;
+    return s;
+}
+
 template <int KS>
 lce_status_t forward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &dev, cudaStream_t st) {
     AttnMaps maps;
-    lce_status_t s = encode(&maps.q, dev, a->q, a->Tq, a->Hq, a->D, a->q_ts, a->q_hs);
-    if (s == LCE_OK) s = encode(&maps.k, dev, a->k, a->Tk, a->Hk, a->D, a->k_ts, a->k_hs);
-    if (s == LCE_OK) s = encode(&maps.v, dev, a->v, a->Tk, a->Hk, a->D, a->v_ts, a->v_hs);
+    lce_status_t s = encode_maps(&maps, dev, a, false);
     if (s != LCE_OK) return s;
     const int64_t work = r.pair_heads ? seq_slots(r.sq.T, r.sq.B, kTcTile) * (r.Hq / 2) : seq_slots(r.sq.T, r.sq.B, 2 * kTcTile) * r.Hq;
     if (r.split == 1)
@@ -229,10 +246,7 @@ lce_status_t backward_tc(const lce_attn_t *a, const AttnArgs &r, const HostDev &
     const int64_t dq = seq_slots(r.sq.T, r.sq.B, kTcTile) * r.Hq, dkv = seq_slots(r.sk.T, r.sk.B, kTcTile) * r.Hk * r.split;
     if (dq + dkv >= (int64_t(1) << 31)) return LCE_ERR_SHAPE;
     AttnMaps maps;
-    lce_status_t s = encode(&maps.q, dev, a->q, a->Tq, a->Hq, a->D, a->q_ts, a->q_hs);
-    if (s == LCE_OK) s = encode(&maps.k, dev, a->k, a->Tk, a->Hk, a->D, a->k_ts, a->k_hs);
-    if (s == LCE_OK) s = encode(&maps.v, dev, a->v, a->Tk, a->Hk, a->D, a->v_ts, a->v_hs);
-    if (s == LCE_OK) s = encode(&maps.dO, dev, a->dO, a->Tq, a->Hq, a->D, a->dO_ts, a->dO_hs);
+    lce_status_t s = encode_maps(&maps, dev, a, true);
     if (s == LCE_OK) s = row_stats<__nv_bfloat16, kTcTile>(r, dev, st);
     if (s != LCE_OK) return s;
     auto go = [&](auto two, auto parts) {
