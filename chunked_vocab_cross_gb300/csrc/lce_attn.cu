@@ -224,7 +224,7 @@ int stat_tile(const lce_attn_t *a) { return a->dtype == LCE_BF16 ? kTcTile : kSi
 // 32 of 8 over 2048 tokens 107 against 92.)
 int shares(const lce_attn_t *a, bool causal) {
     const int64_t group = a->Hq / a->Hk, tq = average_tiles(a->Tq, a->B), tk = average_tiles(a->Tk, a->B);
-    if (a->dtype != LCE_BF16 || group == 1 || a->Tk * a->Hk > (1 << 24)) return 1;
+    if (a->dtype != LCE_BF16 || group == 1 || a->Tk == 0 || a->Tk * a->Hk > (1 << 24)) return 1;
     const double kv = static_cast<double>(a->B) * tk * a->Hk, q = static_cast<double>(a->B) * tq * a->Hq, mask = causal ? 0.5 : 1.0;
     auto time = [&](int64_t n) {   // of the longest piece, or of everything shared out
         const double more = n > 1 ? 5 : 3, walk = static_cast<double>(tq * group / n);
