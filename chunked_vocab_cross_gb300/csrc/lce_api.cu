@@ -66,6 +66,13 @@ constexpr int kMaxGBuffers = 4;
 inline bool has_optim(const lce_args_t *a) { return a->optim && a->optim->kind != LCE_OPT_NONE; }
 
 thread_local int t_last_cuda = 0;
+
+// Keeps an error for lce_last_cuda_error() and takes it out of the runtime's own record, where the next launch, here or
+// in the program around the library, would meet it as its own.
+void note_error(cudaError_t e) {
+    t_last_cuda = e;
+    cudaGetLastError();
+}
 std::atomic<int64_t> g_launches{0};
 std::mutex g_mu;
 
@@ -128,7 +135,7 @@ lce_status_t device_info(DevInfo **out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) {
-        t_last_cuda = e;
+        note_error(e);
         return LCE_ERR_CUDA;
     }
     if (dev < 0 || dev >= kMaxDevices) return LCE_ERR_DEVICE;
@@ -138,7 +145,7 @@ lce_status_t device_info(DevInfo **out) {
         cudaDeviceProp p;
         e = cudaGetDeviceProperties(&p, dev);
         if (e != cudaSuccess) {
-            t_last_cuda = e;
+            note_error(e);
             return LCE_ERR_CUDA;
         }
         di.sms = p.multiProcessorCount;
@@ -150,13 +157,13 @@ lce_status_t device_info(DevInfo **out) {
         for (const void *f : gemms) {
             e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
             if (e != cudaSuccess) {
-                t_last_cuda = e;
+                note_error(e);
                 return LCE_ERR_CUDA;
             }
         }
         e = cudaGetSymbolAddress(reinterpret_cast<void **>(&di.status), g_status);
         if (e != cudaSuccess) {
-            t_last_cuda = e;
+            note_error(e);
             return LCE_ERR_CUDA;
         }
         if (!g_encode) {
@@ -164,7 +171,7 @@ lce_status_t device_info(DevInfo **out) {
             cudaDriverEntryPointQueryResult q;
             e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
             if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn) {
-                t_last_cuda = e != cudaSuccess ? e : cudaErrorNotSupported;
+                note_error(e != cudaSuccess ? e : cudaErrorNotSupported);
                 return LCE_ERR_CUDA;
             }
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
@@ -380,7 +387,7 @@ struct WsGuard {
         count_launch();                        \
         cudaError_t e_ = cudaGetLastError();   \
         if (e_ != cudaSuccess) {               \
-            t_last_cuda = e_;                  \
+            note_error(e_);                    \
             return LCE_ERR_CUDA;               \
         }                                      \
     } while (0)
@@ -643,7 +650,7 @@ lce_status_t run_rows(const lce_args_t *a, const DevInfo &di, uint8_t *base, con
                 cfg.numAttrs = 1;
                 cudaError_t e = cudaLaunchKernelEx(&cfg, bwd_kernel, mp, g);
                 if (e != cudaSuccess) {
-                    t_last_cuda = e;
+                    note_error(e);
                     return LCE_ERR_CUDA;
                 }
             }
@@ -677,7 +684,7 @@ lce_status_t run_typed(const lce_args_t *a, const DevInfo &di) {
     } else {
         cudaError_t e = cudaMallocAsync(&ws.p, L.total, st);
         if (e != cudaSuccess) {
-            t_last_cuda = e;
+            note_error(e);
             return LCE_ERR_CUDA;
         }
         ws.owned = true;
@@ -742,7 +749,7 @@ lce_status_t noalloc_scratch(void **out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) {
-        t_last_cuda = e;
+        note_error(e);
         return LCE_ERR_CUDA;
     }
     if (dev < 0 || dev >= kMaxDevices) return LCE_ERR_DEVICE;
@@ -751,7 +758,7 @@ lce_status_t noalloc_scratch(void **out) {
         void *p = nullptr;
         e = cudaGetSymbolAddress(&p, g_noalloc_scratch);
         if (e != cudaSuccess || !p) {
-            t_last_cuda = e != cudaSuccess ? e : cudaErrorInvalidSymbol;
+            note_error(e != cudaSuccess ? e : cudaErrorInvalidSymbol);
             return LCE_ERR_CUDA;
         }
         g_noalloc_ptr[dev] = p;
@@ -777,7 +784,7 @@ lce_status_t host_device(HostDev *out) {
 
 lce_status_t host_cuda(cudaError_t e) {
     if (e == cudaSuccess) return LCE_OK;
-    t_last_cuda = e;
+    note_error(e);
     return LCE_ERR_CUDA;
 }
 
@@ -957,7 +964,7 @@ lce_status_t emb_backward(lce_dtype_t dtype, const void *dE, const int64_t *toke
     } else {
         cudaError_t e = cudaMallocAsync(&ws.p, L.total, st);
         if (e != cudaSuccess) {
-            t_last_cuda = e;
+            note_error(e);
             return LCE_ERR_CUDA;
         }
         ws.owned = true;
@@ -1066,19 +1073,19 @@ lce_status_t lce_get_device_status(lce_stream_t stream, int32_t *bits) {
     if (!bits) return LCE_ERR_NULL;
     cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) {
-        t_last_cuda = e;
+        note_error(e);
         return LCE_ERR_CUDA;
     }
     int v = 0;
     e = cudaMemcpyFromSymbol(&v, g_status, sizeof(int));
     if (e != cudaSuccess) {
-        t_last_cuda = e;
+        note_error(e);
         return LCE_ERR_CUDA;
     }
     const int zero = 0;
     e = cudaMemcpyToSymbol(g_status, &zero, sizeof(int));
     if (e != cudaSuccess) {
-        t_last_cuda = e;
+        note_error(e);
         return LCE_ERR_CUDA;
     }
     *bits = v;
@@ -1131,7 +1138,7 @@ lce_status_t lce_profile_end(double *ms, int64_t *launches, int n) {
         cudaError_t e = cudaEventSynchronize(r.b);
         if (e == cudaSuccess) e = cudaEventElapsedTime(&t, r.a, r.b);
         if (e != cudaSuccess) {
-            t_last_cuda = e;
+            note_error(e);
             st = LCE_ERR_CUDA;
         } else if (r.phase < n) {
             if (ms) ms[r.phase] += t;
@@ -1163,7 +1170,7 @@ lce_status_t lce_forward_noalloc(const void *H, const void *W, const int64_t *ta
     cudaError_t e = cudaMemsetAsync(static_cast<uint8_t *>(scratch) + L.counters, 0, 64,
                                     reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) {
-        t_last_cuda = e;
+        note_error(e);
         return LCE_ERR_CUDA;
     }
     lce_args_t a{};

@@ -23,7 +23,7 @@ struct HostDev {
 // The current device, checked to be sm_103.
 lce_status_t host_device(HostDev *out);
 
-// Records a CUDA error for lce_last_cuda_error(); LCE_OK on cudaSuccess.
+// Records a CUDA error for lce_last_cuda_error(), and clears it in the runtime; LCE_OK on cudaSuccess.
 lce_status_t host_cuda(cudaError_t e);
 
 // Counts a launch for lce_launch_count() and returns its error, if any.
