@@ -305,11 +305,14 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormArgs a) {
 // What bounds them is HBM, once the work between two rows hides behind it. That
 // work is mostly issue slots: hence the packed fp32 arithmetic, 16 to 32
 // elements a thread against the fixed cost of a sum, and no branches on the
-// options inside a row. The forward's inputs and outputs ask to leave L2 first
-// (16384 rows of 4096 bf16 from HBM: 89 us, 95 without; the backward gains
-// nothing from that). At that size, with norms on both sides and a gate per
-// channel: forward 89 us (6.0 TB/s), 125 with a block for each row; backward
-// 138 us with the 4 us of k_norm_cols (5.8 TB/s).
+// options inside a row. The forward's inputs and r ask to leave L2 first (16384
+// rows of 4096 bf16, calls in a row on inputs from HBM: 90 us, 95 without; the
+// backward gains nothing from that); n does not, since the block's first product
+// reads it next (8192 rows of 2048, norm, product, norm: 80.5 us, 84.8 with n
+// marked too, 83.5 with nothing marked). At 16384 x 4096, with norms on both
+// sides and a gate per channel: forward 90 us (6.0 TB/s; 94.5 among other calls),
+// 125 with a block for each row; backward 139 us with the 4 us of k_norm_cols
+// (5.8 TB/s).
 enum NormMode : int { NORM_ANY, NORM_ALL, NORM_FULL_GATE, NORM_NO_DR, NORM_PRE, NORM_POST };
 
 struct RingGeo {
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_fwd_ring(const NormArg
                 Pack16<T>::get(*reinterpret_cast<const uint4 *>(w_pre + byte), w);
 #pragma unroll
                 for (int i = 0; i < P; ++i) w[i] = mul2(mul2(r[c][i], f), w[i]);
-                if (live) __stcs(reinterpret_cast<uint4 *>(out_n + c * g.tpr * 16), Pack16<T>::set(w));
+                if (live) *reinterpret_cast<uint4 *>(out_n + c * g.tpr * 16) = Pack16<T>::set(w);
             }
         }
         if (++s == g.stages) s = 0, phase ^= 1;
