@@ -153,3 +153,9 @@ def test_many_rows_alone_and_in_place(dtype, d, N):
 @pytest.mark.parametrize("post,gate,pre,no_dr", [(True, "channel", True, False), (True, "full", True, True), (False, "none", True, False)])
 def test_wide_rows(dtype, d, N, post, gate, pre, no_dr):
     check(N, d, dtype, post, gate, pre, no_dr=no_dr)
+
+
+@pytest.mark.parametrize("dtype,d,N", [("bf16", 8, 400_009), ("bf16", 24, 150_001), ("fp32", 8, 200_003), ("fp32", 40, 40_009)], ids=lambda v: str(v))
+@pytest.mark.parametrize("gate", ["channel", "full"])
+def test_narrow_rows(dtype, d, N, gate):
+    check(N, d, dtype, True, gate, True)
