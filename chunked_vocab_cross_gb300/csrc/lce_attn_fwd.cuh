@@ -19,7 +19,7 @@
 // where they come in pairs, else two tiles of rows. Per tile and key tile that
 // is 1024 cycles of each instead of 1280 (with a CTA for each, two on an SM).
 // One side's softmax runs beside the other's MMAs. Measured with 32 query and 8
-// key heads of 128 channels, causal: one sequence of 8192 tokens 306 us (1.8
+// key heads of 128 channels, causal: one sequence of 8192 tokens 309 us (1.8
 // PFLOP/s of the products that the mask leaves), eleven of 750 on average 72
 // (850 TFLOP/s; with a CTA for each tile 83). There the tile that the mask cuts
 // and the start and output of each piece count for most. Pairs of heads, not

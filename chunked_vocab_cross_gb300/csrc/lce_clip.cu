@@ -25,8 +25,8 @@ constexpr int kMaxBlocks = 256 * kSqBlocksPerSm;
 // Up to 1 MB (each tensor counted in whole 4 KB) one cluster of eight blocks
 // does both passes in one launch: a warp has one chunk of 4 KB and keeps it in
 // registers, and the blocks' sums are joined through distributed shared memory.
-// What bounds it is latency (0.1 MB in 20 tensors: 4.8 us, 6.6 with the two
-// launches; 0.84 MB in 29: 7.3 us, 8.0; and one launch less for the host).
+// What bounds it is latency (0.1 MB in 20 tensors: 4.3 us, 5.7 with the two
+// launches; 0.84 MB in 28: 6.5 us, 7.9; and one launch less for the host).
 constexpr int kCluster = 8, kClusterThreads = 1024;
 constexpr int kClusterChunks = kCluster * kClusterThreads / 32;
 constexpr int kSmallChunkBytes = 4096;

@@ -99,7 +99,7 @@ __device__ __forceinline__ void block_sum(float (&v)[K], float *red, int &flip) 
 
 // Few rows: one block a row, a thread holds CH packs of its row's elements.
 // What bounds it is latency: a launch, the loads, two sums over the block
-// (one row of 4096 bf16: 3.1 us, 305 rows 4.2 us).
+// (one row of 4096 bf16: 2.7 us, 305 rows 4.4 us).
 template <typename T, int CH>
 __global__ void __launch_bounds__(512) k_norm_fwd(const NormArgs a) {
     __shared__ float red[64];
@@ -934,11 +934,11 @@ int row_packs(int d) { return (d / kVec + 511) / 512; }
 
 constexpr int kRingBytes = 208 * 1024;   // dynamic shared memory of a ring kernel's block at most
 // Ring of the forward, if two stages do not take more: 128 KB are enough in flight, and less in turns is easier on
-// HBM (131072 rows of 512 bf16: 93 us, 94 with all of kRingBytes; 32768 rows of 2048: 88 us, 93).
+// HBM (131072 rows of 512 bf16: 92 us, 95 with all of kRingBytes; 32768 rows of 2048: 89 us, 92).
 constexpr int kFwdRingBytes = 128 * 1024;
 // Few rows have nothing to run ahead of: up to this much of an array the forward takes a block for each row, with
-// fewer steps before its first load (rows of 4096 bf16: 305 in 4.2 us, 5.2 through the ring; 608 in 6.2 us, 5.4;
-// of 1024: 1216 in 3.6 us, 4.8; 4096 in 7.6 us, 7.0).
+// fewer steps before its first load (rows of 4096 bf16: 305 in 4.4 us, 5.6 through the ring; 608 in 7.6 us, 6.4;
+// of 1024: 1216 in 4.5 us, 5.5; 4096 in 9.3 us, 8.6).
 constexpr int64_t kDirectBytes = 4 << 20;
 constexpr int kColGroups = 304;          // blocks of the backward at most (bounds its workspace)
 
@@ -959,7 +959,7 @@ bool ring_geo(RingGeo *g, int d, int elt, int arrays, int ch, int per, int bytes
 }
 
 // Packs a thread in the forward: as few as leave a row to 32 threads, at most
-// 32 elements (16384 rows of 4096 bf16: 95 us with four packs, 137 with one).
+// 32 elements (16384 rows of 4096 bf16: 90 us with four packs, 137 with one).
 int ring_packs(int d, int elt, int most) {
     int ch = 1;
     while (ch < most && d * elt / 16 > 32 * ch) ch *= 2;

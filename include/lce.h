@@ -368,13 +368,14 @@ lce_status_t lce_embedding_backward_bf16(lce_dtype_t dtype, const void *dE, cons
  *
  * dtype LCE_BF16 runs on the bf16 tensor cores with fp32 accumulation (the
  * probabilities and their gradient are rounded to bf16 once, as operands; to
- * two bf16 parts where Tq*Hq*D <= 2^18 and sequences average at most 512);
- * LCE_FP32 runs in fp32 arithmetic throughout. Requirements: 1 <= D <= 128,
- * D % 8 == 0, Hq a multiple of Hk, 0 <= Tq, Tk < 2^30, 1 <= B < 2^30, Tq and Tk multiples
- * of B without offsets; bases 16-byte aligned, strides multiples of 16 bytes,
- * positive (but for a single head or token). The rows of an output must be apart
- * from one another (checked), and outputs apart from each other and from every
- * input (not checked).
+ * two bf16 parts where Tq*Hq*D <= 2^18 and sequences average at most 512, so a
+ * sequence's last bits depend on what it is packed with; probabilities below
+ * 2^-126 count as zero); LCE_FP32 runs in fp32 arithmetic throughout.
+ * Requirements: 1 <= D <= 128, D % 8 == 0, Hq a multiple of Hk, 0 <= Tq, Tk <
+ * 2^30, 1 <= B < 2^30, Tq and Tk multiples of B without offsets; bases 16-byte
+ * aligned, strides multiples of 16 bytes, positive (but for a single head or
+ * token). The rows of an output must be apart from one another (checked), and
+ * outputs apart from each other and from every input (not checked).
  * Results are deterministic. Scratch: lce_attention_forward_workspace_size bytes
  * (0 but for few rows over long keys, whose keys are taken in ranges) or
  * lce_attention_workspace_size bytes (backward), device, 16-byte aligned, or
@@ -414,17 +415,19 @@ size_t lce_attention_forward_workspace_size(const lce_attn_t *args);
  *   n = r / rms(r) * w_pre      (the next block's input; absent without w_pre)
  * The forward writes r, n and the fp32 rows rstd_post = 1/rms(b) and
  * rstd_pre = 1/rms(r); r may be x (updated in place). Without b, r is x itself
- * and only n and rstd_pre are written (r NULL). The backward takes r, b and
- * the stored rstd, the gradients dr (of r, or NULL for zero) and dn (of n),
- * and writes
+ * and only n and rstd_pre are written (r NULL). n and rstd_pre are formed from r
+ * before r is rounded to its type. The backward takes r as it was rounded, b and
+ * the stored rstd, the gradients dr (of r, or NULL for zero) and dn (of n), and
+ * writes
  *   dx = dr + rstd_pre * (u - rhat * mean(u * rhat)),   u = w_pre * dn,
  *   dy = scale * gate * dx,  dgate = scale * dx * y (summed over rows for [d]),
  *   db = rstd_post * (t - bhat * mean(t * bhat)),       t = w_post * dy,
  *   dw_post = sum over rows of dy * bhat,  dw_pre = sum of dn * rhat,
  * each rounded once to its own type. All tensors are of `dtype` (statistics
- * fp32), rows of d contiguous elements, ld_* apart (0 = d); outputs are
- * contiguous. d % 8 == 0, 8 <= d <= 16384, 0 <= N < 2^31, bases and row
- * strides 16-byte aligned. Sums are fp32 in a fixed order (deterministic).
+ * fp32), rows of d contiguous elements, ld_* apart (0 stands for d: rows that
+ * all lie in one place have to be copied first); outputs are contiguous.
+ * d % 8 == 0, 8 <= d <= 16384, 0 <= N < 2^31, bases and row strides 16-byte
+ * aligned. Sums are fp32 in a fixed order (deterministic).
  * Scratch (backward): lce_block_norm_workspace_size bytes or NULL.
  */
 typedef struct {
