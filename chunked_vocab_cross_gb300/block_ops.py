@@ -55,7 +55,7 @@ def _scratch(given, need: int, device):
 
 
 # Autograd learns of tensors that a caller gives to be written: one that it keeps for a backward pass is then an error
-# there. (0.3 us for one tensor, 1.7 for 29.)
+# there. (0.2 us for one tensor, 0.9 for 28; clipping 28 gradients that were just made takes 3 us longer, 38 instead of 35.)
 _written = torch.autograd.graph.increment_version
 
 
