@@ -63,6 +63,15 @@ SIGNATURES = {
     "lce_grad_norm": (c_int, [c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "lce_clip_grads": (c_int, [c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_float, c_float, c_void_p, c_void_p,
                                c_void_p, c_size_t, c_void_p]),
+    "lce_layer_norm_forward": (c_int, [c_void_p]),
+    "lce_layer_norm_backward": (c_int, [c_void_p]),
+    "lce_layer_norm_workspace_size": (c_size_t, [c_void_p]),
+    "lce_pack8": (c_int, [c_int, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
+    "lce_unpack8": (c_int, [c_int, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64, c_void_p]),
+    "lce_packed_wgrad": (c_int, [c_void_p]),
+    "lce_packed_wgrad_workspace_size": (c_size_t, [c_void_p]),
+    "lce_recurrence_forward": (c_int, [c_void_p]),
+    "lce_recurrence_backward": (c_int, [c_void_p]),
 }
 
 
@@ -128,6 +137,40 @@ class LceNorm(ctypes.Structure):
         ("dr", c_void_p), ("dn", c_void_p), ("ld_r", c_int64), ("ld_dr", c_int64), ("ld_dn", c_int64),
         ("dx", c_void_p), ("db", c_void_p), ("dw_post", c_void_p), ("dgate", c_void_p), ("dw_pre", c_void_p),
         ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("stream", c_void_p),
+    ]
+
+
+class LceLayerNorm(ctypes.Structure):
+    """Mirror of lce_layer_norm_t."""
+    _fields_ = [
+        ("dtype", c_int), ("N", c_int64), ("d", c_int64), ("eps", c_float),
+        ("x", c_void_p), ("b", c_void_p), ("weight", c_void_p), ("bias", c_void_p), ("ld_x", c_int64), ("ld_b", c_int64),
+        ("r", c_void_p), ("n", c_void_p), ("mean", c_void_p), ("rstd", c_void_p),
+        ("codes", c_void_p), ("exps", c_void_p), ("ld_codes", c_int64), ("ld_exps", c_int64),
+        ("dr", c_void_p), ("dn", c_void_p), ("ld_r", c_int64), ("ld_dr", c_int64), ("ld_dn", c_int64),
+        ("dx", c_void_p), ("dweight", c_void_p), ("dbias", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("stream", c_void_p),
+    ]
+
+
+class LceWgrad(ctypes.Structure):
+    """Mirror of lce_wgrad_t."""
+    _fields_ = [
+        ("dtype", c_int), ("dw_dtype", c_int), ("T", c_int64), ("n", c_int64), ("k", c_int64),
+        ("dy", c_void_p), ("ld_dy", c_int64), ("codes", c_void_p), ("exps", c_void_p), ("ld_codes", c_int64),
+        ("ld_exps", c_int64), ("dw", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("stream", c_void_p),
+    ]
+
+
+class LceRecurrence(ctypes.Structure):
+    """Mirror of lce_recurrence_t."""
+    _fields_ = [
+        ("dtype", c_int), ("B", c_int64), ("T", c_int64), ("d", c_int64), ("cu", c_void_p),
+        ("x", c_void_p), ("g", c_void_p), ("ld_x", c_int64), ("ld_g", c_int64), ("state", c_void_p), ("kept", c_void_p),
+        ("h", c_void_p), ("ld_h", c_int64), ("final", c_void_p),
+        ("dh", c_void_p), ("ld_dh", c_int64), ("dfinal", c_void_p), ("dx", c_void_p), ("dg", c_void_p),
+        ("ld_dx", c_int64), ("ld_dg", c_int64), ("dstate", c_void_p), ("stream", c_void_p),
     ]
 
 

@@ -1,6 +1,6 @@
 """Compile liblce.so (the CUDA library behind include/lce.h) in-tree for sm_103a.
 
-Four translation units compiled in parallel by one nvcc call, one -gencode, no
+Seven translation units compiled in parallel by one nvcc call, one -gencode, no
 cmake: nvcc cross-compiles them on a machine without a GPU as well.
 """
 from __future__ import annotations
@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblce.so")
-SOURCES = ["lce_api.cu", "lce_attn.cu", "lce_norm.cu", "lce_clip.cu"]
+SOURCES = ["lce_api.cu", "lce_attn.cu", "lce_norm.cu", "lce_clip.cu", "lce_layer_norm.cu", "lce_pack.cu", "lce_scan.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -96,4 +96,11 @@ lce_status_t host_launch_early(void (*kernel)(P...), dim3 grid, int threads, int
 
 inline bool host_misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
+// The layout of N rows of d channels in 8 bits, where there are rows.
+inline lce_status_t host_check_packed(const void *codes, int64_t ld_codes, const void *exps, int64_t ld_exps, int64_t N, int64_t d) {
+    if (!codes || !exps) return LCE_ERR_NULL;
+    if (ld_codes < d || ld_exps < N || ld_codes >= (int64_t(1) << 36) || ld_exps >= (int64_t(1) << 36)) return LCE_ERR_SHAPE;
+    return host_misaligned(codes) || host_misaligned(exps) || ld_codes % 16 || ld_exps % 16 ? LCE_ERR_ALIGN : LCE_OK;
+}
+
 }  // namespace lce

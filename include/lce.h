@@ -476,6 +476,157 @@ lce_status_t lce_clip_grads(int64_t count, const void *const *grads, void *const
                             const int32_t *dtypes, float max_norm, float eps, float *norm, float *factor,
                             void *workspace, size_t workspace_bytes, lce_stream_t stream);
 
+/*
+ * Layer norm with the residual sum before it: for the stream x and a block's
+ * output b (or none), row by row over d channels,
+ *   r = x + b   (rounded to its type; x itself without b),
+ *   mean = sum r / d,   rstd = 1 / sqrt(sum (r - mean)^2 / d + eps),
+ *   n = (r - mean) * rstd * weight + bias   (bias may be NULL).
+ * n and the statistics are those of r as it is stored; the sum of squares is
+ * taken after the mean is known. The forward writes r (with b; it may be x or
+ * b), n, mean and rstd (fp32 [N]) and, where `codes` is given, r packed to 8
+ * bits (lce_pack8 below, in the same pass). The backward takes r, or its 8-bit
+ * form where `codes` is given (r is then not read), the gradients dr (of r, or
+ * NULL for zero) and dn (of n), and writes
+ *   dx = dr + rstd * (u - mean(u) - rhat * mean(u * rhat)),  u = weight * dn,
+ *   rhat = (r - mean) * rstd   (the gradient of x and of b alike),
+ *   dweight = sum over rows of dn * rhat,  dbias = sum of dn (NULL: not wanted),
+ * each rounded once to its own type. All tensors are of `dtype`, rows of d
+ * contiguous elements, ld_* apart (0 stands for d); outputs are contiguous.
+ * d % 8 == 0, 8 <= d <= 16384, 0 <= N < 2^31, bases and row strides 16-byte
+ * aligned. Sums are fp32 in a fixed order (deterministic).
+ * Scratch (backward): lce_layer_norm_workspace_size bytes or NULL.
+ */
+typedef struct {
+    lce_dtype_t dtype;
+    int64_t N, d;
+    float eps;
+    const void *x, *b;               /* forward only */
+    const void *weight, *bias;       /* [d] */
+    int64_t ld_x, ld_b;
+    void *r, *n;                     /* r: written by the forward (with b), read by the backward */
+    float *mean, *rstd;              /* [N]: written by the forward, read by the backward */
+    uint8_t *codes;                  /* r in 8 bits, or NULL: written by the forward, read by the backward */
+    int8_t *exps;
+    int64_t ld_codes, ld_exps;
+    const void *dr, *dn;             /* backward only, as are the rest */
+    int64_t ld_r, ld_dr, ld_dn;
+    void *dx, *dweight, *dbias;
+    void *workspace;
+    size_t workspace_bytes;
+    lce_stream_t stream;
+} lce_layer_norm_t;
+lce_status_t lce_layer_norm_forward(const lce_layer_norm_t *args);
+lce_status_t lce_layer_norm_backward(const lce_layer_norm_t *args);
+size_t lce_layer_norm_workspace_size(const lce_layer_norm_t *args);
+
+/*
+ * Activations in 8 bits, for what a backward pass needs of them. A row's
+ * channels are taken in blocks of 128 (the last may be shorter); a block has
+ * one exponent e and a code for each value x:
+ *   e    = the least integer in [-100, 119] with max |x| <= 448 * 2^e,
+ *   code = x * 2^-e rounded to the nearest e4m3 value (ties to even, at most
+ *          448 in magnitude), standing for code * 2^e.
+ * A value is off by at most 2^-4 of itself, or 2^-10 * 2^e where that is more.
+ * The scale is a power of two so that what a code stands for is exact in bf16
+ * (and in fp32): the products that read codes round nothing further. A block
+ * with an infinity or NaN in it gets e = -128 and stands for NaNs throughout.
+ * Magnitudes beyond 448 * 2^119 = 2.98e38 come back as that.
+ * codes: [N] rows of d bytes, ld_codes apart (a multiple of 16, at least d);
+ * exps: int8 [ceil(d/128)][N], rows ld_exps apart (a multiple of 16, at least
+ * N). x and out are of `dtype`, rows ld_x and ld_out elements apart (0 stands
+ * for d). d % 8 == 0, 8 <= d < 2^24, 0 <= N < 2^31, bases 16-byte aligned, row strides
+ * multiples of 16 bytes.
+ */
+lce_status_t lce_pack8(lce_dtype_t dtype, const void *x, int64_t ld_x, int64_t N, int64_t d, uint8_t *codes,
+                       int64_t ld_codes, int8_t *exps, int64_t ld_exps, lce_stream_t stream);
+lce_status_t lce_unpack8(lce_dtype_t dtype, const uint8_t *codes, int64_t ld_codes, const int8_t *exps,
+                         int64_t ld_exps, int64_t N, int64_t d, void *out, int64_t ld_out, lce_stream_t stream);
+
+/*
+ * The gradient of a linear layer's weight [n][k] from the gradient dy [T][n] of
+ * its output and its input packed to 8 bits (T rows of k channels):
+ *   dw[i][j] = sum over t of dy[t][i] * x[t][j],
+ * x being what the codes stand for. dy is of `dtype`, dw of `dw_dtype` (fp32,
+ * or bf16 with a bf16 dy), contiguous, rounded once from fp32 sums. bf16 dy
+ * runs on the bf16 tensor cores with the codes widened on the way to them; an
+ * fp32 dy is taken as three bf16 parts, which hold it exactly (but for parts
+ * below 1.2e-38, that is values below 2^-109). Sums are
+ * in a fixed order (deterministic). n % 8 == 0, k % 8 == 0, n and k >= 8 and
+ * < 2^24, 0 <= T < 2^30, bases and row strides of dy 16-byte aligned (ld_dy 0
+ * stands for n). T = 0 writes zeros.
+ * Scratch: lce_packed_wgrad_workspace_size bytes or NULL.
+ */
+typedef struct {
+    lce_dtype_t dtype, dw_dtype;
+    int64_t T, n, k;
+    const void *dy;
+    int64_t ld_dy;
+    const uint8_t *codes;
+    const int8_t *exps;
+    int64_t ld_codes, ld_exps;
+    void *dw;
+    void *workspace;
+    size_t workspace_bytes;
+    lce_stream_t stream;
+} lce_wgrad_t;
+lce_status_t lce_packed_wgrad(const lce_wgrad_t *args);
+size_t lce_packed_wgrad_workspace_size(const lce_wgrad_t *args);
+
+/*
+ * Gated recurrence over packed sequences, channel by channel, and its backward
+ * pass: a token mixer whose memory is one state a sequence. With the gate's
+ * logit g,
+ *   a_t = 1 / (1 + exp(-g_t)),   h_t = a_t * h_{t-1} + (1 - a_t) * x_t,
+ * h before a sequence's first token being its `state` (fp32 [B][d], NULL for
+ * zeros) and `final` (fp32 [B][d], may be NULL, may be `state`) receiving h
+ * after its last (the state itself for an empty sequence). Logits, not gates,
+ * are the input, since gates near 1 have no neighbours in bf16 that would tell
+ * a memory of 1000 tokens from an endless one. From the gradients dh of h and
+ * dfinal of `final` (NULL for zeros) the backward goes through the tokens from
+ * the last, with m after a sequence's last token being its dfinal:
+ *   l_t = dh_t + m_{t+1},   m_t = a_t * l_t,
+ *   dx_t = (1 - a_t) * l_t,   dg_t = l_t * (h_{t-1} - x_t) * a_t * (1 - a_t),
+ *   dstate = m of the first token (dfinal itself for an empty sequence).
+ * h is not read: the forward may leave `kept`, the fp32 state after every 128
+ * tokens (fp32 [ceil(T/128)][d]; row c is h of token 128 c - 1, zeros for c =
+ * 0), from which the backward forms h again.
+ *
+ * x and g are of `dtype`, T rows of d contiguous elements, ld_* apart, so they
+ * may be slices of one projection's output, and dx and dg slices of its
+ * gradient. cu: B+1 ascending token offsets (device int32, cu[0] = 0, cu[B] <=
+ * T), NULL for B sequences of equal length; tokens after cu[B] belong to no
+ * sequence (h = 0, zero gradients, kept = 0 behind them). Sequences may be empty. Values of one
+ * sequence, infinities and NaN among them, never reach another. States and all
+ * arithmetic are fp32; h, dx and dg are rounded once. Logits below -87 count as
+ * -87. d % 8 == 0, 8 <= d < 2^24, 0 <= T < 2^30, 1 <= B < 2^30, T a multiple
+ * of B without offsets; bases 16-byte aligned, strides multiples of 16 bytes,
+ * at least d (0 stands for d). Outputs must not overlap one another or, but for
+ * `final`, any input. Deterministic. Offsets that are not ascending within the
+ * tokens set LCE_DEV_SEQLENS; the outputs are then unspecified.
+ */
+typedef struct {
+    lce_dtype_t dtype;
+    int64_t B, T, d;
+    const int32_t *cu;               /* [B+1] device, or NULL */
+    const void *x, *g;
+    int64_t ld_x, ld_g;
+    const float *state;              /* [B][d], or NULL */
+    float *kept;                     /* written by the forward (may be NULL), read by the backward */
+    void *h;                         /* forward only, as is final */
+    int64_t ld_h;
+    float *final;
+    const void *dh;                  /* backward only, as are the rest */
+    int64_t ld_dh;
+    const float *dfinal;             /* [B][d], or NULL */
+    void *dx, *dg;
+    int64_t ld_dx, ld_dg;
+    float *dstate;                   /* [B][d], may be NULL */
+    lce_stream_t stream;
+} lce_recurrence_t;
+lce_status_t lce_recurrence_forward(const lce_recurrence_t *args);
+lce_status_t lce_recurrence_backward(const lce_recurrence_t *args);
+
 /* ABI version: major*10000 + minor*100 + patch. */
 int lce_version(void);
 
