@@ -3,10 +3,11 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "lce_host.h"
-#include "tc_ptx.cuh"
+#include "row_ring.cuh"
 
 using namespace lce;
 
@@ -27,81 +28,469 @@ struct ScanArgs {
     __device__ __forceinline__ int start(int b) const { return cu ? min(max(cu[b], 0), T) : b * len; }
 };
 
-// The gate and its complement, each to its own relative precision. The exponent
-// is bounded so that neither the sum nor its reciprocal leaves fp32.
-__device__ __forceinline__ void gate(float g, float &a, float &rest) {
-    const float z = -g * 1.4426950408889634f;
-    const float e = exp2f(z > 126.f ? 126.f : z);   // (a NaN stays one)
-    a = 1.f / (1.f + e);
-    rest = e * a;
-}
-
-__device__ __forceinline__ void check_offsets(const ScanArgs &a) {
-    if (!a.cu || blockIdx.x || threadIdx.x >= 32) return;
-    bool bad = false;
-    for (int b = threadIdx.x; b <= a.B; b += 32) bad |= b == 0 ? a.cu[0] != 0 : a.cu[b] < a.cu[b - 1] || a.cu[b] > a.T;
-    if (__any_sync(0xffffffffu, bad) && threadIdx.x == 0) atomicOr(a.status, LCE_DEV_SEQLENS);
-}
-
-// A thread a channel of a sequence
+// The state of a channel pair (bf16) or a channel (fp32), the 4 bytes of a row
+// that a thread takes.
 template <typename T>
-__global__ void __launch_bounds__(128) k_scan_fwd_simple(const ScanArgs a, int slices) {
-    check_offsets(a);
-    const int b = blockIdx.x / slices, ch = (blockIdx.x - b * slices) * 128 + threadIdx.x;
-    if (ch >= a.d) return;
-    const int64_t at = static_cast<int64_t>(b) * a.d + ch;
-    const bool tail = b == a.B;
-    float h = tail || !a.state ? 0.f : a.state[at];
-    const int end = tail ? a.T : max(a.start(b + 1), a.start(b));
-    if (tail && a.kept) a.kept[ch] = 0.f;
-    for (int t = a.start(b); t < end; ++t) {
-        if (!tail) {
-            float f, rest;
-            gate(static_cast<float>(static_cast<const T *>(a.g)[t * a.ld_g + ch]), f, rest);
-            h = fmaf(f, h, rest * static_cast<float>(static_cast<const T *>(a.x)[t * a.ld_x + ch]));
-        }
-        static_cast<T *>(a.h)[t * a.ld_h + ch] = static_cast<T>(h);
-        if (a.kept && (t + 1) % kEvery == 0 && t + 1 < a.T) a.kept[static_cast<int64_t>((t + 1) / kEvery) * a.d + ch] = h;
+struct Lane;
+template <>
+struct Lane<__nv_bfloat16> {
+    using F = f32x2;
+    static constexpr int kCh = 2;
+    static __device__ __forceinline__ F get(uint32_t w) { return pack2u(w << 16, w & 0xffff0000u); }
+    static __device__ __forceinline__ uint32_t put(F v) {
+        float a, b;
+        unpack2(v, a, b);
+        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&p);
     }
-    if (!tail && a.final) a.final[at] = h;
+    static __device__ __forceinline__ F all(float v) { return both(v); }
+    static __device__ __forceinline__ F fma(F a, F b, F c) { return fma2(a, b, c); }
+    static __device__ __forceinline__ F mul(F a, F b) { return mul2(a, b); }
+    static __device__ __forceinline__ F add(F a, F b) { return add2(a, b); }
+    static __device__ __forceinline__ float first(F v) {
+        float a, b;
+        unpack2(v, a, b);
+        return a;
+    }
+    template <typename G>
+    static __device__ __forceinline__ F each(F v, G g) {
+        float a, b;
+        unpack2(v, a, b);
+        return pack2(g(a), g(b));
+    }
+    static __device__ __forceinline__ F load(const float *p) { return *reinterpret_cast<const F *>(p); }
+    static __device__ __forceinline__ void save(float *p, F v) { *reinterpret_cast<F *>(p) = v; }
+};
+template <>
+struct Lane<float> {
+    using F = float;
+    static constexpr int kCh = 1;
+    static __device__ __forceinline__ F get(uint32_t w) { return __uint_as_float(w); }
+    static __device__ __forceinline__ uint32_t put(F v) { return __float_as_uint(v); }
+    static __device__ __forceinline__ F all(float v) { return v; }
+    static __device__ __forceinline__ F fma(F a, F b, F c) { return fmaf(a, b, c); }
+    static __device__ __forceinline__ F mul(F a, F b) { return a * b; }
+    static __device__ __forceinline__ F add(F a, F b) { return a + b; }
+    static __device__ __forceinline__ float first(F v) { return v; }
+    template <typename G>
+    static __device__ __forceinline__ F each(F v, G g) { return g(v); }
+    static __device__ __forceinline__ F load(const float *p) { return *p; }
+    static __device__ __forceinline__ void save(float *p, F v) { *p = v; }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) k_scan_bwd_simple(const ScanArgs a, int slices) {
-    check_offsets(a);
-    const int b = blockIdx.x / slices, ch = (blockIdx.x - b * slices) * 128 + threadIdx.x;
-    if (ch >= a.d) return;
-    const int64_t at = static_cast<int64_t>(b) * a.d + ch;
-    const bool tail = b == a.B;
-    const int begin = a.start(b), end = tail ? a.T : max(a.start(b + 1), begin);
-    if (tail) {
-        for (int t = begin; t < end; ++t)
-            static_cast<T *>(a.dx)[t * a.ld_dx + ch] = static_cast<T *>(a.dg)[t * a.ld_dg + ch] = static_cast<T>(0.f);
+// exp(-g), bounded so that neither 1 + it nor its reciprocal leaves fp32 (a NaN stays one)
+template <typename L>
+__device__ __forceinline__ typename L::F gate_exp(typename L::F g) {
+    return L::each(L::mul(g, L::all(-1.4426950408889634f)), [](float z) { return ex2(z > 126.f ? 126.f : z); });
+}
+// The gate and its complement, each to its own relative precision
+template <typename L>
+__device__ __forceinline__ void gate(typename L::F g, typename L::F &a, typename L::F &rest) {
+    const typename L::F e = gate_exp<L>(g);
+    a = L::each(L::add(e, L::all(1.f)), rcp);
+    rest = L::mul(e, a);
+}
+
+// What a run of tokens does to the state before it: s -> A s + H, or, where a
+// sequence begins among them, just H: A is kReset then, which no product of
+// gates is, so that nothing of the state before gets through, NaN or infinite.
+constexpr float kReset = -1.f;
+template <typename L>
+struct Step {
+    typename L::F A, H;
+};
+template <typename L>
+__device__ __forceinline__ typename L::F apply(const Step<L> &s, typename L::F before) {
+    return L::first(s.A) < 0.f ? s.H : L::fma(s.A, before, s.H);
+}
+template <typename L>
+__device__ __forceinline__ Step<L> then(const Step<L> &a, const Step<L> &b) {   // a, then b
+    Step<L> r;
+    r.H = apply(b, a.H);
+    r.A = L::first(b.A) < 0.f || L::first(a.A) < 0.f ? L::all(kReset) : L::mul(a.A, b.A);
+    return r;
+}
+
+// Work is split over channels and over time. A slice is the channels of 128
+// bytes of a row; a cluster of CTAs takes a slice through the tokens, each CTA a
+// tile of 128 tokens in every group of as many tiles, and 8 warps 16 tokens each
+// of a tile. A warp forms its gates once, into registers, and from them what its
+// tokens do to the state (a Step); the tile's Step goes to every CTA of the
+// cluster through distributed shared memory, each folds those before its own
+// into the state that the group began with, and the tokens are gone through once
+// more from their true state. Tiles come ahead through a ring of TMA copies, with
+// the places where sequences begin and end in them, which the copying warp looks
+// up. The backward forms h of a tile again from the state kept before it, which
+// needs no other tile, and goes through the tiles from the last.
+constexpr int kTok = kEvery, kWarps = 8, kPer = kTok / kWarps, kScanThreads = kWarps * 32 + 32;
+constexpr int kTileBytes = kTok * 128, kMaxCluster = 16, kMaxStages = 4;
+constexpr long long kScanWaitCycles = 2000000000LL;   // ~1 s: far above any legitimate wait
+
+struct TileSeqs {
+    uint32_t begin[kTok / 32], end[kTok / 32], dead[kTok / 32];   // bits: first tokens, last tokens, tokens of no sequence
+    int seq[kTok];                                                // of the first and last tokens
+};
+struct ScanBars {
+    uint64_t full[kMaxStages], empty[kMaxStages], steps[2];
+    uint32_t flags[kTok];
+    TileSeqs seqs[kMaxStages];
+};
+constexpr int kWarpStepBytes = kWarps * 32 * 16, kTileStepBytes = 32 * 16;   // of a tile, of a cluster's CTA
+
+struct ScanMaps {
+    CUtensorMap x, g, dh;
+};
+struct ScanGeo {
+    int tiles, cluster, groups, stages;   // groups: of `cluster` tiles
+};
+
+template <typename L>
+__device__ __forceinline__ uint4 pack_step(const Step<L> &s) {
+    if constexpr (L::kCh == 2) {
+        float a, b, c, d;
+        unpack2(s.A, a, b), unpack2(s.H, c, d);
+        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+    } else {
+        return make_uint4(__float_as_uint(s.A), __float_as_uint(s.H), 0, 0);
+    }
+}
+template <typename L>
+__device__ __forceinline__ Step<L> unpack_step(const uint4 &v) {
+    Step<L> s;
+    if constexpr (L::kCh == 2) s.A = pack2u(v.x, v.y), s.H = pack2u(v.z, v.w);
+    else s.A = __uint_as_float(v.x), s.H = __uint_as_float(v.y);
+    return s;
+}
+
+// 16 bytes to the shared memory of a CTA of the cluster, counted on a barrier there
+__device__ __forceinline__ void store_remote(uint32_t addr, const uint4 &v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr), "r"(v.x),
+                 "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+                 : "memory");
+}
+
+// A bounded wait; after one that gave up the thread makes no other and goes
+// through the rest with whatever is there, in step with the others.
+__device__ __forceinline__ void scan_wait(uint64_t *bar, uint32_t parity, bool &lost, int *status) {
+    if (lost) return;
+    const uint32_t at = smem_u32(bar);
+    if (mbar_try_wait(at, parity)) return;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(at, parity))
+        if (clock64() - t0 > kScanWaitCycles) {
+            atomicOr(status, LCE_DEV_TIMEOUT);
+            lost = true;
+            return;
+        }
+}
+
+// Where sequences begin and end among the tokens from t0 on, by one warp.
+__device__ __forceinline__ void find_seqs(const ScanArgs &a, int t0, uint32_t *flags, TileSeqs &out) {
+    const int lane = threadIdx.x & 31;
+    if (!a.cu) {
+#pragma unroll
+        for (int k = 0; k < kTok / 32; ++k) {
+            const int t = t0 + 32 * k + lane;
+            const bool live = t < a.T;
+            const int b = live ? t / a.len : 0, at = t - b * a.len;
+            const uint32_t begin = __ballot_sync(0xffffffffu, live && at == 0), end = __ballot_sync(0xffffffffu, live && at == a.len - 1),
+                           dead = __ballot_sync(0xffffffffu, !live);
+            out.seq[32 * k + lane] = b;
+            if (lane == 0) out.begin[k] = begin, out.end[k] = end, out.dead[k] = dead;
+        }
         return;
     }
-    float m = a.dfinal ? a.dfinal[at] : 0.f;
-    float before[kEvery];
-    for (int hi = end; hi > begin;) {
-        const int lo = max(begin, (hi - 1) / kEvery * kEvery);
-        float h = lo == begin ? (a.state ? a.state[at] : 0.f) : a.kept[static_cast<int64_t>(lo / kEvery) * a.d + ch];
-        for (int t = lo; t < hi; ++t) {
-            float f, rest;
-            gate(static_cast<float>(static_cast<const T *>(a.g)[t * a.ld_g + ch]), f, rest);
-            before[t - lo] = h;
-            h = fmaf(f, h, rest * static_cast<float>(static_cast<const T *>(a.x)[t * a.ld_x + ch]));
-        }
-        for (int t = hi - 1; t >= lo; --t) {
-            float f, rest;
-            gate(static_cast<float>(static_cast<const T *>(a.g)[t * a.ld_g + ch]), f, rest);
-            const float l = static_cast<float>(static_cast<const T *>(a.dh)[t * a.ld_dh + ch]) + m;
-            const float x = static_cast<float>(static_cast<const T *>(a.x)[t * a.ld_x + ch]);
-            static_cast<T *>(a.dx)[t * a.ld_dx + ch] = static_cast<T>(rest * l);
-            static_cast<T *>(a.dg)[t * a.ld_dg + ch] = static_cast<T>(l * (before[t - lo] - x) * f * rest);
-            m = f * l;
-        }
-        hi = lo;
+#pragma unroll
+    for (int k = 0; k < kTok / 32; ++k) flags[32 * k + lane] = 0;
+    // the last sequence that does not begin after t0, among 32 probes a round
+    int lo = 0, n = a.B + 1;
+    while (n > 1) {
+        const int step = (n + 31) / 32, off = lane * step;
+        const uint32_t mask = __ballot_sync(0xffffffffu, off < n && a.start(lo + off) <= t0);
+        const int hit = mask ? 31 - __clz(mask) : 0;   // offsets that do not ascend may leave holes
+        lo += hit * step;
+        n = min(step, n - hit * step);
     }
-    if (a.dstate) a.dstate[at] = m;
+    __syncwarp();
+    const int live = a.start(a.B);
+    for (int b = lo; b < a.B; b += 32) {
+        const int mine = b + lane, s = mine < a.B ? a.start(mine) : a.T, e = mine < a.B ? a.start(mine + 1) : a.T;
+        if (mine < a.B && e > s) {
+            if (s >= t0 && s < t0 + kTok) out.seq[s - t0] = mine, atomicOr(&flags[s - t0], 1u);
+            if (e > t0 && e <= t0 + kTok) out.seq[e - 1 - t0] = mine, atomicOr(&flags[e - 1 - t0], 2u);
+        }
+        if (__any_sync(0xffffffffu, s >= t0 + kTok)) break;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kTok / 32; ++k) {
+        const uint32_t f = flags[32 * k + lane];
+        const uint32_t begin = __ballot_sync(0xffffffffu, f & 1), end = __ballot_sync(0xffffffffu, f & 2),
+                       dead = __ballot_sync(0xffffffffu, t0 + 32 * k + lane >= live);
+        if (lane == 0) out.begin[k] = begin & ~dead, out.end[k] = end & ~dead, out.dead[k] = dead;
+    }
+}
+
+// The states of empty sequences pass through; a warp of every CTA takes its share of the sequences.
+template <typename L>
+__device__ __forceinline__ void empty_seqs(const ScanArgs &a, int rank, int cluster, int ch0, const float *from, float *to) {
+    if (!to || (!a.cu && a.len > 0)) return;
+    const int lane = threadIdx.x & 31, ch = ch0 + lane * L::kCh;
+    for (int b = rank * 32; b < a.B; b += cluster * 32) {
+        const int mine = b + lane;
+        uint32_t mask = __ballot_sync(0xffffffffu, mine < a.B && a.start(mine + 1) <= a.start(mine));
+        for (; mask; mask &= mask - 1) {
+            const int64_t at = static_cast<int64_t>(b + __ffs(mask) - 1) * a.d + ch;
+            if (ch < a.d) L::save(to + at, from ? L::load(from + at) : L::all(0.f));
+        }
+    }
+}
+
+__device__ __forceinline__ void check_offsets(const ScanArgs &a) {   // one warp
+    if (!a.cu) return;
+    bool bad = false;
+    for (int b = threadIdx.x & 31; b <= a.B; b += 32) bad |= b == 0 ? a.cu[0] != 0 : a.cu[b] < a.cu[b - 1] || a.cu[b] > a.T;
+    if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) atomicOr(a.status, LCE_DEV_SEQLENS);
+}
+
+template <typename T, bool kBack>
+__global__ void __launch_bounds__(kScanThreads, 2) k_scan(const ScanArgs a, const ScanGeo geo, const __grid_constant__ ScanMaps maps) {
+    using L = Lane<T>;
+    using F = typename L::F;
+    constexpr int kStageBytes = (kBack ? 3 : 2) * kTileBytes, kSlice = 32 * L::kCh;
+    extern __shared__ __align__(128) uint8_t ring[];   // tiles of x, g (and dh); the warps' steps; the cluster's
+    __shared__ ScanBars sm;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int rank = geo.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int ch0 = static_cast<int>(blockIdx.x) / geo.cluster * kSlice;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < geo.stages; ++i) mbar_init(&sm.full[i], 2), mbar_init(&sm.empty[i], kWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(&sm.steps[i], 1);
+        fence_mbar_init();
+    }
+    if (geo.cluster > 1) cluster_sync_all();
+    else __syncthreads();
+    bool lost = false;
+    int s = 0;
+    uint32_t phase = 0;
+    if (warp == kWarps) {
+        int issued = 0;
+        for (int group = 0; group < geo.groups; ++group) {
+            const int tile = kBack ? geo.tiles - 1 - (group * geo.cluster + rank) : group * geo.cluster + rank;
+            if (tile < 0 || tile >= geo.tiles) break;   // (in the last group)
+            scan_wait(&sm.empty[s], phase ^ 1, lost, a.status);
+            if (__any_sync(0xffffffffu, lost)) break;
+            if (lane == 0) {
+                uint8_t *dst = ring + s * kStageBytes;
+                mbar_arrive_expect_tx(&sm.full[s], kStageBytes);
+                tma_load_2d(dst, &maps.x, &sm.full[s], ch0, tile * kTok);
+                tma_load_2d(dst + kTileBytes, &maps.g, &sm.full[s], ch0, tile * kTok);
+                if (kBack) tma_load_2d(dst + 2 * kTileBytes, &maps.dh, &sm.full[s], ch0, tile * kTok);
+            }
+            find_seqs(a, tile * kTok, sm.flags, sm.seqs[s]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.full[s]);
+            ++issued;
+            if (++s == geo.stages) s = 0, phase ^= 1;
+        }
+        empty_seqs<L>(a, rank, geo.cluster, ch0, kBack ? a.dfinal : a.state, kBack ? a.dstate : a.final);
+        if (blockIdx.x == 0) check_offsets(a);
+        // copies in flight have to land before the CTA gives up its memory (all have, unless a wait gave up)
+        for (int i = 0; i < min(issued, geo.stages); ++i) {
+            if (--s < 0) s = geo.stages - 1, phase ^= 1;
+            const long long t0 = clock64();
+            while (!mbar_try_wait(smem_u32(&sm.full[s]), phase) && clock64() - t0 < kScanWaitCycles / 10) {}
+        }
+    } else {
+        uint8_t *warp_steps = ring + geo.stages * kStageBytes, *tile_steps = warp_steps + (kBack ? 4 : 2) * kWarpStepBytes;
+        const int ch = ch0 + lane * L::kCh;
+        const bool in = ch < a.d;
+        F carry = L::all(0.f);   // the state before the group, or (backward) the gradient that comes from behind it
+        for (int group = 0; group < geo.groups; ++group) {
+            const int tile = kBack ? geo.tiles - 1 - (group * geo.cluster + rank) : group * geo.cluster + rank, par = group & 1;
+            const bool have = tile >= 0 && tile < geo.tiles;
+            const uint8_t *xs = ring + s * kStageBytes + warp * kPer * 128 + lane * 4, *gs = xs + kTileBytes, *ds = gs + kTileBytes;
+            auto word = [](const uint8_t *p, int i) { return *reinterpret_cast<const uint32_t *>(p + i * 128); };
+            const int *seq = sm.seqs[s].seq + warp * kPer;
+            uint32_t begin = 0, end = 0, dead = 0;
+            F av[kPer], v[kPer];   // gates; what a token adds to the state, in the backward later h_{t-1} - x_t
+            Step<L> fwd{L::all(1.f), L::all(0.f)}, bwd{L::all(1.f), L::all(0.f)};
+            F before = L::all(0.f);   // (backward) the state before the tile
+            auto state = [&](const float *p, int i) {
+                return p && in ? L::load(p + static_cast<int64_t>(seq[i]) * a.d + ch) : L::all(0.f);
+            };
+            // what to do at a token, for a warp with and without the ends of sequences among its tokens
+            auto at = [](uint32_t bits, int i) { return (bits >> i & 1u) != 0; };
+            auto gates = [&](auto special) {
+                constexpr bool kSpecial = decltype(special)::value;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    F rest;
+                    gate<L>(L::get(word(gs, i)), av[i], rest);
+                    v[i] = L::mul(rest, L::get(word(xs, i)));
+                    if (kSpecial && at(dead, i)) av[i] = v[i] = L::all(0.f);
+                    if (kSpecial && at(begin, i)) v[i] = L::fma(av[i], state(a.state, i), v[i]);
+                    if (kSpecial && at(begin | dead, i)) fwd.A = L::all(kReset), fwd.H = v[i];
+                    else {
+                        fwd.H = L::fma(av[i], fwd.H, v[i]);
+                        if (!kSpecial || !(L::first(fwd.A) < 0.f)) fwd.A = L::mul(fwd.A, av[i]);
+                    }
+                }
+                if constexpr (kBack) {
+#pragma unroll
+                    for (int i = kPer - 1; i >= 0; --i) {
+                        F l = L::get(word(ds, i));
+                        if (kSpecial && at(dead, i)) l = L::all(0.f);
+                        if (kSpecial && at(end, i)) l = L::add(l, state(a.dfinal, i));
+                        if (kSpecial && at(end | dead, i)) bwd.A = L::all(kReset), bwd.H = L::mul(av[i], l);
+                        else {
+                            bwd.H = L::mul(av[i], L::add(l, bwd.H));
+                            if (!kSpecial || !(L::first(bwd.A) < 0.f)) bwd.A = L::mul(bwd.A, av[i]);
+                        }
+                    }
+                }
+            };
+            if (have) {
+                if (kBack && in) before = L::load(a.kept + static_cast<int64_t>(tile) * a.d + ch);
+                scan_wait(&sm.full[s], phase, lost, a.status);
+                const int sh = warp % 2 * kPer;
+                begin = sm.seqs[s].begin[warp / 2] >> sh & 0xffffu;
+                end = sm.seqs[s].end[warp / 2] >> sh & 0xffffu;
+                dead = sm.seqs[s].dead[warp / 2] >> sh & 0xffffu;
+                if (begin | end | dead) gates(std::true_type());
+                else gates(std::false_type());
+            }
+            uint8_t *mine = warp_steps + par * kWarpStepBytes, *mine_b = mine + 2 * kWarpStepBytes;
+            auto warp_step = [&](const uint8_t *p, int w) { return unpack_step<L>(*reinterpret_cast<const uint4 *>(p + (w * 32 + lane) * 16)); };
+            *reinterpret_cast<uint4 *>(mine + (warp * 32 + lane) * 16) = pack_step(fwd);
+            if (kBack) *reinterpret_cast<uint4 *>(mine_b + (warp * 32 + lane) * 16) = pack_step(bwd);
+            asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+            uint8_t *theirs = tile_steps + par * geo.cluster * kTileStepBytes;
+            if (geo.cluster > 1) {
+                if (threadIdx.x == 0) mbar_arrive_expect_tx(&sm.steps[par], geo.cluster * kTileStepBytes);
+                if (warp < geo.cluster) {
+                    Step<L> all = kBack ? warp_step(mine_b, kWarps - 1) : warp_step(mine, 0);
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) all = then(all, kBack ? warp_step(mine_b, kWarps - 1 - w) : warp_step(mine, w));
+                    for (int to = warp; to < geo.cluster; to += kWarps)
+                        store_remote(map_to_cta(smem_u32(theirs + rank * kTileStepBytes + lane * 16), to), pack_step(all),
+                                     map_to_cta(smem_u32(&sm.steps[par]), to));
+                }
+            }
+            if (kBack && have) {   // h again, from the state before the tile
+                F h = before;
+                for (int w = 0; w < warp; ++w) h = apply(warp_step(mine, w), h);
+                auto again = [&](auto special) {
+                    constexpr bool kSpecial = decltype(special)::value;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        const F minus_x = L::mul(L::get(word(xs, i)), L::all(-1.f));
+                        const bool first = kSpecial && at(begin, i);
+                        const F next = kSpecial && at(begin | dead, i) ? v[i] : L::fma(av[i], h, v[i]);
+                        v[i] = L::add(first ? state(a.state, i) : h, minus_x);
+                        h = next;
+                    }
+                };
+                if (begin | dead) again(std::true_type());
+                else again(std::false_type());
+            }
+            F c = carry;
+            if (geo.cluster > 1) {
+                scan_wait(&sm.steps[par], group >> 1 & 1, lost, a.status);
+                for (int r = 0; r < geo.cluster; ++r) {
+                    if (r == rank) c = carry;
+                    carry = apply(unpack_step<L>(*reinterpret_cast<const uint4 *>(theirs + r * kTileStepBytes + lane * 16)), carry);
+                }
+            }
+            if (!kBack && a.kept && have && warp == 0 && in) L::save(a.kept + static_cast<int64_t>(tile) * a.d + ch, c);
+            if (kBack)
+                for (int w = kWarps - 1; w > warp; --w) c = apply(warp_step(mine_b, w), c);
+            else
+                for (int w = 0; w < warp; ++w) c = apply(warp_step(mine, w), c);
+            if (geo.cluster == 1) {
+                carry = c;
+                if (kBack)
+                    for (int w = warp; w >= 0; --w) carry = apply(warp_step(mine_b, w), carry);
+                else
+                    for (int w = warp; w < kWarps; ++w) carry = apply(warp_step(mine, w), carry);
+            }
+            if (!have) continue;
+            const int t0 = tile * kTok + warp * kPer;
+            auto put = [&](void *p, int64_t ld, int i, F value) {
+                *reinterpret_cast<uint32_t *>(static_cast<T *>(p) + (t0 + i) * ld + ch) = L::put(value);
+            };
+            auto out = [&](auto special) {
+                constexpr bool kSpecial = decltype(special)::value;
+                if (!kBack) {
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        c = kSpecial && at(begin | dead, i) ? v[i] : L::fma(av[i], c, v[i]);
+                        if (in && (!kSpecial || t0 + i < a.T)) put(a.h, a.ld_h, i, c);
+                        if (kSpecial && at(end, i) && a.final && in) L::save(a.final + static_cast<int64_t>(seq[i]) * a.d + ch, c);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = kPer - 1; i >= 0; --i) {
+                        const F rest = L::mul(gate_exp<L>(L::get(word(gs, i))), av[i]);
+                        F l = L::get(word(ds, i));
+                        l = L::add(l, kSpecial && at(end, i) ? state(a.dfinal, i) : c);
+                        F dx = L::mul(rest, l), dg = L::mul(L::mul(l, v[i]), L::mul(av[i], rest));
+                        c = L::mul(av[i], l);
+                        if (kSpecial && at(dead, i)) dx = dg = c = L::all(0.f);
+                        if (in && (!kSpecial || t0 + i < a.T)) put(a.dx, a.ld_dx, i, dx), put(a.dg, a.ld_dg, i, dg);
+                        if (kSpecial && at(begin, i) && a.dstate && in) L::save(a.dstate + static_cast<int64_t>(seq[i]) * a.d + ch, c);
+                    }
+                }
+            };
+            if (begin | end | dead) out(std::true_type());
+            else out(std::false_type());
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[s]);
+            if (++s == geo.stages) s = 0, phase ^= 1;
+        }
+    }
+    if (geo.cluster > 1) cluster_sync_all();   // no CTA leaves while another may write to its shared memory
+}
+
+// One token of every sequence: no scan. A thread takes 8 channels of a sequence.
+template <typename T>
+__global__ void __launch_bounds__(256) k_scan_step(const ScanArgs a) {
+    const int per = a.d / kVec, id = blockIdx.x * 256 + threadIdx.x;
+    const int64_t b = id / per;
+    const int ch = (id - static_cast<int>(b) * per) * kVec;
+    if (b >= a.B) return;
+    float g[kVec], x[kVec], h[kVec];
+    load_pack(static_cast<const T *>(a.g) + b * a.ld_g + ch).get(g);
+    load_pack(static_cast<const T *>(a.x) + b * a.ld_x + ch).get(x);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) h[i] = 0.f;
+    if (a.state) load_pack(a.state + b * a.d + ch).get(h);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        float f, rest;
+        gate<Lane<float>>(g[i], f, rest);
+        h[i] = fmaf(f, h[i], rest * x[i]);
+    }
+    store_pack(static_cast<T *>(a.h) + b * a.ld_h + ch, h);
+    if (a.final) store_pack(a.final + b * a.d + ch, h);
+    if (!a.kept) return;
+    if ((b + 1) % kEvery == 0 && b + 1 < a.T) store_pack(a.kept + (b + 1) / kEvery * a.d + ch, h);
+    if (b == 0) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) h[i] = 0.f;
+        store_pack(a.kept + ch, h);
+    }
 }
 
 lce_status_t check_rows(const void *p, int64_t ld, int64_t d, int elt) {
@@ -144,6 +533,75 @@ ScanArgs make_args(const lce_recurrence_t *a, const HostDev &dev) {
     return r;
 }
 
+lce_status_t encode(CUtensorMap *m, const HostDev &dev, const void *p, bool bf16, int64_t T, int64_t d, int64_t ld) {
+    const int elt = bf16 ? 2 : 4;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(T)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * elt};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(kTok)}, es[2] = {1, 1};
+    const CUresult r = dev.encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(p), dims,
+                                  strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? LCE_OK : LCE_ERR_SHAPE;
+}
+
+// Two CTAs an SM; the ring takes what the steps leave of half its shared memory.
+constexpr int kScanBytes = 112 * 1024;
+
+template <typename T, bool kBack>
+lce_status_t launch_scan(const ScanArgs &r, const HostDev &dev, cudaStream_t st) {
+    constexpr bool kBf16 = sizeof(T) == 2;
+    constexpr int kStageBytes = (kBack ? 3 : 2) * kTileBytes, kSlice = 128 / sizeof(T);
+    ScanMaps maps{};
+    lce_status_t s = LCE_OK;
+    if (r.T > 0) {
+        s = encode(&maps.x, dev, r.x, kBf16, r.T, r.d, r.ld_x);
+        if (s == LCE_OK) s = encode(&maps.g, dev, r.g, kBf16, r.T, r.d, r.ld_g);
+        if (s == LCE_OK && kBack) s = encode(&maps.dh, dev, r.dh, kBf16, r.T, r.d, r.ld_dh);
+        if (s != LCE_OK) return s;
+    }
+    ScanGeo geo;
+    geo.tiles = (r.T + kTok - 1) / kTok;
+    const int slices = (r.d + kSlice - 1) / kSlice;
+    geo.cluster = 1;
+    while (geo.cluster < kMaxCluster && geo.cluster < geo.tiles && slices * geo.cluster * 2 <= 2 * dev.sms) geo.cluster *= 2;
+    geo.groups = (geo.tiles + geo.cluster - 1) / geo.cluster;
+    const int steps = (kBack ? 4 : 2) * kWarpStepBytes + 2 * geo.cluster * kTileStepBytes;
+    geo.stages = std::max(2, std::min(kMaxStages, (kScanBytes - static_cast<int>(sizeof(ScanBars)) - steps) / kStageBytes));
+    const int smem = geo.stages * kStageBytes + steps;
+    constexpr auto kernel = k_scan<T, kBack>;
+    if ((s = host_smem<kernel>(dev, 2 * kScanBytes)) != LCE_OK) return s;
+    if (geo.cluster > 8) {
+        static std::atomic<uint64_t> done{0};
+        const uint64_t bit = uint64_t(1) << dev.index;
+        if (!(done.load(std::memory_order_relaxed) & bit)) {
+            s = host_cuda(cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+            if (s != LCE_OK) return s;
+            done.fetch_or(bit, std::memory_order_relaxed);
+        }
+    }
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(geo.cluster), attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(slices * geo.cluster));
+    cfg.blockDim = dim3(kScanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    s = host_cuda(cudaLaunchKernelEx(&cfg, kernel, r, geo, maps));
+    return s != LCE_OK ? s : host_launched();
+}
+
+template <typename T>
+lce_status_t forward(const ScanArgs &r, const HostDev &dev, cudaStream_t st) {
+    if (!r.cu && r.len == 1 && static_cast<int64_t>(r.B) * r.d <= (int64_t(1) << 30)) {
+        k_scan_step<T><<<static_cast<unsigned>((static_cast<int64_t>(r.B) * (r.d / kVec) + 255) / 256), 256, 0, st>>>(r);
+        return host_launched();
+    }
+    return launch_scan<T, false>(r, dev, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -155,11 +613,7 @@ lce_status_t lce_recurrence_forward(const lce_recurrence_t *a) {
     if ((s = host_device(&dev)) != LCE_OK) return s;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
     const ScanArgs r = make_args(a, dev);
-    const int slices = (r.d + 127) / 128;
-    const unsigned grid = static_cast<unsigned>((a->B + 1) * slices);
-    if (a->dtype == LCE_BF16) k_scan_fwd_simple<__nv_bfloat16><<<grid, 128, 0, st>>>(r, slices);
-    else k_scan_fwd_simple<float><<<grid, 128, 0, st>>>(r, slices);
-    return host_launched();
+    return a->dtype == LCE_BF16 ? forward<__nv_bfloat16>(r, dev, st) : forward<float>(r, dev, st);
 }
 
 lce_status_t lce_recurrence_backward(const lce_recurrence_t *a) {
@@ -169,11 +623,7 @@ lce_status_t lce_recurrence_backward(const lce_recurrence_t *a) {
     if ((s = host_device(&dev)) != LCE_OK) return s;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
     const ScanArgs r = make_args(a, dev);
-    const int slices = (r.d + 127) / 128;
-    const unsigned grid = static_cast<unsigned>((a->B + 1) * slices);
-    if (a->dtype == LCE_BF16) k_scan_bwd_simple<__nv_bfloat16><<<grid, 128, 0, st>>>(r, slices);
-    else k_scan_bwd_simple<float><<<grid, 128, 0, st>>>(r, slices);
-    return host_launched();
+    return a->dtype == LCE_BF16 ? launch_scan<__nv_bfloat16, true>(r, dev, st) : launch_scan<float, true>(r, dev, st);
 }
 
 }  // extern "C"
