@@ -28,6 +28,17 @@ struct ScanArgs {
     __device__ __forceinline__ int start(int b) const { return cu ? min(max(cu[b], 0), T) : b * len; }
 };
 
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // The state of a channel pair (bf16) or a channel (fp32), the 4 bytes of a row
 // that a thread takes.
 template <typename T>
@@ -78,21 +89,13 @@ struct Lane<float> {
     static __device__ __forceinline__ void save(float *p, F v) { *p = v; }
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float rcp(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // exp(-g), bounded so that neither 1 + it nor its reciprocal leaves fp32 (a NaN stays one)
 template <typename L>
 __device__ __forceinline__ typename L::F gate_exp(typename L::F g) {
-    return L::each(L::mul(g, L::all(-1.4426950408889634f)), [](float z) { return ex2(z > 126.f ? 126.f : z); });
+    return L::each(L::mul(g, L::all(-1.4426950408889634f)), [](float z) {
+        asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(z));   // 126
+        return ex2(z);
+    });
 }
 // The gate and its complement, each to its own relative precision
 template <typename L>
@@ -114,13 +117,6 @@ template <typename L>
 __device__ __forceinline__ typename L::F apply(const Step<L> &s, typename L::F before) {
     return L::first(s.A) < 0.f ? s.H : L::fma(s.A, before, s.H);
 }
-template <typename L>
-__device__ __forceinline__ Step<L> then(const Step<L> &a, const Step<L> &b) {   // a, then b
-    Step<L> r;
-    r.H = apply(b, a.H);
-    r.A = L::first(b.A) < 0.f || L::first(a.A) < 0.f ? L::all(kReset) : L::mul(a.A, b.A);
-    return r;
-}
 
 // Work is split over channels and over time. A slice is the channels of 128
 // bytes of a row; a cluster of CTAs takes a slice through the tokens, each CTA a
@@ -133,8 +129,8 @@ __device__ __forceinline__ Step<L> then(const Step<L> &a, const Step<L> &b) {   
 // the places where sequences begin and end in them, which the copying warp looks
 // up. The backward forms h of a tile again from the state kept before it, which
 // needs no other tile, and goes through the tiles from the last.
-constexpr int kTok = kEvery, kWarps = 8, kPer = kTok / kWarps, kScanThreads = kWarps * 32 + 32;
-constexpr int kTileBytes = kTok * 128, kMaxCluster = 16, kMaxStages = 4;
+constexpr int kTok = kEvery, kWarps = 8, kPer = kTok / kWarps, kScanThreads = kWarps * 32;
+constexpr int kTileBytes = kTok * 128, kMaxCluster = 16, kMaxStages = 3;
 constexpr long long kScanWaitCycles = 2000000000LL;   // ~1 s: far above any legitimate wait
 
 struct TileSeqs {
@@ -142,11 +138,12 @@ struct TileSeqs {
     int seq[kTok];                                                // of the first and last tokens
 };
 struct ScanBars {
-    uint64_t full[kMaxStages], empty[kMaxStages], steps[2];
+    uint64_t full[kMaxStages], done[kMaxStages], steps[2];
     uint32_t flags[kTok];
-    TileSeqs seqs[kMaxStages];
+    TileSeqs seqs[kMaxStages + 1];   // one more than tiles, since a tile's are read until its results are out
 };
-constexpr int kWarpStepBytes = kWarps * 32 * 16, kTileStepBytes = 32 * 16;   // of a tile, of a cluster's CTA
+// Steps of a warp's channels; 32 bytes apart, so that the lanes that join two warps each meet in no more banks than they must.
+constexpr int kStepBytes = 32 * 16, kWarpStepBytes = kStepBytes + 32;
 
 struct ScanMaps {
     CUtensorMap x, g, dh;
@@ -155,28 +152,68 @@ struct ScanGeo {
     int tiles, cluster, groups, stages;   // groups: of `cluster` tiles
 };
 
+// Steps in memory: A and H of one channel after the other
 template <typename L>
-__device__ __forceinline__ uint4 pack_step(const Step<L> &s) {
+__device__ __forceinline__ void save_step(uint8_t *p, const Step<L> &s) {
     if constexpr (L::kCh == 2) {
-        float a, b, c, d;
-        unpack2(s.A, a, b), unpack2(s.H, c, d);
-        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+        float4 v;
+        unpack2(s.A, v.x, v.z), unpack2(s.H, v.y, v.w);
+        *reinterpret_cast<float4 *>(p) = v;
     } else {
-        return make_uint4(__float_as_uint(s.A), __float_as_uint(s.H), 0, 0);
+        *reinterpret_cast<float2 *>(p) = make_float2(s.A, s.H);
     }
 }
 template <typename L>
-__device__ __forceinline__ Step<L> unpack_step(const uint4 &v) {
-    Step<L> s;
-    if constexpr (L::kCh == 2) s.A = pack2u(v.x, v.y), s.H = pack2u(v.z, v.w);
-    else s.A = __uint_as_float(v.x), s.H = __uint_as_float(v.y);
-    return s;
+__device__ __forceinline__ Step<L> load_step(const uint8_t *p) {
+    if constexpr (L::kCh == 2) {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        return Step<L>{pack2(v.x, v.z), pack2(v.y, v.w)};
+    } else {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        return Step<L>{v.x, v.y};
+    }
 }
 
-// 16 bytes to the shared memory of a CTA of the cluster, counted on a barrier there
-__device__ __forceinline__ void store_remote(uint32_t addr, const uint4 &v, uint32_t bar) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr), "r"(v.x),
-                 "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+// A channel's Steps of the warps joined in order (kDown: from the last warp), by
+// the group of 8 / N neighbouring lanes that take it, N warps each: in a warp's
+// place the Step of those before it; the tile's Step is returned to all of them.
+template <int N, bool kDown>
+__device__ __forceinline__ Step<Lane<float>> join_warps(uint8_t *at, int stride, int lane) {
+    using L = Lane<float>;
+    constexpr int kLanes = kWarps / N;
+    auto then = [](const Step<L> &a, const Step<L> &b) {   // a, then b
+        return Step<L>{b.A < 0.f ? b.A : a.A < 0.f ? a.A : a.A * b.A, apply(b, a.H)};
+    };
+    const int q = kDown ? kLanes - 1 - lane % kLanes : lane % kLanes;   // place in order
+    Step<L> own[N], sum;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        own[i] = load_step<L>(at + (kDown ? kWarps - 1 - (q * N + i) : q * N + i) * stride);
+        sum = i == 0 ? own[0] : then(sum, own[i]);
+    }
+    auto from = [&](const Step<L> &s, int off) {   // of the lane `off` places before
+        return kDown ? Step<L>{__shfl_down_sync(0xffffffffu, s.A, off, kLanes), __shfl_down_sync(0xffffffffu, s.H, off, kLanes)}
+                     : Step<L>{__shfl_up_sync(0xffffffffu, s.A, off, kLanes), __shfl_up_sync(0xffffffffu, s.H, off, kLanes)};
+    };
+#pragma unroll
+    for (int off = 1; off < kLanes; off *= 2) {
+        const Step<L> b = from(sum, off);
+        if (q >= off) sum = then(b, sum);
+    }
+    Step<L> before = from(sum, 1);
+    if (q == 0) before = Step<L>{1.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        save_step<L>(at + (kDown ? kWarps - 1 - (q * N + i) : q * N + i) * stride, before);
+        if (i + 1 < N) before = then(before, own[i]);
+    }
+    const int last = kDown ? 0 : kLanes - 1;
+    return Step<L>{__shfl_sync(0xffffffffu, sum.A, last, kLanes), __shfl_sync(0xffffffffu, sum.H, last, kLanes)};
+}
+
+// 8 bytes to the shared memory of a CTA of the cluster, counted on a barrier there
+__device__ __forceinline__ void store_remote(uint32_t addr, float a, float b, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr), "f"(a), "f"(b), "r"(bar)
                  : "memory");
 }
 
@@ -195,52 +232,83 @@ __device__ __forceinline__ void scan_wait(uint64_t *bar, uint32_t parity, bool &
         }
 }
 
-// Where sequences begin and end among the tokens from t0 on, by one warp.
-__device__ __forceinline__ void find_seqs(const ScanArgs &a, int t0, uint32_t *flags, TileSeqs &out) {
-    const int lane = threadIdx.x & 31;
-    if (!a.cu) {
+// Where sequences begin and end in a tile, by one warp, which keeps the ends of
+// 32 sequences in its registers: tiles come in order, so that it seldom has to
+// look for others.
+struct SeqFinder {
+    const ScanArgs &a;
+    uint32_t *flags;
+    int live;                 // tokens of all sequences
+    int lo = -1, s = 0, e = 0;   // first token of sequence lo + lane, and the one behind its last
+    __device__ __forceinline__ SeqFinder(const ScanArgs &a_, uint32_t *f) : a(a_), flags(f), live(a_.cu ? a_.start(a_.B) : a_.T) {}
+
+    __device__ __forceinline__ void take(int from) {
+        const int mine = from + (threadIdx.x & 31);
+        s = mine < a.B ? a.start(mine) : a.T, e = mine < a.B ? a.start(mine + 1) : a.T;
+    }
+    __device__ __forceinline__ bool holds(int t0) const {   // all sequences with tokens in the tile
+        return lo >= 0 && __shfl_sync(0xffffffffu, s, 0) <= t0 && (lo + 32 >= a.B || __shfl_sync(0xffffffffu, e, 31) >= t0 + kTok);
+    }
+    __device__ __forceinline__ void mark(int from, int t0, TileSeqs &out) const {
+        const int mine = from + (threadIdx.x & 31);
+        if (mine >= a.B || e <= s) return;
+        if (s >= t0 && s < t0 + kTok) out.seq[s - t0] = mine, atomicOr(&flags[s - t0], 1u);
+        if (e > t0 && e <= t0 + kTok) out.seq[e - 1 - t0] = mine, atomicOr(&flags[e - 1 - t0], 2u);
+    }
+    template <bool kBack>
+    __device__ __forceinline__ void operator()(int t0, TileSeqs &out) {
+        const int lane = threadIdx.x & 31;
+        if (!a.cu) {
+#pragma unroll
+            for (int k = 0; k < kTok / 32; ++k) {
+                const int t = t0 + 32 * k + lane;
+                const bool live = t < a.T;
+                const int b = live ? t / a.len : 0, at = t - b * a.len;
+                const uint32_t begin = __ballot_sync(0xffffffffu, live && at == 0), end = __ballot_sync(0xffffffffu, live && at == a.len - 1),
+                               dead = __ballot_sync(0xffffffffu, !live);
+                out.seq[32 * k + lane] = b;
+                if (lane == 0) out.begin[k] = begin, out.end[k] = end, out.dead[k] = dead;
+            }
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < kTok / 32; ++k) flags[32 * k + lane] = 0;
+        __syncwarp();
+        if (holds(t0)) {
+            mark(lo, t0, out);
+        } else {
+            // the last sequence that does not begin after t0, among 32 probes a round
+            int b = 0, n = a.B + 1;
+            while (n > 1) {
+                const int step = (n + 31) / 32, off = lane * step;
+                const uint32_t mask = __ballot_sync(0xffffffffu, off < n && a.start(b + off) <= t0);
+                const int hit = mask ? 31 - __clz(mask) : 0;   // offsets that do not ascend may leave holes
+                b += hit * step;
+                n = min(step, n - hit * step);
+            }
+            lo = kBack ? max(0, b - 15) : b;   // the tiles to come are on that side
+            take(lo);
+            if (holds(t0)) {
+                mark(lo, t0, out);
+            } else {
+                lo = -1;
+                for (; b < a.B; b += 32) {
+                    take(b);
+                    mark(b, t0, out);
+                    if (__any_sync(0xffffffffu, s >= t0 + kTok)) break;
+                }
+            }
+        }
+        __syncwarp();
 #pragma unroll
         for (int k = 0; k < kTok / 32; ++k) {
-            const int t = t0 + 32 * k + lane;
-            const bool live = t < a.T;
-            const int b = live ? t / a.len : 0, at = t - b * a.len;
-            const uint32_t begin = __ballot_sync(0xffffffffu, live && at == 0), end = __ballot_sync(0xffffffffu, live && at == a.len - 1),
-                           dead = __ballot_sync(0xffffffffu, !live);
-            out.seq[32 * k + lane] = b;
-            if (lane == 0) out.begin[k] = begin, out.end[k] = end, out.dead[k] = dead;
+            const uint32_t f = flags[32 * k + lane];
+            const uint32_t begin = __ballot_sync(0xffffffffu, f & 1), end = __ballot_sync(0xffffffffu, f & 2),
+                           dead = __ballot_sync(0xffffffffu, t0 + 32 * k + lane >= live);
+            if (lane == 0) out.begin[k] = begin & ~dead, out.end[k] = end & ~dead, out.dead[k] = dead;
         }
-        return;
     }
-#pragma unroll
-    for (int k = 0; k < kTok / 32; ++k) flags[32 * k + lane] = 0;
-    // the last sequence that does not begin after t0, among 32 probes a round
-    int lo = 0, n = a.B + 1;
-    while (n > 1) {
-        const int step = (n + 31) / 32, off = lane * step;
-        const uint32_t mask = __ballot_sync(0xffffffffu, off < n && a.start(lo + off) <= t0);
-        const int hit = mask ? 31 - __clz(mask) : 0;   // offsets that do not ascend may leave holes
-        lo += hit * step;
-        n = min(step, n - hit * step);
-    }
-    __syncwarp();
-    const int live = a.start(a.B);
-    for (int b = lo; b < a.B; b += 32) {
-        const int mine = b + lane, s = mine < a.B ? a.start(mine) : a.T, e = mine < a.B ? a.start(mine + 1) : a.T;
-        if (mine < a.B && e > s) {
-            if (s >= t0 && s < t0 + kTok) out.seq[s - t0] = mine, atomicOr(&flags[s - t0], 1u);
-            if (e > t0 && e <= t0 + kTok) out.seq[e - 1 - t0] = mine, atomicOr(&flags[e - 1 - t0], 2u);
-        }
-        if (__any_sync(0xffffffffu, s >= t0 + kTok)) break;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < kTok / 32; ++k) {
-        const uint32_t f = flags[32 * k + lane];
-        const uint32_t begin = __ballot_sync(0xffffffffu, f & 1), end = __ballot_sync(0xffffffffu, f & 2),
-                       dead = __ballot_sync(0xffffffffu, t0 + 32 * k + lane >= live);
-        if (lane == 0) out.begin[k] = begin & ~dead, out.end[k] = end & ~dead, out.dead[k] = dead;
-    }
-}
+};
 
 // The states of empty sequences pass through; a warp of every CTA takes its share of the sequences.
 template <typename L>
@@ -271,193 +339,205 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan(const ScanArgs a, cons
     constexpr int kStageBytes = (kBack ? 3 : 2) * kTileBytes, kSlice = 32 * L::kCh;
     extern __shared__ __align__(128) uint8_t ring[];   // tiles of x, g (and dh); the warps' steps; the cluster's
     __shared__ ScanBars sm;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
     const int rank = geo.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int ch0 = static_cast<int>(blockIdx.x) / geo.cluster * kSlice;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < geo.stages; ++i) mbar_init(&sm.full[i], 2), mbar_init(&sm.empty[i], kWarps);
+        for (int i = 0; i < geo.stages; ++i) mbar_init(&sm.full[i], 2), mbar_init(&sm.done[i], kWarps);
         for (int i = 0; i < 2; ++i) mbar_init(&sm.steps[i], 1);
         fence_mbar_init();
     }
     if (geo.cluster > 1) cluster_sync_all();
     else __syncthreads();
     bool lost = false;
-    int s = 0;
+    // the tile of a group, or none (in the last group); tiles are asked for by the warp that has the least to do else
+    auto tile_of = [&](int group) {
+        const int i = group * geo.cluster + rank;
+        return i >= geo.tiles ? -1 : kBack ? geo.tiles - 1 - i : i;
+    };
+    const bool asks = warp == (kBack ? kWarps - 1 : 0);
+    SeqFinder find(a, sm.flags);
+    int asked = 0, ask_stage = 0, ask_slot = 0;
+    auto ask = [&]() {
+        const int tile = asked < geo.groups ? tile_of(asked) : -1;
+        if (tile < 0) return;
+        if (lane == 0) {
+            uint8_t *dst = ring + ask_stage * kStageBytes;
+            uint64_t *bar = &sm.full[ask_stage];
+            mbar_arrive_expect_tx(bar, kStageBytes);
+            tma_load_2d(dst, &maps.x, bar, ch0, tile * kTok);
+            tma_load_2d(dst + kTileBytes, &maps.g, bar, ch0, tile * kTok);
+            if (kBack) tma_load_2d(dst + 2 * kTileBytes, &maps.dh, bar, ch0, tile * kTok);
+        }
+        find.template operator()<kBack>(tile * kTok, sm.seqs[ask_slot]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.full[ask_stage]);
+        ++asked;
+        if (++ask_stage == geo.stages) ask_stage = 0;
+        if (++ask_slot > geo.stages) ask_slot = 0;
+    };
+    if (asks)
+        for (int i = 0; i < geo.stages; ++i) ask();
+    uint8_t *steps = ring + geo.stages * kStageBytes, *steps_b = steps + kWarps * kWarpStepBytes;   // of the warps; (backward) the gradient's
+    uint8_t *tile_steps = steps + (kBack ? 2 : 1) * kWarps * kWarpStepBytes;                          // of the cluster's tiles, [parity][rank]
+    const int ch = ch0 + lane * L::kCh;
+    const uint32_t lane_bytes = ch * sizeof(T);
+    const bool in = ch < a.d;
+    F carry = L::all(0.f);   // the state before the group, or (backward) the gradient that comes from behind it
+    int s = 0, slot = 0;
     uint32_t phase = 0;
-    if (warp == kWarps) {
-        int issued = 0;
-        for (int group = 0; group < geo.groups; ++group) {
-            const int tile = kBack ? geo.tiles - 1 - (group * geo.cluster + rank) : group * geo.cluster + rank;
-            if (tile < 0 || tile >= geo.tiles) break;   // (in the last group)
-            scan_wait(&sm.empty[s], phase ^ 1, lost, a.status);
-            if (__any_sync(0xffffffffu, lost)) break;
-            if (lane == 0) {
-                uint8_t *dst = ring + s * kStageBytes;
-                mbar_arrive_expect_tx(&sm.full[s], kStageBytes);
-                tma_load_2d(dst, &maps.x, &sm.full[s], ch0, tile * kTok);
-                tma_load_2d(dst + kTileBytes, &maps.g, &sm.full[s], ch0, tile * kTok);
-                if (kBack) tma_load_2d(dst + 2 * kTileBytes, &maps.dh, &sm.full[s], ch0, tile * kTok);
+    for (int group = 0; group < geo.groups; ++group) {
+        const int tile = tile_of(group), par = group & 1;
+        const bool have = tile >= 0;
+        const uint8_t *xs = ring + s * kStageBytes + warp * kPer * 128 + lane * 4, *gs = xs + kTileBytes, *ds = gs + kTileBytes;
+        auto word = [](const uint8_t *p, int i) { return *reinterpret_cast<const uint32_t *>(p + i * 128); };
+        const TileSeqs &seqs = sm.seqs[slot];
+        const int *seq = seqs.seq + warp * kPer;
+        uint32_t begin = 0, end = 0, dead = 0;
+        F av[kPer], v[kPer];   // gates; what a token adds to the state, in the backward later h_{t-1} - x_t
+        Step<L> fwd{L::all(1.f), L::all(0.f)}, bwd{L::all(1.f), L::all(0.f)};
+        F before = L::all(0.f);   // (backward) the state before the tile
+        auto state = [&](const float *p, int i) {
+            return p && in ? L::load(p + static_cast<int64_t>(seq[i]) * a.d + ch) : L::all(0.f);
+        };
+        // what to do at a token, for a warp with and without the ends of sequences among its tokens
+        auto at = [](uint32_t bits, int i) { return (bits >> i & 1u) != 0; };
+        auto gates = [&](auto special) {
+            constexpr bool kSpecial = decltype(special)::value;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                F rest;
+                gate<L>(L::get(word(gs, i)), av[i], rest);
+                v[i] = L::mul(rest, L::get(word(xs, i)));
+                if (kSpecial && at(dead, i)) av[i] = v[i] = L::all(0.f);
+                if (kSpecial && at(begin, i)) v[i] = L::fma(av[i], state(a.state, i), v[i]);
+                if (kSpecial && at(begin | dead, i)) fwd.A = L::all(kReset), fwd.H = v[i];
+                else {
+                    fwd.H = L::fma(av[i], fwd.H, v[i]);
+                    if (!kSpecial || !(L::first(fwd.A) < 0.f)) fwd.A = L::mul(fwd.A, av[i]);
+                }
             }
-            find_seqs(a, tile * kTok, sm.flags, sm.seqs[s]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.full[s]);
-            ++issued;
-            if (++s == geo.stages) s = 0, phase ^= 1;
+            if constexpr (kBack) {
+#pragma unroll
+                for (int i = kPer - 1; i >= 0; --i) {
+                    F l = L::get(word(ds, i));
+                    if (kSpecial && at(dead, i)) l = L::all(0.f);
+                    if (kSpecial && at(end, i)) l = L::add(l, state(a.dfinal, i));
+                    if (kSpecial && at(end | dead, i)) bwd.A = L::all(kReset), bwd.H = L::mul(av[i], l);
+                    else {
+                        bwd.H = L::mul(av[i], L::add(l, bwd.H));
+                        if (!kSpecial || !(L::first(bwd.A) < 0.f)) bwd.A = L::mul(bwd.A, av[i]);
+                    }
+                }
+            }
+        };
+        if (have) {
+            if (kBack && in) before = L::load(a.kept + static_cast<int64_t>(tile) * a.d + ch);
+            scan_wait(&sm.full[s], phase, lost, a.status);
+            const int sh = warp % 2 * kPer;
+            begin = seqs.begin[warp / 2] >> sh & 0xffffu;
+            end = seqs.end[warp / 2] >> sh & 0xffffu;
+            dead = seqs.dead[warp / 2] >> sh & 0xffffu;
+            if (begin | end | dead) gates(std::true_type());
+            else gates(std::false_type());
         }
-        empty_seqs<L>(a, rank, geo.cluster, ch0, kBack ? a.dfinal : a.state, kBack ? a.dstate : a.final);
-        if (blockIdx.x == 0) check_offsets(a);
-        // copies in flight have to land before the CTA gives up its memory (all have, unless a wait gave up)
-        for (int i = 0; i < min(issued, geo.stages); ++i) {
-            if (--s < 0) s = geo.stages - 1, phase ^= 1;
-            const long long t0 = clock64();
-            while (!mbar_try_wait(smem_u32(&sm.full[s]), phase) && clock64() - t0 < kScanWaitCycles / 10) {}
+        constexpr int kLaneStep = L::kCh * 8;
+        save_step(steps + warp * kWarpStepBytes + lane * kLaneStep, fwd);
+        if (kBack) save_step(steps_b + warp * kWarpStepBytes + lane * kLaneStep, bwd);
+        __syncthreads();
+        uint8_t *theirs = tile_steps + par * geo.cluster * kStepBytes;
+        {
+            constexpr int kLanes = 8 / L::kCh;   // that take a channel
+            const int at = threadIdx.x / kLanes * 8;
+            Step<Lane<float>> all = join_warps<L::kCh, false>(steps + at, kWarpStepBytes, lane);
+            if (kBack) all = join_warps<L::kCh, true>(steps_b + at, kWarpStepBytes, lane);
+            if (geo.cluster > 1) {
+                uint64_t *bar = &sm.steps[par];
+                if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, geo.cluster * 32 * kLaneStep);
+                for (int to = lane % kLanes; to < geo.cluster; to += kLanes)
+                    store_remote(map_to_cta(smem_u32(theirs + rank * kStepBytes + at), to), all.A, all.H, map_to_cta(smem_u32(bar), to));
+            } else if (lane % kLanes == 0) {
+                save_step<Lane<float>>(theirs + at, all);
+            }
         }
-    } else {
-        uint8_t *warp_steps = ring + geo.stages * kStageBytes, *tile_steps = warp_steps + (kBack ? 4 : 2) * kWarpStepBytes;
-        const int ch = ch0 + lane * L::kCh;
-        const bool in = ch < a.d;
-        F carry = L::all(0.f);   // the state before the group, or (backward) the gradient that comes from behind it
-        for (int group = 0; group < geo.groups; ++group) {
-            const int tile = kBack ? geo.tiles - 1 - (group * geo.cluster + rank) : group * geo.cluster + rank, par = group & 1;
-            const bool have = tile >= 0 && tile < geo.tiles;
-            const uint8_t *xs = ring + s * kStageBytes + warp * kPer * 128 + lane * 4, *gs = xs + kTileBytes, *ds = gs + kTileBytes;
-            auto word = [](const uint8_t *p, int i) { return *reinterpret_cast<const uint32_t *>(p + i * 128); };
-            const int *seq = sm.seqs[s].seq + warp * kPer;
-            uint32_t begin = 0, end = 0, dead = 0;
-            F av[kPer], v[kPer];   // gates; what a token adds to the state, in the backward later h_{t-1} - x_t
-            Step<L> fwd{L::all(1.f), L::all(0.f)}, bwd{L::all(1.f), L::all(0.f)};
-            F before = L::all(0.f);   // (backward) the state before the tile
-            auto state = [&](const float *p, int i) {
-                return p && in ? L::load(p + static_cast<int64_t>(seq[i]) * a.d + ch) : L::all(0.f);
-            };
-            // what to do at a token, for a warp with and without the ends of sequences among its tokens
-            auto at = [](uint32_t bits, int i) { return (bits >> i & 1u) != 0; };
-            auto gates = [&](auto special) {
+        __syncthreads();
+        if (kBack && have) {   // h again, from the state before the tile
+            F h = apply(load_step<L>(steps + warp * kWarpStepBytes + lane * kLaneStep), before);
+            auto again = [&](auto special) {
                 constexpr bool kSpecial = decltype(special)::value;
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
-                    F rest;
-                    gate<L>(L::get(word(gs, i)), av[i], rest);
-                    v[i] = L::mul(rest, L::get(word(xs, i)));
-                    if (kSpecial && at(dead, i)) av[i] = v[i] = L::all(0.f);
-                    if (kSpecial && at(begin, i)) v[i] = L::fma(av[i], state(a.state, i), v[i]);
-                    if (kSpecial && at(begin | dead, i)) fwd.A = L::all(kReset), fwd.H = v[i];
-                    else {
-                        fwd.H = L::fma(av[i], fwd.H, v[i]);
-                        if (!kSpecial || !(L::first(fwd.A) < 0.f)) fwd.A = L::mul(fwd.A, av[i]);
-                    }
-                }
-                if constexpr (kBack) {
-#pragma unroll
-                    for (int i = kPer - 1; i >= 0; --i) {
-                        F l = L::get(word(ds, i));
-                        if (kSpecial && at(dead, i)) l = L::all(0.f);
-                        if (kSpecial && at(end, i)) l = L::add(l, state(a.dfinal, i));
-                        if (kSpecial && at(end | dead, i)) bwd.A = L::all(kReset), bwd.H = L::mul(av[i], l);
-                        else {
-                            bwd.H = L::mul(av[i], L::add(l, bwd.H));
-                            if (!kSpecial || !(L::first(bwd.A) < 0.f)) bwd.A = L::mul(bwd.A, av[i]);
-                        }
-                    }
+                    const F from = kSpecial && at(begin, i) ? state(a.state, i) : h;
+                    h = kSpecial && at(begin | dead, i) ? v[i] : L::fma(av[i], h, v[i]);
+                    v[i] = L::fma(L::get(word(xs, i)), L::all(-1.f), from);
                 }
             };
-            if (have) {
-                if (kBack && in) before = L::load(a.kept + static_cast<int64_t>(tile) * a.d + ch);
-                scan_wait(&sm.full[s], phase, lost, a.status);
-                const int sh = warp % 2 * kPer;
-                begin = sm.seqs[s].begin[warp / 2] >> sh & 0xffffu;
-                end = sm.seqs[s].end[warp / 2] >> sh & 0xffffu;
-                dead = sm.seqs[s].dead[warp / 2] >> sh & 0xffffu;
-                if (begin | end | dead) gates(std::true_type());
-                else gates(std::false_type());
-            }
-            uint8_t *mine = warp_steps + par * kWarpStepBytes, *mine_b = mine + 2 * kWarpStepBytes;
-            auto warp_step = [&](const uint8_t *p, int w) { return unpack_step<L>(*reinterpret_cast<const uint4 *>(p + (w * 32 + lane) * 16)); };
-            *reinterpret_cast<uint4 *>(mine + (warp * 32 + lane) * 16) = pack_step(fwd);
-            if (kBack) *reinterpret_cast<uint4 *>(mine_b + (warp * 32 + lane) * 16) = pack_step(bwd);
-            asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-            uint8_t *theirs = tile_steps + par * geo.cluster * kTileStepBytes;
-            if (geo.cluster > 1) {
-                if (threadIdx.x == 0) mbar_arrive_expect_tx(&sm.steps[par], geo.cluster * kTileStepBytes);
-                if (warp < geo.cluster) {
-                    Step<L> all = kBack ? warp_step(mine_b, kWarps - 1) : warp_step(mine, 0);
+            if (begin | dead) again(std::true_type());
+            else again(std::false_type());
+        }
+        // (forward: every warp has its gates and is through with the group before)
+        if (!kBack && asks && !lost) ask();
+        F c = carry;
+        if (geo.cluster > 1) scan_wait(&sm.steps[par], group >> 1 & 1, lost, a.status);
+        for (int r = 0; r < geo.cluster; ++r) {
+            if (r == rank) c = carry;
+            carry = apply(load_step<L>(theirs + r * kStepBytes + lane * kLaneStep), carry);
+        }
+        if (!kBack && a.kept && have && warp == 0 && in) L::save(a.kept + static_cast<int64_t>(tile) * a.d + ch, c);
+        c = apply(load_step<L>((kBack ? steps_b : steps) + warp * kWarpStepBytes + lane * kLaneStep), c);
+        if (!have) continue;
+        const int t0 = tile * kTok + warp * kPer;
+        auto rows = [&](void *p, int64_t ld) { return static_cast<uint8_t *>(p) + t0 * ld * sizeof(T); };
+        auto put = [&](uint8_t *p, F value) { *reinterpret_cast<uint32_t *>(p + lane_bytes) = L::put(value); };
+        auto out = [&](auto special) {
+            constexpr bool kSpecial = decltype(special)::value;
+            if (!kBack) {
+                uint8_t *h = rows(a.h, a.ld_h);
 #pragma unroll
-                    for (int w = 1; w < kWarps; ++w) all = then(all, kBack ? warp_step(mine_b, kWarps - 1 - w) : warp_step(mine, w));
-                    for (int to = warp; to < geo.cluster; to += kWarps)
-                        store_remote(map_to_cta(smem_u32(theirs + rank * kTileStepBytes + lane * 16), to), pack_step(all),
-                                     map_to_cta(smem_u32(&sm.steps[par]), to));
+                for (int i = 0; i < kPer; ++i, h += a.ld_h * sizeof(T)) {
+                    c = kSpecial && at(begin | dead, i) ? v[i] : L::fma(av[i], c, v[i]);
+                    if (!kSpecial || t0 + i < a.T) put(h, c);
+                    if (kSpecial && at(end, i) && a.final) L::save(a.final + static_cast<int64_t>(seq[i]) * a.d + ch, c);
+                }
+            } else {
+                uint8_t *x = rows(a.dx, a.ld_dx) + (kPer - 1) * a.ld_dx * sizeof(T), *g = rows(a.dg, a.ld_dg) + (kPer - 1) * a.ld_dg * sizeof(T);
+#pragma unroll
+                for (int i = kPer - 1; i >= 0; --i, x -= a.ld_dx * sizeof(T), g -= a.ld_dg * sizeof(T)) {
+                    const F rest = L::mul(gate_exp<L>(L::get(word(gs, i))), av[i]);
+                    F l = L::get(word(ds, i));
+                    l = L::add(l, kSpecial && at(end, i) ? state(a.dfinal, i) : c);
+                    F dx = L::mul(rest, l), dg = L::mul(L::mul(l, v[i]), L::mul(av[i], rest));
+                    c = L::mul(av[i], l);
+                    if (kSpecial && at(dead, i)) dx = dg = c = L::all(0.f);
+                    if (!kSpecial || t0 + i < a.T) put(x, dx), put(g, dg);
+                    if (kSpecial && at(begin, i) && a.dstate) L::save(a.dstate + static_cast<int64_t>(seq[i]) * a.d + ch, c);
                 }
             }
-            if (kBack && have) {   // h again, from the state before the tile
-                F h = before;
-                for (int w = 0; w < warp; ++w) h = apply(warp_step(mine, w), h);
-                auto again = [&](auto special) {
-                    constexpr bool kSpecial = decltype(special)::value;
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) {
-                        const F minus_x = L::mul(L::get(word(xs, i)), L::all(-1.f));
-                        const bool first = kSpecial && at(begin, i);
-                        const F next = kSpecial && at(begin | dead, i) ? v[i] : L::fma(av[i], h, v[i]);
-                        v[i] = L::add(first ? state(a.state, i) : h, minus_x);
-                        h = next;
-                    }
-                };
-                if (begin | dead) again(std::true_type());
-                else again(std::false_type());
-            }
-            F c = carry;
-            if (geo.cluster > 1) {
-                scan_wait(&sm.steps[par], group >> 1 & 1, lost, a.status);
-                for (int r = 0; r < geo.cluster; ++r) {
-                    if (r == rank) c = carry;
-                    carry = apply(unpack_step<L>(*reinterpret_cast<const uint4 *>(theirs + r * kTileStepBytes + lane * 16)), carry);
-                }
-            }
-            if (!kBack && a.kept && have && warp == 0 && in) L::save(a.kept + static_cast<int64_t>(tile) * a.d + ch, c);
-            if (kBack)
-                for (int w = kWarps - 1; w > warp; --w) c = apply(warp_step(mine_b, w), c);
-            else
-                for (int w = 0; w < warp; ++w) c = apply(warp_step(mine, w), c);
-            if (geo.cluster == 1) {
-                carry = c;
-                if (kBack)
-                    for (int w = warp; w >= 0; --w) carry = apply(warp_step(mine_b, w), carry);
-                else
-                    for (int w = warp; w < kWarps; ++w) carry = apply(warp_step(mine, w), carry);
-            }
-            if (!have) continue;
-            const int t0 = tile * kTok + warp * kPer;
-            auto put = [&](void *p, int64_t ld, int i, F value) {
-                *reinterpret_cast<uint32_t *>(static_cast<T *>(p) + (t0 + i) * ld + ch) = L::put(value);
-            };
-            auto out = [&](auto special) {
-                constexpr bool kSpecial = decltype(special)::value;
-                if (!kBack) {
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) {
-                        c = kSpecial && at(begin | dead, i) ? v[i] : L::fma(av[i], c, v[i]);
-                        if (in && (!kSpecial || t0 + i < a.T)) put(a.h, a.ld_h, i, c);
-                        if (kSpecial && at(end, i) && a.final && in) L::save(a.final + static_cast<int64_t>(seq[i]) * a.d + ch, c);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = kPer - 1; i >= 0; --i) {
-                        const F rest = L::mul(gate_exp<L>(L::get(word(gs, i))), av[i]);
-                        F l = L::get(word(ds, i));
-                        l = L::add(l, kSpecial && at(end, i) ? state(a.dfinal, i) : c);
-                        F dx = L::mul(rest, l), dg = L::mul(L::mul(l, v[i]), L::mul(av[i], rest));
-                        c = L::mul(av[i], l);
-                        if (kSpecial && at(dead, i)) dx = dg = c = L::all(0.f);
-                        if (in && (!kSpecial || t0 + i < a.T)) put(a.dx, a.ld_dx, i, dx), put(a.dg, a.ld_dg, i, dg);
-                        if (kSpecial && at(begin, i) && a.dstate && in) L::save(a.dstate + static_cast<int64_t>(seq[i]) * a.d + ch, c);
-                    }
-                }
-            };
+        };
+        if (in) {
             if (begin | end | dead) out(std::true_type());
             else out(std::false_type());
+        }
+        if (kBack) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.empty[s]);
-            if (++s == geo.stages) s = 0, phase ^= 1;
+            if (lane == 0) mbar_arrive(&sm.done[s]);
+            if (asks) {
+                scan_wait(&sm.done[s], phase, lost, a.status);
+                lost = __any_sync(0xffffffffu, lost);
+                if (!lost) ask();
+            }
+        }
+        if (++s == geo.stages) s = 0, phase ^= 1;
+        if (++slot > geo.stages) slot = 0;
+    }
+    if (asks) {
+        empty_seqs<L>(a, rank, geo.cluster, ch0, kBack ? a.dfinal : a.state, kBack ? a.dstate : a.final);
+        if (blockIdx.x == 0) check_offsets(a);
+        // copies in flight have to land before the CTA gives up its memory (all have, unless a wait gave up)
+        for (int i = min(asked, geo.stages); lost && i > 0; --i) {
+            const int k = asked - i;   // the group asked for, in stage k % stages, in its (k / stages)th use
+            const long long t0 = clock64();
+            while (!mbar_try_wait(smem_u32(&sm.full[k % geo.stages]), k / geo.stages & 1) && clock64() - t0 < kScanWaitCycles / 10) {}
         }
     }
     if (geo.cluster > 1) cluster_sync_all();   // no CTA leaves while another may write to its shared memory
@@ -546,6 +626,7 @@ lce_status_t encode(CUtensorMap *m, const HostDev &dev, const void *p, bool bf16
 
 // Two CTAs an SM; the ring takes what the steps leave of half its shared memory.
 constexpr int kScanBytes = 112 * 1024;
+constexpr int kMostScanBytes = 200 * 1024;   // two stages and the steps of the largest cluster
 
 template <typename T, bool kBack>
 lce_status_t launch_scan(const ScanArgs &r, const HostDev &dev, cudaStream_t st) {
@@ -562,14 +643,19 @@ lce_status_t launch_scan(const ScanArgs &r, const HostDev &dev, cudaStream_t st)
     ScanGeo geo;
     geo.tiles = (r.T + kTok - 1) / kTok;
     const int slices = (r.d + kSlice - 1) / kSlice;
+    // as many CTAs as find room at once, two on an SM where their memory allows it
+    auto step_bytes = [](int cluster) { return (kBack ? 2 : 1) * kWarps * kWarpStepBytes + 2 * cluster * kStepBytes; };
+    auto stages = [&](int cluster) { return (kScanBytes - static_cast<int>(sizeof(ScanBars)) - step_bytes(cluster)) / kStageBytes; };
     geo.cluster = 1;
-    while (geo.cluster < kMaxCluster && geo.cluster < geo.tiles && slices * geo.cluster * 2 <= 2 * dev.sms) geo.cluster *= 2;
+    while (geo.cluster < kMaxCluster && geo.cluster < geo.tiles &&
+           slices * geo.cluster * 2 <= (stages(geo.cluster * 2) < 2 ? 1 : 2) * dev.sms)
+        geo.cluster *= 2;
     geo.groups = (geo.tiles + geo.cluster - 1) / geo.cluster;
-    const int steps = (kBack ? 4 : 2) * kWarpStepBytes + 2 * geo.cluster * kTileStepBytes;
-    geo.stages = std::max(2, std::min(kMaxStages, (kScanBytes - static_cast<int>(sizeof(ScanBars)) - steps) / kStageBytes));
+    const int steps = step_bytes(geo.cluster);
+    geo.stages = std::max(2, std::min(kMaxStages, stages(geo.cluster)));
     const int smem = geo.stages * kStageBytes + steps;
     constexpr auto kernel = k_scan<T, kBack>;
-    if ((s = host_smem<kernel>(dev, 2 * kScanBytes)) != LCE_OK) return s;
+    if ((s = host_smem<kernel>(dev, kMostScanBytes)) != LCE_OK) return s;
     if (geo.cluster > 8) {
         static std::atomic<uint64_t> done{0};
         const uint64_t bit = uint64_t(1) << dev.index;
