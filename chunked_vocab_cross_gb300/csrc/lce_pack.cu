@@ -6,6 +6,7 @@
 
 #include "e4m3.cuh"
 #include "lce_host.h"
+#include "lce_wgrad.cuh"
 #include "row_ring.cuh"
 
 using namespace lce;
@@ -55,45 +56,6 @@ __global__ void __launch_bounds__(256) k_unpack8(const PackArgs a) {
     }
 }
 
-struct WgradArgs {
-    const void *dy;
-    const uint8_t *codes;
-    const int8_t *exps;
-    void *dw;
-    int64_t ld_dy, ld_codes, ld_exps;
-    int T, n, k;
-};
-
-// 64 x 64 outputs a block, 4 x 4 a thread
-template <typename T, typename O>
-__global__ void __launch_bounds__(256) k_wgrad_simple(const WgradArgs a) {
-    __shared__ float sy[16][64], sx[16][64];
-    const int n0 = blockIdx.y * 64, k0 = blockIdx.x * 64;
-    const int ti = threadIdx.x / 16 * 4, tj = threadIdx.x % 16 * 4;
-    float acc[4][4] = {};
-    for (int t0 = 0; t0 < a.T; t0 += 16) {
-        for (int i = threadIdx.x; i < 16 * 64; i += 256) {
-            const int t = t0 + i / 64, c = i % 64;
-            sy[i / 64][c] = t < a.T && n0 + c < a.n ? static_cast<float>(static_cast<const T *>(a.dy)[t * a.ld_dy + n0 + c]) : 0.f;
-            float v = 0.f, u;
-            if (t < a.T && k0 + c < a.k) {
-                from_codes(a.codes[t * a.ld_codes + k0 + c], v, u);
-                v *= unpack_scale(a.exps[(k0 + c) / kPackBlock * a.ld_exps + t]);
-            }
-            sx[i / 64][c] = v;
-        }
-        __syncthreads();
-        for (int t = 0; t < 16; ++t)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sy[t][ti + i], sx[t][tj + j], acc[i][j]);
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j)
-            if (n0 + ti + i < a.n && k0 + tj + j < a.k)
-                static_cast<O *>(a.dw)[static_cast<int64_t>(n0 + ti + i) * a.k + k0 + tj + j] = static_cast<O>(acc[i][j]);
-}
-
 lce_status_t check_plain(lce_dtype_t dtype, const void *x, int64_t ld, int64_t N, int64_t d, const void *codes, int64_t ld_codes,
                          const void *exps, int64_t ld_exps, bool out) {
     if (dtype != LCE_BF16 && dtype != LCE_FP32) return LCE_ERR_DTYPE;
@@ -114,8 +76,89 @@ lce_status_t check_wgrad(const lce_wgrad_t *a) {
     if (!a) return LCE_ERR_NULL;
     if (a->dtype != LCE_BF16 && a->dtype != LCE_FP32) return LCE_ERR_DTYPE;
     if (a->dw_dtype != LCE_FP32 && !(a->dw_dtype == LCE_BF16 && a->dtype == LCE_BF16)) return LCE_ERR_DTYPE;
-    if (a->T < 0 || a->T >= (int64_t(1) << 30) || a->n < 8 || a->k < 8 || a->n >= (1 << 24) || a->k >= (1 << 24)) return LCE_ERR_SHAPE;
+    if (a->T < 0 || a->T >= (int64_t(1) << 30) || a->n < 8 || a->k < 8 || a->n >= (1 << 24) || a->k >= (1 << 24) ||
+        a->n * a->k >= (int64_t(1) << 40))
+        return LCE_ERR_SHAPE;
     return a->n % 8 || a->k % 8 ? LCE_ERR_ALIGN : LCE_OK;
+}
+
+// SMs that the rule below reckons with: those of the one part this library runs on, as a constant, since the workspace
+// function answers from the sizes alone, without a device.
+constexpr int kSms = 152;
+
+// Splits of the tokens where there are few tiles. The times compared are in steps of 64 tokens of a unit (0.27 us): a unit
+// costs 10 more for its start and output, and the join 8 and its bytes.
+int splits(const lce_wgrad_t *a) {
+    const int64_t tiles = (a->n + kWgTile - 1) / kWgTile * ((a->k + kWgTile - 1) / kWgTile), parts = a->dtype == LCE_FP32 ? 3 : 1,
+                  steps = (a->T + kWgK - 1) / kWgK;
+    auto time = [&](int64_t s) {
+        const double waves = static_cast<double>((tiles * s + kSms / 2 - 1) / (kSms / 2)), sums = static_cast<double>(a->n) * a->k * 4;
+        return waves * (static_cast<double>((steps + s - 1) / s * parts) + 10) + (s > 1 ? 8 + (2 * s + 1) * sums / 1.5e6 : 0);
+    };
+    int64_t best = 1;
+    for (int64_t s = 2; s <= steps && tiles * s <= kSms; ++s)
+        if (time(s) < 0.95 * time(best)) best = s;
+    const int64_t per = (steps + best - 1) / best;   // no split without steps
+    return static_cast<int>(steps > 0 ? (steps + per - 1) / per : 1);
+}
+size_t split_bytes(const lce_wgrad_t *a, int s) { return s > 1 ? static_cast<size_t>(s) * a->n * a->k * sizeof(float) : 0; }
+int64_t part_columns(const lce_wgrad_t *a) { return (a->n + 63) / 64 * 64; }
+size_t part_bytes(const lce_wgrad_t *a) { return a->dtype == LCE_FP32 ? static_cast<size_t>(a->T) * part_columns(a) * 6 : 0; }
+
+bool encode_dy(CUtensorMap *m, const HostDev &dev, const void *p, int64_t T, int64_t n, int64_t ld, bool whole) {
+    const cuuint64_t two[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(T)}, row[2] = {static_cast<cuuint64_t>(ld) * 2, 128};
+    const cuuint64_t three[3] = {64, static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(n / 64)};
+    const cuuint32_t box[3] = {64, kWgK, 2}, es[3] = {1, 1, 1};
+    return dev.encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, whole ? 3 : 2, const_cast<void *>(p), whole ? three : two, row, box, es,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_codes(CUtensorMap *m, const HostDev &dev, const void *p, int64_t T, int64_t k, int64_t ld) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(T)}, row[1] = {static_cast<cuuint64_t>(ld)};
+    const cuuint32_t box[2] = {kWgHalf, kWgK}, es[2] = {1, 1};
+    return dev.encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, row, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename O>
+lce_status_t wgrad(const lce_wgrad_t *a, const HostDev &dev, uint8_t *scratch, cudaStream_t st) {
+    WgMaps maps{};
+    WgArgs r{};
+    const int64_t ld = a->ld_dy ? a->ld_dy : a->n;
+    r.exps = a->exps, r.ld_exps = a->ld_exps, r.T = static_cast<int>(a->T), r.n = static_cast<int>(a->n), r.k = static_cast<int>(a->k);
+    r.mt = (r.n + kWgTile - 1) / kWgTile, r.nt = (r.k + kWgTile - 1) / kWgTile, r.steps = (r.T + kWgK - 1) / kWgK;
+    r.splits = splits(a), r.per = (r.steps + r.splits - 1) / r.splits, r.status = dev.status;
+    if (!encode_codes(&maps.codes, dev, a->codes, a->T, a->k, a->ld_codes)) return LCE_ERR_SHAPE;
+    if (a->dtype == LCE_FP32) {
+        const int64_t wide = part_columns(a), size = a->T * wide;
+        auto *parts = reinterpret_cast<__nv_bfloat16 *>(scratch + split_bytes(a, r.splits));
+        r.parts = 3, r.whole = 1;
+        for (int p = 0; p < 3; ++p)
+            if (!encode_dy(&maps.dy[p], dev, parts + p * size, a->T, wide, wide, true)) return LCE_ERR_SHAPE;
+        k_wgrad_parts<<<static_cast<unsigned>((size / 4 + 255) / 256), 256, 0, st>>>(static_cast<const float *>(a->dy), ld, r.T, r.n,
+                                                                                   static_cast<int>(wide), parts);
+        const lce_status_t s = host_launched();
+        if (s != LCE_OK) return s;
+    } else {
+        r.parts = 1, r.whole = a->n % 64 == 0;
+        if (!encode_dy(&maps.dy[0], dev, a->dy, a->T, a->n, ld, r.whole != 0)) return LCE_ERR_SHAPE;
+    }
+    const int units = r.mt * r.nt * r.splits, grid = 2 * std::min(units, dev.sms / 2);
+    if (r.splits == 1) {
+        r.out = a->dw;
+        const lce_status_t s = host_smem<k_wgrad<O>>(dev, kWgSmem);
+        if (s != LCE_OK) return s;
+        k_wgrad<O><<<grid, kWgThreads, kWgSmem, st>>>(maps, r);
+        return host_launched();
+    }
+    r.out = scratch;
+    lce_status_t s = host_smem<k_wgrad<float>>(dev, kWgSmem);
+    if (s != LCE_OK) return s;
+    k_wgrad<float><<<grid, kWgThreads, kWgSmem, st>>>(maps, r);
+    if ((s = host_launched()) != LCE_OK) return s;
+    const int64_t count = a->n * a->k;
+    return host_launch_early(k_wgrad_join<O>, dim3(static_cast<unsigned>((count / 4 + 255) / 256)), 256, 0, st,
+                             reinterpret_cast<const float *>(scratch), r.splits, count, static_cast<O *>(a->dw));
 }
 
 }  // namespace
@@ -154,8 +197,7 @@ lce_status_t lce_unpack8(lce_dtype_t dtype, const uint8_t *codes, int64_t ld_cod
 }
 
 size_t lce_packed_wgrad_workspace_size(const lce_wgrad_t *a) {
-    if (check_wgrad(a) != LCE_OK) return 0;
-    return 0;
+    return check_wgrad(a) == LCE_OK ? split_bytes(a, splits(a)) + part_bytes(a) : 0;
 }
 
 lce_status_t lce_packed_wgrad(const lce_wgrad_t *a) {
@@ -172,13 +214,12 @@ lce_status_t lce_packed_wgrad(const lce_wgrad_t *a) {
     HostDev dev;
     if ((s = host_device(&dev)) != LCE_OK) return s;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
-    const WgradArgs r{a->dy, a->codes, a->exps, a->dw, a->ld_dy ? a->ld_dy : a->n, a->ld_codes, a->ld_exps, static_cast<int>(a->T),
-                      static_cast<int>(a->n), static_cast<int>(a->k)};
-    const dim3 grid(static_cast<unsigned>((a->k + 63) / 64), static_cast<unsigned>((a->n + 63) / 64));
-    if (a->dtype == LCE_FP32) k_wgrad_simple<float, float><<<grid, 256, 0, st>>>(r);
-    else if (a->dw_dtype == LCE_FP32) k_wgrad_simple<__nv_bfloat16, float><<<grid, 256, 0, st>>>(r);
-    else k_wgrad_simple<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, st>>>(r);
-    return host_launched();
+    if (a->T == 0)
+        return host_cuda(cudaMemsetAsync(a->dw, 0, static_cast<size_t>(a->n) * a->k * (a->dw_dtype == LCE_BF16 ? 2 : 4), st));
+    HostScratch scratch(st);
+    uint8_t *base = nullptr;
+    if ((s = scratch.get(a->workspace, a->workspace_bytes, lce_packed_wgrad_workspace_size(a), &base)) != LCE_OK) return s;
+    return a->dw_dtype == LCE_BF16 ? wgrad<__nv_bfloat16>(a, dev, base, st) : wgrad<float>(a, dev, base, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,323 @@
+// The gradient of a weight from packed activations, dw = dy^T x, on the tensor
+// cores: x is widened from its codes on the way.
+//
+// CTA pairs (clusters of two) take 256 x 256 tiles of dw, K being the tokens, 64
+// at a time. Both operands lie token-major in memory, which is MN-major for this
+// product. dy comes by TMA straight into the layout the MMA reads; the codes of
+// the CTA's 128 channels, and their one exponent a token (128 channels are a
+// block of the format), come by TMA into a stage of their own, from which eight
+// warps write the bf16 operand: a code's bits, moved to where a bf16 has them, are
+// its value times 2^-120, and two products with powers of two bring it to scale
+// without a rounding. Of the 512 cycles that the MMAs of 64 tokens run for, the
+// widening takes about 250 issue slots of each scheduler, beside them. The other
+// warps: 0 asks for tiles, 1 issues the MMAs (of both CTAs, in the even one), 2 to
+// 5 bring a finished accumulator to memory while the next one fills.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "e4m3.cuh"
+#include "lce.h"
+#include "tc_ptx.cuh"
+
+namespace lce {
+
+constexpr int kWgTile = 256, kWgHalf = 128, kWgK = 64;   // of a pair, of a CTA; tokens a step
+constexpr int kWgStages = 6, kWgWide = 4;                // stages of dy and codes; of widened codes
+constexpr int kWgConverters = 8, kWgThreads = (6 + kWgConverters) * 32;
+constexpr int kWgABytes = kWgHalf * kWgK * 2, kWgCodeBytes = kWgHalf * kWgK, kWgBlockBytes = kWgK * 128;
+constexpr int kWgSmem = kWgStages * (kWgABytes + kWgCodeBytes) + kWgWide * kWgABytes + 1024;
+constexpr long long kWgWaitCycles = 2000000000LL;   // ~1 s: far above any legitimate wait
+
+struct WgMaps {
+    CUtensorMap dy[3], codes;   // dy: itself, or the parts of an fp32 one
+};
+struct WgArgs {
+    const int8_t *exps;
+    int64_t ld_exps;
+    void *out;        // dw, or the fp32 sums of the splits, one after the other
+    int T, n, k;
+    int parts;        // of dy
+    int whole;        // n is a multiple of 64: dy has a three-dimensional map
+    int mt, nt;       // tiles along n and k
+    int steps, per;   // of 64 tokens; of a split
+    int splits;
+    int *status;
+};
+
+struct WgBars {
+    uint64_t full_a[kWgStages], full_c[kWgStages], empty[kWgStages], full_b[kWgWide], empty_b[kWgWide], full_t[2], empty_t[2], done;
+    uint32_t tmem;
+    volatile int abort;
+    __align__(16) int8_t exps[kWgStages][kWgK];
+};
+
+__device__ __forceinline__ bool wg_wait(uint64_t *bar, uint32_t parity, WgBars &sm, int *status) {
+    const uint32_t at = smem_u32(bar);
+    if (mbar_try_wait(at, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(at, parity)) {
+        if (sm.abort) return false;
+        if (clock64() - t0 > kWgWaitCycles) {
+            sm.abort = 1;
+            atomicOr(status, LCE_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void wg_drain(uint64_t *bar, uint32_t parity) {   // while leaving after a wait that gave up
+    const long long t0 = clock64();
+    while (!mbar_try_wait(smem_u32(bar), parity) && clock64() - t0 < kWgWaitCycles / 10) {}
+}
+
+// A unit of work: a tile and its range of steps. Tiles go by groups of eight
+// along n, so that those in flight together share what they read of both sides.
+struct WgUnit {
+    int m, n, split, k0, k1;
+};
+__device__ __forceinline__ WgUnit wg_unit(const WgArgs &a, int u) {
+    WgUnit r;
+    r.split = u % a.splits;
+    const int tile = u / a.splits, group = tile / (8 * a.nt), in = tile - group * 8 * a.nt, rows = min(8, a.mt - group * 8);
+    r.n = in / rows, r.m = group * 8 + in - r.n * rows;
+    r.k0 = r.split * a.per, r.k1 = min(a.steps, r.k0 + a.per);
+    return r;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Four codes to two bf16 pairs, times two powers of two (pairs as well).
+__device__ __forceinline__ uint2 wg_widen(uint32_t codes, uint32_t s1, uint32_t s2) {
+    const uint32_t lo = __byte_perm(codes, 0, 0x1404), hi = __byte_perm(codes, 0, 0x3424);   // a code in the high byte of a half
+    const uint32_t a = (lo >> 4 & 0x07f007f0u) | (lo & 0x80008000u), b = (hi >> 4 & 0x07f007f0u) | (hi & 0x80008000u);
+    return make_uint2(mul_bf16x2(mul_bf16x2(a, s1), s2), mul_bf16x2(mul_bf16x2(b, s1), s2));
+}
+
+template <typename O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgrad(const __grid_constant__ WgMaps maps, const WgArgs a) {
+    constexpr uint32_t kIdesc = idesc_f32acc(1, kWgTile, kWgTile, true, true);
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ WgBars sm;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *wide = smem + kWgStages * kWgABytes, *codes = wide + kWgWide * kWgABytes;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, units = a.mt * a.nt * a.splits;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWgStages; ++i) mbar_init(&sm.full_a[i], 1), mbar_init(&sm.full_c[i], 1), mbar_init(&sm.empty[i], 1);
+        for (int i = 0; i < kWgWide; ++i) mbar_init(&sm.full_b[i], 2 * kWgConverters / kWgWide), mbar_init(&sm.empty_b[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&sm.full_t[i], 1), mbar_init(&sm.empty_t[i], 8);   // four warps in each CTA
+        mbar_init(&sm.done, 1);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&sm.tmem, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t full_even = map_to_cta(smem_u32(sm.full_a), 0);
+            const int blocks = (a.k + kPackBlock - 1) / kPackBlock;
+            int it = 0;
+            for (int u = pair; ok && u < units; u += pairs) {
+                const WgUnit w = wg_unit(a, u);
+                const int n0 = w.m * kWgTile + rank * kWgHalf, k0 = w.n * kWgTile + rank * kWgHalf, block = k0 / kPackBlock;
+                for (int part = a.parts - 1; ok && part >= 0; --part)   // the small parts first
+                    for (int step = w.k0; step < w.k1; ++step, ++it) {
+                        const int st = it % kWgStages, t0 = step * kWgK;
+                        if (!(ok = wg_wait(&sm.empty[st], it / kWgStages & 1 ^ 1, sm, a.status))) break;
+                        if (rank == 0) mbar_arrive_expect_tx(&sm.full_a[st], 2 * kWgABytes);
+                        uint8_t *dst = smem + st * kWgABytes;
+                        if (a.whole) tma_load_3d_pair(dst, &maps.dy[part], full_even + st * 8, 0, t0, n0 / 64);
+                        else {
+                            tma_load_2d_pair(dst, &maps.dy[part], full_even + st * 8, n0, t0);
+                            tma_load_2d_pair(dst + kWgBlockBytes, &maps.dy[part], full_even + st * 8, n0 + 64, t0);
+                        }
+                        const uint32_t bytes = block < blocks ? min(kWgK, (a.T - t0 + 15) & ~15) : 0;   // rows of exps are of whole 16 bytes
+                        mbar_arrive_expect_tx(&sm.full_c[st], kWgCodeBytes + bytes);
+                        tma_load_2d(codes + st * kWgCodeBytes, &maps.codes, &sm.full_c[st], k0, t0);
+                        if (bytes) bulk_load(sm.exps[st], a.exps + block * a.ld_exps + t0, bytes, &sm.full_c[st]);
+                    }
+            }
+            // copies in flight have to land before the CTA leaves (in the normal course all have)
+            for (int i = max(0, it - kWgStages); !ok && i < it; ++i) {
+                wg_drain(&sm.full_c[i % kWgStages], i / kWgStages & 1);
+                if (rank == 0) wg_drain(&sm.full_a[i % kWgStages], i / kWgStages & 1);
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const bool issue = elect_one();
+            int it = 0, tile = 0;
+            for (int u = pair; ok && u < units; u += pairs, ++tile) {
+                const WgUnit w = wg_unit(a, u);
+                const int acc = tile & 1, steps = (w.k1 - w.k0) * a.parts;
+                if (!(ok = wg_wait(&sm.empty_t[acc], tile >> 1 & 1 ^ 1, sm, a.status))) break;
+                tc_fence_after();
+                for (int i = 0; i < steps; ++i, ++it) {
+                    const int st = it % kWgStages, sb = it % kWgWide;
+                    ok = wg_wait(&sm.full_a[st], it / kWgStages & 1, sm, a.status) && wg_wait(&sm.full_b[sb], it / kWgWide & 1, sm, a.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (issue) {
+                        const uint32_t pa = smem_u32(smem + st * kWgABytes), pb = smem_u32(wide + sb * kWgABytes);
+#pragma unroll
+                        for (int kk = 0; kk < kWgK / 16; ++kk)
+                            umma_f16_pair(tmem + acc * kWgTile, sdesc_sw128(pa + kk * 2048, kWgBlockBytes, 1024),
+                                          sdesc_sw128(pb + kk * 2048, kWgBlockBytes, 1024), kIdesc, (i | kk) != 0);
+                        umma_commit_pair_mc(&sm.empty[st], 3);
+                        umma_commit_pair_mc(&sm.empty_b[sb], 3);
+                    }
+                    __syncwarp();
+                }
+                if (ok && issue) umma_commit_pair_mc(&sm.full_t[acc], 3);
+            }
+            if (issue) {
+                umma_commit_pair_mc(&sm.done, 1);
+                wg_drain(&sm.done, 0);
+            }
+        }
+    } else if (warp < 6) {
+        const uint32_t empty_even = map_to_cta(smem_u32(sm.empty_t), 0);
+        const int quarter = warp & 3;
+        int tile = 0;
+        for (int u = pair; ok && u < units; u += pairs, ++tile) {
+            const WgUnit w = wg_unit(a, u);
+            const int acc = tile & 1, row = w.m * kWgTile + rank * kWgHalf + quarter * 32 + lane, col0 = w.n * kWgTile;
+            ok = __all_sync(0xffffffffu, wg_wait(&sm.full_t[acc], tile >> 1 & 1, sm, a.status));
+            if (!ok) break;
+            tc_fence_after();
+            O *out = static_cast<O *>(a.out) + (static_cast<int64_t>(w.split) * a.n + row) * a.k + col0;
+            for (int c = 0; c < kWgTile && col0 + c < a.k; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(tmem + acc * kWgTile + c + (static_cast<uint32_t>(quarter * 32) << 16), v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    if (row >= a.n || col0 + c + i >= a.k) continue;   // (k is a multiple of 8)
+                    if constexpr (sizeof(O) == 2) {
+                        uint4 x;
+                        uint32_t *p = &x.x;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
+                            p[j] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        *reinterpret_cast<uint4 *>(out + c + i) = x;
+                    } else {
+                        *reinterpret_cast<uint4 *>(out + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        *reinterpret_cast<uint4 *>(out + c + i + 4) = make_uint4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
+                    }
+                }
+                __syncwarp();   // the next load is the whole warp's
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(empty_even + acc * 8);
+        }
+    } else {
+        // Every stage has its warps: they have the time of four steps for one, which hides the waits, the fence and the way to
+        // the even CTA. 16 codes a lane and turn, 8 lanes a token, half of the stage's tokens a warp.
+        constexpr int kEach = kWgConverters / kWgWide, kTurns = kWgK / kEach / 4;
+        const uint32_t full_even = map_to_cta(smem_u32(sm.full_b), 0);
+        const int sb = (warp - 6) / kEach, row = (warp - 6) % kEach * (kWgK / kEach) + lane / 8, chunk = lane & 7;
+        // the token's line, its 16-byte pieces in the order of the 128-byte swizzle; the lanes of one half of the channels
+        // write their second piece first, so that eight lanes together use all banks
+        const int piece = (chunk & 3) * 2, swap = chunk >> 2;
+        uint8_t *to = wide + sb * kWgABytes + swap * kWgBlockBytes;
+        int it = 0;
+        for (int u = pair; ok && u < units; u += pairs) {
+            const WgUnit w = wg_unit(a, u);
+            for (int part = 0; ok && part < a.parts; ++part)
+                for (int step = w.k0; step < w.k1; ++step, ++it) {
+                    if (it % kWgWide != sb) continue;
+                    const int st = it % kWgStages;
+                    ok = wg_wait(&sm.full_c[st], it / kWgStages & 1, sm, a.status) && wg_wait(&sm.empty_b[sb], it / kWgWide & 1 ^ 1, sm, a.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint8_t *from = codes + st * kWgCodeBytes + chunk * 16;
+#pragma unroll
+                    for (int j = 0; j < kTurns; ++j) {
+                        const int r = row + j * 4;
+                        const uint4 c = *reinterpret_cast<const uint4 *>(from + r * 128);
+                        const int e = sm.exps[st][r], s = 120 + e, half = s >> 1;
+                        uint32_t s1 = static_cast<uint32_t>(127 + half) << 7, s2 = static_cast<uint32_t>(127 + s - half) << 7;
+                        if (e == kPackNaN) s1 = 0x7fffu;
+                        if (step * kWgK + r >= a.T) s1 = s2 = 0;   // behind the last token the exponents are whatever lies there
+                        s1 |= s1 << 16, s2 |= s2 << 16;
+                        const uint2 x0 = wg_widen(c.x, s1, s2), x1 = wg_widen(c.y, s1, s2), x2 = wg_widen(c.z, s1, s2), x3 = wg_widen(c.w, s1, s2);
+                        const uint4 first = make_uint4(x0.x, x0.y, x1.x, x1.y), second = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                        uint8_t *line = to + r * 128;
+                        *reinterpret_cast<uint4 *>(line + (((piece + swap) ^ (r & 7)) << 4)) = swap ? second : first;
+                        *reinterpret_cast<uint4 *>(line + (((piece + 1 - swap) ^ (r & 7)) << 4)) = swap ? first : second;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(full_even + sb * 8);
+                }
+        }
+    }
+    // Both CTAs stay until every arrive, commit and copy aimed at either has landed.
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// The splits' sums, in order
+template <typename O>
+__global__ void __launch_bounds__(256) k_wgrad_join(const float *part, int splits, int64_t count, O *out) {
+    griddep_wait();
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (at >= count) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < splits; ++i) {
+        const float4 v = *reinterpret_cast<const float4 *>(part + i * count + at);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    if constexpr (sizeof(O) == 2) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(s.x, s.y), y = __floats2bfloat162_rn(s.z, s.w);
+        *reinterpret_cast<uint2 *>(out + at) = make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+    } else {
+        *reinterpret_cast<float4 *>(out + at) = s;
+    }
+}
+
+// An fp32 dy in three bf16 parts whose sum it is, [part][T][wide], wide being n
+// rounded up to 64 and the columns between zero.
+__global__ void __launch_bounds__(256) k_wgrad_parts(const float *dy, int64_t ld, int T, int n, int wide, __nv_bfloat16 *out) {
+    const int per = wide / 4;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = id / per, size = static_cast<int64_t>(T) * wide;
+    const int col = static_cast<int>(id - row * per) * 4;
+    if (row >= T) return;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < n) v = *reinterpret_cast<const float4 *>(dy + row * ld + col);
+    float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+        __nv_bfloat16 h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = __float2bfloat16_rn(x[i]);
+            const float f = __bfloat162float(h[i]);
+            x[i] = fabsf(f) < INFINITY ? x[i] - f : 0.f;   // what is not finite is in the first part alone
+        }
+        *reinterpret_cast<uint2 *>(out + p * size + row * wide + col) = *reinterpret_cast<const uint2 *>(h);
+    }
+}
+
+}  // namespace lce
