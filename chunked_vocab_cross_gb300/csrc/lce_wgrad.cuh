@@ -5,16 +5,19 @@
 // at a time. Both operands lie token-major in memory, which is MN-major for this
 // product. dy comes by TMA straight into the layout the MMA reads; the codes of
 // the CTA's 128 channels, and their one exponent a token (128 channels are a
-// block of the format), come by TMA into a stage of their own, from which eight
-// warps write the bf16 operand: a code's bits, moved to where a bf16 has them, are
-// its value times 2^-120, and two products with powers of two bring it to scale
-// without a rounding. Of the 512 cycles that the MMAs of 64 tokens run for, the
-// widening takes about 250 issue slots of each scheduler, beside them. The other
-// warps: 0 asks for tiles, 1 issues the MMAs (of both CTAs, in the even one), 2 to
-// 5 bring a finished accumulator to memory while the next one fills.
+// block of the format), come by TMA into a ring of their own, from which sixteen
+// warps write the bf16 operand into a third ring. A code's bits, moved to where a
+// bf16 has them, are its value times 2^-120, and a product with a power of two
+// brings it to scale without a rounding (two products where the scale is above
+// 2^7). The rings are apart, since each has a latency of its own to hide. The
+// other warps: 0 asks for dy and 2 for codes, 1 issues the MMAs (of both CTAs, in
+// the even one), 4 to 7 bring a finished accumulator to memory while the next one
+// fills.
 #pragma once
 
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "e4m3.cuh"
 #include "lce.h"
@@ -23,10 +26,14 @@
 namespace lce {
 
 constexpr int kWgTile = 256, kWgHalf = 128, kWgK = 64;   // of a pair, of a CTA; tokens a step
-constexpr int kWgStages = 6, kWgWide = 4;                // stages of dy and codes; of widened codes
-constexpr int kWgConverters = 8, kWgThreads = (6 + kWgConverters) * 32;
+constexpr int kWgDy = 6, kWgCodes = 8, kWgWide = 4;      // stages of dy, of codes, of widened codes
+constexpr int kWgGroups = 4, kWgEach = 2;                // groups of warps that widen a step each in turn, and their warps
+constexpr int kWgFirst = 8, kWgThreads = (kWgFirst + kWgGroups * kWgEach) * 32;   // the first of these warps
 constexpr int kWgABytes = kWgHalf * kWgK * 2, kWgCodeBytes = kWgHalf * kWgK, kWgBlockBytes = kWgK * 128;
-constexpr int kWgSmem = kWgStages * (kWgABytes + kWgCodeBytes) + kWgWide * kWgABytes + 1024;
+constexpr int kWgSmem = kWgDy * kWgABytes + kWgCodes * kWgCodeBytes + kWgWide * kWgABytes + 1024;
+// A wait on a barrier tells phases apart by their parity alone: a step's stage of codes is always its group's own, and a
+// group is never two rounds of the widened stages ahead of the MMAs.
+static_assert(kWgCodes % kWgGroups == 0 && kWgWide >= kWgGroups, "");
 constexpr long long kWgWaitCycles = 2000000000LL;   // ~1 s: far above any legitimate wait
 
 struct WgMaps {
@@ -46,10 +53,10 @@ struct WgArgs {
 };
 
 struct WgBars {
-    uint64_t full_a[kWgStages], full_c[kWgStages], empty[kWgStages], full_b[kWgWide], empty_b[kWgWide], full_t[2], empty_t[2], done;
+    uint64_t full_a[kWgDy], empty_a[kWgDy], full_c[kWgCodes], empty_c[kWgCodes], full_b[kWgWide], empty_b[kWgWide], full_t[2], empty_t[2], done;
     uint32_t tmem;
     volatile int abort;
-    __align__(16) int8_t exps[kWgStages][kWgK];
+    __align__(16) int8_t exps[kWgCodes][kWgK];
 };
 
 __device__ __forceinline__ bool wg_wait(uint64_t *bar, uint32_t parity, WgBars &sm, int *status) {
@@ -85,16 +92,34 @@ __device__ __forceinline__ WgUnit wg_unit(const WgArgs &a, int u) {
     return r;
 }
 
+// Arrives on a barrier of either CTA. What the pair's MMAs read of it lies in the
+// arriving CTA's own shared memory and has been handed to the async proxy: no
+// release beyond the CTA is wanted (one of cluster scope takes 1800 cycles here).
+__device__ __forceinline__ void wg_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Four codes to two bf16 pairs, times two powers of two (pairs as well).
+// Two bytes of a word, extended by their signs to 16 bits
+template <uint32_t kSelect>
+__device__ __forceinline__ uint32_t wg_extend(uint32_t codes) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(codes), "n"(kSelect));
+    return r;
+}
+// Four codes to two bf16 pairs, times a power of two (a pair as well) or two:
+// a code is extended to 16 bits by its sign, moved up by 4 bits and cleared
+// between sign and exponent.
+template <bool kTwo>
 __device__ __forceinline__ uint2 wg_widen(uint32_t codes, uint32_t s1, uint32_t s2) {
-    const uint32_t lo = __byte_perm(codes, 0, 0x1404), hi = __byte_perm(codes, 0, 0x3424);   // a code in the high byte of a half
-    const uint32_t a = (lo >> 4 & 0x07f007f0u) | (lo & 0x80008000u), b = (hi >> 4 & 0x07f007f0u) | (hi & 0x80008000u);
-    return make_uint2(mul_bf16x2(mul_bf16x2(a, s1), s2), mul_bf16x2(mul_bf16x2(b, s1), s2));
+    const uint32_t lo = wg_extend<0x9180>(codes), hi = wg_extend<0xb3a2>(codes);
+    uint32_t a = mul_bf16x2(lo * 16 & 0x87f087f0u, s1), b = mul_bf16x2(hi * 16 & 0x87f087f0u, s1);
+    if (kTwo) a = mul_bf16x2(a, s2), b = mul_bf16x2(b, s2);
+    return make_uint2(a, b);
 }
 
 template <typename O>
@@ -103,13 +128,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
     extern __shared__ uint8_t smem_raw[];
     __shared__ WgBars sm;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *wide = smem + kWgStages * kWgABytes, *codes = wide + kWgWide * kWgABytes;
+    uint8_t *wide = smem + kWgDy * kWgABytes, *codes = wide + kWgWide * kWgABytes;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, units = a.mt * a.nt * a.splits;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kWgStages; ++i) mbar_init(&sm.full_a[i], 1), mbar_init(&sm.full_c[i], 1), mbar_init(&sm.empty[i], 1);
-        for (int i = 0; i < kWgWide; ++i) mbar_init(&sm.full_b[i], 2 * kWgConverters / kWgWide), mbar_init(&sm.empty_b[i], 1);
+        for (int i = 0; i < kWgDy; ++i) mbar_init(&sm.full_a[i], 1), mbar_init(&sm.empty_a[i], 1);
+        for (int i = 0; i < kWgCodes; ++i) mbar_init(&sm.full_c[i], 1), mbar_init(&sm.empty_c[i], kWgEach);
+        for (int i = 0; i < kWgWide; ++i) mbar_init(&sm.full_b[i], 2 * kWgEach), mbar_init(&sm.empty_b[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&sm.full_t[i], 1), mbar_init(&sm.empty_t[i], 8);   // four warps in each CTA
         mbar_init(&sm.done, 1);
         sm.abort = 0;
@@ -127,15 +153,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
     if (warp == 0) {
         if (lane == 0) {
             const uint32_t full_even = map_to_cta(smem_u32(sm.full_a), 0);
-            const int blocks = (a.k + kPackBlock - 1) / kPackBlock;
             int it = 0;
             for (int u = pair; ok && u < units; u += pairs) {
                 const WgUnit w = wg_unit(a, u);
-                const int n0 = w.m * kWgTile + rank * kWgHalf, k0 = w.n * kWgTile + rank * kWgHalf, block = k0 / kPackBlock;
+                const int n0 = w.m * kWgTile + rank * kWgHalf;
                 for (int part = a.parts - 1; ok && part >= 0; --part)   // the small parts first
                     for (int step = w.k0; step < w.k1; ++step, ++it) {
-                        const int st = it % kWgStages, t0 = step * kWgK;
-                        if (!(ok = wg_wait(&sm.empty[st], it / kWgStages & 1 ^ 1, sm, a.status))) break;
+                        const int st = it % kWgDy, t0 = step * kWgK;
+                        if (!(ok = wg_wait(&sm.empty_a[st], it / kWgDy & 1 ^ 1, sm, a.status))) break;
                         if (rank == 0) mbar_arrive_expect_tx(&sm.full_a[st], 2 * kWgABytes);
                         uint8_t *dst = smem + st * kWgABytes;
                         if (a.whole) tma_load_3d_pair(dst, &maps.dy[part], full_even + st * 8, 0, t0, n0 / 64);
@@ -143,17 +168,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
                             tma_load_2d_pair(dst, &maps.dy[part], full_even + st * 8, n0, t0);
                             tma_load_2d_pair(dst + kWgBlockBytes, &maps.dy[part], full_even + st * 8, n0 + 64, t0);
                         }
+                    }
+            }
+            // copies in flight have to land before the pair leaves (in the normal course all have)
+            for (int i = max(0, it - kWgDy); !ok && rank == 0 && i < it; ++i) wg_drain(&sm.full_a[i % kWgDy], i / kWgDy & 1);
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            const int blocks = (a.k + kPackBlock - 1) / kPackBlock;
+            int it = 0;
+            for (int u = pair; ok && u < units; u += pairs) {
+                const WgUnit w = wg_unit(a, u);
+                const int k0 = w.n * kWgTile + rank * kWgHalf, block = k0 / kPackBlock;
+                for (int part = 0; ok && part < a.parts; ++part)
+                    for (int step = w.k0; step < w.k1; ++step, ++it) {
+                        const int st = it % kWgCodes, t0 = step * kWgK;
+                        if (!(ok = wg_wait(&sm.empty_c[st], it / kWgCodes & 1 ^ 1, sm, a.status))) break;
                         const uint32_t bytes = block < blocks ? min(kWgK, (a.T - t0 + 15) & ~15) : 0;   // rows of exps are of whole 16 bytes
                         mbar_arrive_expect_tx(&sm.full_c[st], kWgCodeBytes + bytes);
                         tma_load_2d(codes + st * kWgCodeBytes, &maps.codes, &sm.full_c[st], k0, t0);
                         if (bytes) bulk_load(sm.exps[st], a.exps + block * a.ld_exps + t0, bytes, &sm.full_c[st]);
                     }
             }
-            // copies in flight have to land before the CTA leaves (in the normal course all have)
-            for (int i = max(0, it - kWgStages); !ok && i < it; ++i) {
-                wg_drain(&sm.full_c[i % kWgStages], i / kWgStages & 1);
-                if (rank == 0) wg_drain(&sm.full_a[i % kWgStages], i / kWgStages & 1);
-            }
+            for (int i = max(0, it - kWgCodes); !ok && i < it; ++i) wg_drain(&sm.full_c[i % kWgCodes], i / kWgCodes & 1);
         }
     } else if (warp == 1) {
         if (rank == 0) {
@@ -165,8 +202,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
                 if (!(ok = wg_wait(&sm.empty_t[acc], tile >> 1 & 1 ^ 1, sm, a.status))) break;
                 tc_fence_after();
                 for (int i = 0; i < steps; ++i, ++it) {
-                    const int st = it % kWgStages, sb = it % kWgWide;
-                    ok = wg_wait(&sm.full_a[st], it / kWgStages & 1, sm, a.status) && wg_wait(&sm.full_b[sb], it / kWgWide & 1, sm, a.status);
+                    const int st = it % kWgDy, sb = it % kWgWide;
+                    ok = wg_wait(&sm.full_a[st], it / kWgDy & 1, sm, a.status) && wg_wait(&sm.full_b[sb], it / kWgWide & 1, sm, a.status);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
@@ -176,7 +213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
                         for (int kk = 0; kk < kWgK / 16; ++kk)
                             umma_f16_pair(tmem + acc * kWgTile, sdesc_sw128(pa + kk * 2048, kWgBlockBytes, 1024),
                                           sdesc_sw128(pb + kk * 2048, kWgBlockBytes, 1024), kIdesc, (i | kk) != 0);
-                        umma_commit_pair_mc(&sm.empty[st], 3);
+                        umma_commit_pair_mc(&sm.empty_a[st], 3);
                         umma_commit_pair_mc(&sm.empty_b[sb], 3);
                     }
                     __syncwarp();
@@ -188,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
                 wg_drain(&sm.done, 0);
             }
         }
-    } else if (warp < 6) {
+    } else if (warp >= 4 && warp < kWgFirst) {
         const uint32_t empty_even = map_to_cta(smem_u32(sm.empty_t), 0);
         const int quarter = warp & 3;
         int tile = 0;
@@ -226,45 +263,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(empty_even + acc * 8);
         }
-    } else {
-        // Every stage has its warps: they have the time of four steps for one, which hides the waits, the fence and the way to
-        // the even CTA. 16 codes a lane and turn, 8 lanes a token, half of the stage's tokens a warp.
-        constexpr int kEach = kWgConverters / kWgWide, kTurns = kWgK / kEach / 4;
+    } else if (warp >= kWgFirst) {
+        // The groups take steps in turn: each has the time of four for one, which hides the waits, the fence and the way to
+        // the even CTA. 16 codes a lane and turn, 8 lanes a token, 16 tokens a warp.
+        constexpr int kTurns = kWgK / kWgEach / 4;
         const uint32_t full_even = map_to_cta(smem_u32(sm.full_b), 0);
-        const int sb = (warp - 6) / kEach, row = (warp - 6) % kEach * (kWgK / kEach) + lane / 8, chunk = lane & 7;
-        // the token's line, its 16-byte pieces in the order of the 128-byte swizzle; the lanes of one half of the channels
-        // write their second piece first, so that eight lanes together use all banks
+        const int group = (warp - kWgFirst) / kWgEach, row = (warp - kWgFirst) % kWgEach * (kWgK / kWgEach) + lane / 8, chunk = lane & 7;
+        // The token's line, its 16-byte pieces in the order of the 128-byte swizzle. The lanes of one half of the channels
+        // take their second piece first, so that eight lanes together use all banks.
         const int piece = (chunk & 3) * 2, swap = chunk >> 2;
-        uint8_t *to = wide + sb * kWgABytes + swap * kWgBlockBytes;
+        const int to1[2] = {swap * kWgBlockBytes + row * 128 + (((piece + swap) ^ (row & 7)) << 4),
+                            swap * kWgBlockBytes + row * 128 + (((piece + swap) ^ (row & 7) ^ 4) << 4)};   // of even and odd turns
         int it = 0;
         for (int u = pair; ok && u < units; u += pairs) {
             const WgUnit w = wg_unit(a, u);
             for (int part = 0; ok && part < a.parts; ++part)
                 for (int step = w.k0; step < w.k1; ++step, ++it) {
-                    if (it % kWgWide != sb) continue;
-                    const int st = it % kWgStages;
-                    ok = wg_wait(&sm.full_c[st], it / kWgStages & 1, sm, a.status) && wg_wait(&sm.empty_b[sb], it / kWgWide & 1 ^ 1, sm, a.status);
-                    ok = __all_sync(0xffffffffu, ok);
+                    if (it % kWgGroups != group) continue;
+                    const int st = it % kWgCodes, sb = it % kWgWide;
+                    ok = __all_sync(0xffffffffu, wg_wait(&sm.full_c[st], it / kWgCodes & 1, sm, a.status));
                     if (!ok) break;
-                    const uint8_t *from = codes + st * kWgCodeBytes + chunk * 16;
+                    const uint8_t *from = codes + st * kWgCodeBytes + row * 128 + chunk * 16;
+                    uint2 first[kTurns], second[kTurns];
+                    int e[kTurns];
+                    bool rare = (step + 1) * kWgK > a.T;   // behind the last token the exponents are whatever lies there
 #pragma unroll
                     for (int j = 0; j < kTurns; ++j) {
-                        const int r = row + j * 4;
-                        const uint4 c = *reinterpret_cast<const uint4 *>(from + r * 128);
-                        const int e = sm.exps[st][r], s = 120 + e, half = s >> 1;
-                        uint32_t s1 = static_cast<uint32_t>(127 + half) << 7, s2 = static_cast<uint32_t>(127 + s - half) << 7;
-                        if (e == kPackNaN) s1 = 0x7fffu;
-                        if (step * kWgK + r >= a.T) s1 = s2 = 0;   // behind the last token the exponents are whatever lies there
-                        s1 |= s1 << 16, s2 |= s2 << 16;
-                        const uint2 x0 = wg_widen(c.x, s1, s2), x1 = wg_widen(c.y, s1, s2), x2 = wg_widen(c.z, s1, s2), x3 = wg_widen(c.w, s1, s2);
-                        const uint4 first = make_uint4(x0.x, x0.y, x1.x, x1.y), second = make_uint4(x2.x, x2.y, x3.x, x3.y);
-                        uint8_t *line = to + r * 128;
-                        *reinterpret_cast<uint4 *>(line + (((piece + swap) ^ (r & 7)) << 4)) = swap ? second : first;
-                        *reinterpret_cast<uint4 *>(line + (((piece + 1 - swap) ^ (r & 7)) << 4)) = swap ? first : second;
+                        first[j] = *reinterpret_cast<const uint2 *>(from + j * 512 + swap * 8);
+                        second[j] = *reinterpret_cast<const uint2 *>(from + j * 512 + 8 - swap * 8);
+                        e[j] = sm.exps[st][row + j * 4];
+                        rare |= e[j] > 7 || e[j] == kPackNaN;
                     }
+                    rare = __any_sync(0xffffffffu, rare);
+                    if (lane == 0) mbar_arrive(&sm.empty_c[st]);
+                    ok = __all_sync(0xffffffffu, wg_wait(&sm.empty_b[sb], it / kWgWide & 1 ^ 1, sm, a.status));
+                    if (!ok) break;
+                    uint8_t *to = wide + sb * kWgABytes;
+                    auto widen = [&](auto two) {
+                        constexpr bool kTwo = decltype(two)::value;
+#pragma unroll
+                        for (int j = 0; j < kTurns; ++j) {
+                            // 2^(120 + e), twice, or two such that make it
+                            const int s = 120 + e[j], half = kTwo ? s >> 1 : s;
+                            uint32_t s1 = static_cast<uint32_t>(half) * 0x00800080u + 0x3f803f80u, s2 = static_cast<uint32_t>(s - half) * 0x00800080u + 0x3f803f80u;
+                            if (kTwo && e[j] == kPackNaN) s1 = 0x7fff7fffu;
+                            if (kTwo && step * kWgK + row + j * 4 >= a.T) s1 = s2 = 0;
+                            uint8_t *line = to + j * 512 + to1[j & 1];
+                            const uint2 x0 = wg_widen<kTwo>(first[j].x, s1, s2), x1 = wg_widen<kTwo>(first[j].y, s1, s2);
+                            *reinterpret_cast<uint4 *>(line) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                            const uint2 x2 = wg_widen<kTwo>(second[j].x, s1, s2), x3 = wg_widen<kTwo>(second[j].y, s1, s2);
+                            *reinterpret_cast<uint4 *>(to + j * 512 + (to1[j & 1] ^ 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                        }
+                    };
+                    if (rare) widen(std::true_type());
+                    else widen(std::false_type());
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(full_even + sb * 8);
+                    if (lane == 0) wg_arrive(full_even + sb * 8);
                 }
         }
     }
