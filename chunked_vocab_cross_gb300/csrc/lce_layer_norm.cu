@@ -148,6 +148,362 @@ __global__ void __launch_bounds__(512) k_ln_bwd(const LnArgs a) {
         a.part[(static_cast<int64_t>(i / d) * gridDim.x + blockIdx.x) * d + i % d] = sums[i];
 }
 
+// ---------------------------------------------------------------- ring kernels
+//
+// Persistent blocks whose rows arrive through a ring of bulk copies, as in the
+// block norms; what a thread holds of a row are packs of 16 bytes, `tpr` threads
+// a row, and row groups join their sums on barriers of their own.
+
+constexpr int kLnArrays = 3;
+struct LnGeo {
+    int tpr, groups, stages, arrays;
+    uint32_t row_bytes;                              // of the tensors' type
+    uint32_t bytes[kLnArrays], at[kLnArrays];        // of a row of each array; the array's place in a stage
+    uint32_t stage_bytes;
+};
+struct LnSource {
+    const uint8_t *src[kLnArrays];
+    int64_t ld[kLnArrays];   // bytes
+    // Starts the copies of the `per` rows from r0 on into stage s, if there are
+    // any. Rows past the last arrive as copies of the last.
+    template <bool kOnce>
+    __device__ __forceinline__ void issue(uint8_t *ring, RingBars &bars, const LnGeo &g, int per, int s, int64_t r0, int64_t N) const {
+        if (r0 >= N) return;
+        mbar_arrive_expect_tx(&bars.full[s], g.stage_bytes);
+        uint8_t *stage = ring + s * g.stage_bytes;
+        auto load = [&](uint8_t *to, const uint8_t *from, uint32_t bytes) {
+            if (kOnce) bulk_load_once(to, from, bytes, &bars.full[s]);
+            else bulk_load(to, from, bytes, &bars.full[s]);
+        };
+#pragma unroll
+        for (int k = 0; k < kLnArrays; ++k) {
+            if (k >= g.arrays) continue;
+            if (ld[k] == g.bytes[k] && r0 + per <= N) load(stage + g.at[k], src[k] + r0 * ld[k], per * g.bytes[k]);
+            else
+                for (int r = 0; r < per; ++r) load(stage + g.at[k] + r * g.bytes[k], src[k] + min(r0 + r, N - 1) * ld[k], g.bytes[k]);
+        }
+    }
+};
+// After a wait that gave up in stage s: lets the copies in flight land.
+__device__ __forceinline__ void ln_drain(RingBars &bars, const LnGeo &g, int per, int s, uint32_t phase, int64_t r0, int64_t N) {
+    for (int i = 0; i < g.stages && r0 < N; ++i, r0 += static_cast<int64_t>(gridDim.x) * per) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(smem_u32(&bars.full[s]), phase) && clock64() - t0 < kNormWaitCycles / 10) {}
+        if (++s == g.stages) s = 0, phase ^= 1;
+    }
+}
+
+// A row's weights in shared memory (zeros where there are none)
+__device__ __forceinline__ void load_row(uint8_t *dst, const void *w, int row_bytes) {
+    for (int i = threadIdx.x * 16; i < row_bytes; i += blockDim.x * 16)
+        *reinterpret_cast<uint4 *>(dst + i) = w ? *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(w) + i) : make_uint4(0, 0, 0, 0);
+}
+
+// The codes of a pack's values, and from them
+template <typename T>
+__device__ __forceinline__ uint2 pack_codes(const f32x2 (&x)[kPack<T> / 2], float scale) {
+    uint32_t c[kPack<T> / 2];
+#pragma unroll
+    for (int i = 0; i < kPack<T> / 2; ++i) {
+        float a, b;
+        unpack2(x[i], a, b);
+        c[i] = to_codes(a * scale, b * scale);
+    }
+    return sizeof(T) == 2 ? make_uint2(c[0] | c[1] << 16, c[kPack<T> / 2 - 2] | c[kPack<T> / 2 - 1] << 16) : make_uint2(c[0] | c[1] << 16, 0);
+}
+template <typename T>
+__device__ __forceinline__ void pack_values(const uint8_t *p, float scale, f32x2 (&x)[kPack<T> / 2]) {
+    uint32_t w[2] = {*reinterpret_cast<const uint32_t *>(p), 0};
+    if (sizeof(T) == 2) w[1] = *reinterpret_cast<const uint32_t *>(p + 4);
+    const f32x2 f = both(scale);
+#pragma unroll
+    for (int i = 0; i < kPack<T> / 2; ++i) {
+        float a, b;
+        from_codes(w[i / 2] >> (i % 2 * 16), a, b);
+        x[i] = mul2(pack2(a, b), f);
+    }
+}
+
+// Forward. kAdd: there is a block's output to add; kKeep: r is packed as well (a
+// block of 128 channels lies in 16 lanes' packs of bf16, in a warp's of fp32).
+template <typename T, int CH, bool kAdd, bool kKeep>
+__global__ void __launch_bounds__(kRingThreads, 1) k_ln_fwd_ring(const LnArgs a, const LnGeo g) {
+    constexpr int V = kPack<T>, P = V / 2;
+    extern __shared__ __align__(128) uint8_t smem[];   // ring, then weight, bias
+    __shared__ RingBars bars;
+    __shared__ __align__(16) float red[16 * kRedFloats];
+    const int nwarps = blockDim.x / 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < g.stages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], nwarps);
+        for (int i = 0; i < 16; ++i) bars.gave_up[i] = 0;
+        fence_mbar_init();
+    }
+    uint8_t *w_row = smem + g.stages * g.stage_bytes, *c_row = w_row + g.row_bytes;
+    load_row(w_row, a.w, g.row_bytes);
+    load_row(c_row, a.c, g.row_bytes);
+    for (int i = threadIdx.x; i < 16 * kRedFloats; i += blockDim.x) red[i] = 0.f;
+    __syncthreads();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * g.groups;
+    int64_t r0 = static_cast<int64_t>(blockIdx.x) * g.groups;
+    const LnSource src = {{static_cast<const uint8_t *>(a.x), static_cast<const uint8_t *>(a.b), nullptr},
+                          {a.ld_x * static_cast<int>(sizeof(T)), a.ld_b * static_cast<int>(sizeof(T)), 0}};
+    if (threadIdx.x == 0)
+        for (int i = 0; i < g.stages; ++i) src.issue<true>(smem, bars, g, g.groups, i, r0 + i * step, a.N);
+    const int group = threadIdx.x / g.tpr, t = threadIdx.x % g.tpr;
+    float *my_red = red + group * kRedFloats;
+    const float inv_d = 1.f / a.d;
+    uint8_t *out_r = static_cast<uint8_t *>(a.r) + (r0 + group) * g.row_bytes + t * 16;
+    uint8_t *out_n = static_cast<uint8_t *>(a.n) + (r0 + group) * g.row_bytes + t * 16;
+    int flip = 0, s = 0;
+    uint32_t phase = 0;
+    for (; r0 < a.N; r0 += step, out_r += step * g.row_bytes, out_n += step * g.row_bytes) {
+        const int64_t row = r0 + group;
+        // the vote also tells the compiler that the warp is together again
+        if (!__all_sync(0xffffffffu, ring_wait(&bars.full[s], phase, a.status))) bars.gave_up[group] = 1;
+        const bool live = row < a.N;
+        const uint8_t *at = smem + s * g.stage_bytes + group * g.row_bytes;
+        f32x2 r[CH][P];
+        f32x2 q = both(0.f);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int byte = (c * g.tpr + t) * 16;
+            const bool in = byte < g.row_bytes;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (in) x = *reinterpret_cast<const uint4 *>(at + byte);
+            Pack16<T>::get(x, r[c]);
+            if (kAdd) {
+                f32x2 b[P];
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (in) v = *reinterpret_cast<const uint4 *>(at + g.at[1] + byte);
+                Pack16<T>::get(v, b);
+#pragma unroll
+                for (int i = 0; i < P; ++i) b[i] = add2(r[c][i], b[i]);
+                v = Pack16<T>::set(b);
+                if (live && in) __stcs(reinterpret_cast<uint4 *>(out_r + c * g.tpr * 16), v);
+                Pack16<T>::get(v, r[c]);   // as it is stored
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) q = add2(q, r[c][i]);
+            if (kKeep) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    float lo, hi;
+                    unpack2(r[c][i], lo, hi);
+                    top = max(top, max(__float_as_uint(lo) & 0x7fffffffu, __float_as_uint(hi) & 0x7fffffffu));
+                }
+#pragma unroll
+                for (int m = kPackBlock / V / 2; m; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+                const int e = pack_exponent(top), col = (c * g.tpr + t) * V;
+                const uint2 codes = pack_codes<T>(r[c], pack_scale(e));
+                if (live && in) {
+                    uint8_t *to = a.codes + row * a.ld_codes + col;
+                    if (sizeof(T) == 2) *reinterpret_cast<uint2 *>(to) = codes;
+                    else *reinterpret_cast<uint32_t *>(to) = codes.x;
+                    if (col % kPackBlock == 0) a.exps[col / kPackBlock * a.ld_exps + row] = static_cast<int8_t>(e);
+                }
+            }
+        }
+        __syncwarp();
+        if ((t & 31) == 0) mbar_arrive(&bars.empty[s]);   // everything is in registers
+        float sum[1] = {hsum2(q)};
+        group_sum(sum, my_red, flip, g.tpr, group, t);
+        const float mean = sum[0] * inv_d;
+        const f32x2 minus = both(-mean);
+        q = both(0.f);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            if ((c * g.tpr + t) * 16 >= g.row_bytes) continue;
+#pragma unroll
+            for (int i = 0; i < P; ++i) r[c][i] = add2(r[c][i], minus), q = fma2(r[c][i], r[c][i], q);
+        }
+        sum[0] = hsum2(q);
+        group_sum(sum, my_red, flip, g.tpr, group, t);
+        if (bars.gave_up[group]) {
+            if (threadIdx.x == 0) ln_drain(bars, g, g.groups, s, phase, r0, a.N);
+            break;
+        }
+        // the stage's next rows, once every warp has taken its share
+        if (threadIdx.x == 0 && r0 + g.stages * step < a.N && ring_wait(&bars.empty[s], phase, a.status))
+            src.issue<true>(smem, bars, g, g.groups, s, r0 + g.stages * step, a.N);
+        const float rs = rsqrtf(sum[0] * inv_d + a.eps);
+        if (t == 0 && live) a.mean[row] = mean, a.rstd[row] = rs;
+        const f32x2 f = both(rs);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int byte = (c * g.tpr + t) * 16;
+            if (byte >= g.row_bytes) continue;
+            f32x2 w[P], y[P];
+            Pack16<T>::get(*reinterpret_cast<const uint4 *>(w_row + byte), w);
+            Pack16<T>::get(*reinterpret_cast<const uint4 *>(c_row + byte), y);
+#pragma unroll
+            for (int i = 0; i < P; ++i) y[i] = fma2(mul2(r[c][i], f), w[i], y[i]);
+            if (live) *reinterpret_cast<uint4 *>(out_n + c * g.tpr * 16) = Pack16<T>::set(y);
+        }
+        if (++s == g.stages) s = 0, phase ^= 1;
+    }
+}
+
+// Backward, a thread's columns of R rows at a time: the two row sums in one
+// round; the column sums stay in registers, one set a row group, and are joined
+// across the groups in shared memory at the end. kCodes: the stream comes in 8
+// bits; kDr: there is a gradient of r.
+template <typename T, int CH, int R, bool kCodes, bool kDr>
+__global__ void __launch_bounds__(kRingThreads, 1) k_ln_bwd_ring(const LnArgs a, const LnGeo g) {
+    constexpr int V = kPack<T>, P = V / 2;
+    extern __shared__ __align__(128) uint8_t smem[];   // ring, then weight
+    __shared__ RingBars bars;
+    __shared__ __align__(16) float red[16 * kRedFloats];
+    const int nwarps = blockDim.x / 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < g.stages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], nwarps);
+        for (int i = 0; i < 16; ++i) bars.gave_up[i] = 0;
+        fence_mbar_init();
+    }
+    uint8_t *w_row = smem + g.stages * g.stage_bytes;
+    load_row(w_row, a.w, g.row_bytes);
+    for (int i = threadIdx.x; i < 16 * kRedFloats; i += blockDim.x) red[i] = 0.f;
+    __syncthreads();
+    const int per = g.groups * R;   // rows of a stage
+    const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+    int64_t r0 = static_cast<int64_t>(blockIdx.x) * per;
+    const LnSource src = {{kCodes ? a.codes : static_cast<const uint8_t *>(a.r_in), static_cast<const uint8_t *>(a.dn), static_cast<const uint8_t *>(a.dr)},
+                          {kCodes ? a.ld_codes : a.ld_r * static_cast<int>(sizeof(T)), a.ld_dn * static_cast<int>(sizeof(T)), a.ld_dr * static_cast<int>(sizeof(T))}};
+    if (threadIdx.x == 0)
+        for (int i = 0; i < g.stages; ++i) src.issue<false>(smem, bars, g, per, i, r0 + i * step, a.N);
+    const int group = threadIdx.x / g.tpr, t = threadIdx.x % g.tpr;
+    float *my_red = red + group * kRedFloats;
+    const float inv_d = 1.f / a.d;
+    f32x2 s_w[CH][P], s_c[CH][P];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < P; ++i) s_w[c][i] = s_c[c][i] = both(0.f);
+    uint8_t *out = static_cast<uint8_t *>(a.dx) + (r0 + group * R) * g.row_bytes + t * 16;
+    int flip = 0, s = 0;
+    uint32_t phase = 0;
+    // statistics (and exponents) of the rows to come, asked for a round ahead; zeros past the last row
+    float mean_next[R], rs_next[R];
+    int e_next[R][CH];
+    auto ask = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const bool live = row + k < a.N;
+            mean_next[k] = live ? a.mean[row + k] : 0.f;
+            rs_next[k] = live ? a.rstd[row + k] : 0.f;
+            if (kCodes)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const int col = (c * g.tpr + t) * V;
+                    e_next[k][c] = live && col < a.d ? a.exps[col / kPackBlock * a.ld_exps + row + k] : 0;
+                }
+        }
+    };
+    ask(r0 + group * R);
+    for (; r0 < a.N; r0 += step, out += step * g.row_bytes) {
+        const int64_t row = r0 + group * R;
+        float mean[R], rs[R], scale[R][CH];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            mean[k] = mean_next[k], rs[k] = rs_next[k];
+            if (kCodes)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) scale[k][c] = unpack_scale(e_next[k][c]);
+        }
+        ask(row + step);
+        if (!__all_sync(0xffffffffu, ring_wait(&bars.full[s], phase, a.status))) bars.gave_up[group] = 1;
+        const uint8_t *stage = smem + s * g.stage_bytes;
+        f32x2 hat[R][CH][P], u[R][CH][P], q[R][2];
+#pragma unroll
+        for (int k = 0; k < R; ++k) q[k][0] = q[k][1] = both(0.f);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int byte = (c * g.tpr + t) * 16;
+            f32x2 w[P];
+            const bool in = byte < g.row_bytes;
+            if (in) Pack16<T>::get(*reinterpret_cast<const uint4 *>(w_row + byte), w);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                if (!in || row + k >= a.N) {   // rows past the last add nothing to the columns
+#pragma unroll
+                    for (int i = 0; i < P; ++i) hat[k][c][i] = u[k][c][i] = both(0.f);
+                    continue;
+                }
+                if (kCodes) pack_values<T>(stage + (group * R + k) * g.bytes[0] + (c * g.tpr + t) * V, scale[k][c], hat[k][c]);
+                else Pack16<T>::get(*reinterpret_cast<const uint4 *>(stage + (group * R + k) * g.bytes[0] + byte), hat[k][c]);
+                Pack16<T>::get(*reinterpret_cast<const uint4 *>(stage + g.at[1] + (group * R + k) * g.row_bytes + byte), u[k][c]);
+                const f32x2 minus = both(-mean[k]), f = both(rs[k]);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    hat[k][c][i] = mul2(add2(hat[k][c][i], minus), f);
+                    s_w[c][i] = fma2(u[k][c][i], hat[k][c][i], s_w[c][i]);
+                    s_c[c][i] = add2(u[k][c][i], s_c[c][i]);
+                    u[k][c][i] = mul2(u[k][c][i], w[i]);
+                    q[k][0] = add2(q[k][0], u[k][c][i]);
+                    q[k][1] = fma2(u[k][c][i], hat[k][c][i], q[k][1]);
+                }
+            }
+        }
+        float sum[2 * R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) sum[2 * k] = hsum2(q[k][0]), sum[2 * k + 1] = hsum2(q[k][1]);
+        group_sum(sum, my_red, flip, g.tpr, group, t);
+        if (bars.gave_up[group]) {
+            if (threadIdx.x == 0) ln_drain(bars, g, per, s, phase, r0, a.N);
+            break;
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int byte = (c * g.tpr + t) * 16;
+            if (byte >= g.row_bytes) continue;
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                if (row + k >= a.N) continue;
+                const f32x2 m0 = both(-sum[2 * k] * inv_d), m1 = both(-sum[2 * k + 1] * inv_d), f = both(rs[k]);
+                f32x2 y[P];
+                if (kDr) Pack16<T>::get(*reinterpret_cast<const uint4 *>(stage + g.at[2] + (group * R + k) * g.row_bytes + byte), y);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const f32x2 v = fma2(hat[k][c][i], m1, add2(u[k][c][i], m0));
+                    y[i] = kDr ? fma2(v, f, y[i]) : mul2(v, f);
+                }
+                *reinterpret_cast<uint4 *>(out + k * g.row_bytes + c * g.tpr * 16) = Pack16<T>::set(y);
+            }
+        }
+        __syncwarp();
+        if ((t & 31) == 0) mbar_arrive(&bars.empty[s]);
+        // the stage's next rows, once every warp is through with it
+        if (threadIdx.x == 0 && r0 + g.stages * step < a.N && ring_wait(&bars.empty[s], phase, a.status))
+            src.issue<false>(smem, bars, g, per, s, r0 + g.stages * step, a.N);
+        if (++s == g.stages) s = 0, phase ^= 1;
+    }
+    // the groups' sums, [group][d] at a time through the (now idle) ring
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int col = (c * g.tpr + t) * V;
+            if (col >= a.d) continue;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                float2 v;
+                unpack2(k == 0 ? s_w[c][i] : s_c[c][i], v.x, v.y);
+                *reinterpret_cast<float2 *>(sums + group * a.d + col + 2 * i) = v;
+            }
+        }
+        __syncthreads();
+        float *to = a.part + (static_cast<int64_t>(k) * gridDim.x + blockIdx.x) * a.d;
+        for (int i = threadIdx.x; i < a.d; i += blockDim.x) {
+            float v = 0.f;
+            for (int q = 0; q < g.groups; ++q) v += sums[q * a.d + i];
+            to[i] = v;
+        }
+        __syncthreads();
+    }
+}
+
 constexpr int64_t kMaxD = 16384;
 constexpr int kColGroups = 304;   // blocks of the backward at most (bounds its workspace)
 
@@ -199,8 +555,65 @@ int row_threads(int d) {
     return packs >= 512 ? 512 : (packs + 31) / 32 * 32;
 }
 
+constexpr int kRingBytes = 208 * 1024;      // dynamic shared memory of a ring kernel's block at most
+constexpr int kFwdRingBytes = 128 * 1024;   // ring of the forward, if two stages do not take more
+// Few rows have nothing to run ahead of: up to this much of an array the forward takes a block for each row.
+constexpr int64_t kDirectBytes = 4 << 20;
+
+// The ring kernels' geometry for rows of d elements: `ch` packs a thread, `per` rows a group and stage, `weights` rows
+// beside the ring; codes: the first array is of bytes. False where rows are too wide.
+bool ln_geo(LnGeo *g, int d, int elt, int arrays, bool codes, int ch, int per, int weights, int bytes) {
+    const int packs = d * elt / 16;
+    g->tpr = ((packs + ch - 1) / ch + 31) / 32 * 32;
+    if (g->tpr > kRingThreads) return false;
+    g->groups = kRingThreads / g->tpr;
+    g->arrays = arrays;
+    g->row_bytes = d * elt;
+    g->stage_bytes = 0;
+    for (int k = 0; k < kLnArrays; ++k) {
+        g->bytes[k] = k == 0 && codes ? (d + 15) / 16 * 16 : g->row_bytes;
+        g->at[k] = g->stage_bytes;
+        if (k < arrays) g->stage_bytes += g->groups * per * g->bytes[k];
+    }
+    const int rows = weights * static_cast<int>(g->row_bytes), stage = static_cast<int>(g->stage_bytes);
+    if (2 * stage + rows > kRingBytes) return false;
+    g->stages = std::max(2, std::min(kRingMaxStages, std::min(bytes, kRingBytes - rows) / stage));
+    return true;
+}
+
+// Rows are handed out a stage at a time; at least one block, so that column sums of no rows come out as zeros.
+int ring_grid(int64_t N, int rows, int most) { return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((N + rows - 1) / rows, most))); }
+
+template <auto kKernel>
+lce_status_t launch_ring(const HostDev &dev, const LnArgs &r, const LnGeo &g, int grid, int smem, cudaStream_t st) {
+    const lce_status_t s = host_smem<kKernel>(dev, kRingBytes);
+    if (s != LCE_OK) return s;
+    kKernel<<<grid, g.tpr * g.groups, smem, st>>>(r, g);
+    return host_launched();
+}
+
 template <typename T>
-lce_status_t forward(const LnArgs &r, cudaStream_t st) {
+lce_status_t forward(const LnArgs &r, const HostDev &dev, cudaStream_t st) {
+    LnGeo g;
+    // packs a thread: as few as leave a row to 32 threads, at most 32 elements
+    int ch = 1;
+    while (ch < 32 / kPack<T> && r.d * static_cast<int>(sizeof(T)) / 16 > 32 * ch) ch *= 2;
+    if (r.N * r.d * static_cast<int64_t>(sizeof(T)) > kDirectBytes && ln_geo(&g, r.d, sizeof(T), r.b ? 2 : 1, false, ch, 1, 2, kFwdRingBytes)) {
+        const int grid = ring_grid(r.N, g.groups, dev.sms), smem = g.stages * g.stage_bytes + 2 * g.row_bytes;
+        auto go = [&](auto c) {
+            constexpr int CH = decltype(c)::value;
+            return r.b ? r.codes ? launch_ring<k_ln_fwd_ring<T, CH, true, true>>(dev, r, g, grid, smem, st)
+                                 : launch_ring<k_ln_fwd_ring<T, CH, true, false>>(dev, r, g, grid, smem, st)
+                       : r.codes ? launch_ring<k_ln_fwd_ring<T, CH, false, true>>(dev, r, g, grid, smem, st)
+                                 : launch_ring<k_ln_fwd_ring<T, CH, false, false>>(dev, r, g, grid, smem, st);
+        };
+        switch (ch) {
+            case 1: return go(std::integral_constant<int, 1>());
+            case 2: return go(std::integral_constant<int, 2>());
+            case 4: return go(std::integral_constant<int, 4>());
+            default: return go(std::integral_constant<int, 32 / kPack<T>>());   // fp32: 8
+        }
+    }
     const unsigned grid = static_cast<unsigned>(r.N);
     const int th = row_threads(r.d), packs = (r.d / kVec + 511) / 512;
     switch (packs) {
@@ -212,19 +625,36 @@ lce_status_t forward(const LnArgs &r, cudaStream_t st) {
 }
 
 template <typename T>
-lce_status_t backward(const lce_layer_norm_t *a, LnArgs r, const HostDev &dev, cudaStream_t st) {
-    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(r.N, kColGroups)));
-    const int th = row_threads(r.d), smem = 2 * r.d * 4, packs = (r.d / kVec + 511) / 512;
-    auto go = [&](auto ch) {
-        constexpr auto kernel = k_ln_bwd<T, decltype(ch)::value>;
-        const lce_status_t s = host_smem<kernel>(dev, 2 * kMaxD * 4);
-        if (s != LCE_OK) return s;
-        kernel<<<grid, th, smem, st>>>(r);
-        return host_launched();
-    };
-    const lce_status_t s = packs == 1   ? go(std::integral_constant<int, 1>())
-                           : packs == 2 ? go(std::integral_constant<int, 2>())
-                                        : go(std::integral_constant<int, 4>());
+lce_status_t backward(const lce_layer_norm_t *a, const LnArgs &r, const HostDev &dev, cudaStream_t st) {
+    LnGeo g;
+    int grid;
+    lce_status_t s;
+    // two rows a thread while a row's packs go round once, else one; packs a thread: one, or as many as a row needs of 512 threads
+    const int packs = r.d * static_cast<int>(sizeof(T)) / 16;
+    const int ch = packs <= kRingThreads ? 1 : packs <= 2 * kRingThreads ? 2 : 16 / kPack<T>, per = ch == 1 ? 2 : 1;
+    if (ln_geo(&g, r.d, sizeof(T), r.dr ? 3 : 2, r.codes != nullptr, ch, per, 1, kRingBytes)) {
+        grid = ring_grid(r.N, g.groups * per, dev.sms);
+        const int smem = std::max<int>(g.stages * g.stage_bytes + g.row_bytes, g.groups * r.d * 4);
+        auto go = [&](auto c, auto rows) {
+            constexpr int CH = decltype(c)::value, R = decltype(rows)::value;
+            return r.codes ? r.dr ? launch_ring<k_ln_bwd_ring<T, CH, R, true, true>>(dev, r, g, grid, smem, st)
+                                  : launch_ring<k_ln_bwd_ring<T, CH, R, true, false>>(dev, r, g, grid, smem, st)
+                           : r.dr ? launch_ring<k_ln_bwd_ring<T, CH, R, false, true>>(dev, r, g, grid, smem, st)
+                                  : launch_ring<k_ln_bwd_ring<T, CH, R, false, false>>(dev, r, g, grid, smem, st);
+        };
+        switch (ch) {
+            case 1: s = go(std::integral_constant<int, 1>(), std::integral_constant<int, 2>()); break;
+            case 2: s = go(std::integral_constant<int, 2>(), std::integral_constant<int, 1>()); break;
+            default: s = go(std::integral_constant<int, 16 / kPack<T>>(), std::integral_constant<int, 1>());   // fp32: 4
+        }
+    } else {   // rows too wide for two stages
+        grid = ring_grid(r.N, 1, kColGroups);
+        const int th = row_threads(r.d), smem = 2 * r.d * 4;
+        if ((s = host_smem<k_ln_bwd<T, 4>>(dev, 2 * kMaxD * 4)) == LCE_OK) {
+            k_ln_bwd<T, 4><<<grid, th, smem, st>>>(r);
+            s = host_launched();
+        }
+    }
     if (s != LCE_OK) return s;
     return host_launch_early(k_norm_cols<T>, dim3((r.d + 31) / 32, 2), 256, 0, st, r.part, grid, r.d, static_cast<T *>(a->dweight),
                              static_cast<T *>(a->dbias), static_cast<T *>(nullptr));
@@ -247,7 +677,7 @@ lce_status_t lce_layer_norm_forward(const lce_layer_norm_t *a) {
     if (a->N == 0) return LCE_OK;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(a->stream);
     const LnArgs r = make_args(a, dev);
-    return a->dtype == LCE_BF16 ? forward<__nv_bfloat16>(r, st) : forward<float>(r, st);
+    return a->dtype == LCE_BF16 ? forward<__nv_bfloat16>(r, dev, st) : forward<float>(r, dev, st);
 }
 
 lce_status_t lce_layer_norm_backward(const lce_layer_norm_t *a) {

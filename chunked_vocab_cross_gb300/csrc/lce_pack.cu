@@ -18,41 +18,79 @@ struct PackArgs {
     void *out;
     uint8_t *codes;
     int8_t *exps;
-    int64_t ld, ld_codes, ld_exps, pieces;   // pieces: N * wpr
-    int d, wpr;                              // wpr: pieces of 256 channels in a row, each taken by a warp
+    int64_t ld, ld_codes, ld_exps, N;
+    int d, per;   // per: pieces of 256 channels in a row
 };
 
+// The pieces that a warp takes: every gridDim.x * 8th of all rows' pieces, without a division a piece.
+struct Pieces {
+    int64_t row, rows;   // of the next piece; rows to go on by
+    int at, ats, per;    // its place in the row; places to go on by
+    __device__ __forceinline__ Pieces(int per_) : per(per_) {
+        const int64_t first = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32, step = static_cast<int64_t>(gridDim.x) * 8;
+        row = first / per, at = static_cast<int>(first - row * per);
+        rows = step / per, ats = static_cast<int>(step - rows * per);
+    }
+    __device__ __forceinline__ void next() {
+        row += rows, at += ats;
+        if (at >= per) at -= per, ++row;
+    }
+};
+
+constexpr int kTogether = 4;   // pieces whose loads a warp has in flight
+
+// Both are bounded by HBM: no lane waits for another but within 16, and four
+// loads of 16 bytes (of fp32, eight) are in flight a thread.
 template <typename T>
 __global__ void __launch_bounds__(256) k_pack8(const PackArgs a) {
     const int lane = threadIdx.x & 31;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
-    for (int64_t p = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; p < a.pieces; p += step) {
-        const int64_t row = p / a.wpr;
-        const int col = static_cast<int>(p - row * a.wpr) * 256 + lane * kVec;
-        float x[kVec];
+    for (Pieces p(a.per); p.row < a.N;) {
+        Pack<T> v[kTogether];
+        int64_t row[kTogether];
+        int col[kTogether];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) x[i] = 0.f;
-        if (col < a.d) load_pack(static_cast<const T *>(a.x) + row * a.ld + col).get(x);
-        const int e = pack_exponent(block_top(x));
-        if (col < a.d) {
-            *reinterpret_cast<uint2 *>(a.codes + row * a.ld_codes + col) = codes8(x, pack_scale(e));
-            if (col % kPackBlock == 0) a.exps[col / kPackBlock * a.ld_exps + row] = static_cast<int8_t>(e);
+        for (int i = 0; i < kTogether; ++i, p.next()) {
+            row[i] = p.row, col[i] = p.at * 256 + lane * kVec;
+            if (col[i] >= a.d) row[i] = a.N;   // nothing there
+            if (row[i] < a.N) v[i] = load_pack(static_cast<const T *>(a.x) + row[i] * a.ld + col[i]);
         }
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+            float x[kVec];
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) x[k] = 0.f;
+            if (row[i] < a.N) v[i].get(x);
+            const int e = pack_exponent(block_top(x));
+            if (row[i] >= a.N) continue;
+            *reinterpret_cast<uint2 *>(a.codes + row[i] * a.ld_codes + col[i]) = codes8(x, pack_scale(e));
+            if (col[i] % kPackBlock == 0) a.exps[col[i] / kPackBlock * a.ld_exps + row[i]] = static_cast<int8_t>(e);
+        }
+        __syncwarp();
     }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(256) k_unpack8(const PackArgs a) {
     const int lane = threadIdx.x & 31;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
-    for (int64_t p = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; p < a.pieces; p += step) {
-        const int64_t row = p / a.wpr;
-        const int col = static_cast<int>(p - row * a.wpr) * 256 + lane * kVec;
-        if (col >= a.d) continue;
-        float x[kVec];
-        values8(*reinterpret_cast<const uint2 *>(a.codes + row * a.ld_codes + col),
-                unpack_scale(a.exps[col / kPackBlock * a.ld_exps + row]), x);
-        store_pack(static_cast<T *>(a.out) + row * a.ld + col, x);
+    for (Pieces p(a.per); p.row < a.N;) {
+        uint2 c[kTogether];
+        int e[kTogether], col[kTogether];
+        int64_t row[kTogether];
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i, p.next()) {
+            row[i] = p.row, col[i] = p.at * 256 + lane * kVec;
+            if (col[i] >= a.d) row[i] = a.N;
+            if (row[i] >= a.N) continue;
+            c[i] = *reinterpret_cast<const uint2 *>(a.codes + row[i] * a.ld_codes + col[i]);
+            e[i] = a.exps[col[i] / kPackBlock * a.ld_exps + row[i]];
+        }
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+            if (row[i] >= a.N) continue;
+            float x[kVec];
+            values8(c[i], unpack_scale(e[i]), x);
+            store_pack(static_cast<T *>(a.out) + row[i] * a.ld + col[i], x);
+        }
     }
 }
 
@@ -68,8 +106,13 @@ lce_status_t check_plain(lce_dtype_t dtype, const void *x, int64_t ld, int64_t N
     return host_check_packed(codes, ld_codes, exps, ld_exps, N, d);
 }
 
-int plain_grid(const PackArgs &r, const HostDev &dev) {
-    return static_cast<int>(std::min<int64_t>((r.pieces + 7) / 8, static_cast<int64_t>(dev.sms) * 8));
+PackArgs pack_args(const void *x, void *out, int64_t ld, int64_t N, int64_t d, const uint8_t *codes, int64_t ld_codes, const int8_t *exps,
+                   int64_t ld_exps) {
+    return PackArgs{x, out, const_cast<uint8_t *>(codes), const_cast<int8_t *>(exps), ld ? ld : d, ld_codes, ld_exps, N,
+                    static_cast<int>(d), static_cast<int>((d + 255) / 256)};
+}
+int pack_grid(const PackArgs &r, const HostDev &dev) {
+    return static_cast<int>(std::min<int64_t>((r.N * r.per + 7) / 8, static_cast<int64_t>(dev.sms) * 8));
 }
 
 lce_status_t check_wgrad(const lce_wgrad_t *a) {
@@ -172,11 +215,10 @@ lce_status_t lce_pack8(lce_dtype_t dtype, const void *x, int64_t ld_x, int64_t N
     HostDev dev;
     if ((s = host_device(&dev)) != LCE_OK) return s;
     if (N == 0) return LCE_OK;
-    const int wpr = static_cast<int>((d + 255) / 256);
-    const PackArgs r{x, nullptr, codes, exps, ld_x ? ld_x : d, ld_codes, ld_exps, N * wpr, static_cast<int>(d), wpr};
+    const PackArgs r = pack_args(x, nullptr, ld_x, N, d, codes, ld_codes, exps, ld_exps);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == LCE_BF16) k_pack8<__nv_bfloat16><<<plain_grid(r, dev), 256, 0, st>>>(r);
-    else k_pack8<float><<<plain_grid(r, dev), 256, 0, st>>>(r);
+    if (dtype == LCE_BF16) k_pack8<__nv_bfloat16><<<pack_grid(r, dev), 256, 0, st>>>(r);
+    else k_pack8<float><<<pack_grid(r, dev), 256, 0, st>>>(r);
     return host_launched();
 }
 
@@ -187,12 +229,10 @@ lce_status_t lce_unpack8(lce_dtype_t dtype, const uint8_t *codes, int64_t ld_cod
     HostDev dev;
     if ((s = host_device(&dev)) != LCE_OK) return s;
     if (N == 0) return LCE_OK;
-    const int wpr = static_cast<int>((d + 255) / 256);
-    const PackArgs r{nullptr, out, const_cast<uint8_t *>(codes), const_cast<int8_t *>(exps), ld_out ? ld_out : d, ld_codes, ld_exps,
-                     N * wpr, static_cast<int>(d), wpr};
+    const PackArgs r = pack_args(nullptr, out, ld_out, N, d, codes, ld_codes, exps, ld_exps);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == LCE_BF16) k_unpack8<__nv_bfloat16><<<plain_grid(r, dev), 256, 0, st>>>(r);
-    else k_unpack8<float><<<plain_grid(r, dev), 256, 0, st>>>(r);
+    if (dtype == LCE_BF16) k_unpack8<__nv_bfloat16><<<pack_grid(r, dev), 256, 0, st>>>(r);
+    else k_unpack8<float><<<pack_grid(r, dev), 256, 0, st>>>(r);
     return host_launched();
 }
 
