@@ -12,7 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from .block_ops import _DT, _like, _on_stream, _rows, _scratch, _spread, _stream, _vector, _written
+from .block_ops import _DT, _Expanded, _like, _on_stream, _rows, _scratch, _spread, _stream, _vector, _written
 
 _LN, _WGRAD, _SCAN = _abi.packer(_abi.LceLayerNorm), _abi.packer(_abi.LceWgrad), _abi.packer(_abi.LceRecurrence)
 _at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
@@ -27,7 +27,7 @@ class PackedActivation:
     block held an infinity or NaN and stands for NaNs). Both have rows on
     16-byte strides, and are copied to such where they have not (brought back
     from host memory, say). `dtype`: of the tensor that was packed."""
-    __slots__ = ("codes", "exps", "dtype")
+    __slots__ = ("codes", "exps", "dtype", "_fields")
 
     def __init__(self, codes, exps, dtype):
         if codes.dtype != torch.uint8 or exps.dtype != torch.int8 or codes.dim() != 2 or exps.dim() != 2 or dtype not in _DT:
@@ -36,7 +36,12 @@ class PackedActivation:
             raise ValueError("exps must be [ceil(d / 128), N] for codes [N, d], both on one CUDA device (there is no CPU path)")
         if (codes.stride(1) != 1 and codes.shape[1] > 1) or (exps.stride(1) != 1 and exps.shape[1] > 1):
             raise ValueError("the rows of codes and exps must be contiguous")
-        self.codes, self.exps, self.dtype = _on_16(codes), _on_16(exps), dtype
+        codes, exps = _on_16(codes), _on_16(exps)
+        self.codes, self.exps, self.dtype = codes, exps, dtype
+        (n, d), blocks = codes.shape, exps.shape[0]
+        # addresses and row strides; a single row has no stride of its own
+        self._fields = (codes.data_ptr(), exps.data_ptr(), codes.stride(0) if n > 1 else _up16(d),
+                        exps.stride(0) if blocks > 1 else _up16(n))
 
     @property
     def shape(self):
@@ -45,12 +50,6 @@ class PackedActivation:
     @property
     def device(self):
         return self.codes.device
-
-    def _fields(self):
-        """(address of codes, of exps, their row strides); a single row has no stride of its own."""
-        c, e = self.codes, self.exps
-        return (c.data_ptr(), e.data_ptr(), c.stride(0) if c.shape[0] > 1 else _up16(c.shape[1]),
-                e.stride(0) if e.shape[0] > 1 else _up16(e.shape[1]))
 
 
 def _up16(n: int) -> int:
@@ -67,12 +66,13 @@ def _on_16(t):
 
 
 def _packed_like(n: int, d: int, device, dtype) -> PackedActivation:
-    """Room for n rows of d channels, rows on 16-byte strides, in one allocation."""
-    blocks, ld, le = (d + 127) // 128, _up16(d), _up16(n)
-    room = torch.empty(n * ld + blocks * le, dtype=torch.uint8, device=device)
+    """Room for n rows of d channels."""
+    ld, le, blocks = _up16(d), _up16(n), (d + 127) // 128
+    codes = torch.empty((n, ld), dtype=torch.uint8, device=device)
+    exps = torch.empty((blocks, le), dtype=torch.int8, device=device)
     p = PackedActivation.__new__(PackedActivation)
-    p.codes, p.dtype = room.as_strided((n, d), (ld, 1)), dtype
-    p.exps = room.view(torch.int8).as_strided((blocks, n), (le, 1), n * ld)
+    p._fields = codes.data_ptr(), exps.data_ptr(), ld, le
+    p.codes, p.exps, p.dtype = codes if ld == d else codes[:, :d], exps if le == n else exps[:, :n], dtype
     return p
 
 
@@ -89,11 +89,13 @@ def pack_activation(x) -> PackedActivation:
     needs of it: e4m3 codes with one power of two for every 128 channels of a
     row. A value comes back within 2**-4 of itself, or 2**-10 of its block's
     scale where that is more. `stream`: the stream to run on."""
-    x = _spread(x)
-    px, ld = _matrix("x", x)
+    try:
+        px, ld = _matrix("x", x)
+    except _Expanded:
+        return pack_activation(_spread(x))
     n, d = x.shape
     p = _packed_like(n, d, x.device, x.dtype)
-    codes, exps, ldc, lde = p._fields()
+    codes, exps, ldc, lde = p._fields
     _abi.check(_abi.lib().lce_pack8(_DT[x.dtype], px, ld, n, d, codes, ldc, exps, lde, _stream(x.device.index)), "lce_pack8")
     return p
 
@@ -116,7 +118,7 @@ def unpack_activation(p: PackedActivation, *, dtype=None, out=None):
             raise ValueError("dtype must be bfloat16 or float32")
         out = torch.empty((n, d), dtype=dtype, device=p.device)
     po, ld = _matrix("out", out)
-    codes, exps, ldc, lde = p._fields()
+    codes, exps, ldc, lde = p._fields
     _abi.check(_abi.lib().lce_unpack8(_DT[out.dtype], codes, ldc, exps, lde, n, d, po, ld, _stream(p.device.index)),
                "lce_unpack8")
     if given:
@@ -140,8 +142,10 @@ def packed_weight_grad(dy, x: PackedActivation, *, out=None, out_dtype=None, wor
     with out_dtype=torch.float32; `out` receives it. `workspace`: a uint8 CUDA
     tensor of at least packed_weight_grad_workspace_size bytes; `stream`: the
     stream to run on."""
-    dy = _spread(dy)
-    py, ld = _matrix("dy", dy)
+    try:
+        py, ld = _matrix("dy", dy)
+    except _Expanded:
+        return packed_weight_grad(_spread(dy), x, out=out, out_dtype=out_dtype, workspace=workspace)
     T, n = dy.shape
     if x.shape[0] != T or x.device != dy.device:
         raise ValueError("dy and x must have the same number of rows and one device")
@@ -161,7 +165,7 @@ def packed_weight_grad(dy, x: PackedActivation, *, out=None, out_dtype=None, wor
     need = packed_weight_grad_workspace_size(T, n, k, dy.dtype, out_dtype)
     if need:
         ws, size, keep = _scratch(workspace, need, dy.device)
-    codes, exps, ldc, lde = x._fields()
+    codes, exps, ldc, lde = x._fields
     args = _WGRAD.pack(_DT[dy.dtype], _DT[out_dtype], T, n, k, py, ld, codes, exps, ldc, lde, out.data_ptr(), ws, size,
                        _stream(dy.device.index))
     _abi.check(_abi.lib().lce_packed_wgrad(args), "lce_packed_wgrad")
@@ -224,12 +228,14 @@ def layer_norm_forward(x, b=None, *, weight, bias=None, eps: float = 1e-5, keep8
     or b; `stream`: the stream to run on. Expanded rows are copied first."""
     if x.dtype not in _DT or not x.is_cuda or x.dim() != 2:
         raise ValueError("the stream must be a bfloat16 or float32 CUDA tensor [N, d] (there is no CPU path)")
-    source = _spread(x)
-    px, ldx = _rows("x", source, x)
     pb = ldb = 0
-    if b is not None:
-        b = _spread(b)
-        pb, ldb = _rows("b", b, x)
+    try:
+        px, ldx = _rows("x", x, x)
+        if b is not None:
+            pb, ldb = _rows("b", b, x)
+    except _Expanded:
+        r, *rest = layer_norm_forward(_spread(x), _spread(b), weight=weight, bias=bias, eps=eps, keep8=keep8, out_r=out_r)
+        return x if b is None else r, *rest
     w = _vector("weight", weight, x)
     c = 0 if bias is None else _vector("bias", bias, x)
     (N, d), device = x.shape, x.device
@@ -245,11 +251,12 @@ def layer_norm_forward(x, b=None, *, weight, bias=None, eps: float = 1e-5, keep8
     elif out_r is not None:
         raise ValueError("without b, r is x itself: there is nothing to write to out_r")
     n = _like(x)
-    mean, rstd = torch.empty((2, N), dtype=torch.float32, device=device)
+    mean = torch.empty(N, dtype=torch.float32, device=device)
+    rstd = torch.empty_like(mean)
     kept, packed = None, (0, 0, 0, 0)
     if keep8:
         kept = _packed_like(N, d, device, x.dtype)
-        packed = kept._fields()
+        packed = kept._fields
     args = _LN.pack(_DT[x.dtype], N, d, eps, px, pb, w, c, ldx, ldb, pr, n.data_ptr(), mean.data_ptr(), rstd.data_ptr(), *packed,
                     0, 0, 0, 0, 0, 0, 0, 0, 0, 0, _stream(device.index))
     _abi.check(_abi.lib().lce_layer_norm_forward(args), "lce_layer_norm_forward")
@@ -267,20 +274,22 @@ def layer_norm_backward(dr, dn, r, *, weight, mean, rstd, bias: bool = True, wor
     on."""
     if dn.dtype not in _DT or not dn.is_cuda or dn.dim() != 2:
         raise ValueError("dn must be a bfloat16 or float32 CUDA tensor [N, d] (there is no CPU path)")
-    dn = _spread(dn)
-    pn, ldn = _rows("dn", dn, dn)
-    pd = ldd = 0
-    if dr is not None:
-        dr = _spread(dr)
-        pd, ldd = _rows("dr", dr, dn)
-    pr, ldr, packed = 0, 0, (0, 0, 0, 0)
-    if isinstance(r, PackedActivation):
+    kept = isinstance(r, PackedActivation)
+    pd = ldd = pr = ldr = 0
+    packed = (0, 0, 0, 0)
+    try:
+        pn, ldn = _rows("dn", dn, dn)
+        if dr is not None:
+            pd, ldd = _rows("dr", dr, dn)
+        if not kept:
+            pr, ldr = _rows("r", r, dn)
+    except _Expanded:
+        return layer_norm_backward(_spread(dr), _spread(dn), r if kept else _spread(r), weight=weight, mean=mean, rstd=rstd,
+                                   bias=bias, workspace=workspace)
+    if kept:
         if r.shape != dn.shape or r.device != dn.device:
             raise ValueError(f"the packed r must be {tuple(dn.shape)} on dn's device")
-        packed = r._fields()
-    else:
-        r = _spread(r)
-        pr, ldr = _rows("r", r, dn)
+        packed = r._fields
     w = _vector("weight", weight, dn)
     (N, d), device = dn.shape, dn.device
     for name, t in (("mean", mean), ("rstd", rstd)):
