@@ -304,10 +304,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_ln_fwd_ring(const LnArgs a,
                 }
             }
         }
-        __syncwarp();
-        if ((t & 31) == 0) mbar_arrive(&bars.empty[s]);   // everything is in registers
         float sum[1] = {hsum2(q)};
         group_sum(sum, my_red, flip, g.tpr, group, t);
+        __syncwarp();
+        if ((t & 31) == 0) mbar_arrive(&bars.empty[s]);   // everything is in registers: it has gone into the sum
         const float mean = sum[0] * inv_d;
         const f32x2 minus = both(-mean);
         q = both(0.f);

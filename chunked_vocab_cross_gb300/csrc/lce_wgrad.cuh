@@ -295,7 +295,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
                         rare |= e[j] > 7 || e[j] == kPackNaN;
                     }
                     rare = __any_sync(0xffffffffu, rare);
-                    if (lane == 0) mbar_arrive(&sm.empty_c[st]);
                     ok = __all_sync(0xffffffffu, wg_wait(&sm.empty_b[sb], it / kWgWide & 1 ^ 1, sm, a.status));
                     if (!ok) break;
                     uint8_t *to = wide + sb * kWgABytes;
@@ -319,7 +318,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
                     else widen(std::false_type());
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) wg_arrive(full_even + sb * 8);
+                    // The codes' place is given up only now that their widened forms are out. Given up after the loads alone,
+                    // an arrival could overtake loads that still waited in the queue behind the other warps' stores to memory.
+                    if (lane == 0) mbar_arrive(&sm.empty_c[st]), wg_arrive(full_even + sb * 8);
                 }
         }
     }

@@ -123,6 +123,16 @@ def test_weight_gradient(size, dtype, out_dtype):
     check_wgrad(*size, dtype, out_dtype)
 
 
+@pytest.mark.parametrize("size", [(512, 4096, 4096), (769, 4104, 2568), (2048, 2304, 4096)], ids=lambda s: "x".join(map(str, s)))
+def test_weight_gradient_of_more_tiles_than_run_at_once(size):
+    """A tile's output beside the next one's steps, again and again: the same bits each time."""
+    dy, p, got = check_wgrad(*size, "bf16", "fp32")
+    for _ in range(20):
+        assert torch.equal(lce.packed_weight_grad(dy, p, out_dtype=torch.float32), got)
+    if size[0] < 1000:
+        check_wgrad(*size, "fp32")
+
+
 def test_weight_gradient_of_slices_of_no_rows_and_into_a_given_tensor():
     dy, p, got = check_wgrad(500, 120, 264, "bf16", wide=40)
     out = torch.full((120 * 264 + 64,), 5.0, dtype=torch.bfloat16, device="cuda")
