@@ -643,12 +643,15 @@ lce_status_t launch_scan(const ScanArgs &r, const HostDev &dev, cudaStream_t st)
     ScanGeo geo;
     geo.tiles = (r.T + kTok - 1) / kTok;
     const int slices = (r.d + kSlice - 1) / kSlice;
-    // as many CTAs as find room at once, two on an SM where their memory allows it
+    // As many CTAs as find room at once, two on an SM where their memory allows it. The most of a group's time is the way of
+    // a tile through its CTA, so more of them at once pay until they contend; clusters of 16 have more to wait for and pay
+    // only where they leave SMs free (bf16: 16384 tokens of 4096 channels, clusters of 2, 4 and 8: 121, 85 and 97 us; 8192 of
+    // 2048: 64, 35 and 28, of 16: 46; 4096 of 1024, of 8 and 16: 16 and 21; 65536 of 1024: 168 and 161).
     auto step_bytes = [](int cluster) { return (kBack ? 2 : 1) * kWarps * kWarpStepBytes + 2 * cluster * kStepBytes; };
     auto stages = [&](int cluster) { return (kScanBytes - static_cast<int>(sizeof(ScanBars)) - step_bytes(cluster)) / kStageBytes; };
     geo.cluster = 1;
     while (geo.cluster < kMaxCluster && geo.cluster < geo.tiles &&
-           slices * geo.cluster * 2 <= (stages(geo.cluster * 2) < 2 ? 1 : 2) * dev.sms)
+           slices * geo.cluster * 2 <= (geo.cluster == 8 || stages(geo.cluster * 2) < 2 ? 1 : 2) * dev.sms)
         geo.cluster *= 2;
     geo.groups = (geo.tiles + geo.cluster - 1) / geo.cluster;
     const int steps = step_bytes(geo.cluster);

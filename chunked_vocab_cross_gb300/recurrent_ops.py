@@ -27,7 +27,7 @@ class PackedActivation:
     block held an infinity or NaN and stands for NaNs). Both have rows on
     16-byte strides, and are copied to such where they have not (brought back
     from host memory, say). `dtype`: of the tensor that was packed."""
-    __slots__ = ("codes", "exps", "dtype", "_fields")
+    __slots__ = ("shape", "dtype", "device", "_codes", "_exps", "_fields")
 
     def __init__(self, codes, exps, dtype):
         if codes.dtype != torch.uint8 or exps.dtype != torch.int8 or codes.dim() != 2 or exps.dim() != 2 or dtype not in _DT:
@@ -37,19 +37,19 @@ class PackedActivation:
         if (codes.stride(1) != 1 and codes.shape[1] > 1) or (exps.stride(1) != 1 and exps.shape[1] > 1):
             raise ValueError("the rows of codes and exps must be contiguous")
         codes, exps = _on_16(codes), _on_16(exps)
-        self.codes, self.exps, self.dtype = codes, exps, dtype
+        self.shape, self.dtype, self.device, self._codes, self._exps = codes.shape, dtype, codes.device, codes, exps
         (n, d), blocks = codes.shape, exps.shape[0]
         # addresses and row strides; a single row has no stride of its own
         self._fields = (codes.data_ptr(), exps.data_ptr(), codes.stride(0) if n > 1 else _up16(d),
                         exps.stride(0) if blocks > 1 else _up16(n))
 
     @property
-    def shape(self):
-        return self.codes.shape
+    def codes(self):
+        return self._codes[:, :self.shape[1]]
 
     @property
-    def device(self):
-        return self.codes.device
+    def exps(self):
+        return self._exps[:, :self.shape[0]]
 
 
 def _up16(n: int) -> int:
@@ -65,14 +65,15 @@ def _on_16(t):
     return room.copy_(t)
 
 
-def _packed_like(n: int, d: int, device, dtype) -> PackedActivation:
-    """Room for n rows of d channels."""
-    ld, le, blocks = _up16(d), _up16(n), (d + 127) // 128
-    codes = torch.empty((n, ld), dtype=torch.uint8, device=device)
-    exps = torch.empty((blocks, le), dtype=torch.int8, device=device)
+def _packed_like(x) -> PackedActivation:
+    """Room for the rows of x [N, d]."""
+    n, d = x.shape
+    ld, le, device = _up16(d), _up16(n), x.device
     p = PackedActivation.__new__(PackedActivation)
+    p.shape, p.dtype, p.device = x.shape, x.dtype, device
+    p._codes = codes = torch.empty((n, ld), dtype=torch.uint8, device=device)
+    p._exps = exps = torch.empty(((d + 127) // 128, le), dtype=torch.int8, device=device)
     p._fields = codes.data_ptr(), exps.data_ptr(), ld, le
-    p.codes, p.exps, p.dtype = codes if ld == d else codes[:, :d], exps if le == n else exps[:, :n], dtype
     return p
 
 
@@ -94,7 +95,7 @@ def pack_activation(x) -> PackedActivation:
     except _Expanded:
         return pack_activation(_spread(x))
     n, d = x.shape
-    p = _packed_like(n, d, x.device, x.dtype)
+    p = _packed_like(x)
     codes, exps, ldc, lde = p._fields
     _abi.check(_abi.lib().lce_pack8(_DT[x.dtype], px, ld, n, d, codes, ldc, exps, lde, _stream(x.device.index)), "lce_pack8")
     return p
@@ -255,7 +256,7 @@ def layer_norm_forward(x, b=None, *, weight, bias=None, eps: float = 1e-5, keep8
     rstd = torch.empty_like(mean)
     kept, packed = None, (0, 0, 0, 0)
     if keep8:
-        kept = _packed_like(N, d, device, x.dtype)
+        kept = _packed_like(x)
         packed = kept._fields
     args = _LN.pack(_DT[x.dtype], N, d, eps, px, pb, w, c, ldx, ldb, pr, n.data_ptr(), mean.data_ptr(), rstd.data_ptr(), *packed,
                     0, 0, 0, 0, 0, 0, 0, 0, 0, 0, _stream(device.index))
