@@ -25,9 +25,10 @@
 // and finally k_loss_final (loss = sum of the chunks' sums / Nv). With a
 // stored lse (lse_in), k_lse_from_input replaces steps 3-5.
 // The input-embedding lookup and its gradient (lce_embedding_*) are separate
-// entry points over the kernels of lce_embed.cuh; attention, the block norms
-// and gradient clipping are translation units of their own (lce_attn.cu,
-// lce_norm.cu, lce_clip.cu) over the shared host record of lce_host.h.
+// entry points over the kernels of lce_embed.cuh; attention, the norms, gradient
+// clipping, packed activations and the recurrence are translation units of their
+// own (lce_attn.cu, lce_norm.cu, lce_layer_norm.cu, lce_clip.cu, lce_pack.cu,
+// lce_scan.cu) over the shared host record of lce_host.h.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>

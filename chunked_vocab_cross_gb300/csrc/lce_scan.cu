@@ -140,7 +140,7 @@ struct TileSeqs {
 struct ScanBars {
     uint64_t full[kMaxStages], done[kMaxStages], steps[2];
     uint32_t flags[kTok];
-    TileSeqs seqs[kMaxStages + 1];   // one more than tiles, since a tile's are read until its results are out
+    TileSeqs seqs[kMaxStages + 1];   // one more than tiles: the forward gives up a tile before its sequences
 };
 // Steps of a warp's channels; 32 bytes apart, so that the lanes that join two warps each meet in no more banks than they must.
 constexpr int kStepBytes = 32 * 16, kWarpStepBytes = kStepBytes + 32;
@@ -217,19 +217,17 @@ __device__ __forceinline__ void store_remote(uint32_t addr, float a, float b, ui
                  : "memory");
 }
 
-// A bounded wait; after one that gave up the thread makes no other and goes
-// through the rest with whatever is there, in step with the others.
+// A bounded wait of a warp; after one that gave up the warp makes no other and
+// goes through the rest with whatever is there, in step with the others.
 __device__ __forceinline__ void scan_wait(uint64_t *bar, uint32_t parity, bool &lost, int *status) {
     if (lost) return;
     const uint32_t at = smem_u32(bar);
-    if (mbar_try_wait(at, parity)) return;
-    const long long t0 = clock64();
-    while (!mbar_try_wait(at, parity))
-        if (clock64() - t0 > kScanWaitCycles) {
-            atomicOr(status, LCE_DEV_TIMEOUT);
-            lost = true;
-            return;
-        }
+    if (!mbar_try_wait(at, parity)) {
+        const long long t0 = clock64();
+        while (!lost && !mbar_try_wait(at, parity)) lost = clock64() - t0 > kScanWaitCycles;
+        if (lost) atomicOr(status, LCE_DEV_TIMEOUT);
+    }
+    lost = __any_sync(0xffffffffu, lost);
 }
 
 // Where sequences begin and end in a tile, by one warp, which keeps the ends of
@@ -523,7 +521,6 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan(const ScanArgs a, cons
             if (lane == 0) mbar_arrive(&sm.done[s]);
             if (asks) {
                 scan_wait(&sm.done[s], phase, lost, a.status);
-                lost = __any_sync(0xffffffffu, lost);
                 if (!lost) ask();
             }
         }

@@ -534,7 +534,7 @@ size_t lce_layer_norm_workspace_size(const lce_layer_norm_t *args);
  * Magnitudes beyond 448 * 2^119 = 2.98e38 come back as that.
  * codes: [N] rows of d bytes, ld_codes apart (a multiple of 16, at least d);
  * exps: int8 [ceil(d/128)][N], rows ld_exps apart (a multiple of 16, at least
- * N). x and out are of `dtype`, rows ld_x and ld_out elements apart (0 stands
+ * N); d and N rounded up to 16 bytes of every row, the last too, may be read. x and out are of `dtype`, rows ld_x and ld_out elements apart (0 stands
  * for d). d % 8 == 0, 8 <= d < 2^24, 0 <= N < 2^31, bases 16-byte aligned, row strides
  * multiples of 16 bytes.
  */
