@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include "row_ring.cuh"
+
 namespace lce {
 
 constexpr int kPackBlock = 128;              // channels of a block
@@ -37,15 +39,19 @@ __device__ __forceinline__ void from_codes(uint32_t codes, float &a, float &b) {
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}" : "=f"(a), "=f"(b) : "r"(h));
 }
 
-// Eight values of a row, their block's other values with the 15 neighbouring
-// lanes of an aligned group of 16: the largest magnitude's bits among them all.
-__device__ __forceinline__ uint32_t block_top(const float (&x)[8]) {
-    uint32_t top = 0;
+// The bits of the largest magnitude of a block, of which this lane has the
+// words `w` and each other lane of an aligned group of kLanes its own. Magnitudes
+// compare as integers, bf16 ones two at a time.
+template <typename T, int kWords, int kLanes>
+__device__ __forceinline__ uint32_t block_top(const uint32_t (&w)[kWords]) {
+    constexpr uint32_t kMask = sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu;
+    auto larger = [](uint32_t a, uint32_t b) { return sizeof(T) == 2 ? __vmaxu2(a, b) : max(a, b); };
+    uint32_t top = w[0] & kMask;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    for (int i = 1; i < kWords; ++i) top = larger(top, w[i] & kMask);
 #pragma unroll
-    for (int m = 8; m; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-    return top;
+    for (int m = kLanes / 2; m; m >>= 1) top = larger(top, __shfl_xor_sync(0xffffffffu, top, m));
+    return sizeof(T) == 2 ? max(top << 16, top & 0xffff0000u) : top;
 }
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
     return make_uint2(to_codes(x[0] * scale, x[1] * scale) | to_codes(x[2] * scale, x[3] * scale) << 16,
@@ -56,6 +62,31 @@ __device__ __forceinline__ void values8(uint2 c, float scale, float (&x)[8]) {
     from_codes(c.y, x[4], x[5]), from_codes(c.y >> 16, x[6], x[7]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] *= scale;
+}
+
+// The codes of a pack's values, and from them
+template <typename T>
+__device__ __forceinline__ uint2 pack_codes(const f32x2 (&x)[kPack<T> / 2], float scale) {
+    uint32_t c[kPack<T> / 2];
+    const f32x2 f = both(scale);
+#pragma unroll
+    for (int i = 0; i < kPack<T> / 2; ++i) {
+        float a, b;
+        unpack2(mul2(x[i], f), a, b);
+        c[i] = to_codes(a, b);
+    }
+    return sizeof(T) == 2 ? make_uint2(c[0] | c[1] << 16, c[kPack<T> / 2 - 2] | c[kPack<T> / 2 - 1] << 16) : make_uint2(c[0] | c[1] << 16, 0);
+}
+template <typename T>
+__device__ __forceinline__ void pack_values(uint2 codes, float scale, f32x2 (&x)[kPack<T> / 2]) {
+    const uint32_t w[2] = {codes.x, codes.y};   // (fp32: the first alone)
+    const f32x2 f = both(scale);
+#pragma unroll
+    for (int i = 0; i < kPack<T> / 2; ++i) {
+        float a, b;
+        from_codes(w[i / 2] >> (i % 2 * 16), a, b);
+        x[i] = mul2(pack2(a, b), f);
+    }
 }
 
 }  // namespace lce

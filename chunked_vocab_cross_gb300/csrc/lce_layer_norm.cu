@@ -56,7 +56,10 @@ __global__ void __launch_bounds__(512) k_ln_fwd(const LnArgs a) {
 #pragma unroll
         for (int i = 0; i < kVec; ++i) s[0] += r[c][i];
         if (a.codes) {
-            const int e = pack_exponent(block_top(r[c]));
+            uint32_t bits[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) bits[i] = __float_as_uint(r[c][i]);
+            const int e = pack_exponent(block_top<float, kVec, kPackBlock / kVec>(bits));
             if (col < d) {
                 *reinterpret_cast<uint2 *>(a.codes + row * a.ld_codes + col) = codes8(r[c], pack_scale(e));
                 if (col % kPackBlock == 0) a.exps[col / kPackBlock * a.ld_exps + row] = static_cast<int8_t>(e);
@@ -199,31 +202,6 @@ __device__ __forceinline__ void load_row(uint8_t *dst, const void *w, int row_by
         *reinterpret_cast<uint4 *>(dst + i) = w ? *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(w) + i) : make_uint4(0, 0, 0, 0);
 }
 
-// The codes of a pack's values, and from them
-template <typename T>
-__device__ __forceinline__ uint2 pack_codes(const f32x2 (&x)[kPack<T> / 2], float scale) {
-    uint32_t c[kPack<T> / 2];
-#pragma unroll
-    for (int i = 0; i < kPack<T> / 2; ++i) {
-        float a, b;
-        unpack2(x[i], a, b);
-        c[i] = to_codes(a * scale, b * scale);
-    }
-    return sizeof(T) == 2 ? make_uint2(c[0] | c[1] << 16, c[kPack<T> / 2 - 2] | c[kPack<T> / 2 - 1] << 16) : make_uint2(c[0] | c[1] << 16, 0);
-}
-template <typename T>
-__device__ __forceinline__ void pack_values(const uint8_t *p, float scale, f32x2 (&x)[kPack<T> / 2]) {
-    uint32_t w[2] = {*reinterpret_cast<const uint32_t *>(p), 0};
-    if (sizeof(T) == 2) w[1] = *reinterpret_cast<const uint32_t *>(p + 4);
-    const f32x2 f = both(scale);
-#pragma unroll
-    for (int i = 0; i < kPack<T> / 2; ++i) {
-        float a, b;
-        from_codes(w[i / 2] >> (i % 2 * 16), a, b);
-        x[i] = mul2(pack2(a, b), f);
-    }
-}
-
 // Forward. kAdd: there is a block's output to add; kKeep: r is packed as well (a
 // block of 128 channels lies in 16 lanes' packs of bf16, in a warp's of fp32).
 template <typename T, int CH, bool kAdd, bool kKeep>
@@ -278,22 +256,15 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_ln_fwd_ring(const LnArgs a,
                 Pack16<T>::get(v, b);
 #pragma unroll
                 for (int i = 0; i < P; ++i) b[i] = add2(r[c][i], b[i]);
-                v = Pack16<T>::set(b);
-                if (live && in) __stcs(reinterpret_cast<uint4 *>(out_r + c * g.tpr * 16), v);
-                Pack16<T>::get(v, r[c]);   // as it is stored
+                x = Pack16<T>::set(b);
+                if (live && in) __stcs(reinterpret_cast<uint4 *>(out_r + c * g.tpr * 16), x);
+                Pack16<T>::get(x, r[c]);   // as it is stored
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) q = add2(q, r[c][i]);
             if (kKeep) {
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    float lo, hi;
-                    unpack2(r[c][i], lo, hi);
-                    top = max(top, max(__float_as_uint(lo) & 0x7fffffffu, __float_as_uint(hi) & 0x7fffffffu));
-                }
-#pragma unroll
-                for (int m = kPackBlock / V / 2; m; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+                const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+                const uint32_t top = block_top<T, 4, kPackBlock / V>(words);
                 const int e = pack_exponent(top), col = (c * g.tpr + t) * V;
                 const uint2 codes = pack_codes<T>(r[c], pack_scale(e));
                 if (live && in) {
@@ -429,7 +400,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_ln_bwd_ring(const LnArgs a,
                     for (int i = 0; i < P; ++i) hat[k][c][i] = u[k][c][i] = both(0.f);
                     continue;
                 }
-                if (kCodes) pack_values<T>(stage + (group * R + k) * g.bytes[0] + (c * g.tpr + t) * V, scale[k][c], hat[k][c]);
+                if (kCodes) {
+                    const uint8_t *from = stage + (group * R + k) * g.bytes[0] + (c * g.tpr + t) * V;
+                    const uint2 codes = sizeof(T) == 2 ? *reinterpret_cast<const uint2 *>(from) : make_uint2(*reinterpret_cast<const uint32_t *>(from), 0);
+                    pack_values<T>(codes, scale[k][c], hat[k][c]);
+                }
                 else Pack16<T>::get(*reinterpret_cast<const uint4 *>(stage + (group * R + k) * g.bytes[0] + byte), hat[k][c]);
                 Pack16<T>::get(*reinterpret_cast<const uint4 *>(stage + g.at[1] + (group * R + k) * g.row_bytes + byte), u[k][c]);
                 const f32x2 minus = both(-mean[k]), f = both(rs[k]);
