@@ -45,32 +45,27 @@ template <typename T>
 struct Lane;
 template <>
 struct Lane<__nv_bfloat16> {
-    using F = f32x2;
-    static constexpr int kCh = 2;
-    static __device__ __forceinline__ F get(uint32_t w) { return pack2u(w << 16, w & 0xffff0000u); }
-    static __device__ __forceinline__ uint32_t put(F v) {
+    struct F {
         float a, b;
-        unpack2(v, a, b);
-        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    };
+    static constexpr int kCh = 2;
+    static __device__ __forceinline__ F get(uint32_t w) { return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)}; }
+    static __device__ __forceinline__ uint32_t put(F v) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v.a, v.b);
         return *reinterpret_cast<const uint32_t *>(&p);
     }
-    static __device__ __forceinline__ F all(float v) { return both(v); }
-    static __device__ __forceinline__ F fma(F a, F b, F c) { return fma2(a, b, c); }
-    static __device__ __forceinline__ F mul(F a, F b) { return mul2(a, b); }
-    static __device__ __forceinline__ F add(F a, F b) { return add2(a, b); }
-    static __device__ __forceinline__ float first(F v) {
-        float a, b;
-        unpack2(v, a, b);
-        return a;
-    }
+    static __device__ __forceinline__ F all(float v) { return {v, v}; }
+    static __device__ __forceinline__ F fma(F a, F b, F c) { return {fmaf(a.a, b.a, c.a), fmaf(a.b, b.b, c.b)}; }
+    static __device__ __forceinline__ F mul(F a, F b) { return {a.a * b.a, a.b * b.b}; }
+    static __device__ __forceinline__ F add(F a, F b) { return {a.a + b.a, a.b + b.b}; }
+    static __device__ __forceinline__ float first(F v) { return v.a; }
     template <typename G>
-    static __device__ __forceinline__ F each(F v, G g) {
-        float a, b;
-        unpack2(v, a, b);
-        return pack2(g(a), g(b));
+    static __device__ __forceinline__ F each(F v, G g) { return {g(v.a), g(v.b)}; }
+    static __device__ __forceinline__ F load(const float *p) {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        return {v.x, v.y};
     }
-    static __device__ __forceinline__ F load(const float *p) { return *reinterpret_cast<const F *>(p); }
-    static __device__ __forceinline__ void save(float *p, F v) { *reinterpret_cast<F *>(p) = v; }
+    static __device__ __forceinline__ void save(float *p, F v) { *reinterpret_cast<float2 *>(p) = make_float2(v.a, v.b); }
 };
 template <>
 struct Lane<float> {
@@ -129,6 +124,17 @@ __device__ __forceinline__ typename L::F apply(const Step<L> &s, typename L::F b
 // the places where sequences begin and end in them, which the copying warp looks
 // up. The backward forms h of a tile again from the state kept before it, which
 // needs no other tile, and goes through the tiles from the last.
+//
+// What bounds it in bf16 is a tile's way through its CTA: about 5000 cycles, of
+// which the gates are 1000, the joins with their barriers and the exchange 2000,
+// the asking warp's work 800 and the tokens' second time 700, and two CTAs share
+// an SM: 16384 tokens of 4096 channels in 81 us (5.0 TB/s, 73% of the copy rate),
+// backward 139 us (4.8 TB/s); fp32, half the channels a byte, 65 us for 8192
+// tokens (6.2 TB/s, 91%). Neither its arithmetic nor its stores: without
+// exponentials and reciprocals, or without stores, it takes as long. Tried: lanes
+// along time, joined by shuffles alone (copies of 2 KB, partial lines: 112 us
+// where this stood at 90); one reciprocal for two gates (+8%: the case of a NaN is
+// a branch); pairs of channels in packed arithmetic (the same).
 constexpr int kTok = kEvery, kWarps = 8, kPer = kTok / kWarps, kScanThreads = kWarps * 32;
 constexpr int kTileBytes = kTok * 128, kMaxCluster = 16, kMaxStages = 3;
 constexpr long long kScanWaitCycles = 2000000000LL;   // ~1 s: far above any legitimate wait
@@ -156,9 +162,7 @@ struct ScanGeo {
 template <typename L>
 __device__ __forceinline__ void save_step(uint8_t *p, const Step<L> &s) {
     if constexpr (L::kCh == 2) {
-        float4 v;
-        unpack2(s.A, v.x, v.z), unpack2(s.H, v.y, v.w);
-        *reinterpret_cast<float4 *>(p) = v;
+        *reinterpret_cast<float4 *>(p) = make_float4(s.A.a, s.H.a, s.A.b, s.H.b);
     } else {
         *reinterpret_cast<float2 *>(p) = make_float2(s.A, s.H);
     }
@@ -167,7 +171,7 @@ template <typename L>
 __device__ __forceinline__ Step<L> load_step(const uint8_t *p) {
     if constexpr (L::kCh == 2) {
         const float4 v = *reinterpret_cast<const float4 *>(p);
-        return Step<L>{pack2(v.x, v.z), pack2(v.y, v.w)};
+        return Step<L>{{v.x, v.z}, {v.y, v.w}};
     } else {
         const float2 v = *reinterpret_cast<const float2 *>(p);
         return Step<L>{v.x, v.y};
@@ -253,9 +257,24 @@ struct SeqFinder {
         if (s >= t0 && s < t0 + kTok) out.seq[s - t0] = mine, atomicOr(&flags[s - t0], 1u);
         if (e > t0 && e <= t0 + kTok) out.seq[e - 1 - t0] = mine, atomicOr(&flags[e - 1 - t0], 2u);
     }
+    // The ends of the tile from t0 on. Most tiles have none, and all warps wait
+    // for the one that looks: that is settled first (16384 tokens of 4096 channels
+    // bf16: 84 us with the full account of every tile, 81 this way).
     template <bool kBack>
     __device__ __forceinline__ void operator()(int t0, TileSeqs &out) {
         const int lane = threadIdx.x & 31;
+        bool plain;   // within one sequence, neither its first token nor its last among them
+        if (a.cu) {
+            plain = holds(t0) && t0 + kTok <= live &&
+                    !__any_sync(0xffffffffu, e > s && ((s >= t0 && s < t0 + kTok) || (e > t0 && e <= t0 + kTok)));
+        } else {
+            const int at = t0 % a.len;
+            plain = at > 0 && at + kTok < a.len;
+        }
+        if (plain) {
+            if (lane < kTok / 32) out.begin[lane] = out.end[lane] = out.dead[lane] = 0;
+            return;
+        }
         if (!a.cu) {
 #pragma unroll
             for (int k = 0; k < kTok / 32; ++k) {
