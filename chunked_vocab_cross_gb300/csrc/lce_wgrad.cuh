@@ -56,6 +56,7 @@ struct WgArgs {
     int whole;        // n is a multiple of 64: dy has a three-dimensional map
     int mt, nt;       // tiles along n and k
     int steps, per;   // of 64 tokens; of a split
+    int run;          // steps that an accumulator takes: of an fp32 dy few, and the runs of a tile are added up in fp32 in memory
     int splits;
     int *status;
 };
@@ -165,8 +166,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
             for (int u = pair; ok && u < units; u += pairs) {
                 const WgUnit w = wg_unit(a, u);
                 const int n0 = w.m * kWgTile + rank * kWgHalf;
-                for (int part = a.parts - 1; ok && part >= 0; --part)   // the small parts first
-                    for (int step = w.k0; step < w.k1; ++step, ++it) {
+                for (int k = w.k0; ok && k < w.k1; k += a.run)
+                  for (int part = a.parts - 1; ok && part >= 0; --part)   // the small parts first
+                    for (int step = k; step < min(k + a.run, w.k1); ++step, ++it) {
                         const int st = it % kWgDy, t0 = step * kWgK;
                         if (!(ok = wg_wait(&sm.empty_a[st], it / kWgDy & 1 ^ 1, sm, a.status))) break;
                         if (rank == 0) mbar_arrive_expect_tx(&sm.full_a[st], 2 * kWgABytes);
@@ -188,8 +190,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
             for (int u = pair; ok && u < units; u += pairs) {
                 const WgUnit w = wg_unit(a, u);
                 const int k0 = w.n * kWgTile + rank * kWgHalf, block = k0 / kPackBlock;
-                for (int part = 0; ok && part < a.parts; ++part)
-                    for (int step = w.k0; step < w.k1; ++step, ++it) {
+                for (int k = w.k0; ok && k < w.k1; k += a.run)
+                  for (int part = 0; ok && part < a.parts; ++part)
+                    for (int step = k; step < min(k + a.run, w.k1); ++step, ++it) {
                         const int st = it % kWgCodes, t0 = step * kWgK;
                         if (!(ok = wg_wait(&sm.empty_c[st], it / kWgCodes & 1 ^ 1, sm, a.status))) break;
                         const uint32_t bytes = block < blocks ? min(kWgK, (a.T - t0 + 15) & ~15) : 0;   // rows of exps are of whole 16 bytes
@@ -204,29 +207,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
         if (rank == 0) {
             const bool issue = elect_one();
             int it = 0, tile = 0;
-            for (int u = pair; ok && u < units; u += pairs, ++tile) {
+            for (int u = pair; ok && u < units; u += pairs) {
                 const WgUnit w = wg_unit(a, u);
-                const int acc = tile & 1, steps = (w.k1 - w.k0) * a.parts;
-                if (!(ok = wg_wait(&sm.empty_t[acc], tile >> 1 & 1 ^ 1, sm, a.status))) break;
-                tc_fence_after();
-                for (int i = 0; i < steps; ++i, ++it) {
-                    const int st = it % kWgDy, sb = it % kWgWide;
-                    ok = wg_wait(&sm.full_a[st], it / kWgDy & 1, sm, a.status) && wg_wait(&sm.full_b[sb], it / kWgWide & 1, sm, a.status);
-                    ok = __all_sync(0xffffffffu, ok);
+                for (int k = w.k0; ok && k < w.k1; k += a.run, ++tile) {
+                    const int acc = tile & 1, steps = (min(k + a.run, w.k1) - k) * a.parts;
+                    ok = __all_sync(0xffffffffu, wg_wait(&sm.empty_t[acc], tile >> 1 & 1 ^ 1, sm, a.status));
                     if (!ok) break;
                     tc_fence_after();
-                    if (issue) {
-                        const uint32_t pa = smem_u32(smem + st * kWgABytes), pb = smem_u32(wide + sb * kWgABytes);
+                    for (int i = 0; i < steps; ++i, ++it) {
+                        const int st = it % kWgDy, sb = it % kWgWide;
+                        ok = wg_wait(&sm.full_a[st], it / kWgDy & 1, sm, a.status) && wg_wait(&sm.full_b[sb], it / kWgWide & 1, sm, a.status);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (issue) {
+                            const uint32_t pa = smem_u32(smem + st * kWgABytes), pb = smem_u32(wide + sb * kWgABytes);
 #pragma unroll
-                        for (int kk = 0; kk < kWgK / 16; ++kk)
-                            umma_f16_pair(tmem + acc * kWgTile, sdesc_sw128(pa + kk * 2048, kWgBlockBytes, 1024),
-                                          sdesc_sw128(pb + kk * 2048, kWgBlockBytes, 1024), kIdesc, (i | kk) != 0);
-                        umma_commit_pair_mc(&sm.empty_a[st], 3);
-                        umma_commit_pair_mc(&sm.empty_b[sb], 3);
+                            for (int kk = 0; kk < kWgK / 16; ++kk)
+                                umma_f16_pair(tmem + acc * kWgTile, sdesc_sw128(pa + kk * 2048, kWgBlockBytes, 1024),
+                                              sdesc_sw128(pb + kk * 2048, kWgBlockBytes, 1024), kIdesc, (i | kk) != 0);
+                            umma_commit_pair_mc(&sm.empty_a[st], 3);
+                            umma_commit_pair_mc(&sm.empty_b[sb], 3);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (ok && issue) umma_commit_pair_mc(&sm.full_t[acc], 3);
                 }
-                if (ok && issue) umma_commit_pair_mc(&sm.full_t[acc], 3);
             }
             if (issue) {
                 umma_commit_pair_mc(&sm.done, 1);
@@ -237,39 +243,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
         const uint32_t empty_even = map_to_cta(smem_u32(sm.empty_t), 0);
         const int quarter = warp & 3;
         int tile = 0;
-        for (int u = pair; ok && u < units; u += pairs, ++tile) {
+        for (int u = pair; ok && u < units; u += pairs) {
             const WgUnit w = wg_unit(a, u);
-            const int acc = tile & 1, row = w.m * kWgTile + rank * kWgHalf + quarter * 32 + lane, col0 = w.n * kWgTile;
-            ok = __all_sync(0xffffffffu, wg_wait(&sm.full_t[acc], tile >> 1 & 1, sm, a.status));
-            if (!ok) break;
-            tc_fence_after();
+            const int row = w.m * kWgTile + rank * kWgHalf + quarter * 32 + lane, col0 = w.n * kWgTile;
             O *out = static_cast<O *>(a.out) + (static_cast<int64_t>(w.split) * a.n + row) * a.k + col0;
-            for (int c = 0; c < kWgTile && col0 + c < a.k; c += 32) {
-                uint32_t v[32];
-                tmem_ld32(tmem + acc * kWgTile + c + (static_cast<uint32_t>(quarter * 32) << 16), v);
-                tmem_ld_wait();
+            for (int k = w.k0; k < w.k1; k += a.run, ++tile) {
+                const int acc = tile & 1;
+                ok = __all_sync(0xffffffffu, wg_wait(&sm.full_t[acc], tile >> 1 & 1, sm, a.status));
+                if (!ok) break;
+                tc_fence_after();
+                for (int c = 0; c < kWgTile && col0 + c < a.k; c += 32) {
+                    uint32_t v[32];
+                    float4 sum[sizeof(O) == 2 ? 1 : 8];   // of the runs before, in flight together
+                    if constexpr (sizeof(O) == 4) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    if (row >= a.n || col0 + c + i >= a.k) continue;   // (k is a multiple of 8)
-                    if constexpr (sizeof(O) == 2) {
-                        uint4 x;
-                        uint32_t *p = &x.x;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
-                            p[j] = *reinterpret_cast<const uint32_t *>(&h);
-                        }
-                        *reinterpret_cast<uint4 *>(out + c + i) = x;
-                    } else {
-                        *reinterpret_cast<uint4 *>(out + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                        *reinterpret_cast<uint4 *>(out + c + i + 4) = make_uint4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
+                        for (int i = 0; i < 32; i += 4)
+                            sum[i / 4] = k > w.k0 && row < a.n && col0 + c + i < a.k ? *reinterpret_cast<const float4 *>(out + c + i) : float4{};
                     }
+                    tmem_ld32(tmem + acc * kWgTile + c + (static_cast<uint32_t>(quarter * 32) << 16), v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        if (row >= a.n || col0 + c + i >= a.k) continue;   // (k is a multiple of 8)
+                        if constexpr (sizeof(O) == 2) {
+                            uint4 x;
+                            uint32_t *p = &x.x;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
+                                p[j] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
+                            *reinterpret_cast<uint4 *>(out + c + i) = x;
+                        } else {
+#pragma unroll
+                            for (int j = i; j < i + 8; j += 4)
+                                *reinterpret_cast<float4 *>(out + c + j) =
+                                    make_float4(sum[j / 4].x + __uint_as_float(v[j]), sum[j / 4].y + __uint_as_float(v[j + 1]),
+                                                sum[j / 4].z + __uint_as_float(v[j + 2]), sum[j / 4].w + __uint_as_float(v[j + 3]));
+                        }
+                    }
+                    __syncwarp();   // the next load is the whole warp's
                 }
-                __syncwarp();   // the next load is the whole warp's
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(empty_even + acc * 8);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(empty_even + acc * 8);
         }
     } else if (warp >= kWgFirst) {
         // The groups take steps in turn: each has the time of four for one, which hides the waits, the fence and the way to
@@ -285,8 +303,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1) k_wgr
         int it = 0;
         for (int u = pair; ok && u < units; u += pairs) {
             const WgUnit w = wg_unit(a, u);
-            for (int part = 0; ok && part < a.parts; ++part)
-                for (int step = w.k0; step < w.k1; ++step, ++it) {
+            for (int k = w.k0; ok && k < w.k1; k += a.run)
+              for (int part = 0; ok && part < a.parts; ++part)
+                for (int step = k; step < min(k + a.run, w.k1); ++step, ++it) {
                     if (it % kWgGroups != group) continue;
                     const int st = it % kWgCodes, sb = it % kWgWide;
                     ok = __all_sync(0xffffffffu, wg_wait(&sm.full_c[st], it / kWgCodes & 1, sm, a.status));
