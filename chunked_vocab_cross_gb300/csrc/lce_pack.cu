@@ -182,7 +182,21 @@ int splits(const lce_wgrad_t *a) {
     const int64_t per = (steps + best - 1) / best;   // no split without steps
     return static_cast<int>(steps > 0 ? (steps + per - 1) / per : 1);
 }
-size_t split_bytes(const lce_wgrad_t *a, int s) { return s > 1 ? static_cast<size_t>(s) * a->n * a->k * sizeof(float) : 0; }
+// Steps that an accumulator takes. The tensor cores truncate their fp32 sums, which is a loss in one direction that grows
+// with the number of additions, so longer sums are those of runs, added up in fp32 in memory. Off by, of the norm (all terms
+// positive; in brackets terms of random signs), and the time:
+//   fp32 dy, 8192 tokens: runs of 8 steps 3.2e-7 (1.7e-7), 12 5.5e-7, 16 8.3e-7, one run 1.3e-5 (3.6e-6), a product of
+//     plain fp32 1.3e-6 (1.6e-6); 4096 tokens, 4096 x 4096: 533, 471, 398 us for runs of 8, 12 and 16, 295 in one
+//   bf16 dy, fp32 dw, 7373 tokens: 8 2.5e-7 (1.6e-7), 16 6.7e-7 (2.9e-7), 32 1.7e-6 (6.0e-7), one run 1.0e-5 (3.2e-6), plain
+//     7.7e-7 (3.4e-7); 4096 tokens, 4096 x 4096: 388, 224, 145 us for runs of 8, 16 and 32, 111 in one; 7373 tokens,
+//     16384 x 4096: 2515, 1505, 955 and 584
+// A bf16 dw is rounded by up to 2^-8 anyway: 32768 tokens (off by 9e-5; 65536 by 1.8e-4, 262144 by 7e-4) are one run.
+int longest_run(const lce_wgrad_t *a) { return a->dw_dtype == LCE_BF16 ? 512 : a->dtype == LCE_FP32 ? 8 : 16; }
+// A bf16 dw of several splits or runs is rounded from fp32 sums in scratch, by the join.
+bool through_scratch(const lce_wgrad_t *a, int s) {
+    return s > 1 || (a->dw_dtype == LCE_BF16 && a->T > static_cast<int64_t>(longest_run(a)) * kWgK);
+}
+size_t split_bytes(const lce_wgrad_t *a, int s) { return through_scratch(a, s) ? static_cast<size_t>(s) * a->n * a->k * sizeof(float) : 0; }
 int64_t part_columns(const lce_wgrad_t *a) { return (a->n + 63) / 64 * 64; }
 size_t part_bytes(const lce_wgrad_t *a) { return a->dtype == LCE_FP32 ? static_cast<size_t>(a->T) * part_columns(a) * 6 : 0; }
 
@@ -208,16 +222,12 @@ lce_status_t wgrad(const lce_wgrad_t *a, const HostDev &dev, uint8_t *scratch, c
     const int64_t ld = a->ld_dy ? a->ld_dy : a->n;
     r.exps = a->exps, r.ld_exps = a->ld_exps, r.T = static_cast<int>(a->T), r.n = static_cast<int>(a->n), r.k = static_cast<int>(a->k);
     r.mt = (r.n + kWgTile - 1) / kWgTile, r.nt = (r.k + kWgTile - 1) / kWgTile, r.steps = (r.T + kWgK - 1) / kWgK;
-    r.splits = splits(a), r.per = (r.steps + r.splits - 1) / r.splits, r.status = dev.status;
+    r.splits = splits(a), r.per = (r.steps + r.splits - 1) / r.splits, r.run = longest_run(a), r.status = dev.status;
     if (!encode_codes(&maps.codes, dev, a->codes, a->T, a->k, a->ld_codes)) return LCE_ERR_SHAPE;
     if (a->dtype == LCE_FP32) {
         const int64_t wide = part_columns(a), size = a->T * wide;
         auto *parts = reinterpret_cast<__nv_bfloat16 *>(scratch + split_bytes(a, r.splits));
-        // Tensor cores truncate their fp32 sums. In runs of 8 steps that are added up in memory the gradient of 8192 tokens is
-        // off by 1.7e-7 of its norm (3.2e-7 where all terms are positive); in one run by 3.6e-6 (1.3e-5), in runs of 12 or
-        // 16 by 5.5e-7 or 8.3e-7 at worst, and a product of plain fp32 by 1.6e-6 (1.3e-6). 4096 tokens, 4096 x 4096: 533 us, in one run
-        // 295, in runs of 12 or 16 471 or 398.
-        r.parts = 3, r.whole = 1, r.run = 8;
+        r.parts = 3, r.whole = 1;
         for (int p = 0; p < 3; ++p)
             if (!encode_dy(&maps.dy[p], dev, parts + p * size, a->T, wide, wide, true)) return LCE_ERR_SHAPE;
         k_wgrad_parts<<<static_cast<unsigned>((size / 4 + 255) / 256), 256, 0, st>>>(static_cast<const float *>(a->dy), ld, r.T, r.n,
@@ -225,11 +235,11 @@ lce_status_t wgrad(const lce_wgrad_t *a, const HostDev &dev, uint8_t *scratch, c
         const lce_status_t s = host_launched();
         if (s != LCE_OK) return s;
     } else {
-        r.parts = 1, r.whole = a->n % 64 == 0, r.run = std::max(r.per, 1);
+        r.parts = 1, r.whole = a->n % 64 == 0;
         if (!encode_dy(&maps.dy[0], dev, a->dy, a->T, a->n, ld, r.whole != 0)) return LCE_ERR_SHAPE;
     }
     const int units = r.mt * r.nt * r.splits, grid = 2 * std::min(units, dev.sms / 2);
-    if (r.splits == 1) {
+    if (!through_scratch(a, r.splits)) {
         r.out = a->dw;
         const lce_status_t s = host_smem<k_wgrad<O>>(dev, kWgSmem);
         if (s != LCE_OK) return s;

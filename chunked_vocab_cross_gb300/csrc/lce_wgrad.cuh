@@ -56,7 +56,7 @@ struct WgArgs {
     int whole;        // n is a multiple of 64: dy has a three-dimensional map
     int mt, nt;       // tiles along n and k
     int steps, per;   // of 64 tokens; of a split
-    int run;          // steps that an accumulator takes: of an fp32 dy few, and the runs of a tile are added up in fp32 in memory
+    int run;          // steps that an accumulator takes; the runs of a unit are added up in fp32 in memory (a bf16 out has one)
     int splits;
     int *status;
 };

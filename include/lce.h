@@ -551,9 +551,10 @@ lce_status_t lce_unpack8(lce_dtype_t dtype, const uint8_t *codes, int64_t ld_cod
  * or bf16 with a bf16 dy), contiguous, rounded once from fp32 sums. bf16 dy
  * runs on the bf16 tensor cores with the codes widened on the way to them; an
  * fp32 dy is taken as three bf16 parts, which hold it exactly (but for parts
- * below 1.2e-38, that is values below 2^-109), and its sums over 512 tokens,
- * which the tensor cores take, are added up in fp32. Sums are in a fixed order
- * (deterministic). n % 8 == 0, k % 8 == 0, n and k >= 8 and
+ * below 1.2e-38, that is values below 2^-109). The tensor cores truncate their
+ * fp32 sums, so they take no more than 1024 tokens (fp32 dw; 512 of an fp32 dy)
+ * or 32768 (bf16 dw) at a time, and what they make of those is added up in fp32.
+ * Sums are in a fixed order (deterministic). n % 8 == 0, k % 8 == 0, n and k >= 8 and
  * < 2^24, 0 <= T < 2^30, bases and row strides of dy 16-byte aligned (ld_dy 0
  * stands for n). T = 0 writes zeros.
  * Scratch: lce_packed_wgrad_workspace_size bytes or NULL.

@@ -1,0 +1,87 @@
+"""The recurrent block's operators where they can go wrong: long sums, values at
+the ends of their types, geometries that only large calls reach, layouts that
+autograd hands over. Tolerances count half steps of the output's type (2^-8 for
+bf16, 2^-24 for fp32) and are derived beside each test."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import chunked_vocab_cross_gb300 as lce  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+U = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -24}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from chunked_vocab_cross_gb300.build import build
+    build()
+    lce.device_status()
+    yield
+
+
+def rand(*shape, seed=0, dtype=torch.float32, positive=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.rand if positive else torch.randn)(*shape, generator=g, device="cuda").to(dtype)
+
+
+def packed_grad64(dy, p, rows):
+    """The first `rows` rows of dy^T x in fp64."""
+    return dy[:, :rows].double().T @ lce.unpack_activation(p, dtype=torch.float32).double()
+
+
+# ------------------------------------------------------------ weight gradient
+
+@pytest.mark.parametrize("T,n,k", [(4097, 1024, 4096), (16384, 4096, 2568), (20000, 256, 256)])
+def test_fp32_gradient_of_a_bf16_dy_of_many_tokens_that_all_add_up(T, n, k):
+    """Each addition of 16 products is truncated twice, by less than a step each, 2^-23 of a sum that is half filled on average. A
+    run of 1024 tokens has 64 additions, so it is off by at most 2^-17 of itself, and by half of that on average; the runs are
+    added up with roundings of 2^-24 of what there is by then."""
+    dy, p = rand(T, n, seed=3, dtype=torch.bfloat16, positive=True), lce.pack_activation(rand(T, k, seed=4, positive=True))
+    got = lce.packed_weight_grad(dy, p, out_dtype=torch.float32)
+    want = packed_grad64(dy, p, 256)
+    off = (got[:256].double() - want) / want
+    runs = (T + 1023) // 1024 + 152   # and splits
+    assert off.abs().max().item() <= 2.0 ** -17 + runs * 2.0 ** -24
+    assert abs(off.mean().item()) <= 2.0 ** -18 + 2.0 ** -24 * runs ** 0.5
+    assert off.norm().item() / off.numel() ** 0.5 <= 1e-6   # what a product of plain fp32 is off by
+    assert torch.equal(lce.packed_weight_grad(dy, p, out_dtype=torch.float32), got)
+
+
+def test_bf16_gradient_of_very_many_tokens_that_all_add_up():
+    """A run of 32768 tokens has 2048 additions, truncated twice, by half a step each on average: one step of 2^-23 of a sum that
+    is half filled, 2^-13 of it together, give or take 6 times sqrt(4096 / 12) steps, less than a sixteenth of that. Rounding
+    to bf16 keeps the order, so the result lies between the roundings of the sum less that and of the sum (1 + 2^-22: the runs'
+    joins)."""
+    T, n, k = 262144, 4096, 2432
+    dy, p = rand(T, n, seed=5, dtype=torch.bfloat16, positive=True), lce.pack_activation(rand(T, k, seed=6, positive=True))
+    got = lce.packed_weight_grad(dy, p)
+    want = packed_grad64(dy, p, 64)
+    assert bool((got[:64] >= (want * (1 - 2.0 ** -13 * 1.0625)).bfloat16()).all())
+    assert bool((got[:64] <= (want * (1 + 2.0 ** -22)).bfloat16()).all())
+    need = lce.packed_weight_grad_workspace_size(T, n, k)
+    ws = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    assert torch.equal(lce.packed_weight_grad(dy, p, workspace=ws[:need]), got) and bool((ws[need:] == 77).all())
+    with pytest.raises(RuntimeError):
+        lce.packed_weight_grad(dy, p, workspace=ws[:need - 1])
+    assert lce.device_status() == 0
+
+
+def test_a_large_gradient_repeats_itself_beside_other_work():
+    """7373 tokens of a 4096 to 16384 layer: the same bits whatever runs beside it, and its error that of rounding to bf16."""
+    dy, p = rand(7373, 16384, seed=7, dtype=torch.bfloat16), lce.pack_activation(rand(7373, 4096, seed=8, dtype=torch.bfloat16))
+    got, junk, side = lce.packed_weight_grad(dy, p), torch.zeros(1 << 28, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    for i in range(30):
+        if i % 2:
+            with torch.cuda.stream(side):
+                junk.add_(1)
+        assert torch.equal(lce.packed_weight_grad(dy, p), got)
+    want = packed_grad64(dy, p, 512)
+    off, rounding = (got[:512].double() - want).norm().item(), (want.bfloat16().double() - want).norm().item()
+    # the sums' own error, 1e-5 of the norm at most, is independent of the rounding's, 1.6e-3 of it
+    assert off <= rounding * (1 + 1e-4)
+    torch.cuda.synchronize()
