@@ -600,8 +600,9 @@ size_t lce_packed_wgrad_workspace_size(const lce_wgrad_t *args);
  * T), NULL for B sequences of equal length; tokens after cu[B] belong to no
  * sequence (h = 0, zero gradients, kept = 0 behind them). Sequences may be empty. Values of one
  * sequence, infinities and NaN among them, never reach another. States and all
- * arithmetic are fp32; h, dx and dg are rounded once. Logits below -87 count as
- * -87. d % 8 == 0, 8 <= d < 2^24, 0 <= T < 2^30, 1 <= B < 2^30, T a multiple
+ * arithmetic are fp32; h, dx and dg are rounded once. a_t and 1 - a_t are off by
+ * at most 9 units of 2^-24 of themselves (bf16 logits: 9 + |g_t|). Logits below -87 count
+ * as -87, and above 87 1 - a_t is 0. d % 8 == 0, 8 <= d < 2^24, 0 <= T < 2^30, 1 <= B < 2^30, T a multiple
  * of B without offsets; bases 16-byte aligned, strides multiples of 16 bytes,
  * at least d (0 stands for d). Outputs must not overlap one another or, but for
  * `final`, any input. Deterministic. Offsets that are not ascending within the

@@ -85,3 +85,25 @@ def test_a_large_gradient_repeats_itself_beside_other_work():
     # the sums' own error, 1e-5 of the norm at most, is independent of the rounding's, 1.6e-3 of it
     assert off <= rounding * (1 + 1e-4)
     torch.cuda.synchronize()
+
+
+# ----------------------------------------------------------------- recurrence
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gates_and_their_complements_to_their_own_precision(dtype):
+    """Seen one at a time: from zero states and x = 1 a token's state is 1 - a, from a gradient of 1 of that state alone the
+    state's own is a. In units of 2^-24: the exponential is off by 4 (two steps of the approximation) and a rounding, the sum
+    with 1 and the product by a rounding each, the reciprocal by 2 (a step): 9. bf16 logits add |z| / 2 for z = g log2(e),
+    times ln 2: |g| / 2 and the same for what fp32 leaves of log2(e)."""
+    for lo, hi in ((-4, 4), (4, 8), (8, 16), (16, 30), (30, 60), (60, 87), (-8, -4), (-30, -8), (-87, -30)):
+        g = (rand(4096, 64, seed=lo + 100, positive=True) * (hi - lo) + lo).to(DT[dtype])
+        one, zero, ones = torch.ones_like(g), torch.zeros(4096, 64, device="cuda"), torch.ones(4096, 64, device="cuda")
+        cu = torch.arange(4097, dtype=torch.int32, device="cuda")
+        _, rest, kept = lce.gated_recurrence_forward(one, g, cu, state=zero, keep=True)
+        _, rest1, _ = lce.gated_recurrence_forward(one.unsqueeze(1), g.unsqueeze(1), state=zero)
+        dx, _, a = lce.gated_recurrence_backward(torch.zeros_like(g), one, g, kept, cu, state=zero, dfinal=ones)
+        G, units = g.double(), 9 + (g.abs().max().item() if dtype == "bf16" else 0)
+        for got, want in ((rest, 1 / (1 + torch.exp(G))), (rest1, 1 / (1 + torch.exp(G))), (a, 1 / (1 + torch.exp(-G)))):
+            assert ((got.double() - want).abs() / want).max().item() <= units * 2.0 ** -24, (lo, hi)
+        want = 1 / (1 + torch.exp(G))
+        assert ((dx.double() - want).abs() / want).max().item() <= (units + 1) * 2.0 ** -24 + (U["bf16"] if dtype == "bf16" else 0)
