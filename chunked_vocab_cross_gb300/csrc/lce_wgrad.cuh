@@ -395,7 +395,8 @@ __global__ void __launch_bounds__(256) k_wgrad_parts(const float *dy, int64_t ld
         __nv_bfloat16 h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            h[i] = __float2bfloat16_rn(x[i]);
+            // finite values beyond bf16's largest are rounded towards zero: to it
+            h[i] = fabsf(x[i]) < INFINITY && fabsf(x[i]) > 3.3895313892515355e38f ? __float2bfloat16_rz(x[i]) : __float2bfloat16_rn(x[i]);
             const float f = __bfloat162float(h[i]);
             x[i] = fabsf(f) < INFINITY ? x[i] - f : 0.f;   // what is not finite is in the first part alone
         }

@@ -87,6 +87,18 @@ def test_a_large_gradient_repeats_itself_beside_other_work():
     torch.cuda.synchronize()
 
 
+def test_fp32_dy_up_to_the_largest_value():
+    """Values that bf16 would round to infinity: the lowest value of a mask among them, beside codes of zero and of one."""
+    most = torch.finfo(torch.float32).max
+    dy, x = torch.zeros(70, 64, device="cuda"), torch.zeros(70, 256, device="cuda")
+    dy[0, 0], dy[1, 1], dy[2, 2], dy[3, 3], dy[65, 4] = most, -most, 3.395e38, 3.39e38, float("inf")
+    x[:4, 0], x[65, 0] = 1.0, 1.0
+    x[:4, 1] = 0.5
+    got, want = lce.packed_weight_grad(dy, lce.pack_activation(x)), (dy.double().T @ x.double()).float()
+    assert torch.equal(got[:4], want[:4]) and got[0, 0] == most and got[1, 0] == -most and not got[:4, 2:].any()
+    assert got[4, 0] == float("inf") and got[4, 1:].isnan().all() and not got[5:].any()
+
+
 # ----------------------------------------------------------------- recurrence
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
