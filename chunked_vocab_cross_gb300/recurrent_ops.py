@@ -57,9 +57,15 @@ def _up16(n: int) -> int:
 
 
 def _on_16(t):
-    """t [rows, n] with its rows on 16-byte strides that do not overlap."""
+    """t [rows, n] of bytes with its rows on 16-byte strides that do not overlap
+    and, since the kernels read whole 16 bytes, the last of them inside its
+    memory."""
     rows, n = t.shape
-    if t.data_ptr() % 16 == 0 and (rows < 2 or (t.stride(0) % 16 == 0 and t.stride(0) >= n)):
+    if rows == 0:
+        return t
+    last = (rows - 1) * t.stride(0)
+    if (t.data_ptr() % 16 == 0 and (rows < 2 or (t.stride(0) % 16 == 0 and t.stride(0) >= n))
+            and t.storage_offset() + last + _up16(n) <= t.untyped_storage().nbytes()):
         return t
     room = torch.empty((rows, _up16(n)), dtype=t.dtype, device=t.device)[:, :n]
     return room.copy_(t)
