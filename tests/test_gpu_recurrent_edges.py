@@ -99,6 +99,24 @@ def test_fp32_dy_up_to_the_largest_value():
     assert got[4, 0] == float("inf") and got[4, 1:].isnan().all() and not got[5:].any()
 
 
+# --------------------------------------------------------------- linear_keep8
+
+def test_linear_keep8_refuses_at_the_call_what_its_gradient_cannot_take():
+    x = rand(40, 64, dtype=torch.bfloat16)
+    for shape in ((12, 64), (0, 64)):
+        with pytest.raises(ValueError, match="multiples of 8"):
+            lce.linear_keep8(x, rand(*shape, dtype=torch.bfloat16).requires_grad_(True))
+    with pytest.raises(ValueError, match="multiples of 8"):
+        lce.linear_keep8(rand(40, 20), rand(16, 20).requires_grad_(True))
+    with torch.no_grad():
+        lce.linear_keep8(x, rand(12, 64, dtype=torch.bfloat16).requires_grad_(True))
+    # a frozen weight has no such gradient
+    w = rand(12, 64, dtype=torch.bfloat16)
+    y = lce.linear_keep8(x.requires_grad_(True), w)
+    assert torch.equal(y, torch.nn.functional.linear(x, w))
+    assert torch.equal(torch.autograd.grad(y, x, torch.ones_like(y))[0], torch.ones_like(y) @ w)
+
+
 # ----------------------------------------------------------------- recurrence
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
