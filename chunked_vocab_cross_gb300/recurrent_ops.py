@@ -209,7 +209,13 @@ class _LinearKeep8(torch.autograd.Function):
 def linear_keep8(x, w):
     """x w^T for x [..., k] and w [n, k], differentiable (once); of x only its
     8-bit form is kept for w's gradient, for which n and k must be multiples of
-    8. The two other products are PyTorch's."""
+    8. Under autocast both are cast to its dtype first, as for PyTorch's own
+    linear. The two other products are PyTorch's."""
+    if torch.is_autocast_enabled("cuda"):
+        dtype = torch.get_autocast_dtype("cuda")
+        cast = lambda t: t.to(dtype) if t.dtype in (torch.float32, torch.bfloat16, torch.float16) else t  # noqa: E731
+        with torch.autocast("cuda", enabled=False):
+            return linear_keep8(cast(x), cast(w))
     if x.dtype not in _DT or not x.is_cuda or x.dtype != w.dtype or w.dim() != 2 or x.shape[-1] != w.shape[1] or x.device != w.device:
         raise ValueError("x [..., k] and w [n, k] must be bfloat16 or float32 tensors of one dtype on one CUDA device")
     if torch.is_grad_enabled() and w.requires_grad and (w.shape[0] % 8 or w.shape[1] % 8 or not w.numel()):

@@ -117,6 +117,23 @@ def test_linear_keep8_refuses_at_the_call_what_its_gradient_cannot_take():
     assert torch.equal(torch.autograd.grad(y, x, torch.ones_like(y))[0], torch.ones_like(y) @ w)
 
 
+@pytest.mark.parametrize("x_dtype,w_dtype", [("fp32", "fp32"), ("bf16", "fp32"), ("fp32", "bf16")])
+def test_linear_keep8_under_autocast(x_dtype, w_dtype):
+    """The gradients of the casts and of the bf16 operator, bit for bit; the products outside it are autocast's as before."""
+    x = rand(3, 30, 136, dtype=DT[x_dtype]).requires_grad_(True)
+    w, dy = rand(72, 136, seed=1, dtype=DT[w_dtype]).requires_grad_(True), rand(3, 30, 72, seed=2, dtype=torch.bfloat16)
+    with torch.autocast("cuda", dtype=torch.bfloat16):
+        y = lce.linear_keep8(x, w)
+        assert (x @ w.T).dtype == torch.bfloat16
+    xb, wb = x.detach().bfloat16(), w.detach().bfloat16()
+    assert y.dtype == torch.bfloat16 and torch.equal(y, torch.nn.functional.linear(xb, wb))
+    dx, dw = torch.autograd.grad(y, (x, w), dy)
+    want = lce.packed_weight_grad(dy.view(90, 72), lce.pack_activation(xb.view(90, 136)))
+    assert dx.dtype == x.dtype and dw.dtype == w.dtype and torch.equal(dx, (dy @ wb).to(x.dtype)) and torch.equal(dw, want.to(w.dtype))
+    with torch.autocast("cuda", dtype=torch.float16), pytest.raises(ValueError, match="bfloat16 or float32"):
+        lce.linear_keep8(x, w)
+
+
 # ----------------------------------------------------------------- recurrence
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
