@@ -182,12 +182,21 @@ def packed_weight_grad(dy, x: PackedActivation, *, out=None, out_dtype=None, wor
     return out
 
 
+def _readable(t):
+    """t [..., d] as [N, d] rows that the kernels can read: itself, or a copy where
+    its elements, its address or its rows' distance are not theirs."""
+    t = t.reshape(-1, t.shape[-1])
+    if (t.stride(1) == 1 and t.data_ptr() % 16 == 0
+            and (t.shape[0] < 2 or (t.stride(0) > 0 and t.stride(0) * t.element_size() % 16 == 0))):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 class _LinearKeep8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w):
-        rows = x.reshape(-1, x.shape[-1])
         if ctx.needs_input_grad[1]:
-            p = pack_activation(rows)
+            p = pack_activation(_readable(x))
             ctx.save_for_backward(w, p.codes, p.exps)
         else:
             ctx.save_for_backward(w, None, None)

@@ -134,6 +134,20 @@ def test_linear_keep8_under_autocast(x_dtype, w_dtype):
         lce.linear_keep8(x, w)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_linear_keep8_takes_x_in_any_layout(dtype):
+    """Transposed, expanded, off 16 bytes, with odd rows: what PyTorch's linear takes, and the gradient of a plain copy."""
+    base = rand(41 * 137, dtype=DT[dtype])
+    w, dy = rand(72, 136, seed=1, dtype=DT[dtype]).requires_grad_(True), rand(40, 72, seed=2, dtype=DT[dtype])
+    layouts = (rand(136, 40, seed=3, dtype=DT[dtype]).t(), base[1:1 + 40 * 136].view(40, 136), base[:40 * 137].view(40, 137)[:, :136],
+               base[:136].expand(40, 136), base[:40].view(40, 1).expand(40, 136), rand(40, 272, dtype=DT[dtype])[:, ::2])
+    for x in layouts:
+        y = lce.linear_keep8(x, w)
+        (dw,) = torch.autograd.grad(y, w, dy)
+        want = lce.packed_weight_grad(dy, lce.pack_activation(x.clone(memory_format=torch.contiguous_format)))
+        assert torch.equal(y, torch.nn.functional.linear(x, w)) and torch.equal(dw, want)
+
+
 # ----------------------------------------------------------------- recurrence
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
