@@ -182,6 +182,13 @@ def packed_weight_grad(dy, x: PackedActivation, *, out=None, out_dtype=None, wor
     return out
 
 
+def _recorded(*tensors) -> bool:
+    """Whether a backward pass can follow a call on these. (ctx.needs_input_grad
+    tells of the inputs alone: parameters have it where no gradient is recorded
+    as well.)"""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 def _readable(t):
     """t [..., d] as [N, d] rows that the kernels can read: itself, or a copy where
     its elements, its address or its rows' distance are not theirs."""
@@ -227,7 +234,9 @@ def linear_keep8(x, w):
             return linear_keep8(cast(x), cast(w))
     if x.dtype not in _DT or not x.is_cuda or x.dtype != w.dtype or w.dim() != 2 or x.shape[-1] != w.shape[1] or x.device != w.device:
         raise ValueError("x [..., k] and w [n, k] must be bfloat16 or float32 tensors of one dtype on one CUDA device")
-    if torch.is_grad_enabled() and w.requires_grad and (w.shape[0] % 8 or w.shape[1] % 8 or not w.numel()):
+    if not _recorded(x, w):
+        return torch.nn.functional.linear(x, w)
+    if w.requires_grad and (w.shape[0] % 8 or w.shape[1] % 8 or not w.numel()):
         raise ValueError(f"w's gradient needs n and k that are multiples of 8, got {tuple(w.shape)}")
     return _LinearKeep8.apply(x, w)
 
@@ -361,6 +370,8 @@ class _LayerNorm(torch.autograd.Function):
 def layer_norm(x, b=None, *, weight, bias=None, eps: float = 1e-5, keep8: bool = False):
     """Autograd form of layer_norm_forward: (r, n). With keep8 the backward pass
     keeps r's 8-bit form instead of r."""
+    if not _recorded(x, b, weight, bias):
+        return layer_norm_forward(x, b, weight=weight, bias=bias, eps=eps)[:2]
     return _LayerNorm.apply(x, b, weight, bias, eps, keep8)
 
 
@@ -477,7 +488,7 @@ def gated_recurrence_backward(dh, x, g, kept, cu_seqlens=None, *, state=None, df
 class _GatedRecurrence(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, g, cu, state):
-        h, final, kept = gated_recurrence_forward(x, g, cu, state=state, keep=any(ctx.needs_input_grad))
+        h, final, kept = gated_recurrence_forward(x, g, cu, state=state, keep=True)
         ctx.save_for_backward(x, g, cu, state, kept)
         ctx.set_materialize_grads(False)
         return h, final
@@ -496,4 +507,6 @@ class _GatedRecurrence(torch.autograd.Function):
 
 def gated_recurrence(x, g, cu_seqlens=None, *, state=None):
     """Autograd form of gated_recurrence_forward: (h, final)."""
+    if not _recorded(x, g, state):
+        return gated_recurrence_forward(x, g, cu_seqlens, state=state)[:2]
     return _GatedRecurrence.apply(x, g, cu_seqlens, state)

@@ -148,6 +148,32 @@ def test_linear_keep8_takes_x_in_any_layout(dtype):
         assert torch.equal(y, torch.nn.functional.linear(x, w)) and torch.equal(dw, want)
 
 
+def test_nothing_is_kept_where_no_gradient_is_recorded():
+    """Parameters ask for gradients under no_grad as well; what a call leaves and takes there is its result alone."""
+    N, d = 4096, 1024
+    x, g = rand(N, d, dtype=torch.bfloat16).requires_grad_(True), rand(N, d, seed=1, dtype=torch.bfloat16).requires_grad_(True)
+    w, s = rand(d, d, seed=2, dtype=torch.bfloat16).requires_grad_(True), torch.zeros(1, d, device="cuda")
+    v = torch.ones(d, dtype=torch.bfloat16, device="cuda").requires_grad_(True)
+    calls = ((lambda: lce.linear_keep8(x, w), 0, N * d * 2), (lambda: lce.layer_norm(x, weight=v, keep8=True), 1, N * d * 2 + N * 8),
+             (lambda: lce.layer_norm(x, g, weight=v, bias=v, keep8=True), 1, N * d * 4 + N * 8),
+             (lambda: lce.gated_recurrence(x, g), 1, N * d * 2 + d * 4))
+    for call, launches, size in calls:
+        recorded = call()
+        for grad_off in (torch.no_grad, torch.inference_mode):
+            with grad_off():
+                torch.cuda.synchronize()
+                before, held = lce.launch_count(), torch.cuda.memory_allocated()
+                torch.cuda.reset_peak_memory_stats()
+                got = call()
+                assert lce.launch_count() - before == launches and torch.cuda.max_memory_allocated() - held <= size + (1 << 14)
+            pairs = [(got, recorded)] if torch.is_tensor(got) else zip(got, recorded)
+            assert all(torch.equal(a, b) and not a.requires_grad for a, b in pairs if a is not x)
+    # nor with gradients recorded, where no input asks for one
+    before = lce.launch_count()
+    lce.linear_keep8(x.detach(), w.detach())
+    assert lce.launch_count() == before
+
+
 # ----------------------------------------------------------------- recurrence
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
