@@ -63,6 +63,15 @@ def _like(t):
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
+def _whole(t):
+    """A gradient from autograd as the kernels can read it: it may be expanded,
+    permuted, or contiguous at an address off 16 bytes (a slice of another)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 # ------------------------------------------------------------------ attention
 
 def _tokens(name, t, device, dtype, shape=None):
@@ -226,8 +235,7 @@ class _Attention(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
-        # autograd may hand over an expanded or permuted gradient, whose rows the kernels cannot read
-        dq, dk, dv = attention_backward(do.contiguous(), q, k, v, o, lse, cu_q, cu_k, causal=ctx.causal, scale=ctx.scale)
+        dq, dk, dv = attention_backward(_whole(do), q, k, v, o, lse, cu_q, cu_k, causal=ctx.causal, scale=ctx.scale)
         need = ctx.needs_input_grad
         return dq if need[0] else None, dk if need[1] else None, dv if need[2] else None, None, None, None, None
 
@@ -400,9 +408,8 @@ class _BlockNorm(torch.autograd.Function):
             dn = torch.zeros_like(ref)
         if dr is None and w_pre is None:
             dr = torch.zeros_like(ref)
-        rows = lambda t: None if t is None else t.contiguous()  # noqa: E731
         dx, db, dw_post, dgate, dw_pre = block_norm_backward(
-            rows(dr), rows(dn), r, b, w_post=w_post, gate=gate, w_pre=w_pre, scale=ctx.scale, rstd_post=rstd_post,
+            _whole(dr), _whole(dn), r, b, w_post=w_post, gate=gate, w_pre=w_pre, scale=ctx.scale, rstd_post=rstd_post,
             rstd_pre=rstd_pre)
         need = ctx.needs_input_grad
         return tuple(g if n else None for g, n in zip((dx, db, dw_post, dgate, dw_pre), need)) + (None, None)
@@ -435,8 +442,7 @@ class _Norm(torch.autograd.Function):
         x, w_pre, rstd = ctx.saved_tensors
         if dn is None:
             dn = torch.zeros_like(x)
-        dx, _, _, _, dw = block_norm_backward(None if dr is None else dr.contiguous(), dn.contiguous(), x, w_pre=w_pre,
-                                              rstd_pre=rstd)
+        dx, _, _, _, dw = block_norm_backward(_whole(dr), _whole(dn), x, w_pre=w_pre, rstd_pre=rstd)
         return dx if ctx.needs_input_grad[0] else None, dw if ctx.needs_input_grad[1] else None, None
 
 

@@ -12,7 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from .block_ops import _DT, _Expanded, _like, _on_stream, _rows, _scratch, _spread, _stream, _vector, _written
+from .block_ops import _DT, _Expanded, _like, _on_stream, _rows, _scratch, _spread, _stream, _vector, _whole, _written
 
 _LN, _WGRAD, _SCAN = _abi.packer(_abi.LceLayerNorm), _abi.packer(_abi.LceWgrad), _abi.packer(_abi.LceRecurrence)
 _at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
@@ -217,8 +217,7 @@ class _LinearKeep8(torch.autograd.Function):
         dx = dy @ w if ctx.needs_input_grad[0] else None
         dw = None
         if ctx.needs_input_grad[1]:
-            rows = dy.reshape(-1, dy.shape[-1]).contiguous()
-            dw = packed_weight_grad(rows, PackedActivation(codes, exps, ctx.dtype))
+            dw = packed_weight_grad(_readable(dy), PackedActivation(codes, exps, ctx.dtype))
         return dx, dw
 
 
@@ -360,9 +359,8 @@ class _LayerNorm(torch.autograd.Function):
         r, exps, weight, mean, rstd = ctx.saved_tensors
         if exps is not None:
             r = PackedActivation(r, exps, weight.dtype)
-        dn = torch.zeros(r.shape, dtype=weight.dtype, device=weight.device) if dn is None else dn.contiguous()
-        dx, dw, dc = layer_norm_backward(None if dr is None else dr.contiguous(), dn, r, weight=weight, mean=mean, rstd=rstd,
-                                         bias=ctx.bias)
+        dn = torch.zeros(r.shape, dtype=weight.dtype, device=weight.device) if dn is None else _whole(dn)
+        dx, dw, dc = layer_norm_backward(_whole(dr), dn, r, weight=weight, mean=mean, rstd=rstd, bias=ctx.bias)
         need = ctx.needs_input_grad
         return tuple(g if n else None for g, n in zip((dx, dx, dw, dc), need)) + (None, None)
 
@@ -497,10 +495,8 @@ class _GatedRecurrence(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dh, dfinal):
         x, g, cu, state, kept = ctx.saved_tensors
-        # autograd may hand over expanded or permuted gradients, whose rows the kernels cannot read
-        dh = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dh is None else dh.contiguous()
-        dx, dg, dstate = gated_recurrence_backward(dh, x, g, kept, cu, state=state,
-                                                   dfinal=None if dfinal is None else dfinal.contiguous())
+        dh = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dh is None else _whole(dh)
+        dx, dg, dstate = gated_recurrence_backward(dh, x, g, kept, cu, state=state, dfinal=_whole(dfinal))
         need = ctx.needs_input_grad
         return dx if need[0] else None, dg if need[1] else None, None, dstate if need[3] else None
 

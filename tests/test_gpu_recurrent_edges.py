@@ -174,6 +174,33 @@ def test_nothing_is_kept_where_no_gradient_is_recorded():
     assert lce.launch_count() == before
 
 
+# ------------------------------------------------------------------- autograd
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradients_at_addresses_off_16_bytes(dtype):
+    """A slice of another gradient, as an output that was flattened behind a few other values gets it, is contiguous and starts
+    anywhere: the same bits as from a gradient of its own."""
+    r = lambda *s, seed=0: rand(*s, seed=seed, dtype=DT[dtype]).requires_grad_(True)  # noqa: E731
+    x, b, w, c, m = r(40, 64), r(40, 64, seed=1), r(64, seed=2), r(64, seed=3), r(24, 64, seed=4)
+    s, q, k = rand(1, 64, seed=5).requires_grad_(True), r(40, 2, 64, seed=6), r(40, 1, 64, seed=7)
+    calls = ((lambda: lce.linear_keep8(x, m), (x, m)), (lambda: lce.layer_norm(x, b, weight=w, bias=c), (x, b, w, c)),
+             (lambda: lce.layer_norm(x, weight=w, bias=c, keep8=True), (x, w, c)), (lambda: lce.gated_recurrence(x, b, state=s), (x, b, s)),
+             (lambda: lce.attention(q, k, k), (q, k)), (lambda: lce.block_norm(x, b, w_post=w, w_pre=c), (x, b, w, c)),
+             (lambda: lce.block_norm(x, w_pre=w), (x, w)))
+    for call, leaves in calls:
+        outs = call()
+        outs = (outs,) if torch.is_tensor(outs) else outs
+        grads = [rand(*o.shape, seed=9 + i, dtype=o.dtype) for i, o in enumerate(outs)]
+        odd = []
+        for g in grads:
+            room = torch.empty(g.numel() + 3, dtype=g.dtype, device="cuda")
+            odd.append(room[3:].view(g.shape).copy_(g))
+            assert odd[-1].is_contiguous() and odd[-1].data_ptr() % 16
+        want = torch.autograd.grad(outs, leaves, grads, retain_graph=True)
+        got = torch.autograd.grad(outs, leaves, odd)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 # ----------------------------------------------------------------- recurrence
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
