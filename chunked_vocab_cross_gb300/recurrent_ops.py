@@ -408,7 +408,7 @@ def _recurrent(x, cu):
     if x.dim() not in (2, 3):
         raise ValueError("x must be [T, d] or [B, L, d]")
     if cu is None:
-        return (max(x.shape[0], 1), x.shape[0] * x.shape[1], x.shape[2], 0) if x.dim() == 3 else (1, x.shape[0], x.shape[1], 0)
+        return (x.shape[0], x.shape[0] * x.shape[1], x.shape[2], 0) if x.dim() == 3 else (1, x.shape[0], x.shape[1], 0)
     if x.dim() == 3:
         raise ValueError("sequence offsets go with [T, d] tensors")
     if cu.dtype != torch.int32 or cu.dim() != 1 or cu.device != x.device or not cu.is_contiguous() or cu.numel() < 2:
@@ -448,7 +448,7 @@ def gated_recurrence_forward(x, g, cu_seqlens=None, *, state=None, out=None, out
         out_state = torch.empty((B, d), dtype=torch.float32, device=device)
     pf = _states("out_state", out_state, B, d, device)
     kept = torch.empty(((T + _EVERY - 1) // _EVERY, d), dtype=torch.float32, device=device) if keep else None
-    args = _SCAN.pack(_DT[x.dtype], B, T, d, pc, px[0], pg[0], px[1], pg[1], ps, _at(kept), ph[0], ph[1], pf, 0, 0, 0, 0, 0, 0, 0, 0,
+    args = _SCAN.pack(_DT[x.dtype], max(B, 1), T, d, pc, px[0], pg[0], px[1], pg[1], ps, _at(kept), ph[0], ph[1], pf, 0, 0, 0, 0, 0, 0, 0, 0,
                       _stream(device.index))
     _abi.check(_abi.lib().lce_recurrence_forward(args), "lce_recurrence_forward")
     if given:
@@ -475,7 +475,7 @@ def gated_recurrence_backward(dh, x, g, kept, cu_seqlens=None, *, state=None, df
     dg = torch.empty(x.shape, dtype=x.dtype, device=device) if dg is None else dg
     pdx, pdg = _tokens("dx", dx, x), _tokens("dg", dg, x)
     dstate = None if state is None else torch.empty((B, d), dtype=torch.float32, device=device)
-    args = _SCAN.pack(_DT[x.dtype], B, T, d, pc, px[0], pg[0], px[1], pg[1], ps, kept.data_ptr(), 0, 0, 0, pd[0], pd[1], pf, pdx[0],
+    args = _SCAN.pack(_DT[x.dtype], max(B, 1), T, d, pc, px[0], pg[0], px[1], pg[1], ps, kept.data_ptr(), 0, 0, 0, pd[0], pd[1], pf, pdx[0],
                       pdg[0], pdx[1], pdg[1], _at(dstate), _stream(device.index))
     _abi.check(_abi.lib().lce_recurrence_backward(args), "lce_recurrence_backward")
     if given:

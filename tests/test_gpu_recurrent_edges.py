@@ -221,3 +221,18 @@ def test_gates_and_their_complements_to_their_own_precision(dtype):
             assert ((got.double() - want).abs() / want).max().item() <= units * 2.0 ** -24, (lo, hi)
         want = 1 / (1 + torch.exp(G))
         assert ((dx.double() - want).abs() / want).max().item() <= (units + 1) * 2.0 ** -24 + (U["bf16"] if dtype == "bf16" else 0)
+
+
+@pytest.mark.parametrize("B,L", [(0, 5), (0, 1), (0, 0), (3, 0)])
+def test_batches_without_sequences_or_tokens(B, L):
+    x = torch.empty(B, L, 64, device="cuda")
+    state, dfinal = rand(B, 64), rand(B, 64, seed=1)
+    for s in (state, None):
+        h, final, kept = lce.gated_recurrence_forward(x, x, state=s, keep=True, out_state=torch.full((B, 64), 7.0, device="cuda"))
+        assert h.shape == x.shape and torch.equal(final, state if s is not None else torch.zeros(B, 64, device="cuda"))
+        dx, dg, dstate = lce.gated_recurrence_backward(x, x, x, kept, state=s, dfinal=dfinal)
+        assert dx.shape == dg.shape == x.shape and (dstate is None if s is None else torch.equal(dstate, dfinal))
+    leaf, s = x.clone().requires_grad_(True), state.clone().requires_grad_(True)
+    h, final = lce.gated_recurrence(leaf, leaf, state=s)
+    (ds,) = torch.autograd.grad(final, s, dfinal)
+    assert torch.equal(ds, dfinal)
