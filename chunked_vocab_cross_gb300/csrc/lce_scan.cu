@@ -125,6 +125,10 @@ __device__ __forceinline__ typename L::F apply(const Step<L> &s, typename L::F b
     return L::first(s.A) < 0.f ? s.H : L::fma(s.A, before, s.H);
 }
 
+// A product of gates, which are never zero, that ran out of fp32: its smallest value, so that an infinite state stays one
+// (0 would make it a NaN). No finite state shows it: 2^-149 of the largest is 2^-21.
+__device__ __forceinline__ float never_zero(float a) { return __uint_as_float(max(__float_as_uint(a), 1u)); }   // kReset stays, NaN too
+
 // Work is split over channels and over time. A slice is the channels of 128
 // bytes of a row; a cluster of CTAs takes a slice through the tokens, each CTA a
 // tile of 128 tokens in every group of as many tiles, and 8 warps 16 tokens each
@@ -198,7 +202,7 @@ __device__ __forceinline__ Step<Lane<float>> join_warps(uint8_t *at, int stride,
     using L = Lane<float>;
     constexpr int kLanes = kWarps / N;
     auto then = [](const Step<L> &a, const Step<L> &b) {   // a, then b
-        return Step<L>{b.A < 0.f ? b.A : a.A < 0.f ? a.A : a.A * b.A, apply(b, a.H)};
+        return Step<L>{b.A < 0.f ? b.A : a.A < 0.f ? a.A : never_zero(a.A * b.A), apply(b, a.H)};
     };
     const int q = kDown ? kLanes - 1 - lane % kLanes : lane % kLanes;   // place in order
     Step<L> own[N], sum;
@@ -472,8 +476,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan(const ScanArgs a, cons
             else gates(std::false_type());
         }
         constexpr int kLaneStep = L::kCh * 8;
+        fwd.A = L::each(fwd.A, never_zero);
         save_step(steps + warp * kWarpStepBytes + lane * kLaneStep, fwd);
-        if (kBack) save_step(steps_b + warp * kWarpStepBytes + lane * kLaneStep, bwd);
+        if (kBack) bwd.A = L::each(bwd.A, never_zero), save_step(steps_b + warp * kWarpStepBytes + lane * kLaneStep, bwd);
         __syncthreads();
         uint8_t *theirs = tile_steps + par * geo.cluster * kStepBytes;
         {

@@ -236,3 +236,32 @@ def test_batches_without_sequences_or_tokens(B, L):
     h, final = lce.gated_recurrence(leaf, leaf, state=s)
     (ds,) = torch.autograd.grad(final, s, dfinal)
     assert torch.equal(ds, dfinal)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("where", [0, 5, 140, 700])
+def test_an_infinity_stays_one_through_gates_that_forget(where, dtype):
+    """A gate is never zero, so no token after an infinite one (or before an infinite gradient) has a finite state or a NaN,
+    however small the product of the gates between them: here e^-20 each."""
+    T, d = 1400, 64
+    x, g, dh = rand(T, d, dtype=DT[dtype]), torch.full((T, d), -20.0, dtype=DT[dtype], device="cuda"), rand(T, d, seed=1, dtype=DT[dtype])
+    x[where, ::2], x[where, 1::2] = float("inf"), float("-inf")
+    sign = torch.tensor([1.0, -1.0], device="cuda").repeat(d // 2)
+    h, final, kept = lce.gated_recurrence_forward(x, g, keep=True)
+    assert bool((h[where:].float() == sign * float("inf")).all()) and bool(h[:where].isfinite().all())
+    assert torch.equal(final[0], sign * float("inf"))
+    dh[T - 1 - where, ::2], dh[T - 1 - where, 1::2] = float("inf"), float("-inf")
+    x = rand(T, d, dtype=DT[dtype])
+    _, _, kept = lce.gated_recurrence_forward(x, g, keep=True)
+    state = torch.ones(1, d, device="cuda")
+    dx, _, dstate = lce.gated_recurrence_backward(dh, x, g, kept, state=state)
+    assert bool((dx[:T - where].float() == sign * float("inf")).all()) and bool(dx[T - where:].isfinite().all())
+    assert torch.equal(dstate[0], sign * float("inf"))
+    # an infinite state, and one sequence among others
+    lens = [300, 500, 600]
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    state = torch.ones(3, d, device="cuda")
+    state[1] = sign * float("inf")
+    h, final, _ = lce.gated_recurrence_forward(x, g, cu, state=state)
+    assert bool((h[300:800].float() == sign * float("inf")).all()) and torch.equal(final[1], state[1])
+    assert bool(h[:300].isfinite().all()) and bool(h[800:].isfinite().all())
