@@ -122,7 +122,9 @@ __device__ __forceinline__ uint32_t wg_extend(uint32_t codes) {
 }
 // Four codes to two bf16 pairs, times a power of two (a pair as well) or two:
 // a code is extended to 16 bits by its sign, moved up by 4 bits and cleared
-// between sign and exponent.
+// between sign and exponent. A NaN's code comes out as 480: lce_pack8 leaves
+// them only in blocks whose exponent makes NaNs of all codes (looking for them
+// here takes 600 us where the product takes 568).
 template <bool kTwo>
 __device__ __forceinline__ uint2 wg_widen(uint32_t codes, uint32_t s1, uint32_t s2) {
     const uint32_t lo = wg_extend<0x9180>(codes), hi = wg_extend<0xb3a2>(codes);

@@ -26,7 +26,10 @@ class PackedActivation:
     channels of a row; a code stands for its value times 2**exponent (-128: the
     block held an infinity or NaN and stands for NaNs). Both have rows on
     16-byte strides, and are copied to such where they have not (brought back
-    from host memory, say). `dtype`: of the tensor that was packed."""
+    from host memory, say). Their bytes have to be those that pack_activation
+    leaves, which is not checked: exponents of -128 or -100 to 119, and the codes
+    of NaN (0x7f, 0xff) only under -128. `dtype`: of the tensor that was
+    packed."""
     __slots__ = ("shape", "dtype", "device", "_codes", "_exps", "_fields")
 
     def __init__(self, codes, exps, dtype):

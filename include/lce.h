@@ -534,9 +534,13 @@ size_t lce_layer_norm_workspace_size(const lce_layer_norm_t *args);
  * Magnitudes beyond 448 * 2^119 = 2.98e38 come back as that.
  * codes: [N] rows of d bytes, ld_codes apart (a multiple of 16, at least d);
  * exps: int8 [ceil(d/128)][N], rows ld_exps apart (a multiple of 16, at least
- * N); d and N rounded up to 16 bytes of every row, the last too, may be read. x and out are of `dtype`, rows ld_x and ld_out elements apart (0 stands
- * for d). d % 8 == 0, 8 <= d < 2^24, 0 <= N < 2^31, bases 16-byte aligned, row strides
- * multiples of 16 bytes.
+ * N). Of every row, the last too, d and N rounded up to 16 bytes may be read.
+ * Whatever reads codes and exponents takes them to be lce_pack8's, unchecked:
+ * exponents of -128 or -100 to 119, and the codes 0x7f and 0xff (NaN) only under
+ * -128; others give other values, and not the same in every operator.
+ * x and out are of `dtype`, rows ld_x and ld_out elements apart (0 stands for
+ * d). d % 8 == 0, 8 <= d < 2^24, 0 <= N < 2^31, bases 16-byte aligned, row
+ * strides multiples of 16 bytes.
  */
 lce_status_t lce_pack8(lce_dtype_t dtype, const void *x, int64_t ld_x, int64_t N, int64_t d, uint8_t *codes,
                        int64_t ld_codes, int8_t *exps, int64_t ld_exps, lce_stream_t stream);
