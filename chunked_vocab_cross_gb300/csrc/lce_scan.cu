@@ -273,6 +273,19 @@ struct SeqFinder {
         if (s >= t0 && s < t0 + kTok) out.seq[s - t0] = mine, atomicOr(&flags[s - t0], 1u);
         if (e > t0 && e <= t0 + kTok) out.seq[e - 1 - t0] = mine, atomicOr(&flags[e - 1 - t0], 2u);
     }
+    // The last sequence that does not begin after t, among 32 probes a round
+    __device__ __forceinline__ int last_at(int t) const {
+        const int lane = threadIdx.x & 31;
+        int b = 0, n = a.B + 1;
+        while (n > 1) {
+            const int step = (n + 31) / 32, off = lane * step;
+            const uint32_t mask = __ballot_sync(0xffffffffu, off < n && a.start(b + off) <= t);
+            const int hit = mask ? 31 - __clz(mask) : 0;   // offsets that do not ascend may leave holes
+            b += hit * step;
+            n = min(step, n - hit * step);
+        }
+        return b;
+    }
     // The ends of the tile from t0 on. Most tiles have none, and all warps wait
     // for the one that looks: that is settled first (16384 tokens of 4096 channels
     // bf16: 84 us with the full account of every tile, 81 this way).
@@ -310,25 +323,22 @@ struct SeqFinder {
         if (holds(t0)) {
             mark(lo, t0, out);
         } else {
-            // the last sequence that does not begin after t0, among 32 probes a round
-            int b = 0, n = a.B + 1;
-            while (n > 1) {
-                const int step = (n + 31) / 32, off = lane * step;
-                const uint32_t mask = __ballot_sync(0xffffffffu, off < n && a.start(b + off) <= t0);
-                const int hit = mask ? 31 - __clz(mask) : 0;   // offsets that do not ascend may leave holes
-                b += hit * step;
-                n = min(step, n - hit * step);
-            }
+            int b = last_at(t0);
             lo = kBack ? max(0, b - 15) : b;   // the tiles to come are on that side
             take(lo);
             if (holds(t0)) {
                 mark(lo, t0, out);
             } else {
                 lo = -1;
-                for (; b < a.B; b += 32) {
+                while (b < a.B) {
                     take(b);
                     mark(b, t0, out);
                     if (__any_sync(0xffffffffu, s >= t0 + kTok)) break;
+                    // where all are empty there may be millions, and the other warps wait: on to the last that begins there
+                    const bool some = __any_sync(0xffffffffu, e > s);
+                    const int here = __shfl_sync(0xffffffffu, s, 0);
+                    b += 32;
+                    if (!some) b = max(b, last_at(here));
                 }
             }
         }

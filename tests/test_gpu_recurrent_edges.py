@@ -265,3 +265,28 @@ def test_an_infinity_stays_one_through_gates_that_forget(where, dtype):
     h, final, _ = lce.gated_recurrence_forward(x, g, cu, state=state)
     assert bool((h[300:800].float() == sign * float("inf")).all()) and torch.equal(final[1], state[1])
     assert bool(h[:300].isfinite().all()) and bool(h[800:].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_millions_of_empty_sequences(dtype):
+    """Before, between and behind sequences, in a tile and at its border: the results are those without them, bit for bit, and
+    their states pass through."""
+    lens, d, many = [200, 56, 300, 84], 16, 700_000
+    x, g, dh = (rand(700, d, seed=i, dtype=DT[dtype]) for i in range(3))   # the last 60 tokens belong to no sequence
+    ends = torch.tensor([0] + lens).cumsum(0)
+    some = torch.tensor([0, 1, 2, 3]) + many * torch.tensor([1, 2, 3, 4])   # their numbers with `many` empty ones before each
+    cu = torch.cat([ends[i].repeat(many + 1) for i in range(4)] + [ends[4].repeat(many)])
+    cu = torch.cat([cu, ends[4:]]).to(torch.int32).cuda()
+    B = cu.numel() - 1
+    state, dfinal = rand(B, d, seed=4), rand(B, d, seed=5)
+    few, less, dless = ends.to(torch.int32).cuda(), state[some].contiguous(), dfinal[some].contiguous()
+    h, final, kept = lce.gated_recurrence_forward(x, g, cu, state=state, keep=True)
+    h2, final2, kept2 = lce.gated_recurrence_forward(x, g, few, state=less, keep=True)
+    assert torch.equal(h, h2) and torch.equal(final[some], final2) and torch.equal(kept, kept2)
+    got = lce.gated_recurrence_backward(dh, x, g, kept, cu, state=state, dfinal=dfinal)
+    want = lce.gated_recurrence_backward(dh, x, g, kept2, few, state=less, dfinal=dless)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2][some], want[2])
+    rest = torch.ones(B, dtype=torch.bool)
+    rest[some] = False
+    assert torch.equal(final[rest], state[rest]) and torch.equal(got[2][rest], dfinal[rest])
+    assert lce.device_status() == 0
