@@ -174,6 +174,25 @@ def test_nothing_is_kept_where_no_gradient_is_recorded():
     assert lce.launch_count() == before
 
 
+# ----------------------------------------------------------------- layer norm
+
+@pytest.mark.parametrize("N,d,dtype", [(16001, 1032, "bf16"), (30011, 64, "bf16"), (4099, 4104, "bf16"), (9001, 1032, "fp32"),
+                                       (1501, 4096, "fp32")])
+@pytest.mark.parametrize("keep8", [False, True], ids=["", "keep8"])
+def test_layer_norm_in_place_through_the_ring(N, d, dtype, keep8):
+    """r written over x or over b while later rows are still on their way, the last row copied in place of rows past it: the bits
+    of a call with an r of its own, at sizes whose blocks refill their ring and end inside a stage."""
+    x, b, w, c = rand(N, d, dtype=DT[dtype]), rand(N, d, seed=1, dtype=DT[dtype]), rand(d, seed=2, dtype=DT[dtype]), rand(d, seed=3, dtype=DT[dtype])
+    r, n, mean, rstd, kept = lce.layer_norm_forward(x, b, weight=w, bias=c, keep8=keep8)
+    assert torch.equal(r, (x.float() + b.float()).to(DT[dtype]))
+    for into in (0, 1):
+        pair = [x.clone(), b.clone()]
+        r2, n2, mean2, rstd2, kept2 = lce.layer_norm_forward(*pair, weight=w, bias=c, keep8=keep8, out_r=pair[into])
+        assert r2 is pair[into] and torch.equal(r2, r) and torch.equal(pair[1 - into], (x, b)[1 - into])
+        assert torch.equal(n2, n) and torch.equal(mean2, mean) and torch.equal(rstd2, rstd)
+        assert not keep8 or (torch.equal(kept2.codes, kept.codes) and torch.equal(kept2.exps, kept.exps))
+
+
 # ------------------------------------------------------------------- autograd
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -289,4 +308,65 @@ def test_millions_of_empty_sequences(dtype):
     rest = torch.ones(B, dtype=torch.bool)
     rest[some] = False
     assert torch.equal(final[rest], state[rest]) and torch.equal(got[2][rest], dfinal[rest])
+    assert lce.device_status() == 0
+
+
+def recurrence64(x, g, dh, lens, state, dfinal):
+    """The recurrence and its gradients in fp64, a token at a time, each with the absolute sums of the terms of all steps before
+    it: {name: (value, terms)}. A step that is off by a share of its terms, every step before it as well, is off by that share."""
+    x, g, dh, state, dfinal = (t.double() for t in (x, g, dh, state, dfinal))
+    T, d = x.shape
+    a, rest = 1 / (1 + torch.exp(-g)), 1 / (1 + torch.exp(g))
+    h, eh, dx, ex, dg, eg = (torch.zeros_like(x) for _ in range(6))
+    final, ef, ds, es = (torch.zeros_like(state) for _ in range(4))
+    begin = 0
+    for i, n in enumerate(lens):
+        s, z, e = state[i], state[i].abs(), state[i].abs()
+        before = []
+        for t in range(begin, begin + n):
+            before.append((s, e))
+            s, z = a[t] * s + rest[t] * x[t], a[t] * z + rest[t] * x[t].abs()
+            e = a[t] * e + z
+            h[t], eh[t] = s, e
+        final[i], ef[i] = s, e
+        m, z, e = dfinal[i], dfinal[i].abs(), dfinal[i].abs()
+        for t in range(begin + n - 1, begin - 1, -1):
+            hp, ep = before[t - begin]
+            m, z = dh[t] + m, dh[t].abs() + z
+            e = e + z
+            dx[t], ex[t] = rest[t] * m, rest[t] * e
+            dg[t], eg[t] = m * (hp - x[t]) * a[t] * rest[t], e * (ep + x[t].abs()) * a[t] * rest[t]
+            m, z, e = a[t] * m, a[t] * z, a[t] * e
+        ds[i], es[i] = m, e
+        begin += n
+    return {"h": (h, eh), "final": (final, ef), "dx": (dx, ex), "dg": (dg, eg), "dstate": (ds, es)}
+
+
+@pytest.mark.parametrize("d,lens,tail,dtype", [
+    (4096, [1012, 433, 0, 761, 1290, 64, 1], 300, "bf16"), (4096, [2900], 0, "bf16"), (8192, [700, 1250], 90, "bf16"),
+    (2048, [3100, 5, 900], 30, "bf16"), (2560, [1999, 1300], 0, "bf16"), (10000, [900, 640], 10, "bf16"), (10000, [1500], 0, "bf16"),
+    (2048, [1012, 433, 0, 761, 1290, 64, 1], 300, "fp32"), (4096, [2000, 300], 0, "fp32"), (5000, [900, 640], 10, "fp32"),
+    (1024, [3500, 600], 0, "fp32"), (1024, [2600, 2, 1500], 20, "bf16"), (256, [4000, 1500], 0, "bf16")], ids=lambda v: str(v).replace(" ", ""))
+def test_wide_models_over_many_tiles(d, lens, tail, dtype):
+    """Widths whose channels leave each slice clusters of 1 to 16 CTAs over thousands of tokens: the rings of tiles, of their
+    sequences' ends and of the cluster's steps go round many times. The tolerances are those of the narrow models: a rounding to
+    the type, and before it F = 2^-24 (16 + 2 max|g|) of the terms, twice that for products of two sums; below fp32's normal
+    range 2^-74."""
+    T, B = sum(lens) + tail, len(lens)
+    xg = torch.cat([rand(T, d, seed=1), rand(T, d, seed=2) * 1.5 + 2], 1).to(DT[dtype])
+    x, g, dh = xg[:, :d], xg[:, d:], rand(T, d, seed=3, dtype=DT[dtype])
+    state, dfinal = rand(B, d, seed=4), rand(B, d, seed=5)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    h, final, kept = lce.gated_recurrence_forward(x, g, cu, state=state, keep=True)
+    dx, dg, dstate = lce.gated_recurrence_backward(dh, x, g, kept, cu, state=state, dfinal=dfinal)
+    for _ in range(3):
+        assert torch.equal(lce.gated_recurrence_forward(x, g, cu, state=state)[0], h)
+        assert all(torch.equal(p, q) for p, q in zip(lce.gated_recurrence_backward(dh, x, g, kept, cu, state=state, dfinal=dfinal),
+                                                     (dx, dg, dstate)))
+    want, F = recurrence64(x, g, dh, lens, state, dfinal), 2.0 ** -24 * (16 + 2 * g.abs().max().item())
+    for name, got, u, share in (("h", h, U[dtype], F), ("final", final, U["fp32"], F), ("dx", dx, U[dtype], 2 * F),
+                                ("dg", dg, U[dtype], 2 * F), ("dstate", dstate, U["fp32"], 2 * F)):
+        value, terms = want[name]
+        over = (got.double() - value).abs() - (u * value.abs() + share * terms + 2.0 ** -74)
+        assert over.max().item() <= 0, (name, over.max().item())
     assert lce.device_status() == 0
