@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_ln_fwd_ring(const LnArgs a,
         group_sum(sum, my_red, flip, g.tpr, group, t);
         __syncwarp();
         if ((t & 31) == 0) mbar_arrive(&bars.empty[s]);   // everything is in registers: it has gone into the sum
-        const float mean = sum[0] * inv_d;
+        const float mean = sum[0] / a.d;   // not * inv_d: a row of one value has that as its mean, and no spread
         const f32x2 minus = both(-mean);
         q = both(0.f);
 #pragma unroll

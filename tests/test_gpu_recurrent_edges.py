@@ -193,6 +193,17 @@ def test_layer_norm_in_place_through_the_ring(N, d, dtype, keep8):
         assert not keep8 or (torch.equal(kept2.codes, kept.codes) and torch.equal(kept2.exps, kept.exps))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,d", [(3, 1000), (5000, 1000), (5000, 1032), (3000, 2600), (1200, 5000)])
+def test_layer_norm_of_rows_of_one_value(N, d, dtype):
+    """Rows of whole numbers whose sums fp32 holds: the mean is the value itself, so nothing is left to be scaled up by the square
+    root of 1 / eps."""
+    x = (torch.arange(N, device="cuda") - N // 2).remainder(256).sub(128).mul(8.0)[:, None].expand(N, d).to(DT[dtype]).contiguous()
+    w, c = rand(d, dtype=DT[dtype]), rand(d, seed=1, dtype=DT[dtype])
+    _, n, mean, rstd, _ = lce.layer_norm_forward(x, weight=w, bias=c)
+    assert torch.equal(mean, x[:, 0].float()) and torch.equal(n, c.expand(N, d))
+
+
 # ------------------------------------------------------------------- autograd
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
