@@ -97,7 +97,10 @@ __global__ void __launch_bounds__(512) k_ln_fwd(const LnArgs a) {
 }
 
 // Persistent blocks, one row at a time; the column sums stay in shared memory,
-// each column owned by one thread, until the block's rows are done.
+// each column owned by one thread, until the block's rows are done. For rows that
+// leave no room for two stages of a ring: nothing is loaded ahead, and every
+// element reads and writes two sums (8192 x 8192 fp32 with dr 434 us, where the
+// copy rate would take 158; from 8 bits the ring holds them: 137).
 template <typename T, int CH>
 __global__ void __launch_bounds__(512) k_ln_bwd(const LnArgs a) {
     extern __shared__ float sums[];   // [2][d]
@@ -315,7 +318,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_ln_fwd_ring(const LnArgs a,
     }
 }
 
-// Backward, a thread's columns of R rows at a time: the two row sums in one
+// Backward (16384 x 4096 bf16 with dr 92 us, 86% of the copy rate; from 8 bits 96,
+// though that reads 67 MB less: both are at the pace of a row's instructions and
+// its sums, 16 warps an SM issuing in 53% of the cycles, and from codes a row
+// takes 6% more of them; fp32, half the elements a byte, 159 and 155).
+// A thread's columns of R rows at a time: the two row sums in one
 // round; the column sums stay in registers, one set a row group, and are joined
 // across the groups in shared memory at the end. kCodes: the stream comes in 8
 // bits; kDr: there is a gradient of r.

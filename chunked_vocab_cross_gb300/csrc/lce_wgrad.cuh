@@ -15,8 +15,10 @@
 // bring a finished accumulator to memory while the next one fills.
 //
 // What bounds it is the tensor core under the power cap: 7373 tokens, 16384 x
-// 4096 bf16, 564 to 634 us with the box and the values (1560 to 1760 TFLOP/s;
-// cuBLAS on plain bf16 1730 sustained, 1930 in a burst). Measured on the way:
+// 4096 bf16, 556 to 650 us with the box and the values (1520 to 1780 TFLOP/s;
+// cuBLAS on plain bf16 1730 sustained, 1930 in a burst). An fp32 dw is bound by
+// the sums of its runs in memory, 16 bytes of 32 rows at a time: 1502 us, and
+// 220 where bf16 takes 96 (4096 tokens, 4096 x 4096). Measured on the way:
 // one ring for dy and codes and eight warps that widen every step together 1780
 // us; in groups that take steps in turn 1024; arrivals of cluster scope on the
 // even CTA's barrier (1800 cycles each) 824, of CTA scope 594; codes and widened

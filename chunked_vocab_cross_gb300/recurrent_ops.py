@@ -436,7 +436,8 @@ def gated_recurrence_forward(x, g, cu_seqlens=None, *, state=None, out=None, out
     of equal lengths; L = 1 is one step of B sequences. `state` (fp32 [B, d];
     zeros if not given) is h before the first tokens and `final` h after the
     last ones, fp32; `out` receives h, `out_state` receives final and may be
-    `state`. Tokens behind the last sequence get h = 0. `kept` is what
+    `state` (the backward then needs a copy of that as it was); else outputs
+    must not overlap inputs or one another. Tokens behind the last sequence get h = 0. `kept` is what
     gated_recurrence_backward needs (with keep=True): fp32 states, one for 128
     tokens. `stream`: the stream to run on."""
     B, T, d, pc = _recurrent(x, cu_seqlens)
@@ -464,8 +465,8 @@ def gated_recurrence_backward(dh, x, g, kept, cu_seqlens=None, *, state=None, df
     """(dx, dg, dstate) from the gradients dh of h and dfinal of the final states
     (fp32 [B, d]; None: zero), the forward's x, g and state, and the states it
     kept; h is formed again from those. dstate is None without a state. dx and
-    dg may be given (strided slices of one gradient, say). `stream`: the stream
-    to run on."""
+    dg may be given (strided slices of one gradient, say; not overlapping an
+    input). `stream`: the stream to run on."""
     B, T, d, pc = _recurrent(x, cu_seqlens)
     device = x.device
     px, pg, pd = _tokens("x", x, x), _tokens("g", g, x), _tokens("dh", dh, x)

@@ -494,7 +494,9 @@ lce_status_t lce_clip_grads(int64_t count, const void *const *grads, void *const
  * each rounded once to its own type. All tensors are of `dtype`, rows of d
  * contiguous elements, ld_* apart (0 stands for d); outputs are contiguous.
  * d % 8 == 0, 8 <= d <= 16384, 0 <= N < 2^31, bases and row strides 16-byte
- * aligned. Sums are fp32 in a fixed order (deterministic).
+ * aligned. Sums are fp32 in a fixed order (deterministic): a row whose sum, or
+ * sum of squares around its mean, leaves fp32 (values of 1e19 and more) has no
+ * finite mean or an rstd of 0.
  * Scratch (backward): lce_layer_norm_workspace_size bytes or NULL.
  */
 typedef struct {
