@@ -126,7 +126,7 @@ __device__ __forceinline__ typename L::F apply(const Step<L> &s, typename L::F b
 }
 
 // A product of gates, which are never zero, that ran out of fp32: its smallest value, so that an infinite state stays one
-// (0 would make it a NaN). No finite state shows it: 2^-149 of the largest is 2^-21.
+// (0 would make it a NaN). A finite state adds 2^-21 at most by it, where it is fp32's largest.
 __device__ __forceinline__ float never_zero(float a) { return __uint_as_float(max(__float_as_uint(a), 1u)); }   // kReset stays, NaN too
 
 // Work is split over channels and over time. A slice is the channels of 128

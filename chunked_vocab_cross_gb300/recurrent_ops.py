@@ -197,7 +197,7 @@ def _readable(t):
     its elements, its address or its rows' distance are not theirs."""
     t = t.reshape(-1, t.shape[-1])
     if (t.stride(1) == 1 and t.data_ptr() % 16 == 0
-            and (t.shape[0] < 2 or (t.stride(0) > 0 and t.stride(0) * t.element_size() % 16 == 0))):
+            and (t.shape[0] < 2 or (t.stride(0) >= t.shape[1] and t.stride(0) * t.element_size() % 16 == 0))):
         return t
     return t.clone(memory_format=torch.contiguous_format)
 
@@ -437,9 +437,9 @@ def gated_recurrence_forward(x, g, cu_seqlens=None, *, state=None, out=None, out
     zeros if not given) is h before the first tokens and `final` h after the
     last ones, fp32; `out` receives h, `out_state` receives final and may be
     `state` (the backward then needs a copy of that as it was); else outputs
-    must not overlap inputs or one another. Tokens behind the last sequence get h = 0. `kept` is what
-    gated_recurrence_backward needs (with keep=True): fp32 states, one for 128
-    tokens. `stream`: the stream to run on."""
+    must not overlap inputs or one another. Tokens behind the last sequence get
+    h = 0. `kept` is what gated_recurrence_backward needs (with keep=True): fp32
+    states, one for 128 tokens. `stream`: the stream to run on."""
     B, T, d, pc = _recurrent(x, cu_seqlens)
     device = x.device
     px, pg = _tokens("x", x, x), _tokens("g", g, x)

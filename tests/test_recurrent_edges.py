@@ -22,3 +22,18 @@ def test_rows_of_packed_activations_have_whole_16_bytes(rows, n):
         if rows:
             assert got.storage_offset() + (rows - 1) * got.stride(0) + wide <= got.untyped_storage().nbytes()
     assert recurrent_ops._on_16(room) is room
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_that_the_kernels_cannot_read_are_copied(dtype):
+    base = torch.arange(4096).to(dtype)
+    good = (base[:640].view(10, 64), base.view(16, 256)[:10, :64], base[:640].view(2, 5, 64), base[:64].view(1, 64), base[:0].view(0, 64))
+    bad = (base[1:641].view(10, 64), base[:650].view(10, 65)[:, :64], base[:640].view(64, 10).t(), base[:64].expand(10, 64),
+           base[:10].view(10, 1).expand(10, 64), base[:1280].view(10, 128)[:, ::2], base.as_strided((10, 64), (16, 1)), base[1:65].view(1, 64))
+    for t in good:
+        assert recurrent_ops._readable(t).data_ptr() == t.data_ptr()
+    for t in bad:
+        got = recurrent_ops._readable(t)
+        assert got.is_contiguous() and got.data_ptr() != t.data_ptr() and got.data_ptr() % 16 == 0
+    for t in good + bad:
+        assert torch.equal(recurrent_ops._readable(t), t.reshape(-1, 64))
